@@ -1,0 +1,442 @@
+// conv.cu -- short causal depthwise convolution over tokens (include/mamba2_layer.h).
+//
+//   s[t] = bias + sum_k w[k] x[t - (W - 1) + k]      y = s or s sigmoid(s)
+//
+// Bytes bound: forward x in, y out; backward x, dy in, dx out.  A thread owns V
+// neighbouring channels (16 bytes of a token in the forward) and walks a stretch
+// of tokens with the last W - 1 inputs in registers, so each input is read once
+// plus W - 1 tokens of overlap per stretch; neighbouring threads read neighbouring
+// bytes of one token's row.
+#include <algorithm>
+
+#include "internal.h"
+#include "layer.cuh"
+
+namespace m2 {
+namespace {
+
+template <typename TI, int V>
+__device__ __forceinline__ void load_f(const TI* p, float* o) {
+    Conv<TI, V>::to(load_raw<TI, V>(p), o);
+}
+template <int V> __device__ __forceinline__ void zero_f(float* o) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) o[j] = 0.f;
+}
+template <int V, int W>
+__device__ __forceinline__ void load_w(const float* w, const float* bias, int64_t c, float (&wk)[W][V],
+                                       float (&bi)[V]) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) wk[k][j] = __ldg(w + (c + j) * W + k);
+        bi[j] = bias ? __ldg(bias + c + j) : 0.f;
+    }
+}
+
+constexpr int kFwdThreads = 128;
+
+// Block: one stretch of TS tokens of one sequence, kFwdThreads * V channels.
+template <typename TI, int V, int W, bool SILU>
+__global__ void __launch_bounds__(kFwdThreads)
+conv_fwd_kernel(const TI* __restrict__ x, const float* __restrict__ w,
+                const float* __restrict__ bias, const TI* __restrict__ init,
+                const int32_t* __restrict__ lengths, TI* __restrict__ y, TI* __restrict__ fin,
+                int T, int D, int TS, int nseg, int ncb, Tok sx, Tok sy) {
+    const int cb = blockIdx.x % ncb, bs = blockIdx.x / ncb;
+    const int seg = bs % nseg, b = bs / nseg;
+    const int c = (cb * kFwdThreads + threadIdx.x) * V;
+    if (c >= D) return;
+    const int n = lengths ? min(max(__ldg(lengths + b), 0), T) : T;
+    const TI* xb = x + (int64_t)b * sx.b + c;
+    TI* yb = y + (int64_t)b * sy.b + c;
+    const TI* ib = init ? init + ((int64_t)b * (W - 1)) * D + c : nullptr;
+    typedef typename Pack<TI, V>::Raw Raw;
+    if (seg == 0 && fin) {
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) {
+            const int t = n - (W - 1) + k;
+            Raw r = zero_raw<Raw>();
+            if (t >= 0) r = load_raw<TI, V>(xb + (int64_t)t * sx.t);
+            else if (ib) r = load_raw<TI, V>(ib + (int64_t)(t + W - 1) * D);
+            store_raw<TI, V>(fin + ((int64_t)b * (W - 1) + k) * D + c, r);
+        }
+    }
+    float wk[W][V], bi[V], win[W - 1][V];
+    load_w<V, W>(w, bias, c, wk, bi);
+    const int t0 = seg * TS, t1 = min(t0 + TS, T), tn = min(t1, n);
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {
+        const int t = t0 - (W - 1) + k;
+        zero_f<V>(win[k]);
+        if (t >= 0) {
+            if (t < n) load_f<TI, V>(xb + (int64_t)t * sx.t, win[k]);
+        } else if (ib) {
+            load_f<TI, V>(ib + (int64_t)(t + W - 1) * D, win[k]);
+        }
+    }
+    constexpr int U = 8;   // tokens whose loads are in flight together
+    for (int t = t0; t < tn; t += U) {
+        Raw r[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (t + u < tn) r[u] = load_raw<TI, V>(xb + (int64_t)(t + u) * sx.t);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (t + u >= tn) break;
+            float cur[V], o[V];
+            Conv<TI, V>::to(r[u], cur);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float s = bi[j];
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k) s = fmaf(wk[k][j], win[k][j], s);
+                s = fmaf(wk[W - 1][j], cur[j], s);
+                o[j] = SILU ? s * sigmoid(s) : s;
+#pragma unroll
+                for (int k = 0; k + 1 < W - 1; ++k) win[k][j] = win[k + 1][j];
+                win[W - 2][j] = cur[j];
+            }
+            store_raw<TI, V>(yb + (int64_t)(t + u) * sy.t, Conv<TI, V>::from(o));
+        }
+    }
+    for (int t = max(tn, t0); t < t1; ++t) store_raw<TI, V>(yb + (int64_t)t * sy.t, zero_raw<Raw>());
+}
+
+// One token: the window is read, applied and moved on.
+template <typename TI, int V, int W, bool SILU>
+__global__ void __launch_bounds__(128)
+conv_step_kernel(TI* __restrict__ state, const TI* __restrict__ x, const float* __restrict__ w,
+                 const float* __restrict__ bias, TI* __restrict__ y, int D, int ncb, int64_t sxb,
+                 int64_t syb) {
+    const int cb = blockIdx.x % ncb, b = blockIdx.x / ncb;
+    const int c = (cb * 128 + threadIdx.x) * V;
+    if (c >= D) return;
+    typedef typename Pack<TI, V>::Raw Raw;
+    TI* sb = state + (int64_t)b * (W - 1) * D + c;
+    Raw r[W];
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) r[k] = *reinterpret_cast<const Raw*>(sb + (int64_t)k * D);
+    r[W - 1] = load_raw<TI, V>(x + (int64_t)b * sxb + c);
+    float wk[W][V], o[V];
+    load_w<V, W>(w, bias, c, wk, o);
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+        float v[V];
+        Conv<TI, V>::to(r[k], v);
+#pragma unroll
+        for (int j = 0; j < V; ++j) o[j] = fmaf(wk[k][j], v[j], o[j]);
+    }
+    if (SILU) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) o[j] *= sigmoid(o[j]);
+    }
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) store_raw<TI, V>(sb + (int64_t)k * D, r[k + 1]);
+    store_raw<TI, V>(y + (int64_t)b * syb + c, Conv<TI, V>::from(o));
+}
+
+// Backward.  ds = dy silu'(s) with s recomputed;  dx[t] = sum_k w[k] ds[t + W-1 - k];
+// dw[k] = sum_t ds[t] x[t - (W-1) + k];  dbias = sum_t ds[t].
+// A thread walks its stretch and W - 1 tokens past it (whose ds its last dx need)
+// with windows of x and ds in registers; at t it finishes dx[t - (W - 1)], which
+// for the first stretch includes the gradients of the initial window.  The kBwdTY
+// stretches of a block are summed in shared memory into one slot of dw and dbias.
+constexpr int kBwdTX = 32, kBwdTY = 8;
+
+template <typename TI, int V, int W, bool SILU>
+__global__ void __launch_bounds__(kBwdTX * kBwdTY)
+conv_bwd_kernel(const TI* __restrict__ x, const float* __restrict__ w,
+                const float* __restrict__ bias, const TI* __restrict__ init,
+                const TI* __restrict__ dy, const TI* __restrict__ dfin,
+                const int32_t* __restrict__ lengths, TI* __restrict__ dx, TI* __restrict__ dinit,
+                float* __restrict__ part, int T, int D, int TS, int nblk, int ncb, Tok sx, Tok sdy) {
+    __shared__ float red[kBwdTY][kBwdTX * V * (W + 1)];
+    const int cb = blockIdx.x % ncb, slot = blockIdx.x / ncb;
+    const int tb = slot % nblk, b = slot / nblk;
+    const int c = (cb * kBwdTX + threadIdx.x) * V;
+    const int seg = tb * kBwdTY + threadIdx.y;
+    const bool first = seg == 0;
+    const int t0 = min(seg * TS, T), t1 = min(t0 + TS, T);
+    float dwk[W][V], dbi[V];
+#pragma unroll
+    for (int k = 0; k < W; ++k) zero_f<V>(dwk[k]);
+    zero_f<V>(dbi);
+    if (c < D && (t0 < t1 || first)) {
+        const int n = lengths ? min(max(__ldg(lengths + b), 0), T) : T;
+        const TI* xb = x + (int64_t)b * sx.b + c;
+        const TI* db = dy + (int64_t)b * sdy.b + c;
+        TI* ob = dx + (int64_t)b * T * D + c;
+        const int64_t wrow = (int64_t)b * (W - 1) * D + c;
+        float wk[W][V], bi[V], xw[W][V], dsw[W][V];   // xw[W-1], dsw[W-1]: the current token
+        load_w<V, W>(w, bias, c, wk, bi);
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            zero_f<V>(dsw[k]);
+            zero_f<V>(xw[k]);
+            const int t = t0 - W + k;   // shifted once before use
+            if (k > 0) {
+                if (t >= 0) {
+                    if (t < n) load_f<TI, V>(xb + (int64_t)t * sx.t, xw[k]);
+                } else if (init) {
+                    load_f<TI, V>(init + wrow + (int64_t)(t + W - 1) * D, xw[k]);
+                }
+            }
+        }
+        typedef typename Pack<TI, V>::Raw Raw;
+        constexpr int U = 4;
+        const int te = t1 + W - 1;
+        for (int tq = t0; tq < te; tq += U) {
+            Raw rx[U], rd[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                rx[u] = rd[u] = zero_raw<Raw>();
+                if (tq + u < min(te, n)) {
+                    rx[u] = load_raw<TI, V>(xb + (int64_t)(tq + u) * sx.t);
+                    rd[u] = load_raw<TI, V>(db + (int64_t)(tq + u) * sdy.t);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int t = tq + u;
+                if (t >= te) break;
+                const bool real = t < n, mine = t < t1;
+                float cx[V], cd[V], o[V];
+                Conv<TI, V>::to(rx[u], cx);
+                Conv<TI, V>::to(rd[u], cd);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+#pragma unroll
+                    for (int k = 0; k + 1 < W; ++k) {
+                        xw[k][j] = xw[k + 1][j];
+                        dsw[k][j] = dsw[k + 1][j];
+                    }
+                    xw[W - 1][j] = cx[j];
+                    float s = bi[j], ds = cd[j];
+                    if (SILU) {
+#pragma unroll
+                        for (int k = 0; k < W; ++k) s = fmaf(wk[k][j], xw[k][j], s);
+                        const float sg = sigmoid(s);
+                        ds *= sg * fmaf(s, 1.f - sg, 1.f);
+                    }
+                    ds = real ? ds : 0.f;
+                    dsw[W - 1][j] = ds;
+                    const float own = mine ? ds : 0.f;
+#pragma unroll
+                    for (int k = 0; k < W; ++k) dwk[k][j] = fmaf(own, xw[k][j], dwk[k][j]);
+                    dbi[j] += own;
+                    float a = 0.f;
+#pragma unroll
+                    for (int k = 0; k < W; ++k) a = fmaf(wk[k][j], dsw[W - 1 - k][j], a);
+                    o[j] = a;
+                }
+                const int tp = t - (W - 1);
+                if (tp >= t0 || first) {
+                    if (dfin && tp < n && tp >= n - (W - 1)) {
+                        float f[V];
+                        load_f<TI, V>(dfin + wrow + (int64_t)(tp - (n - (W - 1))) * D, f);
+#pragma unroll
+                        for (int j = 0; j < V; ++j) o[j] += f[j];
+                    }
+                    if (tp >= 0) store_raw<TI, V>(ob + (int64_t)tp * D, Conv<TI, V>::from(o));
+                    else if (dinit)
+                        store_raw<TI, V>(dinit + wrow + (int64_t)(tp + W - 1) * D, Conv<TI, V>::from(o));
+                }
+            }
+        }
+    }
+    float* mr = red[threadIdx.y] + threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) mr[(j * (W + 1) + k) * kBwdTX] = dwk[k][j];
+        mr[(j * (W + 1) + W) * kBwdTX] = dbi[j];
+    }
+    __syncthreads();
+    const int tid = threadIdx.y * kBwdTX + threadIdx.x;
+    for (int i = tid; i < kBwdTX * V * (W + 1); i += kBwdTX * kBwdTY) {
+        const int cx = i % kBwdTX, jk = i / kBwdTX, j = jk / (W + 1), k = jk % (W + 1);
+        const int64_t ch = (int64_t)(cb * kBwdTX + cx) * V + j;
+        if (ch >= D) continue;
+        float a = 0.f;
+#pragma unroll
+        for (int q = 0; q < kBwdTY; ++q) a += red[q][i];
+        float* row = part + (int64_t)slot * D * (W + 1);
+        if (k < W) row[ch * W + k] = a;
+        else row[(int64_t)D * W + ch] = a;
+    }
+}
+
+// Stretch lengths: long ones amortise the W - 1 tokens of overlap (and, backward,
+// the slots of dw), short ones fill the GPU when there are few rows.
+int pick_ts(int64_t rows_of_threads, int64_t T, int64_t want) {
+    for (int ts : {64, 32, 16}) {
+        if (rows_of_threads * ((T + ts - 1) / ts) >= want) return ts;
+    }
+    return 8;
+}
+
+int bwd_vec(const ConvArgs& a) { return a.D % 4 == 0 ? 4 : 1; }
+int bwd_ts(const ConvArgs& a) {
+    const int64_t lanes = (a.D + bwd_vec(a) - 1) / bwd_vec(a);
+    return pick_ts(a.b * lanes, a.T, (int64_t)sm_count() * 512);
+}
+int64_t bwd_blocks(const ConvArgs& a) {
+    const int64_t per = (int64_t)bwd_ts(a) * kBwdTY;
+    return std::max<int64_t>(1, (a.T + per - 1) / per);
+}
+
+template <typename TI, int V, int W>
+cudaError_t fwd_w(const ConvArgs& a, const TI* x, const float* w, const float* bias, const TI* init,
+                  const int32_t* lengths, TI* y, TI* fin, cudaStream_t st) {
+    const int64_t lanes = (a.D + V - 1) / V, ncb = (lanes + kFwdThreads - 1) / kFwdThreads;
+    const int ts = pick_ts(a.b * lanes, a.T, (int64_t)sm_count() * 1024);
+    const int64_t nseg = std::max<int64_t>(1, (a.T + ts - 1) / ts);
+    if (a.b * nseg * ncb >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    auto k = a.silu ? conv_fwd_kernel<TI, V, W, true> : conv_fwd_kernel<TI, V, W, false>;
+    k<<<(unsigned)(a.b * nseg * ncb), kFwdThreads, 0, st>>>(
+        x, w, bias, init, lengths, y, fin, (int)a.T, (int)a.D, ts, (int)nseg, (int)ncb, a.sx, a.sy);
+    return cudaGetLastError();
+}
+
+template <typename TI, int V, int W>
+cudaError_t step_w(const ConvArgs& a, TI* state, const TI* x, const float* w, const float* bias, TI* y,
+                   cudaStream_t st) {
+    const int64_t ncb = ((a.D + V - 1) / V + 127) / 128;
+    if (a.b * ncb >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    auto k = a.silu ? conv_step_kernel<TI, V, W, true> : conv_step_kernel<TI, V, W, false>;
+    k<<<(unsigned)(a.b * ncb), 128, 0, st>>>(state, x, w, bias, y, (int)a.D, (int)ncb, a.sx.b, a.sy.b);
+    return cudaGetLastError();
+}
+
+template <typename TI, int V, int W>
+cudaError_t bwd_w(const ConvArgs& a, const TI* x, const float* w, const float* bias, const TI* init,
+                  const TI* dy, const TI* dfin, const int32_t* lengths, TI* dx, TI* dinit, float* part,
+                  cudaStream_t st) {
+    const int64_t ncb = ((a.D + V - 1) / V + kBwdTX - 1) / kBwdTX, nblk = bwd_blocks(a);
+    if (a.b * nblk * ncb >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    auto k = a.silu ? conv_bwd_kernel<TI, V, W, true> : conv_bwd_kernel<TI, V, W, false>;
+    k<<<(unsigned)(a.b * nblk * ncb), dim3(kBwdTX, kBwdTY), 0, st>>>(
+        x, w, bias, init, dy, dfin, lengths, dx, dinit, part, (int)a.T, (int)a.D, bwd_ts(a), (int)nblk,
+        (int)ncb, a.sx, a.sy);
+    return cudaGetLastError();
+}
+
+template <typename TI, int V>
+cudaError_t fwd_v(const ConvArgs& a, const void* x, const float* w, const float* bias, const void* init,
+                  const int32_t* lengths, void* y, void* fin, cudaStream_t st) {
+    auto go = [&](auto f) {
+        return f(a, static_cast<const TI*>(x), w, bias, static_cast<const TI*>(init), lengths,
+                 static_cast<TI*>(y), static_cast<TI*>(fin), st);
+    };
+    return a.W == 2 ? go(fwd_w<TI, V, 2>) : a.W == 3 ? go(fwd_w<TI, V, 3>) : go(fwd_w<TI, V, 4>);
+}
+template <typename TI, int V>
+cudaError_t step_v(const ConvArgs& a, void* state, const void* x, const float* w, const float* bias,
+                   void* y, cudaStream_t st) {
+    auto go = [&](auto f) {
+        return f(a, static_cast<TI*>(state), static_cast<const TI*>(x), w, bias, static_cast<TI*>(y), st);
+    };
+    return a.W == 2 ? go(step_w<TI, V, 2>) : a.W == 3 ? go(step_w<TI, V, 3>) : go(step_w<TI, V, 4>);
+}
+template <typename TI, int V>
+cudaError_t bwd_v(const ConvArgs& a, const void* x, const float* w, const float* bias, const void* init,
+                  const void* dy, const void* dfin, const int32_t* lengths, void* dx, void* dinit,
+                  float* part, cudaStream_t st) {
+    auto go = [&](auto f) {
+        return f(a, static_cast<const TI*>(x), w, bias, static_cast<const TI*>(init),
+                 static_cast<const TI*>(dy), static_cast<const TI*>(dfin), lengths, static_cast<TI*>(dx),
+                 static_cast<TI*>(dinit), part, st);
+    };
+    return a.W == 2 ? go(bwd_w<TI, V, 2>) : a.W == 3 ? go(bwd_w<TI, V, 3>) : go(bwd_w<TI, V, 4>);
+}
+
+// Every access of the call is whole and aligned at V elements a piece.
+bool wide(const ConvArgs& a, int64_t V, const void* x, const void* y, const void* s0, const void* s1,
+          const void* o) {
+    const int64_t es = a.dtype == 1 ? 2 : 4, bytes = V * es;
+    const Tok row{0, a.D};
+    return a.D % V == 0 && vec_ok(x, a.sx, bytes, es) && vec_ok(y, a.sy, bytes, es) &&
+           vec_ok(s0, row, bytes, es) && vec_ok(s1, row, bytes, es) && vec_ok(o, row, bytes, es);
+}
+
+// Sum of one column of part over the slots: 32 columns x 8 rows of slots a block.
+__global__ void __launch_bounds__(256)
+column_sum_kernel(const float* __restrict__ part, int64_t slots, int64_t cols, float* __restrict__ out1,
+                  int64_t n1, float* __restrict__ out2) {
+    __shared__ float red[8][33];
+    const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
+    float a = 0.f;
+    if (c < cols)
+        for (int64_t s = threadIdx.y; s < slots; s += 8) a += __ldg(part + s * cols + c);
+    red[threadIdx.y][threadIdx.x] = a;
+    __syncthreads();
+    if (threadIdx.y == 0 && c < cols) {
+#pragma unroll
+        for (int q = 1; q < 8; ++q) a += red[q][threadIdx.x];
+        if (c < n1) {
+            if (out1) out1[c] = a;
+        } else if (out2) {
+            out2[c - n1] = a;
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_column_sum(const float* part, int64_t slots, int64_t cols, float* out1, int64_t n1,
+                              float* out2, cudaStream_t st) {
+    if (cols == 0) return cudaSuccess;
+    if ((cols + 31) / 32 >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    column_sum_kernel<<<(unsigned)((cols + 31) / 32), dim3(32, 8), 0, st>>>(part, slots, cols, out1, n1,
+                                                                           out2);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_conv_fwd(const ConvArgs& a, const void* x, const float* w, const float* bias,
+                            const void* init, const int32_t* lengths, void* y, void* fin,
+                            cudaStream_t st) {
+    if (a.b == 0 || a.D == 0) return cudaSuccess;
+    if (a.dtype == 1)
+        return wide(a, 8, x, y, init, fin, nullptr)
+                   ? fwd_v<__nv_bfloat16, 8>(a, x, w, bias, init, lengths, y, fin, st)
+                   : fwd_v<__nv_bfloat16, 1>(a, x, w, bias, init, lengths, y, fin, st);
+    return wide(a, 4, x, y, init, fin, nullptr)
+               ? fwd_v<float, 4>(a, x, w, bias, init, lengths, y, fin, st)
+               : fwd_v<float, 1>(a, x, w, bias, init, lengths, y, fin, st);
+}
+
+cudaError_t launch_conv_step(const ConvArgs& a, void* state, const void* x, const float* w,
+                             const float* bias, void* y, cudaStream_t st) {
+    if (a.b == 0 || a.D == 0) return cudaSuccess;
+    if (a.dtype == 1)
+        return wide(a, 2, x, y, state, nullptr, nullptr)
+                   ? step_v<__nv_bfloat16, 2>(a, state, x, w, bias, y, st)
+                   : step_v<__nv_bfloat16, 1>(a, state, x, w, bias, y, st);
+    return step_v<float, 1>(a, state, x, w, bias, y, st);
+}
+
+int64_t conv_bwd_slots(const ConvArgs& a) { return a.b * bwd_blocks(a); }
+
+cudaError_t launch_conv_bwd(const ConvArgs& a, const void* x, const float* w, const float* bias,
+                            const void* init, const void* dy, const void* dfin, const int32_t* lengths,
+                            void* dx, float* dw, float* dbias, void* dinit, float* part,
+                            cudaStream_t st) {
+    if (a.D == 0) return cudaSuccess;
+    cudaError_t e = cudaSuccess;
+    if (a.b > 0) {
+        // dfin and dinit are rows of D like the initial window
+        const bool v4 = wide(a, 4, x, dy, init, dfin, dinit) &&
+                        wide(a, 4, x, dy, dx, nullptr, nullptr);
+        if (a.dtype == 1)
+            e = v4 ? bwd_v<__nv_bfloat16, 4>(a, x, w, bias, init, dy, dfin, lengths, dx, dinit, part, st)
+                   : bwd_v<__nv_bfloat16, 1>(a, x, w, bias, init, dy, dfin, lengths, dx, dinit, part, st);
+        else
+            e = v4 ? bwd_v<float, 4>(a, x, w, bias, init, dy, dfin, lengths, dx, dinit, part, st)
+                   : bwd_v<float, 1>(a, x, w, bias, init, dy, dfin, lengths, dx, dinit, part, st);
+    }
+    if (e != cudaSuccess) return e;
+    return launch_column_sum(part, a.b ? conv_bwd_slots(a) : 0, a.D * (a.W + 1), dw, a.D * a.W, dbias, st);
+}
+
+}  // namespace m2

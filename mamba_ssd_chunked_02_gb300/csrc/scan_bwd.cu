@@ -1,0 +1,706 @@
+// scan_bwd.cu -- gradients of the selective scan (include/mamba2_layer.h).
+//
+// With dY = dy silu(z) (or dy) and g_t the adjoint of h_t:
+//   g_t = C_t dY_t + a_{t+1} g_{t+1},  a_t = exp(d_t A)      (last: + dfinal)
+//   dC_t[n] = sum_c dY_t h_t           dB_t[n] = sum_c d_t x_t g_t
+//   q_t = sum_n g_t B_t[n]             e_t = a_t g_t h_{t-1}
+//   dx_t = d_t q_t + D dY_t            dd_t = x_t q_t + sum_n A e_t     ddt = dd (softplus')
+//   dA = sum_t d_t e_t                 dD = sum_t dY_t x_t              dz = dy silu'(z) (C.h + D x)
+//
+// Three kernels.  (1) scan_local_kernel runs every stretch of the token axis from a
+// zero state, forwards only: it stores the state every kL tokens, the stretch's
+// final state S, its adjoint G = sum_t (prod_{s <= t} a_s) dY_t C_t of the state that
+// enters it, and the sums of d.  (2) scan_join2_kernel carries the true states
+// forwards and the true adjoints backwards over the stretches.  (3) scan_grad_kernel
+// takes kL tokens at a time, last first: state = stored local state + exp(A sum d) x
+// entering state, recomputed token by token into registers, then the adjoint walks
+// back over them.  A lane does kK channels in turn, so that dB and dC are summed over
+// them in registers before the warp's lanes, the block's warps and (through memory,
+// by a last kernel in a fixed order) the blocks.
+#include <algorithm>
+
+#include "internal.h"
+#include "scan.cuh"
+
+namespace m2 {
+namespace {
+
+constexpr int kL = 8;      // tokens between stored states = tokens of a gradient tile
+constexpr int kK = 4;      // channels a lane does in turn
+constexpr int kGT = 128;   // threads of the gradient kernel
+
+struct BwdP {
+    const void *x, *dt, *B, *C, *z, *dy;
+    const float *A, *D, *bias;
+    const int32_t* lengths;
+    const float *h_in, *g_in;   // [nseg][b][D][N] or null (zeros)
+    float* ck;                  // [b][nck][D][N]
+    float* ck_d;                // [b][nck][D]: sum of d from the stretch's start
+    float *seg_h, *seg_g, *seg_d;
+    void *dx, *ddt, *dz;
+    float *dinit;
+    float* part_bc;             // [ncb][b T G][2 N]
+    float* part_A;              // [b nseg][D][N]
+    float* part_v;              // [b nseg][2][D]: dD, ddt_bias
+    int T, Dch, G, Dg, ncb, nseg, SL, nck, softplus;
+    int64_t b;
+    Tok sx, sdt, sB, sC, sz, sy;
+};
+
+// (1) Each stretch from zero.  ADJ: also its adjoint (only needed when there are
+// several stretches).
+template <typename TI, int N, int V, bool ADJ>
+__global__ void __launch_bounds__(Cfg<N>::NT)
+scan_local_kernel(const BwdP p) {
+    using K = Cfg<N>;
+    constexpr int NT = K::NT, LPC = K::LPC, CB = K::CB, TT = K::TT;
+    constexpr int PR = CB / V, RS = NT / PR, IT = TT / RS;
+    constexpr int BI = TT * N / V / NT;
+    extern __shared__ __align__(16) unsigned char smem[];
+    ulonglong2* sP = reinterpret_cast<ulonglong2*>(smem);                 // [TT][CB] (d, d, dx, dx)
+    f2* sY = reinterpret_cast<f2*>(smem + (size_t)TT * CB * 16);          // [TT][CB] (dY, dY)
+    float* sB = reinterpret_cast<float*>(smem + (size_t)TT * CB * (ADJ ? 24 : 16));   // [TT][N]
+    float* sC = sB + TT * N;
+    typedef typename Pack<TI, V>::Raw Raw;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int id = blockIdx.x;
+    const int cb = id % p.ncb;
+    id /= p.ncb;
+    const int g = id % p.G;
+    id /= p.G;
+    const int seg = id % p.nseg, b = id / p.nseg;
+    const int n = p.lengths ? min(max(__ldg(p.lengths + b), 0), p.T) : p.T;
+    const int s0 = seg * p.SL, s1 = min(s0 + p.SL, p.T), sn = min(s1, n);
+    const int lc = (tid % PR) * V, r0 = tid / PR;
+    const bool con = cb * CB + lc < p.Dg;
+    const int64_t c = (int64_t)g * p.Dg + cb * CB + lc;
+    const TI* xp = static_cast<const TI*>(p.x) + (int64_t)b * p.sx.b + c;
+    const TI* dp = static_cast<const TI*>(p.dt) + (int64_t)b * p.sdt.b + c;
+    const TI* zp = static_cast<const TI*>(p.z) + (int64_t)b * p.sz.b + c;
+    const TI* yp = static_cast<const TI*>(p.dy) + (int64_t)b * p.sy.b + c;
+    const TI* Bp = static_cast<const TI*>(p.B) + (int64_t)b * p.sB.b + (int64_t)g * N;
+    const TI* Cp = static_cast<const TI*>(p.C) + (int64_t)b * p.sC.b + (int64_t)g * N;
+    float bias[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) bias[j] = p.bias && con ? __ldg(p.bias + c + j) : 0.f;
+
+    const int q = lane % LPC, ch = warp * K::CPW + lane / LPC;
+    const bool on = cb * CB + ch < p.Dg;
+    const int64_t cg = (int64_t)g * p.Dg + cb * CB + ch;
+    f2 A2[2] = {0, 0}, h[2] = {0, 0}, G[2] = {0, 0}, P[2];
+    P[0] = P[1] = dup2(1.f);
+    if (on) {
+        const float* Ap = p.A + cg * N + q * kNS;
+        A2[0] = pack2(__ldg(Ap) * kLog2e, __ldg(Ap + 1) * kLog2e);
+        A2[1] = pack2(__ldg(Ap + 2) * kLog2e, __ldg(Ap + 3) * kLog2e);
+    }
+    float dsum = 0.f;
+    float* ck = p.ck + ((int64_t)b * p.nck * p.Dch + cg) * N + q * kNS;
+    float* ckd = p.ck_d + (int64_t)b * p.nck * p.Dch + cg;
+
+    for (int t0 = s0; t0 < s1; t0 += TT) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int r = r0 + i * RS, t = t0 + r;
+            const bool real = con && t < sn;
+            float fx[V], fd[V], fz[V], fy[V];
+            Raw rx = zero_raw<Raw>(), rd = rx, rz = rx, ry = rx;
+            if (real) {
+                rx = load_raw<TI, V>(xp + (int64_t)t * p.sx.t);
+                rd = load_raw<TI, V>(dp + (int64_t)t * p.sdt.t);
+                if (ADJ && p.z) rz = load_raw<TI, V>(zp + (int64_t)t * p.sz.t);
+                if (ADJ) ry = load_raw<TI, V>(yp + (int64_t)t * p.sy.t);
+            }
+            Conv<TI, V>::to(rx, fx);
+            Conv<TI, V>::to(rd, fd);
+            Conv<TI, V>::to(rz, fz);
+            Conv<TI, V>::to(ry, fy);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float v = fd[j] + bias[j];
+                const float d = real ? (p.softplus ? softplus(v) : v) : 0.f;
+                const int cc = lc + j;
+                ulonglong2 w;
+                w.x = dup2(d);
+                w.y = dup2(d * fx[j]);
+                sP[r * CB + (cc ^ ((cc >> 3) & 1))] = w;
+                if (ADJ) sY[r * CB + cc] = dup2(p.z ? fy[j] * fz[j] * sigmoid(fz[j]) : fy[j]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < BI; ++i) {
+            const int e = (tid + i * NT) * V, t = t0 + e / N;
+            Raw rB = zero_raw<Raw>(), rC = rB;
+            if (t < sn) {
+                rB = load_raw<TI, V>(Bp + (int64_t)t * p.sB.t + e % N);
+                if (ADJ) rC = load_raw<TI, V>(Cp + (int64_t)t * p.sC.t + e % N);
+            }
+            float f[V];
+            Conv<TI, V>::to(rB, f);
+#pragma unroll
+            for (int j = 0; j < V; ++j) sB[e + j] = f[j];
+            if (ADJ) {
+                Conv<TI, V>::to(rC, f);
+#pragma unroll
+                for (int j = 0; j < V; ++j) sC[e + j] = f[j];
+            }
+        }
+        __syncthreads();
+        const ulonglong2* pP = sP + (ch ^ ((ch >> 3) & 1));
+        const f2* pY = sY + ch;
+#pragma unroll 1
+        for (int tb = 0; tb < TT; tb += kL) {
+            if (t0 + tb >= s1) break;
+            if (on) {
+                const int64_t at = (int64_t)((t0 + tb) / kL) * p.Dch;
+                float4 v;
+                unpack2(h[0], v.x, v.y);
+                unpack2(h[1], v.z, v.w);
+                *reinterpret_cast<float4*>(ck + at * N) = v;
+                if (q == 0) ckd[at] = dsum;
+            }
+#pragma unroll
+            for (int u = 0; u < kL; ++u) {
+                const ulonglong2 w = pP[(tb + u) * CB];
+                const ulonglong2 Bv = *reinterpret_cast<const ulonglong2*>(sB + (tb + u) * N + q * kNS);
+                const f2 a0 = ex2_2(mul2(w.x, A2[0])), a1 = ex2_2(mul2(w.x, A2[1]));
+                h[0] = fma2(a0, h[0], mul2(w.y, Bv.x));
+                h[1] = fma2(a1, h[1], mul2(w.y, Bv.y));
+                float lo, hi;
+                unpack2(w.x, lo, hi);
+                dsum += lo;
+                if (ADJ) {
+                    const ulonglong2 Cv = *reinterpret_cast<const ulonglong2*>(sC + (tb + u) * N + q * kNS);
+                    const f2 yv = pY[(tb + u) * CB];
+                    P[0] = mul2(P[0], a0);
+                    P[1] = mul2(P[1], a1);
+                    G[0] = fma2(P[0], mul2(yv, Cv.x), G[0]);
+                    G[1] = fma2(P[1], mul2(yv, Cv.y), G[1]);
+                }
+            }
+        }
+        __syncthreads();
+    }
+    if (ADJ && on) {
+        const int64_t at = (((int64_t)seg * p.b + b) * p.Dch + cg);
+        float4 v;
+        unpack2(h[0], v.x, v.y);
+        unpack2(h[1], v.z, v.w);
+        *reinterpret_cast<float4*>(p.seg_h + at * N + q * kNS) = v;
+        unpack2(G[0], v.x, v.y);
+        unpack2(G[1], v.z, v.w);
+        *reinterpret_cast<float4*>(p.seg_g + at * N + q * kNS) = v;
+        if (q == 0) p.seg_d[at] = dsum;
+    }
+}
+
+// (2) One thread per (b, c, n): seg_h becomes the state entering each stretch, seg_g
+// the adjoint of the state leaving it.
+__global__ void __launch_bounds__(256)
+scan_join2_kernel(float* __restrict__ seg_h, float* __restrict__ seg_g, const float* __restrict__ seg_d,
+                  const float* __restrict__ A, const float* __restrict__ init,
+                  const float* __restrict__ dfinal, int64_t total, int64_t DN, int N, int nseg) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= total) return;
+    const float a = __ldg(A + i % DN) * kLog2e;
+    const int64_t bd = i / N, nbd = total / N;
+    float h = init ? init[i] : 0.f, g = dfinal ? dfinal[i] : 0.f;
+    for (int s = 0; s < nseg; ++s) {
+        const int r = nseg - 1 - s;
+        const float hl = seg_h[s * total + i], gl = seg_g[r * total + i];
+        const float hd = seg_d[s * nbd + bd], gd = seg_d[r * nbd + bd];
+        seg_h[s * total + i] = h;
+        seg_g[r * total + i] = g;
+        h = fmaf(ex2(a * hd), h, hl);
+        g = fmaf(ex2(a * gd), g, gl);
+    }
+}
+
+// Sum of 2^k-strided lanes: v[0 .. M) over the CPW lanes lane, lane ^ LPC, ...; each
+// lane ends with M / CPW of the sums, those of values  sel + CPW * j  where sel is the
+// lane's channel index within the warp.
+template <int M, int CPW, int LPC> __device__ __forceinline__ void channel_sum(float (&v)[M]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1, m = M; o < CPW; o <<= 1, m >>= 1) {
+        const bool hi = lane & (o * LPC);
+#pragma unroll
+        for (int i = 0; i < M / 2; ++i)
+            if (i < m / 2) {
+                const float give = hi ? v[2 * i] : v[2 * i + 1], keep = hi ? v[2 * i + 1] : v[2 * i];
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o * LPC);
+            }
+    }
+}
+
+template <int N> struct GCfg {
+    static constexpr int LPC = N / kNS, CPW = 32 / LPC, WARPS = kGT / 32;
+    static constexpr int CK = WARPS * CPW;       // channels of one turn
+    static constexpr int CB = CK * kK;           // channels of the block
+    static constexpr int U = LPC < 8 ? LPC : 8;
+    static constexpr int QP = CB + (CPW < 2 ? 2 : CPW);   // pitch of the q, r, y tiles
+    static constexpr size_t smem = (size_t)kL * CB * 24 + 3 * (size_t)kL * QP * 4 + 2 * (size_t)kL * N * 4 +
+                                   (size_t)WARPS * 2 * kL * N * 4 + 4 * (size_t)kK * kGT * 16;
+};
+
+// (3) Gradients.  Block: CB channels of one group, one stretch of one sequence.
+template <typename TI, int N, int V, bool GATE>
+__global__ void __launch_bounds__(kGT)
+scan_grad_kernel(const BwdP p) {
+    using K = GCfg<N>;
+    constexpr int LPC = K::LPC, CPW = K::CPW, CB = K::CB, QP = K::QP, U = K::U;
+    constexpr int PR0 = CB / V, PR = PR0 < kGT ? PR0 : kGT;          // threads a row
+    constexpr int RS = kGT / PR, CI = PR0 / PR, RI = RS < kL ? kL / RS : 1;   // rows a pass, column passes, row passes
+    static_assert(RS * RI >= kL && CI * PR == PR0, "tile shape");    // RS > kL: the last threads have no row
+    extern __shared__ __align__(16) unsigned char smem[];
+    ulonglong2* sP = reinterpret_cast<ulonglong2*>(smem);                 // [kL][CB] (d, d, dx, dx)
+    float4* sA = reinterpret_cast<float4*>(sP + kL * CB);                 // [kK][kGT] A log2(e)
+    float4* sH = sA + kK * kGT;                                           // entering state
+    float4* sG = sH + kK * kGT;                                           // adjoint carried back
+    float4* sD = sG + kK * kGT;                                           // dA
+    f2* sY = reinterpret_cast<f2*>(sD + kK * kGT);                        // [kL][CB] (dY, dY)
+    float* sB = reinterpret_cast<float*>(sY + kL * CB);                   // [kL][N]
+    float* sC = sB + kL * N;
+    float* sR = sC + kL * N;                                              // [WARPS][2 kL N]
+    float* sQ = sR + K::WARPS * 2 * kL * N;                               // [kL][QP] q; then r, then C.h
+    float* sE = sQ + kL * QP;
+    float* sO = sE + kL * QP;
+    typedef typename Pack<TI, V>::Raw Raw;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int id = blockIdx.x;
+    const int cb = id % p.ncb;
+    id /= p.ncb;
+    const int g = id % p.G;
+    id /= p.G;
+    const int seg = id % p.nseg, b = id / p.nseg;
+    const int n = p.lengths ? min(max(__ldg(p.lengths + b), 0), p.T) : p.T;
+    const int s0 = seg * p.SL, s1 = min(s0 + p.SL, p.T), sn = min(s1, n);
+    const int64_t cg0 = (int64_t)g * p.Dg + cb * CB;   // first channel of the block
+    const int left = p.Dg - cb * CB;                    // channels of the block that exist
+
+    const int lc0 = (tid % PR) * V, r0 = tid / PR;
+    float bias[CI][V], skip[CI][V], accD[CI][V], accB[CI][V];
+#pragma unroll
+    for (int ci = 0; ci < CI; ++ci)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int lc = lc0 + ci * PR * V + j;
+            bias[ci][j] = p.bias && lc < left ? __ldg(p.bias + cg0 + lc) : 0.f;
+            skip[ci][j] = p.D && lc < left ? __ldg(p.D + cg0 + lc) : 0.f;
+            accD[ci][j] = accB[ci][j] = 0.f;
+        }
+    const int q = lane % LPC, cw = lane / LPC;
+    const int64_t seg_at = ((int64_t)seg * p.b + b) * p.Dch;
+#pragma unroll
+    for (int k = 0; k < kK; ++k) {
+        const int ch = k * K::CK + warp * CPW + cw;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), h = a, gg = a;
+        if (ch < left) {
+            const float* Ap = p.A + (cg0 + ch) * N + q * kNS;
+            a = make_float4(__ldg(Ap) * kLog2e, __ldg(Ap + 1) * kLog2e, __ldg(Ap + 2) * kLog2e, __ldg(Ap + 3) * kLog2e);
+            const int64_t o = (seg_at + cg0 + ch) * N + q * kNS;
+            if (p.h_in) h = make_float4(p.h_in[o], p.h_in[o + 1], p.h_in[o + 2], p.h_in[o + 3]);
+            if (p.g_in) gg = make_float4(p.g_in[o], p.g_in[o + 1], p.g_in[o + 2], p.g_in[o + 3]);
+        }
+        sA[k * kGT + tid] = a;
+        sH[k * kGT + tid] = h;
+        sG[k * kGT + tid] = gg;
+        sD[k * kGT + tid] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+
+    const int tiles = (s1 - s0 + kL - 1) / kL;
+    for (int ti = tiles - 1; ti >= 0; --ti) {
+        const int t0 = s0 + ti * kL;
+        Raw kx[CI][RI], kd[CI][RI], kz[CI][RI], ky[CI][RI];
+#pragma unroll
+        for (int ci = 0; ci < CI; ++ci)
+#pragma unroll
+            for (int i = 0; i < RI; ++i) {
+                const int r = r0 + i * RS, t = t0 + r, lc = lc0 + ci * PR * V;
+                if (r >= kL) continue;
+                const bool real = lc < left && t < sn;
+                kx[ci][i] = kd[ci][i] = kz[ci][i] = ky[ci][i] = zero_raw<Raw>();
+                const int64_t c = cg0 + lc;
+                if (real) {
+                    kx[ci][i] = load_raw<TI, V>(static_cast<const TI*>(p.x) + (int64_t)b * p.sx.b + (int64_t)t * p.sx.t + c);
+                    kd[ci][i] = load_raw<TI, V>(static_cast<const TI*>(p.dt) + (int64_t)b * p.sdt.b + (int64_t)t * p.sdt.t + c);
+                    if (GATE) kz[ci][i] = load_raw<TI, V>(static_cast<const TI*>(p.z) + (int64_t)b * p.sz.b + (int64_t)t * p.sz.t + c);
+                    ky[ci][i] = load_raw<TI, V>(static_cast<const TI*>(p.dy) + (int64_t)b * p.sy.b + (int64_t)t * p.sy.t + c);
+                }
+                float fx[V], fd[V], fz[V], fy[V];
+                Conv<TI, V>::to(kx[ci][i], fx);
+                Conv<TI, V>::to(kd[ci][i], fd);
+                Conv<TI, V>::to(kz[ci][i], fz);
+                Conv<TI, V>::to(ky[ci][i], fy);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float v = fd[j] + bias[ci][j];
+                    const float d = real ? (p.softplus ? softplus(v) : v) : 0.f;
+                    const int cc = lc + j;
+                    ulonglong2 w;
+                    w.x = dup2(d);
+                    w.y = dup2(d * fx[j]);
+                    sP[r * CB + (cc ^ ((cc >> 3) & 1))] = w;
+                    sY[r * CB + cc] = dup2(GATE ? fy[j] * fz[j] * sigmoid(fz[j]) : fy[j]);
+                }
+            }
+        for (int e = tid * V; e < kL * N; e += kGT * V) {
+            const int t = t0 + e / N;
+            float fb[V], fc[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) fb[j] = fc[j] = 0.f;
+            if (t < sn) {
+                const int64_t o = (int64_t)g * N + e % N;
+                Conv<TI, V>::to(load_raw<TI, V>(static_cast<const TI*>(p.B) + (int64_t)b * p.sB.b + (int64_t)t * p.sB.t + o), fb);
+                Conv<TI, V>::to(load_raw<TI, V>(static_cast<const TI*>(p.C) + (int64_t)b * p.sC.b + (int64_t)t * p.sC.t + o), fc);
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                sB[e + j] = fb[j];
+                sC[e + j] = fc[j];
+            }
+        }
+        __syncthreads();
+
+        f2 dBC[2][kL][2];   // dB, dC of the lane's states, summed over its channels
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int t = 0; t < kL; ++t) dBC[w][t][0] = dBC[w][t][1] = 0;
+        const int64_t ck_at = ((int64_t)b * p.nck + t0 / kL) * p.Dch + cg0;
+#pragma unroll 1
+        for (int k = 0; k < kK; ++k) {
+            const int ch = k * K::CK + warp * CPW + cw;
+            const ulonglong2* pP = sP + (ch ^ ((ch >> 3) & 1));
+            const f2* pY = sY + ch;
+            const ulonglong2 A2 = *reinterpret_cast<const ulonglong2*>(sA + k * kGT + tid);
+            f2 hs[kL + 1][2], as[kL][2];
+            {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                float cd = 0.f;
+                if (ch < left) {
+                    v = *reinterpret_cast<const float4*>(p.ck + (ck_at + ch) * N + q * kNS);
+                    cd = p.ck_d[ck_at + ch];
+                }
+                const ulonglong2 hi = *reinterpret_cast<const ulonglong2*>(sH + k * kGT + tid);
+                const f2 c2 = dup2(cd);
+                hs[0][0] = fma2(ex2_2(mul2(c2, A2.x)), hi.x, pack2(v.x, v.y));
+                hs[0][1] = fma2(ex2_2(mul2(c2, A2.y)), hi.y, pack2(v.z, v.w));
+            }
+#pragma unroll
+            for (int t = 0; t < kL; ++t) {
+                const ulonglong2 w = pP[t * CB];
+                const ulonglong2 Bv = *reinterpret_cast<const ulonglong2*>(sB + t * N + q * kNS);
+                as[t][0] = ex2_2(mul2(w.x, A2.x));
+                as[t][1] = ex2_2(mul2(w.x, A2.y));
+                hs[t + 1][0] = fma2(as[t][0], hs[t][0], mul2(w.y, Bv.x));
+                hs[t + 1][1] = fma2(as[t][1], hs[t][1], mul2(w.y, Bv.y));
+            }
+            ulonglong2 G = *reinterpret_cast<const ulonglong2*>(sG + k * kGT + tid);
+            ulonglong2 dA = *reinterpret_cast<const ulonglong2*>(sD + k * kGT + tid);
+#pragma unroll
+            for (int tb = kL - U; tb >= 0; tb -= U) {
+                float vq[U], ve[U], vo[U];
+#pragma unroll
+                for (int u = U - 1; u >= 0; --u) {
+                    const int t = tb + u;
+                    const ulonglong2 w = pP[t * CB];
+                    const ulonglong2 Bv = *reinterpret_cast<const ulonglong2*>(sB + t * N + q * kNS);
+                    const ulonglong2 Cv = *reinterpret_cast<const ulonglong2*>(sC + t * N + q * kNS);
+                    const f2 y2 = pY[t * CB];
+                    G.x = fma2(y2, Cv.x, G.x);
+                    G.y = fma2(y2, Cv.y, G.y);
+                    dBC[1][t][0] = fma2(y2, hs[t + 1][0], dBC[1][t][0]);
+                    dBC[1][t][1] = fma2(y2, hs[t + 1][1], dBC[1][t][1]);
+                    dBC[0][t][0] = fma2(w.y, G.x, dBC[0][t][0]);
+                    dBC[0][t][1] = fma2(w.y, G.y, dBC[0][t][1]);
+                    vq[u] = sum2(fma2(G.y, Bv.y, mul2(G.x, Bv.x)));
+                    if (GATE) vo[u] = sum2(fma2(hs[t + 1][1], Cv.y, mul2(hs[t + 1][0], Cv.x)));
+                    G.x = mul2(G.x, as[t][0]);
+                    G.y = mul2(G.y, as[t][1]);
+                    const f2 e0 = mul2(G.x, hs[t][0]), e1 = mul2(G.y, hs[t][1]);
+                    ve[u] = sum2(fma2(e1, A2.y, mul2(e0, A2.x)));
+                    dA.x = fma2(w.x, e0, dA.x);
+                    dA.y = fma2(w.x, e1, dA.y);
+                }
+                const int at = (tb + (lane & (U - 1))) * QP + ch;
+                const float fq = lanes_sum<LPC, U>(vq), fe = lanes_sum<LPC, U>(ve);
+                float fo = 0.f;
+                if (GATE) fo = lanes_sum<LPC, U>(vo);
+                if (LPC <= U || q < U) {
+                    sQ[at] = fq;
+                    sE[at] = fe;
+                    if (GATE) sO[at] = fo;
+                }
+            }
+            *reinterpret_cast<ulonglong2*>(sG + k * kGT + tid) = G;
+            *reinterpret_cast<ulonglong2*>(sD + k * kGT + tid) = dA;
+        }
+        // dB, dC: over the warp's channels, then its warps.  Values are numbered
+        // ((which kL) + t) 4 + state.
+        {
+            float v[8 * kL];
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+                for (int t = 0; t < kL; ++t) {
+                    unpack2(dBC[w][t][0], v[(w * kL + t) * 4], v[(w * kL + t) * 4 + 1]);
+                    unpack2(dBC[w][t][1], v[(w * kL + t) * 4 + 2], v[(w * kL + t) * 4 + 3]);
+                }
+            channel_sum<8 * kL, CPW, LPC>(v);
+#pragma unroll
+            for (int i = 0; i < 8 * kL / CPW; ++i) {
+                const int e = cw + CPW * i, wt = e >> 2, s = e & 3;   // wt = which kL + t
+                sR[(warp * 2 * kL + wt) * N + q * kNS + s] = v[i];
+            }
+        }
+        __syncthreads();
+        for (int e = tid; e < 2 * kL * N; e += kGT) {
+            const int wt = e / N, t = t0 + wt % kL;
+            float a = 0.f;
+#pragma unroll
+            for (int w = 0; w < K::WARPS; ++w) a += sR[w * 2 * kL * N + e];
+            if (t < s1)
+                p.part_bc[(((int64_t)cb * p.b * p.T + (int64_t)b * p.T + t) * p.G + g) * (2 * N) + (wt / kL) * N + e % N] = a;
+        }
+#pragma unroll
+        for (int ci = 0; ci < CI; ++ci)
+#pragma unroll
+            for (int i = 0; i < RI; ++i) {
+                const int r = r0 + i * RS, t = t0 + r, lc = lc0 + ci * PR * V;
+                if (r >= kL || lc >= left || t >= s1) continue;
+                const bool real = t < sn;
+                float fx[V], fd[V], fz[V], fy[V], ox[V], od[V], oz[V];
+                Conv<TI, V>::to(kx[ci][i], fx);
+                Conv<TI, V>::to(kd[ci][i], fd);
+                Conv<TI, V>::to(kz[ci][i], fz);
+                Conv<TI, V>::to(ky[ci][i], fy);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const int cc = lc + j;
+                    const float v = fd[j] + bias[ci][j];
+                    float d, dup;
+                    unpack2(sP[r * CB + (cc ^ ((cc >> 3) & 1))].x, d, dup);
+                    float dY = fy[j], slope = 0.f;
+                    if (GATE) {
+                        const float sg = sigmoid(fz[j]);
+                        dY = fy[j] * fz[j] * sg;
+                        slope = fy[j] * sg * fmaf(fz[j], 1.f - sg, 1.f);
+                    }
+                    const float qv = sQ[r * QP + cc], dd = fmaf(fx[j], qv, 0.6931471805599453f * sE[r * QP + cc]);
+                    ox[j] = fmaf(d, qv, skip[ci][j] * dY);
+                    od[j] = real ? (p.softplus ? dd * sigmoid(v) : dd) : 0.f;
+                    oz[j] = GATE ? slope * fmaf(skip[ci][j], fx[j], sO[r * QP + cc]) : 0.f;
+                    accD[ci][j] = fmaf(dY, fx[j], accD[ci][j]);
+                    accB[ci][j] += od[j];
+                }
+                const int64_t o = ((int64_t)b * p.T + t) * p.Dch + cg0 + lc;
+                store_raw<TI, V>(static_cast<TI*>(p.dx) + o, Conv<TI, V>::from(ox));
+                store_raw<TI, V>(static_cast<TI*>(p.ddt) + o, Conv<TI, V>::from(od));
+                if (GATE) store_raw<TI, V>(static_cast<TI*>(p.dz) + o, Conv<TI, V>::from(oz));
+            }
+        __syncthreads();
+    }
+    // dA, dinit
+#pragma unroll
+    for (int k = 0; k < kK; ++k) {
+        const int ch = k * K::CK + warp * CPW + cw;
+        if (ch < left) {
+            const int64_t o = (((int64_t)b * p.nseg + seg) * p.Dch + cg0 + ch) * N + q * kNS;
+            *reinterpret_cast<float4*>(p.part_A + o) = sD[k * kGT + tid];
+            if (p.dinit && seg == 0) {
+                const float4 v = sG[k * kGT + tid];
+                float* f = p.dinit + ((int64_t)b * p.Dch + cg0 + ch) * N + q * kNS;
+                f[0] = v.x;
+                f[1] = v.y;
+                f[2] = v.z;
+                f[3] = v.w;
+            }
+        }
+    }
+    // dD, ddt_bias: over the block's rows, through the q tile (RS <= kL rows of it)
+    __syncthreads();
+    if (r0 < kL)
+#pragma unroll
+    for (int ci = 0; ci < CI; ++ci)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            sQ[r0 * QP + lc0 + ci * PR * V + j] = accD[ci][j];
+            sE[r0 * QP + lc0 + ci * PR * V + j] = accB[ci][j];
+        }
+    __syncthreads();
+    for (int c = tid; c < CB && c < left; c += kGT) {
+        float a = 0.f, d = 0.f;
+#pragma unroll
+        for (int r = 0; r < (RS < kL ? RS : kL); ++r) {
+            a += sQ[r * QP + c];
+            d += sE[r * QP + c];
+        }
+        float* o = p.part_v + ((int64_t)b * p.nseg + seg) * 2 * p.Dch + cg0 + c;
+        o[0] = a;
+        o[p.Dch] = d;
+    }
+}
+
+// dB, dC [b,T,G,N] in the I/O type: the sum over the channel blocks of a group.
+template <typename TI>
+__global__ void __launch_bounds__(256)
+scan_bc_sum_kernel(const float* __restrict__ part, int ncb, int64_t rows, int N, TI* __restrict__ dB,
+                   TI* __restrict__ dC) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, total = rows * 2 * N;
+    if (i >= total) return;
+    float a = 0.f;
+    for (int s = 0; s < ncb; ++s) a += __ldg(part + s * total + i);
+    const int64_t row = i / (2 * N);
+    const int e = (int)(i - row * 2 * N);
+    if (e < N) dB[row * N + e] = from_f32<TI>(a);
+    else dC[row * N + e - N] = from_f32<TI>(a);
+}
+
+struct Plan {
+    int64_t SL, nseg, nck, ncb, blocks_local;
+    size_t ck, ck_d, seg, seg_d, bc, A, v, total;
+};
+
+// Stretches: enough that the gradient kernel's blocks (two an SM) go around about
+// four times, none shorter than two tiles of the first pass.
+Plan plan_of(const ScanArgs& a) {
+    Plan p;
+    const int64_t Dg = a.D / a.G, lpc = a.N / kNS;
+    const int64_t CB = (kGT / lpc) * kK;
+    p.ncb = (Dg + CB - 1) / CB;
+    const int64_t tt = a.N >= 128 ? 64 : 32;
+    const int64_t per = std::max<int64_t>(1, a.b * a.G * p.ncb), want = (int64_t)sm_count() * 8;
+    const int64_t n = std::max<int64_t>(1, std::min<int64_t>((want + per - 1) / per, a.T / (2 * tt)));
+    p.SL = std::max<int64_t>(tt, ((a.T + n - 1) / n + tt - 1) / tt * tt);
+    p.nseg = std::max<int64_t>(1, (a.T + p.SL - 1) / p.SL);
+    p.nck = (a.T + kL - 1) / kL;
+    auto al = [](size_t v) { return (v + 255) & ~size_t(255); };
+    const size_t f = sizeof(float);
+    size_t o = 0;
+    auto take = [&](size_t& at, size_t bytes) { at = o; o += al(bytes); };
+    take(p.ck, f * (size_t)(a.b * p.nck * a.D * a.N));
+    take(p.ck_d, f * (size_t)(a.b * p.nck * a.D));
+    take(p.seg, p.nseg > 1 ? 2 * f * (size_t)(p.nseg * a.b * a.D * a.N) : 0);
+    take(p.seg_d, p.nseg > 1 ? f * (size_t)(p.nseg * a.b * a.D) : 0);
+    take(p.bc, f * (size_t)(p.ncb * a.b * a.T * a.G * 2 * a.N));
+    take(p.A, f * (size_t)(p.nseg * a.b * a.D * a.N));
+    take(p.v, f * (size_t)(p.nseg * a.b * 2 * a.D));
+    p.total = o;
+    return p;
+}
+
+template <typename KT> cudaError_t allow(KT k, size_t smem) {
+    return smem > 48 * 1024 ? cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
+                            : cudaSuccess;
+}
+
+template <typename TI, int N, int V>
+cudaError_t bwd_v(const BwdP& p, int64_t lncb, const float* init, const float* dfinal, cudaStream_t st) {
+    using L = Cfg<N>;
+    const bool adj = p.nseg > 1;
+    const size_t ls = (size_t)L::TT * (L::CB * (adj ? 24 : 16) + 2 * N * 4);
+    const int64_t lb = p.b * p.nseg * p.G * lncb, gb = p.b * p.nseg * p.G * p.ncb;
+    const int64_t total = p.b * p.Dch * N;
+    if (lb >= (int64_t(1) << 31) || gb >= (int64_t(1) << 31) || (total + 255) / 256 >= (int64_t(1) << 31))
+        return cudaErrorInvalidValue;
+    BwdP l = p;
+    l.ncb = (int)lncb;
+    auto lk = adj ? scan_local_kernel<TI, N, V, true> : scan_local_kernel<TI, N, V, false>;
+    cudaError_t e = allow(lk, ls);
+    if (e != cudaSuccess) return e;
+    lk<<<(unsigned)lb, L::NT, ls, st>>>(l);
+    BwdP m = p;
+    if (adj) {
+        scan_join2_kernel<<<(unsigned)((total + 255) / 256), 256, 0, st>>>(
+            p.seg_h, p.seg_g, p.seg_d, p.A, init, dfinal, total, (int64_t)p.Dch * N, N, p.nseg);
+        m.h_in = p.seg_h;
+        m.g_in = p.seg_g;
+    } else {
+        m.h_in = init;
+        m.g_in = dfinal;
+    }
+    auto gk = p.z ? scan_grad_kernel<TI, N, V, true> : scan_grad_kernel<TI, N, V, false>;
+    e = allow(gk, GCfg<N>::smem);
+    if (e != cudaSuccess) return e;
+    gk<<<(unsigned)gb, kGT, GCfg<N>::smem, st>>>(m);
+    return cudaGetLastError();
+}
+
+template <typename TI, int N>
+cudaError_t bwd_n(const ScanArgs& a, const BwdP& p, const float* init, const float* dfinal, cudaStream_t st) {
+    const int64_t es = sizeof(TI), by = 2 * es, lncb = (p.Dg + Cfg<N>::CB - 1) / Cfg<N>::CB;
+    const Tok row{0, a.D};
+    const bool two = p.Dg % 2 == 0 && vec_ok(p.x, a.sx, by, es) && vec_ok(p.dt, a.sdt, by, es) &&
+                     vec_ok(p.B, a.sB, by, es) && vec_ok(p.C, a.sC, by, es) &&
+                     (!p.z || (vec_ok(p.z, a.sz, by, es) && vec_ok(p.dz, row, by, es))) &&
+                     vec_ok(p.dy, a.sy, by, es) && vec_ok(p.dx, row, by, es) && vec_ok(p.ddt, row, by, es);
+    return two ? bwd_v<TI, N, 2>(p, lncb, init, dfinal, st) : bwd_v<TI, N, 1>(p, lncb, init, dfinal, st);
+}
+
+}  // namespace
+
+size_t scan_bwd_workspace(const ScanArgs& a) { return a.b * a.T * a.D ? plan_of(a).total : 0; }
+
+cudaError_t launch_scan_bwd(const ScanArgs& a, const void* x, const void* dt, const float* A, const void* B,
+                            const void* C, const float* D, const void* z, const float* dt_bias,
+                            const float* init, const void* dy, const float* dfinal, const int32_t* lengths,
+                            const ScanGrads& g, void* ws, cudaStream_t st) {
+    if (a.D == 0) return cudaSuccess;
+    const size_t f = sizeof(float), states = f * (size_t)(a.b * a.D * a.N);
+    if (a.b * a.T == 0) {   // nothing was computed from the parameters; the state passes through
+        cudaError_t e = cudaMemsetAsync(g.dA, 0, f * (size_t)(a.D * a.N), st);
+        if (e == cudaSuccess && g.dD) e = cudaMemsetAsync(g.dD, 0, f * (size_t)a.D, st);
+        if (e == cudaSuccess && g.ddt_bias) e = cudaMemsetAsync(g.ddt_bias, 0, f * (size_t)a.D, st);
+        if (e == cudaSuccess && g.dinit && states)
+            e = dfinal ? cudaMemcpyAsync(g.dinit, dfinal, states, cudaMemcpyDeviceToDevice, st)
+                       : cudaMemsetAsync(g.dinit, 0, states, st);
+        return e;
+    }
+    const Plan pl = plan_of(a);
+    char* w = static_cast<char*>(ws);
+    BwdP p = {};
+    p.x = x, p.dt = dt, p.B = B, p.C = C, p.z = z, p.dy = dy, p.A = A, p.D = D, p.bias = dt_bias;
+    p.lengths = lengths;
+    p.ck = reinterpret_cast<float*>(w + pl.ck), p.ck_d = reinterpret_cast<float*>(w + pl.ck_d);
+    p.seg_h = reinterpret_cast<float*>(w + pl.seg);
+    p.seg_g = p.seg_h + pl.nseg * a.b * a.D * a.N;
+    p.seg_d = reinterpret_cast<float*>(w + pl.seg_d);
+    p.dx = g.dx, p.ddt = g.ddt, p.dz = g.dz, p.dinit = g.dinit;
+    p.part_bc = reinterpret_cast<float*>(w + pl.bc), p.part_A = reinterpret_cast<float*>(w + pl.A);
+    p.part_v = reinterpret_cast<float*>(w + pl.v);
+    p.T = (int)a.T, p.Dch = (int)a.D, p.G = (int)a.G, p.Dg = (int)(a.D / a.G), p.ncb = (int)pl.ncb;
+    p.nseg = (int)pl.nseg, p.SL = (int)pl.SL, p.nck = (int)pl.nck, p.softplus = a.softplus, p.b = a.b;
+    p.sx = a.sx, p.sdt = a.sdt, p.sB = a.sB, p.sC = a.sC, p.sz = a.sz, p.sy = a.sy;
+    auto go = [&](auto f16, auto f32) {
+        return a.dtype == 1 ? f16(a, p, init, dfinal, st) : f32(a, p, init, dfinal, st);
+    };
+    cudaError_t e = cudaErrorInvalidValue;
+    switch (a.N) {
+        case 8: e = go(bwd_n<__nv_bfloat16, 8>, bwd_n<float, 8>); break;
+        case 16: e = go(bwd_n<__nv_bfloat16, 16>, bwd_n<float, 16>); break;
+        case 32: e = go(bwd_n<__nv_bfloat16, 32>, bwd_n<float, 32>); break;
+        case 64: e = go(bwd_n<__nv_bfloat16, 64>, bwd_n<float, 64>); break;
+        case 128: e = go(bwd_n<__nv_bfloat16, 128>, bwd_n<float, 128>); break;
+    }
+    if (e != cudaSuccess) return e;
+    const int64_t rows = a.b * a.T * a.G, blocks = (rows * 2 * a.N + 255) / 256;
+    if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    if (a.dtype == 1)
+        scan_bc_sum_kernel<<<(unsigned)blocks, 256, 0, st>>>(p.part_bc, p.ncb, rows, (int)a.N,
+                                                            static_cast<__nv_bfloat16*>(g.dB),
+                                                            static_cast<__nv_bfloat16*>(g.dC));
+    else
+        scan_bc_sum_kernel<<<(unsigned)blocks, 256, 0, st>>>(p.part_bc, p.ncb, rows, (int)a.N,
+                                                            static_cast<float*>(g.dB), static_cast<float*>(g.dC));
+    e = cudaGetLastError();
+    const int64_t slots = pl.nseg * a.b;
+    if (e == cudaSuccess) e = launch_column_sum(p.part_A, slots, a.D * a.N, g.dA, a.D * a.N, nullptr, st);
+    if (e == cudaSuccess && (g.dD || g.ddt_bias))
+        e = launch_column_sum(p.part_v, slots, 2 * a.D, g.dD, a.D, g.ddt_bias, st);
+    return e;
+}
+
+}  // namespace m2

@@ -1,0 +1,418 @@
+// scan_fwd.cu -- selective scan with a decay per channel and state (include/mamba2_layer.h):
+// the forward pass and the single-token step.
+//
+//   h_t[c,n] = exp(d_t[c] A[c,n]) h_{t-1}[c,n] + d_t[c] x_t[c] B_t[n]
+//   y_t[c]   = sum_n C_t[n] h_t[c,n] + D[c] x_t[c]     (times silu(z_t[c]))
+//
+// Unlike the chunked scan's one decay per head, the decay differs for every (c, n),
+// so there is no matrix product to regroup: per (t, c, n) the pass needs one
+// exponential and four multiply-adds, and it is bound by those pipes, not by bytes.
+#include <algorithm>
+
+#include "internal.h"
+#include "scan.cuh"
+
+namespace m2 {
+namespace {
+
+struct FwdP {
+    const void *x, *dt, *B, *C, *z;
+    const float *A, *D, *bias, *init;
+    const int32_t* lengths;
+    void* y;
+    float* fin;
+    float* seg_h;     // [nseg][b][D][N]: local final states, then incoming states
+    float* seg_d;     // [nseg][b][D]: sums of d
+    int T, Dch, G, Dg, ncb, nseg, SL, softplus;
+    int64_t b;
+    Tok sx, sdt, sB, sC, sz, sy;
+};
+
+// STATES: only the segment's final state from zero and its sum of d (first of the
+// two passes when the token axis is split).  V: channels per access of x, dt, z, y
+// and elements per access of B, C.
+template <typename TI, int N, int V, bool STATES>
+__global__ void __launch_bounds__(Cfg<N>::NT)
+scan_fwd_kernel(const FwdP p) {
+    using K = Cfg<N>;
+    constexpr int NT = K::NT, LPC = K::LPC, CB = K::CB, TT = K::TT, U = K::U, YP = K::YP;
+    constexpr int PR = CB / V, RS = NT / PR, IT = TT / RS;        // threads a row, rows a pass, passes
+    constexpr int BI = TT * N / V / NT;                            // accesses of B (and of C) a thread
+    static_assert(IT >= 1 && RS * IT == TT && BI >= 1, "tile shape");
+    extern __shared__ __align__(16) unsigned char smem[];
+    ulonglong2* sP = reinterpret_cast<ulonglong2*>(smem);                       // [TT][CB] (d, d, dx, dx)
+    float* sB = reinterpret_cast<float*>(smem + (size_t)TT * CB * 16);          // [TT][N]
+    float* sC = sB + TT * N;
+    float* sY = sC + TT * N;                                                    // [TT][YP]
+    typedef typename Pack<TI, V>::Raw Raw;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int id = blockIdx.x;
+    const int cb = id % p.ncb;
+    id /= p.ncb;
+    const int g = id % p.G;
+    id /= p.G;
+    const int seg = id % p.nseg, b = id / p.nseg;
+    const int n = p.lengths ? min(max(__ldg(p.lengths + b), 0), p.T) : p.T;
+    const int s0 = seg * p.SL, s1 = min(s0 + p.SL, p.T);
+
+    // tile duty: V channels of rows r0, r0 + RS, ...
+    const int lc = (tid % PR) * V, r0 = tid / PR;
+    const int cg = cb * CB + lc;                       // channel inside the group
+    const bool con = cg < p.Dg;
+    const int64_t c = (int64_t)g * p.Dg + cg;
+    const TI* xp = static_cast<const TI*>(p.x) + (int64_t)b * p.sx.b + c;
+    const TI* dp = static_cast<const TI*>(p.dt) + (int64_t)b * p.sdt.b + c;
+    const TI* zp = static_cast<const TI*>(p.z) + (int64_t)b * p.sz.b + c;
+    TI* yp = static_cast<TI*>(p.y) + (int64_t)b * p.sy.b + c;
+    const TI* Bp = static_cast<const TI*>(p.B) + (int64_t)b * p.sB.b + (int64_t)g * N;
+    const TI* Cp = static_cast<const TI*>(p.C) + (int64_t)b * p.sC.b + (int64_t)g * N;
+    float bias[V], skip[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        bias[j] = p.bias && con ? __ldg(p.bias + c + j) : 0.f;
+        skip[j] = p.D && con && !STATES ? __ldg(p.D + c + j) : 0.f;
+    }
+
+    // scan duty: states q kNS .. of channel ch
+    const int q = lane % LPC, ch = warp * K::CPW + lane / LPC;
+    const bool on = cb * CB + ch < p.Dg;
+    const int64_t sc = ((int64_t)b * p.Dch + (int64_t)g * p.Dg + cb * CB + ch) * N + q * kNS;   // in [b][D][N]
+    const int64_t seg_off = (int64_t)seg * p.b * p.Dch * N;
+    f2 A2[kNS / 2], h[kNS / 2];
+    {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), v = a;
+        if (on) {
+            const float* Ap = p.A + ((int64_t)g * p.Dg + cb * CB + ch) * N + q * kNS;
+            a = make_float4(__ldg(Ap), __ldg(Ap + 1), __ldg(Ap + 2), __ldg(Ap + 3));
+            const float* hp = STATES ? nullptr : p.nseg > 1 ? p.seg_h + seg_off + sc : p.init ? p.init + sc : nullptr;
+            if (hp) v = make_float4(hp[0], hp[1], hp[2], hp[3]);
+        }
+        A2[0] = pack2(a.x * kLog2e, a.y * kLog2e);
+        A2[1] = pack2(a.z * kLog2e, a.w * kLog2e);
+        h[0] = pack2(v.x, v.y);
+        h[1] = pack2(v.z, v.w);
+    }
+    float dsum = 0.f;
+
+    Raw rx[IT], rd[IT], rz[IT], rB[BI], rC[BI];
+    auto load = [&](int t0) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int t = t0 + r0 + i * RS;
+            rx[i] = rd[i] = rz[i] = zero_raw<Raw>();
+            if (con && t < min(n, s1)) {
+                rx[i] = load_raw<TI, V>(xp + (int64_t)t * p.sx.t);
+                rd[i] = load_raw<TI, V>(dp + (int64_t)t * p.sdt.t);
+                if (!STATES && p.z) rz[i] = load_raw<TI, V>(zp + (int64_t)t * p.sz.t);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < BI; ++i) {
+            const int e = (tid + i * NT) * V, t = t0 + e / N;
+            rB[i] = rC[i] = zero_raw<Raw>();
+            if (t < min(n, s1)) {
+                rB[i] = load_raw<TI, V>(Bp + (int64_t)t * p.sB.t + e % N);
+                if (!STATES) rC[i] = load_raw<TI, V>(Cp + (int64_t)t * p.sC.t + e % N);
+            }
+        }
+    };
+    load(s0);
+    for (int t0 = s0; t0 < s1; t0 += TT) {
+        if (t0 >= n) {   // padding only
+            if (!STATES && con)
+#pragma unroll
+                for (int i = 0; i < IT; ++i) {
+                    const int t = t0 + r0 + i * RS;
+                    if (t < s1) store_raw<TI, V>(yp + (int64_t)t * p.sy.t, zero_raw<Raw>());
+                }
+            continue;
+        }
+        Raw kx[IT], kz[IT];   // kept for the epilogue while the next tile loads
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            float fx[V], fd[V];
+            Conv<TI, V>::to(rx[i], fx);
+            Conv<TI, V>::to(rd[i], fd);
+            kx[i] = rx[i];
+            kz[i] = rz[i];
+            const int r = r0 + i * RS;
+            const bool real = con && t0 + r < min(n, s1);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float v = fd[j] + bias[j];
+                const float d = real ? (p.softplus ? softplus(v) : v) : 0.f;
+                const int cc = lc + j;
+                ulonglong2 w;
+                w.x = dup2(d);
+                w.y = dup2(d * fx[j]);
+                sP[r * CB + (cc ^ ((cc >> 3) & 1))] = w;   // swizzled: conflict-free 16-byte stores
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < BI; ++i) {
+            const int e = (tid + i * NT) * V;
+            float f[V];
+            Conv<TI, V>::to(rB[i], f);
+#pragma unroll
+            for (int j = 0; j < V; ++j) sB[e + j] = f[j];
+            if (!STATES) {
+                Conv<TI, V>::to(rC[i], f);
+#pragma unroll
+                for (int j = 0; j < V; ++j) sC[e + j] = f[j];
+            }
+        }
+        __syncthreads();
+        if (t0 + TT < s1) load(t0 + TT);
+        const ulonglong2* pP = sP + (ch ^ ((ch >> 3) & 1));
+        const float* pB = sB + q * kNS;
+        const float* pC = sC + q * kNS;
+#pragma unroll 1
+        for (int tb = 0; tb < TT; tb += U) {
+            float yv[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const ulonglong2 w = pP[(tb + u) * CB];
+                const ulonglong2 Bv = *reinterpret_cast<const ulonglong2*>(pB + (tb + u) * N);
+                h[0] = fma2(ex2_2(mul2(w.x, A2[0])), h[0], mul2(w.y, Bv.x));
+                h[1] = fma2(ex2_2(mul2(w.x, A2[1])), h[1], mul2(w.y, Bv.y));
+                if (STATES) {
+                    float lo, hi;
+                    unpack2(w.x, lo, hi);
+                    dsum += lo;
+                } else {
+                    const ulonglong2 Cv = *reinterpret_cast<const ulonglong2*>(pC + (tb + u) * N);
+                    yv[u] = sum2(fma2(h[1], Cv.y, mul2(h[0], Cv.x)));
+                }
+            }
+            if (!STATES) {
+                const float s = lanes_sum<LPC, U>(yv);
+                if (LPC <= U || q < U) sY[(tb + (lane & (U - 1))) * YP + ch] = s;
+            }
+        }
+        __syncthreads();
+        if (!STATES && con) {
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const int r = r0 + i * RS, t = t0 + r;
+                float fx[V], fz[V], o[V];
+                Conv<TI, V>::to(kx[i], fx);
+                if (p.z) Conv<TI, V>::to(kz[i], fz);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    float v = fmaf(skip[j], fx[j], sY[r * YP + lc + j]);
+                    if (p.z) v *= fz[j] * sigmoid(fz[j]);
+                    o[j] = t < n ? v : 0.f;
+                }
+                if (t < s1) store_raw<TI, V>(yp + (int64_t)t * p.sy.t, Conv<TI, V>::from(o));
+            }
+        }
+    }
+    if (!on) return;
+    float4 v;
+    unpack2(h[0], v.x, v.y);
+    unpack2(h[1], v.z, v.w);
+    if (STATES) {
+        *reinterpret_cast<float4*>(p.seg_h + seg_off + sc) = v;
+        if (q == 0) p.seg_d[((int64_t)seg * p.b + b) * p.Dch + (int64_t)g * p.Dg + cb * CB + ch] = dsum;
+    } else if (seg == p.nseg - 1) {
+        float* f = p.fin + sc;
+        f[0] = v.x;
+        f[1] = v.y;
+        f[2] = v.z;
+        f[3] = v.w;
+    }
+}
+
+// The states entering each segment: h = init; for each segment: in = h, h = exp(A
+// sum d) h + local.  One thread per (b, c, n).
+__global__ void __launch_bounds__(256)
+scan_join_kernel(float* __restrict__ seg_h, const float* __restrict__ seg_d, const float* __restrict__ A,
+                 const float* __restrict__ init, int64_t total, int64_t DN, int N, int nseg) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= total) return;
+    const float a = __ldg(A + i % DN) * kLog2e;
+    float h = init ? init[i] : 0.f;
+    const int64_t bd = i / N, nbd = total / N;
+    for (int s = 0; s < nseg; ++s) {
+        const float local = seg_h[s * total + i], d = seg_d[s * nbd + bd];
+        seg_h[s * total + i] = h;
+        h = fmaf(ex2(a * d), h, local);
+    }
+}
+
+// One token.  A lane owns four states of a channel (one 16-byte access), N / 4
+// neighbouring lanes a channel.
+template <typename TI, int N>
+__global__ void __launch_bounds__(256)
+scan_step_kernel(float* __restrict__ state, const TI* __restrict__ x, const TI* __restrict__ dt,
+                 const float* __restrict__ A, const TI* __restrict__ B, const TI* __restrict__ C,
+                 const float* __restrict__ D, const TI* __restrict__ z, const float* __restrict__ bias,
+                 TI* __restrict__ y, int64_t total, int Dch, int Dg, int softplus_on, int wide,
+                 int64_t sx, int64_t sdt, int64_t sB, int64_t sC, int64_t sz, int64_t sy) {
+    constexpr int LPC = N / 4;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const bool on = i < total;                 // whole channels: total is a multiple of LPC
+    const int64_t ch = on ? i / LPC : 0;
+    const int qn = on ? (int)(i % LPC) * 4 : 0;
+    const int64_t b = ch / Dch;
+    const int c = (int)(ch - b * Dch), g = c / Dg;
+    float* sp = state + ch * N + qn;
+    const float* Ap = A + (int64_t)c * N + qn;
+    float h[4], a[4], Bv[4], Cv[4];
+    if (wide) {
+        const float4 v = *reinterpret_cast<const float4*>(sp), w = __ldg(reinterpret_cast<const float4*>(Ap));
+        h[0] = v.x, h[1] = v.y, h[2] = v.z, h[3] = v.w;
+        a[0] = w.x, a[1] = w.y, a[2] = w.z, a[3] = w.w;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = sp[k], a[k] = __ldg(Ap + k);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        Bv[k] = to_f32(B[b * sB + (int64_t)g * N + qn + k]);
+        Cv[k] = to_f32(C[b * sC + (int64_t)g * N + qn + k]);
+    }
+    const float xv = to_f32(x[b * sx + c]), zv = z ? to_f32(z[b * sz + c]) : 0.f;
+    const float raw = to_f32(dt[b * sdt + c]) + (bias ? __ldg(bias + c) : 0.f);
+    const float skip = D ? __ldg(D + c) : 0.f;
+    const float d = softplus_on ? softplus(raw) : raw, dx = d * xv;
+    float acc = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        h[k] = fmaf(ex2(d * (a[k] * kLog2e)), h[k], dx * Bv[k]);
+        acc = fmaf(h[k], Cv[k], acc);
+    }
+#pragma unroll
+    for (int o = 1; o < LPC; o <<= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if (!on) return;
+    if (wide) {
+        *reinterpret_cast<float4*>(sp) = make_float4(h[0], h[1], h[2], h[3]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sp[k] = h[k];
+    }
+    if (qn == 0) {
+        acc = fmaf(skip, xv, acc);
+        if (z) acc *= zv * sigmoid(zv);
+        y[b * sy + c] = from_f32<TI>(acc);
+    }
+}
+
+// Splitting the token axis costs a second pass over it (the first without y), so
+// it is done only where one pass leaves most of the GPU without warps.
+int64_t warps_of(const ScanArgs& a) {
+    const int64_t Dg = a.D / a.G, nt = a.N >= 64 ? 256 : 128, CB = nt / (a.N / kNS);
+    return a.b * a.G * ((Dg + CB - 1) / CB) * (nt / 32);
+}
+int64_t tile_of(const ScanArgs& a) { return a.N >= 128 ? 64 : 32; }
+int64_t seg_len(const ScanArgs& a) {
+    const int64_t tt = tile_of(a), full = (int64_t)sm_count() * 16, w = std::max<int64_t>(1, warps_of(a));
+    if (2 * w >= full) return std::max<int64_t>(tt, (a.T + tt - 1) / tt * tt);
+    const int64_t n = std::min<int64_t>((full + w - 1) / w, std::max<int64_t>(1, a.T / (2 * tt)));
+    return std::max<int64_t>(tt, ((a.T + n - 1) / n + tt - 1) / tt * tt);
+}
+
+template <typename TI, int N, int V>
+cudaError_t fwd_v(const FwdP& p, cudaStream_t st) {
+    using K = Cfg<N>;
+    const int64_t blocks = p.b * p.nseg * p.G * p.ncb;
+    if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    auto k = scan_fwd_kernel<TI, N, V, false>;
+    auto s = scan_fwd_kernel<TI, N, V, true>;
+    if (K::smem > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::smem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(s, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::smem);
+        if (e != cudaSuccess) return e;
+    }
+    if (p.nseg > 1) {
+        s<<<(unsigned)blocks, K::NT, K::smem, st>>>(p);
+        const int64_t total = p.b * p.Dch * N;
+        scan_join_kernel<<<(unsigned)((total + 255) / 256), 256, 0, st>>>(p.seg_h, p.seg_d, p.A, p.init, total,
+                                                                         (int64_t)p.Dch * N, N, p.nseg);
+    }
+    k<<<(unsigned)blocks, K::NT, K::smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename TI, int N> cudaError_t fwd_n(const ScanArgs& a, FwdP p, cudaStream_t st) {
+    p.ncb = (int)((p.Dg + Cfg<N>::CB - 1) / Cfg<N>::CB);
+    const int64_t es = sizeof(TI), by = 2 * es;
+    const bool two = p.Dg % 2 == 0 && vec_ok(p.x, a.sx, by, es) && vec_ok(p.dt, a.sdt, by, es) &&
+                     vec_ok(p.B, a.sB, by, es) && vec_ok(p.C, a.sC, by, es) &&
+                     (!p.z || vec_ok(p.z, a.sz, by, es)) && vec_ok(p.y, a.sy, by, es);
+    return two ? fwd_v<TI, N, 2>(p, st) : fwd_v<TI, N, 1>(p, st);
+}
+
+}  // namespace
+
+int64_t scan_fwd_segments(const ScanArgs& a) {
+    if (a.T == 0) return 1;
+    const int64_t sl = seg_len(a);
+    return (a.T + sl - 1) / sl;
+}
+
+cudaError_t launch_scan_fwd(const ScanArgs& a, const void* x, const void* dt, const float* A, const void* B,
+                            const void* C, const float* D, const void* z, const float* dt_bias,
+                            const float* init, const int32_t* lengths, void* y, float* fin, float* ws,
+                            cudaStream_t st) {
+    if (a.b == 0 || a.D == 0) return cudaSuccess;
+    if (a.T == 0) {
+        const size_t bytes = sizeof(float) * (size_t)(a.b * a.D * a.N);
+        return init ? cudaMemcpyAsync(fin, init, bytes, cudaMemcpyDeviceToDevice, st)
+                    : cudaMemsetAsync(fin, 0, bytes, st);
+    }
+    FwdP p;
+    p.x = x, p.dt = dt, p.B = B, p.C = C, p.z = z, p.A = A, p.D = D, p.bias = dt_bias, p.init = init;
+    p.lengths = lengths, p.y = y, p.fin = fin;
+    p.T = (int)a.T, p.Dch = (int)a.D, p.G = (int)a.G, p.Dg = (int)(a.D / a.G), p.softplus = a.softplus;
+    p.SL = (int)seg_len(a), p.nseg = (int)scan_fwd_segments(a), p.b = a.b, p.ncb = 0;
+    p.seg_h = ws, p.seg_d = ws ? ws + (int64_t)p.nseg * a.b * a.D * a.N : nullptr;
+    p.sx = a.sx, p.sdt = a.sdt, p.sB = a.sB, p.sC = a.sC, p.sz = a.sz, p.sy = a.sy;
+    auto go = [&](auto f16, auto f32) { return a.dtype == 1 ? f16(a, p, st) : f32(a, p, st); };
+    switch (a.N) {
+        case 8: return go(fwd_n<__nv_bfloat16, 8>, fwd_n<float, 8>);
+        case 16: return go(fwd_n<__nv_bfloat16, 16>, fwd_n<float, 16>);
+        case 32: return go(fwd_n<__nv_bfloat16, 32>, fwd_n<float, 32>);
+        case 64: return go(fwd_n<__nv_bfloat16, 64>, fwd_n<float, 64>);
+        case 128: return go(fwd_n<__nv_bfloat16, 128>, fwd_n<float, 128>);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+namespace {
+template <typename TI>
+cudaError_t step_t(const ScanArgs& a, float* state, const void* x, const void* dt, const float* A,
+                   const void* B, const void* C, const float* D, const void* z, const float* bias, void* y,
+                   cudaStream_t st) {
+    const int64_t total = a.b * a.D * (a.N / 4), blocks = (total + 255) / 256;
+    if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    const int wide = reinterpret_cast<uintptr_t>(state) % 16 == 0 && reinterpret_cast<uintptr_t>(A) % 16 == 0;
+    auto go = [&](auto k) {
+        k<<<(unsigned)blocks, 256, 0, st>>>(
+            state, static_cast<const TI*>(x), static_cast<const TI*>(dt), A, static_cast<const TI*>(B),
+            static_cast<const TI*>(C), D, static_cast<const TI*>(z), bias, static_cast<TI*>(y), total, (int)a.D,
+            (int)(a.D / a.G), (int)a.softplus, wide, a.sx.b, a.sdt.b, a.sB.b, a.sC.b, a.sz.b, a.sy.b);
+        return cudaGetLastError();
+    };
+    switch (a.N) {
+        case 8: return go(scan_step_kernel<TI, 8>);
+        case 16: return go(scan_step_kernel<TI, 16>);
+        case 32: return go(scan_step_kernel<TI, 32>);
+        case 64: return go(scan_step_kernel<TI, 64>);
+        case 128: return go(scan_step_kernel<TI, 128>);
+        default: return cudaErrorInvalidValue;
+    }
+}
+}  // namespace
+
+cudaError_t launch_scan_step(const ScanArgs& a, float* state, const void* x, const void* dt, const float* A,
+                             const void* B, const void* C, const float* D, const void* z,
+                             const float* dt_bias, void* y, cudaStream_t st) {
+    if (a.b == 0 || a.D == 0) return cudaSuccess;
+    return a.dtype == 1 ? step_t<__nv_bfloat16>(a, state, x, dt, A, B, C, D, z, dt_bias, y, st)
+                        : step_t<float>(a, state, x, dt, A, B, C, D, z, dt_bias, y, st);
+}
+
+}  // namespace m2
