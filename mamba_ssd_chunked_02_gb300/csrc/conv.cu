@@ -16,21 +16,18 @@ namespace m2 {
 namespace {
 
 template <typename TI, int V>
-__device__ __forceinline__ void load_f(const TI* p, float* o) {
-    Conv<TI, V>::to(load_raw<TI, V>(p), o);
-}
-template <int V> __device__ __forceinline__ void zero_f(float* o) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) o[j] = 0.f;
+__device__ __forceinline__ void load_2(const TI* p, f2 (&o)[(V + 1) / 2]) {
+    to_pairs<TI, V>(load_raw<TI, V>(p), o);
 }
 template <int V, int W>
-__device__ __forceinline__ void load_w(const float* w, const float* bias, int64_t c, float (&wk)[W][V],
-                                       float (&bi)[V]) {
+__device__ __forceinline__ void load_w(const float* w, const float* bias, int64_t c,
+                                       f2 (&wk)[W][(V + 1) / 2], f2 (&bi)[(V + 1) / 2]) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
+    for (int i = 0; i < (V + 1) / 2; ++i) {
+        const int64_t lo = c + 2 * i, hi = V == 1 ? lo : lo + 1;
 #pragma unroll
-        for (int k = 0; k < W; ++k) wk[k][j] = __ldg(w + (c + j) * W + k);
-        bi[j] = bias ? __ldg(bias + c + j) : 0.f;
+        for (int k = 0; k < W; ++k) wk[k][i] = pack2(__ldg(w + lo * W + k), __ldg(w + hi * W + k));
+        bi[i] = bias ? pack2(__ldg(bias + lo), __ldg(bias + hi)) : dup2(0.f);
     }
 }
 
@@ -62,45 +59,57 @@ conv_fwd_kernel(const TI* __restrict__ x, const float* __restrict__ w,
             store_raw<TI, V>(fin + ((int64_t)b * (W - 1) + k) * D + c, r);
         }
     }
-    float wk[W][V], bi[V], win[W - 1][V];
+    constexpr int H = (V + 1) / 2;
+    f2 wk[W][H], bi[H], win[W - 1][H];
     load_w<V, W>(w, bias, c, wk, bi);
     const int t0 = seg * TS, t1 = min(t0 + TS, T), tn = min(t1, n);
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
         const int t = t0 - (W - 1) + k;
-        zero_f<V>(win[k]);
+#pragma unroll
+        for (int i = 0; i < H; ++i) win[k][i] = dup2(0.f);
         if (t >= 0) {
-            if (t < n) load_f<TI, V>(xb + (int64_t)t * sx.t, win[k]);
+            if (t < n) load_2<TI, V>(xb + (int64_t)t * sx.t, win[k]);
         } else if (ib) {
-            load_f<TI, V>(ib + (int64_t)(t + W - 1) * D, win[k]);
+            load_2<TI, V>(ib + (int64_t)(t + W - 1) * D, win[k]);
         }
     }
-    constexpr int U = 8;   // tokens whose loads are in flight together
-    for (int t = t0; t < tn; t += U) {
+    auto one = [&](Raw r, int t) {
+        f2 cur[H], o[H];
+        to_pairs<TI, V>(r, cur);
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            f2 s = fma2(wk[W - 1][i], cur[i], bi[i]);
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) s = fma2(wk[k][i], win[k][i], s);
+            o[i] = SILU ? mul2(s, sigmoid2(s)) : s;
+#pragma unroll
+            for (int k = 0; k + 1 < W - 1; ++k) win[k][i] = win[k + 1][i];
+            win[W - 2][i] = cur[i];
+        }
+        store_raw<TI, V>(yb + (int64_t)t * sy.t, from_pairs<TI, V>(o));
+    };
+    // Whole groups of U tokens, the next group's loads in flight under this one's work.
+    constexpr int U = 8;
+    int t = t0;
+    if (t + U <= tn) {
         Raw r[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (t + u < tn) r[u] = load_raw<TI, V>(xb + (int64_t)(t + u) * sx.t);
+        for (int u = 0; u < U; ++u) r[u] = load_raw<TI, V>(xb + (int64_t)(t + u) * sx.t);
+        for (; t + U <= tn; t += U) {
+            Raw nx[U];
+            const bool more = t + 2 * U <= tn;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (t + u >= tn) break;
-            float cur[V], o[V];
-            Conv<TI, V>::to(r[u], cur);
+            for (int u = 0; u < U; ++u)
+                if (more) nx[u] = load_raw<TI, V>(xb + (int64_t)(t + U + u) * sx.t);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float s = bi[j];
+            for (int u = 0; u < U; ++u) one(r[u], t + u);
 #pragma unroll
-                for (int k = 0; k < W - 1; ++k) s = fmaf(wk[k][j], win[k][j], s);
-                s = fmaf(wk[W - 1][j], cur[j], s);
-                o[j] = SILU ? s * sigmoid(s) : s;
-#pragma unroll
-                for (int k = 0; k + 1 < W - 1; ++k) win[k][j] = win[k + 1][j];
-                win[W - 2][j] = cur[j];
-            }
-            store_raw<TI, V>(yb + (int64_t)(t + u) * sy.t, Conv<TI, V>::from(o));
+            for (int u = 0; u < U; ++u) r[u] = nx[u];
         }
     }
-    for (int t = max(tn, t0); t < t1; ++t) store_raw<TI, V>(yb + (int64_t)t * sy.t, zero_raw<Raw>());
+    for (; t < tn; ++t) one(load_raw<TI, V>(xb + (int64_t)t * sx.t), t);
+    for (t = max(tn, t0); t < t1; ++t) store_raw<TI, V>(yb + (int64_t)t * sy.t, zero_raw<Raw>());
 }
 
 // One token: the window is read, applied and moved on.
@@ -118,22 +127,23 @@ conv_step_kernel(TI* __restrict__ state, const TI* __restrict__ x, const float* 
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) r[k] = *reinterpret_cast<const Raw*>(sb + (int64_t)k * D);
     r[W - 1] = load_raw<TI, V>(x + (int64_t)b * sxb + c);
-    float wk[W][V], o[V];
+    constexpr int H = (V + 1) / 2;
+    f2 wk[W][H], o[H];
     load_w<V, W>(w, bias, c, wk, o);
 #pragma unroll
     for (int k = 0; k < W; ++k) {
-        float v[V];
-        Conv<TI, V>::to(r[k], v);
+        f2 v[H];
+        to_pairs<TI, V>(r[k], v);
 #pragma unroll
-        for (int j = 0; j < V; ++j) o[j] = fmaf(wk[k][j], v[j], o[j]);
+        for (int i = 0; i < H; ++i) o[i] = fma2(wk[k][i], v[i], o[i]);
     }
     if (SILU) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) o[j] *= sigmoid(o[j]);
+        for (int i = 0; i < H; ++i) o[i] = mul2(o[i], sigmoid2(o[i]));
     }
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) store_raw<TI, V>(sb + (int64_t)k * D, r[k + 1]);
-    store_raw<TI, V>(y + (int64_t)b * syb + c, Conv<TI, V>::from(o));
+    store_raw<TI, V>(y + (int64_t)b * syb + c, from_pairs<TI, V>(o));
 }
 
 // Backward.  ds = dy silu'(s) with s recomputed;  dx[t] = sum_k w[k] ds[t + W-1 - k];
@@ -158,100 +168,138 @@ conv_bwd_kernel(const TI* __restrict__ x, const float* __restrict__ w,
     const int seg = tb * kBwdTY + threadIdx.y;
     const bool first = seg == 0;
     const int t0 = min(seg * TS, T), t1 = min(t0 + TS, T);
-    float dwk[W][V], dbi[V];
+    constexpr int H = (V + 1) / 2;
+    f2 dwk[W][H], dbi[H];
 #pragma unroll
-    for (int k = 0; k < W; ++k) zero_f<V>(dwk[k]);
-    zero_f<V>(dbi);
+    for (int i = 0; i < H; ++i) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) dwk[k][i] = dup2(0.f);
+        dbi[i] = dup2(0.f);
+    }
     if (c < D && (t0 < t1 || first)) {
         const int n = lengths ? min(max(__ldg(lengths + b), 0), T) : T;
         const TI* xb = x + (int64_t)b * sx.b + c;
         const TI* db = dy + (int64_t)b * sdy.b + c;
         TI* ob = dx + (int64_t)b * T * D + c;
         const int64_t wrow = (int64_t)b * (W - 1) * D + c;
-        float wk[W][V], bi[V], xw[W][V], dsw[W][V];   // xw[W-1], dsw[W-1]: the current token
+        f2 wk[W][H], bi[H], xw[W][H], dsw[W][H];   // xw[W-1], dsw[W-1]: the current token
         load_w<V, W>(w, bias, c, wk, bi);
 #pragma unroll
         for (int k = 0; k < W; ++k) {
-            zero_f<V>(dsw[k]);
-            zero_f<V>(xw[k]);
+#pragma unroll
+            for (int i = 0; i < H; ++i) dsw[k][i] = xw[k][i] = dup2(0.f);
             const int t = t0 - W + k;   // shifted once before use
             if (k > 0) {
                 if (t >= 0) {
-                    if (t < n) load_f<TI, V>(xb + (int64_t)t * sx.t, xw[k]);
+                    if (t < n) load_2<TI, V>(xb + (int64_t)t * sx.t, xw[k]);
                 } else if (init) {
-                    load_f<TI, V>(init + wrow + (int64_t)(t + W - 1) * D, xw[k]);
+                    load_2<TI, V>(init + wrow + (int64_t)(t + W - 1) * D, xw[k]);
                 }
             }
         }
         typedef typename Pack<TI, V>::Raw Raw;
+        // Token t: its ds, its part of dw, and the finished dx[t - (W-1)] in o.  ANY: t may
+        // be padding or past the stretch.
+        auto one = [&](const bool ANY, Raw rx, Raw rd, int t, f2 (&o)[H]) {
+            f2 cx[H], ds[H];
+            to_pairs<TI, V>(rx, cx);
+            to_pairs<TI, V>(rd, ds);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+#pragma unroll
+                for (int k = 0; k + 1 < W; ++k) {
+                    xw[k][i] = xw[k + 1][i];
+                    dsw[k][i] = dsw[k + 1][i];
+                }
+                xw[W - 1][i] = cx[i];
+                if (SILU) {
+                    f2 s = bi[i];
+#pragma unroll
+                    for (int k = 0; k < W; ++k) s = fma2(wk[k][i], xw[k][i], s);
+                    const f2 sg = sigmoid2(s);   // silu' = sg (1 + s (1 - sg))
+                    ds[i] = mul2(ds[i], mul2(sg, fma2(s, fma2(sg, dup2(-1.f), dup2(1.f)), dup2(1.f))));
+                }
+                f2 own = ds[i];
+                if (ANY) {
+                    if (t >= n) ds[i] = own = dup2(0.f);
+                    if (t >= t1) own = dup2(0.f);
+                }
+                dsw[W - 1][i] = ds[i];
+#pragma unroll
+                for (int k = 0; k < W; ++k) dwk[k][i] = fma2(own, xw[k][i], dwk[k][i]);
+                dbi[i] = add2(dbi[i], own);
+                f2 a = mul2(wk[W - 1][i], dsw[0][i]);
+#pragma unroll
+                for (int k = 0; k + 1 < W; ++k) a = fma2(wk[k][i], dsw[W - 1 - k][i], a);
+                o[i] = a;
+            }
+        };
+        auto slow = [&](int t) {
+            Raw rx = zero_raw<Raw>(), rd = rx;
+            if (t < n) {
+                rx = load_raw<TI, V>(xb + (int64_t)t * sx.t);
+                rd = load_raw<TI, V>(db + (int64_t)t * sdy.t);
+            }
+            f2 o[H];
+            one(true, rx, rd, t, o);
+            const int tp = t - (W - 1);
+            if (tp < t0 && !first) return;
+            if (dfin && tp < n && tp >= n - (W - 1)) {
+                f2 f[H];
+                load_2<TI, V>(dfin + wrow + (int64_t)(tp - (n - (W - 1))) * D, f);
+#pragma unroll
+                for (int i = 0; i < H; ++i) o[i] = add2(o[i], f[i]);
+            }
+            if (tp >= 0) store_raw<TI, V>(ob + (int64_t)tp * D, from_pairs<TI, V>(o));
+            else if (dinit) store_raw<TI, V>(dinit + wrow + (int64_t)(tp + W - 1) * D, from_pairs<TI, V>(o));
+        };
         constexpr int U = 4;
-        const int te = t1 + W - 1;
-        for (int tq = t0; tq < te; tq += U) {
+        const int te = t1 + W - 1, tf = min(t1, n);
+        int t = t0;
+        for (; t < min(t0 + W - 1, te); ++t) slow(t);
+        // Whole groups of U real tokens of this stretch (dfinal only reaches tokens finished
+        // at or after n), the next group's loads in flight under this one's work.
+        if (t + U <= tf) {
             Raw rx[U], rd[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                rx[u] = rd[u] = zero_raw<Raw>();
-                if (tq + u < min(te, n)) {
-                    rx[u] = load_raw<TI, V>(xb + (int64_t)(tq + u) * sx.t);
-                    rd[u] = load_raw<TI, V>(db + (int64_t)(tq + u) * sdy.t);
-                }
+                rx[u] = load_raw<TI, V>(xb + (int64_t)(t + u) * sx.t);
+                rd[u] = load_raw<TI, V>(db + (int64_t)(t + u) * sdy.t);
             }
+            for (; t + U <= tf; t += U) {
+                Raw nx[U], nd[U];
+                const bool more = t + 2 * U <= tf;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int t = tq + u;
-                if (t >= te) break;
-                const bool real = t < n, mine = t < t1;
-                float cx[V], cd[V], o[V];
-                Conv<TI, V>::to(rx[u], cx);
-                Conv<TI, V>::to(rd[u], cd);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-#pragma unroll
-                    for (int k = 0; k + 1 < W; ++k) {
-                        xw[k][j] = xw[k + 1][j];
-                        dsw[k][j] = dsw[k + 1][j];
+                for (int u = 0; u < U; ++u)
+                    if (more) {
+                        nx[u] = load_raw<TI, V>(xb + (int64_t)(t + U + u) * sx.t);
+                        nd[u] = load_raw<TI, V>(db + (int64_t)(t + U + u) * sdy.t);
                     }
-                    xw[W - 1][j] = cx[j];
-                    float s = bi[j], ds = cd[j];
-                    if (SILU) {
 #pragma unroll
-                        for (int k = 0; k < W; ++k) s = fmaf(wk[k][j], xw[k][j], s);
-                        const float sg = sigmoid(s);
-                        ds *= sg * fmaf(s, 1.f - sg, 1.f);
-                    }
-                    ds = real ? ds : 0.f;
-                    dsw[W - 1][j] = ds;
-                    const float own = mine ? ds : 0.f;
-#pragma unroll
-                    for (int k = 0; k < W; ++k) dwk[k][j] = fmaf(own, xw[k][j], dwk[k][j]);
-                    dbi[j] += own;
-                    float a = 0.f;
-#pragma unroll
-                    for (int k = 0; k < W; ++k) a = fmaf(wk[k][j], dsw[W - 1 - k][j], a);
-                    o[j] = a;
+                for (int u = 0; u < U; ++u) {
+                    f2 o[H];
+                    one(false, rx[u], rd[u], t + u, o);
+                    store_raw<TI, V>(ob + (int64_t)(t + u - (W - 1)) * D, from_pairs<TI, V>(o));
                 }
-                const int tp = t - (W - 1);
-                if (tp >= t0 || first) {
-                    if (dfin && tp < n && tp >= n - (W - 1)) {
-                        float f[V];
-                        load_f<TI, V>(dfin + wrow + (int64_t)(tp - (n - (W - 1))) * D, f);
 #pragma unroll
-                        for (int j = 0; j < V; ++j) o[j] += f[j];
-                    }
-                    if (tp >= 0) store_raw<TI, V>(ob + (int64_t)tp * D, Conv<TI, V>::from(o));
-                    else if (dinit)
-                        store_raw<TI, V>(dinit + wrow + (int64_t)(tp + W - 1) * D, Conv<TI, V>::from(o));
+                for (int u = 0; u < U; ++u) {
+                    rx[u] = nx[u];
+                    rd[u] = nd[u];
                 }
             }
         }
+        for (; t < te; ++t) slow(t);
     }
     float* mr = red[threadIdx.y] + threadIdx.x;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
+    for (int i = 0; i < H; ++i)
 #pragma unroll
-        for (int k = 0; k < W; ++k) mr[(j * (W + 1) + k) * kBwdTX] = dwk[k][j];
-        mr[(j * (W + 1) + W) * kBwdTX] = dbi[j];
-    }
+        for (int k = 0; k <= W; ++k) {
+            float lo, hi;
+            unpack2(k < W ? dwk[k < W ? k : 0][i] : dbi[i], lo, hi);
+            mr[(2 * i * (W + 1) + k) * kBwdTX] = lo;
+            if (V > 1) mr[((2 * i + 1) * (W + 1) + k) * kBwdTX] = hi;
+        }
     __syncthreads();
     const int tid = threadIdx.y * kBwdTX + threadIdx.x;
     for (int i = tid; i < kBwdTX * V * (W + 1); i += kBwdTX * kBwdTY) {
@@ -398,8 +446,8 @@ cudaError_t launch_conv_fwd(const ConvArgs& a, const void* x, const float* w, co
                             cudaStream_t st) {
     if (a.b == 0 || a.D == 0) return cudaSuccess;
     if (a.dtype == 1)
-        return wide(a, 8, x, y, init, fin, nullptr)
-                   ? fwd_v<__nv_bfloat16, 8>(a, x, w, bias, init, lengths, y, fin, st)
+        return wide(a, 4, x, y, init, fin, nullptr)
+                   ? fwd_v<__nv_bfloat16, 4>(a, x, w, bias, init, lengths, y, fin, st)
                    : fwd_v<__nv_bfloat16, 1>(a, x, w, bias, init, lengths, y, fin, st);
     return wide(a, 4, x, y, init, fin, nullptr)
                ? fwd_v<float, 4>(a, x, w, bias, init, lengths, y, fin, st)

@@ -77,6 +77,23 @@ __device__ __forceinline__ float softplus(float v) {
     return fmaf(p, e, v > 0.f ? v : 0.f);
 }
 
+// The same for a pair.
+__device__ __forceinline__ f2 softplus2(f2 v) {
+    float a, b;
+    unpack2(v, a, b);
+    const f2 e = ex2_2(mul2(pack2(fabsf(a), fabsf(b)), dup2(-kLog2e)));
+    f2 p = dup2(0.005253457929939032f);
+    p = fma2(p, e, dup2(-0.02958850748836994f));
+    p = fma2(p, e, dup2(0.07836166769266129f));
+    p = fma2(p, e, dup2(-0.13674770295619965f));
+    p = fma2(p, e, dup2(0.19111430644989014f));
+    p = fma2(p, e, dup2(-0.24844369292259216f));
+    p = fma2(p, e, dup2(0.33319270610809326f));
+    p = fma2(p, e, dup2(-0.49999502301216125f));
+    p = fma2(p, e, dup2(1.f));
+    return fma2(p, e, pack2(a > 0.f ? a : 0.f, b > 0.f ? b : 0.f));
+}
+
 // V elements of type TI moved as one access (V * sizeof(TI) is 2, 4, 8 or 16 bytes).
 template <int BYTES> struct RawOf;
 template <> struct RawOf<2> { typedef unsigned short type; };
@@ -174,6 +191,31 @@ template <> struct Conv<__nv_bfloat16, 8> {
                           bf_pack(o[6], o[7]));
     }
 };
+
+// A raw access as packed pairs and back; one value is a pair with an idle half.
+template <typename TI, int V>
+__device__ __forceinline__ void to_pairs(typename Pack<TI, V>::Raw r, f2 (&o)[(V + 1) / 2]) {
+    float f[V];
+    Conv<TI, V>::to(r, f);
+    if constexpr (V == 1) {
+        o[0] = pack2(f[0], 0.f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) o[i] = pack2(f[2 * i], f[2 * i + 1]);
+    }
+}
+template <typename TI, int V>
+__device__ __forceinline__ typename Pack<TI, V>::Raw from_pairs(const f2 (&v)[(V + 1) / 2]) {
+    float f[V + 1];
+#pragma unroll
+    for (int i = 0; i < (V + 1) / 2; ++i) unpack2(v[i], f[2 * i], f[2 * i + 1]);
+    return Conv<TI, V>::from(f);
+}
+__device__ __forceinline__ f2 sigmoid2(f2 v) {
+    float a, b;
+    unpack2(add2(ex2_2(mul2(v, dup2(-kLog2e))), dup2(1.f)), a, b);
+    return pack2(rcp(a), rcp(b));
+}
 
 template <typename TI, int V>
 __device__ __forceinline__ void store_raw(TI* p, typename Pack<TI, V>::Raw r) {

@@ -48,6 +48,27 @@ __device__ __forceinline__ float2 team_sum(float a, float b, float2* red) {
 
 enum { kNone = 0, kFirst = 1, kAfter = 2 };
 
+// V weights from w (ones when null), 16 bytes at a time where V allows (w is then
+// 16-byte aligned: scalar loads of 8 neighbouring weights a lane cost four times
+// the load unit's time).
+template <int V> __device__ __forceinline__ void load_weights(const float* w, float (&o)[V]) {
+    if (!w) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) o[j] = 1.f;
+    } else if constexpr (V == 1) {
+        o[0] = __ldg(w);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(w + j));
+            o[j] = v.x;
+            o[j + 1] = v.y;
+            o[j + 2] = v.z;
+            o[j + 3] = v.w;
+        }
+    }
+}
+
 // silu(z) and its derivative.
 __device__ __forceinline__ void silu_d(float z, float& s, float& d) {
     const float sg = sigmoid(z);
@@ -89,14 +110,15 @@ norm_fwd_kernel(const TI* __restrict__ x, const float* __restrict__ w, const TI*
         }
     };
     auto result = [&](int i, Raw vx, Raw vz, float r) {
-        float fx[V], fz[V], o[V];
+        float fx[V], fz[V], o[V], fw[V];
         Conv<TI, V>::to(vx, fx);
         if (GATE != kNone) Conv<TI, V>::to(vz, fz);
+        load_weights<V>(wr ? wr + i * V : nullptr, fw);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             float v = fx[j] * r;
             if (GATE != kNone) v *= fz[j] * sigmoid(fz[j]);
-            o[j] = wr ? v * __ldg(wr + i * V + j) : v;
+            o[j] = v * fw[j];
         }
         store_raw<TI, V>(yr + i * V, Conv<TI, V>::from(o));
     };
@@ -167,15 +189,16 @@ norm_bwd_kernel(const TI* __restrict__ x, const float* __restrict__ w, const TI*
         TI* oz = dz + row * D + (int64_t)g * q.S;
         float ss = 0.f, qv = 0.f;
         auto sums = [&](int i, Raw vx, Raw vz, Raw vd) {
-            float fx[V], fz[V], fd[V];
+            float fx[V], fz[V], fd[V], fw[V];
             Conv<TI, V>::to(vx, fx);
             if (GATE != kNone) Conv<TI, V>::to(vz, fz);
             Conv<TI, V>::to(vd, fd);
+            load_weights<V>(wr ? wr + i * V : nullptr, fw);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float gate = GATE != kNone ? fz[j] * sigmoid(fz[j]) : 1.f;
                 const float v = GATE == kFirst ? fx[j] * gate : fx[j];
-                float d = wr ? fd[j] * __ldg(wr + i * V + j) : fd[j];
+                float d = fd[j] * fw[j];
                 if (GATE == kAfter) d *= gate;
                 ss = fmaf(v, v, ss);
                 qv = fmaf(d, v, qv);
@@ -183,16 +206,17 @@ norm_bwd_kernel(const TI* __restrict__ x, const float* __restrict__ w, const TI*
         };
         // dx, dz; returns this token's part of dw in p
         auto result = [&](int i, Raw vx, Raw vz, Raw vd, float r, float m, float* p) {
-            float fx[V], fz[V], fd[V], ax[V], az[V];
+            float fx[V], fz[V], fd[V], ax[V], az[V], fw[V];
             Conv<TI, V>::to(vx, fx);
             if (GATE != kNone) Conv<TI, V>::to(vz, fz);
             Conv<TI, V>::to(vd, fd);
+            load_weights<V>(wr ? wr + i * V : nullptr, fw);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 float gate = 1.f, slope = 0.f;
                 if (GATE != kNone) silu_d(fz[j], gate, slope);
                 const float v = GATE == kFirst ? fx[j] * gate : fx[j];
-                const float wj = wr ? __ldg(wr + i * V + j) : 1.f;
+                const float wj = fw[j];
                 const float n = v * r;
                 const float d = GATE == kAfter ? fd[j] * gate : fd[j];
                 const float dv = fmaf(r, d * wj, -v * m);
@@ -257,9 +281,16 @@ norm_bwd_kernel(const TI* __restrict__ x, const float* __restrict__ w, const TI*
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int i = tid + k * nt;
-            if (i < nv)
+            if (i < nv) {
+                if constexpr (V == 1) {
+                    pr[i] = acc[k][0];
+                } else {
 #pragma unroll
-                for (int j = 0; j < V; ++j) pr[i * V + j] = acc[k][j];
+                    for (int j = 0; j < V; j += 4)
+                        *reinterpret_cast<float4*>(pr + i * V + j) =
+                            make_float4(acc[k][j], acc[k][j + 1], acc[k][j + 2], acc[k][j + 3]);
+                }
+            }
         }
     } else if (!begun) {
         for (int i = tid; i < nv * V; i += nt) pr[i] = 0.f;
@@ -333,11 +364,11 @@ cudaError_t bwd_gate(const NormArgs& a, const void* x, const float* w, const voi
     return !z ? go(bwd_go<TI, V, kNone>) : a.after ? go(bwd_go<TI, V, kAfter>) : go(bwd_go<TI, V, kFirst>);
 }
 
-bool wide(const NormArgs& a, int64_t V, const void* x, const void* z, const void* y, const void* o1,
-          const void* o2) {
+bool wide(const NormArgs& a, int64_t V, const void* x, const float* w, const void* z, const void* y,
+          const void* o1, const void* o2) {
     const int64_t es = a.dtype == 1 ? 2 : 4;
     const Tok row{0, a.D};
-    return (a.D / a.G) % V == 0 && vec_ok(x, a.sx, 16, es) && (!z || vec_ok(z, a.sz, 16, es)) &&
+    return (a.D / a.G) % V == 0 && reinterpret_cast<uintptr_t>(w) % 16 == 0 && vec_ok(x, a.sx, 16, es) && (!z || vec_ok(z, a.sz, 16, es)) &&
            vec_ok(y, a.sy, 16, es) && vec_ok(o1, row, 16, es) && vec_ok(o2, row, 16, es);
 }
 
@@ -347,9 +378,9 @@ cudaError_t launch_norm_fwd(const NormArgs& a, const void* x, const float* w, co
                             cudaStream_t st) {
     if (a.b * a.T == 0 || a.D == 0) return cudaSuccess;
     if (a.dtype == 1)
-        return wide(a, 8, x, z, y, nullptr, nullptr) ? fwd_gate<__nv_bfloat16, 8>(a, x, w, z, y, st)
+        return wide(a, 8, x, w, z, y, nullptr, nullptr) ? fwd_gate<__nv_bfloat16, 8>(a, x, w, z, y, st)
                                                      : fwd_gate<__nv_bfloat16, 1>(a, x, w, z, y, st);
-    return wide(a, 4, x, z, y, nullptr, nullptr) ? fwd_gate<float, 4>(a, x, w, z, y, st)
+    return wide(a, 4, x, w, z, y, nullptr, nullptr) ? fwd_gate<float, 4>(a, x, w, z, y, st)
                                                  : fwd_gate<float, 1>(a, x, w, z, y, st);
 }
 
@@ -363,7 +394,7 @@ cudaError_t launch_norm_bwd(const NormArgs& a, const void* x, const float* w, co
     if (!dw) part = nullptr;
     const bool none = a.b * a.T == 0;
     if (!none) {
-        const bool v = wide(a, a.dtype == 1 ? 8 : 4, x, z, dy, dx, dz);
+        const bool v = wide(a, a.dtype == 1 ? 8 : 4, x, w, z, dy, dx, dz);
         if (a.dtype == 1)
             e = v ? bwd_gate<__nv_bfloat16, 8>(a, x, w, z, dy, dx, dz, part, st)
                   : bwd_gate<__nv_bfloat16, 1>(a, x, w, z, dy, dx, dz, part, st);

@@ -5,23 +5,34 @@
 
 namespace m2 {
 
-// Lanes and tiles.  A lane keeps kNS states of one channel; N / kNS neighbouring
-// lanes make a channel.  A block holds CB channels of one group and one sequence
-// and walks over tokens in tiles of TT.
+// Lanes and tiles.  A lane keeps kNS states of each of two neighbouring channels, and
+// N / kNS neighbouring lanes a pair of channels: shared memory hands 128 bytes a clock to
+// an SM's registers whether lanes read the same address or not, so B and C (16 bytes each
+// per token and lane) are used twice per load.  (One channel a lane: 12 bytes per state
+// update and the load unit the limit; this: 6.)  A block holds CB channels of one group and
+// one sequence and walks over tokens in tiles of TT; blocks are small, so that the large
+// cases' blocks divide evenly over the SMs.
 constexpr int kNS = 4;
 template <int N> struct Cfg {
-    static constexpr int NT = N >= 64 ? 256 : 128;
+    static constexpr int NT = N >= 64 ? 128 : 64;
     static constexpr int LPC = N / kNS;
-    static constexpr int CPW = 32 / LPC;
-    static constexpr int CB = NT / LPC;
-    static constexpr int TT = N >= 128 ? 64 : 32;
-    static constexpr int U = LPC < 8 ? LPC : 8;           // tokens reduced together
-    static constexpr int YP = CB + (CPW < 2 ? 2 : CPW);   // pitch of the y tile (bank-conflict free)
-    static constexpr size_t smem = (size_t)TT * (CB * 16 + 2 * N * 4 + YP * 4);
+    static constexpr int CPW = 32 / LPC;                  // pairs a warp
+    static constexpr int CB = 2 * (NT / LPC);
+    static constexpr int TT = N >= 128 ? 32 : 16;
+    static constexpr int U = LPC < 8 ? LPC : 8;           // values reduced together: 2 channels x UT tokens
+    static constexpr int UT = U / 2;
+    static constexpr int YP = CB + 2 * CPW;               // pitch of the y tile (bank-conflict free)
+    static constexpr size_t smem = (size_t)TT * (CB * 8 + 2 * N * 4 + YP * 4);
 };
 
-// Sum v[u] over the LPC lanes of a channel for U tokens at once: at each step a lane
-// hands over the half it does not keep.  On return v[0] is the sum for token
+// Blocks an SM the registers are kept to: nine (96 registers) where the tile's registers
+// are few, else what does not spill.
+template <typename TI, int N, int V> constexpr int min_blocks() {
+    return N >= 64 ? 4 : V == 2 && sizeof(TI) == 2 && N >= 16 ? 9 : 6;
+}
+
+// Sum v[u] over the LPC lanes of a channel for U values at once: at each step a lane
+// hands over the half it does not keep.  On return v[0] is the sum for value
 // (lane & (U - 1)).
 template <int LPC, int U> __device__ __forceinline__ float lanes_sum(float (&v)[U]) {
     const int lane = threadIdx.x & 31;

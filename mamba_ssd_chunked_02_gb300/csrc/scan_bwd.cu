@@ -47,20 +47,21 @@ struct BwdP {
     Tok sx, sdt, sB, sC, sz, sy;
 };
 
-// (1) Each stretch from zero.  ADJ: also its adjoint (only needed when there are
-// several stretches).
+// (1) Each stretch from zero, with the forward's lanes and tiles.  ADJ: also its adjoint
+// (only needed when there are several stretches).
 template <typename TI, int N, int V, bool ADJ>
-__global__ void __launch_bounds__(Cfg<N>::NT)
+__global__ void __launch_bounds__(Cfg<N>::NT, (min_blocks<TI, N, V>() < 8 ? min_blocks<TI, N, V>() : 8))
 scan_local_kernel(const BwdP p) {
     using K = Cfg<N>;
     constexpr int NT = K::NT, LPC = K::LPC, CB = K::CB, TT = K::TT;
     constexpr int PR = CB / V, RS = NT / PR, IT = TT / RS;
     constexpr int BI = TT * N / V / NT;
+    static_assert(TT % kL == 0, "whole stored states");
     extern __shared__ __align__(16) unsigned char smem[];
-    ulonglong2* sP = reinterpret_cast<ulonglong2*>(smem);                 // [TT][CB] (d, d, dx, dx)
-    f2* sY = reinterpret_cast<f2*>(smem + (size_t)TT * CB * 16);          // [TT][CB] (dY, dY)
-    float* sB = reinterpret_cast<float*>(smem + (size_t)TT * CB * (ADJ ? 24 : 16));   // [TT][N]
-    float* sC = sB + TT * N;
+    float2* sP = reinterpret_cast<float2*>(smem);                         // [TT][CB] (d, dx)
+    float* sB = reinterpret_cast<float*>(smem + (size_t)TT * CB * 8);     // [TT][N]
+    float* sC = sB + TT * N;                                              // [TT][N]
+    float* sY = sC + TT * N;                                              // [TT][CB] dY
     typedef typename Pack<TI, V>::Raw Raw;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -85,113 +86,151 @@ scan_local_kernel(const BwdP p) {
 #pragma unroll
     for (int j = 0; j < V; ++j) bias[j] = p.bias && con ? __ldg(p.bias + c + j) : 0.f;
 
-    const int q = lane % LPC, ch = warp * K::CPW + lane / LPC;
-    const bool on = cb * CB + ch < p.Dg;
+    const int q = lane % LPC, ch = 2 * (warp * K::CPW + lane / LPC);
     const int64_t cg = (int64_t)g * p.Dg + cb * CB + ch;
-    f2 A2[2] = {0, 0}, h[2] = {0, 0}, G[2] = {0, 0}, P[2];
-    P[0] = P[1] = dup2(1.f);
-    if (on) {
-        const float* Ap = p.A + cg * N + q * kNS;
-        A2[0] = pack2(__ldg(Ap) * kLog2e, __ldg(Ap + 1) * kLog2e);
-        A2[1] = pack2(__ldg(Ap + 2) * kLog2e, __ldg(Ap + 3) * kLog2e);
+    bool on[2];
+    f2 A2[2][2], h[2][2], G[2][2], P[2][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        on[j] = cb * CB + ch + j < p.Dg;
+        h[j][0] = h[j][1] = G[j][0] = G[j][1] = A2[j][0] = A2[j][1] = dup2(0.f);
+        P[j][0] = P[j][1] = dup2(1.f);
+        if (on[j]) {
+            const float* Ap = p.A + (cg + j) * N + q * kNS;
+            A2[j][0] = pack2(__ldg(Ap) * kLog2e, __ldg(Ap + 1) * kLog2e);
+            A2[j][1] = pack2(__ldg(Ap + 2) * kLog2e, __ldg(Ap + 3) * kLog2e);
+        }
     }
-    float dsum = 0.f;
+    float dsum[2] = {0.f, 0.f};
     float* ck = p.ck + ((int64_t)b * p.nck * p.Dch + cg) * N + q * kNS;
     float* ckd = p.ck_d + (int64_t)b * p.nck * p.Dch + cg;
 
-    for (int t0 = s0; t0 < s1; t0 += TT) {
+    Raw rx[IT], rd[IT], rz[IT], ry[IT], rB[BI], rC[BI];
+    auto load = [&](int t0) {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int r = r0 + i * RS, t = t0 + r;
-            const bool real = con && t < sn;
-            float fx[V], fd[V], fz[V], fy[V];
-            Raw rx = zero_raw<Raw>(), rd = rx, rz = rx, ry = rx;
-            if (real) {
-                rx = load_raw<TI, V>(xp + (int64_t)t * p.sx.t);
-                rd = load_raw<TI, V>(dp + (int64_t)t * p.sdt.t);
-                if (ADJ && p.z) rz = load_raw<TI, V>(zp + (int64_t)t * p.sz.t);
-                if (ADJ) ry = load_raw<TI, V>(yp + (int64_t)t * p.sy.t);
-            }
-            Conv<TI, V>::to(rx, fx);
-            Conv<TI, V>::to(rd, fd);
-            Conv<TI, V>::to(rz, fz);
-            Conv<TI, V>::to(ry, fy);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float v = fd[j] + bias[j];
-                const float d = real ? (p.softplus ? softplus(v) : v) : 0.f;
-                const int cc = lc + j;
-                ulonglong2 w;
-                w.x = dup2(d);
-                w.y = dup2(d * fx[j]);
-                sP[r * CB + (cc ^ ((cc >> 3) & 1))] = w;
-                if (ADJ) sY[r * CB + cc] = dup2(p.z ? fy[j] * fz[j] * sigmoid(fz[j]) : fy[j]);
+            const int t = t0 + r0 + i * RS;
+            rx[i] = rd[i] = rz[i] = ry[i] = zero_raw<Raw>();
+            if (con && t < sn) {
+                rx[i] = load_raw<TI, V>(xp + (int64_t)t * p.sx.t);
+                rd[i] = load_raw<TI, V>(dp + (int64_t)t * p.sdt.t);
+                if (ADJ && p.z) rz[i] = load_raw<TI, V>(zp + (int64_t)t * p.sz.t);
+                if (ADJ) ry[i] = load_raw<TI, V>(yp + (int64_t)t * p.sy.t);
             }
         }
 #pragma unroll
         for (int i = 0; i < BI; ++i) {
             const int e = (tid + i * NT) * V, t = t0 + e / N;
-            Raw rB = zero_raw<Raw>(), rC = rB;
+            rB[i] = rC[i] = zero_raw<Raw>();
             if (t < sn) {
-                rB = load_raw<TI, V>(Bp + (int64_t)t * p.sB.t + e % N);
-                if (ADJ) rC = load_raw<TI, V>(Cp + (int64_t)t * p.sC.t + e % N);
+                rB[i] = load_raw<TI, V>(Bp + (int64_t)t * p.sB.t + e % N);
+                if (ADJ) rC[i] = load_raw<TI, V>(Cp + (int64_t)t * p.sC.t + e % N);
             }
+        }
+    };
+    load(s0);
+    for (int t0 = s0; t0 < s1; t0 += TT) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int r = r0 + i * RS;
+            const bool real = con && t0 + r < sn;
+            f2 fx[1], fd[1], fz[1], fy[1];
+            to_pairs<TI, V>(rx[i], fx);
+            to_pairs<TI, V>(rd[i], fd);
+            f2 d = add2(fd[0], pack2(bias[0], bias[V - 1]));
+            if (p.softplus) d = softplus2(d);
+            if (!real) d = dup2(0.f);
+            float d0, d1, u0, u1;
+            unpack2(d, d0, d1);
+            unpack2(mul2(d, fx[0]), u0, u1);
+            if constexpr (V == 2)
+                *reinterpret_cast<float4*>(sP + r * CB + lc) = make_float4(d0, u0, d1, u1);
+            else
+                sP[r * CB + lc] = make_float2(d0, u0);
+            if (ADJ) {
+                to_pairs<TI, V>(ry[i], fy);
+                if (p.z) {
+                    to_pairs<TI, V>(rz[i], fz);
+                    fy[0] = mul2(fy[0], mul2(fz[0], sigmoid2(fz[0])));
+                }
+                unpack2(fy[0], u0, u1);
+                sY[r * CB + lc] = u0;
+                if (V == 2) sY[r * CB + lc + 1] = u1;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < BI; ++i) {
+            const int e = (tid + i * NT) * V;
             float f[V];
-            Conv<TI, V>::to(rB, f);
+            Conv<TI, V>::to(rB[i], f);
 #pragma unroll
             for (int j = 0; j < V; ++j) sB[e + j] = f[j];
             if (ADJ) {
-                Conv<TI, V>::to(rC, f);
+                Conv<TI, V>::to(rC[i], f);
 #pragma unroll
                 for (int j = 0; j < V; ++j) sC[e + j] = f[j];
             }
         }
         __syncthreads();
-        const ulonglong2* pP = sP + (ch ^ ((ch >> 3) & 1));
-        const f2* pY = sY + ch;
+        if (t0 + TT < s1) load(t0 + TT);
+        const float4* pP = reinterpret_cast<const float4*>(sP + ch);
+        const float2* pY = reinterpret_cast<const float2*>(sY + ch);
 #pragma unroll 1
         for (int tb = 0; tb < TT; tb += kL) {
             if (t0 + tb >= s1) break;
-            if (on) {
-                const int64_t at = (int64_t)((t0 + tb) / kL) * p.Dch;
-                float4 v;
-                unpack2(h[0], v.x, v.y);
-                unpack2(h[1], v.z, v.w);
-                *reinterpret_cast<float4*>(ck + at * N) = v;
-                if (q == 0) ckd[at] = dsum;
-            }
+            const int64_t at = (int64_t)((t0 + tb) / kL) * p.Dch;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (on[j]) {
+                    float4 v;
+                    unpack2(h[j][0], v.x, v.y);
+                    unpack2(h[j][1], v.z, v.w);
+                    *reinterpret_cast<float4*>(ck + (at + j) * N) = v;
+                    if (q == 0) ckd[at + j] = dsum[j];
+                }
 #pragma unroll
             for (int u = 0; u < kL; ++u) {
-                const ulonglong2 w = pP[(tb + u) * CB];
-                const ulonglong2 Bv = *reinterpret_cast<const ulonglong2*>(sB + (tb + u) * N + q * kNS);
-                const f2 a0 = ex2_2(mul2(w.x, A2[0])), a1 = ex2_2(mul2(w.x, A2[1]));
-                h[0] = fma2(a0, h[0], mul2(w.y, Bv.x));
-                h[1] = fma2(a1, h[1], mul2(w.y, Bv.y));
-                float lo, hi;
-                unpack2(w.x, lo, hi);
-                dsum += lo;
+                const int t = tb + u;
+                const float4 w = pP[t * (CB / 2)];
+                const ulonglong2 Bv = *reinterpret_cast<const ulonglong2*>(sB + t * N + q * kNS);
+                ulonglong2 Cv = {0, 0};
+                float2 yv = make_float2(0.f, 0.f);
                 if (ADJ) {
-                    const ulonglong2 Cv = *reinterpret_cast<const ulonglong2*>(sC + (tb + u) * N + q * kNS);
-                    const f2 yv = pY[(tb + u) * CB];
-                    P[0] = mul2(P[0], a0);
-                    P[1] = mul2(P[1], a1);
-                    G[0] = fma2(P[0], mul2(yv, Cv.x), G[0]);
-                    G[1] = fma2(P[1], mul2(yv, Cv.y), G[1]);
+                    Cv = *reinterpret_cast<const ulonglong2*>(sC + t * N + q * kNS);
+                    yv = pY[t * (CB / 2)];
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const f2 d = dup2(j ? w.z : w.x), dx = dup2(j ? w.w : w.y);
+                    const f2 a0 = ex2_2(mul2(d, A2[j][0])), a1 = ex2_2(mul2(d, A2[j][1]));
+                    h[j][0] = fma2(a0, h[j][0], mul2(dx, Bv.x));
+                    h[j][1] = fma2(a1, h[j][1], mul2(dx, Bv.y));
+                    dsum[j] += j ? w.z : w.x;
+                    if (ADJ) {
+                        const f2 y2 = dup2(j ? yv.y : yv.x);
+                        P[j][0] = mul2(P[j][0], a0);
+                        P[j][1] = mul2(P[j][1], a1);
+                        G[j][0] = fma2(P[j][0], mul2(y2, Cv.x), G[j][0]);
+                        G[j][1] = fma2(P[j][1], mul2(y2, Cv.y), G[j][1]);
+                    }
                 }
             }
         }
         __syncthreads();
     }
-    if (ADJ && on) {
-        const int64_t at = (((int64_t)seg * p.b + b) * p.Dch + cg);
+    if (!ADJ) return;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if (!on[j]) continue;
+        const int64_t at = ((int64_t)seg * p.b + b) * p.Dch + cg + j;
         float4 v;
-        unpack2(h[0], v.x, v.y);
-        unpack2(h[1], v.z, v.w);
+        unpack2(h[j][0], v.x, v.y);
+        unpack2(h[j][1], v.z, v.w);
         *reinterpret_cast<float4*>(p.seg_h + at * N + q * kNS) = v;
-        unpack2(G[0], v.x, v.y);
-        unpack2(G[1], v.z, v.w);
+        unpack2(G[j][0], v.x, v.y);
+        unpack2(G[j][1], v.z, v.w);
         *reinterpret_cast<float4*>(p.seg_g + at * N + q * kNS) = v;
-        if (q == 0) p.seg_d[at] = dsum;
+        if (q == 0) p.seg_d[at] = dsum[j];
     }
 }
 
@@ -571,7 +610,7 @@ Plan plan_of(const ScanArgs& a) {
     const int64_t Dg = a.D / a.G, lpc = a.N / kNS;
     const int64_t CB = (kGT / lpc) * kK;
     p.ncb = (Dg + CB - 1) / CB;
-    const int64_t tt = a.N >= 128 ? 64 : 32;
+    const int64_t tt = 32;   // a multiple of the first pass's tile and of kL
     const int64_t per = std::max<int64_t>(1, a.b * a.G * p.ncb), want = (int64_t)sm_count() * 8;
     const int64_t n = std::max<int64_t>(1, std::min<int64_t>((want + per - 1) / per, a.T / (2 * tt)));
     p.SL = std::max<int64_t>(tt, ((a.T + n - 1) / n + tt - 1) / tt * tt);
@@ -601,7 +640,7 @@ template <typename TI, int N, int V>
 cudaError_t bwd_v(const BwdP& p, int64_t lncb, const float* init, const float* dfinal, cudaStream_t st) {
     using L = Cfg<N>;
     const bool adj = p.nseg > 1;
-    const size_t ls = (size_t)L::TT * (L::CB * (adj ? 24 : 16) + 2 * N * 4);
+    const size_t ls = (size_t)L::TT * (L::CB * 12 + 2 * N * 4);
     const int64_t lb = p.b * p.nseg * p.G * lncb, gb = p.b * p.nseg * p.G * p.ncb;
     const int64_t total = p.b * p.Dch * N;
     if (lb >= (int64_t(1) << 31) || gb >= (int64_t(1) << 31) || (total + 255) / 256 >= (int64_t(1) << 31))

@@ -32,16 +32,16 @@ struct FwdP {
 // two passes when the token axis is split).  V: channels per access of x, dt, z, y
 // and elements per access of B, C.
 template <typename TI, int N, int V, bool STATES>
-__global__ void __launch_bounds__(Cfg<N>::NT)
+__global__ void __launch_bounds__(Cfg<N>::NT, (min_blocks<TI, N, V>()))
 scan_fwd_kernel(const FwdP p) {
     using K = Cfg<N>;
-    constexpr int NT = K::NT, LPC = K::LPC, CB = K::CB, TT = K::TT, U = K::U, YP = K::YP;
+    constexpr int NT = K::NT, LPC = K::LPC, CB = K::CB, TT = K::TT, U = K::U, UT = K::UT, YP = K::YP;
     constexpr int PR = CB / V, RS = NT / PR, IT = TT / RS;        // threads a row, rows a pass, passes
     constexpr int BI = TT * N / V / NT;                            // accesses of B (and of C) a thread
     static_assert(IT >= 1 && RS * IT == TT && BI >= 1, "tile shape");
     extern __shared__ __align__(16) unsigned char smem[];
-    ulonglong2* sP = reinterpret_cast<ulonglong2*>(smem);                       // [TT][CB] (d, d, dx, dx)
-    float* sB = reinterpret_cast<float*>(smem + (size_t)TT * CB * 16);          // [TT][N]
+    float2* sP = reinterpret_cast<float2*>(smem);                               // [TT][CB] (d, dx)
+    float* sB = reinterpret_cast<float*>(smem + (size_t)TT * CB * 8);           // [TT][N]
     float* sC = sB + TT * N;
     float* sY = sC + TT * N;                                                    // [TT][YP]
     typedef typename Pack<TI, V>::Raw Raw;
@@ -54,13 +54,12 @@ scan_fwd_kernel(const FwdP p) {
     id /= p.G;
     const int seg = id % p.nseg, b = id / p.nseg;
     const int n = p.lengths ? min(max(__ldg(p.lengths + b), 0), p.T) : p.T;
-    const int s0 = seg * p.SL, s1 = min(s0 + p.SL, p.T);
+    const int s0 = seg * p.SL, s1 = min(s0 + p.SL, p.T), sn = min(s1, n);
 
     // tile duty: V channels of rows r0, r0 + RS, ...
     const int lc = (tid % PR) * V, r0 = tid / PR;
-    const int cg = cb * CB + lc;                       // channel inside the group
-    const bool con = cg < p.Dg;
-    const int64_t c = (int64_t)g * p.Dg + cg;
+    const bool con = cb * CB + lc < p.Dg;
+    const int64_t c = (int64_t)g * p.Dg + cb * CB + lc;
     const TI* xp = static_cast<const TI*>(p.x) + (int64_t)b * p.sx.b + c;
     const TI* dp = static_cast<const TI*>(p.dt) + (int64_t)b * p.sdt.b + c;
     const TI* zp = static_cast<const TI*>(p.z) + (int64_t)b * p.sz.b + c;
@@ -74,26 +73,26 @@ scan_fwd_kernel(const FwdP p) {
         skip[j] = p.D && con && !STATES ? __ldg(p.D + c + j) : 0.f;
     }
 
-    // scan duty: states q kNS .. of channel ch
-    const int q = lane % LPC, ch = warp * K::CPW + lane / LPC;
-    const bool on = cb * CB + ch < p.Dg;
+    // scan duty: states q kNS .. of channels ch, ch + 1
+    const int q = lane % LPC, ch = 2 * (warp * K::CPW + lane / LPC);
     const int64_t sc = ((int64_t)b * p.Dch + (int64_t)g * p.Dg + cb * CB + ch) * N + q * kNS;   // in [b][D][N]
     const int64_t seg_off = (int64_t)seg * p.b * p.Dch * N;
-    f2 A2[kNS / 2], h[kNS / 2];
-    {
+    f2 A2[2][2], h[2][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f), v = a;
-        if (on) {
-            const float* Ap = p.A + ((int64_t)g * p.Dg + cb * CB + ch) * N + q * kNS;
+        if (cb * CB + ch + j < p.Dg) {
+            const float* Ap = p.A + ((int64_t)g * p.Dg + cb * CB + ch + j) * N + q * kNS;
             a = make_float4(__ldg(Ap), __ldg(Ap + 1), __ldg(Ap + 2), __ldg(Ap + 3));
             const float* hp = STATES ? nullptr : p.nseg > 1 ? p.seg_h + seg_off + sc : p.init ? p.init + sc : nullptr;
-            if (hp) v = make_float4(hp[0], hp[1], hp[2], hp[3]);
+            if (hp) v = make_float4(hp[j * N], hp[j * N + 1], hp[j * N + 2], hp[j * N + 3]);
         }
-        A2[0] = pack2(a.x * kLog2e, a.y * kLog2e);
-        A2[1] = pack2(a.z * kLog2e, a.w * kLog2e);
-        h[0] = pack2(v.x, v.y);
-        h[1] = pack2(v.z, v.w);
+        A2[j][0] = pack2(a.x * kLog2e, a.y * kLog2e);
+        A2[j][1] = pack2(a.z * kLog2e, a.w * kLog2e);
+        h[j][0] = pack2(v.x, v.y);
+        h[j][1] = pack2(v.z, v.w);
     }
-    float dsum = 0.f;
+    float dsum[2] = {0.f, 0.f};
 
     Raw rx[IT], rd[IT], rz[IT], rB[BI], rC[BI];
     auto load = [&](int t0) {
@@ -101,7 +100,7 @@ scan_fwd_kernel(const FwdP p) {
         for (int i = 0; i < IT; ++i) {
             const int t = t0 + r0 + i * RS;
             rx[i] = rd[i] = rz[i] = zero_raw<Raw>();
-            if (con && t < min(n, s1)) {
+            if (con && t < sn) {
                 rx[i] = load_raw<TI, V>(xp + (int64_t)t * p.sx.t);
                 rd[i] = load_raw<TI, V>(dp + (int64_t)t * p.sdt.t);
                 if (!STATES && p.z) rz[i] = load_raw<TI, V>(zp + (int64_t)t * p.sz.t);
@@ -111,7 +110,7 @@ scan_fwd_kernel(const FwdP p) {
         for (int i = 0; i < BI; ++i) {
             const int e = (tid + i * NT) * V, t = t0 + e / N;
             rB[i] = rC[i] = zero_raw<Raw>();
-            if (t < min(n, s1)) {
+            if (t < sn) {
                 rB[i] = load_raw<TI, V>(Bp + (int64_t)t * p.sB.t + e % N);
                 if (!STATES) rC[i] = load_raw<TI, V>(Cp + (int64_t)t * p.sC.t + e % N);
             }
@@ -131,23 +130,23 @@ scan_fwd_kernel(const FwdP p) {
         Raw kx[IT], kz[IT];   // kept for the epilogue while the next tile loads
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            float fx[V], fd[V];
-            Conv<TI, V>::to(rx[i], fx);
-            Conv<TI, V>::to(rd[i], fd);
             kx[i] = rx[i];
             kz[i] = rz[i];
             const int r = r0 + i * RS;
-            const bool real = con && t0 + r < min(n, s1);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float v = fd[j] + bias[j];
-                const float d = real ? (p.softplus ? softplus(v) : v) : 0.f;
-                const int cc = lc + j;
-                ulonglong2 w;
-                w.x = dup2(d);
-                w.y = dup2(d * fx[j]);
-                sP[r * CB + (cc ^ ((cc >> 3) & 1))] = w;   // swizzled: conflict-free 16-byte stores
-            }
+            const bool real = con && t0 + r < sn;
+            f2 fx[1], fd[1];
+            to_pairs<TI, V>(rx[i], fx);
+            to_pairs<TI, V>(rd[i], fd);
+            f2 d = add2(fd[0], pack2(bias[0], bias[V - 1]));
+            if (p.softplus) d = softplus2(d);
+            if (!real) d = dup2(0.f);
+            float d0, d1, u0, u1;
+            unpack2(d, d0, d1);
+            unpack2(mul2(d, fx[0]), u0, u1);
+            if constexpr (V == 2)
+                *reinterpret_cast<float4*>(sP + r * CB + lc) = make_float4(d0, u0, d1, u1);
+            else
+                sP[r * CB + lc] = make_float2(d0, u0);
         }
 #pragma unroll
         for (int i = 0; i < BI; ++i) {
@@ -164,30 +163,38 @@ scan_fwd_kernel(const FwdP p) {
         }
         __syncthreads();
         if (t0 + TT < s1) load(t0 + TT);
-        const ulonglong2* pP = sP + (ch ^ ((ch >> 3) & 1));
+        const float4* pP = reinterpret_cast<const float4*>(sP + ch);
         const float* pB = sB + q * kNS;
         const float* pC = sC + q * kNS;
+        constexpr int UN = 8;   // tokens unrolled
 #pragma unroll 1
-        for (int tb = 0; tb < TT; tb += U) {
-            float yv[U];
+        for (int tb = 0; tb < TT; tb += UN) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const ulonglong2 w = pP[(tb + u) * CB];
-                const ulonglong2 Bv = *reinterpret_cast<const ulonglong2*>(pB + (tb + u) * N);
-                h[0] = fma2(ex2_2(mul2(w.x, A2[0])), h[0], mul2(w.y, Bv.x));
-                h[1] = fma2(ex2_2(mul2(w.x, A2[1])), h[1], mul2(w.y, Bv.y));
-                if (STATES) {
-                    float lo, hi;
-                    unpack2(w.x, lo, hi);
-                    dsum += lo;
-                } else {
-                    const ulonglong2 Cv = *reinterpret_cast<const ulonglong2*>(pC + (tb + u) * N);
-                    yv[u] = sum2(fma2(h[1], Cv.y, mul2(h[0], Cv.x)));
+            for (int tu = 0; tu < UN; tu += UT) {
+                float yv[U];
+#pragma unroll
+                for (int u = 0; u < UT; ++u) {
+                    const int t = tb + tu + u;
+                    const float4 w = pP[t * (CB / 2)];
+                    const ulonglong2 Bv = *reinterpret_cast<const ulonglong2*>(pB + t * N);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const f2 d = dup2(j ? w.z : w.x), dx = dup2(j ? w.w : w.y);
+                        h[j][0] = fma2(ex2_2(mul2(d, A2[j][0])), h[j][0], mul2(dx, Bv.x));
+                        h[j][1] = fma2(ex2_2(mul2(d, A2[j][1])), h[j][1], mul2(dx, Bv.y));
+                        if (STATES) dsum[j] += j ? w.z : w.x;
+                    }
+                    if (!STATES) {
+                        const ulonglong2 Cv = *reinterpret_cast<const ulonglong2*>(pC + t * N);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            yv[2 * u + j] = sum2(fma2(h[j][1], Cv.y, mul2(h[j][0], Cv.x)));
+                    }
                 }
-            }
-            if (!STATES) {
-                const float s = lanes_sum<LPC, U>(yv);
-                if (LPC <= U || q < U) sY[(tb + (lane & (U - 1))) * YP + ch] = s;
+                if (!STATES) {   // value 2 u + j: token u of the UT, channel ch + j
+                    const float s = lanes_sum<LPC, U>(yv);
+                    if (LPC <= U || q < U) sY[(tb + tu + ((lane & (U - 1)) >> 1)) * YP + ch + (lane & 1)] = s;
+                }
             }
         }
         __syncthreads();
@@ -195,32 +202,42 @@ scan_fwd_kernel(const FwdP p) {
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
                 const int r = r0 + i * RS, t = t0 + r;
-                float fx[V], fz[V], o[V];
-                Conv<TI, V>::to(kx[i], fx);
-                if (p.z) Conv<TI, V>::to(kz[i], fz);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    float v = fmaf(skip[j], fx[j], sY[r * YP + lc + j]);
-                    if (p.z) v *= fz[j] * sigmoid(fz[j]);
-                    o[j] = t < n ? v : 0.f;
+                f2 fx[1], o[1];
+                to_pairs<TI, V>(kx[i], fx);
+                if constexpr (V == 2) {
+                    const float2 yv = *reinterpret_cast<const float2*>(sY + r * YP + lc);
+                    o[0] = pack2(yv.x, yv.y);
+                } else {
+                    o[0] = pack2(sY[r * YP + lc], 0.f);
                 }
-                if (t < s1) store_raw<TI, V>(yp + (int64_t)t * p.sy.t, Conv<TI, V>::from(o));
+                o[0] = fma2(pack2(skip[0], skip[V - 1]), fx[0], o[0]);
+                if (p.z) {
+                    f2 fz[1];
+                    to_pairs<TI, V>(kz[i], fz);
+                    o[0] = mul2(o[0], mul2(fz[0], sigmoid2(fz[0])));
+                }
+                if (t >= n) o[0] = dup2(0.f);
+                if (t < s1) store_raw<TI, V>(yp + (int64_t)t * p.sy.t, from_pairs<TI, V>(o));
             }
         }
     }
-    if (!on) return;
-    float4 v;
-    unpack2(h[0], v.x, v.y);
-    unpack2(h[1], v.z, v.w);
-    if (STATES) {
-        *reinterpret_cast<float4*>(p.seg_h + seg_off + sc) = v;
-        if (q == 0) p.seg_d[((int64_t)seg * p.b + b) * p.Dch + (int64_t)g * p.Dg + cb * CB + ch] = dsum;
-    } else if (seg == p.nseg - 1) {
-        float* f = p.fin + sc;
-        f[0] = v.x;
-        f[1] = v.y;
-        f[2] = v.z;
-        f[3] = v.w;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if (cb * CB + ch + j >= p.Dg) continue;
+        float4 v;
+        unpack2(h[j][0], v.x, v.y);
+        unpack2(h[j][1], v.z, v.w);
+        if (STATES) {
+            *reinterpret_cast<float4*>(p.seg_h + seg_off + sc + j * N) = v;
+            if (q == 0)
+                p.seg_d[((int64_t)seg * p.b + b) * p.Dch + (int64_t)g * p.Dg + cb * CB + ch + j] = dsum[j];
+        } else if (seg == p.nseg - 1) {
+            float* f = p.fin + sc + j * N;
+            f[0] = v.x;
+            f[1] = v.y;
+            f[2] = v.z;
+            f[3] = v.w;
+        }
     }
 }
 
@@ -302,10 +319,10 @@ scan_step_kernel(float* __restrict__ state, const TI* __restrict__ x, const TI* 
 // Splitting the token axis costs a second pass over it (the first without y), so
 // it is done only where one pass leaves most of the GPU without warps.
 int64_t warps_of(const ScanArgs& a) {
-    const int64_t Dg = a.D / a.G, nt = a.N >= 64 ? 256 : 128, CB = nt / (a.N / kNS);
+    const int64_t Dg = a.D / a.G, nt = a.N >= 64 ? 128 : 64, CB = 2 * (nt / (a.N / kNS));
     return a.b * a.G * ((Dg + CB - 1) / CB) * (nt / 32);
 }
-int64_t tile_of(const ScanArgs& a) { return a.N >= 128 ? 64 : 32; }
+int64_t tile_of(const ScanArgs& a) { return a.N >= 128 ? 32 : 16; }
 int64_t seg_len(const ScanArgs& a) {
     const int64_t tt = tile_of(a), full = (int64_t)sm_count() * 16, w = std::max<int64_t>(1, warps_of(a));
     if (2 * w >= full) return std::max<int64_t>(tt, (a.T + tt - 1) / tt * tt);

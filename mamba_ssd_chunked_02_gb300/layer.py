@@ -86,10 +86,17 @@ def _call(name, *args):
         raise Mamba2Error("mamba2_" + name, rc)
 
 
+# The current stream's handle without a Stream object, and the current device without the
+# lazy-initialisation check: 0.1 us instead of 3 us of a 10 us call.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _raw_stream(stream, device):
     """The cudaStream_t to launch on: `stream`, or the current one of `device`."""
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _current_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -101,7 +108,7 @@ def _io(x, name):
         raise TypeError(f"unsupported element type {d}: {name} must be bfloat16 or float32")
     if not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
-    if x.get_device() != torch.cuda.current_device():
+    if x.get_device() != _current_device():
         raise ValueError(f"{name} must be on the current CUDA device")
     return d
 
@@ -141,11 +148,13 @@ def _token(t, name, dtype, shape, device, st, at, lead=2, optional=False):
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     s = t.stride()
-    width = 1
-    for k in range(len(shape) - 1, lead - 1, -1):
-        if shape[k] != 1 and s[k] != width:
+    width = shape[-1]
+    if s[-1] != 1 and width > 1:
+        raise ValueError(f"{name}: each token's data must be contiguous")
+    if len(shape) > lead + 1:       # groups by states
+        if s[-2] != width and shape[-2] > 1:
             raise ValueError(f"{name}: each token's data must be contiguous")
-        width *= shape[k]
+        width *= shape[-2]
     # a dimension of one entry is never stepped over: any stride does
     st[at] = s[0] if shape[0] > 1 else width
     st[at + 1] = s[1] if lead == 2 and shape[1] > 1 else width
@@ -165,8 +174,7 @@ def _space(kind, shape, workspace, device):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _addr(s):
-    return ctypes.addressof(s)
+_addr = ctypes.addressof
 
 
 # ---- conv -------------------------------------------------------------------
