@@ -218,7 +218,7 @@ scan_local_kernel(const BwdP p) {
         }
         __syncthreads();
     }
-    if (!ADJ) return;
+    if constexpr (ADJ)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         if (!on[j]) continue;
@@ -273,33 +273,64 @@ template <int M, int CPW, int LPC> __device__ __forceinline__ void channel_sum(f
     }
 }
 
-template <int N> struct GCfg {
+template <typename TI, int N> struct GCfg {
     static constexpr int LPC = N / kNS, CPW = 32 / LPC, WARPS = kGT / 32;
     static constexpr int CK = WARPS * CPW;       // channels of one turn
     static constexpr int CB = CK * kK;           // channels of the block
     static constexpr int U = LPC < 8 ? LPC : 8;
     static constexpr int QP = CB + (CPW < 2 ? 2 : CPW);   // pitch of the q, r, y tiles
-    static constexpr size_t smem = (size_t)kL * CB * 24 + 3 * (size_t)kL * QP * 4 + 2 * (size_t)kL * N * 4 +
-                                   (size_t)WARPS * 2 * kL * N * 4 + 4 * (size_t)kK * kGT * 16;
+    // shared memory, in bytes
+    static constexpr size_t lane16 = (size_t)kK * kGT * 16;                   // a float4 a channel and lane
+    static constexpr size_t raw = (size_t)kL * CB * sizeof(TI), rawBC = (size_t)kL * N * sizeof(TI);
+    static constexpr size_t stage = 4 * raw + 2 * rawBC + lane16 + (size_t)kK * kGT * 4;
+    static constexpr size_t smem = (size_t)kL * CB * 12 + 3 * (size_t)kL * QP * 4 + 2 * (size_t)kL * N * 4 +
+                                   (size_t)WARPS * 2 * kL * N * 4 + 4 * lane16 + stage;
 };
 
-// (3) Gradients.  Block: CB channels of one group, one stretch of one sequence.
+// BYTES from global to shared memory without registers, zeros when !real.  Two bytes
+// (one bf16) are too few for an asynchronous copy.
+template <int BYTES> __device__ __forceinline__ void stage_copy(void* dst, const void* src, bool real) {
+    if constexpr (BYTES >= 4) {
+        const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(BYTES),
+                     "r"(real ? BYTES : 0)
+                     : "memory");
+    } else {
+        *static_cast<unsigned short*>(dst) = real ? *static_cast<const unsigned short*>(src) : 0;
+    }
+}
+__device__ __forceinline__ void stage_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void stage_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+// (3) Gradients.  Block: CB channels of one group, one stretch of one sequence.  What a
+// thread stages for the tile before (inputs, stored states) only it reads, so the copies
+// need no barrier; they run under the arithmetic of the tile at hand.
 template <typename TI, int N, int V, bool GATE>
 __global__ void __launch_bounds__(kGT)
 scan_grad_kernel(const BwdP p) {
-    using K = GCfg<N>;
+    using K = GCfg<TI, N>;
     constexpr int LPC = K::LPC, CPW = K::CPW, CB = K::CB, QP = K::QP, U = K::U;
     constexpr int PR0 = CB / V, PR = PR0 < kGT ? PR0 : kGT;          // threads a row
     constexpr int RS = kGT / PR, CI = PR0 / PR, RI = RS < kL ? kL / RS : 1;   // rows a pass, column passes, row passes
     static_assert(RS * RI >= kL && CI * PR == PR0, "tile shape");    // RS > kL: the last threads have no row
+    constexpr int BI = (kL * N / V + kGT - 1) / kGT;                 // accesses of B (and of C) a thread
+    constexpr int VB = V * (int)sizeof(TI);
     extern __shared__ __align__(16) unsigned char smem[];
-    ulonglong2* sP = reinterpret_cast<ulonglong2*>(smem);                 // [kL][CB] (d, d, dx, dx)
+    float2* sP = reinterpret_cast<float2*>(smem);                         // [kL][CB] (d, dx)
     float4* sA = reinterpret_cast<float4*>(sP + kL * CB);                 // [kK][kGT] A log2(e)
     float4* sH = sA + kK * kGT;                                           // entering state
     float4* sG = sH + kK * kGT;                                           // adjoint carried back
     float4* sD = sG + kK * kGT;                                           // dA
-    f2* sY = reinterpret_cast<f2*>(sD + kK * kGT);                        // [kL][CB] (dY, dY)
-    float* sB = reinterpret_cast<float*>(sY + kL * CB);                   // [kL][N]
+    float4* stK = sD + kK * kGT;                                          // staged: stored state
+    float* stD = reinterpret_cast<float*>(stK + kK * kGT);                // staged: its sum of d
+    TI* stX = reinterpret_cast<TI*>(stD + kK * kGT);                      // staged: x, dt, dy, z [kL][CB], B, C [kL][N]
+    TI* stT = stX + kL * CB;
+    TI* stY = stT + kL * CB;
+    TI* stZ = stY + kL * CB;
+    TI* stB = stZ + kL * CB;
+    TI* stC = stB + kL * N;
+    float* sY = reinterpret_cast<float*>(stC + kL * N);                   // [kL][CB] dY
+    float* sB = sY + kL * CB;                                             // [kL][N]
     float* sC = sB + kL * N;
     float* sR = sC + kL * N;                                              // [WARPS][2 kL N]
     float* sQ = sR + K::WARPS * 2 * kL * N;                               // [kL][QP] q; then r, then C.h
@@ -320,16 +351,17 @@ scan_grad_kernel(const BwdP p) {
     const int left = p.Dg - cb * CB;                    // channels of the block that exist
 
     const int lc0 = (tid % PR) * V, r0 = tid / PR;
-    float bias[CI][V], skip[CI][V], accD[CI][V], accB[CI][V];
+    f2 bias[CI], skip[CI], accD[CI], accB[CI];
 #pragma unroll
-    for (int ci = 0; ci < CI; ++ci)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int lc = lc0 + ci * PR * V + j;
-            bias[ci][j] = p.bias && lc < left ? __ldg(p.bias + cg0 + lc) : 0.f;
-            skip[ci][j] = p.D && lc < left ? __ldg(p.D + cg0 + lc) : 0.f;
-            accD[ci][j] = accB[ci][j] = 0.f;
-        }
+    for (int ci = 0; ci < CI; ++ci) {
+        const int lc = lc0 + ci * PR * V;
+        const bool in = lc < left;
+        const float* pb = p.bias && in ? p.bias + cg0 + lc : nullptr;
+        const float* pd = p.D && in ? p.D + cg0 + lc : nullptr;
+        bias[ci] = pb ? pack2(__ldg(pb), __ldg(pb + V - 1)) : dup2(0.f);
+        skip[ci] = pd ? pack2(__ldg(pd), __ldg(pd + V - 1)) : dup2(0.f);
+        accD[ci] = accB[ci] = dup2(0.f);
+    }
     const int q = lane % LPC, cw = lane / LPC;
     const int64_t seg_at = ((int64_t)seg * p.b + b) * p.Dch;
 #pragma unroll
@@ -348,94 +380,142 @@ scan_grad_kernel(const BwdP p) {
         sG[k * kGT + tid] = gg;
         sD[k * kGT + tid] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    const TI* xb = static_cast<const TI*>(p.x) + (int64_t)b * p.sx.b + cg0;
+    const TI* tb_ = static_cast<const TI*>(p.dt) + (int64_t)b * p.sdt.b + cg0;
+    const TI* zb = static_cast<const TI*>(p.z) + (int64_t)b * p.sz.b + cg0;
+    const TI* yb = static_cast<const TI*>(p.dy) + (int64_t)b * p.sy.b + cg0;
+    const TI* Bb = static_cast<const TI*>(p.B) + (int64_t)b * p.sB.b + (int64_t)g * N;
+    const TI* Cb = static_cast<const TI*>(p.C) + (int64_t)b * p.sC.b + (int64_t)g * N;
+
+    auto stage = [&](int t0) {
+#pragma unroll
+        for (int ci = 0; ci < CI; ++ci)
+#pragma unroll
+            for (int i = 0; i < RI; ++i) {
+                const int r = r0 + i * RS, lc = lc0 + ci * PR * V, at = r * CB + lc;
+                if (r >= kL) continue;
+                const bool real = lc < left && t0 + r < sn;
+                const int64_t t = real ? t0 + r : 0;   // an address inside the tensor either way
+                const int cc = real ? lc : 0;
+                stage_copy<VB>(stX + at, xb + t * p.sx.t + cc, real);
+                stage_copy<VB>(stT + at, tb_ + t * p.sdt.t + cc, real);
+                stage_copy<VB>(stY + at, yb + t * p.sy.t + cc, real);
+                if (GATE) stage_copy<VB>(stZ + at, zb + t * p.sz.t + cc, real);
+            }
+#pragma unroll
+        for (int i = 0; i < BI; ++i) {
+            const int e = (tid + i * kGT) * V, r = e / N;
+            if (e >= kL * N) continue;
+            const bool real = t0 + r < sn;
+            const int64_t t = real ? t0 + r : 0;
+            stage_copy<VB>(stB + e, Bb + t * p.sB.t + e % N, real);
+            stage_copy<VB>(stC + e, Cb + t * p.sC.t + e % N, real);
+        }
+        const int64_t ck_at = ((int64_t)b * p.nck + t0 / kL) * p.Dch + cg0;
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+            const int ch = k * K::CK + warp * CPW + cw;
+            const int64_t o = ck_at + (ch < left ? ch : 0);
+            stage_copy<16>(stK + k * kGT + tid, p.ck + o * N + q * kNS, ch < left);
+            stage_copy<4>(stD + k * kGT + tid, p.ck_d + o, ch < left);
+        }
+        stage_commit();
+    };
 
     const int tiles = (s1 - s0 + kL - 1) / kL;
+    stage(s0 + (tiles - 1) * kL);
     for (int ti = tiles - 1; ti >= 0; --ti) {
         const int t0 = s0 + ti * kL;
+        stage_wait();
         Raw kx[CI][RI], kd[CI][RI], kz[CI][RI], ky[CI][RI];
 #pragma unroll
         for (int ci = 0; ci < CI; ++ci)
 #pragma unroll
             for (int i = 0; i < RI; ++i) {
-                const int r = r0 + i * RS, t = t0 + r, lc = lc0 + ci * PR * V;
+                const int r = r0 + i * RS, lc = lc0 + ci * PR * V, at = r * CB + lc;
                 if (r >= kL) continue;
-                const bool real = lc < left && t < sn;
-                kx[ci][i] = kd[ci][i] = kz[ci][i] = ky[ci][i] = zero_raw<Raw>();
-                const int64_t c = cg0 + lc;
-                if (real) {
-                    kx[ci][i] = load_raw<TI, V>(static_cast<const TI*>(p.x) + (int64_t)b * p.sx.b + (int64_t)t * p.sx.t + c);
-                    kd[ci][i] = load_raw<TI, V>(static_cast<const TI*>(p.dt) + (int64_t)b * p.sdt.b + (int64_t)t * p.sdt.t + c);
-                    if (GATE) kz[ci][i] = load_raw<TI, V>(static_cast<const TI*>(p.z) + (int64_t)b * p.sz.b + (int64_t)t * p.sz.t + c);
-                    ky[ci][i] = load_raw<TI, V>(static_cast<const TI*>(p.dy) + (int64_t)b * p.sy.b + (int64_t)t * p.sy.t + c);
+                const bool real = lc < left && t0 + r < sn;
+                kx[ci][i] = *reinterpret_cast<const Raw*>(stX + at);
+                kd[ci][i] = *reinterpret_cast<const Raw*>(stT + at);
+                ky[ci][i] = *reinterpret_cast<const Raw*>(stY + at);
+                if (GATE) kz[ci][i] = *reinterpret_cast<const Raw*>(stZ + at);
+                f2 fx[1], fd[1], fz[1], fy[1];
+                to_pairs<TI, V>(kx[ci][i], fx);
+                to_pairs<TI, V>(kd[ci][i], fd);
+                to_pairs<TI, V>(ky[ci][i], fy);
+                f2 d = add2(fd[0], bias[ci]);
+                if (p.softplus) d = softplus2(d);
+                if (!real) d = dup2(0.f);
+                if (GATE) {
+                    to_pairs<TI, V>(kz[ci][i], fz);
+                    fy[0] = mul2(fy[0], mul2(fz[0], sigmoid2(fz[0])));
                 }
-                float fx[V], fd[V], fz[V], fy[V];
-                Conv<TI, V>::to(kx[ci][i], fx);
-                Conv<TI, V>::to(kd[ci][i], fd);
-                Conv<TI, V>::to(kz[ci][i], fz);
-                Conv<TI, V>::to(ky[ci][i], fy);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float v = fd[j] + bias[ci][j];
-                    const float d = real ? (p.softplus ? softplus(v) : v) : 0.f;
-                    const int cc = lc + j;
-                    ulonglong2 w;
-                    w.x = dup2(d);
-                    w.y = dup2(d * fx[j]);
-                    sP[r * CB + (cc ^ ((cc >> 3) & 1))] = w;
-                    sY[r * CB + cc] = dup2(GATE ? fy[j] * fz[j] * sigmoid(fz[j]) : fy[j]);
+                float d0, d1, u0, u1, y0, y1;
+                unpack2(d, d0, d1);
+                unpack2(mul2(d, fx[0]), u0, u1);
+                unpack2(fy[0], y0, y1);
+                if constexpr (V == 2) {
+                    *reinterpret_cast<float4*>(sP + at) = make_float4(d0, u0, d1, u1);
+                    *reinterpret_cast<float2*>(sY + at) = make_float2(y0, y1);
+                } else {
+                    sP[at] = make_float2(d0, u0);
+                    sY[at] = y0;
                 }
             }
-        for (int e = tid * V; e < kL * N; e += kGT * V) {
-            const int t = t0 + e / N;
-            float fb[V], fc[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) fb[j] = fc[j] = 0.f;
-            if (t < sn) {
-                const int64_t o = (int64_t)g * N + e % N;
-                Conv<TI, V>::to(load_raw<TI, V>(static_cast<const TI*>(p.B) + (int64_t)b * p.sB.b + (int64_t)t * p.sB.t + o), fb);
-                Conv<TI, V>::to(load_raw<TI, V>(static_cast<const TI*>(p.C) + (int64_t)b * p.sC.b + (int64_t)t * p.sC.t + o), fc);
-            }
+        for (int i = 0; i < BI; ++i) {
+            const int e = (tid + i * kGT) * V;
+            if (e >= kL * N) continue;
+            float f[V];
+            Conv<TI, V>::to(*reinterpret_cast<const Raw*>(stB + e), f);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                sB[e + j] = fb[j];
-                sC[e + j] = fc[j];
-            }
+            for (int j = 0; j < V; ++j) sB[e + j] = f[j];
+            Conv<TI, V>::to(*reinterpret_cast<const Raw*>(stC + e), f);
+#pragma unroll
+            for (int j = 0; j < V; ++j) sC[e + j] = f[j];
+        }
+        // the stored states, brought to the true ones (the staging room is then free)
+        f2 h0[kK][2];
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+            const float4 v = stK[k * kGT + tid];
+            const f2 c2 = dup2(stD[k * kGT + tid]);
+            const ulonglong2 A2 = *reinterpret_cast<const ulonglong2*>(sA + k * kGT + tid);
+            const ulonglong2 hi = *reinterpret_cast<const ulonglong2*>(sH + k * kGT + tid);
+            h0[k][0] = fma2(ex2_2(mul2(c2, A2.x)), hi.x, pack2(v.x, v.y));
+            h0[k][1] = fma2(ex2_2(mul2(c2, A2.y)), hi.y, pack2(v.z, v.w));
         }
         __syncthreads();
+        if (ti > 0) stage(t0 - kL);
 
         f2 dBC[2][kL][2];   // dB, dC of the lane's states, summed over its channels
 #pragma unroll
         for (int w = 0; w < 2; ++w)
 #pragma unroll
             for (int t = 0; t < kL; ++t) dBC[w][t][0] = dBC[w][t][1] = 0;
-        const int64_t ck_at = ((int64_t)b * p.nck + t0 / kL) * p.Dch + cg0;
 #pragma unroll 1
         for (int k = 0; k < kK; ++k) {
             const int ch = k * K::CK + warp * CPW + cw;
-            const ulonglong2* pP = sP + (ch ^ ((ch >> 3) & 1));
-            const f2* pY = sY + ch;
+            const float2* pP = sP + ch;
+            const float* pY = sY + ch;
             const ulonglong2 A2 = *reinterpret_cast<const ulonglong2*>(sA + k * kGT + tid);
             f2 hs[kL + 1][2], as[kL][2];
-            {
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                float cd = 0.f;
-                if (ch < left) {
-                    v = *reinterpret_cast<const float4*>(p.ck + (ck_at + ch) * N + q * kNS);
-                    cd = p.ck_d[ck_at + ch];
-                }
-                const ulonglong2 hi = *reinterpret_cast<const ulonglong2*>(sH + k * kGT + tid);
-                const f2 c2 = dup2(cd);
-                hs[0][0] = fma2(ex2_2(mul2(c2, A2.x)), hi.x, pack2(v.x, v.y));
-                hs[0][1] = fma2(ex2_2(mul2(c2, A2.y)), hi.y, pack2(v.z, v.w));
+            hs[0][0] = h0[0][0];
+            hs[0][1] = h0[0][1];
+#pragma unroll
+            for (int i = 0; i + 1 < kK; ++i) {   // the loop over k is not unrolled: the next one moves up
+                h0[i][0] = h0[i + 1][0];
+                h0[i][1] = h0[i + 1][1];
             }
 #pragma unroll
             for (int t = 0; t < kL; ++t) {
-                const ulonglong2 w = pP[t * CB];
+                const float2 w = pP[t * CB];
                 const ulonglong2 Bv = *reinterpret_cast<const ulonglong2*>(sB + t * N + q * kNS);
-                as[t][0] = ex2_2(mul2(w.x, A2.x));
-                as[t][1] = ex2_2(mul2(w.x, A2.y));
-                hs[t + 1][0] = fma2(as[t][0], hs[t][0], mul2(w.y, Bv.x));
-                hs[t + 1][1] = fma2(as[t][1], hs[t][1], mul2(w.y, Bv.y));
+                const f2 d = dup2(w.x), dx = dup2(w.y);
+                as[t][0] = ex2_2(mul2(d, A2.x));
+                as[t][1] = ex2_2(mul2(d, A2.y));
+                hs[t + 1][0] = fma2(as[t][0], hs[t][0], mul2(dx, Bv.x));
+                hs[t + 1][1] = fma2(as[t][1], hs[t][1], mul2(dx, Bv.y));
             }
             ulonglong2 G = *reinterpret_cast<const ulonglong2*>(sG + k * kGT + tid);
             ulonglong2 dA = *reinterpret_cast<const ulonglong2*>(sD + k * kGT + tid);
@@ -445,24 +525,24 @@ scan_grad_kernel(const BwdP p) {
 #pragma unroll
                 for (int u = U - 1; u >= 0; --u) {
                     const int t = tb + u;
-                    const ulonglong2 w = pP[t * CB];
+                    const float2 w = pP[t * CB];
                     const ulonglong2 Bv = *reinterpret_cast<const ulonglong2*>(sB + t * N + q * kNS);
                     const ulonglong2 Cv = *reinterpret_cast<const ulonglong2*>(sC + t * N + q * kNS);
-                    const f2 y2 = pY[t * CB];
+                    const f2 y2 = dup2(pY[t * CB]), d = dup2(w.x), dx = dup2(w.y);
                     G.x = fma2(y2, Cv.x, G.x);
                     G.y = fma2(y2, Cv.y, G.y);
                     dBC[1][t][0] = fma2(y2, hs[t + 1][0], dBC[1][t][0]);
                     dBC[1][t][1] = fma2(y2, hs[t + 1][1], dBC[1][t][1]);
-                    dBC[0][t][0] = fma2(w.y, G.x, dBC[0][t][0]);
-                    dBC[0][t][1] = fma2(w.y, G.y, dBC[0][t][1]);
+                    dBC[0][t][0] = fma2(dx, G.x, dBC[0][t][0]);
+                    dBC[0][t][1] = fma2(dx, G.y, dBC[0][t][1]);
                     vq[u] = sum2(fma2(G.y, Bv.y, mul2(G.x, Bv.x)));
                     if (GATE) vo[u] = sum2(fma2(hs[t + 1][1], Cv.y, mul2(hs[t + 1][0], Cv.x)));
                     G.x = mul2(G.x, as[t][0]);
                     G.y = mul2(G.y, as[t][1]);
                     const f2 e0 = mul2(G.x, hs[t][0]), e1 = mul2(G.y, hs[t][1]);
                     ve[u] = sum2(fma2(e1, A2.y, mul2(e0, A2.x)));
-                    dA.x = fma2(w.x, e0, dA.x);
-                    dA.y = fma2(w.x, e1, dA.y);
+                    dA.x = fma2(d, e0, dA.x);
+                    dA.y = fma2(d, e1, dA.y);
                 }
                 const int at = (tb + (lane & (U - 1))) * QP + ch;
                 const float fq = lanes_sum<LPC, U>(vq), fe = lanes_sum<LPC, U>(ve);
@@ -511,34 +591,45 @@ scan_grad_kernel(const BwdP p) {
                 const int r = r0 + i * RS, t = t0 + r, lc = lc0 + ci * PR * V;
                 if (r >= kL || lc >= left || t >= s1) continue;
                 const bool real = t < sn;
-                float fx[V], fd[V], fz[V], fy[V], ox[V], od[V], oz[V];
-                Conv<TI, V>::to(kx[ci][i], fx);
-                Conv<TI, V>::to(kd[ci][i], fd);
-                Conv<TI, V>::to(kz[ci][i], fz);
-                Conv<TI, V>::to(ky[ci][i], fy);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const int cc = lc + j;
-                    const float v = fd[j] + bias[ci][j];
-                    float d, dup;
-                    unpack2(sP[r * CB + (cc ^ ((cc >> 3) & 1))].x, d, dup);
-                    float dY = fy[j], slope = 0.f;
+                f2 fx[1], fd[1], fz[1], fy[1], od[1], o[1], qv, ev, ov, d;
+                to_pairs<TI, V>(kx[ci][i], fx);
+                to_pairs<TI, V>(kd[ci][i], fd);
+                to_pairs<TI, V>(ky[ci][i], fy);
+                if constexpr (V == 2) {
+                    const float4 w = *reinterpret_cast<const float4*>(sP + r * CB + lc);
+                    const float2 a = *reinterpret_cast<const float2*>(sQ + r * QP + lc);
+                    const float2 e = *reinterpret_cast<const float2*>(sE + r * QP + lc);
+                    d = pack2(w.x, w.z);
+                    qv = pack2(a.x, a.y);
+                    ev = pack2(e.x, e.y);
                     if (GATE) {
-                        const float sg = sigmoid(fz[j]);
-                        dY = fy[j] * fz[j] * sg;
-                        slope = fy[j] * sg * fmaf(fz[j], 1.f - sg, 1.f);
+                        const float2 h = *reinterpret_cast<const float2*>(sO + r * QP + lc);
+                        ov = pack2(h.x, h.y);
                     }
-                    const float qv = sQ[r * QP + cc], dd = fmaf(fx[j], qv, 0.6931471805599453f * sE[r * QP + cc]);
-                    ox[j] = fmaf(d, qv, skip[ci][j] * dY);
-                    od[j] = real ? (p.softplus ? dd * sigmoid(v) : dd) : 0.f;
-                    oz[j] = GATE ? slope * fmaf(skip[ci][j], fx[j], sO[r * QP + cc]) : 0.f;
-                    accD[ci][j] = fmaf(dY, fx[j], accD[ci][j]);
-                    accB[ci][j] += od[j];
+                } else {
+                    d = pack2(sP[r * CB + lc].x, 0.f);
+                    qv = pack2(sQ[r * QP + lc], 0.f);
+                    ev = pack2(sE[r * QP + lc], 0.f);
+                    if (GATE) ov = pack2(sO[r * QP + lc], 0.f);
                 }
-                const int64_t o = ((int64_t)b * p.T + t) * p.Dch + cg0 + lc;
-                store_raw<TI, V>(static_cast<TI*>(p.dx) + o, Conv<TI, V>::from(ox));
-                store_raw<TI, V>(static_cast<TI*>(p.ddt) + o, Conv<TI, V>::from(od));
-                if (GATE) store_raw<TI, V>(static_cast<TI*>(p.dz) + o, Conv<TI, V>::from(oz));
+                const int64_t at = ((int64_t)b * p.T + t) * p.Dch + cg0 + lc;
+                if (GATE) {
+                    to_pairs<TI, V>(kz[ci][i], fz);
+                    const f2 sg = sigmoid2(fz[0]);
+                    // silu' = sg (1 + z (1 - sg))
+                    const f2 slope = mul2(sg, fma2(fz[0], fma2(sg, dup2(-1.f), dup2(1.f)), dup2(1.f)));
+                    o[0] = mul2(mul2(fy[0], slope), fma2(skip[ci], fx[0], ov));
+                    store_raw<TI, V>(static_cast<TI*>(p.dz) + at, from_pairs<TI, V>(o));
+                    fy[0] = mul2(fy[0], mul2(fz[0], sg));
+                }
+                o[0] = fma2(d, qv, mul2(skip[ci], fy[0]));
+                store_raw<TI, V>(static_cast<TI*>(p.dx) + at, from_pairs<TI, V>(o));
+                od[0] = fma2(fx[0], qv, mul2(dup2(0.6931471805599453f), ev));   // e was taken with A log2(e)
+                if (p.softplus) od[0] = mul2(od[0], sigmoid2(add2(fd[0], bias[ci])));
+                if (!real) od[0] = dup2(0.f);
+                store_raw<TI, V>(static_cast<TI*>(p.ddt) + at, from_pairs<TI, V>(od));
+                accD[ci] = fma2(fy[0], fx[0], accD[ci]);
+                accB[ci] = add2(accB[ci], od[0]);
             }
         __syncthreads();
     }
@@ -559,16 +650,20 @@ scan_grad_kernel(const BwdP p) {
             }
         }
     }
-    // dD, ddt_bias: over the block's rows, through the q tile (RS <= kL rows of it)
-    __syncthreads();
-    if (r0 < kL)
+    // dD, ddt_bias: over the block's rows, through the q and r tiles
+    if (r0 < kL) {
 #pragma unroll
-    for (int ci = 0; ci < CI; ++ci)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            sQ[r0 * QP + lc0 + ci * PR * V + j] = accD[ci][j];
-            sE[r0 * QP + lc0 + ci * PR * V + j] = accB[ci][j];
+        for (int ci = 0; ci < CI; ++ci) {
+            const int at = r0 * QP + lc0 + ci * PR * V;
+            float a, c;
+            unpack2(accD[ci], a, c);
+            sQ[at] = a;
+            if (V == 2) sQ[at + 1] = c;
+            unpack2(accB[ci], a, c);
+            sE[at] = a;
+            if (V == 2) sE[at + 1] = c;
         }
+    }
     __syncthreads();
     for (int c = tid; c < CB && c < left; c += kGT) {
         float a = 0.f, d = 0.f;
@@ -662,9 +757,9 @@ cudaError_t bwd_v(const BwdP& p, int64_t lncb, const float* init, const float* d
         m.g_in = dfinal;
     }
     auto gk = p.z ? scan_grad_kernel<TI, N, V, true> : scan_grad_kernel<TI, N, V, false>;
-    e = allow(gk, GCfg<N>::smem);
+    e = allow(gk, (GCfg<TI, N>::smem));
     if (e != cudaSuccess) return e;
-    gk<<<(unsigned)gb, kGT, GCfg<N>::smem, st>>>(m);
+    gk<<<(unsigned)gb, kGT, (GCfg<TI, N>::smem), st>>>(m);
     return cudaGetLastError();
 }
 
