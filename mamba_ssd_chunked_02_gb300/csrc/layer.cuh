@@ -77,21 +77,12 @@ __device__ __forceinline__ float softplus(float v) {
     return fmaf(p, e, v > 0.f ? v : 0.f);
 }
 
-// The same for a pair.
+// The same for a pair: two scalar chains, whose constants are immediates (packed, each
+// constant takes a register pair that is set anew where registers are short).
 __device__ __forceinline__ f2 softplus2(f2 v) {
     float a, b;
     unpack2(v, a, b);
-    const f2 e = ex2_2(mul2(pack2(fabsf(a), fabsf(b)), dup2(-kLog2e)));
-    f2 p = dup2(0.005253457929939032f);
-    p = fma2(p, e, dup2(-0.02958850748836994f));
-    p = fma2(p, e, dup2(0.07836166769266129f));
-    p = fma2(p, e, dup2(-0.13674770295619965f));
-    p = fma2(p, e, dup2(0.19111430644989014f));
-    p = fma2(p, e, dup2(-0.24844369292259216f));
-    p = fma2(p, e, dup2(0.33319270610809326f));
-    p = fma2(p, e, dup2(-0.49999502301216125f));
-    p = fma2(p, e, dup2(1.f));
-    return fma2(p, e, pack2(a > 0.f ? a : 0.f, b > 0.f ? b : 0.f));
+    return pack2(softplus(a), softplus(b));
 }
 
 // V elements of type TI moved as one access (V * sizeof(TI) is 2, 4, 8 or 16 bytes).
@@ -213,8 +204,8 @@ __device__ __forceinline__ typename Pack<TI, V>::Raw from_pairs(const f2 (&v)[(V
 }
 __device__ __forceinline__ f2 sigmoid2(f2 v) {
     float a, b;
-    unpack2(add2(ex2_2(mul2(v, dup2(-kLog2e))), dup2(1.f)), a, b);
-    return pack2(rcp(a), rcp(b));
+    unpack2(v, a, b);
+    return pack2(sigmoid(a), sigmoid(b));
 }
 
 template <typename TI, int V>

@@ -55,13 +55,14 @@ scan_local_kernel(const BwdP p) {
     using K = Cfg<N>;
     constexpr int NT = K::NT, LPC = K::LPC, CB = K::CB, TT = K::TT;
     constexpr int PR = CB / V, RS = NT / PR, IT = TT / RS;
-    constexpr int BI = TT * N / V / NT;
+    constexpr int BI = TT * N / V / NT, VB = V * (int)sizeof(TI);
     static_assert(TT % kL == 0, "whole stored states");
     extern __shared__ __align__(16) unsigned char smem[];
     float2* sP = reinterpret_cast<float2*>(smem);                         // [TT][CB] (d, dx)
     float* sB = reinterpret_cast<float*>(smem + (size_t)TT * CB * 8);     // [TT][N]
     float* sC = sB + TT * N;                                              // [TT][N]
     float* sY = sC + TT * N;                                              // [TT][CB] dY
+    TI* sS = reinterpret_cast<TI*>(sY + TT * CB);                         // staged: x, dt, dy, z [TT][CB], B, C [TT][N]
     typedef typename Pack<TI, V>::Raw Raw;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -76,12 +77,17 @@ scan_local_kernel(const BwdP p) {
     const int lc = (tid % PR) * V, r0 = tid / PR;
     const bool con = cb * CB + lc < p.Dg;
     const int64_t c = (int64_t)g * p.Dg + cb * CB + lc;
-    const TI* xp = static_cast<const TI*>(p.x) + (int64_t)b * p.sx.b + c;
-    const TI* dp = static_cast<const TI*>(p.dt) + (int64_t)b * p.sdt.b + c;
-    const TI* zp = static_cast<const TI*>(p.z) + (int64_t)b * p.sz.b + c;
-    const TI* yp = static_cast<const TI*>(p.dy) + (int64_t)b * p.sy.b + c;
-    const TI* Bp = static_cast<const TI*>(p.B) + (int64_t)b * p.sB.b + (int64_t)g * N;
-    const TI* Cp = static_cast<const TI*>(p.C) + (int64_t)b * p.sC.b + (int64_t)g * N;
+    // pointers to this thread's first row of the tile to load next, and the steps to its others
+    const int64_t tr = s0 + r0;
+    const TI* xp = static_cast<const TI*>(p.x) + (int64_t)b * p.sx.b + tr * p.sx.t + c;
+    const TI* dp = static_cast<const TI*>(p.dt) + (int64_t)b * p.sdt.b + tr * p.sdt.t + c;
+    const TI* zp = static_cast<const TI*>(p.z) + (int64_t)b * p.sz.b + tr * p.sz.t + c;
+    const TI* yp = static_cast<const TI*>(p.dy) + (int64_t)b * p.sy.b + tr * p.sy.t + c;
+    constexpr int BR = NT * V / N;     // rows of B between a thread's accesses
+    static_assert(BR * N == NT * V, "B tile shape");
+    const int br = tid * V / N;
+    const TI* Bp = static_cast<const TI*>(p.B) + (int64_t)b * p.sB.b + (s0 + br) * p.sB.t + g * N + tid * V % N;
+    const TI* Cp = static_cast<const TI*>(p.C) + (int64_t)b * p.sC.b + (s0 + br) * p.sC.t + g * N + tid * V % N;
     float bias[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) bias[j] = p.bias && con ? __ldg(p.bias + c + j) : 0.f;
@@ -105,38 +111,44 @@ scan_local_kernel(const BwdP p) {
     float* ck = p.ck + ((int64_t)b * p.nck * p.Dch + cg) * N + q * kNS;
     float* ckd = p.ck_d + (int64_t)b * p.nck * p.Dch + cg;
 
-    Raw rx[IT], rd[IT], rz[IT], ry[IT], rB[BI], rC[BI];
-    auto load = [&](int t0) {
+    const int own = r0 * CB + lc;   // this thread's first element of a staged tile
+    auto stage = [&](int t0) {      // tile after tile
+        const int lim = sn - t0;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int t = t0 + r0 + i * RS;
-            rx[i] = rd[i] = rz[i] = ry[i] = zero_raw<Raw>();
-            if (con && t < sn) {
-                rx[i] = load_raw<TI, V>(xp + (int64_t)t * p.sx.t);
-                rd[i] = load_raw<TI, V>(dp + (int64_t)t * p.sdt.t);
-                if (ADJ && p.z) rz[i] = load_raw<TI, V>(zp + (int64_t)t * p.sz.t);
-                if (ADJ) ry[i] = load_raw<TI, V>(yp + (int64_t)t * p.sy.t);
-            }
+            const bool real = con && r0 + i * RS < lim;
+            TI* d = sS + own + i * RS * CB;
+            stage_copy<VB>(d, real ? xp + i * (RS * p.sx.t) : p.x, real);
+            stage_copy<VB>(d + TT * CB, real ? dp + i * (RS * p.sdt.t) : p.x, real);
+            if (ADJ) stage_copy<VB>(d + 2 * TT * CB, real ? yp + i * (RS * p.sy.t) : p.x, real);
+            if (ADJ && p.z) stage_copy<VB>(d + 3 * TT * CB, real ? zp + i * (RS * p.sz.t) : p.x, real);
         }
 #pragma unroll
         for (int i = 0; i < BI; ++i) {
-            const int e = (tid + i * NT) * V, t = t0 + e / N;
-            rB[i] = rC[i] = zero_raw<Raw>();
-            if (t < sn) {
-                rB[i] = load_raw<TI, V>(Bp + (int64_t)t * p.sB.t + e % N);
-                if (ADJ) rC[i] = load_raw<TI, V>(Cp + (int64_t)t * p.sC.t + e % N);
-            }
+            const bool real = br + i * BR < lim;
+            TI* d = sS + 4 * TT * CB + (tid + i * NT) * V;
+            stage_copy<VB>(d, real ? Bp + i * (BR * p.sB.t) : p.x, real);
+            if (ADJ) stage_copy<VB>(d + TT * N, real ? Cp + i * (BR * p.sC.t) : p.x, real);
         }
+        stage_commit();
+        xp += TT * p.sx.t;
+        dp += TT * p.sdt.t;
+        zp += TT * p.sz.t;
+        yp += TT * p.sy.t;
+        Bp += TT * p.sB.t;
+        Cp += TT * p.sC.t;
     };
-    load(s0);
+    stage(s0);
     for (int t0 = s0; t0 < s1; t0 += TT) {
+        stage_wait();
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int r = r0 + i * RS;
             const bool real = con && t0 + r < sn;
+            const TI* st = sS + own + i * RS * CB;
             f2 fx[1], fd[1], fz[1], fy[1];
-            to_pairs<TI, V>(rx[i], fx);
-            to_pairs<TI, V>(rd[i], fd);
+            to_pairs<TI, V>(*reinterpret_cast<const Raw*>(st), fx);
+            to_pairs<TI, V>(*reinterpret_cast<const Raw*>(st + TT * CB), fd);
             f2 d = add2(fd[0], pack2(bias[0], bias[V - 1]));
             if (p.softplus) d = softplus2(d);
             if (!real) d = dup2(0.f);
@@ -148,31 +160,34 @@ scan_local_kernel(const BwdP p) {
             else
                 sP[r * CB + lc] = make_float2(d0, u0);
             if (ADJ) {
-                to_pairs<TI, V>(ry[i], fy);
+                to_pairs<TI, V>(*reinterpret_cast<const Raw*>(st + 2 * TT * CB), fy);
                 if (p.z) {
-                    to_pairs<TI, V>(rz[i], fz);
+                    to_pairs<TI, V>(*reinterpret_cast<const Raw*>(st + 3 * TT * CB), fz);
                     fy[0] = mul2(fy[0], mul2(fz[0], sigmoid2(fz[0])));
                 }
                 unpack2(fy[0], u0, u1);
-                sY[r * CB + lc] = u0;
-                if (V == 2) sY[r * CB + lc + 1] = u1;
+                if constexpr (V == 2)
+                    *reinterpret_cast<float2*>(sY + r * CB + lc) = make_float2(u0, u1);
+                else
+                    sY[r * CB + lc] = u0;
             }
         }
 #pragma unroll
         for (int i = 0; i < BI; ++i) {
             const int e = (tid + i * NT) * V;
+            const TI* st = sS + 4 * TT * CB + e;
             float f[V];
-            Conv<TI, V>::to(rB[i], f);
+            Conv<TI, V>::to(*reinterpret_cast<const Raw*>(st), f);
 #pragma unroll
             for (int j = 0; j < V; ++j) sB[e + j] = f[j];
             if (ADJ) {
-                Conv<TI, V>::to(rC[i], f);
+                Conv<TI, V>::to(*reinterpret_cast<const Raw*>(st + TT * N), f);
 #pragma unroll
                 for (int j = 0; j < V; ++j) sC[e + j] = f[j];
             }
         }
         __syncthreads();
-        if (t0 + TT < s1) load(t0 + TT);
+        if (t0 + TT < s1) stage(t0 + TT);
         const float4* pP = reinterpret_cast<const float4*>(sP + ch);
         const float2* pY = reinterpret_cast<const float2*>(sY + ch);
 #pragma unroll 1
@@ -245,14 +260,24 @@ scan_join2_kernel(float* __restrict__ seg_h, float* __restrict__ seg_g, const fl
     const float a = __ldg(A + i % DN) * kLog2e;
     const int64_t bd = i / N, nbd = total / N;
     float h = init ? init[i] : 0.f, g = dfinal ? dfinal[i] : 0.f;
-    for (int s = 0; s < nseg; ++s) {
-        const int r = nseg - 1 - s;
-        const float hl = seg_h[s * total + i], gl = seg_g[r * total + i];
-        const float hd = seg_d[s * nbd + bd], gd = seg_d[r * nbd + bd];
-        seg_h[s * total + i] = h;
-        seg_g[r * total + i] = g;
-        h = fmaf(ex2(a * hd), h, hl);
-        g = fmaf(ex2(a * gd), g, gl);
+    for (int s0 = 0; s0 < nseg; s0 += 4) {   // four stretches' loads in flight
+        float hl[4], gl[4], hd[4], gd[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (s0 + k < nseg) {
+                const int s = s0 + k, r = nseg - 1 - s;
+                hl[k] = seg_h[s * total + i], gl[k] = seg_g[r * total + i];
+                hd[k] = seg_d[s * nbd + bd], gd[k] = seg_d[r * nbd + bd];
+            }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (s0 + k < nseg) {
+                const int s = s0 + k, r = nseg - 1 - s;
+                seg_h[s * total + i] = h;
+                seg_g[r * total + i] = g;
+                h = fmaf(ex2(a * hd[k]), h, hl[k]);
+                g = fmaf(ex2(a * gd[k]), g, gl[k]);
+            }
     }
 }
 
@@ -286,21 +311,6 @@ template <typename TI, int N> struct GCfg {
     static constexpr size_t smem = (size_t)kL * CB * 12 + 3 * (size_t)kL * QP * 4 + 2 * (size_t)kL * N * 4 +
                                    (size_t)WARPS * 2 * kL * N * 4 + 4 * lane16 + stage;
 };
-
-// BYTES from global to shared memory without registers, zeros when !real.  Two bytes
-// (one bf16) are too few for an asynchronous copy.
-template <int BYTES> __device__ __forceinline__ void stage_copy(void* dst, const void* src, bool real) {
-    if constexpr (BYTES >= 4) {
-        const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(BYTES),
-                     "r"(real ? BYTES : 0)
-                     : "memory");
-    } else {
-        *static_cast<unsigned short*>(dst) = real ? *static_cast<const unsigned short*>(src) : 0;
-    }
-}
-__device__ __forceinline__ void stage_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void stage_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 // (3) Gradients.  Block: CB channels of one group, one stretch of one sequence.  What a
 // thread stages for the tile before (inputs, stored states) only it reads, so the copies
@@ -735,7 +745,7 @@ template <typename TI, int N, int V>
 cudaError_t bwd_v(const BwdP& p, int64_t lncb, const float* init, const float* dfinal, cudaStream_t st) {
     using L = Cfg<N>;
     const bool adj = p.nseg > 1;
-    const size_t ls = (size_t)L::TT * (L::CB * 12 + 2 * N * 4);
+    const size_t ls = (size_t)L::TT * (L::CB * (12 + 4 * sizeof(TI)) + 2 * N * (4 + sizeof(TI)));
     const int64_t lb = p.b * p.nseg * p.G * lncb, gb = p.b * p.nseg * p.G * p.ncb;
     const int64_t total = p.b * p.Dch * N;
     if (lb >= (int64_t(1) << 31) || gb >= (int64_t(1) << 31) || (total + 255) / 256 >= (int64_t(1) << 31))

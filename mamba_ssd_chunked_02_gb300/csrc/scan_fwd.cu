@@ -38,12 +38,15 @@ scan_fwd_kernel(const FwdP p) {
     constexpr int NT = K::NT, LPC = K::LPC, CB = K::CB, TT = K::TT, U = K::U, UT = K::UT, YP = K::YP;
     constexpr int PR = CB / V, RS = NT / PR, IT = TT / RS;        // threads a row, rows a pass, passes
     constexpr int BI = TT * N / V / NT;                            // accesses of B (and of C) a thread
+    constexpr int VB = V * (int)sizeof(TI);
     static_assert(IT >= 1 && RS * IT == TT && BI >= 1, "tile shape");
     extern __shared__ __align__(16) unsigned char smem[];
     float2* sP = reinterpret_cast<float2*>(smem);                               // [TT][CB] (d, dx)
     float* sB = reinterpret_cast<float*>(smem + (size_t)TT * CB * 8);           // [TT][N]
     float* sC = sB + TT * N;
     float* sY = sC + TT * N;                                                    // [TT][YP]
+    constexpr int ST = 3 * TT * CB + 2 * TT * N;                                // elements of a staged tile
+    TI* sS = reinterpret_cast<TI*>(sY + TT * YP);                               // [2] x, dt, z [TT][CB], B, C [TT][N]
     typedef typename Pack<TI, V>::Raw Raw;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -60,12 +63,17 @@ scan_fwd_kernel(const FwdP p) {
     const int lc = (tid % PR) * V, r0 = tid / PR;
     const bool con = cb * CB + lc < p.Dg;
     const int64_t c = (int64_t)g * p.Dg + cb * CB + lc;
-    const TI* xp = static_cast<const TI*>(p.x) + (int64_t)b * p.sx.b + c;
-    const TI* dp = static_cast<const TI*>(p.dt) + (int64_t)b * p.sdt.b + c;
-    const TI* zp = static_cast<const TI*>(p.z) + (int64_t)b * p.sz.b + c;
-    TI* yp = static_cast<TI*>(p.y) + (int64_t)b * p.sy.b + c;
-    const TI* Bp = static_cast<const TI*>(p.B) + (int64_t)b * p.sB.b + (int64_t)g * N;
-    const TI* Cp = static_cast<const TI*>(p.C) + (int64_t)b * p.sC.b + (int64_t)g * N;
+    // pointers to this thread's first row of the tile to load next, and the steps to its others
+    const int64_t tr = s0 + r0;
+    const TI* xp = static_cast<const TI*>(p.x) + (int64_t)b * p.sx.b + tr * p.sx.t + c;
+    const TI* dp = static_cast<const TI*>(p.dt) + (int64_t)b * p.sdt.b + tr * p.sdt.t + c;
+    const TI* zp = static_cast<const TI*>(p.z) + (int64_t)b * p.sz.b + tr * p.sz.t + c;
+    TI* yp = static_cast<TI*>(p.y) + (int64_t)b * p.sy.b + tr * p.sy.t + c;
+    constexpr int BR = NT * V / N;     // rows of B between a thread's accesses
+    static_assert(BR * N == NT * V, "B tile shape");
+    const int br = tid * V / N;
+    const TI* Bp = static_cast<const TI*>(p.B) + (int64_t)b * p.sB.b + (s0 + br) * p.sB.t + g * N + tid * V % N;
+    const TI* Cp = static_cast<const TI*>(p.C) + (int64_t)b * p.sC.b + (s0 + br) * p.sC.t + g * N + tid * V % N;
     float bias[V], skip[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -94,49 +102,53 @@ scan_fwd_kernel(const FwdP p) {
     }
     float dsum[2] = {0.f, 0.f};
 
-    Raw rx[IT], rd[IT], rz[IT], rB[BI], rC[BI];
-    auto load = [&](int t0) {
+    // What a thread stages for the next tile only it reads: the copies need no barrier and no
+    // registers, and run under the scan of the tile at hand.
+    const int own = r0 * CB + lc;   // this thread's first element of a staged tile
+    auto stage = [&](int t0, TI* buf) {   // tile after tile
+        const int lim = sn - t0;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int t = t0 + r0 + i * RS;
-            rx[i] = rd[i] = rz[i] = zero_raw<Raw>();
-            if (con && t < sn) {
-                rx[i] = load_raw<TI, V>(xp + (int64_t)t * p.sx.t);
-                rd[i] = load_raw<TI, V>(dp + (int64_t)t * p.sdt.t);
-                if (!STATES && p.z) rz[i] = load_raw<TI, V>(zp + (int64_t)t * p.sz.t);
-            }
+            const bool real = con && r0 + i * RS < lim;
+            TI* d = buf + own + i * RS * CB;
+            stage_copy<VB>(d, real ? xp + i * (RS * p.sx.t) : p.x, real);
+            stage_copy<VB>(d + TT * CB, real ? dp + i * (RS * p.sdt.t) : p.x, real);
+            if (!STATES && p.z) stage_copy<VB>(d + 2 * TT * CB, real ? zp + i * (RS * p.sz.t) : p.x, real);
         }
 #pragma unroll
         for (int i = 0; i < BI; ++i) {
-            const int e = (tid + i * NT) * V, t = t0 + e / N;
-            rB[i] = rC[i] = zero_raw<Raw>();
-            if (t < sn) {
-                rB[i] = load_raw<TI, V>(Bp + (int64_t)t * p.sB.t + e % N);
-                if (!STATES) rC[i] = load_raw<TI, V>(Cp + (int64_t)t * p.sC.t + e % N);
-            }
+            const bool real = br + i * BR < lim;
+            TI* d = buf + 3 * TT * CB + (tid + i * NT) * V;
+            stage_copy<VB>(d, real ? Bp + i * (BR * p.sB.t) : p.x, real);
+            if (!STATES) stage_copy<VB>(d + TT * N, real ? Cp + i * (BR * p.sC.t) : p.x, real);
         }
+        stage_commit();
+        xp += TT * p.sx.t;
+        dp += TT * p.sdt.t;
+        zp += TT * p.sz.t;
+        Bp += TT * p.sB.t;
+        Cp += TT * p.sC.t;
     };
-    load(s0);
+    TI *cur = sS, *nxt = sS + ST;
+    stage(s0, cur);
     for (int t0 = s0; t0 < s1; t0 += TT) {
         if (t0 >= n) {   // padding only
             if (!STATES && con)
 #pragma unroll
-                for (int i = 0; i < IT; ++i) {
-                    const int t = t0 + r0 + i * RS;
-                    if (t < s1) store_raw<TI, V>(yp + (int64_t)t * p.sy.t, zero_raw<Raw>());
-                }
+                for (int i = 0; i < IT; ++i)
+                    if (t0 + r0 + i * RS < s1) store_raw<TI, V>(yp + i * (RS * p.sy.t), zero_raw<Raw>());
+            yp += TT * p.sy.t;
             continue;
         }
-        Raw kx[IT], kz[IT];   // kept for the epilogue while the next tile loads
+        stage_wait();
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            kx[i] = rx[i];
-            kz[i] = rz[i];
             const int r = r0 + i * RS;
             const bool real = con && t0 + r < sn;
+            const TI* st = cur + own + i * RS * CB;
             f2 fx[1], fd[1];
-            to_pairs<TI, V>(rx[i], fx);
-            to_pairs<TI, V>(rd[i], fd);
+            to_pairs<TI, V>(*reinterpret_cast<const Raw*>(st), fx);
+            to_pairs<TI, V>(*reinterpret_cast<const Raw*>(st + TT * CB), fd);
             f2 d = add2(fd[0], pack2(bias[0], bias[V - 1]));
             if (p.softplus) d = softplus2(d);
             if (!real) d = dup2(0.f);
@@ -151,18 +163,19 @@ scan_fwd_kernel(const FwdP p) {
 #pragma unroll
         for (int i = 0; i < BI; ++i) {
             const int e = (tid + i * NT) * V;
+            const TI* st = cur + 3 * TT * CB + e;
             float f[V];
-            Conv<TI, V>::to(rB[i], f);
+            Conv<TI, V>::to(*reinterpret_cast<const Raw*>(st), f);
 #pragma unroll
             for (int j = 0; j < V; ++j) sB[e + j] = f[j];
             if (!STATES) {
-                Conv<TI, V>::to(rC[i], f);
+                Conv<TI, V>::to(*reinterpret_cast<const Raw*>(st + TT * N), f);
 #pragma unroll
                 for (int j = 0; j < V; ++j) sC[e + j] = f[j];
             }
         }
         __syncthreads();
-        if (t0 + TT < s1) load(t0 + TT);
+        if (t0 + TT < s1) stage(t0 + TT, nxt);
         const float4* pP = reinterpret_cast<const float4*>(sP + ch);
         const float* pB = sB + q * kNS;
         const float* pC = sC + q * kNS;
@@ -203,7 +216,8 @@ scan_fwd_kernel(const FwdP p) {
             for (int i = 0; i < IT; ++i) {
                 const int r = r0 + i * RS, t = t0 + r;
                 f2 fx[1], o[1];
-                to_pairs<TI, V>(kx[i], fx);
+                const TI* st = cur + own + i * RS * CB;
+                to_pairs<TI, V>(*reinterpret_cast<const Raw*>(st), fx);
                 if constexpr (V == 2) {
                     const float2 yv = *reinterpret_cast<const float2*>(sY + r * YP + lc);
                     o[0] = pack2(yv.x, yv.y);
@@ -213,13 +227,17 @@ scan_fwd_kernel(const FwdP p) {
                 o[0] = fma2(pack2(skip[0], skip[V - 1]), fx[0], o[0]);
                 if (p.z) {
                     f2 fz[1];
-                    to_pairs<TI, V>(kz[i], fz);
+                    to_pairs<TI, V>(*reinterpret_cast<const Raw*>(st + 2 * TT * CB), fz);
                     o[0] = mul2(o[0], mul2(fz[0], sigmoid2(fz[0])));
                 }
                 if (t >= n) o[0] = dup2(0.f);
-                if (t < s1) store_raw<TI, V>(yp + (int64_t)t * p.sy.t, from_pairs<TI, V>(o));
+                if (t < s1) store_raw<TI, V>(yp + i * (RS * p.sy.t), from_pairs<TI, V>(o));
             }
         }
+        yp += TT * p.sy.t;
+        TI* was = cur;
+        cur = nxt;
+        nxt = was;
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -251,10 +269,17 @@ scan_join_kernel(float* __restrict__ seg_h, const float* __restrict__ seg_d, con
     const float a = __ldg(A + i % DN) * kLog2e;
     float h = init ? init[i] : 0.f;
     const int64_t bd = i / N, nbd = total / N;
-    for (int s = 0; s < nseg; ++s) {
-        const float local = seg_h[s * total + i], d = seg_d[s * nbd + bd];
-        seg_h[s * total + i] = h;
-        h = fmaf(ex2(a * d), h, local);
+    for (int s0 = 0; s0 < nseg; s0 += 4) {   // four stretches' loads in flight
+        float local[4], d[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (s0 + k < nseg) local[k] = seg_h[(s0 + k) * total + i], d[k] = seg_d[(s0 + k) * nbd + bd];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (s0 + k < nseg) {
+                seg_h[(s0 + k) * total + i] = h;
+                h = fmaf(ex2(a * d[k]), h, local[k]);
+            }
     }
 }
 
@@ -334,22 +359,24 @@ template <typename TI, int N, int V>
 cudaError_t fwd_v(const FwdP& p, cudaStream_t st) {
     using K = Cfg<N>;
     const int64_t blocks = p.b * p.nseg * p.G * p.ncb;
+    constexpr size_t smem = (size_t)K::TT * (K::CB * 8 + 2 * N * 4 + K::YP * 4) +
+                            2 * (size_t)K::TT * (3 * K::CB + 2 * N) * sizeof(TI);
     if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     auto k = scan_fwd_kernel<TI, N, V, false>;
     auto s = scan_fwd_kernel<TI, N, V, true>;
-    if (K::smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::smem);
+    if (smem > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(s, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::smem);
+            e = cudaFuncSetAttribute(s, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
     if (p.nseg > 1) {
-        s<<<(unsigned)blocks, K::NT, K::smem, st>>>(p);
+        s<<<(unsigned)blocks, K::NT, smem, st>>>(p);
         const int64_t total = p.b * p.Dch * N;
         scan_join_kernel<<<(unsigned)((total + 255) / 256), 256, 0, st>>>(p.seg_h, p.seg_d, p.A, p.init, total,
                                                                          (int64_t)p.Dch * N, N, p.nseg);
     }
-    k<<<(unsigned)blocks, K::NT, K::smem, st>>>(p);
+    k<<<(unsigned)blocks, K::NT, smem, st>>>(p);
     return cudaGetLastError();
 }
 
