@@ -25,13 +25,27 @@ __device__ __forceinline__ void load_w(const float* w, const float* bias, int64_
 #pragma unroll
     for (int i = 0; i < (V + 1) / 2; ++i) {
         const int64_t lo = c + 2 * i, hi = V == 1 ? lo : lo + 1;
+        if (W == 4 && V > 1) {   // one 16-byte access a channel (the launcher checked w's alignment)
+            const float4 a = __ldg(reinterpret_cast<const float4*>(w) + lo);
+            const float4 b = __ldg(reinterpret_cast<const float4*>(w) + hi);
+            wk[0][i] = pack2(a.x, b.x);
+            wk[1][i] = pack2(a.y, b.y);
+            wk[2][i] = pack2(a.z, b.z);
+            wk[W - 1][i] = pack2(a.w, b.w);
+        } else {
 #pragma unroll
-        for (int k = 0; k < W; ++k) wk[k][i] = pack2(__ldg(w + lo * W + k), __ldg(w + hi * W + k));
+            for (int k = 0; k < W; ++k) wk[k][i] = pack2(__ldg(w + lo * W + k), __ldg(w + hi * W + k));
+        }
         bi[i] = bias ? pack2(__ldg(bias + lo), __ldg(bias + hi)) : dup2(0.f);
     }
 }
 
-constexpr int kFwdThreads = 128;
+constexpr int kFwdThreads = 64;
+// Groups of four tokens in a thread's ring; none where an element is too small for an
+// asynchronous copy (single bf16 values).
+template <typename TI, int V> constexpr int ring() {
+    return V * sizeof(TI) < 4 ? 0 : V * sizeof(TI) > 8 ? 3 : 4;
+}
 
 // Block: one stretch of TS tokens of one sequence, kFwdThreads * V channels.
 template <typename TI, int V, int W, bool SILU>
@@ -89,23 +103,43 @@ conv_fwd_kernel(const TI* __restrict__ x, const float* __restrict__ w,
         }
         store_raw<TI, V>(yb + (int64_t)t * sy.t, from_pairs<TI, V>(o));
     };
-    // Whole groups of U tokens, the next group's loads in flight under this one's work.
-    constexpr int U = 8;
+    // Whole groups of U tokens pass through a ring in shared memory, in which each thread
+    // reads only what it copied: kRing - 1 groups in flight, without registers.
+    constexpr int NB = ring<TI, V>(), U = NB ? 4 : 8;
     int t = t0;
-    if (t + U <= tn) {
-        Raw r[U];
+    if constexpr (NB > 0) {
+        extern __shared__ __align__(16) unsigned char smem[];
+        Raw* mine = reinterpret_cast<Raw*>(smem) + threadIdx.x;
+        const int groups = max(tn - t0, 0) / U;
+        const TI* src = xb + (int64_t)t0 * sx.t;
+        auto copy = [&](int g) {
+            if (g < groups) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) r[u] = load_raw<TI, V>(xb + (int64_t)(t + u) * sx.t);
-        for (; t + U <= tn; t += U) {
-            Raw nx[U];
-            const bool more = t + 2 * U <= tn;
+                for (int u = 0; u < U; ++u) {
+                    stage_copy<V * (int)sizeof(TI)>(mine + ((g % NB) * U + u) * kFwdThreads, src, true);
+                    src += sx.t;
+                }
+            }
+            stage_commit();
+        };
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (more) nx[u] = load_raw<TI, V>(xb + (int64_t)(t + U + u) * sx.t);
+        for (int g = 0; g < NB - 1; ++g) copy(g);
+        for (int g = 0; g < groups; ++g, t += U) {
+            stage_wait<NB - 2>();
+            Raw r[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) r[u] = mine[((g % NB) * U + u) * kFwdThreads];
+            copy(g + NB - 1);   // into the group read in the round before
 #pragma unroll
             for (int u = 0; u < U; ++u) one(r[u], t + u);
+        }
+    } else {
+        for (; t + U <= tn; t += U) {
+            Raw r[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) r[u] = nx[u];
+            for (int u = 0; u < U; ++u) r[u] = load_raw<TI, V>(xb + (int64_t)(t + u) * sx.t);
+#pragma unroll
+            for (int u = 0; u < U; ++u) one(r[u], t + u);
         }
     }
     for (; t < tn; ++t) one(load_raw<TI, V>(xb + (int64_t)t * sx.t), t);
@@ -152,7 +186,7 @@ conv_step_kernel(TI* __restrict__ state, const TI* __restrict__ x, const float* 
 // with windows of x and ds in registers; at t it finishes dx[t - (W - 1)], which
 // for the first stretch includes the gradients of the initial window.  The kBwdTY
 // stretches of a block are summed in shared memory into one slot of dw and dbias.
-constexpr int kBwdTX = 32, kBwdTY = 8;
+constexpr int kBwdTX = 32, kBwdTY = 4;
 
 template <typename TI, int V, int W, bool SILU>
 __global__ void __launch_bounds__(kBwdTX * kBwdTY)
@@ -161,7 +195,12 @@ conv_bwd_kernel(const TI* __restrict__ x, const float* __restrict__ w,
                 const TI* __restrict__ dy, const TI* __restrict__ dfin,
                 const int32_t* __restrict__ lengths, TI* __restrict__ dx, TI* __restrict__ dinit,
                 float* __restrict__ part, int T, int D, int TS, int nblk, int ncb, Tok sx, Tok sdy) {
-    __shared__ float red[kBwdTY][kBwdTX * V * (W + 1)];
+    typedef typename Pack<TI, V>::Raw Raw;
+    // the ring, and after it in the same place the sums
+    extern __shared__ __align__(16) unsigned char smem[];
+    Raw* mine = reinterpret_cast<Raw*>(smem) + threadIdx.y * kBwdTX + threadIdx.x;
+    constexpr int RW = kBwdTX * V * (W + 1);
+    float* red = reinterpret_cast<float*>(smem);   // [kBwdTY][RW]
     const int cb = blockIdx.x % ncb, slot = blockIdx.x / ncb;
     const int tb = slot % nblk, b = slot / nblk;
     const int c = (cb * kBwdTX + threadIdx.x) * V;
@@ -197,7 +236,6 @@ conv_bwd_kernel(const TI* __restrict__ x, const float* __restrict__ w,
                 }
             }
         }
-        typedef typename Pack<TI, V>::Raw Raw;
         // Token t: its ds, its part of dw, and the finished dx[t - (W-1)] in o.  ANY: t may
         // be padding or past the stretch.
         auto one = [&](const bool ANY, Raw rx, Raw rd, int t, f2 (&o)[H]) {
@@ -234,63 +272,99 @@ conv_bwd_kernel(const TI* __restrict__ x, const float* __restrict__ w,
                 o[i] = a;
             }
         };
-        auto slow = [&](int t) {
-            Raw rx = zero_raw<Raw>(), rd = rx;
-            if (t < n) {
-                rx = load_raw<TI, V>(xb + (int64_t)t * sx.t);
-                rd = load_raw<TI, V>(db + (int64_t)t * sdy.t);
-            }
-            f2 o[H];
-            one(true, rx, rd, t, o);
-            const int tp = t - (W - 1);
-            if (tp < t0 && !first) return;
-            if (dfin && tp < n && tp >= n - (W - 1)) {
-                f2 f[H];
-                load_2<TI, V>(dfin + wrow + (int64_t)(tp - (n - (W - 1))) * D, f);
-#pragma unroll
-                for (int i = 0; i < H; ++i) o[i] = add2(o[i], f[i]);
-            }
-            if (tp >= 0) store_raw<TI, V>(ob + (int64_t)tp * D, from_pairs<TI, V>(o));
-            else if (dinit) store_raw<TI, V>(dinit + wrow + (int64_t)(tp + W - 1) * D, from_pairs<TI, V>(o));
-        };
-        constexpr int U = 4;
+        // Up to W - 1 tokens from t, before te, that may be anything; their loads together.
         const int te = t1 + W - 1, tf = min(t1, n);
-        int t = t0;
-        for (; t < min(t0 + W - 1, te); ++t) slow(t);
-        // Whole groups of U real tokens of this stretch (dfinal only reaches tokens finished
-        // at or after n), the next group's loads in flight under this one's work.
-        if (t + U <= tf) {
-            Raw rx[U], rd[U];
+        auto slow = [&](int t, int end) {
+            Raw rx[W - 1], rd[W - 1];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                rx[u] = load_raw<TI, V>(xb + (int64_t)(t + u) * sx.t);
-                rd[u] = load_raw<TI, V>(db + (int64_t)(t + u) * sdy.t);
+            for (int u = 0; u < W - 1; ++u) {
+                rx[u] = rd[u] = zero_raw<Raw>();
+                if (t + u < min(end, n)) {
+                    rx[u] = load_raw<TI, V>(xb + (int64_t)(t + u) * sx.t);
+                    rd[u] = load_raw<TI, V>(db + (int64_t)(t + u) * sdy.t);
+                }
             }
-            for (; t + U <= tf; t += U) {
-                Raw nx[U], nd[U];
-                const bool more = t + 2 * U <= tf;
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (more) {
-                        nx[u] = load_raw<TI, V>(xb + (int64_t)(t + U + u) * sx.t);
-                        nd[u] = load_raw<TI, V>(db + (int64_t)(t + U + u) * sdy.t);
+            for (int u = 0; u < W - 1; ++u) {
+                if (t + u >= end) break;
+                f2 o[H];
+                one(true, rx[u], rd[u], t + u, o);
+                const int tp = t + u - (W - 1);
+                if (tp < t0 && !first) continue;
+                if (dfin && tp < n && tp >= n - (W - 1)) {
+                    f2 f[H];
+                    load_2<TI, V>(dfin + wrow + (int64_t)(tp - (n - (W - 1))) * D, f);
+#pragma unroll
+                    for (int i = 0; i < H; ++i) o[i] = add2(o[i], f[i]);
+                }
+                if (tp >= 0) store_raw<TI, V>(ob + (int64_t)tp * D, from_pairs<TI, V>(o));
+                else if (dinit)
+                    store_raw<TI, V>(dinit + wrow + (int64_t)(tp + W - 1) * D, from_pairs<TI, V>(o));
+            }
+        };
+        constexpr int NB = ring<TI, V>(), U = NB ? 4 : 8;
+        int t = min(t0 + W - 1, te);
+        slow(t0, t);
+        // Whole groups of U real tokens of this stretch (dfinal only reaches tokens finished
+        // at or after n), through a ring as in the forward.
+        if constexpr (NB > 0) {
+            const int groups = max(tf - t, 0) / U;
+            const TI* srcx = xb + (int64_t)t * sx.t;
+            const TI* srcd = db + (int64_t)t * sdy.t;
+            TI* dst = ob + (int64_t)(t - (W - 1)) * D;
+            auto copy = [&](int g) {
+                if (g < groups) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        Raw* at = mine + ((g % NB) * U + u) * (2 * kBwdTX * kBwdTY);
+                        stage_copy<V * (int)sizeof(TI)>(at, srcx, true);
+                        stage_copy<V * (int)sizeof(TI)>(at + kBwdTX * kBwdTY, srcd, true);
+                        srcx += sx.t;
+                        srcd += sdy.t;
                     }
+                }
+                stage_commit();
+            };
+#pragma unroll
+            for (int g = 0; g < NB - 1; ++g) copy(g);
+            for (int g = 0; g < groups; ++g, t += U) {
+                stage_wait<NB - 2>();
+                Raw rx[U], rd[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const Raw* at = mine + ((g % NB) * U + u) * (2 * kBwdTX * kBwdTY);
+                    rx[u] = at[0];
+                    rd[u] = at[kBwdTX * kBwdTY];
+                }
+                copy(g + NB - 1);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    f2 o[H];
+                    one(false, rx[u], rd[u], t + u, o);
+                    store_raw<TI, V>(dst, from_pairs<TI, V>(o));
+                    dst += D;
+                }
+            }
+        } else {
+            for (; t + U <= tf; t += U) {
+                Raw rx[U], rd[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    rx[u] = load_raw<TI, V>(xb + (int64_t)(t + u) * sx.t);
+                    rd[u] = load_raw<TI, V>(db + (int64_t)(t + u) * sdy.t);
+                }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     f2 o[H];
                     one(false, rx[u], rd[u], t + u, o);
                     store_raw<TI, V>(ob + (int64_t)(t + u - (W - 1)) * D, from_pairs<TI, V>(o));
                 }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    rx[u] = nx[u];
-                    rd[u] = nd[u];
-                }
             }
         }
-        for (; t < te; ++t) slow(t);
+        for (; t < te; t += W - 1) slow(t, te);
     }
-    float* mr = red[threadIdx.y] + threadIdx.x;
+    __syncthreads();   // every thread is through with its ring
+    float* mr = red + threadIdx.y * RW + threadIdx.x;
 #pragma unroll
     for (int i = 0; i < H; ++i)
 #pragma unroll
@@ -302,32 +376,43 @@ conv_bwd_kernel(const TI* __restrict__ x, const float* __restrict__ w,
         }
     __syncthreads();
     const int tid = threadIdx.y * kBwdTX + threadIdx.x;
-    for (int i = tid; i < kBwdTX * V * (W + 1); i += kBwdTX * kBwdTY) {
+    for (int i = tid; i < RW; i += kBwdTX * kBwdTY) {
         const int cx = i % kBwdTX, jk = i / kBwdTX, j = jk / (W + 1), k = jk % (W + 1);
         const int64_t ch = (int64_t)(cb * kBwdTX + cx) * V + j;
         if (ch >= D) continue;
         float a = 0.f;
 #pragma unroll
-        for (int q = 0; q < kBwdTY; ++q) a += red[q][i];
+        for (int q = 0; q < kBwdTY; ++q) a += red[q * RW + i];
         float* row = part + (int64_t)slot * D * (W + 1);
         if (k < W) row[ch * W + k] = a;
         else row[(int64_t)D * W + ch] = a;
     }
 }
 
-// Stretch lengths: long ones amortise the W - 1 tokens of overlap (and, backward,
-// the slots of dw), short ones fill the GPU when there are few rows.
-int pick_ts(int64_t rows_of_threads, int64_t T, int64_t want) {
-    for (int ts : {64, 32, 16}) {
-        if (rows_of_threads * ((T + ts - 1) / ts) >= want) return ts;
+// Stretch lengths: long ones amortise the start (weights, the tokens of overlap and,
+// backward, the slots of dw); short ones fill the GPU when there are few rows, and spread
+// the blocks evenly over it.  Picks the best share of time spent on whole tokens: `lanes`
+// threads a token row, `start` tokens' worth of start, `resident` threads an SM.
+int pick_ts(int64_t lanes, int64_t T, int start, int resident) {
+    const double room = (double)sm_count() * resident;
+    int best = 8;
+    double top = 0.;
+    for (int ts = 8; ts <= 256; ts *= 2) {
+        const double waves = (double)lanes * (double)((T + ts - 1) / ts) / room;
+        const double used = waves < 1. ? waves : waves / (double)(int64_t)(waves + 0.999);
+        const double share = used * ts / (ts + start);
+        if (share > top * 1.01) {
+            top = share;
+            best = ts;
+        }
     }
-    return 8;
+    return best;
 }
 
-int bwd_vec(const ConvArgs& a) { return a.D % 4 == 0 ? 4 : 1; }
+int bwd_vec(const ConvArgs& a) { return a.D % 4 == 0 ? 4 : a.dtype == 1 && a.D % 2 == 0 ? 2 : 1; }
 int bwd_ts(const ConvArgs& a) {
     const int64_t lanes = (a.D + bwd_vec(a) - 1) / bwd_vec(a);
-    return pick_ts(a.b * lanes, a.T, (int64_t)sm_count() * 512);
+    return pick_ts(a.b * lanes, a.T, 40, 512);
 }
 int64_t bwd_blocks(const ConvArgs& a) {
     const int64_t per = (int64_t)bwd_ts(a) * kBwdTY;
@@ -338,11 +423,13 @@ template <typename TI, int V, int W>
 cudaError_t fwd_w(const ConvArgs& a, const TI* x, const float* w, const float* bias, const TI* init,
                   const int32_t* lengths, TI* y, TI* fin, cudaStream_t st) {
     const int64_t lanes = (a.D + V - 1) / V, ncb = (lanes + kFwdThreads - 1) / kFwdThreads;
-    const int ts = pick_ts(a.b * lanes, a.T, (int64_t)sm_count() * 1024);
+    const int ts = pick_ts(a.b * lanes, a.T, 6, 768);
     const int64_t nseg = std::max<int64_t>(1, (a.T + ts - 1) / ts);
     if (a.b * nseg * ncb >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     auto k = a.silu ? conv_fwd_kernel<TI, V, W, true> : conv_fwd_kernel<TI, V, W, false>;
-    k<<<(unsigned)(a.b * nseg * ncb), kFwdThreads, 0, st>>>(
+    constexpr size_t smem = (size_t)ring<TI, V>() * 4 * kFwdThreads * V * sizeof(TI);
+    static_assert(smem <= 48 * 1024, "the default limit");
+    k<<<(unsigned)(a.b * nseg * ncb), kFwdThreads, smem, st>>>(
         x, w, bias, init, lengths, y, fin, (int)a.T, (int)a.D, ts, (int)nseg, (int)ncb, a.sx, a.sy);
     return cudaGetLastError();
 }
@@ -364,7 +451,13 @@ cudaError_t bwd_w(const ConvArgs& a, const TI* x, const float* w, const float* b
     const int64_t ncb = ((a.D + V - 1) / V + kBwdTX - 1) / kBwdTX, nblk = bwd_blocks(a);
     if (a.b * nblk * ncb >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     auto k = a.silu ? conv_bwd_kernel<TI, V, W, true> : conv_bwd_kernel<TI, V, W, false>;
-    k<<<(unsigned)(a.b * nblk * ncb), dim3(kBwdTX, kBwdTY), 0, st>>>(
+    constexpr size_t rings = (size_t)ring<TI, V>() * 4 * 2 * kBwdTX * kBwdTY * V * sizeof(TI);
+    constexpr size_t sums = (size_t)kBwdTY * kBwdTX * V * (W + 1) * sizeof(float), smem = rings > sums ? rings : sums;
+    if (smem > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    k<<<(unsigned)(a.b * nblk * ncb), dim3(kBwdTX, kBwdTY), smem, st>>>(
         x, w, bias, init, dy, dfin, lengths, dx, dinit, part, (int)a.T, (int)a.D, bwd_ts(a), (int)nblk,
         (int)ncb, a.sx, a.sy);
     return cudaGetLastError();
@@ -400,11 +493,11 @@ cudaError_t bwd_v(const ConvArgs& a, const void* x, const float* w, const float*
 }
 
 // Every access of the call is whole and aligned at V elements a piece.
-bool wide(const ConvArgs& a, int64_t V, const void* x, const void* y, const void* s0, const void* s1,
-          const void* o) {
+bool wide(const ConvArgs& a, int64_t V, const float* w, const void* x, const void* y, const void* s0,
+          const void* s1, const void* o) {
     const int64_t es = a.dtype == 1 ? 2 : 4, bytes = V * es;
     const Tok row{0, a.D};
-    return a.D % V == 0 && vec_ok(x, a.sx, bytes, es) && vec_ok(y, a.sy, bytes, es) &&
+    return a.D % V == 0 && (a.W != 4 || reinterpret_cast<uintptr_t>(w) % 16 == 0) && vec_ok(x, a.sx, bytes, es) && vec_ok(y, a.sy, bytes, es) &&
            vec_ok(s0, row, bytes, es) && vec_ok(s1, row, bytes, es) && vec_ok(o, row, bytes, es);
 }
 
@@ -446,10 +539,12 @@ cudaError_t launch_conv_fwd(const ConvArgs& a, const void* x, const float* w, co
                             cudaStream_t st) {
     if (a.b == 0 || a.D == 0) return cudaSuccess;
     if (a.dtype == 1)
-        return wide(a, 4, x, y, init, fin, nullptr)
+        return wide(a, 4, w, x, y, init, fin, nullptr)
                    ? fwd_v<__nv_bfloat16, 4>(a, x, w, bias, init, lengths, y, fin, st)
+               : wide(a, 2, w, x, y, init, fin, nullptr)
+                   ? fwd_v<__nv_bfloat16, 2>(a, x, w, bias, init, lengths, y, fin, st)
                    : fwd_v<__nv_bfloat16, 1>(a, x, w, bias, init, lengths, y, fin, st);
-    return wide(a, 4, x, y, init, fin, nullptr)
+    return wide(a, 4, w, x, y, init, fin, nullptr)
                ? fwd_v<float, 4>(a, x, w, bias, init, lengths, y, fin, st)
                : fwd_v<float, 1>(a, x, w, bias, init, lengths, y, fin, st);
 }
@@ -458,7 +553,7 @@ cudaError_t launch_conv_step(const ConvArgs& a, void* state, const void* x, cons
                              const float* bias, void* y, cudaStream_t st) {
     if (a.b == 0 || a.D == 0) return cudaSuccess;
     if (a.dtype == 1)
-        return wide(a, 2, x, y, state, nullptr, nullptr)
+        return wide(a, 2, w, x, y, state, nullptr, nullptr)
                    ? step_v<__nv_bfloat16, 2>(a, state, x, w, bias, y, st)
                    : step_v<__nv_bfloat16, 1>(a, state, x, w, bias, y, st);
     return step_v<float, 1>(a, state, x, w, bias, y, st);
@@ -474,10 +569,14 @@ cudaError_t launch_conv_bwd(const ConvArgs& a, const void* x, const float* w, co
     cudaError_t e = cudaSuccess;
     if (a.b > 0) {
         // dfin and dinit are rows of D like the initial window
-        const bool v4 = wide(a, 4, x, dy, init, dfin, dinit) &&
-                        wide(a, 4, x, dy, dx, nullptr, nullptr);
+        auto fits = [&](int64_t V) {
+            return wide(a, V, w, x, dy, init, dfin, dinit) && wide(a, V, w, x, dy, dx, nullptr, nullptr);
+        };
+        const bool v4 = fits(4);
         if (a.dtype == 1)
             e = v4 ? bwd_v<__nv_bfloat16, 4>(a, x, w, bias, init, dy, dfin, lengths, dx, dinit, part, st)
+                : fits(2)
+                   ? bwd_v<__nv_bfloat16, 2>(a, x, w, bias, init, dy, dfin, lengths, dx, dinit, part, st)
                    : bwd_v<__nv_bfloat16, 1>(a, x, w, bias, init, dy, dfin, lengths, dx, dinit, part, st);
         else
             e = v4 ? bwd_v<float, 4>(a, x, w, bias, init, dy, dfin, lengths, dx, dinit, part, st)

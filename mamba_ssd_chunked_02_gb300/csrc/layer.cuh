@@ -213,6 +213,24 @@ __device__ __forceinline__ void store_raw(TI* p, typename Pack<TI, V>::Raw r) {
     *reinterpret_cast<typename Pack<TI, V>::Raw*>(p) = r;
 }
 
+// BYTES from global to shared memory without registers, zeros when !real.  Two bytes
+// (one bf16) are too few for an asynchronous copy.
+template <int BYTES> __device__ __forceinline__ void stage_copy(void* dst, const void* src, bool real) {
+    if constexpr (BYTES >= 4) {
+        const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(BYTES),
+                     "r"(real ? BYTES : 0)
+                     : "memory");
+    } else {
+        *static_cast<unsigned short*>(dst) = real ? *static_cast<const unsigned short*>(src) : 0;
+    }
+}
+__device__ __forceinline__ void stage_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most PENDING of this thread's committed groups are in flight.
+template <int PENDING = 0> __device__ __forceinline__ void stage_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
 // Host: true when every access of V elements at base + i * strides + k * V is aligned.
 inline bool vec_ok(const void* p, const Tok& s, int64_t bytes, int64_t esize) {
     return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (s.b * esize) % bytes == 0 &&

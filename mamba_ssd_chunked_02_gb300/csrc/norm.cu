@@ -48,32 +48,23 @@ __device__ __forceinline__ float2 team_sum(float a, float b, float2* red) {
 
 enum { kNone = 0, kFirst = 1, kAfter = 2 };
 
-// V weights from w (ones when null), 16 bytes at a time where V allows (w is then
-// 16-byte aligned: scalar loads of 8 neighbouring weights a lane cost four times
-// the load unit's time).
-template <int V> __device__ __forceinline__ void load_weights(const float* w, float (&o)[V]) {
+// V weights from w (ones when null) as pairs, 16 bytes at a time where V allows (w is
+// then 16-byte aligned: scalar loads of 8 neighbouring weights a lane cost four times the
+// load unit's time).
+template <int V> __device__ __forceinline__ void load_weights(const float* w, f2 (&o)[(V + 1) / 2]) {
     if (!w) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) o[j] = 1.f;
+        for (int i = 0; i < (V + 1) / 2; ++i) o[i] = dup2(1.f);
     } else if constexpr (V == 1) {
-        o[0] = __ldg(w);
+        o[0] = pack2(__ldg(w), 0.f);
     } else {
 #pragma unroll
-        for (int j = 0; j < V; j += 4) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(w + j));
-            o[j] = v.x;
-            o[j + 1] = v.y;
-            o[j + 2] = v.z;
-            o[j + 3] = v.w;
+        for (int i = 0; i < V / 2; i += 2) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(w + 2 * i));
+            o[i] = pack2(v.x, v.y);
+            o[i + 1] = pack2(v.z, v.w);
         }
     }
-}
-
-// silu(z) and its derivative.
-__device__ __forceinline__ void silu_d(float z, float& s, float& d) {
-    const float sg = sigmoid(z);
-    s = z * sg;
-    d = sg * fmaf(z, 1.f - sg, 1.f);
 }
 
 constexpr int kWarpTeams = 4;   // warps a block when a team is a warp
@@ -96,67 +87,77 @@ norm_fwd_kernel(const TI* __restrict__ x, const float* __restrict__ w, const TI*
     const float* wr = w ? w + (int64_t)g * q.S : nullptr;
     const int nv = q.S / V;
     typedef typename Pack<TI, V>::Raw Raw;
-    constexpr int K = VPT > 0 ? VPT : 1;
-    Raw rx[K], rz[K];
-    float ss = 0.f;
-    auto square = [&](Raw vx, Raw vz) {
-        float fx[V], fz[V];
-        Conv<TI, V>::to(vx, fx);
-        if (GATE == kFirst) Conv<TI, V>::to(vz, fz);
+    constexpr int K = VPT > 0 ? VPT : 1, H = (V + 1) / 2;
+    f2 ss = dup2(0.f);
+    // v = x or x silu(z), kept in fp32 for the result; the gate that comes after waits as raw z
+    auto value = [&](Raw vx, Raw vz, f2 (&v)[H]) {
+        to_pairs<TI, V>(vx, v);
+        if (GATE == kFirst) {
+            f2 fz[H];
+            to_pairs<TI, V>(vz, fz);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float v = GATE == kFirst ? fx[j] * fz[j] * sigmoid(fz[j]) : fx[j];
-            ss = fmaf(v, v, ss);
+            for (int i = 0; i < H; ++i) v[i] = mul2(v[i], mul2(fz[i], sigmoid2(fz[i])));
         }
     };
-    auto result = [&](int i, Raw vx, Raw vz, float r) {
-        float fx[V], fz[V], o[V], fw[V];
-        Conv<TI, V>::to(vx, fx);
-        if (GATE != kNone) Conv<TI, V>::to(vz, fz);
-        load_weights<V>(wr ? wr + i * V : nullptr, fw);
+    auto square = [&](const f2 (&v)[H]) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float v = fx[j] * r;
-            if (GATE != kNone) v *= fz[j] * sigmoid(fz[j]);
-            o[j] = v * fw[j];
-        }
-        store_raw<TI, V>(yr + i * V, Conv<TI, V>::from(o));
+        for (int i = 0; i < H; ++i) ss = fma2(v[i], v[i], ss);
     };
-    if (VPT > 0) {
+    auto result = [&](int at, f2 (&v)[H], Raw vz, f2 r) {
+        f2 fw[H];
+        load_weights<V>(wr ? wr + at * V : nullptr, fw);
+#pragma unroll
+        for (int i = 0; i < H; ++i) v[i] = mul2(mul2(v[i], r), fw[i]);
+        if (GATE == kAfter) {
+            f2 fz[H];
+            to_pairs<TI, V>(vz, fz);
+#pragma unroll
+            for (int i = 0; i < H; ++i) v[i] = mul2(v[i], mul2(fz[i], sigmoid2(fz[i])));
+        }
+        store_raw<TI, V>(yr + at * V, from_pairs<TI, V>(v));
+    };
+    const auto scale = [&] { return dup2(rsqrtf(team_sum<WARP>(sum2(ss), 0.f, red).x / (float)q.S + q.eps)); };
+    if constexpr (VPT > 0) {
+        Raw rx[K], rz[K];
+        f2 v[K][H];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int i = tid + k * nt;
-            rx[k] = rz[k] = zero_raw<Raw>();
+            rx[k] = rz[k] = zero_raw<Raw>();   // absent vectors are zeros
             if (i < nv) {
                 rx[k] = load_raw<TI, V>(xr + i * V);
                 if (GATE != kNone) rz[k] = load_raw<TI, V>(zr + i * V);
             }
         }
 #pragma unroll
-        for (int k = 0; k < K; ++k) square(rx[k], rz[k]);   // absent vectors are zeros
-    } else {
-        for (int i = tid; i < nv; i += nt)
-            square(load_raw<TI, V>(xr + i * V),
-                   GATE == kFirst ? load_raw<TI, V>(zr + i * V) : zero_raw<Raw>());
-    }
-    const float r = rsqrtf(team_sum<WARP>(ss, 0.f, red).x / (float)q.S + q.eps);
-    if (VPT > 0) {
-#pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int i = tid + k * nt;
-            if (i < nv) result(i, rx[k], rz[k], r);
+            value(rx[k], rz[k], v[k]);
+            square(v[k]);
         }
+        const f2 r = scale();
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (tid + k * nt < nv) result(tid + k * nt, v[k], rz[k], r);
     } else {
-        for (int i = tid; i < nv; i += nt)
-            result(i, load_raw<TI, V>(xr + i * V),
-                   GATE != kNone ? load_raw<TI, V>(zr + i * V) : zero_raw<Raw>(), r);
+        f2 v[H];
+        const auto zraw = [&](int i) { return GATE != kNone ? load_raw<TI, V>(zr + i * V) : zero_raw<Raw>(); };
+        for (int i = tid; i < nv; i += nt) {
+            value(load_raw<TI, V>(xr + i * V), zraw(i), v);
+            square(v);
+        }
+        const f2 r = scale();
+        for (int i = tid; i < nv; i += nt) {
+            const Raw z0 = zraw(i);
+            value(load_raw<TI, V>(xr + i * V), z0, v);
+            result(i, v, z0, r);
+        }
     }
 }
 
 // Team `team` of `teams` (a multiple of G) has group team % G and tokens team / G,
 // + teams / G, ...; its dw goes to slot team / G of part ([slots][D]).
 template <typename TI, int V, int VPT, int GATE, bool WARP>
-__global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : 1024)
+__global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : 1024, WARP ? 4 : 1)
 norm_bwd_kernel(const TI* __restrict__ x, const float* __restrict__ w, const TI* __restrict__ z,
                 const TI* __restrict__ dy, TI* __restrict__ dx, TI* __restrict__ dz,
                 float* __restrict__ part, int teams, Rows q) {
@@ -170,16 +171,41 @@ norm_bwd_kernel(const TI* __restrict__ x, const float* __restrict__ w, const TI*
     const float* wr = w ? w + (int64_t)g * q.S : nullptr;
     float* pr = part ? part + slot * D + (int64_t)g * q.S : nullptr;
     typedef typename Pack<TI, V>::Raw Raw;
-    constexpr int K = VPT > 0 ? VPT : 1;
-    Raw rx[K], rz[K], rd[K];
-    float acc[K][V];
+    constexpr int K = VPT > 0 ? VPT : 1, H = (V + 1) / 2;
+    f2 acc[K][H];
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[k][j] = 0.f;
+        for (int i = 0; i < H; ++i) acc[k][i] = dup2(0.f);
     int parity = 0;
     bool begun = false;   // VPT = 0: the slot holds a sum already
     const float inv = 1.f / (float)q.S;
+    const f2 one = dup2(1.f), minus = dup2(-1.f);
+    // The next token's row is copied into the other half of a thread's own room in shared
+    // memory while this one is summed and applied.
+    constexpr bool STAGE = VPT > 0 && V > 1;
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int bt = blockDim.x;
+    Raw* st = reinterpret_cast<Raw*>(smem) + threadIdx.x;   // [2][K][3 tensors][threads]
+    Raw own[1][STAGE ? 1 : K][3];
+    int half = 0;
+    auto copy = [&](int64_t row, int to) {
+        const int64_t b = row / q.T, t = row - b * q.T;
+        const TI* xr = x + b * q.sx.b + t * q.sx.t + (int64_t)g * q.S;
+        const TI* zr = z + b * q.sz.b + t * q.sz.t + (int64_t)g * q.S;
+        const TI* dr = dy + b * q.sy.b + t * q.sy.t + (int64_t)g * q.S;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (tid + k * nt < nv) {
+                const int at = (tid + k * nt) * V;
+                Raw* d = st + (to * K + k) * 3 * bt;
+                stage_copy<V * (int)sizeof(TI)>(d, xr + at, true);
+                if (GATE != kNone) stage_copy<V * (int)sizeof(TI)>(d + bt, zr + at, true);
+                stage_copy<V * (int)sizeof(TI)>(d + 2 * bt, dr + at, true);
+            }
+        stage_commit();
+    };
+    if (STAGE && slot < q.rows) copy(slot, 0);
     for (int64_t row = slot; row < q.rows; row += nslot) {
         const int64_t b = row / q.T, t = row - b * q.T;
         const TI* xr = x + b * q.sx.b + t * q.sx.t + (int64_t)g * q.S;
@@ -187,91 +213,124 @@ norm_bwd_kernel(const TI* __restrict__ x, const float* __restrict__ w, const TI*
         const TI* dr = dy + b * q.sy.b + t * q.sy.t + (int64_t)g * q.S;
         TI* ox = dx + row * D + (int64_t)g * q.S;
         TI* oz = dz + row * D + (int64_t)g * q.S;
-        float ss = 0.f, qv = 0.f;
-        auto sums = [&](int i, Raw vx, Raw vz, Raw vd) {
-            float fx[V], fz[V], fd[V], fw[V];
-            Conv<TI, V>::to(vx, fx);
-            if (GATE != kNone) Conv<TI, V>::to(vz, fz);
-            Conv<TI, V>::to(vd, fd);
-            load_weights<V>(wr ? wr + i * V : nullptr, fw);
+        f2 ss = dup2(0.f), qv = dup2(0.f);
+        // sg = sigmoid(z), kept for the result
+        auto sums = [&](int at, Raw vx, Raw vz, Raw vd, f2 (&sg)[H]) {
+            f2 v[H], fz[H], d[H], fw[H];
+            to_pairs<TI, V>(vx, v);
+            to_pairs<TI, V>(vd, d);
+            load_weights<V>(wr ? wr + at * V : nullptr, fw);
+            if (GATE != kNone) to_pairs<TI, V>(vz, fz);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float gate = GATE != kNone ? fz[j] * sigmoid(fz[j]) : 1.f;
-                const float v = GATE == kFirst ? fx[j] * gate : fx[j];
-                float d = fd[j] * fw[j];
-                if (GATE == kAfter) d *= gate;
-                ss = fmaf(v, v, ss);
-                qv = fmaf(d, v, qv);
-            }
-        };
-        // dx, dz; returns this token's part of dw in p
-        auto result = [&](int i, Raw vx, Raw vz, Raw vd, float r, float m, float* p) {
-            float fx[V], fz[V], fd[V], ax[V], az[V], fw[V];
-            Conv<TI, V>::to(vx, fx);
-            if (GATE != kNone) Conv<TI, V>::to(vz, fz);
-            Conv<TI, V>::to(vd, fd);
-            load_weights<V>(wr ? wr + i * V : nullptr, fw);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float gate = 1.f, slope = 0.f;
-                if (GATE != kNone) silu_d(fz[j], gate, slope);
-                const float v = GATE == kFirst ? fx[j] * gate : fx[j];
-                const float wj = fw[j];
-                const float n = v * r;
-                const float d = GATE == kAfter ? fd[j] * gate : fd[j];
-                const float dv = fmaf(r, d * wj, -v * m);
-                p[j] = d * n;
-                ax[j] = GATE == kFirst ? dv * gate : dv;
-                az[j] = GATE == kFirst ? dv * fx[j] * slope : fd[j] * n * wj * slope;
-            }
-            store_raw<TI, V>(ox + i * V, Conv<TI, V>::from(ax));
-            if (GATE != kNone) store_raw<TI, V>(oz + i * V, Conv<TI, V>::from(az));
-        };
-        if (VPT > 0) {
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int i = tid + k * nt;
-                rx[k] = rz[k] = rd[k] = zero_raw<Raw>();
-                if (i < nv) {
-                    rx[k] = load_raw<TI, V>(xr + i * V);
-                    if (GATE != kNone) rz[k] = load_raw<TI, V>(zr + i * V);
-                    rd[k] = load_raw<TI, V>(dr + i * V);
+            for (int i = 0; i < H; ++i) {
+                d[i] = mul2(d[i], fw[i]);
+                if (GATE != kNone) {
+                    sg[i] = sigmoid2(fz[i]);
+                    const f2 gate = mul2(fz[i], sg[i]);
+                    if (GATE == kFirst) v[i] = mul2(v[i], gate);
+                    else d[i] = mul2(d[i], gate);
                 }
+                ss = fma2(v[i], v[i], ss);
+                qv = fma2(d[i], v[i], qv);
             }
+        };
+        // dx, dz; adds this token's part of dw to p
+        auto result = [&](int at, Raw vx, Raw vz, Raw vd, const f2 (&sg)[H], f2 r, f2 m, f2 (&p)[H]) {
+            f2 fx[H], fz[H], d[H], fw[H], ax[H], az[H];
+            to_pairs<TI, V>(vx, fx);
+            to_pairs<TI, V>(vd, d);
+            load_weights<V>(wr ? wr + at * V : nullptr, fw);
+            if (GATE != kNone) to_pairs<TI, V>(vz, fz);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                f2 v = fx[i], gate = one, slope = one;
+                if (GATE != kNone) {   // slope = silu'(z) = sg + z sg (1 - sg)
+                    gate = mul2(fz[i], sg[i]);
+                    slope = fma2(gate, fma2(sg[i], minus, one), sg[i]);
+                }
+                if (GATE == kFirst) v = mul2(v, gate);
+                const f2 n = mul2(v, r);
+                if (GATE == kAfter) az[i] = mul2(mul2(d[i], n), mul2(fw[i], slope));
+                if (GATE == kAfter) d[i] = mul2(d[i], gate);
+                const f2 dv = fma2(r, mul2(d[i], fw[i]), mul2(v, m));   // m < 0: see below
+                p[i] = fma2(d[i], n, p[i]);
+                ax[i] = GATE == kFirst ? mul2(dv, gate) : dv;
+                if (GATE == kFirst) az[i] = mul2(mul2(dv, fx[i]), slope);
+            }
+            store_raw<TI, V>(ox + at * V, from_pairs<TI, V>(ax));
+            if (GATE != kNone) store_raw<TI, V>(oz + at * V, from_pairs<TI, V>(az));
+        };
+        f2 r2, m2;
+        auto scales = [&] {
+            // two halves of red in turn: the next token's sums do not overwrite one being read
+            const float2 s = team_sum<WARP>(sum2(ss), sum2(qv), red[parity]);
+            parity ^= 1;
+            const float r = rsqrtf(s.x * inv + q.eps);
+            r2 = dup2(r);
+            m2 = dup2(-r * r * r * (s.y * inv));   // dv = r q - v r^3 mean(q v)
+        };
+        if constexpr (VPT > 0) {
+            f2 sg[K][H];
+            Raw rx, rz, rd;
+            if (STAGE) {
+                stage_wait();
+            } else {
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (tid + k * nt < nv) {
+                        const int at = (tid + k * nt) * V;
+                        own[0][k][0] = load_raw<TI, V>(xr + at);
+                        if (GATE != kNone) own[0][k][1] = load_raw<TI, V>(zr + at);
+                        own[0][k][2] = load_raw<TI, V>(dr + at);
+                    }
+            }
+            auto get = [&](int k, int w) {
+                if constexpr (STAGE) return st[((half * K + k) * 3 + w) * bt];
+                else return own[0][k][w];
+            };
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (tid + k * nt < nv) sums(tid + k * nt, rx[k], rz[k], rd[k]);
-        } else {
-            for (int i = tid; i < nv; i += nt)
-                sums(i, load_raw<TI, V>(xr + i * V),
-                     GATE != kNone ? load_raw<TI, V>(zr + i * V) : zero_raw<Raw>(),
-                     load_raw<TI, V>(dr + i * V));
-        }
-        // two halves of red in turn: the next token's sums do not overwrite one being read
-        const float2 s = team_sum<WARP>(ss, qv, red[parity]);
-        parity ^= 1;
-        const float r = rsqrtf(s.x * inv + q.eps);
-        const float m = r * r * r * (s.y * inv);
-        if (VPT > 0) {
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int i = tid + k * nt;
-                float p[V];
-                if (i < nv) {
-                    result(i, rx[k], rz[k], rd[k], r, m, p);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) acc[k][j] += p[j];
+                if (tid + k * nt < nv) {
+                    rz = zero_raw<Raw>();
+                    if (GATE != kNone) rz = get(k, 1);
+                    sums(tid + k * nt, get(k, 0), rz, get(k, 2), sg[k]);
                 }
-            }
+            if (STAGE && row + nslot < q.rows) copy(row + nslot, half ^ 1);
+            scales();
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (tid + k * nt < nv) {
+                    rx = get(k, 0);
+                    rd = get(k, 2);
+                    rz = zero_raw<Raw>();
+                    if (GATE != kNone) rz = get(k, 1);
+                    result(tid + k * nt, rx, rz, rd, sg[k], r2, m2, acc[k]);
+                }
+            half ^= 1;
         } else {
+            f2 sg[H];
+            const auto zraw = [&](int i) { return GATE != kNone ? load_raw<TI, V>(zr + i * V) : zero_raw<Raw>(); };
+            for (int i = tid; i < nv; i += nt)
+                sums(i, load_raw<TI, V>(xr + i * V), zraw(i), load_raw<TI, V>(dr + i * V), sg);
+            scales();
             for (int i = tid; i < nv; i += nt) {
-                float p[V];
-                result(i, load_raw<TI, V>(xr + i * V),
-                       GATE != kNone ? load_raw<TI, V>(zr + i * V) : zero_raw<Raw>(),
-                       load_raw<TI, V>(dr + i * V), r, m, p);
+                const Raw z0 = zraw(i);
+                f2 p[H], fz[H];
+                to_pairs<TI, V>(z0, fz);
+#pragma unroll
+                for (int j = 0; j < H; ++j) {
+                    p[j] = dup2(0.f);
+                    sg[j] = sigmoid2(fz[j]);
+                }
+                result(i, load_raw<TI, V>(xr + i * V), z0, load_raw<TI, V>(dr + i * V), sg, r2, m2, p);
                 if (pr)
 #pragma unroll
-                    for (int j = 0; j < V; ++j) pr[i * V + j] = begun ? pr[i * V + j] + p[j] : p[j];
+                    for (int j = 0; j < V; ++j) {
+                        float lo, hi;
+                        unpack2(p[j / 2], lo, hi);
+                        const float add = j & 1 ? hi : lo;
+                        pr[i * V + j] = begun ? pr[i * V + j] + add : add;
+                    }
             }
             begun = true;
         }
@@ -280,15 +339,13 @@ norm_bwd_kernel(const TI* __restrict__ x, const float* __restrict__ w, const TI*
     if (VPT > 0) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int i = tid + k * nt;
-            if (i < nv) {
-                if constexpr (V == 1) {
-                    pr[i] = acc[k][0];
-                } else {
+            const int at = tid + k * nt;
+            if (at < nv) {
 #pragma unroll
-                    for (int j = 0; j < V; j += 4)
-                        *reinterpret_cast<float4*>(pr + i * V + j) =
-                            make_float4(acc[k][j], acc[k][j + 1], acc[k][j + 2], acc[k][j + 3]);
+                for (int j = 0; j < V; ++j) {
+                    float lo, hi;
+                    unpack2(acc[k][j / 2], lo, hi);
+                    pr[at * V + j] = j & 1 ? hi : lo;
                 }
             }
         }
@@ -306,11 +363,13 @@ int team_threads(int64_t nv, int vpt) {
     return (int)std::min<int64_t>(1024, std::max<int64_t>(1, (nv + vpt * 32 - 1) / (vpt * 32)) * 32);
 }
 
-// Backward teams: enough to fill the GPU (1024 threads an SM), at most one per
-// token of each group, a multiple of G; the warp teams are the bound for slots.
+// Backward slots of dw: as many teams as an SM holds at once (16 warps, or blocks of 1024
+// threads in all), each with an equal share of the tokens, over the groups.
 int64_t bwd_team_slots(const NormArgs& a) {
-    const int64_t teams = (int64_t)sm_count() * 16;
-    return std::max<int64_t>(1, std::min<int64_t>(a.b * a.T, (teams + a.G - 1) / a.G));
+    const int64_t S = a.D / a.G, full = a.dtype == 1 ? 8 : 4, V = S % full ? 1 : full, nv = S / V;
+    const int64_t per_sm = nv <= 96 ? 16 : std::max<int64_t>(1, 1024 / team_threads(nv, nv <= 1024 ? 1 : 2));
+    const int64_t teams = (int64_t)sm_count() * per_sm;
+    return std::max<int64_t>(1, std::min<int64_t>(a.b * a.T, teams / a.G));
 }
 
 template <typename TI, int V, int GATE>
@@ -338,11 +397,23 @@ cudaError_t bwd_go(const NormArgs& a, const TI* x, const float* w, const TI* z, 
     const int teams = (int)teams64;
     const unsigned wb = (unsigned)((teams64 + kWarpTeams - 1) / kWarpTeams);
     const unsigned bb = (unsigned)teams;
-    if (nv <= 32) norm_bwd_kernel<TI, V, 1, GATE, true><<<wb, kWarpTeams * 32, 0, st>>>(x, w, z, dy, dx, dz, part, teams, q);
-    else if (nv <= 96) norm_bwd_kernel<TI, V, 3, GATE, true><<<wb, kWarpTeams * 32, 0, st>>>(x, w, z, dy, dx, dz, part, teams, q);
-    else if (nv <= 1024) norm_bwd_kernel<TI, V, 1, GATE, false><<<bb, team_threads(nv, 1), 0, st>>>(x, w, z, dy, dx, dz, part, teams, q);
-    else if (nv <= 2048) norm_bwd_kernel<TI, V, 2, GATE, false><<<bb, team_threads(nv, 2), 0, st>>>(x, w, z, dy, dx, dz, part, teams, q);
-    else norm_bwd_kernel<TI, V, 0, GATE, false><<<bb, 1024, 0, st>>>(x, w, z, dy, dx, dz, part, teams, q);
+    // [2 halves][vectors a thread][3 tensors] of 16 bytes a thread: 12 to 96 KB a block
+    auto go = [&](auto k, unsigned blocks, int threads, int vpt) {
+        const size_t smem = V > 1 ? (size_t)2 * vpt * 3 * 16 * threads : 0;
+        if (smem > 48 * 1024) {
+            cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+        }
+        k<<<blocks, threads, smem, st>>>(x, w, z, dy, dx, dz, part, teams, q);
+        return cudaSuccess;
+    };
+    cudaError_t e;
+    if (nv <= 32) e = go(norm_bwd_kernel<TI, V, 1, GATE, true>, wb, kWarpTeams * 32, 1);
+    else if (nv <= 96) e = go(norm_bwd_kernel<TI, V, 3, GATE, true>, wb, kWarpTeams * 32, 3);
+    else if (nv <= 1024) e = go(norm_bwd_kernel<TI, V, 1, GATE, false>, bb, team_threads(nv, 1), 1);
+    else if (nv <= 2048) e = go(norm_bwd_kernel<TI, V, 2, GATE, false>, bb, team_threads(nv, 2), 2);
+    else e = go(norm_bwd_kernel<TI, V, 0, GATE, false>, bb, 1024, 0);
+    if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
 

@@ -24,21 +24,6 @@ template <int N> struct Cfg {
     static constexpr int YP = CB + 2 * CPW;               // pitch of the y tile (bank-conflict free)
 };
 
-// BYTES from global to shared memory without registers, zeros when !real.  Two bytes
-// (one bf16) are too few for an asynchronous copy.
-template <int BYTES> __device__ __forceinline__ void stage_copy(void* dst, const void* src, bool real) {
-    if constexpr (BYTES >= 4) {
-        const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(BYTES),
-                     "r"(real ? BYTES : 0)
-                     : "memory");
-    } else {
-        *static_cast<unsigned short*>(dst) = real ? *static_cast<const unsigned short*>(src) : 0;
-    }
-}
-__device__ __forceinline__ void stage_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void stage_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
-
 // Blocks an SM the registers are kept to: nine (96 registers) where the tile's registers
 // are few, else what does not spill.
 template <typename TI, int N, int V> constexpr int min_blocks() {
