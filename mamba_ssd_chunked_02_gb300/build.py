@@ -5,6 +5,10 @@
 Each .cu file under csrc/ is compiled by nvcc in parallel into _build/, then
 linked (static CUDA runtime, no torch) into _lib/libmamba2_ssd.so.  Objects are
 rebuilt when their source or any header under csrc/ or include/ is newer.
+
+binding/layer_ext.cpp, the native Python binding of the layer operators, is
+compiled by g++ beside them against the installed torch's headers and linked to
+that library (_lib/layer_ext.so).
 """
 from __future__ import annotations
 
@@ -15,6 +19,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -23,6 +28,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libmamba2_ssd.so")
+EXT_SRC = os.path.join(PKG, "binding", "layer_ext.cpp")
+EXT = os.path.join(LIBDIR, "layer_ext.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -61,15 +68,51 @@ def _compile(src: str, force: bool, extra) -> str:
     return obj
 
 
+def _ext_object(force: bool) -> str:
+    """Compile the Python binding; the object depends on the torch it was built for."""
+    import torch
+    obj = os.path.join(BUILD, f"layer_ext-{torch.__version__}.o")
+    if not force and os.path.exists(obj) and os.path.getmtime(obj) >= max(os.path.getmtime(EXT_SRC), _newest_header()):
+        return obj
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    dirs = [inc, os.path.join(inc, "torch", "csrc", "api", "include"), cuda,
+            sysconfig.get_paths()["include"], INCLUDE]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += [f for d in dirs for f in ("-isystem", d)] + ["-c", EXT_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {os.path.basename(EXT_SRC)}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_ext(obj: str, force: bool) -> None:
+    if not force and os.path.exists(EXT) and os.path.getmtime(EXT) >= max(os.path.getmtime(obj), os.path.getmtime(LIB)):
+        return
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = EXT + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", LIBDIR, "-lmamba2_ssd", "-L", libs, "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
+
+
 def build(force: bool = False, jobs: int = 0, extra=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
     srcs = sources()
-    jobs = jobs or min(len(srcs), os.cpu_count() or 4)
+    jobs = jobs or min(len(srcs) + 1, os.cpu_count() or 4)
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        ext = ex.submit(_ext_object, force)
         objs = list(ex.map(lambda s: _compile(s, force, extra), srcs))
+        ext_obj = ext.result()
     if (not force and os.path.exists(LIB)
             and os.path.getmtime(LIB) >= max(os.path.getmtime(o) for o in objs)):
+        _link_ext(ext_obj, force)
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
@@ -77,6 +120,7 @@ def build(force: bool = False, jobs: int = 0, extra=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_ext(ext_obj, force)
     return LIB
 
 

@@ -329,18 +329,12 @@ conv_bwd_kernel(const TI* __restrict__ x, const float* __restrict__ w,
             for (int g = 0; g < NB - 1; ++g) copy(g);
             for (int g = 0; g < groups; ++g, t += U) {
                 stage_wait<NB - 2>();
-                Raw rx[U], rd[U];
+                copy(g + NB - 1);   // into the group read in the round before
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const Raw* at = mine + ((g % NB) * U + u) * (2 * kBwdTX * kBwdTY);
-                    rx[u] = at[0];
-                    rd[u] = at[kBwdTX * kBwdTY];
-                }
-                copy(g + NB - 1);
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
                     f2 o[H];
-                    one(false, rx[u], rd[u], t + u, o);
+                    one(false, at[0], at[kBwdTX * kBwdTY], t + u, o);
                     store_raw<TI, V>(dst, from_pairs<TI, V>(o));
                     dst += D;
                 }

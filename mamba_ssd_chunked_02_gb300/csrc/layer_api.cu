@@ -48,7 +48,7 @@ bool in_strides(const int64_t* s, int64_t T, int64_t width, Tok* out) {
 bool out_strides(const int64_t* s, int64_t b, int64_t T, int64_t width, Tok* out) {
     if (!in_strides(s, T, width, out)) return false;
     const int64_t sb = out->b, st = out->t;
-    if (b <= 1 && T <= 1) return true;
+    if (b == 0 || T == 0 || (b == 1 && T == 1)) return true;
     if (b <= 1) return st >= width;
     if (T <= 1) return sb >= width;
     return (st >= width && sb >= st * (T - 1) + width) || (sb >= width && st >= sb * (b - 1) + width);

@@ -75,12 +75,13 @@ __global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : 1024)
 norm_fwd_kernel(const TI* __restrict__ x, const float* __restrict__ w, const TI* __restrict__ z,
                 TI* __restrict__ y, Rows q) {
     __shared__ float2 red[32];
-    const int64_t id = WARP ? (int64_t)blockIdx.x * kWarpTeams + (threadIdx.x >> 5) : blockIdx.x;
+    // rows and row groups fit 32 bits (the launcher checks): a 64-bit division costs 100 instructions
+    const uint32_t id = WARP ? blockIdx.x * kWarpTeams + (threadIdx.x >> 5) : blockIdx.x;
     const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;
-    if (WARP && id >= q.rows * q.G) return;
-    const int64_t row = id / q.G;
+    if (WARP && id >= (uint32_t)q.rows * q.G) return;
+    const uint32_t row = id / q.G;
     const int g = (int)(id - row * q.G);
-    const int64_t b = row / q.T, t = row - b * q.T;
+    const int64_t b = row / (uint32_t)q.T, t = row - (uint32_t)b * q.T;
     const TI* xr = x + b * q.sx.b + t * q.sx.t + (int64_t)g * q.S;
     const TI* zr = z + b * q.sz.b + t * q.sz.t + (int64_t)g * q.S;
     TI* yr = y + b * q.sy.b + t * q.sy.t + (int64_t)g * q.S;
@@ -190,7 +191,7 @@ norm_bwd_kernel(const TI* __restrict__ x, const float* __restrict__ w, const TI*
     Raw own[1][STAGE ? 1 : K][3];
     int half = 0;
     auto copy = [&](int64_t row, int to) {
-        const int64_t b = row / q.T, t = row - b * q.T;
+        const int64_t b = (uint32_t)row / (uint32_t)q.T, t = row - b * q.T;
         const TI* xr = x + b * q.sx.b + t * q.sx.t + (int64_t)g * q.S;
         const TI* zr = z + b * q.sz.b + t * q.sz.t + (int64_t)g * q.S;
         const TI* dr = dy + b * q.sy.b + t * q.sy.t + (int64_t)g * q.S;
@@ -207,7 +208,7 @@ norm_bwd_kernel(const TI* __restrict__ x, const float* __restrict__ w, const TI*
     };
     if (STAGE && slot < q.rows) copy(slot, 0);
     for (int64_t row = slot; row < q.rows; row += nslot) {
-        const int64_t b = row / q.T, t = row - b * q.T;
+        const int64_t b = (uint32_t)row / (uint32_t)q.T, t = row - b * q.T;
         const TI* xr = x + b * q.sx.b + t * q.sx.t + (int64_t)g * q.S;
         const TI* zr = z + b * q.sz.b + t * q.sz.t + (int64_t)g * q.S;
         const TI* dr = dy + b * q.sy.b + t * q.sy.t + (int64_t)g * q.S;
@@ -393,7 +394,7 @@ cudaError_t bwd_go(const NormArgs& a, const TI* x, const float* w, const TI* z, 
     const Rows q = rows_of(a);
     const int64_t nv = q.S / V;
     const int64_t slots = bwd_team_slots(a), teams64 = slots * q.G;
-    if (teams64 >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    if (teams64 >= (int64_t(1) << 31) || q.rows >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     const int teams = (int)teams64;
     const unsigned wb = (unsigned)((teams64 + kWarpTeams - 1) / kWarpTeams);
     const unsigned bb = (unsigned)teams;
