@@ -109,8 +109,11 @@ typedef struct mamba2_scan_strides {
 /* x, dt [b,T,D] io, A [D,N], B, C [b,T,G,N] io, D [D] or NULL, z [b,T,D] io or
  * NULL, dt_bias [D] or NULL, initial_state [b,D,N] or NULL, lengths or NULL
  * -> y [b,T,D] io, final_state [b,D,N].  workspace: mamba2_scan_workspace_size(
- * shape) bytes (may be 0), 16-byte aligned: the states between the stretches of
- * tokens that run side by side when there are few rows. */
+ * shape) bytes (may be 0), 16-byte aligned, contents ignored on entry: with few rows
+ * the states between the stretches of tokens that run side by side; with more rows
+ * than the GPU holds at once, which then take turns in slices of the token axis, one
+ * word a row (a slice waits for the slice before it, at most two seconds: a wait that
+ * runs out sets MAMBA2_DEVERR_CHAIN_SCAN in the word of mamba2_ssd_device_error). */
 MAMBA2_API size_t mamba2_scan_workspace_size(const mamba2_scan_shape* shape);
 MAMBA2_API mamba2_status mamba2_scan_fwd(const mamba2_scan_shape* shape,
                                          const mamba2_scan_strides* strides,

@@ -337,6 +337,8 @@ MAMBA2_API mamba2_status mamba2_ssd_bwd(const mamba2_ssd_shape* shape,
                                                  for the previous chunk's state */
 #define MAMBA2_DEVERR_SELFTEST 16             /* mamba2_ssd_selftest_wait_timeout ran out */
 #define MAMBA2_DEVERR_TIMEOUT_DECODE 32       /* a wait ran out in the decode kernel */
+#define MAMBA2_DEVERR_CHAIN_SCAN 64           /* mamba2_scan_fwd (mamba2_layer.h) gave up waiting
+                                                 for the state of the tokens before */
 
 /* Device-side error word.  The tensor-core kernels bound every wait; a wait
  * that runs out sets a bit here and the kernel returns early (its outputs are

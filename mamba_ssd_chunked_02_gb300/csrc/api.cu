@@ -239,6 +239,8 @@ bool opt(const void* p) { return !p || aligned16(p); }
 
 }  // namespace
 
+int32_t* m2::device_error_word() { return error_word(); }
+
 extern "C" {
 
 mamba2_status mamba2_ssd_check_shape(const mamba2_ssd_shape* shape) { return check(shape); }

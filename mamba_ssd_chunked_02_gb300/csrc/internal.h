@@ -278,6 +278,10 @@ enum : int32_t {
     kErrChainK23 = 1 << 3,     // the fused stage 2+3 kernel gave up waiting for the previous chunk
     kErrSelfTest = 1 << 4,     // the wait self-test's waits ran out (expected)
     kErrTimeoutDecode = 1 << 5,  // a bounded wait ran out in the decode kernel
+    kErrChainScan = 1 << 6,    // the selective scan gave up waiting for the previous slice
 };
+
+// Address of the current device's error word (api.cu), or null.
+int32_t* device_error_word();
 
 }  // namespace m2

@@ -274,11 +274,11 @@ struct ScanArgs {
     bool softplus;
     Tok sx, sdt, sB, sC, sz, sy;
 };
-int64_t scan_fwd_segments(const ScanArgs& a);
+size_t scan_fwd_workspace(const ScanArgs& a);
 cudaError_t launch_scan_fwd(const ScanArgs& a, const void* x, const void* dt, const float* A,
                             const void* B, const void* C, const float* D, const void* z,
                             const float* dt_bias, const float* init, const int32_t* lengths,
-                            void* y, float* final_state, float* ws, cudaStream_t st);
+                            void* y, float* final_state, void* ws, cudaStream_t st);
 cudaError_t launch_scan_step(const ScanArgs& a, float* state, const void* x, const void* dt,
                              const float* A, const void* B, const void* C, const float* D,
                              const void* z, const float* dt_bias, void* y, cudaStream_t st);

@@ -119,11 +119,6 @@ bool norm_args(const mamba2_norm_shape* s, const mamba2_norm_strides* st, bool y
     return true;
 }
 
-size_t scan_fwd_bytes(const m2::ScanArgs& a) {
-    const int64_t n = m2::scan_fwd_segments(a);
-    return n > 1 ? sizeof(float) * (size_t)(n * a.b * a.D * (a.N + 1)) : 0;
-}
-
 bool space(const void* ws, size_t have, size_t need) {
     return need == 0 || (ws && have >= need && reinterpret_cast<uintptr_t>(ws) % 16 == 0);
 }
@@ -184,7 +179,7 @@ mamba2_status mamba2_conv_bwd(const mamba2_conv_shape* shape, const mamba2_conv_
 size_t mamba2_scan_workspace_size(const mamba2_scan_shape* shape) {
     m2::ScanArgs a;
     mamba2_status e;
-    return scan_args(shape, nullptr, false, &a, &e) ? scan_fwd_bytes(a) : 0;
+    return scan_args(shape, nullptr, false, &a, &e) ? m2::scan_fwd_workspace(a) : 0;
 }
 
 mamba2_status mamba2_scan_fwd(const mamba2_scan_shape* shape, const mamba2_scan_strides* strides, const void* x,
@@ -200,9 +195,9 @@ mamba2_status mamba2_scan_fwd(const mamba2_scan_shape* shape, const mamba2_scan_
         !opt(z, es) || !opt(dt_bias, 4) || !opt(initial_state, 4) || !opt(lengths, 4) || !req(y, all, es) ||
         !req(final_state, bd, 4))
         return MAMBA2_ERR_INVALID_ARG;
-    if (!space(workspace, workspace_bytes, scan_fwd_bytes(a))) return MAMBA2_ERR_WORKSPACE;
+    if (!space(workspace, workspace_bytes, m2::scan_fwd_workspace(a))) return MAMBA2_ERR_WORKSPACE;
     return from_cuda(m2::launch_scan_fwd(a, x, dt, A, B, C, D, z, dt_bias, initial_state, lengths, y, final_state,
-                                         static_cast<float*>(workspace), static_cast<cudaStream_t>(stream)));
+                                         workspace, static_cast<cudaStream_t>(stream)));
 }
 
 mamba2_status mamba2_scan_step(const mamba2_scan_shape* shape, const mamba2_scan_strides* strides, float* state,

@@ -21,13 +21,14 @@ template <int N> struct Cfg {
     static constexpr int TT = N >= 128 ? 32 : 16;
     static constexpr int U = LPC < 8 ? LPC : 8;           // values reduced together: 2 channels x UT tokens
     static constexpr int UT = U / 2;
-    static constexpr int YP = CB + 2 * CPW;               // pitch of the y tile (bank-conflict free)
+    static constexpr int YP = LPC <= 4 ? CB + CPW : CB + 2 * CPW;   // pitch of the y tile (bank-conflict free)
+    static constexpr int YF = TT * (LPC <= 4 ? LPC : 1) * YP;       // floats of the y tile
 };
 
-// Blocks an SM the registers are kept to: nine (96 registers) where the tile's registers
-// are few, else what does not spill.
+// Blocks an SM the registers are kept to.  (Nine, 96 registers, is slower a block by a
+// sixth than eight.)
 template <typename TI, int N, int V> constexpr int min_blocks() {
-    return N >= 64 ? 4 : V == 2 && sizeof(TI) == 2 && N >= 16 ? 9 : 6;
+    return N >= 64 ? 4 : V == 2 && N >= 16 ? 8 : 6;
 }
 
 // Sum v[u] over the LPC lanes of a channel for U values at once: at each step a lane

@@ -11,6 +11,7 @@
 
 #include "internal.h"
 #include "scan.cuh"
+#include "tc5.cuh"
 
 namespace m2 {
 namespace {
@@ -23,10 +24,28 @@ struct FwdP {
     float* fin;
     float* seg_h;     // [nseg][b][D][N]: local final states, then incoming states
     float* seg_d;     // [nseg][b][D]: sums of d
+    int32_t* turns;   // slices: [rows] slices done of each row (-1: given up), then the ticket; or null
+    int32_t* err;
     int T, Dch, G, Dg, ncb, nseg, SL, softplus;
     int64_t b;
     Tok sx, sdt, sB, sC, sz, sy;
 };
+
+// Rows (blocks that walk over all tokens) that are a little more than the GPU holds at
+// once would take two waves.  They take turns instead: the token axis is cut into
+// slices, and blocks take (slice, row) in slice order from a ticket, so that a block
+// only waits for one that started before it.  The state passes through final_state.
+constexpr uint64_t kTurnNs = 2000000000ull;   // 2 s: far beyond any legitimate wait
+__device__ bool await_turn(const int32_t* done, int slice) {
+    int v = tc::ld_acquire_gpu(done);
+    const uint64_t t0 = tc::globaltimer();
+    while (v >= 0 && v < slice) {
+        if (tc::globaltimer() - t0 > kTurnNs) return false;
+        __nanosleep(100);
+        v = tc::ld_acquire_gpu(done);
+    }
+    return v >= 0;
+}
 
 // STATES: only the segment's final state from zero and its sum of d (first of the
 // two passes when the token axis is split).  V: channels per access of x, dt, z, y
@@ -44,18 +63,32 @@ scan_fwd_kernel(const FwdP p) {
     float2* sP = reinterpret_cast<float2*>(smem);                               // [TT][CB] (d, dx)
     float* sB = reinterpret_cast<float*>(smem + (size_t)TT * CB * 8);           // [TT][N]
     float* sC = sB + TT * N;
-    float* sY = sC + TT * N;                                                    // [TT][YP]
+    // y of a tile: with up to four lanes a channel, each lane's part [TT][LPC][YP] (added by
+    // the epilogue: fewer instructions than lane exchanges); else the sums [TT][YP]
+    constexpr bool PART = LPC <= 4;
+    float* sY = sC + TT * N;
     constexpr int ST = 3 * TT * CB + 2 * TT * N;                                // elements of a staged tile
-    TI* sS = reinterpret_cast<TI*>(sY + TT * YP);                               // [2] x, dt, z [TT][CB], B, C [TT][N]
+    TI* sS = reinterpret_cast<TI*>(sY + K::YF);                               // [2] x, dt, z [TT][CB], B, C [TT][N]
     typedef typename Pack<TI, V>::Raw Raw;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int id = blockIdx.x;
+    __shared__ int s_turn, s_go;
+    int id = blockIdx.x, slice = 0, slices = 1;
+    int32_t* done = nullptr;
+    if (!STATES && p.turns) {
+        const int rows = p.ncb * p.G * (int)p.b;
+        slices = gridDim.x / rows;
+        if (tid == 0) s_turn = atomicAdd(p.turns + rows, 1);
+        __syncthreads();
+        slice = s_turn / rows;
+        id = s_turn - slice * rows;
+        done = p.turns + id;
+    }
     const int cb = id % p.ncb;
     id /= p.ncb;
     const int g = id % p.G;
     id /= p.G;
-    const int seg = id % p.nseg, b = id / p.nseg;
+    const int seg = done ? slice : id % p.nseg, b = done ? id : id / p.nseg;
     const int n = p.lengths ? min(max(__ldg(p.lengths + b), 0), p.T) : p.T;
     const int s0 = seg * p.SL, s1 = min(s0 + p.SL, p.T), sn = min(s1, n);
 
@@ -85,31 +118,16 @@ scan_fwd_kernel(const FwdP p) {
     const int q = lane % LPC, ch = 2 * (warp * K::CPW + lane / LPC);
     const int64_t sc = ((int64_t)b * p.Dch + (int64_t)g * p.Dg + cb * CB + ch) * N + q * kNS;   // in [b][D][N]
     const int64_t seg_off = (int64_t)seg * p.b * p.Dch * N;
-    f2 A2[2][2], h[2][2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), v = a;
-        if (cb * CB + ch + j < p.Dg) {
-            const float* Ap = p.A + ((int64_t)g * p.Dg + cb * CB + ch + j) * N + q * kNS;
-            a = make_float4(__ldg(Ap), __ldg(Ap + 1), __ldg(Ap + 2), __ldg(Ap + 3));
-            const float* hp = STATES ? nullptr : p.nseg > 1 ? p.seg_h + seg_off + sc : p.init ? p.init + sc : nullptr;
-            if (hp) v = make_float4(hp[j * N], hp[j * N + 1], hp[j * N + 2], hp[j * N + 3]);
-        }
-        A2[j][0] = pack2(a.x * kLog2e, a.y * kLog2e);
-        A2[j][1] = pack2(a.z * kLog2e, a.w * kLog2e);
-        h[j][0] = pack2(v.x, v.y);
-        h[j][1] = pack2(v.z, v.w);
-    }
     float dsum[2] = {0.f, 0.f};
 
     // What a thread stages for the next tile only it reads: the copies need no barrier and no
     // registers, and run under the scan of the tile at hand.
     const int own = r0 * CB + lc;   // this thread's first element of a staged tile
-    auto stage = [&](int t0, TI* buf) {   // tile after tile
-        const int lim = sn - t0;
+    const bool whole = cb * CB + CB <= p.Dg;   // every channel of the block exists
+    auto stage_tile = [&](const bool FULL, int lim, TI* buf) {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const bool real = con && r0 + i * RS < lim;
+            const bool real = FULL || (con && r0 + i * RS < lim);
             TI* d = buf + own + i * RS * CB;
             stage_copy<VB>(d, real ? xp + i * (RS * p.sx.t) : p.x, real);
             stage_copy<VB>(d + TT * CB, real ? dp + i * (RS * p.sdt.t) : p.x, real);
@@ -117,11 +135,16 @@ scan_fwd_kernel(const FwdP p) {
         }
 #pragma unroll
         for (int i = 0; i < BI; ++i) {
-            const bool real = br + i * BR < lim;
+            const bool real = FULL || br + i * BR < lim;
             TI* d = buf + 3 * TT * CB + (tid + i * NT) * V;
             stage_copy<VB>(d, real ? Bp + i * (BR * p.sB.t) : p.x, real);
             if (!STATES) stage_copy<VB>(d + TT * N, real ? Cp + i * (BR * p.sC.t) : p.x, real);
         }
+    };
+    auto stage = [&](int t0, TI* buf) {   // tile after tile; whole tiles without the edges' checks
+        const int lim = sn - t0;
+        if (whole && lim >= TT) stage_tile(true, lim, buf);
+        else stage_tile(false, lim, buf);
         stage_commit();
         xp += TT * p.sx.t;
         dp += TT * p.sdt.t;
@@ -131,6 +154,33 @@ scan_fwd_kernel(const FwdP p) {
     };
     TI *cur = sS, *nxt = sS + ST;
     stage(s0, cur);
+    f2 A2[2][2], h[2][2];
+    if (slice > 0) {   // the copies of the first tile are under way meanwhile
+        if (tid == 0) s_go = await_turn(done, slice);
+        __syncthreads();
+        if (!s_go) {
+            if (tid == 0) {
+                record_error(p.err, kErrChainScan);
+                tc::st_release_gpu(done, -1);
+            }
+            stage_wait();
+            return;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), v = a;
+        if (cb * CB + ch + j < p.Dg) {
+            const float* Ap = p.A + ((int64_t)g * p.Dg + cb * CB + ch + j) * N + q * kNS;
+            a = make_float4(__ldg(Ap), __ldg(Ap + 1), __ldg(Ap + 2), __ldg(Ap + 3));
+            const float* hp = STATES ? nullptr : slice > 0 ? p.fin + sc : p.seg_h ? p.seg_h + seg_off + sc : p.init ? p.init + sc : nullptr;
+            if (hp) v = make_float4(__ldcg(hp + j * N), __ldcg(hp + j * N + 1), __ldcg(hp + j * N + 2), __ldcg(hp + j * N + 3));
+        }
+        A2[j][0] = pack2(a.x * kLog2e, a.y * kLog2e);
+        A2[j][1] = pack2(a.z * kLog2e, a.w * kLog2e);
+        h[j][0] = pack2(v.x, v.y);
+        h[j][1] = pack2(v.z, v.w);
+    }
     for (int t0 = s0; t0 < s1; t0 += TT) {
         if (t0 >= n) {   // padding only
             if (!STATES && con)
@@ -179,12 +229,12 @@ scan_fwd_kernel(const FwdP p) {
         const float4* pP = reinterpret_cast<const float4*>(sP + ch);
         const float* pB = sB + q * kNS;
         const float* pC = sC + q * kNS;
-        constexpr int UN = 8;   // tokens unrolled
+        constexpr int UN = 16;   // tokens unrolled
 #pragma unroll 1
         for (int tb = 0; tb < TT; tb += UN) {
 #pragma unroll
             for (int tu = 0; tu < UN; tu += UT) {
-                float yv[U];
+                f2 yp2[UT][2];
 #pragma unroll
                 for (int u = 0; u < UT; ++u) {
                     const int t = tb + tu + u;
@@ -201,10 +251,18 @@ scan_fwd_kernel(const FwdP p) {
                         const ulonglong2 Cv = *reinterpret_cast<const ulonglong2*>(pC + t * N);
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
-                            yv[2 * u + j] = sum2(fma2(h[j][1], Cv.y, mul2(h[j][0], Cv.x)));
+                            yp2[u][j] = fma2(h[j][1], Cv.y, mul2(h[j][0], Cv.x));
                     }
                 }
-                if (!STATES) {   // value 2 u + j: token u of the UT, channel ch + j
+                if (!STATES && PART) {
+#pragma unroll
+                    for (int u = 0; u < UT; ++u)
+                        *reinterpret_cast<float2*>(sY + ((tb + tu + u) * LPC + q) * YP + ch) =
+                            make_float2(sum2(yp2[u][0]), sum2(yp2[u][1]));
+                } else if (!STATES) {   // value 2 u + j: token u of the UT, channel ch + j
+                    float yv[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) yv[u] = sum2(yp2[u / 2][u & 1]);
                     const float s = lanes_sum<LPC, U>(yv);
                     if (LPC <= U || q < U) sY[(tb + tu + ((lane & (U - 1)) >> 1)) * YP + ch + (lane & 1)] = s;
                 }
@@ -218,11 +276,19 @@ scan_fwd_kernel(const FwdP p) {
                 f2 fx[1], o[1];
                 const TI* st = cur + own + i * RS * CB;
                 to_pairs<TI, V>(*reinterpret_cast<const Raw*>(st), fx);
-                if constexpr (V == 2) {
-                    const float2 yv = *reinterpret_cast<const float2*>(sY + r * YP + lc);
-                    o[0] = pack2(yv.x, yv.y);
-                } else {
-                    o[0] = pack2(sY[r * YP + lc], 0.f);
+                constexpr int PARTS = PART ? LPC : 1;
+                const float* ys = sY + r * PARTS * YP + lc;
+                o[0] = dup2(0.f);
+#pragma unroll
+                for (int k = 0; k < PARTS; ++k) {
+                    f2 part;
+                    if constexpr (V == 2) {
+                        const float2 yv = *reinterpret_cast<const float2*>(ys + k * YP);
+                        part = pack2(yv.x, yv.y);
+                    } else {
+                        part = pack2(ys[k * YP], 0.f);
+                    }
+                    o[0] = k ? add2(o[0], part) : part;
                 }
                 o[0] = fma2(pack2(skip[0], skip[V - 1]), fx[0], o[0]);
                 if (p.z) {
@@ -249,13 +315,18 @@ scan_fwd_kernel(const FwdP p) {
             *reinterpret_cast<float4*>(p.seg_h + seg_off + sc + j * N) = v;
             if (q == 0)
                 p.seg_d[((int64_t)seg * p.b + b) * p.Dch + (int64_t)g * p.Dg + cb * CB + ch + j] = dsum[j];
-        } else if (seg == p.nseg - 1) {
+        } else if (done || seg == p.nseg - 1) {
             float* f = p.fin + sc + j * N;
             f[0] = v.x;
             f[1] = v.y;
             f[2] = v.z;
             f[3] = v.w;
         }
+    }
+    if (slice + 1 < slices) {
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) tc::st_release_gpu(done, slice + 1);
     }
 }
 
@@ -341,25 +412,42 @@ scan_step_kernel(float* __restrict__ state, const TI* __restrict__ x, const TI* 
     }
 }
 
-// Splitting the token axis costs a second pass over it (the first without y), so
-// it is done only where one pass leaves most of the GPU without warps.
-int64_t warps_of(const ScanArgs& a) {
-    const int64_t Dg = a.D / a.G, nt = a.N >= 64 ? 128 : 64, CB = 2 * (nt / (a.N / kNS));
-    return a.b * a.G * ((Dg + CB - 1) / CB) * (nt / 32);
+// How the token axis is cut.
+// nseg > 1: stretches side by side, for few rows; they cost a second pass (the first
+//   without y), so only where one pass leaves most of the GPU without warps.
+// slices > 1: rows in turns (see await_turn), for rows between one and a few waves of
+//   the blocks the GPU holds.  b8 C5120 N16 bf16 T4096 (1280 rows, 1216 held): 8 slices
+//   against one: see the kernel's figures.
+struct Cut {
+    int64_t nseg, slices, SL;
+};
+int64_t block_threads(const ScanArgs& a) { return a.N >= 64 ? 128 : 64; }
+int64_t rows_of(const ScanArgs& a) {
+    const int64_t Dg = a.D / a.G, CB = 2 * (block_threads(a) / (a.N / kNS));
+    return a.b * a.G * ((Dg + CB - 1) / CB);
 }
-int64_t tile_of(const ScanArgs& a) { return a.N >= 128 ? 32 : 16; }
-int64_t seg_len(const ScanArgs& a) {
-    const int64_t tt = tile_of(a), full = (int64_t)sm_count() * 16, w = std::max<int64_t>(1, warps_of(a));
-    if (2 * w >= full) return std::max<int64_t>(tt, (a.T + tt - 1) / tt * tt);
-    const int64_t n = std::min<int64_t>((full + w - 1) / w, std::max<int64_t>(1, a.T / (2 * tt)));
-    return std::max<int64_t>(tt, ((a.T + n - 1) / n + tt - 1) / tt * tt);
+Cut cut_of(const ScanArgs& a) {
+    const int64_t tt = a.N >= 128 ? 32 : 16, tiles = std::max<int64_t>(1, (a.T + tt - 1) / tt);
+    const int64_t rows = std::max<int64_t>(1, rows_of(a)), held = (int64_t)sm_count() * (a.N >= 64 ? 4 : 8);
+    Cut c{1, 1, tiles * tt};
+    int64_t parts = 1;
+    if (2 * rows <= held) {
+        parts = std::min<int64_t>(held / rows, tiles / 4);
+    } else if (rows > held && rows < 6 * held) {
+        parts = std::min<int64_t>(8, tiles / 8);
+    }
+    if (parts <= 1) return c;
+    c.SL = (tiles + parts - 1) / parts * tt;
+    const int64_t n = (a.T + c.SL - 1) / c.SL;
+    (2 * rows <= held ? c.nseg : c.slices) = n;
+    return c;
 }
 
 template <typename TI, int N, int V>
-cudaError_t fwd_v(const FwdP& p, cudaStream_t st) {
+cudaError_t fwd_v(const FwdP& p, int64_t slices, cudaStream_t st) {
     using K = Cfg<N>;
-    const int64_t blocks = p.b * p.nseg * p.G * p.ncb;
-    constexpr size_t smem = (size_t)K::TT * (K::CB * 8 + 2 * N * 4 + K::YP * 4) +
+    const int64_t rows = p.b * p.G * p.ncb, blocks = rows * p.nseg * slices;
+    constexpr size_t smem = (size_t)K::TT * (K::CB * 8 + 2 * N * 4) + (size_t)K::YF * 4 +
                             2 * (size_t)K::TT * (3 * K::CB + 2 * N) * sizeof(TI);
     if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     auto k = scan_fwd_kernel<TI, N, V, false>;
@@ -368,6 +456,10 @@ cudaError_t fwd_v(const FwdP& p, cudaStream_t st) {
         cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(s, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    if (p.turns) {
+        cudaError_t e = cudaMemsetAsync(p.turns, 0, sizeof(int32_t) * (size_t)(rows + 1), st);
         if (e != cudaSuccess) return e;
     }
     if (p.nseg > 1) {
@@ -380,26 +472,27 @@ cudaError_t fwd_v(const FwdP& p, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <typename TI, int N> cudaError_t fwd_n(const ScanArgs& a, FwdP p, cudaStream_t st) {
+template <typename TI, int N> cudaError_t fwd_n(const ScanArgs& a, FwdP p, int64_t slices, cudaStream_t st) {
     p.ncb = (int)((p.Dg + Cfg<N>::CB - 1) / Cfg<N>::CB);
     const int64_t es = sizeof(TI), by = 2 * es;
     const bool two = p.Dg % 2 == 0 && vec_ok(p.x, a.sx, by, es) && vec_ok(p.dt, a.sdt, by, es) &&
                      vec_ok(p.B, a.sB, by, es) && vec_ok(p.C, a.sC, by, es) &&
                      (!p.z || vec_ok(p.z, a.sz, by, es)) && vec_ok(p.y, a.sy, by, es);
-    return two ? fwd_v<TI, N, 2>(p, st) : fwd_v<TI, N, 1>(p, st);
+    return two ? fwd_v<TI, N, 2>(p, slices, st) : fwd_v<TI, N, 1>(p, slices, st);
 }
 
 }  // namespace
 
-int64_t scan_fwd_segments(const ScanArgs& a) {
-    if (a.T == 0) return 1;
-    const int64_t sl = seg_len(a);
-    return (a.T + sl - 1) / sl;
+size_t scan_fwd_workspace(const ScanArgs& a) {
+    if (a.b * a.T * a.D == 0) return 0;
+    const Cut c = cut_of(a);
+    if (c.nseg > 1) return sizeof(float) * (size_t)(c.nseg * a.b * a.D * (a.N + 1));
+    return c.slices > 1 ? sizeof(int32_t) * (size_t)(rows_of(a) + 1) : 0;
 }
 
 cudaError_t launch_scan_fwd(const ScanArgs& a, const void* x, const void* dt, const float* A, const void* B,
                             const void* C, const float* D, const void* z, const float* dt_bias,
-                            const float* init, const int32_t* lengths, void* y, float* fin, float* ws,
+                            const float* init, const int32_t* lengths, void* y, float* fin, void* ws,
                             cudaStream_t st) {
     if (a.b == 0 || a.D == 0) return cudaSuccess;
     if (a.T == 0) {
@@ -411,10 +504,14 @@ cudaError_t launch_scan_fwd(const ScanArgs& a, const void* x, const void* dt, co
     p.x = x, p.dt = dt, p.B = B, p.C = C, p.z = z, p.A = A, p.D = D, p.bias = dt_bias, p.init = init;
     p.lengths = lengths, p.y = y, p.fin = fin;
     p.T = (int)a.T, p.Dch = (int)a.D, p.G = (int)a.G, p.Dg = (int)(a.D / a.G), p.softplus = a.softplus;
-    p.SL = (int)seg_len(a), p.nseg = (int)scan_fwd_segments(a), p.b = a.b, p.ncb = 0;
-    p.seg_h = ws, p.seg_d = ws ? ws + (int64_t)p.nseg * a.b * a.D * a.N : nullptr;
+    const Cut cut = cut_of(a);
+    p.SL = (int)cut.SL, p.nseg = (int)cut.nseg, p.b = a.b, p.ncb = 0;
+    p.seg_h = cut.nseg > 1 ? static_cast<float*>(ws) : nullptr;
+    p.seg_d = cut.nseg > 1 ? p.seg_h + cut.nseg * a.b * a.D * a.N : nullptr;
+    p.turns = cut.slices > 1 ? static_cast<int32_t*>(ws) : nullptr;
+    p.err = device_error_word();
     p.sx = a.sx, p.sdt = a.sdt, p.sB = a.sB, p.sC = a.sC, p.sz = a.sz, p.sy = a.sy;
-    auto go = [&](auto f16, auto f32) { return a.dtype == 1 ? f16(a, p, st) : f32(a, p, st); };
+    auto go = [&](auto f16, auto f32) { return a.dtype == 1 ? f16(a, p, cut.slices, st) : f32(a, p, cut.slices, st); };
     switch (a.N) {
         case 8: return go(fwd_n<__nv_bfloat16, 8>, fwd_n<float, 8>);
         case 16: return go(fwd_n<__nv_bfloat16, 16>, fwd_n<float, 16>);

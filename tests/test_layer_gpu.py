@@ -230,6 +230,21 @@ def test_scan_long_axis_is_split_and_joined():
         close(g[k], want[k], k)
 
 
+@pytest.mark.parametrize("b,T,D,N,dt,ragged", [(40, 300, 1000, 16, BF16, False), (9, 515, 1100, 64, F32, True)])
+def test_scan_rows_in_turns(b, T, D, N, dt, ragged):
+    """More rows than the GPU holds: slices of the token axis hand the state on."""
+    v, n, _ = scan_inputs((b, T, D, N, 1, dt, True, True, True, True, True, ragged, 0), 15)
+    sh = m2.layer.ScanShape(b, T, D, N, 1, m2.BF16 if dt == BF16 else m2.F32, 1)
+    assert 0 < m2.scan_workspace_size(sh) < 4 * b * D      # a word a row, no states
+    args = [cu(v[k]) for k in ORDER]
+    runs = [m2.scan_fwd(*args, cu(n), dt_softplus=True) for _ in range(3)]
+    yr, fr = R.scan(*[f64(v[k]) for k in ORDER], n)
+    close(runs[0][0], yr, "y")
+    close(runs[0][1], fr, "final_state")
+    assert all(torch.equal(y, runs[0][0]) and torch.equal(f, runs[0][1]) for y, f in runs)
+    assert m2.device_error() == 0
+
+
 def test_scan_strong_and_absent_decay():
     """Steps that wipe the state out (exp(dA) = 0), steps of almost 0, and no decay (A = 0)."""
     case = (1, 50, 4, 16, 1, F32, True, True, False, False, True, False, 0)
