@@ -112,11 +112,11 @@ scan_local_kernel(const BwdP p) {
     float* ckd = p.ck_d + (int64_t)b * p.nck * p.Dch + cg;
 
     const int own = r0 * CB + lc;   // this thread's first element of a staged tile
-    auto stage = [&](int t0) {      // tile after tile
-        const int lim = sn - t0;
+    const bool whole = cb * CB + CB <= p.Dg;   // every channel of the block exists
+    auto stage_tile = [&](const bool FULL, int lim) {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const bool real = con && r0 + i * RS < lim;
+            const bool real = FULL || (con && r0 + i * RS < lim);
             TI* d = sS + own + i * RS * CB;
             stage_copy<VB>(d, real ? xp + i * (RS * p.sx.t) : p.x, real);
             stage_copy<VB>(d + TT * CB, real ? dp + i * (RS * p.sdt.t) : p.x, real);
@@ -125,11 +125,16 @@ scan_local_kernel(const BwdP p) {
         }
 #pragma unroll
         for (int i = 0; i < BI; ++i) {
-            const bool real = br + i * BR < lim;
+            const bool real = FULL || br + i * BR < lim;
             TI* d = sS + 4 * TT * CB + (tid + i * NT) * V;
             stage_copy<VB>(d, real ? Bp + i * (BR * p.sB.t) : p.x, real);
             if (ADJ) stage_copy<VB>(d + TT * N, real ? Cp + i * (BR * p.sC.t) : p.x, real);
         }
+    };
+    auto stage = [&](int t0) {      // tile after tile; whole tiles without the edges' checks
+        const int lim = sn - t0;
+        if (whole && lim >= TT) stage_tile(true, lim);
+        else stage_tile(false, lim);
         stage_commit();
         xp += TT * p.sx.t;
         dp += TT * p.sdt.t;
@@ -390,50 +395,72 @@ scan_grad_kernel(const BwdP p) {
         sG[k * kGT + tid] = gg;
         sD[k * kGT + tid] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    const TI* xb = static_cast<const TI*>(p.x) + (int64_t)b * p.sx.b + cg0;
-    const TI* tb_ = static_cast<const TI*>(p.dt) + (int64_t)b * p.sdt.b + cg0;
-    const TI* zb = static_cast<const TI*>(p.z) + (int64_t)b * p.sz.b + cg0;
-    const TI* yb = static_cast<const TI*>(p.dy) + (int64_t)b * p.sy.b + cg0;
-    const TI* Bb = static_cast<const TI*>(p.B) + (int64_t)b * p.sB.b + (int64_t)g * N;
-    const TI* Cb = static_cast<const TI*>(p.C) + (int64_t)b * p.sC.b + (int64_t)g * N;
+    // pointers to this thread's first element of the tile to stage next (the last tile first)
+    const int tiles = (s1 - s0 + kL - 1) / kL, tl = s0 + (tiles - 1) * kL;
+    const int64_t tr = tl + r0;
+    const TI* xp = static_cast<const TI*>(p.x) + (int64_t)b * p.sx.b + tr * p.sx.t + cg0 + lc0;
+    const TI* dp = static_cast<const TI*>(p.dt) + (int64_t)b * p.sdt.b + tr * p.sdt.t + cg0 + lc0;
+    const TI* zp = static_cast<const TI*>(p.z) + (int64_t)b * p.sz.b + tr * p.sz.t + cg0 + lc0;
+    const TI* yp = static_cast<const TI*>(p.dy) + (int64_t)b * p.sy.b + tr * p.sy.t + cg0 + lc0;
+    constexpr int BR = kGT * V / N > 0 ? kGT * V / N : 1;   // rows of B between a thread's accesses
+    const int br = tid * V / N;
+    const TI* Bp = static_cast<const TI*>(p.B) + (int64_t)b * p.sB.b + (tl + br) * p.sB.t + g * N + tid * V % N;
+    const TI* Cp = static_cast<const TI*>(p.C) + (int64_t)b * p.sC.b + (tl + br) * p.sC.t + g * N + tid * V % N;
+    const int ch0 = warp * CPW + cw;   // the lane's channel of turn 0
+    // stored states and outputs: a base the block shares, and the thread's offset in it
+    const float* ckb = p.ck + (((int64_t)b * p.nck + tl / kL) * p.Dch + cg0) * N;
+    const float* ckdb = p.ck_d + ((int64_t)b * p.nck + tl / kL) * p.Dch + cg0;
+    const int64_t out0 = ((int64_t)b * p.T + tl) * p.Dch + cg0;
+    TI* oxb = static_cast<TI*>(p.dx) + out0;
+    TI* odb = static_cast<TI*>(p.ddt) + out0;
+    TI* ozb = static_cast<TI*>(p.dz) + out0;
+    const int oat = r0 * p.Dch + lc0;   // rows r0 < 8, channels < 2^24
+    float* bcp = p.part_bc + (((int64_t)cb * p.b * p.T + (int64_t)b * p.T + tl) * p.G + g) * (2 * N);
 
-    auto stage = [&](int t0) {
+    auto stage_tile = [&](const bool FULL, int lim) {
 #pragma unroll
         for (int ci = 0; ci < CI; ++ci)
 #pragma unroll
             for (int i = 0; i < RI; ++i) {
-                const int r = r0 + i * RS, lc = lc0 + ci * PR * V, at = r * CB + lc;
+                const int r = r0 + i * RS, off = ci * PR * V, at = r * CB + lc0 + off;
                 if (r >= kL) continue;
-                const bool real = lc < left && t0 + r < sn;
-                const int64_t t = real ? t0 + r : 0;   // an address inside the tensor either way
-                const int cc = real ? lc : 0;
-                stage_copy<VB>(stX + at, xb + t * p.sx.t + cc, real);
-                stage_copy<VB>(stT + at, tb_ + t * p.sdt.t + cc, real);
-                stage_copy<VB>(stY + at, yb + t * p.sy.t + cc, real);
-                if (GATE) stage_copy<VB>(stZ + at, zb + t * p.sz.t + cc, real);
+                const bool real = FULL || (lc0 + off < left && r < lim);
+                stage_copy<VB>(stX + at, real ? xp + i * (RS * p.sx.t) + off : p.x, real);
+                stage_copy<VB>(stT + at, real ? dp + i * (RS * p.sdt.t) + off : p.x, real);
+                stage_copy<VB>(stY + at, real ? yp + i * (RS * p.sy.t) + off : p.x, real);
+                if (GATE) stage_copy<VB>(stZ + at, real ? zp + i * (RS * p.sz.t) + off : p.x, real);
             }
 #pragma unroll
         for (int i = 0; i < BI; ++i) {
-            const int e = (tid + i * kGT) * V, r = e / N;
+            const int e = (tid + i * kGT) * V;
             if (e >= kL * N) continue;
-            const bool real = t0 + r < sn;
-            const int64_t t = real ? t0 + r : 0;
-            stage_copy<VB>(stB + e, Bb + t * p.sB.t + e % N, real);
-            stage_copy<VB>(stC + e, Cb + t * p.sC.t + e % N, real);
+            const bool real = FULL || br + i * BR < lim;
+            stage_copy<VB>(stB + e, real ? Bp + i * (BR * p.sB.t) : p.x, real);
+            stage_copy<VB>(stC + e, real ? Cp + i * (BR * p.sC.t) : p.x, real);
         }
-        const int64_t ck_at = ((int64_t)b * p.nck + t0 / kL) * p.Dch + cg0;
 #pragma unroll
         for (int k = 0; k < kK; ++k) {
-            const int ch = k * K::CK + warp * CPW + cw;
-            const int64_t o = ck_at + (ch < left ? ch : 0);
-            stage_copy<16>(stK + k * kGT + tid, p.ck + o * N + q * kNS, ch < left);
-            stage_copy<4>(stD + k * kGT + tid, p.ck_d + o, ch < left);
+            const bool real = FULL || ch0 + k * K::CK < left;
+            stage_copy<16>(stK + k * kGT + tid, real ? ckb + ((ch0 + k * K::CK) * N + q * kNS) : p.ck, real);
+            stage_copy<4>(stD + k * kGT + tid, real ? ckdb + (ch0 + k * K::CK) : p.ck, real);
         }
+    };
+    auto stage = [&](int t0) {   // tile before tile; whole tiles without the edges' checks
+        const int lim = sn - t0;
+        if (left >= CB && lim >= kL) stage_tile(true, lim);
+        else stage_tile(false, lim);
         stage_commit();
+        xp -= kL * p.sx.t;
+        dp -= kL * p.sdt.t;
+        zp -= kL * p.sz.t;
+        yp -= kL * p.sy.t;
+        Bp -= kL * p.sB.t;
+        Cp -= kL * p.sC.t;
+        ckb -= (int64_t)p.Dch * N;
+        ckdb -= p.Dch;
     };
 
-    const int tiles = (s1 - s0 + kL - 1) / kL;
-    stage(s0 + (tiles - 1) * kL);
+    stage(tl);
     for (int ti = tiles - 1; ti >= 0; --ti) {
         const int t0 = s0 + ti * kL;
         stage_wait();
@@ -587,13 +614,13 @@ scan_grad_kernel(const BwdP p) {
         }
         __syncthreads();
         for (int e = tid; e < 2 * kL * N; e += kGT) {
-            const int wt = e / N, t = t0 + wt % kL;
+            const int wt = e / N, r = wt % kL;
             float a = 0.f;
 #pragma unroll
             for (int w = 0; w < K::WARPS; ++w) a += sR[w * 2 * kL * N + e];
-            if (t < s1)
-                p.part_bc[(((int64_t)cb * p.b * p.T + (int64_t)b * p.T + t) * p.G + g) * (2 * N) + (wt / kL) * N + e % N] = a;
+            if (t0 + r < s1) bcp[r * (p.G * 2 * N) + (wt / kL) * N + e % N] = a;
         }
+        bcp -= kL * p.G * 2 * N;
 #pragma unroll
         for (int ci = 0; ci < CI; ++ci)
 #pragma unroll
@@ -622,25 +649,28 @@ scan_grad_kernel(const BwdP p) {
                     ev = pack2(sE[r * QP + lc], 0.f);
                     if (GATE) ov = pack2(sO[r * QP + lc], 0.f);
                 }
-                const int64_t at = ((int64_t)b * p.T + t) * p.Dch + cg0 + lc;
+                const int at = oat + i * RS * p.Dch + ci * PR * V;
                 if (GATE) {
                     to_pairs<TI, V>(kz[ci][i], fz);
                     const f2 sg = sigmoid2(fz[0]);
                     // silu' = sg (1 + z (1 - sg))
                     const f2 slope = mul2(sg, fma2(fz[0], fma2(sg, dup2(-1.f), dup2(1.f)), dup2(1.f)));
                     o[0] = mul2(mul2(fy[0], slope), fma2(skip[ci], fx[0], ov));
-                    store_raw<TI, V>(static_cast<TI*>(p.dz) + at, from_pairs<TI, V>(o));
+                    store_raw<TI, V>(ozb + at, from_pairs<TI, V>(o));
                     fy[0] = mul2(fy[0], mul2(fz[0], sg));
                 }
                 o[0] = fma2(d, qv, mul2(skip[ci], fy[0]));
-                store_raw<TI, V>(static_cast<TI*>(p.dx) + at, from_pairs<TI, V>(o));
+                store_raw<TI, V>(oxb + at, from_pairs<TI, V>(o));
                 od[0] = fma2(fx[0], qv, mul2(dup2(0.6931471805599453f), ev));   // e was taken with A log2(e)
                 if (p.softplus) od[0] = mul2(od[0], sigmoid2(add2(fd[0], bias[ci])));
                 if (!real) od[0] = dup2(0.f);
-                store_raw<TI, V>(static_cast<TI*>(p.ddt) + at, from_pairs<TI, V>(od));
+                store_raw<TI, V>(odb + at, from_pairs<TI, V>(od));
                 accD[ci] = fma2(fy[0], fx[0], accD[ci]);
                 accB[ci] = add2(accB[ci], od[0]);
             }
+        oxb -= (int64_t)kL * p.Dch;
+        odb -= (int64_t)kL * p.Dch;
+        ozb -= (int64_t)kL * p.Dch;
         __syncthreads();
     }
     // dA, dinit
@@ -708,17 +738,28 @@ struct Plan {
     size_t ck, ck_d, seg, seg_d, bc, A, v, total;
 };
 
-// Stretches: enough that the gradient kernel's blocks (two an SM) go around about
-// four times, none shorter than two tiles of the first pass.
+// Stretches: as many as keep the gradient kernel's blocks (two an SM) busiest, whole waves
+// of them against the start of each; none shorter than two tiles of the first pass.
 Plan plan_of(const ScanArgs& a) {
     Plan p;
     const int64_t Dg = a.D / a.G, lpc = a.N / kNS;
     const int64_t CB = (kGT / lpc) * kK;
     p.ncb = (Dg + CB - 1) / CB;
     const int64_t tt = 32;   // a multiple of the first pass's tile and of kL
-    const int64_t per = std::max<int64_t>(1, a.b * a.G * p.ncb), want = (int64_t)sm_count() * 8;
-    const int64_t n = std::max<int64_t>(1, std::min<int64_t>((want + per - 1) / per, a.T / (2 * tt)));
-    p.SL = std::max<int64_t>(tt, ((a.T + n - 1) / n + tt - 1) / tt * tt);
+    const int64_t per = std::max<int64_t>(1, a.b * a.G * p.ncb), held = (int64_t)sm_count() * 2;
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(64, a.T / (2 * tt)));
+    double top = 0.;
+    p.SL = std::max<int64_t>(tt, (a.T + tt - 1) / tt * tt);
+    for (int64_t n = 1; n <= most; ++n) {
+        const int64_t SL = ((a.T + n - 1) / n + tt - 1) / tt * tt, segs = (a.T + SL - 1) / SL;
+        // waves of blocks, each as long as a stretch and its start (about two tiles)
+        const double waves = (double)((per * segs + held - 1) / held);
+        const double share = (double)per * (double)a.T / (waves * (double)held * (double)(SL + 16));
+        if (share > top * 1.01) {
+            top = share;
+            p.SL = SL;
+        }
+    }
     p.nseg = std::max<int64_t>(1, (a.T + p.SL - 1) / p.SL);
     p.nck = (a.T + kL - 1) / kL;
     auto al = [](size_t v) { return (v + 255) & ~size_t(255); };
