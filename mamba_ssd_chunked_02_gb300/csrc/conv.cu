@@ -495,20 +495,25 @@ bool wide(const ConvArgs& a, int64_t V, const float* w, const void* x, const voi
            vec_ok(s0, row, bytes, es) && vec_ok(s1, row, bytes, es) && vec_ok(o, row, bytes, es);
 }
 
-// Sum of one column of part over the slots: 32 columns x 8 rows of slots a block.
-__global__ void __launch_bounds__(256)
+// Sum of one column of part over the slots: TX columns x 1024 / TX rows of slots a block.
+template <int TX>
+__global__ void __launch_bounds__(1024)
 column_sum_kernel(const float* __restrict__ part, int64_t slots, int64_t cols, float* __restrict__ out1,
                   int64_t n1, float* __restrict__ out2) {
-    __shared__ float red[8][33];
-    const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
+    constexpr int TY = 1024 / TX;
+    __shared__ float red[TY][TX + 1];
+    const int64_t c = (int64_t)blockIdx.x * TX + threadIdx.x;
     float a = 0.f;
     if (c < cols)
-        for (int64_t s = threadIdx.y; s < slots; s += 8) a += __ldg(part + s * cols + c);
+#pragma unroll 4
+        for (int64_t s = threadIdx.y; s < slots; s += TY) a += __ldg(part + s * cols + c);
     red[threadIdx.y][threadIdx.x] = a;
-    __syncthreads();
+    for (int q = TY / 2; q > 0; q /= 2) {
+        __syncthreads();
+        if (threadIdx.y < q) red[threadIdx.y][threadIdx.x] += red[threadIdx.y + q][threadIdx.x];
+    }
     if (threadIdx.y == 0 && c < cols) {
-#pragma unroll
-        for (int q = 1; q < 8; ++q) a += red[q][threadIdx.x];
+        a = red[0][threadIdx.x];
         if (c < n1) {
             if (out1) out1[c] = a;
         } else if (out2) {
@@ -522,9 +527,13 @@ column_sum_kernel(const float* __restrict__ part, int64_t slots, int64_t cols, f
 cudaError_t launch_column_sum(const float* part, int64_t slots, int64_t cols, float* out1, int64_t n1,
                               float* out2, cudaStream_t st) {
     if (cols == 0) return cudaSuccess;
-    if ((cols + 31) / 32 >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-    column_sum_kernel<<<(unsigned)((cols + 31) / 32), dim3(32, 8), 0, st>>>(part, slots, cols, out1, n1,
-                                                                           out2);
+    if ((cols + 7) / 8 >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    // few columns and many slots (a narrow layer): more rows of slots a block, so that a
+    // thread's chain of loads stays short
+    if (cols < (int64_t)sm_count() * 64 && slots > 64)
+        column_sum_kernel<8><<<(unsigned)((cols + 7) / 8), dim3(8, 128), 0, st>>>(part, slots, cols, out1, n1, out2);
+    else
+        column_sum_kernel<32><<<(unsigned)((cols + 31) / 32), dim3(32, 32), 0, st>>>(part, slots, cols, out1, n1, out2);
     return cudaGetLastError();
 }
 

@@ -57,6 +57,9 @@ template <int V> __device__ __forceinline__ void load_weights(const float* w, f2
         for (int i = 0; i < (V + 1) / 2; ++i) o[i] = dup2(1.f);
     } else if constexpr (V == 1) {
         o[0] = pack2(__ldg(w), 0.f);
+    } else if constexpr (V == 2) {
+        const float2 v = __ldg(reinterpret_cast<const float2*>(w));
+        o[0] = pack2(v.x, v.y);
     } else {
 #pragma unroll
         for (int i = 0; i < V / 2; i += 2) {
@@ -184,7 +187,7 @@ norm_bwd_kernel(const TI* __restrict__ x, const float* __restrict__ w, const TI*
     const f2 one = dup2(1.f), minus = dup2(-1.f);
     // The next token's row is copied into the other half of a thread's own room in shared
     // memory while this one is summed and applied.
-    constexpr bool STAGE = VPT > 0 && V > 1;
+    constexpr bool STAGE = VPT > 0 && V * sizeof(TI) >= 4;
     extern __shared__ __align__(16) unsigned char smem[];
     const int bt = blockDim.x;
     Raw* st = reinterpret_cast<Raw*>(smem) + threadIdx.x;   // [2][K][3 tensors][threads]
@@ -367,8 +370,10 @@ int team_threads(int64_t nv, int vpt) {
 // Backward slots of dw: as many teams as an SM holds at once (16 warps, or blocks of 1024
 // threads in all), each with an equal share of the tokens, over the groups.
 int64_t bwd_team_slots(const NormArgs& a) {
-    const int64_t S = a.D / a.G, full = a.dtype == 1 ? 8 : 4, V = S % full ? 1 : full, nv = S / V;
-    const int64_t per_sm = nv <= 96 ? 16 : std::max<int64_t>(1, 1024 / team_threads(nv, nv <= 1024 ? 1 : 2));
+    const int64_t S = a.D / a.G, full = a.dtype == 1 ? 8 : 4;
+    const int64_t V = S % full == 0 ? full : a.dtype != 1 ? 1 : S % 4 == 0 ? 4 : S % 2 == 0 ? 2 : 1, nv = S / V;
+    const int64_t per_sm =
+        nv <= 96 ? 16 : std::max<int64_t>(1, 1024 / team_threads(nv, V <= 2 ? 4 : nv <= 1024 ? 1 : 2));
     const int64_t teams = (int64_t)sm_count() * per_sm;
     return std::max<int64_t>(1, std::min<int64_t>(a.b * a.T, teams / a.G));
 }
@@ -383,6 +388,8 @@ cudaError_t fwd_go(const NormArgs& a, const TI* x, const float* w, const TI* z, 
     if (nv <= 32) norm_fwd_kernel<TI, V, 1, GATE, true><<<wb, kWarpTeams * 32, 0, st>>>(x, w, z, y, q);
     else if (nv <= 64) norm_fwd_kernel<TI, V, 2, GATE, true><<<wb, kWarpTeams * 32, 0, st>>>(x, w, z, y, q);
     else if (nv <= 128) norm_fwd_kernel<TI, V, 4, GATE, true><<<wb, kWarpTeams * 32, 0, st>>>(x, w, z, y, q);
+    else if (V <= 2 && nv <= 8192)   // narrow accesses: more of them a thread, fewer warps to join
+        norm_fwd_kernel<TI, V, V <= 2 ? 8 : 1, GATE, false><<<bb, team_threads(nv, 8), 0, st>>>(x, w, z, y, q);
     else if (nv <= 2048) norm_fwd_kernel<TI, V, 2, GATE, false><<<bb, team_threads(nv, 2), 0, st>>>(x, w, z, y, q);
     else norm_fwd_kernel<TI, V, 0, GATE, false><<<bb, 1024, 0, st>>>(x, w, z, y, q);
     return cudaGetLastError();
@@ -398,9 +405,9 @@ cudaError_t bwd_go(const NormArgs& a, const TI* x, const float* w, const TI* z, 
     const int teams = (int)teams64;
     const unsigned wb = (unsigned)((teams64 + kWarpTeams - 1) / kWarpTeams);
     const unsigned bb = (unsigned)teams;
-    // [2 halves][vectors a thread][3 tensors] of 16 bytes a thread: 12 to 96 KB a block
+    // [2 halves][vectors a thread][3 tensors] of up to 16 bytes a thread: at most 192 KB a block
     auto go = [&](auto k, unsigned blocks, int threads, int vpt) {
-        const size_t smem = V > 1 ? (size_t)2 * vpt * 3 * 16 * threads : 0;
+        const size_t bytes = V * sizeof(TI), smem = bytes >= 4 ? (size_t)2 * vpt * 3 * bytes * threads : 0;
         if (smem > 48 * 1024) {
             cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
             if (e != cudaSuccess) return e;
@@ -410,7 +417,10 @@ cudaError_t bwd_go(const NormArgs& a, const TI* x, const float* w, const TI* z, 
     };
     cudaError_t e;
     if (nv <= 32) e = go(norm_bwd_kernel<TI, V, 1, GATE, true>, wb, kWarpTeams * 32, 1);
+    else if (nv <= 64) e = go(norm_bwd_kernel<TI, V, 2, GATE, true>, wb, kWarpTeams * 32, 2);
     else if (nv <= 96) e = go(norm_bwd_kernel<TI, V, 3, GATE, true>, wb, kWarpTeams * 32, 3);
+    else if (V <= 2 && nv <= 4096)
+        e = go(norm_bwd_kernel<TI, V, V <= 2 ? 4 : 1, GATE, false>, bb, team_threads(nv, 4), 4);
     else if (nv <= 1024) e = go(norm_bwd_kernel<TI, V, 1, GATE, false>, bb, team_threads(nv, 1), 1);
     else if (nv <= 2048) e = go(norm_bwd_kernel<TI, V, 2, GATE, false>, bb, team_threads(nv, 2), 2);
     else e = go(norm_bwd_kernel<TI, V, 0, GATE, false>, bb, 1024, 0);
@@ -436,12 +446,21 @@ cudaError_t bwd_gate(const NormArgs& a, const void* x, const float* w, const voi
     return !z ? go(bwd_go<TI, V, kNone>) : a.after ? go(bwd_go<TI, V, kAfter>) : go(bwd_go<TI, V, kFirst>);
 }
 
-bool wide(const NormArgs& a, int64_t V, const void* x, const float* w, const void* z, const void* y,
-          const void* o1, const void* o2) {
+// Channels an access: the most of 16, 8 and 4 bytes at which every tensor's rows and the
+// groups are aligned, else one.
+int vec_of(const NormArgs& a, const void* x, const float* w, const void* z, const void* y, const void* o1,
+           const void* o2) {
     const int64_t es = a.dtype == 1 ? 2 : 4;
     const Tok row{0, a.D};
-    return (a.D / a.G) % V == 0 && reinterpret_cast<uintptr_t>(w) % 16 == 0 && vec_ok(x, a.sx, 16, es) && (!z || vec_ok(z, a.sz, 16, es)) &&
-           vec_ok(y, a.sy, 16, es) && vec_ok(o1, row, 16, es) && vec_ok(o2, row, 16, es);
+    for (int V : {8, 4, 2}) {
+        if (a.dtype != 1 && V != 4) continue;
+        const int64_t by = V * es;
+        if ((a.D / a.G) % V == 0 && reinterpret_cast<uintptr_t>(w) % (V > 2 ? 16 : 8) == 0 && vec_ok(x, a.sx, by, es) &&
+            (!z || vec_ok(z, a.sz, by, es)) && vec_ok(y, a.sy, by, es) && vec_ok(o1, row, by, es) &&
+            vec_ok(o2, row, by, es))
+            return V;
+    }
+    return 1;
 }
 
 }  // namespace
@@ -449,11 +468,12 @@ bool wide(const NormArgs& a, int64_t V, const void* x, const float* w, const voi
 cudaError_t launch_norm_fwd(const NormArgs& a, const void* x, const float* w, const void* z, void* y,
                             cudaStream_t st) {
     if (a.b * a.T == 0 || a.D == 0) return cudaSuccess;
-    if (a.dtype == 1)
-        return wide(a, 8, x, w, z, y, nullptr, nullptr) ? fwd_gate<__nv_bfloat16, 8>(a, x, w, z, y, st)
-                                                     : fwd_gate<__nv_bfloat16, 1>(a, x, w, z, y, st);
-    return wide(a, 4, x, w, z, y, nullptr, nullptr) ? fwd_gate<float, 4>(a, x, w, z, y, st)
-                                                 : fwd_gate<float, 1>(a, x, w, z, y, st);
+    const int V = vec_of(a, x, w, z, y, nullptr, nullptr);
+    if (a.dtype != 1) return V == 4 ? fwd_gate<float, 4>(a, x, w, z, y, st) : fwd_gate<float, 1>(a, x, w, z, y, st);
+    return V == 8   ? fwd_gate<__nv_bfloat16, 8>(a, x, w, z, y, st)
+           : V == 4 ? fwd_gate<__nv_bfloat16, 4>(a, x, w, z, y, st)
+           : V == 2 ? fwd_gate<__nv_bfloat16, 2>(a, x, w, z, y, st)
+                    : fwd_gate<__nv_bfloat16, 1>(a, x, w, z, y, st);
 }
 
 int64_t norm_bwd_slots(const NormArgs& a) { return bwd_team_slots(a); }
@@ -466,13 +486,15 @@ cudaError_t launch_norm_bwd(const NormArgs& a, const void* x, const float* w, co
     if (!dw) part = nullptr;
     const bool none = a.b * a.T == 0;
     if (!none) {
-        const bool v = wide(a, a.dtype == 1 ? 8 : 4, x, w, z, dy, dx, dz);
-        if (a.dtype == 1)
-            e = v ? bwd_gate<__nv_bfloat16, 8>(a, x, w, z, dy, dx, dz, part, st)
-                  : bwd_gate<__nv_bfloat16, 1>(a, x, w, z, dy, dx, dz, part, st);
+        const int V = vec_of(a, x, w, z, dy, dx, dz);
+        if (a.dtype != 1)
+            e = V == 4 ? bwd_gate<float, 4>(a, x, w, z, dy, dx, dz, part, st)
+                       : bwd_gate<float, 1>(a, x, w, z, dy, dx, dz, part, st);
         else
-            e = v ? bwd_gate<float, 4>(a, x, w, z, dy, dx, dz, part, st)
-                  : bwd_gate<float, 1>(a, x, w, z, dy, dx, dz, part, st);
+            e = V == 8   ? bwd_gate<__nv_bfloat16, 8>(a, x, w, z, dy, dx, dz, part, st)
+                : V == 4 ? bwd_gate<__nv_bfloat16, 4>(a, x, w, z, dy, dx, dz, part, st)
+                : V == 2 ? bwd_gate<__nv_bfloat16, 2>(a, x, w, z, dy, dx, dz, part, st)
+                         : bwd_gate<__nv_bfloat16, 1>(a, x, w, z, dy, dx, dz, part, st);
     }
     if (e != cudaSuccess || !dw) return e;
     return launch_column_sum(part, none ? 0 : norm_bwd_slots(a), a.D, dw, a.D, nullptr, st);

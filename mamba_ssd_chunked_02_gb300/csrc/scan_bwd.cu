@@ -739,7 +739,8 @@ struct Plan {
 };
 
 // Stretches: as many as keep the gradient kernel's blocks (two an SM) busiest, whole waves
-// of them against the start of each; none shorter than two tiles of the first pass.
+// of them against the start of each; none shorter than two tiles of the first
+// pass, and no more than 64 for the join.
 Plan plan_of(const ScanArgs& a) {
     Plan p;
     const int64_t Dg = a.D / a.G, lpc = a.N / kNS;
@@ -747,7 +748,7 @@ Plan plan_of(const ScanArgs& a) {
     p.ncb = (Dg + CB - 1) / CB;
     const int64_t tt = 32;   // a multiple of the first pass's tile and of kL
     const int64_t per = std::max<int64_t>(1, a.b * a.G * p.ncb), held = (int64_t)sm_count() * 2;
-    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(64, a.T / (2 * tt)));
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(64, a.T / tt));
     double top = 0.;
     p.SL = std::max<int64_t>(tt, (a.T + tt - 1) / tt * tt);
     for (int64_t n = 1; n <= most; ++n) {

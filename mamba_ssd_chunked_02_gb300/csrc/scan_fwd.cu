@@ -431,8 +431,8 @@ Cut cut_of(const ScanArgs& a) {
     const int64_t rows = std::max<int64_t>(1, rows_of(a)), held = (int64_t)sm_count() * (a.N >= 64 ? 4 : 8);
     Cut c{1, 1, tiles * tt};
     int64_t parts = 1;
-    if (2 * rows <= held) {
-        parts = std::min<int64_t>(held / rows, tiles / 4);
+    if (2 * rows <= held && tiles >= 8) {   // (fewer tiles: the two more launches cost as much)
+        parts = std::min<int64_t>(held / rows, tiles / 2);
     } else if (rows > held && rows < 6 * held) {
         parts = std::min<int64_t>(8, tiles / 8);
     }
