@@ -24,7 +24,8 @@
  *     A sequence of length 0 leaves its state as it came.
  *   - Outputs must not overlap inputs, except `state` of the step calls, which
  *     is updated in place.
- *   - Results do not depend on the order in which blocks run: no atomics.
+ *   - Results do not depend on the order in which blocks run: sums over blocks are
+ *     taken in a fixed order.  Calls that share a workspace must not overlap.
  *   - A zero batch or channel count is a no-op (gradients of parameters are
  *     written as 0); seqlen 0 copies the initial state to the final state.
  */
@@ -92,7 +93,8 @@ MAMBA2_API mamba2_status mamba2_conv_bwd(const mamba2_conv_shape* shape,
  *   y_t[c]   = sum_n C_t[g,n] h_t[c,n] + D[c] x_t[c],   times silu(z_t[c]) if z
  * Channel c reads group g = c / (channels / groups).  h_{-1} = initial_state
  * [b,D,N] (NULL = 0); final_state is h after the last token.  States are fp32.
- * states N in {8, 16, 32, 64, 128}; channels % groups == 0. */
+ * states N in {8, 16, 32, 64, 128}; channels % groups == 0; groups * states and
+ * channels at most 2^24, seqlen and batch at most 2^30. */
 #define MAMBA2_SCAN_SOFTPLUS 1
 
 typedef struct mamba2_scan_shape {

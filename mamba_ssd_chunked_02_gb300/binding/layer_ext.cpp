@@ -10,9 +10,11 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <initializer_list>
+#include <optional>
 #include <string>
 #include <utility>
 
@@ -127,14 +129,27 @@ struct Call {
         hold = make({(int64_t)need}, at::kByte);
         return hold.data_ptr();
     }
-    void* stream(PyObject* o) const {
-        if (!o || o == Py_None) return c10::cuda::getCurrentCUDAStream(device.index()).stream();
+};
+
+// The stream of a call: the current one, or the one given, which is then the current one
+// for what the call allocates (an output or a workspace of another stream's pool could
+// still be in use there, or be handed out again before this call is through with it).
+struct OnStream {
+    std::optional<c10::cuda::CUDAStreamGuard> guard;
+    void* raw;
+
+    OnStream(const Call& c, PyObject* o) {
+        if (!o || o == Py_None) {
+            raw = c10::cuda::getCurrentCUDAStream(c.device.index()).stream();
+            return;
+        }
         PyObject* h = PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream") : PyNumber_Long(o);
         if (!h) throw Raised();
-        void* p = PyLong_AsVoidPtr(h);
+        raw = PyLong_AsVoidPtr(h);
         Py_DECREF(h);
         if (PyErr_Occurred()) throw Raised();
-        return p;
+        guard.emplace(raw ? c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(raw), c.device.index())
+                          : c10::cuda::getDefaultCUDAStream(c.device.index()));
     }
 };
 
@@ -267,6 +282,7 @@ typedef PyObject* const* Args;
 // ---- conv: (x, w, bias, initial_state, lengths, silu, y, final_state, stream)
 PyObject* conv_fwd(Args a) {
     const Call c(a[0], "x", 3);
+    const OnStream on(c, a[8]);
     const Tensor& x = THPVariable_Unpack(a[0]);
     const int64_t b = x.size(0), T = x.size(1), D = x.size(2), W = second_dim(a[1], "w", "width", D);
     const mamba2_conv_shape sh{b, T, D, (int32_t)W, c.dtype(), truth(a[5]) ? MAMBA2_CONV_SILU : 0};
@@ -279,13 +295,14 @@ PyObject* conv_fwd(Args a) {
     Out y = token_out(c, a[6], "y", {b, T, D}, st.y);
     Out f = dense_out(c, a[7], "final_state", c.io, {b, W > 0 ? W - 1 : 0, D});
     check("mamba2_conv_fwd", mamba2_conv_fwd(&sh, &st, px, (float*)pw, (float*)pb, pi, (int32_t*)pl, y.at, f.at,
-                                             c.stream(a[8])));
+                                             on.raw));
     return pair(y, f);
 }
 
 // (state, x, w, bias, silu, y, stream)
 PyObject* conv_step(Args a) {
     const Call c(a[1], "x", 2);
+    const OnStream on(c, a[6]);
     const Tensor& x = THPVariable_Unpack(a[1]);
     const int64_t b = x.size(0), D = x.size(1), W = second_dim(a[2], "w", "width", D);
     const mamba2_conv_shape sh{b, 1, D, (int32_t)W, c.dtype(), truth(a[4]) ? MAMBA2_CONV_SILU : 0};
@@ -296,13 +313,14 @@ PyObject* conv_step(Args a) {
     void* pb = c.dense(a[3], "bias", at::kFloat, {D}, true);
     Out y = token_out(c, a[5], "y", {b, D}, st.y, 1);
     check("mamba2_conv_step",
-          mamba2_conv_step(&sh, &st, ps, px, (float*)pw, (float*)pb, y.at, c.stream(a[6])));
+          mamba2_conv_step(&sh, &st, ps, px, (float*)pw, (float*)pb, y.at, on.raw));
     return y.give();
 }
 
 // (x, w, bias, initial_state, dy, dfinal, lengths, silu, grads, workspace, stream)
 PyObject* conv_bwd(Args a) {
     const Call c(a[0], "x", 3);
+    const OnStream on(c, a[10]);
     const Tensor& x = THPVariable_Unpack(a[0]);
     const int64_t b = x.size(0), T = x.size(1), D = x.size(2), W = second_dim(a[1], "w", "width", D);
     const mamba2_conv_shape sh{b, T, D, (int32_t)W, c.dtype(), truth(a[7]) ? MAMBA2_CONV_SILU : 0};
@@ -323,7 +341,7 @@ PyObject* conv_bwd(Args a) {
     size_t bytes;
     void* ws = c.space(a[9], mamba2_conv_bwd_workspace_size(&sh), hold, &bytes);
     check("mamba2_conv_bwd", mamba2_conv_bwd(&sh, &st, px, (float*)pw, (float*)pb, pi, py, pf, (int32_t*)pl, dx, (float*)dw,
-                                             (float*)db, di, ws, bytes, c.stream(a[10])));
+                                             (float*)db, di, ws, bytes, on.raw));
     return g.give();
 }
 
@@ -348,6 +366,7 @@ ScanCall scan_call(const Call& c, const Tensor& x, PyObject* A, PyObject* B, boo
 // (x, dt, A, B, C, D, z, dt_bias, initial_state, lengths, dt_softplus, y, final_state, workspace, stream)
 PyObject* scan_fwd(Args a) {
     const Call c(a[0], "x", 3);
+    const OnStream on(c, a[14]);
     const ScanCall s = scan_call(c, THPVariable_Unpack(a[0]), a[2], a[3], false, truth(a[10]));
     const int64_t b = s.b, T = s.T, D = s.D, N = s.N, G = s.G;
     mamba2_scan_strides st;
@@ -369,13 +388,14 @@ PyObject* scan_fwd(Args a) {
     void* ws = c.space(a[13], mamba2_scan_workspace_size(&s.sh), hold, &bytes);
     check("mamba2_scan_fwd",
           mamba2_scan_fwd(&s.sh, &st, px, pt, (float*)pA, pB, pC, (float*)pD, pz, (float*)pb, (float*)pi, (int32_t*)pl,
-                          y.at, (float*)f.at, ws, bytes, c.stream(a[14])));
+                          y.at, (float*)f.at, ws, bytes, on.raw));
     return pair(y, f);
 }
 
 // (state, x, dt, A, B, C, D, z, dt_bias, dt_softplus, y, stream)
 PyObject* scan_step(Args a) {
     const Call c(a[1], "x", 2);
+    const OnStream on(c, a[11]);
     const ScanCall s = scan_call(c, THPVariable_Unpack(a[1]), a[3], a[4], true, truth(a[9]));
     const int64_t b = s.b, D = s.D, N = s.N, G = s.G;
     mamba2_scan_strides st;
@@ -391,13 +411,14 @@ PyObject* scan_step(Args a) {
     void* pb = c.dense(a[8], "dt_bias", at::kFloat, {D}, true);
     Out y = token_out(c, a[10], "y", {b, D}, st.y, 1);
     check("mamba2_scan_step", mamba2_scan_step(&s.sh, &st, (float*)ps, px, pt, (float*)pA, pB, pC, (float*)pD, pz,
-                                               (float*)pb, y.at, c.stream(a[11])));
+                                               (float*)pb, y.at, on.raw));
     return y.give();
 }
 
 // (x, dt, A, B, C, D, z, dt_bias, initial_state, dy, dfinal, lengths, dt_softplus, grads, workspace, stream)
 PyObject* scan_bwd(Args a) {
     const Call c(a[0], "x", 3);
+    const OnStream on(c, a[15]);
     const ScanCall s = scan_call(c, THPVariable_Unpack(a[0]), a[2], a[3], false, truth(a[12]));
     const int64_t b = s.b, T = s.T, D = s.D, N = s.N, G = s.G;
     mamba2_scan_strides st;
@@ -431,13 +452,14 @@ PyObject* scan_bwd(Args a) {
     check("mamba2_scan_bwd",
           mamba2_scan_bwd(&s.sh, &st, px, pt, (float*)pA, pB, pC, (float*)pD, pz, (float*)pb, (float*)pi, py, (float*)pf,
                           (int32_t*)pl, dx, ddt, (float*)dA, dB, dC, (float*)dD, dz, (float*)db, (float*)di, ws, bytes,
-                          c.stream(a[15])));
+                          on.raw));
     return g.give();
 }
 
 // ---- norm: (x, w, z, ngroups, eps, gate_first, y, stream)
 PyObject* norm_fwd(Args a) {
     const Call c(a[0], "x", 3);
+    const OnStream on(c, a[7]);
     const Tensor& x = THPVariable_Unpack(a[0]);
     const int64_t b = x.size(0), T = x.size(1), D = x.size(2);
     const mamba2_norm_shape sh{b, T, D, whole(a[3]), real(a[4]), c.dtype(), truth(a[5]) ? 0 : MAMBA2_NORM_GATE_AFTER};
@@ -447,13 +469,14 @@ PyObject* norm_fwd(Args a) {
     st.z[0] = st.z[1] = 0;
     void* pz = c.token(a[2], "z", {b, T, D}, st.z, 2, true);
     Out y = token_out(c, a[6], "y", {b, T, D}, st.y);
-    check("mamba2_norm_fwd", mamba2_norm_fwd(&sh, &st, px, (float*)pw, pz, y.at, c.stream(a[7])));
+    check("mamba2_norm_fwd", mamba2_norm_fwd(&sh, &st, px, (float*)pw, pz, y.at, on.raw));
     return y.give();
 }
 
 // (x, w, z, dy, ngroups, eps, gate_first, grads, workspace, stream)
 PyObject* norm_bwd(Args a) {
     const Call c(a[0], "x", 3);
+    const OnStream on(c, a[9]);
     const Tensor& x = THPVariable_Unpack(a[0]);
     const int64_t b = x.size(0), T = x.size(1), D = x.size(2);
     const mamba2_norm_shape sh{b, T, D, whole(a[4]), real(a[5]), c.dtype(), truth(a[6]) ? 0 : MAMBA2_NORM_GATE_AFTER};
@@ -471,7 +494,7 @@ PyObject* norm_bwd(Args a) {
     size_t bytes;
     void* ws = c.space(a[8], mamba2_norm_bwd_workspace_size(&sh), hold, &bytes);
     check("mamba2_norm_bwd", mamba2_norm_bwd(&sh, &st, px, (float*)pw, pz, py, dx, dz, (float*)dw, ws, bytes,
-                                             c.stream(a[9])));
+                                             on.raw));
     return g.give();
 }
 

@@ -88,6 +88,10 @@ bool scan_args(const mamba2_scan_shape* s, const mamba2_scan_strides* st, bool y
     a->b = s->batch, a->T = s->seqlen, a->D = s->channels, a->N = s->states, a->G = s->groups;
     if (a->D == 0) a->G = 1;
     a->dtype = s->dtype == MAMBA2_BF16, a->softplus = s->flags & MAMBA2_SCAN_SOFTPLUS;
+    if (s->groups > kMaxD / a->N) {   // a token's B and C: as wide as a token at most
+        *e = MAMBA2_ERR_UNSUPPORTED;
+        return false;
+    }
     const int64_t w = s->groups * a->N;
     if (!in_strides(st ? st->x : nullptr, a->T, a->D, &a->sx) ||
         !in_strides(st ? st->dt : nullptr, a->T, a->D, &a->sdt) ||

@@ -140,7 +140,8 @@ def test_scan_refusals(lib):
     ok = [P] * 12
     for bad in (dict(batch=-1), dict(groups=0), dict(groups=3), dict(states=0), dict(flags=4), dict(dtype=-1)):
         assert _status("scan_fwd", _scan(**bad), ok, space=True) == m2.ERR_INVALID_ARG
-    for bad in (dict(states=12), dict(states=256), dict(seqlen=1 << 31)):
+    for bad in (dict(states=12), dict(states=256), dict(seqlen=1 << 31),
+                dict(channels=1 << 24, groups=1 << 21, states=16)):
         assert _status("scan_fwd", _scan(**bad), ok, space=True) == m2.ERR_UNSUPPORTED
     for k in (0, 1, 2, 3, 4, 10, 11):
         assert _status("scan_fwd", _scan(), ok[:k] + [None] + ok[k + 1:], space=True) == m2.ERR_INVALID_ARG

@@ -347,6 +347,39 @@ def test_given_outputs_and_another_stream():
     assert torch.equal(y, want) and torch.equal(f2, fin) and (wide[:, :, 56:] == 7).all()
 
 
+def test_another_stream_allocates_for_itself():
+    """A call on a given stream takes its outputs and workspace from that stream's memory: work
+    queued on the current stream before and after it does not touch them."""
+    case = (1, 2500, 20, 16, 1, F32, True, True, True, True, True, False, 0)
+    v, _, r = scan_inputs(case, 16)
+    args = [cu(v[k]) for k in ORDER]
+    dy = cu(r.randn(1, 2500, 20))
+    want, fin = m2.scan_fwd(*args, dt_softplus=True)
+    grads = m2.scan_bwd(*args, dy, dt_softplus=True)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(8):
+        y, f = m2.scan_fwd(*args, dt_softplus=True, stream=side)
+        g = m2.scan_bwd(*args, dy, dt_softplus=True, stream=side)
+        torch.full((1 << 20,), NAN, device="cuda")          # would land in a workspace given back too early
+        side.synchronize()
+        assert torch.equal(y, want) and torch.equal(f, fin)
+        assert all(torch.equal(g[k], grads[k]) for k in g if g[k] is not None)
+        del y, f, g
+
+
+def test_lengths_out_of_range_are_clamped():
+    r = Gen(33)
+    x, w = cu(r.randn(3, 7, 8)), cu(r.randn(8, 4))
+    n, m = (torch.tensor(t, dtype=torch.int32, device="cuda") for t in ([-5, 100, 2 ** 31 - 1], [0, 7, 7]))
+    for a, b in zip(m2.conv_fwd(x, w, lengths=n), m2.conv_fwd(x, w, lengths=m)):
+        assert torch.equal(a, b)
+    A, B = -torch.rand(8, 16, device="cuda"), cu(r.randn(3, 7, 1, 16))
+    for a, b in zip(m2.scan_fwd(x, x, A, B, B, lengths=n, dt_softplus=True),
+                    m2.scan_fwd(x, x, A, B, B, lengths=m, dt_softplus=True)):
+        assert torch.equal(a, b)
+
+
 def test_steps_in_a_graph():
     """The single-token forms captured once and replayed token by token."""
     r = Gen(32)
