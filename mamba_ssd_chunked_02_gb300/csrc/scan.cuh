@@ -25,6 +25,13 @@ template <int N> struct Cfg {
     static constexpr int YF = TT * (LPC <= 4 ? LPC : 1) * YP;       // floats of the y tile
 };
 
+// Four neighbouring states of B or C from shared memory.
+__device__ __forceinline__ ulonglong2 states4(const float* p) { return *reinterpret_cast<const ulonglong2*>(p); }
+__device__ __forceinline__ ulonglong2 states4(const __nv_bfloat16* p) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    return ulonglong2{pack2(bf_lo(v.x), bf_hi(v.x)), pack2(bf_lo(v.y), bf_hi(v.y))};
+}
+
 // Blocks an SM the registers are kept to.  (Nine, 96 registers, is slower a block by a
 // sixth than eight.)
 template <typename TI, int N, int V> constexpr int min_blocks() {

@@ -61,12 +61,10 @@ scan_fwd_kernel(const FwdP p) {
     static_assert(IT >= 1 && RS * IT == TT && BI >= 1, "tile shape");
     extern __shared__ __align__(16) unsigned char smem[];
     float2* sP = reinterpret_cast<float2*>(smem);                               // [TT][CB] (d, dx)
-    float* sB = reinterpret_cast<float*>(smem + (size_t)TT * CB * 8);           // [TT][N]
-    float* sC = sB + TT * N;
     // y of a tile: with up to four lanes a channel, each lane's part [TT][LPC][YP] (added by
     // the epilogue: fewer instructions than lane exchanges); else the sums [TT][YP]
     constexpr bool PART = LPC <= 4;
-    float* sY = sC + TT * N;
+    float* sY = reinterpret_cast<float*>(smem + (size_t)TT * CB * 8);
     constexpr int ST = 3 * TT * CB + 2 * TT * N;                                // elements of a staged tile
     TI* sS = reinterpret_cast<TI*>(sY + K::YF);                               // [2] x, dt, z [TT][CB], B, C [TT][N]
     typedef typename Pack<TI, V>::Raw Raw;
@@ -210,25 +208,12 @@ scan_fwd_kernel(const FwdP p) {
             else
                 sP[r * CB + lc] = make_float2(d0, u0);
         }
-#pragma unroll
-        for (int i = 0; i < BI; ++i) {
-            const int e = (tid + i * NT) * V;
-            const TI* st = cur + 3 * TT * CB + e;
-            float f[V];
-            Conv<TI, V>::to(*reinterpret_cast<const Raw*>(st), f);
-#pragma unroll
-            for (int j = 0; j < V; ++j) sB[e + j] = f[j];
-            if (!STATES) {
-                Conv<TI, V>::to(*reinterpret_cast<const Raw*>(st + TT * N), f);
-#pragma unroll
-                for (int j = 0; j < V; ++j) sC[e + j] = f[j];
-            }
-        }
         __syncthreads();
         if (t0 + TT < s1) stage(t0 + TT, nxt);
         const float4* pP = reinterpret_cast<const float4*>(sP + ch);
-        const float* pB = sB + q * kNS;
-        const float* pC = sC + q * kNS;
+        // B and C as they were staged, in the tensors' type: every thread's copies have arrived
+        const TI* pB = cur + 3 * TT * CB + q * kNS;
+        const TI* pC = pB + TT * N;
         constexpr int UN = 16;   // tokens unrolled
 #pragma unroll 1
         for (int tb = 0; tb < TT; tb += UN) {
@@ -239,7 +224,7 @@ scan_fwd_kernel(const FwdP p) {
                 for (int u = 0; u < UT; ++u) {
                     const int t = tb + tu + u;
                     const float4 w = pP[t * (CB / 2)];
-                    const ulonglong2 Bv = *reinterpret_cast<const ulonglong2*>(pB + t * N);
+                    const ulonglong2 Bv = states4(pB + t * N);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const f2 d = dup2(j ? w.z : w.x), dx = dup2(j ? w.w : w.y);
@@ -248,7 +233,7 @@ scan_fwd_kernel(const FwdP p) {
                         if (STATES) dsum[j] += j ? w.z : w.x;
                     }
                     if (!STATES) {
-                        const ulonglong2 Cv = *reinterpret_cast<const ulonglong2*>(pC + t * N);
+                        const ulonglong2 Cv = states4(pC + t * N);
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
                             yp2[u][j] = fma2(h[j][1], Cv.y, mul2(h[j][0], Cv.x));
@@ -447,7 +432,7 @@ template <typename TI, int N, int V>
 cudaError_t fwd_v(const FwdP& p, int64_t slices, cudaStream_t st) {
     using K = Cfg<N>;
     const int64_t rows = p.b * p.G * p.ncb, blocks = rows * p.nseg * slices;
-    constexpr size_t smem = (size_t)K::TT * (K::CB * 8 + 2 * N * 4) + (size_t)K::YF * 4 +
+    constexpr size_t smem = (size_t)K::TT * K::CB * 8 + (size_t)K::YF * 4 +
                             2 * (size_t)K::TT * (3 * K::CB + 2 * N) * sizeof(TI);
     if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     auto k = scan_fwd_kernel<TI, N, V, false>;
