@@ -3,10 +3,17 @@
 //   s[t] = bias + sum_k w[k] x[t - (W - 1) + k]      y = s or s sigmoid(s)
 //
 // Bytes bound: forward x in, y out; backward x, dy in, dx out.  A thread owns V
-// neighbouring channels (16 bytes of a token in the forward) and walks a stretch
-// of tokens with the last W - 1 inputs in registers, so each input is read once
-// plus W - 1 tokens of overlap per stretch; neighbouring threads read neighbouring
-// bytes of one token's row.
+// neighbouring channels and walks a stretch of tokens with the last W - 1 inputs in
+// registers, so each input is read once plus W - 1 tokens of overlap per stretch;
+// neighbouring threads read neighbouring bytes of one token's row.  The tokens arrive
+// through a ring of asynchronous copies in shared memory, which keeps enough bytes in
+// flight without registers (forward 130 -> 114 us, backward 237 -> 195 us).
+//
+// b8 T4096 C5376 W4 bf16, x a column slice: forward 114 us (6.2 TB/s, 0.91 of the
+// measured copy rate), backward 195 us (5.4 TB/s, 0.79: the fp32 pipe at half, the
+// issue slots at 0.55).  Eight channels a thread 160 us, four 114 us; blocks of 128
+// threads 132 us, of 64 114 us (whole waves).  A step of 64 tokens takes 2.2 us on the
+// GPU, the launch.
 #include <algorithm>
 
 #include "internal.h"
@@ -41,8 +48,9 @@ __device__ __forceinline__ void load_w(const float* w, const float* bias, int64_
 }
 
 constexpr int kFwdThreads = 64;
-// Groups of four tokens in a thread's ring; none where an element is too small for an
-// asynchronous copy (single bf16 values).
+// Groups of four tokens in a thread's ring (four: 117 / 195 us forward / backward, six
+// 117 / 202, eight 154 / 214); none where an element is too small for an asynchronous
+// copy (single bf16 values).
 template <typename TI, int V> constexpr int ring() {
     return V * sizeof(TI) < 4 ? 0 : V * sizeof(TI) > 8 ? 3 : 4;
 }

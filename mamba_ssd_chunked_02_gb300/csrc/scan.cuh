@@ -7,11 +7,12 @@ namespace m2 {
 
 // Lanes and tiles.  A lane keeps kNS states of each of two neighbouring channels, and
 // N / kNS neighbouring lanes a pair of channels: shared memory hands 128 bytes a clock to
-// an SM's registers whether lanes read the same address or not, so B and C (16 bytes each
-// per token and lane) are used twice per load.  (One channel a lane: 12 bytes per state
-// update and the load unit the limit; this: 6.)  A block holds CB channels of one group and
-// one sequence and walks over tokens in tiles of TT; blocks are small, so that the large
-// cases' blocks divide evenly over the SMs.
+// an SM's registers whether lanes read the same address or not, so B and C (four states
+// each per token and lane) are used twice per load.  Measured on the forward, b8 T4096
+// C5120 N16 bf16: one channel a lane 1.40 ms (12 bytes per state update, the load unit the
+// limit), two 1.09 ms (6 bytes), four 1.09 ms where two had come to 0.85 (fewer warps, and
+// nothing to hide the latency of exponentials and loads).  A block holds CB channels of one
+// group and one sequence and walks over tokens in tiles of TT (32 tokens: 1.35 against 1.05 ms).
 constexpr int kNS = 4;
 template <int N> struct Cfg {
     static constexpr int NT = N >= 64 ? 128 : 64;
@@ -32,8 +33,8 @@ __device__ __forceinline__ ulonglong2 states4(const __nv_bfloat16* p) {
     return ulonglong2{pack2(bf_lo(v.x), bf_hi(v.x)), pack2(bf_lo(v.y), bf_hi(v.y))};
 }
 
-// Blocks an SM the registers are kept to.  (Nine, 96 registers, is slower a block by a
-// sixth than eight.)
+// Blocks an SM the registers are kept to.  (Nine, 96 registers, is slower by a sixth than
+// eight, 128: 0.24 against 0.20 ms for 16384 tokens of one sequence, C1280.)
 template <typename TI, int N, int V> constexpr int min_blocks() {
     return N >= 64 ? 4 : V == 2 && N >= 16 ? 8 : 6;
 }

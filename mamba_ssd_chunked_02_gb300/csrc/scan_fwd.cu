@@ -6,7 +6,14 @@
 //
 // Unlike the chunked scan's one decay per head, the decay differs for every (c, n),
 // so there is no matrix product to regroup: per (t, c, n) the pass needs one
-// exponential and four multiply-adds, and it is bound by those pipes, not by bytes.
+// exponential and four multiply-adds, and it is bound by those pipes and by the bytes
+// that shared memory hands to registers, not by memory: b8 T4096 C5120 N16 bf16 takes
+// 0.82 ms (1.65 TB/s; its bytes alone 0.20 ms, its exponentials 0.28 ms, its fp32
+// operations about 0.4 ms), with the load unit's data path at three quarters.
+//
+// A block turns a tile's dt and x into (d, d x) once, in fp32 in shared memory, then each
+// lane walks over the tile's tokens with its states in registers; the lanes' parts of y
+// meet in shared memory, and the epilogue adds them, the skip and the gate.
 #include <algorithm>
 
 #include "internal.h"
@@ -401,8 +408,8 @@ scan_step_kernel(float* __restrict__ state, const TI* __restrict__ x, const TI* 
 // nseg > 1: stretches side by side, for few rows; they cost a second pass (the first
 //   without y), so only where one pass leaves most of the GPU without warps.
 // slices > 1: rows in turns (see await_turn), for rows between one and a few waves of
-//   the blocks the GPU holds.  b8 C5120 N16 bf16 T4096 (1280 rows, 1216 held): 8 slices
-//   against one: see the kernel's figures.
+//   the blocks the GPU holds.  b8 T4096 C5120 N16 bf16 (1280 rows, 1216 held): one slice
+//   1.12 ms (0.99 with nine blocks an SM), 4 slices 0.87, 8 slices 0.86, 16 slices 0.88.
 struct Cut {
     int64_t nseg, slices, SL;
 };
