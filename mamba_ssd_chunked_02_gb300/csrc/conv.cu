@@ -7,11 +7,11 @@
 // registers, so each input is read once plus W - 1 tokens of overlap per stretch;
 // neighbouring threads read neighbouring bytes of one token's row.  The tokens arrive
 // through a ring of asynchronous copies in shared memory, which keeps enough bytes in
-// flight without registers (forward 130 -> 114 us, backward 237 -> 195 us).
+// flight without registers (forward 130 -> 114 us, backward 237 -> 195 us when it came).
 //
 // b8 T4096 C5376 W4 bf16, x a column slice: forward 114 us (6.2 TB/s, 0.91 of the
-// measured copy rate), backward 195 us (5.4 TB/s, 0.79: the fp32 pipe at half, the
-// issue slots at 0.55).  Eight channels a thread 160 us, four 114 us; blocks of 128
+// measured copy rate), backward 187 us (5.7 TB/s, 0.83; with registers for four blocks
+// an SM instead of three 196 us: the fp32 pipe at half, the issue slots at 0.55).  Eight channels a thread 160 us, four 114 us; blocks of 128
 // threads 132 us, of 64 114 us (whole waves).  A step of 64 tokens takes 2.2 us on the
 // GPU, the launch.
 #include <algorithm>
@@ -197,7 +197,7 @@ conv_step_kernel(TI* __restrict__ state, const TI* __restrict__ x, const float* 
 constexpr int kBwdTX = 32, kBwdTY = 4;
 
 template <typename TI, int V, int W, bool SILU>
-__global__ void __launch_bounds__(kBwdTX * kBwdTY)
+__global__ void __launch_bounds__(kBwdTX * kBwdTY, 3)
 conv_bwd_kernel(const TI* __restrict__ x, const float* __restrict__ w,
                 const float* __restrict__ bias, const TI* __restrict__ init,
                 const TI* __restrict__ dy, const TI* __restrict__ dfin,
@@ -414,7 +414,7 @@ int pick_ts(int64_t lanes, int64_t T, int start, int resident) {
 int bwd_vec(const ConvArgs& a) { return a.D % 4 == 0 ? 4 : a.dtype == 1 && a.D % 2 == 0 ? 2 : 1; }
 int bwd_ts(const ConvArgs& a) {
     const int64_t lanes = (a.D + bwd_vec(a) - 1) / bwd_vec(a);
-    return pick_ts(a.b * lanes, a.T, 40, 512);
+    return pick_ts(a.b * lanes, a.T, 40, 384);
 }
 int64_t bwd_blocks(const ConvArgs& a) {
     const int64_t per = (int64_t)bwd_ts(a) * kBwdTY;

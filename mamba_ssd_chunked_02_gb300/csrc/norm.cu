@@ -8,7 +8,7 @@
 //   gate first: dx = dv silu(z), dz = dv x silu'(z);  after: dx = dv, dz = dy v r w silu'(z)
 //
 // Bytes bound (b8 T4096 C5120 bf16: forward 159 us, 6.3 TB/s, 0.93 of the measured copy
-// rate; backward in groups of 640 312 us, 5.4 TB/s, 0.79, its issue slots at 0.62; one
+// rate; backward in groups of 640 298 us, 5.6 TB/s, 0.83, its issue slots at 0.6; one
 // token of 64 sequences 2.6 us on the GPU): every tensor moves once.  A team (a warp for groups that fit its
 // registers, else a block) holds a group's row in registers between the sums and
 // the result; the backward's two sums need one pass (mean(q v) does not need r).
@@ -160,10 +160,14 @@ norm_fwd_kernel(const TI* __restrict__ x, const float* __restrict__ w, const TI*
     }
 }
 
+// Warps an SM of the backward's warp teams: four blocks, or five where the registers of a
+// lane's `each` channels allow it.
+constexpr int bwd_warps(int each) { return each > 20 ? 16 : 20; }
+
 // Team `team` of `teams` (a multiple of G) has group team % G and tokens team / G,
 // + teams / G, ...; its dw goes to slot team / G of part ([slots][D]).
 template <typename TI, int V, int VPT, int GATE, bool WARP>
-__global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : 1024, WARP ? 4 : 1)
+__global__ void __launch_bounds__(WARP ? kWarpTeams * 32 : 1024, WARP ? bwd_warps(VPT * V) / kWarpTeams : 1)
 norm_bwd_kernel(const TI* __restrict__ x, const float* __restrict__ w, const TI* __restrict__ z,
                 const TI* __restrict__ dy, TI* __restrict__ dx, TI* __restrict__ dz,
                 float* __restrict__ part, int teams, Rows q) {
@@ -369,13 +373,15 @@ int team_threads(int64_t nv, int vpt) {
     return (int)std::min<int64_t>(1024, std::max<int64_t>(1, (nv + vpt * 32 - 1) / (vpt * 32)) * 32);
 }
 
-// Backward slots of dw: as many teams as an SM holds at once (16 warps, or blocks of 1024
+// Backward slots of dw: as many teams as an SM holds at once (16 or 20 warps, or blocks of 1024
 // threads in all), each with an equal share of the tokens, over the groups.
 int64_t bwd_team_slots(const NormArgs& a) {
     const int64_t S = a.D / a.G, full = a.dtype == 1 ? 8 : 4;
-    const int64_t V = S % full == 0 ? full : a.dtype != 1 ? 1 : S % 4 == 0 ? 4 : S % 2 == 0 ? 2 : 1, nv = S / V;
-    const int64_t per_sm =
-        nv <= 96 ? 16 : std::max<int64_t>(1, 1024 / team_threads(nv, V <= 2 ? 4 : nv <= 1024 ? 1 : 2));
+    const int64_t V = S % full == 0 && !(full == 8 && S > 512 && S <= 640) ? full : a.dtype != 1 ? 1 : S % 4 == 0 ? 4 : S % 2 == 0 ? 2 : 1;
+    const int64_t nv = S / V, each = (nv + 31) / 32 * V;
+    const int64_t per_sm = nv <= 96 || (V == 4 && nv <= 160)
+                               ? bwd_warps((int)each)
+                               : std::max<int64_t>(1, 1024 / team_threads(nv, V <= 2 ? 4 : nv <= 1024 ? 1 : 2));
     const int64_t teams = (int64_t)sm_count() * per_sm;
     return std::max<int64_t>(1, std::min<int64_t>(a.b * a.T, teams / a.G));
 }
@@ -421,6 +427,8 @@ cudaError_t bwd_go(const NormArgs& a, const TI* x, const float* w, const TI* z, 
     if (nv <= 32) e = go(norm_bwd_kernel<TI, V, 1, GATE, true>, wb, kWarpTeams * 32, 1);
     else if (nv <= 64) e = go(norm_bwd_kernel<TI, V, 2, GATE, true>, wb, kWarpTeams * 32, 2);
     else if (nv <= 96) e = go(norm_bwd_kernel<TI, V, 3, GATE, true>, wb, kWarpTeams * 32, 3);
+    else if (V == 4 && nv <= 160)
+        e = go(norm_bwd_kernel<TI, V, V == 4 ? 5 : 1, GATE, true>, wb, kWarpTeams * 32, 5);
     else if (V <= 2 && nv <= 4096)
         e = go(norm_bwd_kernel<TI, V, V <= 2 ? 4 : 1, GATE, false>, bb, team_threads(nv, 4), 4);
     else if (nv <= 1024) e = go(norm_bwd_kernel<TI, V, 1, GATE, false>, bb, team_threads(nv, 1), 1);
@@ -450,13 +458,16 @@ cudaError_t bwd_gate(const NormArgs& a, const void* x, const float* w, const voi
 
 // Channels an access: the most of 16, 8 and 4 bytes at which every tensor's rows and the
 // groups are aligned, else one.
-int vec_of(const NormArgs& a, const void* x, const float* w, const void* z, const void* y, const void* o1,
-           const void* o2) {
+int vec_of(const NormArgs& a, bool back, const void* x, const float* w, const void* z, const void* y,
+           const void* o1, const void* o2) {
     const int64_t es = a.dtype == 1 ? 2 : 4;
     const Tok row{0, a.D};
     for (int V : {8, 4, 2}) {
         if (a.dtype != 1 && V != 4) continue;
         const int64_t by = V * es;
+        // 513 to 640 channels: five rounds of four a lane instead of three of eight, the last of
+        // them half idle (backward, groups of 640: 298 against 312 us)
+        if (back && V == 8 && a.D / a.G > 512 && a.D / a.G <= 640) continue;
         if ((a.D / a.G) % V == 0 && reinterpret_cast<uintptr_t>(w) % (V > 2 ? 16 : 8) == 0 && vec_ok(x, a.sx, by, es) &&
             (!z || vec_ok(z, a.sz, by, es)) && vec_ok(y, a.sy, by, es) && vec_ok(o1, row, by, es) &&
             vec_ok(o2, row, by, es))
@@ -470,7 +481,7 @@ int vec_of(const NormArgs& a, const void* x, const float* w, const void* z, cons
 cudaError_t launch_norm_fwd(const NormArgs& a, const void* x, const float* w, const void* z, void* y,
                             cudaStream_t st) {
     if (a.b * a.T == 0 || a.D == 0) return cudaSuccess;
-    const int V = vec_of(a, x, w, z, y, nullptr, nullptr);
+    const int V = vec_of(a, false, x, w, z, y, nullptr, nullptr);
     if (a.dtype != 1) return V == 4 ? fwd_gate<float, 4>(a, x, w, z, y, st) : fwd_gate<float, 1>(a, x, w, z, y, st);
     return V == 8   ? fwd_gate<__nv_bfloat16, 8>(a, x, w, z, y, st)
            : V == 4 ? fwd_gate<__nv_bfloat16, 4>(a, x, w, z, y, st)
@@ -488,7 +499,7 @@ cudaError_t launch_norm_bwd(const NormArgs& a, const void* x, const float* w, co
     if (!dw) part = nullptr;
     const bool none = a.b * a.T == 0;
     if (!none) {
-        const int V = vec_of(a, x, w, z, dy, dx, dz);
+        const int V = vec_of(a, true, x, w, z, dy, dx, dz);
         if (a.dtype != 1)
             e = V == 4 ? bwd_gate<float, 4>(a, x, w, z, dy, dx, dz, part, st)
                        : bwd_gate<float, 1>(a, x, w, z, dy, dx, dz, part, st);
