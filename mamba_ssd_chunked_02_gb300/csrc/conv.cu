@@ -10,10 +10,10 @@
 // flight without registers (forward 130 -> 114 us, backward 237 -> 195 us when it came).
 //
 // b8 T4096 C5376 W4 bf16, x a column slice: forward 114 us (6.2 TB/s, 0.91 of the
-// measured copy rate), backward 187 us (5.7 TB/s, 0.83; with registers for four blocks
-// an SM instead of three 196 us: the fp32 pipe at half, the issue slots at 0.55).  Eight channels a thread 160 us, four 114 us; blocks of 128
-// threads 132 us, of 64 114 us (whole waves).  A step of 64 tokens takes 2.2 us on the
-// GPU, the launch.
+// measured copy rate), backward 185 us (5.7 TB/s, 0.84; 196 us with registers for four
+// blocks an SM instead of three: the fp32 pipe at half, the issue slots at 0.55).  The
+// forward with eight channels a thread 160 us, with blocks of 128 threads instead of
+// 64 132 us (whole waves).  A step of 64 tokens takes 2.2 us on the GPU, the launch.
 #include <algorithm>
 
 #include "internal.h"

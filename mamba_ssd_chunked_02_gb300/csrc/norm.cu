@@ -7,13 +7,14 @@
 //   dv = r q - v r^3 mean(q v);   dw = sum over tokens of dy (..) v r
 //   gate first: dx = dv silu(z), dz = dv x silu'(z);  after: dx = dv, dz = dy v r w silu'(z)
 //
-// Bytes bound (b8 T4096 C5120 bf16: forward 159 us, 6.3 TB/s, 0.93 of the measured copy
-// rate; backward in groups of 640 298 us, 5.6 TB/s, 0.83, its issue slots at 0.6; one
-// token of 64 sequences 2.6 us on the GPU): every tensor moves once.  A team (a warp for groups that fit its
-// registers, else a block) holds a group's row in registers between the sums and
-// the result; the backward's two sums need one pass (mean(q v) does not need r).
-// A backward team keeps its group and walks over tokens, so that its part of dw
-// stays in registers; the parts are summed by a second kernel, in a fixed order.
+// Bytes bound: every tensor moves once.  b8 T4096 C5120 bf16: forward 159 us (6.3 TB/s,
+// 0.93 of the measured copy rate), backward in groups of 640 295 us (5.7 TB/s, 0.84, its
+// issue slots at 0.6); one token of 64 sequences 2.5 us on the GPU, the launch.
+//
+// A team (a warp for groups that fit its registers, else a block) holds a group's row in
+// registers between the sums and the result; the backward's two sums need one pass (mean(q v)
+// does not need r).  A backward team keeps its group and walks over tokens, so that its part of
+// dw stays in registers; the parts are summed by a second kernel, in a fixed order.
 #include <algorithm>
 
 #include "internal.h"
