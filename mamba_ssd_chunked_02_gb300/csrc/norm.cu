@@ -263,7 +263,7 @@ norm_bwd_kernel(const TI* __restrict__ x, const float* __restrict__ w, const TI*
                 const f2 n = mul2(v, r);
                 if (GATE == kAfter) az[i] = mul2(mul2(d[i], n), mul2(fw[i], slope));
                 if (GATE == kAfter) d[i] = mul2(d[i], gate);
-                const f2 dv = fma2(r, mul2(d[i], fw[i]), mul2(v, m));   // m < 0: see below
+                const f2 dv = fma2(r, mul2(d[i], fw[i]), mul2(n, m));
                 p[i] = fma2(d[i], n, p[i]);
                 ax[i] = GATE == kFirst ? mul2(dv, gate) : dv;
                 if (GATE == kFirst) az[i] = mul2(mul2(dv, fx[i]), slope);
@@ -278,7 +278,7 @@ norm_bwd_kernel(const TI* __restrict__ x, const float* __restrict__ w, const TI*
             parity ^= 1;
             const float r = rsqrtf(s.x * inv + q.eps);
             r2 = dup2(r);
-            m2 = dup2(-r * r * r * (s.y * inv));   // dv = r q - v r^3 mean(q v)
+            m2 = dup2(-r * (r * (s.y * inv)));   // dv = r q - (v r) r (r mean(q v)): no r^3 to underflow
         };
         if constexpr (VPT > 0) {
             f2 sg[K][H];

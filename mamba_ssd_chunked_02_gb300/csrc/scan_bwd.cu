@@ -128,6 +128,8 @@ cudaError_t launch_scan_bwd(const ScanArgs& a, const void* x, const void* dt, co
                        : cudaMemsetAsync(g.dinit, 0, states, st);
         return e;
     }
+    const int64_t rows = a.b * a.T * a.G, blocks = (rows * 2 * a.N + 255) / 256;
+    if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;   // before the first launch
     const Plan pl = plan_of(a);
     char* w = static_cast<char*>(ws);
     BwdP p = {};
@@ -145,8 +147,6 @@ cudaError_t launch_scan_bwd(const ScanArgs& a, const void* x, const void* dt, co
     p.sx = a.sx, p.sdt = a.sdt, p.sB = a.sB, p.sC = a.sC, p.sz = a.sz, p.sy = a.sy;
     cudaError_t e = a.dtype == 1 ? scan_bwd_bf16(a, p, pl.KK, init, dfinal, st) : scan_bwd_f32(a, p, pl.KK, init, dfinal, st);
     if (e != cudaSuccess) return e;
-    const int64_t rows = a.b * a.T * a.G, blocks = (rows * 2 * a.N + 255) / 256;
-    if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     if (a.dtype == 1)
         scan_bc_sum_kernel<<<(unsigned)blocks, 256, 0, st>>>(p.part_bc, p.ncb, rows, (int)a.N,
                                                             static_cast<__nv_bfloat16*>(g.dB),

@@ -324,6 +324,10 @@ def test_norm_rows_of_zeros_and_large_values():
     assert not y[0, 0].any()
     close(y[0, 1], torch.ones(64), "large")
     assert torch.isfinite(y).all()
+    r = Gen(22)
+    big, dy = r.randn(1, 2, 64) * 1e15, r.randn(1, 2, 64)      # 1 / sqrt(..) cubed underflows
+    g, want = m2.norm_bwd(cu(big), None, None, cu(dy)), R.norm(f64(big), None, None, 1, 1e-5, True, f64(dy))
+    close(g["dx"] * 1e15, want["dx"] * 1e15, "dx of large values")
 
 
 # ---- streams, outputs given, refusals -----------------------------------------------------------
