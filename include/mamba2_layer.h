@@ -114,8 +114,10 @@ typedef struct mamba2_scan_strides {
  * shape) bytes (may be 0), 16-byte aligned, contents ignored on entry: with few rows
  * the states between the stretches of tokens that run side by side; with more rows
  * than the GPU holds at once, which then take turns in slices of the token axis, one
- * word a row (a slice waits for the slice before it, at most two seconds: a wait that
- * runs out sets MAMBA2_DEVERR_CHAIN_SCAN in the word of mamba2_ssd_device_error). */
+ * word a row (a slice waits for the slice before it, at most two seconds).  A wait that
+ * runs out sets MAMBA2_DEVERR_CHAIN_SCAN in the word of mamba2_ssd_device_error and gives
+ * the row up: its slices from there on leave at once, y is not written there, and
+ * final_state is not the row's last state. */
 MAMBA2_API size_t mamba2_scan_workspace_size(const mamba2_scan_shape* shape);
 MAMBA2_API mamba2_status mamba2_scan_fwd(const mamba2_scan_shape* shape,
                                          const mamba2_scan_strides* strides,
@@ -125,6 +127,20 @@ MAMBA2_API mamba2_status mamba2_scan_fwd(const mamba2_scan_shape* shape,
                                          const float* initial_state, const int32_t* lengths,
                                          void* y, float* final_state,
                                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* Diagnostic: the failure path of the wait described above, without a fault.  Runs
+ * mamba2_scan_fwd on contiguous tensors with the first slice of tokens launched after all
+ * the others, whose waits run out after `limit_us` microseconds (1 .. 100000).  All
+ * launches return normally and the context stays usable; afterwards
+ * MAMBA2_DEVERR_CHAIN_SCAN is set, y holds the first slice only, and the workspace's word
+ * of every row is -1 (given up; the late first slice does not take that back).  Returns
+ * MAMBA2_ERR_UNSUPPORTED for a shape whose rows do not take turns. */
+MAMBA2_API mamba2_status mamba2_scan_selftest_turn_timeout(const mamba2_scan_shape* shape,
+                                                           const void* x, const void* dt, const float* A,
+                                                           const void* B, const void* C, void* y,
+                                                           float* final_state, void* workspace,
+                                                           size_t workspace_bytes, uint32_t limit_us,
+                                                           void* stream);
 
 /* One token per sequence (seqlen 1): state [b,D,N] fp32 updated in place; x, dt,
  * z, y [b,D] and B, C [b,G,N] io (strides: the batch entries). */

@@ -16,7 +16,7 @@ Entry points (same names as the C ABI, minus the ``mamba2_ssd_`` prefix):
 Around the scan in a layer (module layer, C ABI in include/mamba2_layer.h):
   conv_fwd, conv_bwd, conv_step (short causal convolution), scan_fwd, scan_bwd,
   scan_step (selective scan with a decay per channel and state), norm_fwd,
-  norm_bwd (gated group norm).
+  norm_bwd (gated group norm); scan_selftest_turn_timeout.
 
 Pages: "NVIDIA CUDA Tile로 Mamba-2 순방향 전달 커널 가속화" (devin.kr),
 "Mamba-2 아키텍처의 핵심 연산" (y_t = c_t^T h_t + D x_t) and "세 가지 핵심 커널
@@ -531,4 +531,5 @@ def device_error(clear=True) -> int:
 
 
 from .layer import (conv_bwd, conv_fwd, conv_step, norm_bwd, norm_fwd, scan_bwd,  # noqa: E402,F401
-                    scan_bwd_workspace_size, scan_fwd, scan_step, scan_workspace_size)
+                    scan_bwd_workspace_size, scan_fwd, scan_selftest_turn_timeout, scan_step,
+                    scan_workspace_size)

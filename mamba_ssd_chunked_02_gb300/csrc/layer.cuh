@@ -275,10 +275,14 @@ struct ScanArgs {
     Tok sx, sdt, sB, sC, sz, sy;
 };
 size_t scan_fwd_workspace(const ScanArgs& a);
+bool scan_fwd_turns(const ScanArgs& a);   // rows take turns over slices of the token axis
+// starve_ns: for a shape that takes turns, the first slice is launched behind the others,
+// whose waits run out after that time (0: the ordinary call).
 cudaError_t launch_scan_fwd(const ScanArgs& a, const void* x, const void* dt, const float* A,
                             const void* B, const void* C, const float* D, const void* z,
                             const float* dt_bias, const float* init, const int32_t* lengths,
-                            void* y, float* final_state, void* ws, cudaStream_t st);
+                            void* y, float* final_state, void* ws, cudaStream_t st,
+                            uint64_t starve_ns = 0);
 cudaError_t launch_scan_step(const ScanArgs& a, float* state, const void* x, const void* dt,
                              const float* A, const void* B, const void* C, const float* D,
                              const void* z, const float* dt_bias, void* y, cudaStream_t st);

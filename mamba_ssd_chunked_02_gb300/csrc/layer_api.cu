@@ -204,6 +204,24 @@ mamba2_status mamba2_scan_fwd(const mamba2_scan_shape* shape, const mamba2_scan_
                                          workspace, static_cast<cudaStream_t>(stream)));
 }
 
+mamba2_status mamba2_scan_selftest_turn_timeout(const mamba2_scan_shape* shape, const void* x, const void* dt,
+                                                const float* A, const void* B, const void* C, void* y,
+                                                float* final_state, void* workspace, size_t workspace_bytes,
+                                                uint32_t limit_us, void* stream) {
+    m2::ScanArgs a;
+    mamba2_status e;
+    if (!scan_args(shape, nullptr, true, &a, &e)) return e;
+    if (limit_us < 1 || limit_us > 100000) return MAMBA2_ERR_INVALID_ARG;
+    if (!m2::scan_fwd_turns(a)) return MAMBA2_ERR_UNSUPPORTED;
+    const int64_t es = a.dtype ? 2 : 4;
+    if (!req(x, 1, es) || !req(dt, 1, es) || !req(A, 1, 4) || !req(B, 1, es) || !req(C, 1, es) || !req(y, 1, es) ||
+        !req(final_state, 1, 4))
+        return MAMBA2_ERR_INVALID_ARG;
+    if (!space(workspace, workspace_bytes, m2::scan_fwd_workspace(a))) return MAMBA2_ERR_WORKSPACE;
+    return from_cuda(m2::launch_scan_fwd(a, x, dt, A, B, C, nullptr, nullptr, nullptr, nullptr, nullptr, y, final_state,
+                                         workspace, static_cast<cudaStream_t>(stream), (uint64_t)limit_us * 1000));
+}
+
 mamba2_status mamba2_scan_step(const mamba2_scan_shape* shape, const mamba2_scan_strides* strides, float* state,
                                const void* x, const void* dt, const float* A, const void* B, const void* C,
                                const float* D, const void* z, const float* dt_bias, void* y, void* stream) {

@@ -33,6 +33,8 @@ struct FwdP {
     float* seg_d;     // [nseg][b][D]: sums of d
     int32_t* turns;   // slices: [rows] slices done of each row (-1: given up), then the ticket; or null
     int32_t* err;
+    uint64_t turn_ns; // longest wait for a turn
+    int slices, first;   // slices of the token axis, ticket of the first block
     int T, Dch, G, Dg, ncb, nseg, SL, softplus;
     int64_t b;
     Tok sx, sdt, sB, sC, sz, sy;
@@ -42,12 +44,13 @@ struct FwdP {
 // once would take two waves.  They take turns instead: the token axis is cut into
 // slices, and blocks take (slice, row) in slice order from a ticket, so that a block
 // only waits for one that started before it.  The state passes through final_state.
+// A wait that runs out marks the row -1 for good: its later slices leave at once.
 constexpr uint64_t kTurnNs = 2000000000ull;   // 2 s: far beyond any legitimate wait
-__device__ bool await_turn(const int32_t* done, int slice) {
+__device__ bool await_turn(const int32_t* done, int slice, uint64_t limit_ns) {
     int v = tc::ld_acquire_gpu(done);
     const uint64_t t0 = tc::globaltimer();
     while (v >= 0 && v < slice) {
-        if (tc::globaltimer() - t0 > kTurnNs) return false;
+        if (tc::globaltimer() - t0 > limit_ns) return false;
         __nanosleep(100);
         v = tc::ld_acquire_gpu(done);
     }
@@ -78,12 +81,11 @@ scan_fwd_kernel(const FwdP p) {
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     __shared__ int s_turn, s_go;
-    int id = blockIdx.x, slice = 0, slices = 1;
+    int id = blockIdx.x, slice = 0;
     int32_t* done = nullptr;
     if (!STATES && p.turns) {
         const int rows = p.ncb * p.G * (int)p.b;
-        slices = gridDim.x / rows;
-        if (tid == 0) s_turn = atomicAdd(p.turns + rows, 1);
+        if (tid == 0) s_turn = p.first + atomicAdd(p.turns + rows, 1);
         __syncthreads();
         slice = s_turn / rows;
         id = s_turn - slice * rows;
@@ -161,7 +163,7 @@ scan_fwd_kernel(const FwdP p) {
     stage(s0, cur);
     f2 A2[2][2], h[2][2];
     if (slice > 0) {   // the copies of the first tile are under way meanwhile
-        if (tid == 0) s_go = await_turn(done, slice);
+        if (tid == 0) s_go = await_turn(done, slice, p.turn_ns);
         __syncthreads();
         if (!s_go) {
             if (tid == 0) {
@@ -315,10 +317,10 @@ scan_fwd_kernel(const FwdP p) {
             f[3] = v.w;
         }
     }
-    if (slice + 1 < slices) {
+    if (done && slice + 1 < p.slices) {
         __threadfence();
         __syncthreads();
-        if (tid == 0) tc::st_release_gpu(done, slice + 1);
+        if (tid == 0) tc::cas_release_gpu(done, slice, slice + 1);   // not over the mark of a row given up
     }
 }
 
@@ -436,9 +438,9 @@ Cut cut_of(const ScanArgs& a) {
 }
 
 template <typename TI, int N, int V>
-cudaError_t fwd_v(const FwdP& p, int64_t slices, cudaStream_t st) {
+cudaError_t fwd_v(const FwdP& p, bool starve, cudaStream_t st) {
     using K = Cfg<N>;
-    const int64_t rows = p.b * p.G * p.ncb, blocks = rows * p.nseg * slices;
+    const int64_t rows = p.b * p.G * p.ncb, blocks = rows * p.nseg * p.slices;
     constexpr size_t smem = (size_t)K::TT * K::CB * 8 + (size_t)K::YF * 4 +
                             2 * (size_t)K::TT * (3 * K::CB + 2 * N) * sizeof(TI);
     if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
@@ -460,20 +462,31 @@ cudaError_t fwd_v(const FwdP& p, int64_t slices, cudaStream_t st) {
         scan_join_kernel<<<(unsigned)((total + 255) / 256), 256, 0, st>>>(p.seg_h, p.seg_d, p.A, p.init, total,
                                                                          (int64_t)p.Dch * N, N, p.nseg);
     }
+    if (starve) {   // all slices but the first, then the first
+        FwdP later = p;
+        later.first = (int)rows;
+        k<<<(unsigned)(blocks - rows), K::NT, smem, st>>>(later);
+        const cudaError_t e = cudaMemsetAsync(p.turns + rows, 0, sizeof(int32_t), st);
+        if (e != cudaSuccess) return e;
+        k<<<(unsigned)rows, K::NT, smem, st>>>(p);
+        return cudaGetLastError();
+    }
     k<<<(unsigned)blocks, K::NT, smem, st>>>(p);
     return cudaGetLastError();
 }
 
-template <typename TI, int N> cudaError_t fwd_n(const ScanArgs& a, FwdP p, int64_t slices, cudaStream_t st) {
+template <typename TI, int N> cudaError_t fwd_n(const ScanArgs& a, FwdP p, bool starve, cudaStream_t st) {
     p.ncb = (int)((p.Dg + Cfg<N>::CB - 1) / Cfg<N>::CB);
     const int64_t es = sizeof(TI), by = 2 * es;
     const bool two = p.Dg % 2 == 0 && vec_ok(p.x, a.sx, by, es) && vec_ok(p.dt, a.sdt, by, es) &&
                      vec_ok(p.B, a.sB, by, es) && vec_ok(p.C, a.sC, by, es) &&
                      (!p.z || vec_ok(p.z, a.sz, by, es)) && vec_ok(p.y, a.sy, by, es);
-    return two ? fwd_v<TI, N, 2>(p, slices, st) : fwd_v<TI, N, 1>(p, slices, st);
+    return two ? fwd_v<TI, N, 2>(p, starve, st) : fwd_v<TI, N, 1>(p, starve, st);
 }
 
 }  // namespace
+
+bool scan_fwd_turns(const ScanArgs& a) { return a.b * a.T * a.D && cut_of(a).slices > 1; }
 
 size_t scan_fwd_workspace(const ScanArgs& a) {
     if (a.b * a.T * a.D == 0) return 0;
@@ -485,7 +498,7 @@ size_t scan_fwd_workspace(const ScanArgs& a) {
 cudaError_t launch_scan_fwd(const ScanArgs& a, const void* x, const void* dt, const float* A, const void* B,
                             const void* C, const float* D, const void* z, const float* dt_bias,
                             const float* init, const int32_t* lengths, void* y, float* fin, void* ws,
-                            cudaStream_t st) {
+                            cudaStream_t st, uint64_t starve_ns) {
     if (a.b == 0 || a.D == 0) return cudaSuccess;
     if (a.T == 0) {
         const size_t bytes = sizeof(float) * (size_t)(a.b * a.D * a.N);
@@ -502,8 +515,9 @@ cudaError_t launch_scan_fwd(const ScanArgs& a, const void* x, const void* dt, co
     p.seg_d = cut.nseg > 1 ? p.seg_h + cut.nseg * a.b * a.D * a.N : nullptr;
     p.turns = cut.slices > 1 ? static_cast<int32_t*>(ws) : nullptr;
     p.err = device_error_word();
+    p.turn_ns = starve_ns ? starve_ns : kTurnNs, p.slices = (int)cut.slices, p.first = 0;
     p.sx = a.sx, p.sdt = a.sdt, p.sB = a.sB, p.sC = a.sC, p.sz = a.sz, p.sy = a.sy;
-    auto go = [&](auto f16, auto f32) { return a.dtype == 1 ? f16(a, p, cut.slices, st) : f32(a, p, cut.slices, st); };
+    auto go = [&](auto f16, auto f32) { return a.dtype == 1 ? f16(a, p, starve_ns != 0, st) : f32(a, p, starve_ns != 0, st); };
     switch (a.N) {
         case 8: return go(fwd_n<__nv_bfloat16, 8>, fwd_n<float, 8>);
         case 16: return go(fwd_n<__nv_bfloat16, 16>, fwd_n<float, 16>);

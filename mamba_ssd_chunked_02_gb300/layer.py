@@ -28,8 +28,8 @@ NORM_GATE_AFTER = 1
 # Symbols of include/mamba2_layer.h (checked by the CPU test suite).
 SYMBOLS = ("mamba2_conv_fwd", "mamba2_conv_step", "mamba2_conv_bwd", "mamba2_conv_bwd_workspace_size",
            "mamba2_scan_fwd", "mamba2_scan_step", "mamba2_scan_bwd", "mamba2_scan_workspace_size",
-           "mamba2_scan_bwd_workspace_size", "mamba2_norm_fwd", "mamba2_norm_bwd",
-           "mamba2_norm_bwd_workspace_size")
+           "mamba2_scan_bwd_workspace_size", "mamba2_scan_selftest_turn_timeout", "mamba2_norm_fwd",
+           "mamba2_norm_bwd", "mamba2_norm_bwd_workspace_size")
 
 _i64, _i32 = ctypes.c_int64, ctypes.c_int32
 
@@ -73,6 +73,10 @@ def _bind():
         f.argtypes = [vp]
         f.restype = sz
         _fns[name + "_ws"] = f
+    f = lib.mamba2_scan_selftest_turn_timeout
+    f.argtypes = [vp] * 9 + [sz, ctypes.c_uint32, vp]
+    f.restype = ctypes.c_int
+    _fns["scan_selftest"] = f
     return _fns
 
 
@@ -143,6 +147,21 @@ def scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, initial_state=None, l
     [b,D,N] f32 or None; N in {8, 16, 32, 64, 128}."""
     return (_ext_module or _load_ext()).scan_fwd(x, dt, A, B, C, D, z, dt_bias, initial_state, lengths, dt_softplus,
                                                  y, final_state, workspace, stream)
+
+
+def scan_selftest_turn_timeout(x, dt, A, B, C, y, final_state, workspace, *, limit_us=2000, stream=None):
+    """The failure path of scan_fwd's wait (mamba2_scan_selftest_turn_timeout): tensors as scan_fwd
+    takes them, contiguous, of a shape whose rows take turns.  Sets DEVERR_CHAIN_SCAN."""
+    from torch import float32 as f32
+
+    from . import _check, _dtype_code, _ptr, _stream
+    (b, T, D), (G, N), io = x.shape, B.shape[2:], x.dtype
+    sh = ScanShape(b, T, D, N, G, _dtype_code(io), 0)
+    space = _ptr(workspace, "workspace", workspace.dtype, workspace.shape)
+    _check("mamba2_scan_selftest_turn_timeout", _fn("scan_selftest")(
+        ctypes.addressof(sh), _ptr(x, "x", io, (b, T, D)), _ptr(dt, "dt", io, (b, T, D)), _ptr(A, "A", f32, (D, N)),
+        _ptr(B, "B", io, (b, T, G, N)), _ptr(C, "C", io, (b, T, G, N)), _ptr(y, "y", io, (b, T, D)),
+        _ptr(final_state, "final_state", f32, (b, D, N)), space, workspace.nbytes, int(limit_us), _stream(stream)))
 
 
 def scan_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, *, dt_softplus=False, y=None, stream=None):
