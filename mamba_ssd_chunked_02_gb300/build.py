@@ -8,7 +8,7 @@ rebuilt when their source or any header under csrc/ or include/ is newer.
 
 binding/layer_ext.cpp, the native Python binding of the layer operators, is
 compiled by g++ beside them against the installed torch's headers and linked to
-that library (_lib/layer_ext.so).
+that library (_lib/layer_ext.so); without torch the library alone is built.
 """
 from __future__ import annotations
 
@@ -68,9 +68,12 @@ def _compile(src: str, force: bool, extra) -> str:
     return obj
 
 
-def _ext_object(force: bool) -> str:
-    """Compile the Python binding; the object depends on the torch it was built for."""
-    import torch
+def _ext_object(force: bool) -> str | None:
+    """Compile the Python binding; the object depends on the torch it was built for.  None without torch."""
+    try:
+        import torch
+    except ImportError:
+        return None
     obj = os.path.join(BUILD, f"layer_ext-{torch.__version__}.o")
     if not force and os.path.exists(obj) and os.path.getmtime(obj) >= max(os.path.getmtime(EXT_SRC), _newest_header()):
         return obj
@@ -109,18 +112,19 @@ def build(force: bool = False, jobs: int = 0, extra=()) -> str:
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
         ext = ex.submit(_ext_object, force)
         objs = list(ex.map(lambda s: _compile(s, force, extra), srcs))
-        ext_obj = ext.result()
-    if (not force and os.path.exists(LIB)
-            and os.path.getmtime(LIB) >= max(os.path.getmtime(o) for o in objs)):
+    if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
+        tmp = LIB + f".tmp{os.getpid()}"
+        cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, LIB)
+    # the library is complete; the binding comes after it
+    ext_obj = ext.result()
+    if ext_obj:
         _link_ext(ext_obj, force)
-        return LIB
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    _link_ext(ext_obj, force)
+    else:
+        sys.stderr.write("torch is not installed: the Python binding of the layer operators was not built\n")
     return LIB
 
 
