@@ -8,7 +8,8 @@ rebuilt when their source or any header under csrc/ or include/ is newer.
 
 binding/layer_ext.cpp, the native Python binding of the layer operators, is
 compiled by g++ beside them against the installed torch's headers and linked to
-that library (_lib/layer_ext.so); without torch the library alone is built.
+that library (_lib/layer_ext-<torch and Python>.so, a file for each pair it was
+built for); without torch the library alone is built.
 """
 from __future__ import annotations
 
@@ -29,7 +30,6 @@ BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libmamba2_ssd.so")
 EXT_SRC = os.path.join(PKG, "binding", "layer_ext.cpp")
-EXT = os.path.join(LIBDIR, "layer_ext.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -68,13 +68,24 @@ def _compile(src: str, force: bool, extra) -> str:
     return obj
 
 
+def _ext_tag() -> str:
+    """What the binding's binary interface depends on: the torch and Python it is built for."""
+    import torch
+    return f"{torch.__version__}-{sysconfig.get_config_var('SOABI')}-cxx{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+
+
+def ext_path() -> str:
+    """The Python binding for the torch and Python at hand."""
+    return os.path.join(LIBDIR, f"layer_ext-{_ext_tag()}.so")
+
+
 def _ext_object(force: bool) -> str | None:
-    """Compile the Python binding; the object depends on the torch it was built for.  None without torch."""
+    """Compile the Python binding; None without torch."""
     try:
         import torch
     except ImportError:
         return None
-    obj = os.path.join(BUILD, f"layer_ext-{torch.__version__}.o")
+    obj = os.path.join(BUILD, f"layer_ext-{_ext_tag()}.o")
     if not force and os.path.exists(obj) and os.path.getmtime(obj) >= max(os.path.getmtime(EXT_SRC), _newest_header()):
         return obj
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
@@ -91,17 +102,18 @@ def _ext_object(force: bool) -> str | None:
 
 
 def _link_ext(obj: str, force: bool) -> None:
-    if not force and os.path.exists(EXT) and os.path.getmtime(EXT) >= max(os.path.getmtime(obj), os.path.getmtime(LIB)):
+    out = ext_path()
+    if not force and os.path.exists(out) and os.path.getmtime(out) >= max(os.path.getmtime(obj), os.path.getmtime(LIB)):
         return
     import torch
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
-    tmp = EXT + f".tmp{os.getpid()}"
+    tmp = out + f".tmp{os.getpid()}"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", LIBDIR, "-lmamba2_ssd", "-L", libs, "-ltorch_python", "-ltorch_cpu",
            "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, EXT)
+    os.replace(tmp, out)
 
 
 def build(force: bool = False, jobs: int = 0, extra=()) -> str:

@@ -84,7 +84,6 @@ def _fn(name):
     return _fns[name] if _fns else _bind()[name]
 
 
-_EXT_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "layer_ext.so")
 _ext_module = None
 
 
@@ -92,11 +91,13 @@ def _load_ext():
     """The native binding (raises if it has not been built)."""
     global _ext_module
     from . import Mamba2Error, load
+    from .build import ext_path
     load()
-    if not os.path.exists(_EXT_PATH):
-        raise RuntimeError(f"{_EXT_PATH} is missing: build it with `python -m mamba_ssd_chunked_02_gb300.build`"
+    path = ext_path()
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with `python -m mamba_ssd_chunked_02_gb300.build`"
                            " (there is no CPU fallback)")
-    spec = importlib.util.spec_from_file_location("layer_ext", _EXT_PATH)
+    spec = importlib.util.spec_from_file_location("layer_ext", path)
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
     mod.set_error(Mamba2Error)

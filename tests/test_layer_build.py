@@ -2,7 +2,9 @@
 layer operators, which needs the torch it is loaded into.  On a one-function library."""
 import ctypes
 import os
+import subprocess
 import sys
+import types
 
 import pytest
 
@@ -21,7 +23,6 @@ def tree(tmp_path, monkeypatch):
     for name, at in dict(CSRC=tmp_path / "csrc", INCLUDE=tmp_path / "include", BUILD=tmp_path / "_build", LIBDIR=lib,
                          LIB=lib / "libmamba2_ssd.so", EXT_SRC=ext).items():
         monkeypatch.setattr(m2build, name, str(at))
-    monkeypatch.setattr(m2build, "EXT", str(lib / "layer_ext.so"), raising=False)
     return tmp_path
 
 
@@ -37,3 +38,27 @@ def test_the_library_is_built_when_the_binding_does_not_compile(tree):
     with pytest.raises(RuntimeError, match="layer_ext.cpp"):
         m2build.build()
     assert ctypes.CDLL(m2build.LIB).one() == 1
+
+
+def _torch(root, version, value):
+    """A stand-in for an installed torch: a header that says which, and libraries to link."""
+    at = root / version
+    (at / "include").mkdir(parents=True)
+    (at / "lib").mkdir()
+    (at / "include" / "which.h").write_text(f"#define WHICH {value}\n")
+    for name in ("torch_python", "torch_cpu", "c10", "c10_cuda"):
+        subprocess.run(["gcc", "-shared", "-x", "c", "/dev/null", "-o", str(at / "lib" / f"lib{name}.so")], check=True)
+    fake = types.ModuleType("torch")
+    fake.__version__, fake.__file__ = version, str(at / "__init__.py")
+    fake._C = types.SimpleNamespace(_GLIBCXX_USE_CXX11_ABI=True)
+    return fake
+
+
+def test_each_torch_loads_the_binding_built_for_it(tree, monkeypatch):
+    """Back and forth between two versions, with what the first build left lying there."""
+    fakes = {1: _torch(tree, "1.0", 1), 2: _torch(tree, "2.0", 2)}
+    for value in (1, 2, 1, 2):
+        monkeypatch.setitem(sys.modules, "torch", fakes[value])
+        m2build.build()
+        code = f"import ctypes; print(ctypes.CDLL({m2build.ext_path()!r}).which())"     # a process each: loaded once by name
+        assert int(subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, check=True).stdout) == value
