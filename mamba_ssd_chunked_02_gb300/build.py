@@ -92,12 +92,14 @@ def _ext_object(force: bool) -> str | None:
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     dirs = [inc, os.path.join(inc, "torch", "csrc", "api", "include"), cuda,
             sysconfig.get_paths()["include"], INCLUDE]
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w",
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-Wextra",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     cmd += [f for d in dirs for f in ("-isystem", d)] + ["-c", EXT_SRC, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {os.path.basename(EXT_SRC)}:\n{r.stdout}\n{r.stderr}")
+    if r.stderr.strip():
+        sys.stderr.write(r.stderr)
     return obj
 
 

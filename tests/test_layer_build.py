@@ -62,3 +62,12 @@ def test_each_torch_loads_the_binding_built_for_it(tree, monkeypatch):
         m2build.build()
         code = f"import ctypes; print(ctypes.CDLL({m2build.ext_path()!r}).which())"     # a process each: loaded once by name
         assert int(subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, check=True).stdout) == value
+
+
+def test_warnings_about_the_binding_are_shown(tree, monkeypatch, capsys):
+    monkeypatch.setitem(sys.modules, "torch", _torch(tree, "1.0", 1))
+    m2build.build()
+    assert capsys.readouterr().err == ""
+    (tree / "binding" / "layer_ext.cpp").write_text("int f() { int unused; return 1; }\n")
+    m2build.build(force=True)
+    assert "unused" in capsys.readouterr().err
