@@ -127,10 +127,11 @@ __device__ __forceinline__ int ld_acquire_gpu(const int32_t* p) {
 __device__ __forceinline__ void st_release_gpu(int32_t* p, int v) {
     asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
-// *p = v if it is `was`.
-__device__ __forceinline__ void cas_release_gpu(int32_t* p, int was, int v) {
+// *p = v if it is `was`; returns what it was.
+__device__ __forceinline__ int cas_release_gpu(int32_t* p, int was, int v) {
     int old;
     asm volatile("atom.release.gpu.global.cas.b32 %0, [%1], %2, %3;" : "=r"(old) : "l"(p), "r"(was), "r"(v) : "memory");
+    return old;
 }
 // Wait until *f is 1 (published) for at most limit_ns; -1 (the predecessor gave
 // up) or a timeout raise *abort and return false.
