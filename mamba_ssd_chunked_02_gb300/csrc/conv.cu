@@ -427,7 +427,7 @@ cudaError_t fwd_w(const ConvArgs& a, const TI* x, const float* w, const float* b
     const int64_t lanes = (a.D + V - 1) / V, ncb = (lanes + kFwdThreads - 1) / kFwdThreads;
     const int ts = pick_ts(a.b * lanes, a.T, 6, 768);
     const int64_t nseg = std::max<int64_t>(1, (a.T + ts - 1) / ts);
-    if (a.b * nseg * ncb >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    if (a.b * nseg * ncb >= (int64_t(1) << 31)) return kGridLimit;
     auto k = a.silu ? conv_fwd_kernel<TI, V, W, true> : conv_fwd_kernel<TI, V, W, false>;
     constexpr size_t smem = (size_t)ring<TI, V>() * 4 * kFwdThreads * V * sizeof(TI);
     static_assert(smem <= 48 * 1024, "the default limit");
@@ -440,7 +440,7 @@ template <typename TI, int V, int W>
 cudaError_t step_w(const ConvArgs& a, TI* state, const TI* x, const float* w, const float* bias, TI* y,
                    cudaStream_t st) {
     const int64_t ncb = ((a.D + V - 1) / V + 127) / 128;
-    if (a.b * ncb >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    if (a.b * ncb >= (int64_t(1) << 31)) return kGridLimit;
     auto k = a.silu ? conv_step_kernel<TI, V, W, true> : conv_step_kernel<TI, V, W, false>;
     k<<<(unsigned)(a.b * ncb), 128, 0, st>>>(state, x, w, bias, y, (int)a.D, (int)ncb, a.sx.b, a.sy.b);
     return cudaGetLastError();
@@ -451,7 +451,7 @@ cudaError_t bwd_w(const ConvArgs& a, const TI* x, const float* w, const float* b
                   const TI* dy, const TI* dfin, const int32_t* lengths, TI* dx, TI* dinit, float* part,
                   cudaStream_t st) {
     const int64_t ncb = ((a.D + V - 1) / V + kBwdTX - 1) / kBwdTX, nblk = bwd_blocks(a);
-    if (a.b * nblk * ncb >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    if (a.b * nblk * ncb >= (int64_t(1) << 31)) return kGridLimit;
     auto k = a.silu ? conv_bwd_kernel<TI, V, W, true> : conv_bwd_kernel<TI, V, W, false>;
     constexpr size_t rings = (size_t)ring<TI, V>() * 4 * 2 * kBwdTX * kBwdTY * V * sizeof(TI);
     constexpr size_t sums = (size_t)kBwdTY * kBwdTX * V * (W + 1) * sizeof(float), smem = rings > sums ? rings : sums;
@@ -535,7 +535,7 @@ column_sum_kernel(const float* __restrict__ part, int64_t slots, int64_t cols, f
 cudaError_t launch_column_sum(const float* part, int64_t slots, int64_t cols, float* out1, int64_t n1,
                               float* out2, cudaStream_t st) {
     if (cols == 0) return cudaSuccess;
-    if ((cols + 7) / 8 >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    if ((cols + 7) / 8 >= (int64_t(1) << 31)) return kGridLimit;
     // few columns and many slots (a narrow layer): more rows of slots a block, so that a
     // thread's chain of loads stays short
     if (cols < (int64_t)sm_count() * 64 && slots > 64)

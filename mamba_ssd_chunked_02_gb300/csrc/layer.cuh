@@ -237,6 +237,11 @@ inline bool vec_ok(const void* p, const Tok& s, int64_t bytes, int64_t esize) {
            (s.t * esize) % bytes == 0;
 }
 
+// A launcher's own refusal, before its first launch: the shape takes more blocks than a
+// grid has.  Not a value of CUDA's, whose errors (an invalid value among them) may come from
+// any of a call's launches.
+constexpr cudaError_t kGridLimit = static_cast<cudaError_t>(12289);
+
 struct ConvArgs {
     int64_t b, T, D;
     int W, dtype;

@@ -13,9 +13,7 @@ using m2::Tok;
 constexpr int64_t kMaxT = int64_t(1) << 30, kMaxD = int64_t(1) << 24, kMaxStride = int64_t(1) << 40;
 
 mamba2_status from_cuda(cudaError_t e) {
-    if (e == cudaSuccess) return MAMBA2_OK;
-    // The launchers' own limit on the grid; nothing was launched.
-    return e == cudaErrorInvalidValue ? MAMBA2_ERR_UNSUPPORTED : MAMBA2_ERR_CUDA;
+    return e == cudaSuccess ? MAMBA2_OK : e == m2::kGridLimit ? MAMBA2_ERR_UNSUPPORTED : MAMBA2_ERR_CUDA;
 }
 
 // Pointers need their element type's alignment; a tensor without elements may be null.

@@ -391,7 +391,7 @@ template <typename TI, int V, int GATE>
 cudaError_t fwd_go(const NormArgs& a, const TI* x, const float* w, const TI* z, TI* y, cudaStream_t st) {
     const Rows q = rows_of(a);
     const int64_t items = q.rows * q.G, nv = q.S / V;
-    if (items >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    if (items >= (int64_t(1) << 31)) return kGridLimit;
     const unsigned wb = (unsigned)((items + kWarpTeams - 1) / kWarpTeams);
     const unsigned bb = (unsigned)items;
     if (nv <= 32) norm_fwd_kernel<TI, V, 1, GATE, true><<<wb, kWarpTeams * 32, 0, st>>>(x, w, z, y, q);
@@ -410,7 +410,7 @@ cudaError_t bwd_go(const NormArgs& a, const TI* x, const float* w, const TI* z, 
     const Rows q = rows_of(a);
     const int64_t nv = q.S / V;
     const int64_t slots = bwd_team_slots(a), teams64 = slots * q.G;
-    if (teams64 >= (int64_t(1) << 31) || q.rows >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    if (teams64 >= (int64_t(1) << 31) || q.rows >= (int64_t(1) << 31)) return kGridLimit;
     const int teams = (int)teams64;
     const unsigned wb = (unsigned)((teams64 + kWarpTeams - 1) / kWarpTeams);
     const unsigned bb = (unsigned)teams;

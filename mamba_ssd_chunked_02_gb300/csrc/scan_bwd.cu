@@ -129,7 +129,7 @@ cudaError_t launch_scan_bwd(const ScanArgs& a, const void* x, const void* dt, co
         return e;
     }
     const int64_t rows = a.b * a.T * a.G, blocks = (rows * 2 * a.N + 255) / 256;
-    if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;   // before the first launch
+    if (blocks >= (int64_t(1) << 31)) return kGridLimit;   // before the first launch
     const Plan pl = plan_of(a);
     char* w = static_cast<char*>(ws);
     BwdP p = {};

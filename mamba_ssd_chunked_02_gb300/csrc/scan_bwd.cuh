@@ -717,7 +717,7 @@ cudaError_t bwd_v(const BwdP& p, int KK, int64_t lncb, const float* init, const 
     const int64_t lb = p.b * p.nseg * p.G * lncb, gb = p.b * p.nseg * p.G * p.ncb;
     const int64_t total = p.b * p.Dch * N;
     if (lb >= (int64_t(1) << 31) || gb >= (int64_t(1) << 31) || (total + 255) / 256 >= (int64_t(1) << 31))
-        return cudaErrorInvalidValue;
+        return kGridLimit;
     BwdP l = p;
     l.ncb = (int)lncb;
     auto lk = adj ? scan_local_kernel<TI, N, V, true> : scan_local_kernel<TI, N, V, false>;

@@ -443,7 +443,7 @@ cudaError_t fwd_v(const FwdP& p, bool starve, cudaStream_t st) {
     const int64_t rows = p.b * p.G * p.ncb, blocks = rows * p.nseg * p.slices;
     constexpr size_t smem = (size_t)K::TT * K::CB * 8 + (size_t)K::YF * 4 +
                             2 * (size_t)K::TT * (3 * K::CB + 2 * N) * sizeof(TI);
-    if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    if (blocks >= (int64_t(1) << 31)) return kGridLimit;
     auto k = scan_fwd_kernel<TI, N, V, false>;
     auto s = scan_fwd_kernel<TI, N, V, true>;
     if (smem > 48 * 1024) {
@@ -534,7 +534,7 @@ cudaError_t step_t(const ScanArgs& a, float* state, const void* x, const void* d
                    const void* B, const void* C, const float* D, const void* z, const float* bias, void* y,
                    cudaStream_t st) {
     const int64_t total = a.b * a.D * (a.N / 4), blocks = (total + 255) / 256;
-    if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    if (blocks >= (int64_t(1) << 31)) return kGridLimit;
     const int wide = reinterpret_cast<uintptr_t>(state) % 16 == 0 && reinterpret_cast<uintptr_t>(A) % 16 == 0;
     auto go = [&](auto k) {
         k<<<(unsigned)blocks, 256, 0, st>>>(
