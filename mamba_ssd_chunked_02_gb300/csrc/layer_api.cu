@@ -42,14 +42,19 @@ bool in_strides(const int64_t* s, int64_t T, int64_t width, Tok* out) {
     *out = Tok{s[0], s[1]};
     return true;
 }
+// n pieces of `width` elements, `near` apart, lie apart from each other and within `far`
+// (divided, as near * n may pass 64 bits).
+bool apart(int64_t near, int64_t n, int64_t width, int64_t far) {
+    return near >= width && far >= width && n - 1 <= (far - width) / near;
+}
 // Strides of a written tensor: no two elements in one place.
 bool out_strides(const int64_t* s, int64_t b, int64_t T, int64_t width, Tok* out) {
     if (!in_strides(s, T, width, out)) return false;
     const int64_t sb = out->b, st = out->t;
-    if (b == 0 || T == 0 || (b == 1 && T == 1)) return true;
+    if (b == 0 || T == 0 || width == 0 || (b == 1 && T == 1)) return true;
     if (b <= 1) return st >= width;
     if (T <= 1) return sb >= width;
-    return (st >= width && sb >= st * (T - 1) + width) || (sb >= width && st >= sb * (b - 1) + width);
+    return apart(st, T, width, sb) || apart(sb, b, width, st);
 }
 
 bool conv_args(const mamba2_conv_shape* s, const mamba2_conv_strides* st, bool y_written, m2::ConvArgs* a,

@@ -90,3 +90,15 @@ def test_too_large_a_grid_is_unsupported(lib):
                                   ("scan_bwd", L.ScanShape(1 << 24, 1 << 12, 64, 16, 1, m2.BF16, 0), 21, True)):
         tail = [P, 1 << 62, None] if space else [None]
         assert L._fn(name)(ctypes.addressof(sh), None, *[P] * ptrs, *tail) == m2.ERR_UNSUPPORTED, name
+
+
+def test_overlapping_output_rows_are_refused_at_any_stride(lib):
+    """2^25 sequences of two tokens, rows of 8 elements one element apart: the extent of the
+    sequences passes 64 bits."""
+    far = 1 << 39
+    st = L._strides2(16, 8, far, 1)
+    sh = L.ConvShape(1 << 25, 2, 8, 4, m2.BF16, 0)
+    assert L._fn("conv_fwd")(ctypes.addressof(sh), ctypes.addressof(st), *[P] * 7, None) == m2.ERR_INVALID_ARG
+    st = L._strides2(16, 8, 1, far)       # the same with the two dimensions' parts exchanged
+    sh = L.ConvShape(2, 1 << 25, 8, 4, m2.BF16, 0)
+    assert L._fn("conv_fwd")(ctypes.addressof(sh), ctypes.addressof(st), *[P] * 7, None) == m2.ERR_INVALID_ARG
