@@ -279,13 +279,16 @@ int64_t second_dim(PyObject* o, const char* name, const char* what, int64_t chan
 
 typedef PyObject* const* Args;
 
+// A width as the C ABI takes it; one beyond 32 bits stays one that is refused.
+int32_t width32(int64_t w) { return w > INT32_MAX ? INT32_MAX : (int32_t)w; }
+
 // ---- conv: (x, w, bias, initial_state, lengths, silu, y, final_state, stream)
 PyObject* conv_fwd(Args a) {
     const Call c(a[0], "x", 3);
     const OnStream on(c, a[8]);
     const Tensor& x = THPVariable_Unpack(a[0]);
     const int64_t b = x.size(0), T = x.size(1), D = x.size(2), W = second_dim(a[1], "w", "width", D);
-    const mamba2_conv_shape sh{b, T, D, (int32_t)W, c.dtype(), truth(a[5]) ? MAMBA2_CONV_SILU : 0};
+    const mamba2_conv_shape sh{b, T, D, width32(W), c.dtype(), truth(a[5]) ? MAMBA2_CONV_SILU : 0};
     mamba2_conv_strides st;
     void* px = c.token(a[0], "x", {b, T, D}, st.x);
     void* pw = c.dense(a[1], "w", at::kFloat, {D, W});
@@ -305,7 +308,7 @@ PyObject* conv_step(Args a) {
     const OnStream on(c, a[6]);
     const Tensor& x = THPVariable_Unpack(a[1]);
     const int64_t b = x.size(0), D = x.size(1), W = second_dim(a[2], "w", "width", D);
-    const mamba2_conv_shape sh{b, 1, D, (int32_t)W, c.dtype(), truth(a[4]) ? MAMBA2_CONV_SILU : 0};
+    const mamba2_conv_shape sh{b, 1, D, width32(W), c.dtype(), truth(a[4]) ? MAMBA2_CONV_SILU : 0};
     mamba2_conv_strides st;
     void* ps = c.dense(a[0], "state", c.io, {b, W - 1, D});
     void* px = c.token(a[1], "x", {b, D}, st.x, 1);
@@ -323,7 +326,7 @@ PyObject* conv_bwd(Args a) {
     const OnStream on(c, a[10]);
     const Tensor& x = THPVariable_Unpack(a[0]);
     const int64_t b = x.size(0), T = x.size(1), D = x.size(2), W = second_dim(a[1], "w", "width", D);
-    const mamba2_conv_shape sh{b, T, D, (int32_t)W, c.dtype(), truth(a[7]) ? MAMBA2_CONV_SILU : 0};
+    const mamba2_conv_shape sh{b, T, D, width32(W), c.dtype(), truth(a[7]) ? MAMBA2_CONV_SILU : 0};
     mamba2_conv_strides st;
     void* px = c.token(a[0], "x", {b, T, D}, st.x);
     void* pw = c.dense(a[1], "w", at::kFloat, {D, W});
