@@ -1,6 +1,9 @@
 // layer_ext.cpp -- Python binding of include/mamba2_layer.h: checks torch tensors,
 // allocates outputs and workspaces, and calls the C ABI on the caller's stream.
 //
+// An output given, a state or a workspace that shares memory with another tensor of the call
+// is a ValueError: the kernels read inputs while they write, in no order.
+//
 // Native because the single-token calls take 3 us on the GPU: the same checks in
 // Python (ctypes) cost 7 to 12 us a call, these about 1.  Every function takes its
 // arguments by position (layer.py has the documented signatures) and raises TypeError
@@ -19,6 +22,7 @@
 #include <utility>
 
 #include "mamba2_layer.h"
+#include "overlap.h"
 
 namespace {
 
@@ -55,6 +59,16 @@ const Tensor* tensor(PyObject* o, const char* name) {
 struct Call {
     at::ScalarType io;
     c10::Device device;
+    // The caller's tensors, for distinct(); written: outputs given, a state, a workspace given.
+    struct Held {
+        const char* name;
+        m2::Rows rows;
+        int64_t end;
+        bool written;
+    };
+    mutable Held held[24];
+    mutable int count = 0;
+    mutable bool writes = false;
 
     Call(PyObject* o, const char* name, int64_t rank) : io(at::kFloat), device(c10::DeviceType::CPU) {
         const Tensor* t = tensor(o, name);
@@ -81,8 +95,31 @@ struct Call {
             raise(PyExc_ValueError, std::string(name) + " must have shape " + show(at::IntArrayRef(shape)) + ", got " +
                                         show(t.sizes()));
     }
+    void* note(const Tensor& t, const char* name, bool written, int64_t row, int64_t n0 = 1, int64_t s0 = 0, int64_t n1 = 1,
+               int64_t s1 = 0) const {
+        void* p = t.data_ptr();
+        if (row <= 0 || n0 <= 0 || n1 <= 0) return p;
+        if (count == (int)(sizeof(held) / sizeof(*held))) raise(PyExc_SystemError, "more tensors than a call has");
+        const int64_t e = (int64_t)t.element_size();
+        Held& h = held[count++];
+        h.name = name, h.written = written;
+        h.rows = {(int64_t)reinterpret_cast<intptr_t>(p), row * e, {n0, n1}, {s0 * e, s1 * e}};
+        h.end = h.rows.end();
+        writes |= written;
+        return p;
+    }
+    // Refuses a written tensor that shares memory with another of the call.
+    void distinct() const {
+        if (!writes) return;
+        for (int i = 0; i < count; ++i)
+            for (int j = 0; j < count && held[i].written; ++j)
+                if (j != i && held[i].rows.at < held[j].end && held[j].rows.at < held[i].end &&
+                    m2::overlap(held[i].rows, held[j].rows))
+                    raise(PyExc_ValueError, std::string(held[i].name) + " must not overlap " + held[j].name);
+    }
     // Address of a contiguous tensor; null for an absent optional one.
-    void* dense(PyObject* o, const char* name, at::ScalarType type, Dims shape, bool optional = false) const {
+    void* dense(PyObject* o, const char* name, at::ScalarType type, Dims shape, bool optional = false,
+                bool written = false) const {
         const Tensor* t = tensor(o, name);
         if (!t) {
             if (optional) return nullptr;
@@ -90,10 +127,11 @@ struct Call {
         }
         fits(*t, name, type, shape);
         if (!t->is_contiguous()) raise(PyExc_ValueError, std::string(name) + " must be contiguous");
-        return t->data_ptr();
+        return note(*t, name, written, t->numel());
     }
     // Address of a token tensor and its {batch, token} strides (lead = 1: batch only).
-    void* token(PyObject* o, const char* name, Dims shape, int64_t* st, size_t lead = 2, bool optional = false) const {
+    void* token(PyObject* o, const char* name, Dims shape, int64_t* st, size_t lead = 2, bool optional = false,
+                bool written = false) const {
         const Tensor* t = tensor(o, name);
         if (!t) {
             if (optional) return nullptr;
@@ -111,7 +149,7 @@ struct Call {
         // a dimension of one entry is never stepped over: any stride does
         st[0] = n[0] > 1 ? s[0] : width;
         st[1] = lead == 2 && n[1] > 1 ? s[1] : width;
-        return t->data_ptr();
+        return note(*t, name, written, width, n[0], st[0], lead == 2 ? n[1] : 1, st[1]);
     }
     Tensor make(Dims shape, at::ScalarType type) const {
         return at::empty(at::IntArrayRef(shape), at::TensorOptions().dtype(type).device(device));
@@ -122,7 +160,7 @@ struct Call {
             if (t->device() != device || !t->is_contiguous())
                 raise(PyExc_ValueError, "workspace must be a contiguous CUDA tensor on the same device as the input");
             *bytes = t->nbytes();
-            return t->data_ptr();
+            return note(*t, "workspace", true, t->numel());
         }
         *bytes = need;
         if (!need) return nullptr;
@@ -202,7 +240,7 @@ struct Out {
 Out dense_out(const Call& c, PyObject* given, const char* name, at::ScalarType type, Dims shape) {
     Out o;
     if (given && given != Py_None) {
-        o.at = c.dense(given, name, type, shape);
+        o.at = c.dense(given, name, type, shape, false, true);
         Py_INCREF(given);
         o.obj = given;
     } else {
@@ -215,7 +253,7 @@ Out dense_out(const Call& c, PyObject* given, const char* name, at::ScalarType t
 Out token_out(const Call& c, PyObject* given, const char* name, Dims shape, int64_t* st, size_t lead = 2) {
     if (given && given != Py_None) {
         Out o;
-        o.at = c.token(given, name, shape, st, lead);
+        o.at = c.token(given, name, shape, st, lead, false, true);
         Py_INCREF(given);
         o.obj = given;
         return o;
@@ -297,6 +335,7 @@ PyObject* conv_fwd(Args a) {
     void* pl = c.dense(a[4], "lengths", at::kInt, {b}, true);
     Out y = token_out(c, a[6], "y", {b, T, D}, st.y);
     Out f = dense_out(c, a[7], "final_state", c.io, {b, W > 0 ? W - 1 : 0, D});
+    c.distinct();
     check("mamba2_conv_fwd", mamba2_conv_fwd(&sh, &st, px, (float*)pw, (float*)pb, pi, (int32_t*)pl, y.at, f.at,
                                              on.raw));
     return pair(y, f);
@@ -310,11 +349,12 @@ PyObject* conv_step(Args a) {
     const int64_t b = x.size(0), D = x.size(1), W = second_dim(a[2], "w", "width", D);
     const mamba2_conv_shape sh{b, 1, D, width32(W), c.dtype(), truth(a[4]) ? MAMBA2_CONV_SILU : 0};
     mamba2_conv_strides st;
-    void* ps = c.dense(a[0], "state", c.io, {b, W - 1, D});
+    void* ps = c.dense(a[0], "state", c.io, {b, W - 1, D}, false, true);
     void* px = c.token(a[1], "x", {b, D}, st.x, 1);
     void* pw = c.dense(a[2], "w", at::kFloat, {D, W});
     void* pb = c.dense(a[3], "bias", at::kFloat, {D}, true);
     Out y = token_out(c, a[5], "y", {b, D}, st.y, 1);
+    c.distinct();
     check("mamba2_conv_step",
           mamba2_conv_step(&sh, &st, ps, px, (float*)pw, (float*)pb, y.at, on.raw));
     return y.give();
@@ -343,6 +383,7 @@ PyObject* conv_bwd(Args a) {
     Tensor hold;
     size_t bytes;
     void* ws = c.space(a[9], mamba2_conv_bwd_workspace_size(&sh), hold, &bytes);
+    c.distinct();
     check("mamba2_conv_bwd", mamba2_conv_bwd(&sh, &st, px, (float*)pw, (float*)pb, pi, py, pf, (int32_t*)pl, dx, (float*)dw,
                                              (float*)db, di, ws, bytes, on.raw));
     return g.give();
@@ -389,6 +430,7 @@ PyObject* scan_fwd(Args a) {
     Tensor hold;
     size_t bytes;
     void* ws = c.space(a[13], mamba2_scan_workspace_size(&s.sh), hold, &bytes);
+    c.distinct();
     check("mamba2_scan_fwd",
           mamba2_scan_fwd(&s.sh, &st, px, pt, (float*)pA, pB, pC, (float*)pD, pz, (float*)pb, (float*)pi, (int32_t*)pl,
                           y.at, (float*)f.at, ws, bytes, on.raw));
@@ -402,7 +444,7 @@ PyObject* scan_step(Args a) {
     const ScanCall s = scan_call(c, THPVariable_Unpack(a[1]), a[3], a[4], true, truth(a[9]));
     const int64_t b = s.b, D = s.D, N = s.N, G = s.G;
     mamba2_scan_strides st;
-    void* ps = c.dense(a[0], "state", at::kFloat, {b, D, N});
+    void* ps = c.dense(a[0], "state", at::kFloat, {b, D, N}, false, true);
     void* px = c.token(a[1], "x", {b, D}, st.x, 1);
     void* pt = c.token(a[2], "dt", {b, D}, st.dt, 1);
     void* pA = c.dense(a[3], "A", at::kFloat, {D, N});
@@ -413,6 +455,7 @@ PyObject* scan_step(Args a) {
     void* pz = c.token(a[7], "z", {b, D}, st.z, 1, true);
     void* pb = c.dense(a[8], "dt_bias", at::kFloat, {D}, true);
     Out y = token_out(c, a[10], "y", {b, D}, st.y, 1);
+    c.distinct();
     check("mamba2_scan_step", mamba2_scan_step(&s.sh, &st, (float*)ps, px, pt, (float*)pA, pB, pC, (float*)pD, pz,
                                                (float*)pb, y.at, on.raw));
     return y.give();
@@ -452,6 +495,7 @@ PyObject* scan_bwd(Args a) {
     Tensor hold;
     size_t bytes;
     void* ws = c.space(a[14], mamba2_scan_bwd_workspace_size(&s.sh), hold, &bytes);
+    c.distinct();
     check("mamba2_scan_bwd",
           mamba2_scan_bwd(&s.sh, &st, px, pt, (float*)pA, pB, pC, (float*)pD, pz, (float*)pb, (float*)pi, py, (float*)pf,
                           (int32_t*)pl, dx, ddt, (float*)dA, dB, dC, (float*)dD, dz, (float*)db, (float*)di, ws, bytes,
@@ -472,6 +516,7 @@ PyObject* norm_fwd(Args a) {
     st.z[0] = st.z[1] = 0;
     void* pz = c.token(a[2], "z", {b, T, D}, st.z, 2, true);
     Out y = token_out(c, a[6], "y", {b, T, D}, st.y);
+    c.distinct();
     check("mamba2_norm_fwd", mamba2_norm_fwd(&sh, &st, px, (float*)pw, pz, y.at, on.raw));
     return y.give();
 }
@@ -496,6 +541,7 @@ PyObject* norm_bwd(Args a) {
     Tensor hold;
     size_t bytes;
     void* ws = c.space(a[8], mamba2_norm_bwd_workspace_size(&sh), hold, &bytes);
+    c.distinct();
     check("mamba2_norm_bwd", mamba2_norm_bwd(&sh, &st, px, (float*)pw, pz, py, dx, dz, (float*)dw, ws, bytes,
                                              on.raw));
     return g.give();

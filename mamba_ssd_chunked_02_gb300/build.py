@@ -86,7 +86,8 @@ def _ext_object(force: bool) -> str | None:
     except ImportError:
         return None
     obj = os.path.join(BUILD, f"layer_ext-{_ext_tag()}.o")
-    if not force and os.path.exists(obj) and os.path.getmtime(obj) >= max(os.path.getmtime(EXT_SRC), _newest_header()):
+    newest = max(map(os.path.getmtime, glob.glob(os.path.join(os.path.dirname(EXT_SRC), "*"))))
+    if not force and os.path.exists(obj) and os.path.getmtime(obj) >= max(newest, _newest_header()):
         return obj
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")

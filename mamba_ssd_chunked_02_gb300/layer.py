@@ -10,7 +10,9 @@ need no copy); parameters and scan states are fp32.  `lengths` is an int32 [b] t
 of real tokens per sequence: what lies behind them is never read into a result, and
 outputs and gradients there are 0.  Tensors live on the current CUDA device;
 everything runs on `stream` (default: the current stream), on which the tensors have
-to be ready.  Outputs and workspaces are allocated with torch unless given.
+to be ready.  Outputs and workspaces are allocated with torch unless given; what is given
+to be written (`state` of the step calls too) must not share memory with any other tensor
+of the call, which is checked.
 
 The checks and the call itself are native code (binding/layer_ext.cpp); there is no
 CPU path.
