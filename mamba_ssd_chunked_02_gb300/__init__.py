@@ -16,7 +16,9 @@ Entry points (same names as the C ABI, minus the ``mamba2_ssd_`` prefix):
 Around the scan in a layer (module layer, C ABI in include/mamba2_layer.h):
   conv_fwd, conv_bwd, conv_step (short causal convolution), scan_fwd, scan_bwd,
   scan_step (selective scan with a decay per channel and state), norm_fwd,
-  norm_bwd (gated group norm); scan_selftest_turn_timeout.
+  norm_bwd (gated group norm); conv_bwd_workspace_size, scan_workspace_size,
+  scan_bwd_workspace_size, norm_bwd_workspace_size (of a ConvShape, ScanShape,
+  NormShape), scan_selftest_turn_timeout.
 
 Pages: "NVIDIA CUDA Tile로 Mamba-2 순방향 전달 커널 가속화" (devin.kr),
 "Mamba-2 아키텍처의 핵심 연산" (y_t = c_t^T h_t + D x_t) and "세 가지 핵심 커널
@@ -530,6 +532,6 @@ def device_error(clear=True) -> int:
     return int(code.value)
 
 
-from .layer import (conv_bwd, conv_fwd, conv_step, norm_bwd, norm_fwd, scan_bwd,  # noqa: E402,F401
-                    scan_bwd_workspace_size, scan_fwd, scan_selftest_turn_timeout, scan_step,
-                    scan_workspace_size)
+from .layer import (ConvShape, NormShape, ScanShape, conv_bwd, conv_bwd_workspace_size,  # noqa: E402,F401
+                    conv_fwd, conv_step, norm_bwd, norm_bwd_workspace_size, norm_fwd, scan_bwd,
+                    scan_bwd_workspace_size, scan_fwd, scan_selftest_turn_timeout, scan_step, scan_workspace_size)

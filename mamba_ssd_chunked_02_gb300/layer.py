@@ -131,6 +131,16 @@ def conv_bwd(x, w, bias=None, initial_state=None, dy=None, dfinal=None, lengths=
                                                  workspace, stream)
 
 
+def conv_bwd_workspace_size(shape: ConvShape) -> int:
+    """Bytes of workspace conv_bwd needs for a shape."""
+    return _fn("conv_bwd_ws")(ctypes.addressof(shape))
+
+
+def norm_bwd_workspace_size(shape: NormShape) -> int:
+    """Bytes of workspace norm_bwd needs for a shape."""
+    return _fn("norm_bwd_ws")(ctypes.addressof(shape))
+
+
 def scan_workspace_size(shape: ScanShape) -> int:
     """Bytes of workspace scan_fwd needs for a shape (often 0)."""
     return _fn("scan_ws")(ctypes.addressof(shape))

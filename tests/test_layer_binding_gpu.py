@@ -55,3 +55,21 @@ def test_slices_of_one_buffer_side_by_side_are_fine():
     half = wide[:, :, :16].contiguous()
     assert torch.equal(m2.norm_fwd(half, None, half), m2.norm_fwd(half, None, half.clone()))
     m2.conv_fwd(x[:, :0], w, y=x[:, :0])
+
+
+def test_workspaces_of_the_size_asked_for():
+    b, T, D, N = 2, 300, 64, 16
+    x, w, dy = torch.randn(b, T, D, device="cuda"), torch.randn(D, 4, device="cuda"), torch.randn(b, T, D, device="cuda")
+    one, A, B = torch.randn(D, device="cuda"), -torch.ones(D, N, device="cuda"), torch.randn(b, T, 1, N, device="cuda")
+    for need, call in (
+            (m2.conv_bwd_workspace_size(m2.ConvShape(b, T, D, 4, m2.F32, 1)), lambda s: m2.conv_bwd(x, w, dy=dy, workspace=s)),
+            (m2.norm_bwd_workspace_size(m2.NormShape(b, T, D, 1, 1e-5, m2.F32, 0)),
+             lambda s: m2.norm_bwd(x, one, dy=dy, workspace=s)),
+            (m2.scan_bwd_workspace_size(m2.ScanShape(b, T, D, N, 1, m2.F32, 0)),
+             lambda s: m2.scan_bwd(x, x, A, B, B, dy=dy, workspace=s))):
+        assert need > 0
+        space = torch.empty(need, dtype=torch.uint8, device="cuda")
+        got, want = call(space), call(None)
+        assert all(torch.equal(got[k], want[k]) for k in want if want[k] is not None)
+        with pytest.raises(m2.Mamba2Error, match="workspace"):
+            call(space[:-16])

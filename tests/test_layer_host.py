@@ -102,3 +102,12 @@ def test_overlapping_output_rows_are_refused_at_any_stride(lib):
     st = L._strides2(16, 8, 1, far)       # the same with the two dimensions' parts exchanged
     sh = L.ConvShape(2, 1 << 25, 8, 4, m2.BF16, 0)
     assert L._fn("conv_fwd")(ctypes.addressof(sh), ctypes.addressof(st), *[P] * 7, None) == m2.ERR_INVALID_ARG
+
+
+def test_workspace_sizes_are_public(lib):
+    conv, norm = m2.ConvShape(2, 64, 8, 4, m2.BF16, 0), m2.NormShape(2, 64, 8, 1, 1e-5, m2.BF16, 0)
+    scan = m2.ScanShape(2, 64, 8, 16, 1, m2.BF16, 0)
+    assert m2.conv_bwd_workspace_size(conv) >= 2 * 8 * 5 * 4      # a slot a sequence at least
+    assert m2.scan_bwd_workspace_size(scan) > 2 * 8 * 8 * 16 * 4  # a state every 8 tokens
+    assert m2.norm_bwd_workspace_size(m2.NormShape(0, 64, 8, 1, 1e-5, m2.BF16, 0)) == 0
+    assert m2.norm_bwd_workspace_size(norm) % (8 * 4) == 0
