@@ -41,8 +41,8 @@ class SSDLayer:
 
     def _steps(self, raw, lengths=None):
         dt = torch.nn.functional.softplus(raw.float() + self.dt_bias)
-        if lengths is not None:      # a step of 0 leaves the state as it is
-            dt = dt * (torch.arange(dt.shape[1], device="cuda")[None] < lengths[:, None])[..., None]
+        if lengths is not None:      # a step of 0 leaves the state as it is, whatever the padding holds
+            dt = torch.where((torch.arange(dt.shape[1], device="cuda")[None] < lengths[:, None])[..., None], dt, 0.0)
         return dt
 
     def _heads(self, xbc):
