@@ -54,7 +54,7 @@ class NormShape(ctypes.Structure):
                 ("eps", ctypes.c_float), ("dtype", _i32), ("flags", _i32)]
 
 
-_strides2, _strides3, _strides6 = _i64 * 4, _i64 * 6, _i64 * 12   # mirrors of the strides structs
+_strides2 = _i64 * 4   # mirror of struct mamba2_conv_strides
 _fns = {}
 
 
