@@ -8,8 +8,8 @@
 //   gate first: dx = dv silu(z), dz = dv x silu'(z);  after: dx = dv, dz = dy v r w silu'(z)
 //
 // Bytes bound: every tensor moves once.  b8 T4096 C5120 bf16: forward 159 us (6.3 TB/s,
-// 0.93 of the measured copy rate), backward in groups of 640 295 us (5.7 TB/s, 0.84, its
-// issue slots at 0.6); one token of 64 sequences 2.5 us on the GPU, the launch.
+// 0.93 of the measured copy rate), backward in groups of 640 296 us (5.7 TB/s, 0.83, its
+// issue slots at 0.64); one token of 64 sequences 2.5 us on the GPU, the launch.
 //
 // A team (a warp for groups that fit its registers, else a block) holds a group's row in
 // registers between the sums and the result; the backward's two sums need one pass (mean(q v)
@@ -374,11 +374,18 @@ int team_threads(int64_t nv, int vpt) {
     return (int)std::min<int64_t>(1024, std::max<int64_t>(1, (nv + vpt * 32 - 1) / (vpt * 32)) * 32);
 }
 
-// Backward slots of dw: as many teams as an SM holds at once (16 or 20 warps, or blocks of 1024
-// threads in all), each with an equal share of the tokens, over the groups.
+// bf16 groups of 513 to 640 channels, backward: five rounds of four a lane instead of three of
+// eight, the last of them half idle (b8 T4096 G8: groups of 520 294 against 305 us, 576 296
+// against 309, 640 298 against 313).
+bool five_of_four(const NormArgs& a) { return a.dtype == 1 && a.D / a.G > 512 && a.D / a.G <= 640; }
+
+// Backward slots of dw: 16 or 20 warp teams an SM, or blocks of 1024 threads in all, each with an
+// equal share of the tokens, over the groups.  An SM holds that many at once, except in fp32 at
+// groups of 385 to 640: three blocks of 61,440 bytes of shared memory where five are counted, so
+// that the shares run in two waves.
 int64_t bwd_team_slots(const NormArgs& a) {
     const int64_t S = a.D / a.G, full = a.dtype == 1 ? 8 : 4;
-    const int64_t V = S % full == 0 && !(full == 8 && S > 512 && S <= 640) ? full : a.dtype != 1 ? 1 : S % 4 == 0 ? 4 : S % 2 == 0 ? 2 : 1;
+    const int64_t V = S % full == 0 && !five_of_four(a) ? full : a.dtype != 1 ? 1 : S % 4 == 0 ? 4 : S % 2 == 0 ? 2 : 1;
     const int64_t nv = S / V, each = (nv + 31) / 32 * V;
     const int64_t per_sm = nv <= 96 || (V == 4 && nv <= 160)
                                ? bwd_warps((int)each)
@@ -466,9 +473,7 @@ int vec_of(const NormArgs& a, bool back, const void* x, const float* w, const vo
     for (int V : {8, 4, 2}) {
         if (a.dtype != 1 && V != 4) continue;
         const int64_t by = V * es;
-        // 513 to 640 channels: five rounds of four a lane instead of three of eight, the last of
-        // them half idle (backward, groups of 640: 298 against 312 us)
-        if (back && V == 8 && a.D / a.G > 512 && a.D / a.G <= 640) continue;
+        if (back && V == 8 && five_of_four(a)) continue;
         if ((a.D / a.G) % V == 0 && reinterpret_cast<uintptr_t>(w) % (V > 2 ? 16 : 8) == 0 && vec_ok(x, a.sx, by, es) &&
             (!z || vec_ok(z, a.sz, by, es)) && vec_ok(y, a.sy, by, es) && vec_ok(o1, row, by, es) &&
             vec_ok(o2, row, by, es))

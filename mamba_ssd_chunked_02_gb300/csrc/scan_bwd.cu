@@ -55,11 +55,12 @@ scan_bc_sum_kernel(const float* __restrict__ part, int ncb, int64_t rows, int N,
 
 struct Plan {
     int KK;
-    int64_t SL, nseg, nck, ncb, blocks_local;
+    int64_t SL, nseg, nck, ncb;
     size_t ck, ck_d, seg, seg_d, bc, A, v, total;
 };
 
-// Stretches: as many as keep the gradient kernel's blocks (two an SM) busiest, whole waves
+// Stretches: as many as keep the gradient kernel's blocks (two an SM; one in fp32 at N = 8 with
+// four channels in turn, for 129,536 bytes of shared memory) busiest, whole waves
 // of them against the start of each; none shorter than two tiles of the first
 // pass, and no more than 64 for the join.
 Plan plan_of(const ScanArgs& a) {
@@ -69,7 +70,10 @@ Plan plan_of(const ScanArgs& a) {
     const int64_t held = (int64_t)sm_count() * 2;
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>(64, a.T / tt));
     auto blocks = [&](int KK) { return (Dg + kGT / lpc * KK - 1) / (kGT / lpc * KK); };
-    // (b3 T1956 C320 in groups of 80, N8: 166 us with KK = 4, whose blocks hold 256 channels)
+    // Four channels in turn where that still fills the GPU.  b4 T2048, KK = 4 against 1: C2048 bf16 N16
+    // 482 / 521 us, N32 867 / 1010, N64 1487 / 2339, N128 3359 / 5717, fp32 much the same.  Not everywhere: N8
+    // 373 / 320 (fp32 415 / 325; its blocks hold 256 channels), C2047 N16 920 / 810 (N8 621 / 674, N32 1084 / 1397).
+    // KK = 1 for small problems: b3 T1956 C320 in groups of 80, N8, fp32: 166 us with four in turn, 99 with one.
     p.KK = a.b * a.G * blocks(4) * most >= held && 2 * Dg > kGT / lpc * 4 ? 4 : 1;
     p.ncb = blocks(p.KK);
     const int64_t per = std::max<int64_t>(1, a.b * a.G * p.ncb);
