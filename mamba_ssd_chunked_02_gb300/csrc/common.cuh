@@ -9,10 +9,12 @@ namespace m2 {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// 2^x with the hardware exponent unit (PTX ex2.approx.ftz.f32).  Callers pass
-// x <= 0 (a masked log2-space decay: results in [0, 1], an underflow to 0 is
+// 2^x with the hardware exponent unit (PTX ex2.approx.ftz.f32).  The chunked scan
+// passes x <= 0 (a masked log2-space decay: results in [0, 1], an underflow to 0 is
 // the intended limit), except stage 4's diagonal-block reference factor,
-// whose argument is at most 14.
+// whose argument is at most 14.  The layer operators pass any x: decays as they
+// are given, and sigmoid's argument of either sign, whose overflow to infinity
+// gives the reciprocal's 0.
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));

@@ -7,7 +7,7 @@
 // registers, so each input is read once plus W - 1 tokens of overlap per stretch;
 // neighbouring threads read neighbouring bytes of one token's row.  The tokens arrive
 // through a ring of asynchronous copies in shared memory, which keeps enough bytes in
-// flight without registers (forward 130 -> 114 us, backward 237 -> 195 us when it came).
+// flight without registers (forward 139 -> 117 us, backward 272 -> 195 us when it came).
 //
 // b8 T4096 C5376 W4 bf16, x a column slice: forward 114 us (6.2 TB/s, 0.91 of the
 // measured copy rate), backward 185 us (5.7 TB/s, 0.84; 196 us with registers for four

@@ -19,7 +19,7 @@
 // by a last kernel in a fixed order) the blocks.
 //
 // b4 T4096 C5120 N16 bf16, gated: 1.95 ms, of which (1) 0.48, (2) 0.02, (3) 1.42 ms.  (3)
-// needs 11 fp32 operations and one exponential per (t, c, n), about 0.5 ms of the pipes;
+// needs 12 fp32 operations and one exponential per (t, c, n), about 0.55 ms of the pipes;
 // it runs two warps a quarter of an SM (252 registers: 64 of dB and dC, 36 of states),
 // with the issue slots at 0.53 and the load unit's data path at 0.62.  Three blocks an SM
 // spill (2.45 to 2.9 ms), as do two channels at once (2.13 ms); stretches of four tokens

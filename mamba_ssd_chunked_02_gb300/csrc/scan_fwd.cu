@@ -9,7 +9,7 @@
 // exponential and four multiply-adds, and it is bound by those pipes and by the bytes
 // that shared memory hands to registers, not by memory: b8 T4096 C5120 N16 bf16 takes
 // 0.82 ms (1.65 TB/s; its bytes alone 0.20 ms, its exponentials 0.28 ms, its fp32
-// operations about 0.4 ms), with the load unit's data path at three quarters.
+// operations about 0.4 ms), with the load unit's data path at 0.63.
 //
 // A block turns a tile's dt and x into (d, d x) once, in fp32 in shared memory, then each
 // lane walks over the tile's tokens with its states in registers; the lanes' parts of y
@@ -412,6 +412,14 @@ scan_step_kernel(float* __restrict__ state, const TI* __restrict__ x, const TI* 
 // slices > 1: rows in turns (see await_turn), for rows between one and a few waves of
 //   the blocks the GPU holds.  b8 T4096 C5120 N16 bf16 (1280 rows, 1216 held): one slice
 //   1.12 ms (0.99 with nine blocks an SM), 4 slices 0.87, 8 slices 0.86, 16 slices 0.88.
+//   T2048, one / 8 / 16 slices: 1280 rows 526 / 426 / 442 us (fp32 603 / 506 / 519), 1760 rows
+//   602 / 579 / 600, 2560 rows 883 / 832 / 865, 3840 rows 1244 / 1236 / 1288, 6400 rows
+//   2056 / 2045 / 2135.
+// Held: 8 blocks an SM (4 from N = 64) is what registers and shared memory allow for two
+// channels an access at N = 32, and in bf16 at N = 16.  Others hold fewer: fp32 N16 and bf16
+// N8 7, fp32 N8 5, one channel an access 5 to 7.  That costs them time, nothing else: rows
+// between the true number and this one run in two waves without turns, and no wait depends
+// on how many blocks are held.
 struct Cut {
     int64_t nseg, slices, SL;
 };
