@@ -424,7 +424,8 @@ cudaError_t bwd_go(const NormArgs& a, const TI* x, const float* w, const TI* z, 
     // [2 halves][vectors a thread][3 tensors] of up to 16 bytes a thread: at most 192 KB a block
     auto go = [&](auto k, unsigned blocks, int threads, int vpt) {
         const size_t bytes = V * sizeof(TI), smem = bytes >= 4 ? (size_t)2 * vpt * 3 * bytes * threads : 0;
-        if (smem > 48 * 1024) {
+        constexpr size_t kRed = 2 * 32 * sizeof(float2);   // the kernel's static room counts against the limit too
+        if (smem + kRed > 48 * 1024) {
             cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
             if (e != cudaSuccess) return e;
         }

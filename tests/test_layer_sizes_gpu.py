@@ -162,6 +162,25 @@ def test_norm_backward_with_several_tokens_a_team(case):
     assert same(g, m2.norm_bwd(*args, ngroups=G, eps=1e-5, gate_first=first))
 
 
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("pad", [0, 2])
+def test_norm_at_every_width(dt, pad):
+    """Groups of all sizes up to 4200 in steps of 3 and of 8, and larger ones: every access width, team
+    and staging room."""
+    widths = sorted({*range(1, 4200, 3), *range(8, 4200, 8), *range(4224, 17000, 352)})
+    r = Gen(45)
+    whole = [cu(r.randn(2, 2, widths[-1] + pad, dtype=dt)) for _ in range(3)]
+    w = cu(1 + r.randn(widths[-1], scale=0.1))
+    for S in widths:
+        x, z, dy = (v[:, :, pad:pad + S] if pad else v[:, :, :S].contiguous() for v in whole)
+        y, g = m2.norm_fwd(x, w[:S], z), m2.norm_bwd(x, w[:S], z, dy)
+        ref = [f64(v) for v in (x, w[:S], z)]
+        close(y, R.norm(*ref, 1, 1e-5), f"y of {S}")
+        want = R.norm(*ref, 1, 1e-5, True, f64(dy))
+        for k in want:
+            close(g[k], want[k], f"{k} of {S}")
+
+
 # ---- scan ---------------------------------------------------------------------------------------
 
 SCAN = [  # b, T, D, N, G, dtype, softplus, D, z, bias, init, ragged, pad
