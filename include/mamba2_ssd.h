@@ -339,6 +339,7 @@ MAMBA2_API mamba2_status mamba2_ssd_bwd(const mamba2_ssd_shape* shape,
 #define MAMBA2_DEVERR_TIMEOUT_DECODE 32       /* a wait ran out in the decode kernel */
 #define MAMBA2_DEVERR_CHAIN_SCAN 64           /* mamba2_scan_fwd (mamba2_layer.h) gave up waiting
                                                  for the state of the tokens before */
+#define MAMBA2_DEVERR_TIMEOUT_PROJ8 128       /* a wait ran out in the 8-bit product (mamba2_proj.h) */
 
 /* Device-side error word.  The tensor-core kernels bound every wait; a wait
  * that runs out sets a bit here and the kernel returns early (its outputs are

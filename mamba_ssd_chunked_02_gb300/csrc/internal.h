@@ -279,6 +279,7 @@ enum : int32_t {
     kErrSelfTest = 1 << 4,     // the wait self-test's waits ran out (expected)
     kErrTimeoutDecode = 1 << 5,  // a bounded wait ran out in the decode kernel
     kErrChainScan = 1 << 6,    // the selective scan gave up waiting for the previous slice
+    kErrTimeoutProj8 = 1 << 7,  // a bounded wait ran out in the 8-bit projection
 };
 
 // Address of the current device's error word (api.cu), or null.
