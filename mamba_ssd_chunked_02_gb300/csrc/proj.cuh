@@ -143,9 +143,9 @@ struct Quant8Args {
 };
 cudaError_t launch_quant8(const Quant8Args& a, const void* x, uint8_t* q, uint8_t* s, cudaStream_t st);
 // x [M, N], pitch px: in groups along its rows (qr, sr [M, N / 128]) and along its columns
-// (qc, sc [M / 128, N]); either pair may be null.  pq: pitch of both.
+// (qc, sc [M / 128, N]); either pair may be null.  pq: pitch of both, ps: of sr.
 cudaError_t launch_quant8_both(bool bf16, int64_t M, int64_t N, const void* x, int64_t px, uint8_t* qr,
-                               uint8_t* sr, uint8_t* qc, uint8_t* sc, int64_t pq, cudaStream_t st);
+                               uint8_t* sr, int64_t ps, uint8_t* qc, uint8_t* sc, int64_t pq, cudaStream_t st);
 // e4m3 in groups along rows to e4m3 in groups along columns.
 cudaError_t launch_quant8_turn(int64_t M, int64_t N, const uint8_t* q, int64_t px, const uint8_t* s, uint8_t* qc,
                                uint8_t* sc, int64_t pq, cudaStream_t st);

@@ -28,18 +28,109 @@ constexpr int kThreads = 256;
 constexpr int BM = 128, BK = 128;
 
 // D[tmem] (+)= A B with block scales (kind::mxf8f6f4: one scale per 32 contracted values).
+// PAIR: two blocks' tensor cores on one tile, issued by the even one; every address holds for
+// both blocks' shared and tensor memory.
+template <bool PAIR>
 __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                            uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
 }
 // 32 rows of 16 bytes to 4 columns of tensor memory, the same for each 32 lanes.
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+template <bool PAIR> __device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+    if constexpr (PAIR) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+    else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+// Arrives at `bar` of this block, or of both blocks of the pair, when what was issued is done.
+template <bool PAIR> __device__ __forceinline__ void commit(uint64_t* bar) {
+    if constexpr (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+            "h"((uint16_t)3)
+            : "memory");
+    else mma_commit(bar);
+}
+template <bool PAIR> __device__ __forceinline__ void alloc_tmem(uint32_t* dst, uint32_t cols) {
+    if constexpr (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        tmem_alloc(dst, cols);
+        tmem_relinquish();
+    }
+}
+template <bool PAIR> __device__ __forceinline__ void free_tmem(uint32_t at, uint32_t cols) {
+    if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols) : "memory");
+    else tmem_dealloc(at, cols);
+}
+__device__ __forceinline__ uint32_t block_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// Every thread of the cluster's blocks meets; what they wrote before is visible behind it.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// This block's shared address, in the block of the cluster that has the given rank.
+__device__ __forceinline__ uint32_t of_block(const void* p, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// A tile into this block's shared memory, its bytes counted at a barrier of the pair's even block.
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* m, uint32_t bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(m), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+// mbar_wait_or_abort for a barrier at which the other block of a pair arrives too.
+template <bool PAIR>
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if constexpr (!PAIR) return mbar_wait_or_abort(bar, parity, abort, kWaitNs);
+    const uint32_t a = smem_u32(bar);
+    uint64_t t0 = 0;
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(a), "r"(parity), "r"(kSuspendHintNs)
+            : "memory");
+        if (ok) return true;
+        if (*abort) return false;
+        const uint64_t now = globaltimer();
+        if (!t0) t0 = now;
+        if (now - t0 > kWaitNs) {
+            *abort = 1;
+            return false;
+        }
+    }
+}
+// One lane of a warp that is whole.
+__device__ __forceinline__ bool elected() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 // 32 rows of 16 bytes: groups of 8 rows 128 bytes apart, no swizzle.
 __device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
@@ -55,22 +146,29 @@ struct Scales {
     const uint8_t* p;
     int64_t rs, ks;
     int shift, rows;
+    bool words;   // a row's four blocks are one aligned word
 };
 struct Shape {
     int R, C, kb;          // rows, columns, contracted blocks
     int tr, tiles;         // tiles along the rows, in all
+    int chunk;             // contracted blocks summed in tensor memory before they are added to the result
     int64_t ldo;
 };
 
-template <int BN> struct Cfg {
-    static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE = A_BYTES + B_BYTES;
-    static constexpr int NS = 6, NSF = 4;
+// PAIR: two blocks of a cluster share a tile of 256 x BN (128 rows and BN / 2 columns' operands each).
+template <int BN, bool PAIR> struct Cfg {
+    static constexpr int HALF = PAIR ? BN / 2 : BN;              // columns whose operand a block loads
+    static constexpr int A_BYTES = BM * BK, B_BYTES = HALF * BK;
+    static constexpr int B_BOX = (HALF + 127) / 128 * 128 * BK;  // MN-major: whole boxes of 128
+    static constexpr int STAGE = A_BYTES + (B_BOX > B_BYTES ? B_BOX : B_BYTES);
+    static constexpr int NS = 6, NSF = 2;
     static constexpr int SFB = (BN + 127) / 128;                 // scale tiles of B
     static constexpr int SF_BYTES = 512 * (1 + SFB);
     static constexpr int SMEM = 1024 + NS * STAGE + NSF * SF_BYTES;
     static constexpr uint32_t SF_COL = 2 * BN, SF_COLS = 4 * (1 + SFB);
     static constexpr uint32_t COLS = 512;
     static_assert(2 * BN + NSF * SF_COLS <= COLS, "tensor memory");
+    static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
 struct Bars {
@@ -82,36 +180,47 @@ struct Bars {
     int abort;
 };
 
-// The scales of rows r0 + lane + 32 j (j < 4) for the contracted blocks 4 set .. 4 set + 3, as
-// the 16 bytes that lane `lane` of the tensor memory's copy holds.  Behind the ends: 1.
-__device__ __forceinline__ uint4 gather_scales(const Scales& s, int r0, int set, int kb, int lane) {
+// The scales of rows r0 + lane + 32 j (j < 4) for the contracted blocks k0 .. k0 + 3, as the 16
+// bytes that lane `lane` of the tensor memory's copy holds.  Rows and blocks behind the ends
+// read the last one's: what they scale is zero or not stored.  No branches, so that all loads
+// are in flight at once (one after another they took 5300 cycles where the products take 1800).
+__device__ __forceinline__ uint4 gather_scales(const Scales& s, int r0, int k0, int kb, int lane) {
     uint32_t w[4];
+    if (s.words) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int r = r0 + lane + 32 * j;
-        w[j] = 0x7f7f7f7fu;
-        if (r < s.rows) {
-            const uint8_t* p = s.p + (int64_t)(r >> s.shift) * s.rs + (int64_t)set * 4 * s.ks;
-            uint32_t v = 0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v |= (uint32_t)(4 * set + k < kb ? __ldg(p + k * s.ks) : 0x7f) << (8 * k);
-            w[j] = v;
+        for (int j = 0; j < 4; ++j) {
+            const int r = min(r0 + lane + 32 * j, s.rows - 1);
+            w[j] = __ldg(reinterpret_cast<const uint32_t*>(s.p + (int64_t)(r >> s.shift) * s.rs + k0));
         }
+    } else {
+        uint32_t v[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = min(r0 + lane + 32 * j, s.rows - 1);
+            const uint8_t* p = s.p + (int64_t)(r >> s.shift) * s.rs;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[j][k] = __ldg(p + min(k0 + k, kb - 1) * s.ks);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = v[j][0] | v[j][1] << 8 | v[j][2] << 16 | v[j][3] << 24;
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int BN, bool A_MN, bool B_MN, typename TO>
+template <int BN, bool PAIR, bool A_MN, bool B_MN, typename TO>
 __global__ void __launch_bounds__(kThreads, 1)
 proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const Scales sa,
              const Scales sb, TO* __restrict__ out, const Shape q, int32_t* err) {
-    using C = Cfg<BN>;
+    using C = Cfg<BN, PAIR>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t* ssf = smem + C::NS * C::STAGE;
     __shared__ Bars bars;
     volatile int* abort = &bars.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = PAIR ? (int)block_rank() : 0;
+    const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x, step = PAIR ? gridDim.x >> 1 : gridDim.x;
+    constexpr int kBlocks = PAIR ? 2 : 1, kRows = BM * kBlocks;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NS; ++i) {
@@ -119,152 +228,184 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             mbar_init(&bars.empty[i], 1);
         }
         for (int i = 0; i < C::NSF; ++i) {
-            mbar_init(&bars.sf_full[i], 64);
+            mbar_init(&bars.sf_full[i], 64 * kBlocks);
             mbar_init(&bars.sf_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.acc_full[i], 1);
-            mbar_init(&bars.acc_empty[i], 128);
+            mbar_init(&bars.acc_empty[i], 128 * kBlocks);
         }
         mbar_init(&bars.drain, 1);
         bars.abort = 0;
         fence_barrier_init();
     }
-    if (warp == 1) {
-        tmem_alloc(&bars.tmem, C::COLS);
-        tmem_relinquish();
-    }
+    if (warp == 1) alloc_tmem<PAIR>(&bars.tmem, C::COLS);
+    __syncwarp();
     tc_fence_before();
-    __syncthreads();
+    if (PAIR) cluster_sync();
+    else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars.tmem;
-    const int sets = (q.kb + 3) / 4;
+    // a tile's contracted blocks in chunks of q.chunk: each goes through an accumulator of its own
 
+    // The producing and the issuing warp run whole, with one lane elected for each instruction: what
+    // the loop counts then stays in uniform registers, where the copies and products take it from
+    // (issued from a loop of one lane, four products took 650 cycles instead of 450).
     if (warp == 0) {
-        if (lane == 0) {
+        if (elected()) {
             prefetch_tmap(&tm_a);
             prefetch_tmap(&tm_b);
-            int it = 0;
-            for (int tile = blockIdx.x; tile < q.tiles; tile += gridDim.x) {
-                const int r0 = tile % q.tr * BM, c0 = tile / q.tr * BN;
-                for (int kb = 0; kb < q.kb; ++kb, ++it) {
-                    const int st = it % C::NS;
-                    if (!mbar_wait_or_abort(&bars.empty[st], (it / C::NS & 1) ^ 1, abort, kWaitNs)) goto loaded;
+        }
+        int it = 0, st = 0;
+        uint32_t phase = 1;
+        bool ok = true;
+        for (int tile = first; tile < q.tiles && ok; tile += step) {
+            const int r0 = tile % q.tr * kRows + rank * BM, c0 = tile / q.tr * BN + rank * C::HALF;
+            for (int kb = 0; kb < q.kb; ++kb, ++it) {
+                ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.empty[st], phase, abort, kWaitNs));
+                if (!ok) break;
+                if (elected()) {
                     uint8_t* a = smem + st * C::STAGE;
                     uint8_t* b = a + C::A_BYTES;
-                    mbar_arrive_expect_tx(&bars.full[st], C::STAGE);
-                    if (A_MN) tma_load_2d(a, &tm_a, &bars.full[st], r0, kb * BK);
-                    else tma_load_2d(a, &tm_a, &bars.full[st], kb * BK, r0);
-                    if (B_MN) {
-#pragma unroll
-                        for (int h = 0; h < (BN + 127) / 128; ++h)
-                            tma_load_2d(b + h * 128 * BK, &tm_b, &bars.full[st], c0 + h * 128, kb * BK);
+                    if (rank == 0) mbar_arrive_expect_tx(&bars.full[st], kBlocks * (C::A_BYTES + (B_MN ? C::B_BOX : C::B_BYTES)));
+                    if constexpr (PAIR) {
+                        const uint32_t bar = of_block(&bars.full[st], 0);
+                        tma_load_pair(a, &tm_a, bar, A_MN ? r0 : kb * BK, A_MN ? kb * BK : r0);
+                        tma_load_pair(b, &tm_b, bar, B_MN ? c0 : kb * BK, B_MN ? kb * BK : c0);
                     } else {
-                        tma_load_2d(b, &tm_b, &bars.full[st], kb * BK, c0);
+                        tma_load_2d(a, &tm_a, &bars.full[st], A_MN ? r0 : kb * BK, A_MN ? kb * BK : r0);
+                        tma_load_2d(b, &tm_b, &bars.full[st], B_MN ? c0 : kb * BK, B_MN ? kb * BK : c0);
                     }
                 }
+                __syncwarp();
+                if (++st == C::NS) st = 0, phase ^= 1;
             }
-        loaded:
-            if (*abort)   // copies in flight land before the block ends
-                for (int i = it - 1; i >= 0 && i >= it - C::NS; --i) mbar_wait(&bars.full[i % C::NS], i / C::NS & 1, kWaitNs);
+        }
+        if (!ok && lane == 0) {   // copies in flight land before the block ends
+            if (rank == 0)
+                for (int i = it - 1; i >= 0 && i >= it - C::NS; --i)
+                    mbar_wait(&bars.full[i % C::NS], i / C::NS & 1, kWaitNs);
+            else   // counted at the other block's barriers: a wait ran out long after the last was issued
+                for (int i = 0; i < 1000; ++i) __nanosleep(1000);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_mx(BM, BN, A_MN, B_MN);
+        if (rank == 0) {
+            constexpr uint32_t idesc = idesc_mx(kRows, BN, A_MN, B_MN);
             constexpr uint32_t a_step = (A_MN ? 32 * 128 : 32) >> 4, b_step = (B_MN ? 32 * 128 : 32) >> 4;
-            int it = 0, sit = 0, t = 0;
-            for (int tile = blockIdx.x; tile < q.tiles; tile += gridDim.x, ++t) {
-                const int acc = t & 1;
-                if (!mbar_wait_or_abort(&bars.acc_empty[acc], (t / 2 & 1) ^ 1, abort, kWaitNs)) break;
-                tc_fence_after();
-                const uint32_t d = tmem + acc * BN;
-                bool ok = true;
-                for (int set = 0; set < sets && ok; ++set, ++sit) {
-                    const int sf = sit % C::NSF;
-                    if (!(ok = mbar_wait_or_abort(&bars.sf_full[sf], sit / C::NSF & 1, abort, kWaitNs))) break;
+            // K-major: 8-row groups 1024 bytes apart; MN-major: the same between 8 contracted rows (one
+            // block of 128 m or n)
+            const uint64_t a0 = smem_desc_sw128(smem_u32(smem), A_MN ? 128 * BK : 16, 1024);
+            const uint64_t b0 = smem_desc_sw128(smem_u32(smem) + C::A_BYTES, B_MN ? 128 * BK : 16, 1024);
+            const uint64_t s0 = scale_desc(smem_u32(ssf));
+            int st = 0, sf = 0, t = 0;
+            uint32_t phase = 0, sf_phase = 0;
+            bool ok = true;
+            for (int tile = first; tile < q.tiles && ok; tile += step)
+                for (int k0 = 0; k0 < q.kb && ok; k0 += q.chunk, ++t) {
+                    const int acc = t & 1, k1 = min(q.kb, k0 + q.chunk);
+                    ok = __all_sync(0xffffffffu, wait<PAIR>(&bars.acc_empty[acc], (t / 2 & 1) ^ 1, abort));
+                    if (!ok) break;
                     tc_fence_after();
-                    const uint32_t at = smem_u32(ssf + sf * C::SF_BYTES), ta = tmem + C::SF_COL + sf * C::SF_COLS, tb = ta + 4;
-                    copy_scales(ta, scale_desc(at));
+                    const uint32_t d = tmem + acc * BN;
+                    for (int kb = k0; kb < k1; ++kb) {
+                        const uint32_t id4 = (kb - k0) & 3, ta = tmem + C::SF_COL + sf * C::SF_COLS;
+                        if (id4 == 0) {
+                            ok = __all_sync(0xffffffffu, wait<PAIR>(&bars.sf_full[sf], sf_phase, abort));
+                            if (!ok) break;
+                            tc_fence_after();
+                            if (elected()) {
+                                const uint64_t from = s0 + (uint32_t)(sf * (C::SF_BYTES >> 4));
 #pragma unroll
-                    for (int h = 0; h < C::SFB; ++h) copy_scales(tb + 4 * h, scale_desc(at + 512 * (1 + h)));
-                    const int end = min(q.kb, 4 * set + 4);
-                    for (int kb = 4 * set; kb < end; ++kb, ++it) {
-                        const int st = it % C::NS;
-                        if (!(ok = mbar_wait_or_abort(&bars.full[st], it / C::NS & 1, abort, kWaitNs))) break;
+                                for (int h = 0; h <= C::SFB; ++h) copy_scales<PAIR>(ta + 4 * h, from + h * (512 >> 4));
+                            }
+                            __syncwarp();
+                        }
+                        ok = __all_sync(0xffffffffu, wait<PAIR>(&bars.full[st], phase, abort));
+                        if (!ok) break;
                         tc_fence_after();
-                        const uint32_t a = smem_u32(smem + st * C::STAGE), b = a + C::A_BYTES;
-                        // K-major: 8-row groups 1024 bytes apart; MN-major: the same between 8 contracted
-                        // rows, blocks of 128 m or n one operand tile of 128 rows apart
-                        const uint64_t da = smem_desc_sw128(a, A_MN ? 128 * BK : 16, 1024);
-                        const uint64_t db = smem_desc_sw128(b, B_MN ? 128 * BK : 16, 1024);
-                        const uint32_t id = idesc | (uint32_t)(kb & 3) << 4 | (uint32_t)(kb & 3) << 29;
+                        const bool last4 = id4 == 3 || kb + 1 == k1;
+                        if (elected()) {
+                            const uint32_t at = st * (C::STAGE >> 4), id = idesc | id4 << 4 | id4 << 29;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_scaled(d, da + k * a_step, db + k * b_step, id, ta, tb, kb > 0 || k > 0);
-                        mma_commit(&bars.empty[st]);
+                            for (int k = 0; k < 4; ++k)
+                                mma_scaled<PAIR>(d, a0 + at + k * a_step, b0 + at + k * b_step, id, ta, ta + 4, kb > k0 || k > 0);
+                            commit<PAIR>(&bars.empty[st]);
+                            if (last4) commit<PAIR>(&bars.sf_empty[sf]);
+                            if (kb + 1 == k1) commit<PAIR>(&bars.acc_full[acc]);
+                        }
+                        __syncwarp();
+                        if (++st == C::NS) st = 0, phase ^= 1;
+                        if (last4 && ++sf == C::NSF) sf = 0, sf_phase ^= 1;
                     }
-                    if (ok) mma_commit(&bars.sf_empty[sf]);
                 }
-                if (!ok) break;
-                mma_commit(&bars.acc_full[acc]);
-            }
-            if (*abort) {
-                mma_commit(&bars.drain);
+            if (!ok && elected()) {
+                commit<PAIR>(&bars.drain);
                 mbar_wait(&bars.drain, 0, kWaitNs);
             }
         }
     } else if (warp < 4) {
         const Scales& s = warp == 2 ? sa : sb;
         int sit = 0;
-        for (int tile = blockIdx.x; tile < q.tiles; tile += gridDim.x) {
-            const int r0 = warp == 2 ? tile % q.tr * BM : tile / q.tr * BN;
-            for (int set = 0; set < sets; ++set, ++sit) {
-                const int sf = sit % C::NSF;
-                uint4 w[C::SFB];
+        for (int tile = first; tile < q.tiles; tile += step) {
+            const int r0 = warp == 2 ? tile % q.tr * kRows + rank * BM : tile / q.tr * BN;
+            for (int k0 = 0; k0 < q.kb; k0 += q.chunk)
+                for (int kb = k0; kb < min(q.kb, k0 + q.chunk); kb += 4, ++sit) {
+                    const int sf = sit % C::NSF;
+                    uint4 w[C::SFB];
 #pragma unroll
-                for (int h = 0; h < C::SFB; ++h)
-                    if (h == 0 || warp == 3) w[h] = gather_scales(s, r0 + 128 * h, set, q.kb, lane);
-                if (!mbar_wait_or_abort(&bars.sf_empty[sf], (sit / C::NSF & 1) ^ 1, abort, kWaitNs)) goto scaled;
-                uint4* to = reinterpret_cast<uint4*>(ssf + sf * C::SF_BYTES) + (warp == 2 ? 0 : 32) + lane;
+                    for (int h = 0; h < C::SFB; ++h)
+                        if (h == 0 || warp == 3) w[h] = gather_scales(s, r0 + 128 * h, kb, q.kb, lane);
+                    if (!mbar_wait_or_abort(&bars.sf_empty[sf], (sit / C::NSF & 1) ^ 1, abort, kWaitNs)) goto scaled;
+                    uint4* to = reinterpret_cast<uint4*>(ssf + sf * C::SF_BYTES) + (warp == 2 ? 0 : 32) + lane;
 #pragma unroll
-                for (int h = 0; h < C::SFB; ++h)
-                    if (h == 0 || warp == 3) to[32 * h] = w[h];
-                fence_proxy_async_smem();
-                mbar_arrive(&bars.sf_full[sf]);
-            }
+                    for (int h = 0; h < C::SFB; ++h)
+                        if (h == 0 || warp == 3) to[32 * h] = w[h];
+                    fence_proxy_async_smem();
+                    if constexpr (PAIR) arrive_at(of_block(&bars.sf_full[sf], 0));
+                    else mbar_arrive(&bars.sf_full[sf]);
+                }
         }
     scaled:;
     } else {
         const int quad = warp & 3;
         int t = 0;
-        for (int tile = blockIdx.x; tile < q.tiles; tile += gridDim.x, ++t) {
-            const int acc = t & 1;
-            if (!mbar_wait_or_abort(&bars.acc_full[acc], t / 2 & 1, abort, kWaitNs)) break;
-            tc_fence_after();
-            const int r = tile % q.tr * BM + quad * 32 + lane, c0 = tile / q.tr * BN;
-            const uint32_t from = tmem + acc * BN + ((uint32_t)(quad * 32) << 16);
-            TO* o = out + (int64_t)c0 * q.ldo + r;
-            const int cols = min(BN, q.C - c0);
+        bool ok = true;
+        for (int tile = first; tile < q.tiles && ok; tile += step)
+            for (int k0 = 0; k0 < q.kb; k0 += q.chunk, ++t) {
+                const int acc = t & 1;
+                if (!(ok = mbar_wait_or_abort(&bars.acc_full[acc], t / 2 & 1, abort, kWaitNs))) break;
+                tc_fence_after();
+                const int r = tile % q.tr * kRows + rank * BM + quad * 32 + lane, c0 = tile / q.tr * BN;
+                const uint32_t from = tmem + acc * BN + ((uint32_t)(quad * 32) << 16);
+                TO* o = out + (int64_t)c0 * q.ldo + r;
+                const int cols = min(BN, q.C - c0);
 #pragma unroll 1
-            for (int c = 0; c < BN; c += 32) {
-                uint32_t v[32];
-                tmem_ld32_sync(from + c, v);
-                if (r < q.R)
+                for (int c = 0; c < BN; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld32_sync(from + c, v);
+                    if (r >= q.R) continue;
+                    if (k0 > 0) {   // what this thread stored before
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (c + j < cols) v[j] = __float_as_uint(__uint_as_float(v[j]) + to_f32(o[(int64_t)(c + j) * q.ldo]));
+                    }
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (c + j < cols) o[(int64_t)(c + j) * q.ldo] = from_f32<TO>(__uint_as_float(v[j]));
+                }
+                tc_fence_before();
+                if constexpr (PAIR) arrive_at(of_block(&bars.acc_empty[acc], 0));
+                else mbar_arrive(&bars.acc_empty[acc]);
             }
-            tc_fence_before();
-            mbar_arrive(&bars.acc_empty[acc]);
-        }
     }
     __syncwarp();
     tc_fence_before();
-    __syncthreads();
+    if (PAIR) cluster_sync();
+    else __syncthreads();
     if (threadIdx.x == 0 && *abort) record_error(err, kErrTimeoutProj8);
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, C::COLS);
+        free_tmem<PAIR>(tmem, C::COLS);
     }
 }
 
@@ -275,30 +416,58 @@ bool map_of(CUtensorMap* m, const Operand& o, int64_t rows, int64_t depth, int b
     return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, o.q, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int BN, bool A_MN, bool B_MN, typename TO>
+// Contracted blocks whose sum may stay in tensor memory for an fp32 result.  The tensor cores'
+// sums lose up to 2^-23 of the sum a step, toward zero: 47 steps of 32 are off by 1.6e-7 of a
+// result's norm, 1024 by 3.5e-6 where sums in fp32 registers are off by 5e-7.
+constexpr int kChunk = 32;
+
+template <int BN, bool PAIR, bool A_MN, bool B_MN, typename TO>
 cudaError_t go(const Operand& A, const Operand& B, int64_t R, int64_t Cn, int64_t depth, TO* out, int64_t ldo,
                cudaStream_t st) {
-    using C = Cfg<BN>;
+    using C = Cfg<BN, PAIR>;
+    constexpr int kBlocks = PAIR ? 2 : 1;
     CUtensorMap ma, mb;
-    if (!map_of(&ma, A, R, depth, BM) || !map_of(&mb, B, Cn, depth, BN)) return cudaErrorInvalidValue;
-    const int64_t tr = (R + BM - 1) / BM, tiles = tr * ((Cn + BN - 1) / BN);
+    if (!map_of(&ma, A, R, depth, BM) || !map_of(&mb, B, Cn, depth, C::HALF)) return cudaErrorInvalidValue;
+    const int64_t tr = (R + BM * kBlocks - 1) / (BM * kBlocks), tiles = tr * ((Cn + BN - 1) / BN);
     if (tiles >= (int64_t(1) << 30)) return kGridLimit;
-    const Shape q{(int)R, (int)Cn, (int)((depth + BK - 1) / BK), (int)tr, (int)tiles, ldo};
-    const Scales sa{A.s, A.rs, A.ks, A.shift, (int)R}, sb{B.s, B.rs, B.ks, B.shift, (int)Cn};
-    auto k = proj8_kernel<BN, A_MN, B_MN, TO>;
+    const int kb = (int)((depth + BK - 1) / BK);
+    const Shape q{(int)R, (int)Cn, kb, (int)tr, (int)tiles, sizeof(TO) == 4 ? kChunk : kb, ldo};
+    const auto scales = [&](const Operand& o, int64_t rows) {
+        const bool words = o.ks == 1 && o.rs % 4 == 0 && kb <= o.rs && reinterpret_cast<uintptr_t>(o.s) % 4 == 0;
+        return Scales{o.s, o.rs, o.ks, o.shift, (int)rows, words};
+    };
+    const Scales sa = scales(A, R), sb = scales(B, Cn);
+    auto k = proj8_kernel<BN, PAIR, A_MN, B_MN, TO>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    k<<<(unsigned)(tiles < sm_count() ? tiles : sm_count()), kThreads, C::SMEM, st>>>(ma, mb, sa, sb, out, q,
-                                                                                     device_error_word());
-    return cudaGetLastError();
+    const int64_t most = sm_count() / kBlocks;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(kBlocks * (tiles < most ? tiles : most)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kBlocks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = PAIR ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k, ma, mb, sa, sb, out, q, device_error_word());
+}
+
+template <bool A_MN, bool B_MN, typename TO>
+cudaError_t pick(const Operand& A, const Operand& B, int64_t R, int64_t C, int64_t depth, TO* out, int64_t ldo,
+                 cudaStream_t st) {
+    if (R > 128 && C > 128) return go<224, true, A_MN, B_MN, TO>(A, B, R, C, depth, out, ldo, st);
+    return go<128, false, A_MN, B_MN, TO>(A, B, R, C, depth, out, ldo, st);
 }
 
 template <typename TO>
 cudaError_t pick(const Operand& A, const Operand& B, int64_t R, int64_t C, int64_t depth, TO* out, int64_t ldo,
                  cudaStream_t st) {
-    if (A.mn && B.mn) return go<128, true, true, TO>(A, B, R, C, depth, out, ldo, st);
-    if (A.mn) return go<128, true, false, TO>(A, B, R, C, depth, out, ldo, st);
-    return go<128, false, false, TO>(A, B, R, C, depth, out, ldo, st);
+    if (A.mn && B.mn) return pick<true, true, TO>(A, B, R, C, depth, out, ldo, st);
+    if (A.mn) return pick<true, false, TO>(A, B, R, C, depth, out, ldo, st);
+    return pick<false, false, TO>(A, B, R, C, depth, out, ldo, st);
 }
 
 }  // namespace

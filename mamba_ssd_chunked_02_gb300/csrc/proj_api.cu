@@ -89,7 +89,7 @@ Work work_of(const Proj& a, void* base) {
         at += (size_t)up(n, 256);
         return p;
     };
-    w.dyr = take(a.M * w.pn), w.sr = take(a.M * groups(a.N));
+    w.dyr = take(a.M * w.pn), w.sr = take(a.M * up(groups(a.N), 4));
     w.dyc = take(a.M * w.pn), w.sc = take(groups(a.M) * a.N);
     w.xc = take(a.M * w.pk), w.sx = take(groups(a.M) * a.K);
     w.bytes = at;
@@ -196,10 +196,10 @@ mamba2_status mamba2_proj8_bwd(const mamba2_proj8_shape* shape, const mamba2_pro
     if (!dx && !dw) return MAMBA2_OK;
     const Work k = work_of(a, workspace);
     const int64_t nb = groups(a.N), kb = groups(a.K);
-    cudaError_t c = launch_quant8_both(a.bf16, a.M, a.N, dy, a.py, dx ? k.dyr : nullptr, k.sr, dw ? k.dyc : nullptr, k.sc,
+    cudaError_t c = launch_quant8_both(a.bf16, a.M, a.N, dy, a.py, dx ? k.dyr : nullptr, k.sr, up(nb, 4), dw ? k.dyc : nullptr, k.sc,
                                        k.pn, st);
     if (c == cudaSuccess && dx) {
-        const Operand W{w, a.pw, true, w_scales, 1, kb, 7}, D{k.dyr, k.pn, false, k.sr, nb, 1, 0};
+        const Operand W{w, a.pw, true, w_scales, 1, kb, 7}, D{k.dyr, k.pn, false, k.sr, up(nb, 4), 1, 0};
         c = launch_proj8(W, D, a.K, a.M, a.N, dx, a.K, a.bf16, st);
     }
     if (c == cudaSuccess && dw) {

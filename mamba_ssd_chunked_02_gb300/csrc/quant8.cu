@@ -24,6 +24,7 @@ struct Tile {
     Tok sq;                  // of q (both outputs)
     const uint8_t* s_in;     // scales of an e4m3 input [M, nb]
     uint8_t *qr, *sr, *qc, *sc;
+    int64_t ps;              // bytes between the rows of sr
 };
 
 // Thread (tx, ty) has rows ty + 16 i and columns 8 tx + j (VEC: one access) or tx + 16 j.
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) quant8_kernel(const TI* __restrict__
             for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             const uint32_t byte = scale_byte(top);
             const float f = scale_inverse(byte);
-            if (tx == 0 && ty + 16 * i < rows) p.sr[(m0 + ty + 16 * i) * p.nb + nb] = (uint8_t)byte;
+            if (tx == 0 && ty + 16 * i < rows) p.sr[(m0 + ty + 16 * i) * p.ps + nb] = (uint8_t)byte;
             store(p.qr, i, [&](int) { return f; });
         }
     }
@@ -176,19 +177,19 @@ template <int MODE> cudaError_t go(bool bf16, const void* x, const Tile& p, cuda
 }  // namespace
 
 cudaError_t launch_quant8(const Quant8Args& a, const void* x, uint8_t* q, uint8_t* s, cudaStream_t st) {
-    const Tile p{a.b * a.T, a.D, (uint32_t)a.T, 0, a.sx, a.sq, nullptr, q, s, nullptr, nullptr};
+    const Tile p{a.b * a.T, a.D, (uint32_t)a.T, 0, a.sx, a.sq, nullptr, q, s, nullptr, nullptr, (a.D + kGroup - 1) / kGroup};
     return a.block ? go<kBlock>(a.bf16, x, p, st) : go<kRow>(a.bf16, x, p, st);
 }
 
 cudaError_t launch_quant8_both(bool bf16, int64_t M, int64_t N, const void* x, int64_t px, uint8_t* qr, uint8_t* sr,
-                               uint8_t* qc, uint8_t* sc, int64_t pq, cudaStream_t st) {
-    const Tile p{M, N, (uint32_t)M, 0, Tok{0, px}, Tok{0, pq}, nullptr, qr, sr, qc, sc};
+                               int64_t ps, uint8_t* qc, uint8_t* sc, int64_t pq, cudaStream_t st) {
+    const Tile p{M, N, (uint32_t)M, 0, Tok{0, px}, Tok{0, pq}, nullptr, qr, sr, qc, sc, ps};
     return !qc ? go<kRow>(bf16, x, p, st) : !qr ? go<kCol>(bf16, x, p, st) : go<kRow | kCol>(bf16, x, p, st);
 }
 
 cudaError_t launch_quant8_turn(int64_t M, int64_t N, const uint8_t* q, int64_t px, const uint8_t* s, uint8_t* qc,
                                uint8_t* sc, int64_t pq, cudaStream_t st) {
-    const Tile p{M, N, (uint32_t)M, 0, Tok{0, px}, Tok{0, pq}, s, nullptr, nullptr, qc, sc};
+    const Tile p{M, N, (uint32_t)M, 0, Tok{0, px}, Tok{0, pq}, s, nullptr, nullptr, qc, sc, 0};
     return go<uint8_t, kCol>(q, p, st);
 }
 
