@@ -162,7 +162,7 @@ struct Operand {
     int64_t rs, ks;
     int shift;
 };
-// out[j * ldo + i] = sum_k A[i, k] B[j, k], i < R, j < C, in bf16 or fp32.
+// out[i * ldo + j] = sum_k A[i, k] B[j, k], i < R, j < C, in bf16 or fp32.
 cudaError_t launch_proj8(const Operand& A, const Operand& B, int64_t R, int64_t C, int64_t depth, void* out,
                          int64_t ldo, bool bf16, cudaStream_t st);
 

@@ -1,17 +1,22 @@
 // proj8.cu -- matrix product of e4m3 operands with power-of-two scales (include/mamba2_proj.h).
 //
-//   out[j, i] = sum_k A[i, k] sA[i, k / 128] B[j, k] sB[j, k / 128]
+//   out[i, j] = sum_k A[i, k] sA[i, k / 128] B[j, k] sB[j, k / 128]
 //
 // The scales are e8m0 bytes, which the block-scaled tcgen05.mma applies inside the tensor
 // core: they are staged in shared memory four contracted blocks at a time (one 32-bit word a
 // row), copied to tensor memory (tcgen05.cp) and picked by the instruction's scale id.
 //
-// i, the index that is contiguous in the result, is the accumulator's lane, so that a warp
-// stores 32 neighbours; A is therefore the weight (forward: rows of W; dx: columns of W, read
-// in place as an MN-major operand; dw: columns of x).
+// Operands are read in place in either order (the contracted index inside or outside), so that
+// no transposed copy is made: the forward product takes x and w with the contracted index
+// inside, dx = dy w takes w with it outside, dw = dy^T x both.
 //
+// proj8_kernel: a cluster of PAIRS pairs of blocks; a pair's two tensor cores work on one tile
+// of 256 x BN (cta_group::2), and the pairs, one below the other, share B's tile by multicast.
 // Warp roles: 0 TMA, 1 MMA (and tensor memory), 2 scales of A, 3 scales of B, 4-7 epilogue.
 #include <cuda_bf16.h>
+
+#include <algorithm>
+#include <atomic>
 
 #include "internal.h"
 #include "proj.cuh"
@@ -25,6 +30,8 @@ using namespace tc;
 
 constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s: far beyond any legitimate wait
 constexpr int kThreads = 256;
+constexpr int kDevices = 64;
+constexpr int kPanel = 8;
 constexpr int BM = 128, BK = 128;
 
 // D[tmem] (+)= A B with block scales (kind::mxf8f6f4: one scale per 32 contracted values).
@@ -53,12 +60,12 @@ template <bool PAIR> __device__ __forceinline__ void copy_scales(uint32_t tmem, 
     if constexpr (PAIR) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
     else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
-// Arrives at `bar` of this block, or of both blocks of the pair, when what was issued is done.
-template <bool PAIR> __device__ __forceinline__ void commit(uint64_t* bar) {
+// Arrives at `bar` of this block, or of the cluster's blocks in `mask`, when what was issued is done.
+template <bool PAIR> __device__ __forceinline__ void commit(uint64_t* bar, uint32_t mask = 0) {
     if constexpr (PAIR)
         asm volatile(
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
-            "h"((uint16_t)3)
+            "h"((uint16_t)mask)
             : "memory");
     else mma_commit(bar);
 }
@@ -93,7 +100,8 @@ __device__ __forceinline__ uint32_t of_block(const void* p, uint32_t rank) {
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// A tile into this block's shared memory, its bytes counted at a barrier of the pair's even block.
+// A tile into this block's shared memory, its bytes counted at a barrier of the pair's even block;
+// or into that of every block in `mask`, each counted at its own pair's.
 __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* m, uint32_t bar, int x, int y) {
     asm volatile(
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
@@ -126,6 +134,18 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
         }
     }
 }
+__device__ __forceinline__ void tma_load_pairs(void* dst, const CUtensorMap* m, uint32_t bar, int x, int y, uint32_t mask) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
+        " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
+        "l"(m), "r"(bar), "r"(x), "r"(y), "h"((uint16_t)mask)
+        : "memory");
+}
+__device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* m, const void* src, int x, int y) {
+    asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(m),
+                 "r"(smem_u32(src)), "r"(x), "r"(y)
+                 : "memory");
+}
 // One lane of a warp that is whole.
 __device__ __forceinline__ bool elected() {
     uint32_t p;
@@ -151,24 +171,30 @@ struct Scales {
 struct Shape {
     int R, C, kb;          // rows, columns, contracted blocks
     int tr, tiles;         // tiles along the rows, in all
+    int panel;             // tiles of a panel along the columns
     int chunk;             // contracted blocks summed in tensor memory before they are added to the result
+    bool copied;           // the result's rows start on 16 bytes
     int64_t ldo;
 };
 
-// PAIR: two blocks of a cluster share a tile of 256 x BN (128 rows and BN / 2 columns' operands each).
-template <int BN, bool PAIR> struct Cfg {
-    static constexpr int HALF = PAIR ? BN / 2 : BN;              // columns whose operand a block loads
-    static constexpr int A_BYTES = BM * BK, B_BYTES = HALF * BK;
-    static constexpr int B_BOX = (HALF + 127) / 128 * 128 * BK;  // MN-major: whole boxes of 128
-    static constexpr int STAGE = A_BYTES + (B_BOX > B_BYTES ? B_BOX : B_BYTES);
-    static constexpr int NS = 6, NSF = 2;
+// PAIRS pairs of blocks: each pair a tile of 256 x BN, a block 128 rows of A and BN / 2 columns of B.
+template <int BN, int PAIRS, bool B_MN, int ES> struct Cfg {
+    static constexpr int HALF = BN / 2;
+    static constexpr int A_BYTES = BM * BK;
+    // columns of B in a stage: MN-major copies are whole boxes of 128
+    static constexpr int B_BYTES = (B_MN ? 128 : HALF) * BK, B_PART = B_BYTES / PAIRS;
+    static constexpr int STAGE = A_BYTES + B_BYTES;
+    static constexpr int NSF = 2;
     static constexpr int SFB = (BN + 127) / 128;                 // scale tiles of B
     static constexpr int SF_BYTES = 512 * (1 + SFB);
-    static constexpr int SMEM = 1024 + NS * STAGE + NSF * SF_BYTES;
+    static constexpr int OUT = 32 * 32 * ES, OUT_BYTES = 4 * 2 * OUT;   // two parts of 32 x 32 a warp of the epilogue
+    static constexpr int FIXED = 1024 + NSF * SF_BYTES + OUT_BYTES;
+    static constexpr int NS = (227 * 1024 - FIXED - 512) / STAGE < 6 ? (227 * 1024 - FIXED - 512) / STAGE : 6;
+    static constexpr int SMEM = FIXED + NS * STAGE;
     static constexpr uint32_t SF_COL = 2 * BN, SF_COLS = 4 * (1 + SFB);
     static constexpr uint32_t COLS = 512;
     static_assert(2 * BN + NSF * SF_COLS <= COLS, "tensor memory");
-    static_assert(SMEM <= 227 * 1024, "shared memory");
+    static_assert(STAGE % 1024 == 0 && B_PART % 1024 == 0 && HALF <= 128, "tiles");
 };
 
 struct Bars {
@@ -207,33 +233,50 @@ __device__ __forceinline__ uint4 gather_scales(const Scales& s, int r0, int k0, 
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int BN, bool PAIR, bool A_MN, bool B_MN, typename TO>
+template <int BN, int PAIRS, bool A_MN, bool B_MN, typename TO>
 __global__ void __launch_bounds__(kThreads, 1)
-proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const Scales sa,
-             const Scales sb, TO* __restrict__ out, const Shape q, int32_t* err) {
-    using C = Cfg<BN, PAIR>;
+proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+             const __grid_constant__ CUtensorMap tm_o, const Scales sa, const Scales sb, TO* __restrict__ out, const Shape q,
+             int32_t* err) {
+    using C = Cfg<BN, PAIRS, B_MN, sizeof(TO)>;
+    constexpr bool PAIR = true;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    uint8_t* ssf = smem + C::NS * C::STAGE;
+    uint8_t* sout = smem + C::NS * C::STAGE;
+    uint8_t* ssf = sout + C::OUT_BYTES;
     __shared__ Bars bars;
     volatile int* abort = &bars.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = PAIR ? (int)block_rank() : 0;
-    const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x, step = PAIR ? gridDim.x >> 1 : gridDim.x;
-    constexpr int kBlocks = PAIR ? 2 : 1, kRows = BM * kBlocks;
+    // rank in the pair, the pair of the cluster, the pair's even block, which counts its copies
+    const int rank = (int)block_rank() & 1, pair = (int)block_rank() >> 1;
+    const uint32_t even = block_rank() & ~1u;
+    const int first = blockIdx.x / (2 * PAIRS), step = gridDim.x / (2 * PAIRS);
+    constexpr int kRows = 2 * BM, kAll = (1 << 2 * PAIRS) - 1;
+    const uint32_t both = 3u << (2 * pair);
+    // Tiles go down panels of q.panel columns of tiles, a row of the panel at a time: the clusters that
+    // run side by side then share few rows of A and of B.
+    const int tc = q.tiles / q.tr, each = q.panel * q.tr;
+    const auto row_of = [&](int tile) {
+        const int p = tile / each, in = tile - p * each, w = min(q.panel, tc - p * q.panel);
+        return (in / w * PAIRS + pair) * kRows + rank * BM;
+    };
+    const auto col_of = [&](int tile) {
+        const int p = tile / each, in = tile - p * each, w = min(q.panel, tc - p * q.panel);
+        return (p * q.panel + in % w) * BN;
+    };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NS; ++i) {
             mbar_init(&bars.full[i], 1);
-            mbar_init(&bars.empty[i], 1);
+            mbar_init(&bars.empty[i], PAIRS);   // every pair that the copy reaches
         }
         for (int i = 0; i < C::NSF; ++i) {
-            mbar_init(&bars.sf_full[i], 64 * kBlocks);
+            mbar_init(&bars.sf_full[i], 128);
             mbar_init(&bars.sf_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.acc_full[i], 1);
-            mbar_init(&bars.acc_empty[i], 128 * kBlocks);
+            mbar_init(&bars.acc_empty[i], 256);
         }
         mbar_init(&bars.drain, 1);
         bars.abort = 0;
@@ -242,11 +285,9 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     if (warp == 1) alloc_tmem<PAIR>(&bars.tmem, C::COLS);
     __syncwarp();
     tc_fence_before();
-    if (PAIR) cluster_sync();
-    else __syncthreads();
+    cluster_sync();
     tc_fence_after();
     const uint32_t tmem = bars.tmem;
-    // a tile's contracted blocks in chunks of q.chunk: each goes through an accumulator of its own
 
     // The producing and the issuing warp run whole, with one lane elected for each instruction: what
     // the loop counts then stays in uniform registers, where the copies and products take it from
@@ -260,21 +301,21 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         uint32_t phase = 1;
         bool ok = true;
         for (int tile = first; tile < q.tiles && ok; tile += step) {
-            const int r0 = tile % q.tr * kRows + rank * BM, c0 = tile / q.tr * BN + rank * C::HALF;
+            const int r0 = row_of(tile), c0 = col_of(tile) + rank * C::HALF;
             for (int kb = 0; kb < q.kb; ++kb, ++it) {
                 ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.empty[st], phase, abort, kWaitNs));
                 if (!ok) break;
                 if (elected()) {
                     uint8_t* a = smem + st * C::STAGE;
                     uint8_t* b = a + C::A_BYTES;
-                    if (rank == 0) mbar_arrive_expect_tx(&bars.full[st], kBlocks * (C::A_BYTES + (B_MN ? C::B_BOX : C::B_BYTES)));
-                    if constexpr (PAIR) {
-                        const uint32_t bar = of_block(&bars.full[st], 0);
-                        tma_load_pair(a, &tm_a, bar, A_MN ? r0 : kb * BK, A_MN ? kb * BK : r0);
+                    if (rank == 0) mbar_arrive_expect_tx(&bars.full[st], 2 * C::STAGE);
+                    const uint32_t bar = of_block(&bars.full[st], even);
+                    tma_load_pair(a, &tm_a, bar, A_MN ? r0 : kb * BK, A_MN ? kb * BK : r0);
+                    if constexpr (PAIRS == 1) {
                         tma_load_pair(b, &tm_b, bar, B_MN ? c0 : kb * BK, B_MN ? kb * BK : c0);
-                    } else {
-                        tma_load_2d(a, &tm_a, &bars.full[st], A_MN ? r0 : kb * BK, A_MN ? kb * BK : r0);
-                        tma_load_2d(b, &tm_b, &bars.full[st], B_MN ? c0 : kb * BK, B_MN ? kb * BK : c0);
+                    } else {   // this pair's part of the tile, for the blocks of the same rank
+                        const int at = kb * BK + (B_MN ? pair * (BK / PAIRS) : 0), col = c0 + (B_MN ? 0 : pair * (C::HALF / PAIRS));
+                        tma_load_pairs(b + pair * C::B_PART, &tm_b, bar, B_MN ? col : at, B_MN ? at : col, (0x55u & kAll) << rank);
                     }
                 }
                 __syncwarp();
@@ -329,9 +370,9 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 mma_scaled<PAIR>(d, a0 + at + k * a_step, b0 + at + k * b_step, id, ta, ta + 4, kb > k0 || k > 0);
-                            commit<PAIR>(&bars.empty[st]);
-                            if (last4) commit<PAIR>(&bars.sf_empty[sf]);
-                            if (kb + 1 == k1) commit<PAIR>(&bars.acc_full[acc]);
+                            commit<PAIR>(&bars.empty[st], kAll);
+                            if (last4) commit<PAIR>(&bars.sf_empty[sf], both);
+                            if (kb + 1 == k1) commit<PAIR>(&bars.acc_full[acc], both);
                         }
                         __syncwarp();
                         if (++st == C::NS) st = 0, phase ^= 1;
@@ -339,7 +380,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                     }
                 }
             if (!ok && elected()) {
-                commit<PAIR>(&bars.drain);
+                commit<PAIR>(&bars.drain, 1u << even);
                 mbar_wait(&bars.drain, 0, kWaitNs);
             }
         }
@@ -347,7 +388,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         const Scales& s = warp == 2 ? sa : sb;
         int sit = 0;
         for (int tile = first; tile < q.tiles; tile += step) {
-            const int r0 = warp == 2 ? tile % q.tr * kRows + rank * BM : tile / q.tr * BN;
+            const int r0 = warp == 2 ? row_of(tile) : col_of(tile);
             for (int k0 = 0; k0 < q.kb; k0 += q.chunk)
                 for (int kb = k0; kb < min(q.kb, k0 + q.chunk); kb += 4, ++sit) {
                     const int sf = sit % C::NSF;
@@ -361,47 +402,83 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                     for (int h = 0; h < C::SFB; ++h)
                         if (h == 0 || warp == 3) to[32 * h] = w[h];
                     fence_proxy_async_smem();
-                    if constexpr (PAIR) arrive_at(of_block(&bars.sf_full[sf], 0));
-                    else mbar_arrive(&bars.sf_full[sf]);
+                    arrive_at(of_block(&bars.sf_full[sf], even));
                 }
         }
     scaled:;
     } else {
+        // A warp has 32 lanes of tensor memory, the tile's rows, and moves them 32 columns at a time:
+        // rounded, into shared memory, and by TMA to the result (coalesced stores where the result's
+        // rows do not start on 16 bytes).
         const int quad = warp & 3;
-        int t = 0;
+        uint8_t* stage = sout + quad * 2 * C::OUT;
+        int t = 0, n = 0;
         bool ok = true;
         for (int tile = first; tile < q.tiles && ok; tile += step)
             for (int k0 = 0; k0 < q.kb; k0 += q.chunk, ++t) {
                 const int acc = t & 1;
-                if (!(ok = mbar_wait_or_abort(&bars.acc_full[acc], t / 2 & 1, abort, kWaitNs))) break;
+                ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.acc_full[acc], t / 2 & 1, abort, kWaitNs));
+                if (!ok) break;
                 tc_fence_after();
-                const int r = tile % q.tr * kRows + rank * BM + quad * 32 + lane, c0 = tile / q.tr * BN;
+                const int r0 = row_of(tile) + quad * 32, c0 = col_of(tile);
                 const uint32_t from = tmem + acc * BN + ((uint32_t)(quad * 32) << 16);
-                TO* o = out + (int64_t)c0 * q.ldo + r;
-                const int cols = min(BN, q.C - c0);
+                if (k0 > 0) {   // what is added to has been written
+                    if (lane == 0) bulk_wait<0>();
+                    __syncwarp();
+                }
 #pragma unroll 1
                 for (int c = 0; c < BN; c += 32) {
                     uint32_t v[32];
                     tmem_ld32_sync(from + c, v);
-                    if (r >= q.R) continue;
-                    if (k0 > 0) {   // what this thread stored before
+                    if (r0 >= q.R || c0 + c >= q.C) continue;
+                    uint8_t* part = stage + n * C::OUT;
+                    n ^= 1;
+                    if (lane == 0) bulk_wait_read<1>();   // the copy before the last has read its part
+                    __syncwarp();
+                    uint4* row = reinterpret_cast<uint4*>(part + lane * 32 * sizeof(TO));
+                    // 16-byte pieces in the places where a swizzled copy looks for them
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (c + j < cols) v[j] = __float_as_uint(__uint_as_float(v[j]) + to_f32(o[(int64_t)(c + j) * q.ldo]));
+                    for (int p = 0; p < (int)sizeof(TO) * 2; ++p) {
+                        if constexpr (sizeof(TO) == 2)
+                            row[p ^ (lane >> 1 & 3)] =
+                                make_uint4(pack_bf16x2(__uint_as_float(v[8 * p]), __uint_as_float(v[8 * p + 1])),
+                                           pack_bf16x2(__uint_as_float(v[8 * p + 2]), __uint_as_float(v[8 * p + 3])),
+                                           pack_bf16x2(__uint_as_float(v[8 * p + 4]), __uint_as_float(v[8 * p + 5])),
+                                           pack_bf16x2(__uint_as_float(v[8 * p + 6]), __uint_as_float(v[8 * p + 7])));
+                        else
+                            row[p ^ (lane & 7)] = make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
                     }
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (c + j < cols) o[(int64_t)(c + j) * q.ldo] = from_f32<TO>(__uint_as_float(v[j]));
+                    if (q.copied) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (k0 == 0) tma_store_2d(&tm_o, part, c0 + c, r0);
+                            else tma_reduce_add_2d(&tm_o, part, c0 + c, r0);
+                            bulk_commit();
+                        }
+                    } else {
+                        __syncwarp();
+                        const int rows = min(32, q.R - r0);
+                        TO* o = out + (int64_t)r0 * q.ldo + c0 + c + lane;
+                        if (c0 + c + lane < q.C)
+#pragma unroll 8
+                            for (int r = 0; r < rows; ++r, o += q.ldo) {
+                                constexpr int E = 16 / sizeof(TO);
+                                const int piece = (lane / E) ^ (sizeof(TO) == 2 ? r >> 1 & 3 : r & 7);
+                                const TO w = reinterpret_cast<const TO*>(part)[r * 32 + piece * E + lane % E];
+                                *o = k0 == 0 ? w : from_f32<TO>(to_f32(w) + to_f32(*o));
+                            }
+                        __syncwarp();
+                    }
                 }
                 tc_fence_before();
-                if constexpr (PAIR) arrive_at(of_block(&bars.acc_empty[acc], 0));
-                else mbar_arrive(&bars.acc_empty[acc]);
+                arrive_at(of_block(&bars.acc_empty[acc], even));
             }
+        if (lane == 0) bulk_wait<0>();   // copies out of this block's shared memory
     }
     __syncwarp();
     tc_fence_before();
-    if (PAIR) cluster_sync();
-    else __syncthreads();
+    cluster_sync();
     if (threadIdx.x == 0 && *abort) record_error(err, kErrTimeoutProj8);
     if (warp == 1) {
         tc_fence_after();
@@ -409,11 +486,26 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     }
 }
 
-bool map_of(CUtensorMap* m, const Operand& o, int64_t rows, int64_t depth, int box_rows) {
+// `across` contracted values (MN-major) or rows (K-major) a copy; 128 of the inner index.
+bool map_of(CUtensorMap* m, const Operand& o, int64_t rows, int64_t depth, int across) {
     const uint64_t dims[2] = {(uint64_t)(o.mn ? rows : depth), (uint64_t)(o.mn ? depth : rows)};
     const uint64_t strides[1] = {(uint64_t)o.pitch};
-    const uint32_t box[2] = {128, (uint32_t)(o.mn ? BK : box_rows)};
+    const uint32_t box[2] = {128, (uint32_t)across};
     return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, o.q, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Clusters of `blocks` that the device holds at once (`known`: what was found before, by device).
+template <typename K> int resident_clusters(K k, cudaLaunchConfig_t cfg, int blocks, std::atomic<int>* known) {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return std::max(1, sm_count() / blocks);
+    if ((n = known[dev].load(std::memory_order_relaxed))) return n;
+    cfg.gridDim = dim3((unsigned)(sm_count() / blocks * blocks));
+    if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        n = std::max(1, sm_count() / blocks);
+    }
+    known[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 // Contracted blocks whose sum may stay in tensor memory for an fp32 result.  The tensor cores'
@@ -421,28 +513,36 @@ bool map_of(CUtensorMap* m, const Operand& o, int64_t rows, int64_t depth, int b
 // result's norm, 1024 by 3.5e-6 where sums in fp32 registers are off by 5e-7.
 constexpr int kChunk = 32;
 
-template <int BN, bool PAIR, bool A_MN, bool B_MN, typename TO>
+template <int BN, int PAIRS, bool A_MN, bool B_MN, typename TO>
 cudaError_t go(const Operand& A, const Operand& B, int64_t R, int64_t Cn, int64_t depth, TO* out, int64_t ldo,
                cudaStream_t st) {
-    using C = Cfg<BN, PAIR>;
-    constexpr int kBlocks = PAIR ? 2 : 1;
-    CUtensorMap ma, mb;
-    if (!map_of(&ma, A, R, depth, BM) || !map_of(&mb, B, Cn, depth, C::HALF)) return cudaErrorInvalidValue;
-    const int64_t tr = (R + BM * kBlocks - 1) / (BM * kBlocks), tiles = tr * ((Cn + BN - 1) / BN);
+    using C = Cfg<BN, PAIRS, B_MN, sizeof(TO)>;
+    CUtensorMap ma, mb, mo;
+    if (!map_of(&ma, A, R, depth, 128) || !map_of(&mb, B, Cn, depth, (B_MN ? BK : C::HALF) / PAIRS))
+        return cudaErrorInvalidValue;
+    // the result by copies of 32 x 32, where its rows start on 16 bytes
+    const uint64_t dims[2] = {(uint64_t)Cn, (uint64_t)R};
+    const uint64_t strides[1] = {(uint64_t)((R == 1 ? (Cn + 15) / 16 * 16 : ldo) * sizeof(TO))};
+    const uint32_t box[2] = {32, 32};
+    const bool copied = reinterpret_cast<uintptr_t>(out) % 16 == 0 && strides[0] % 16 == 0 &&
+                        make_tmap(&mo, sizeof(TO) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, out,
+                                  2, dims, strides, box,
+                                  sizeof(TO) == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+    if (!copied) mo = ma;   // not used
+    constexpr int kRows = 2 * BM * PAIRS, kBlocks = 2 * PAIRS;
+    const int64_t tr = (R + kRows - 1) / kRows, tiles = tr * ((Cn + BN - 1) / BN);
     if (tiles >= (int64_t(1) << 30)) return kGridLimit;
     const int kb = (int)((depth + BK - 1) / BK);
-    const Shape q{(int)R, (int)Cn, kb, (int)tr, (int)tiles, sizeof(TO) == 4 ? kChunk : kb, ldo};
+    const Shape q{(int)R, (int)Cn, kb, (int)tr, (int)tiles, kPanel, sizeof(TO) == 4 ? kChunk : kb, copied, ldo};
     const auto scales = [&](const Operand& o, int64_t rows) {
         const bool words = o.ks == 1 && o.rs % 4 == 0 && kb <= o.rs && reinterpret_cast<uintptr_t>(o.s) % 4 == 0;
         return Scales{o.s, o.rs, o.ks, o.shift, (int)rows, words};
     };
     const Scales sa = scales(A, R), sb = scales(B, Cn);
-    auto k = proj8_kernel<BN, PAIR, A_MN, B_MN, TO>;
+    auto k = proj8_kernel<BN, PAIRS, A_MN, B_MN, TO>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    const int64_t most = sm_count() / kBlocks;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(kBlocks * (tiles < most ? tiles : most)));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = st;
@@ -451,22 +551,25 @@ cudaError_t go(const Operand& A, const Operand& B, int64_t R, int64_t Cn, int64_
     attr[0].val.clusterDim.x = kBlocks;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = PAIR ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k, ma, mb, sa, sb, out, q, device_error_word());
+    cfg.numAttrs = 1;
+    static std::atomic<int> known[kDevices];
+    const int64_t most = resident_clusters(k, cfg, kBlocks, known);
+    cfg.gridDim = dim3((unsigned)(kBlocks * (tiles < most ? tiles : most)));
+    return cudaLaunchKernelEx(&cfg, k, ma, mb, mo, sa, sb, out, q, device_error_word());
 }
 
 template <bool A_MN, bool B_MN, typename TO>
 cudaError_t pick(const Operand& A, const Operand& B, int64_t R, int64_t C, int64_t depth, TO* out, int64_t ldo,
                  cudaStream_t st) {
-    if (R > 128 && C > 128) return go<224, true, A_MN, B_MN, TO>(A, B, R, C, depth, out, ldo, st);
-    return go<128, false, A_MN, B_MN, TO>(A, B, R, C, depth, out, ldo, st);
+    if (R > 256) return go<224, 2, A_MN, B_MN, TO>(A, B, R, C, depth, out, ldo, st);
+    return go<224, 1, A_MN, B_MN, TO>(A, B, R, C, depth, out, ldo, st);
 }
 
 template <typename TO>
 cudaError_t pick(const Operand& A, const Operand& B, int64_t R, int64_t C, int64_t depth, TO* out, int64_t ldo,
                  cudaStream_t st) {
     if (A.mn && B.mn) return pick<true, true, TO>(A, B, R, C, depth, out, ldo, st);
-    if (A.mn) return pick<true, false, TO>(A, B, R, C, depth, out, ldo, st);
+    if (B.mn) return pick<false, true, TO>(A, B, R, C, depth, out, ldo, st);
     return pick<false, false, TO>(A, B, R, C, depth, out, ldo, st);
 }
 

@@ -165,7 +165,7 @@ mamba2_status mamba2_proj8_fwd(const mamba2_proj8_shape* shape, const mamba2_pro
         return MAMBA2_ERR_INVALID_ARG;
     const int64_t kb = groups(a.K);
     const Operand W{w, a.pw, false, w_scales, kb, 1, 7}, X{x, a.px, false, x_scales, kb, 1, 0};
-    return from_cuda(launch_proj8(W, X, a.N, a.M, a.K, y, a.py, a.bf16, static_cast<cudaStream_t>(stream)));
+    return from_cuda(launch_proj8(X, W, a.M, a.N, a.K, y, a.py, a.bf16, static_cast<cudaStream_t>(stream)));
 }
 
 size_t mamba2_proj8_bwd_workspace_size(const mamba2_proj8_shape* shape) {
@@ -200,12 +200,12 @@ mamba2_status mamba2_proj8_bwd(const mamba2_proj8_shape* shape, const mamba2_pro
                                        k.pn, st);
     if (c == cudaSuccess && dx) {
         const Operand W{w, a.pw, true, w_scales, 1, kb, 7}, D{k.dyr, k.pn, false, k.sr, up(nb, 4), 1, 0};
-        c = launch_proj8(W, D, a.K, a.M, a.N, dx, a.K, a.bf16, st);
+        c = launch_proj8(D, W, a.M, a.K, a.N, dx, a.K, a.bf16, st);
     }
     if (c == cudaSuccess && dw) {
         c = launch_quant8_turn(a.M, a.K, x, a.px, x_scales, k.xc, k.sx, k.pk, st);
         const Operand X{k.xc, k.pk, true, k.sx, 1, a.K, 0}, D{k.dyc, k.pn, true, k.sc, 1, a.N, 0};
-        if (c == cudaSuccess) c = launch_proj8(X, D, a.K, a.N, a.M, dw, a.K, false, st);
+        if (c == cudaSuccess) c = launch_proj8(D, X, a.N, a.K, a.M, dw, a.K, false, st);
     }
     return from_cuda(c);
 }
