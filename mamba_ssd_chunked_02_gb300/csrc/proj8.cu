@@ -12,7 +12,8 @@
 //
 // proj8_kernel: a cluster of PAIRS pairs of blocks; a pair's two tensor cores work on one tile
 // of 256 x BN (cta_group::2), and the pairs, one below the other, share B's tile by multicast.
-// Warp roles: 0 TMA, 1 MMA (and tensor memory), 2 scales of A, 3 scales of B, 4-7 epilogue.
+// Warp roles: 0 TMA, 1 MMA (and tensor memory), 2 scales of A, 3 scales of B, 4-11 epilogue,
+// 12 hands the scales to the tensor cores.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -29,9 +30,9 @@ namespace {
 using namespace tc;
 
 constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s: far beyond any legitimate wait
-constexpr int kThreads = 256;
+constexpr int kThreads = 416;
 constexpr int kDevices = 64;
-constexpr int kPanel = 8;
+constexpr int kPanel = 12;
 constexpr int BM = 128, BK = 128;
 
 // D[tmem] (+)= A B with block scales (kind::mxf8f6f4: one scale per 32 contracted values).
@@ -109,31 +110,6 @@ __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* m, u
         "l"(m), "r"(bar), "r"(x), "r"(y)
         : "memory");
 }
-// mbar_wait_or_abort for a barrier at which the other block of a pair arrives too.
-template <bool PAIR>
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    if constexpr (!PAIR) return mbar_wait_or_abort(bar, parity, abort, kWaitNs);
-    const uint32_t a = smem_u32(bar);
-    uint64_t t0 = 0;
-    for (;;) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(a), "r"(parity), "r"(kSuspendHintNs)
-            : "memory");
-        if (ok) return true;
-        if (*abort) return false;
-        const uint64_t now = globaltimer();
-        if (!t0) t0 = now;
-        if (now - t0 > kWaitNs) {
-            *abort = 1;
-            return false;
-        }
-    }
-}
 __device__ __forceinline__ void tma_load_pairs(void* dst, const CUtensorMap* m, uint32_t bar, int x, int y, uint32_t mask) {
     asm volatile(
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
@@ -184,10 +160,11 @@ template <int BN, int PAIRS, bool B_MN, int ES> struct Cfg {
     // columns of B in a stage: MN-major copies are whole boxes of 128
     static constexpr int B_BYTES = (B_MN ? 128 : HALF) * BK, B_PART = B_BYTES / PAIRS;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int NSF = 2;
+    static constexpr int NSF = 4;
     static constexpr int SFB = (BN + 127) / 128;                 // scale tiles of B
     static constexpr int SF_BYTES = 512 * (1 + SFB);
-    static constexpr int OUT = 32 * 32 * ES, OUT_BYTES = 4 * 2 * OUT;   // two parts of 32 x 32 a warp of the epilogue
+    // parts of 32 x 32 on their way out, of each of the epilogue's 8 warps
+    static constexpr int OUT = 32 * 32 * ES, OUTS = ES == 2 ? 2 : 1, OUT_BYTES = 8 * OUTS * OUT;
     static constexpr int FIXED = 1024 + NSF * SF_BYTES + OUT_BYTES;
     static constexpr int NS = (227 * 1024 - FIXED - 512) / STAGE < 6 ? (227 * 1024 - FIXED - 512) / STAGE : 6;
     static constexpr int SMEM = FIXED + NS * STAGE;
@@ -199,33 +176,28 @@ template <int BN, int PAIRS, bool B_MN, int ES> struct Cfg {
 
 struct Bars {
     uint64_t full[6], empty[6];
-    uint64_t sf_full[4], sf_empty[4];
+    uint64_t sf_there[4], sf_full[4], sf_empty[4];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drain;
     uint32_t tmem;
     int abort;
 };
 
-// The scales of rows r0 + lane + 32 j (j < 4) for the contracted blocks k0 .. k0 + 3, as the 16
-// bytes that lane `lane` of the tensor memory's copy holds.  Rows and blocks behind the ends
-// read the last one's: what they scale is zero or not stored.  No branches, so that all loads
-// are in flight at once (one after another they took 5300 cycles where the products take 1800).
-__device__ __forceinline__ uint4 gather_scales(const Scales& s, int r0, int k0, int kb, int lane) {
+// The scales of four rows (32 apart) for the contracted blocks k0 .. k0 + 3, as the 16 bytes that
+// a lane of the tensor memory's copy holds.  Rows and blocks behind the ends read the last one's:
+// what they scale is zero or not stored.  No branches, so that all loads are in flight at once.
+__device__ __forceinline__ uint4 gather_scales(const Scales& s, const uint8_t* const* at, int k0, int kb) {
     uint32_t w[4];
     if (s.words) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = min(r0 + lane + 32 * j, s.rows - 1);
-            w[j] = __ldg(reinterpret_cast<const uint32_t*>(s.p + (int64_t)(r >> s.shift) * s.rs + k0));
-        }
+        for (int j = 0; j < 4; ++j) w[j] = __ldg(reinterpret_cast<const uint32_t*>(at[j] + k0));
     } else {
         uint32_t v[4][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = min(r0 + lane + 32 * j, s.rows - 1);
-            const uint8_t* p = s.p + (int64_t)(r >> s.shift) * s.rs;
+        for (int k = 0; k < 4; ++k) {
+            const int64_t off = min(k0 + k, kb - 1) * s.ks;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[j][k] = __ldg(p + min(k0 + k, kb - 1) * s.ks);
+            for (int j = 0; j < 4; ++j) v[j][k] = __ldg(at[j] + off);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = v[j][0] | v[j][1] << 8 | v[j][2] << 16 | v[j][3] << 24;
@@ -255,15 +227,13 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     const uint32_t both = 3u << (2 * pair);
     // Tiles go down panels of q.panel columns of tiles, a row of the panel at a time: the clusters that
     // run side by side then share few rows of A and of B.
-    const int tc = q.tiles / q.tr, each = q.panel * q.tr;
-    const auto row_of = [&](int tile) {
-        const int p = tile / each, in = tile - p * each, w = min(q.panel, tc - p * q.panel);
-        return (in / w * PAIRS + pair) * kRows + rank * BM;
+    const auto place = [&](int tile, int* r, int* c) {
+        const int tc = q.tiles / q.tr, each = q.panel * q.tr, p = tile / each, in = tile - p * each,
+                  w = min(q.panel, tc - p * q.panel);
+        *r = in / w;
+        *c = p * q.panel + in - *r * w;
     };
-    const auto col_of = [&](int tile) {
-        const int p = tile / each, in = tile - p * each, w = min(q.panel, tc - p * q.panel);
-        return (p * q.panel + in % w) * BN;
-    };
+    const auto row_of = [&](int r) { return (r * PAIRS + pair) * kRows + rank * BM; };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NS; ++i) {
@@ -271,12 +241,13 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             mbar_init(&bars.empty[i], PAIRS);   // every pair that the copy reaches
         }
         for (int i = 0; i < C::NSF; ++i) {
-            mbar_init(&bars.sf_full[i], 128);
+            mbar_init(&bars.sf_there[i], 2);   // warps 2 and 3
+            mbar_init(&bars.sf_full[i], 2);    // two blocks
             mbar_init(&bars.sf_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.acc_full[i], 1);
-            mbar_init(&bars.acc_empty[i], 256);
+            mbar_init(&bars.acc_empty[i], 16);   // eight warps of two blocks
         }
         mbar_init(&bars.drain, 1);
         bars.abort = 0;
@@ -300,8 +271,11 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         int it = 0, st = 0;
         uint32_t phase = 1;
         bool ok = true;
+        const uint32_t full0 = of_block(&bars.full[0], even);
         for (int tile = first; tile < q.tiles && ok; tile += step) {
-            const int r0 = row_of(tile), c0 = col_of(tile) + rank * C::HALF;
+            int r, c;
+            place(tile, &r, &c);
+            const int r0 = row_of(r), c0 = c * BN + rank * C::HALF;
             for (int kb = 0; kb < q.kb; ++kb, ++it) {
                 ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.empty[st], phase, abort, kWaitNs));
                 if (!ok) break;
@@ -309,7 +283,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                     uint8_t* a = smem + st * C::STAGE;
                     uint8_t* b = a + C::A_BYTES;
                     if (rank == 0) mbar_arrive_expect_tx(&bars.full[st], 2 * C::STAGE);
-                    const uint32_t bar = of_block(&bars.full[st], even);
+                    const uint32_t bar = full0 + 8 * st;
                     tma_load_pair(a, &tm_a, bar, A_MN ? r0 : kb * BK, A_MN ? kb * BK : r0);
                     if constexpr (PAIRS == 1) {
                         tma_load_pair(b, &tm_b, bar, B_MN ? c0 : kb * BK, B_MN ? kb * BK : c0);
@@ -344,39 +318,47 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             for (int tile = first; tile < q.tiles && ok; tile += step)
                 for (int k0 = 0; k0 < q.kb && ok; k0 += q.chunk, ++t) {
                     const int acc = t & 1, k1 = min(q.kb, k0 + q.chunk);
-                    ok = __all_sync(0xffffffffu, wait<PAIR>(&bars.acc_empty[acc], (t / 2 & 1) ^ 1, abort));
+                    ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.acc_empty[acc], (t / 2 & 1) ^ 1, abort, kWaitNs));
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t d = tmem + acc * BN;
-                    for (int kb = k0; kb < k1; ++kb) {
-                        const uint32_t id4 = (kb - k0) & 3, ta = tmem + C::SF_COL + sf * C::SF_COLS;
-                        if (id4 == 0) {
-                            ok = __all_sync(0xffffffffu, wait<PAIR>(&bars.sf_full[sf], sf_phase, abort));
-                            if (!ok) break;
-                            tc_fence_after();
-                            if (elected()) {
-                                const uint64_t from = s0 + (uint32_t)(sf * (C::SF_BYTES >> 4));
-#pragma unroll
-                                for (int h = 0; h <= C::SFB; ++h) copy_scales<PAIR>(ta + 4 * h, from + h * (512 >> 4));
-                            }
-                            __syncwarp();
-                        }
-                        ok = __all_sync(0xffffffffu, wait<PAIR>(&bars.full[st], phase, abort));
+                    bool there = false;   // the next stage's operands, asked for ahead
+                    for (int kb = k0; kb < k1 && ok; kb += 4) {
+                        const uint32_t ta = tmem + C::SF_COL + sf * C::SF_COLS;
+                        ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.sf_full[sf], sf_phase, abort, kWaitNs));
                         if (!ok) break;
                         tc_fence_after();
-                        const bool last4 = id4 == 3 || kb + 1 == k1;
                         if (elected()) {
-                            const uint32_t at = st * (C::STAGE >> 4), id = idesc | id4 << 4 | id4 << 29;
+                            const uint64_t from = s0 + (uint32_t)(sf * (C::SF_BYTES >> 4));
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_scaled<PAIR>(d, a0 + at + k * a_step, b0 + at + k * b_step, id, ta, ta + 4, kb > k0 || k > 0);
-                            commit<PAIR>(&bars.empty[st], kAll);
-                            if (last4) commit<PAIR>(&bars.sf_empty[sf], both);
-                            if (kb + 1 == k1) commit<PAIR>(&bars.acc_full[acc], both);
+                            for (int h = 0; h <= C::SFB; ++h) copy_scales<PAIR>(ta + 4 * h, from + h * (512 >> 4));
                         }
                         __syncwarp();
-                        if (++st == C::NS) st = 0, phase ^= 1;
-                        if (last4 && ++sf == C::NSF) sf = 0, sf_phase ^= 1;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (kb + i >= k1) break;
+                            if (!there) {
+                                ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.full[st], phase, abort, kWaitNs));
+                                if (!ok) break;
+                            }
+                            tc_fence_after();
+                            const int now = st;
+                            if (++st == C::NS) st = 0, phase ^= 1;
+                            const bool last = kb + i + 1 == k1;
+                            there = !last && mbar_test_wait(smem_u32(&bars.full[st]), phase);
+                            if (elected()) {
+                                const uint32_t at = now * (C::STAGE >> 4);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    mma_scaled<PAIR>(d, a0 + at + k * a_step, b0 + at + k * b_step, idesc | i << 4 | i << 29, ta,
+                                                     ta + 4, kb > k0 || i > 0 || k > 0);
+                                commit<PAIR>(&bars.empty[now], kAll);
+                                if (i == 3 || last) commit<PAIR>(&bars.sf_empty[sf], both);
+                                if (last) commit<PAIR>(&bars.acc_full[acc], both);
+                            }
+                            there = __all_sync(0xffffffffu, there);
+                        }
+                        if (++sf == C::NSF) sf = 0, sf_phase ^= 1;
                     }
                 }
             if (!ok && elected()) {
@@ -385,55 +367,105 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             }
         }
     } else if (warp < 4) {
+        // The scales of the next kFly sets are on their way while this set's room is waited for (a load
+        // takes 2000 cycles beside the copies, a set's products 1800), and places are worked out once a
+        // tile: what a set costs this warp is on the products' path.
+        constexpr int kFly = 3;
         const Scales& s = warp == 2 ? sa : sb;
-        int sit = 0;
-        for (int tile = first; tile < q.tiles; tile += step) {
-            const int r0 = warp == 2 ? row_of(tile) : col_of(tile);
-            for (int k0 = 0; k0 < q.kb; k0 += q.chunk)
-                for (int kb = k0; kb < min(q.kb, k0 + q.chunk); kb += 4, ++sit) {
-                    const int sf = sit % C::NSF;
-                    uint4 w[C::SFB];
+        const int parts = warp == 2 ? 1 : C::SFB;
+        const uint8_t* at[4 * C::SFB];   // scales of rows lane + 32 j of the tile
+        uint4 next[kFly][C::SFB];
+        int tile = first, kb = 0;
+        const auto begin = [&] {
+            int r, c;
+            place(tile, &r, &c);
+            const int r0 = warp == 2 ? row_of(r) : c * BN;
 #pragma unroll
-                    for (int h = 0; h < C::SFB; ++h)
-                        if (h == 0 || warp == 3) w[h] = gather_scales(s, r0 + 128 * h, kb, q.kb, lane);
-                    if (!mbar_wait_or_abort(&bars.sf_empty[sf], (sit / C::NSF & 1) ^ 1, abort, kWaitNs)) goto scaled;
-                    uint4* to = reinterpret_cast<uint4*>(ssf + sf * C::SF_BYTES) + (warp == 2 ? 0 : 32) + lane;
+            for (int j = 0; j < 4 * C::SFB; ++j)
+                at[j] = s.p + (int64_t)(min(r0 + lane + 32 * j, s.rows - 1) >> s.shift) * s.rs;
+        };
+        const auto gather = [&](uint4 (&to)[C::SFB]) {   // the set at (tile, kb), and on to the one after it
+            if (tile >= q.tiles) return;
 #pragma unroll
-                    for (int h = 0; h < C::SFB; ++h)
-                        if (h == 0 || warp == 3) to[32 * h] = w[h];
-                    fence_proxy_async_smem();
-                    arrive_at(of_block(&bars.sf_full[sf], even));
-                }
+            for (int h = 0; h < C::SFB; ++h)
+                if (h < parts) to[h] = gather_scales(s, at + 4 * h, kb, q.kb);
+            if ((kb += 4) >= q.kb) {
+                kb = 0;
+                if ((tile += step) < q.tiles) begin();
+            }
+        };
+        int left = first < q.tiles ? (q.tiles - 1 - first) / step + 1 : 0;
+        left *= (q.kb + 3) / 4;
+        int sf = 0;
+        uint32_t phase = 1;
+        if (left) begin();
+#pragma unroll
+        for (int u = 0; u < kFly; ++u) gather(next[u]);
+        bool ok = true;
+        while (left > 0 && ok) {
+#pragma unroll
+            for (int u = 0; u < kFly; ++u) {
+                if (left <= 0 || !ok) break;
+                uint4 w[C::SFB];
+#pragma unroll
+                for (int h = 0; h < C::SFB; ++h) w[h] = next[u][h];
+                ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.sf_empty[sf], phase, abort, kWaitNs));
+                if (!ok) break;
+                uint4* to = reinterpret_cast<uint4*>(ssf + sf * C::SF_BYTES) + (warp == 2 ? 0 : 32) + lane;
+#pragma unroll
+                for (int h = 0; h < C::SFB; ++h)
+                    if (h < parts) to[32 * h] = w[h];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.sf_there[sf]);
+                gather(next[u]);
+                if (++sf == C::NSF) sf = 0, phase ^= 1;
+                --left;
+            }
         }
-    scaled:;
+    } else if (warp == 12) {
+        // Scales in shared memory to the tensor cores' proxy.  A warp of its own, as the fence waits for
+        // all that its warp has in flight: behind the loads of later sets it took 2000 cycles.
+        if (lane == 0) {
+            const uint32_t full0 = of_block(&bars.sf_full[0], even);
+            int left = first < q.tiles ? ((q.tiles - 1 - first) / step + 1) * ((q.kb + 3) / 4) : 0;
+            int sf = 0;
+            for (uint32_t phase = 0; left > 0; --left) {
+                if (!mbar_wait_or_abort(&bars.sf_there[sf], phase, abort, kWaitNs)) break;
+                fence_proxy_async_smem();
+                arrive_at(full0 + 8 * sf);
+                if (++sf == C::NSF) sf = 0, phase ^= 1;
+            }
+        }
     } else {
         // A warp has 32 lanes of tensor memory, the tile's rows, and moves them 32 columns at a time:
         // rounded, into shared memory, and by TMA to the result (coalesced stores where the result's
         // rows do not start on 16 bytes).
-        const int quad = warp & 3;
-        uint8_t* stage = sout + quad * 2 * C::OUT;
+        const int quad = warp & 3, half = (warp - 4) >> 2;
+        uint8_t* stage = sout + (warp - 4) * C::OUTS * C::OUT;
         int t = 0, n = 0;
         bool ok = true;
-        for (int tile = first; tile < q.tiles && ok; tile += step)
+        for (int tile = first; tile < q.tiles && ok; tile += step) {
+            int rt, ct;
+            place(tile, &rt, &ct);
             for (int k0 = 0; k0 < q.kb; k0 += q.chunk, ++t) {
                 const int acc = t & 1;
                 ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.acc_full[acc], t / 2 & 1, abort, kWaitNs));
                 if (!ok) break;
                 tc_fence_after();
-                const int r0 = row_of(tile) + quad * 32, c0 = col_of(tile);
+                const int r0 = row_of(rt) + quad * 32, c0 = ct * BN;
                 const uint32_t from = tmem + acc * BN + ((uint32_t)(quad * 32) << 16);
                 if (k0 > 0) {   // what is added to has been written
-                    if (lane == 0) bulk_wait<0>();
+                    if (elected()) bulk_wait<0>();
                     __syncwarp();
                 }
 #pragma unroll 1
-                for (int c = 0; c < BN; c += 32) {
+                for (int c = 32 * half; c < BN; c += 64) {
                     uint32_t v[32];
                     tmem_ld32_sync(from + c, v);
                     if (r0 >= q.R || c0 + c >= q.C) continue;
                     uint8_t* part = stage + n * C::OUT;
-                    n ^= 1;
-                    if (lane == 0) bulk_wait_read<1>();   // the copy before the last has read its part
+                    if (C::OUTS == 2) n ^= 1;
+                    if (elected()) bulk_wait_read<C::OUTS - 1>();   // the last copy from this part has read it
                     __syncwarp();
                     uint4* row = reinterpret_cast<uint4*>(part + lane * 32 * sizeof(TO));
                     // 16-byte pieces in the places where a swizzled copy looks for them
@@ -451,7 +483,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                     if (q.copied) {
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) {
+                        if (elected()) {
                             if (k0 == 0) tma_store_2d(&tm_o, part, c0 + c, r0);
                             else tma_reduce_add_2d(&tm_o, part, c0 + c, r0);
                             bulk_commit();
@@ -472,9 +504,12 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                     }
                 }
                 tc_fence_before();
-                arrive_at(of_block(&bars.acc_empty[acc], even));
+                __syncwarp();
+                if (lane == 0) arrive_at(of_block(&bars.acc_empty[acc], even));
             }
-        if (lane == 0) bulk_wait<0>();   // copies out of this block's shared memory
+        }
+        __syncwarp();
+        if (elected()) bulk_wait<0>();   // copies out of this block's shared memory
     }
     __syncwarp();
     tc_fence_before();
