@@ -27,34 +27,25 @@ __device__ __forceinline__ float scale_inverse(uint32_t byte) { return __uint_as
 // 2^e; the byte 0 is 2^-127, a subnormal.
 __device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(byte ? byte << 23 : 0x400000u); }
 
-// The larger of two magnitudes, of which infinities and NaN are left out: the scale is that of
-// a group's finite values, and what is not finite becomes e4m3's NaN.
-__device__ __forceinline__ float top_of(float top, float v) {
+// A group's scale is that of its finite values; what is not finite becomes e4m3's NaN.  fmaxf
+// leaves NaN out and the conversion keeps it, so that infinities alone need a second look: a
+// group whose largest magnitude is one is gone over again with CLEAN.
+__device__ __forceinline__ bool infinite(float top) { return top > 3.402823466e38f; }
+template <bool CLEAN> __device__ __forceinline__ float top_of(float top, float v) {
     const float a = fabsf(v);
-    return a <= 3.402823466e38f ? fmaxf(top, a) : top;
+    return CLEAN && infinite(a) ? top : fmaxf(top, a);
 }
 // Two values (low byte first) rounded to nearest even.
-__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+template <bool CLEAN> __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     uint32_t v = r;
-    // the conversion takes infinities to the largest value
-    if (fabsf(lo) > 3.402823466e38f) v |= 0x7fu;
-    if (fabsf(hi) > 3.402823466e38f) v |= 0x7f00u;
+    if (CLEAN) {   // the conversion takes infinities to the largest value
+        if (infinite(fabsf(lo))) v |= 0x7fu;
+        if (infinite(fabsf(hi))) v |= 0x7f00u;
+    }
     return v;
 }
-// Four e4m3 values as fp32 (exact, by way of fp16).
-__device__ __forceinline__ void e4m3_quad(uint32_t q, float* o) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint32_t h;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(q >> (16 * i))));
-        asm("{.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;}"
-            : "=f"(o[2 * i]), "=f"(o[2 * i + 1])
-            : "r"(h));
-    }
-}
-
 // How a thread's values lie in a row of D: its unit u is V neighbours (VEC: D is a multiple of V
 // and every access aligned), or lane + 32 j of a group of 128, each in its own access.  Either
 // way kLanes neighbouring lanes hold a group.
@@ -96,18 +87,27 @@ template <typename T, bool VEC> struct Units {
     }
     // Rounds the unit with its group's scale; the whole warp calls it.
     static __device__ __forceinline__ void quantise(uint8_t* q, uint8_t* s, int u, int D, const float (&v)[V]) {
+        const float top = group_top<false>(v);
+        if (__any_sync(0xffffffffu, infinite(top))) put<true>(q, s, u, D, v, group_top<true>(v));
+        else put<false>(q, s, u, D, v, top);
+    }
+    template <bool CLEAN> static __device__ __forceinline__ float group_top(const float (&v)[V]) {
         float top = 0.f;
 #pragma unroll
-        for (int j = 0; j < V; ++j) top = top_of(top, v[j]);
+        for (int j = 0; j < V; ++j) top = top_of<CLEAN>(top, v[j]);
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        return top;
+    }
+    template <bool CLEAN>
+    static __device__ __forceinline__ void put(uint8_t* q, uint8_t* s, int u, int D, const float (&v)[V], float top) {
         const uint32_t byte = scale_byte(top);
         const float inv = scale_inverse(byte);
         if (u >= count(D)) return;
         if (u % kLanes == 0) s[u / kLanes] = (uint8_t)byte;
         uint32_t p[V / 2];
 #pragma unroll
-        for (int j = 0; j < V / 2; ++j) p[j] = e4m3_pair(v[2 * j] * inv, v[2 * j + 1] * inv);
+        for (int j = 0; j < V / 2; ++j) p[j] = e4m3_pair<CLEAN>(v[2 * j] * inv, v[2 * j + 1] * inv);
         if constexpr (!VEC) {
 #pragma unroll
             for (int j = 0; j < V; ++j)

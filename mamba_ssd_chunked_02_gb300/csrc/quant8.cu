@@ -3,10 +3,12 @@
 //
 //   s = 2^e, e the smallest whole number >= -127 with max|x| <= 448 s;  q = x / s to nearest even
 //
-// Bytes bound: a block of 256 threads holds a tile of 128 x 128 in registers, 8 x 8 values a
+// Bytes bound: a block of 512 threads holds a tile of 128 x 128 in registers, 4 x 8 values a
 // thread, so that both kinds of groups come from one reading (the backward product takes dy
 // along its rows for dx and along its columns for dw).
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "internal.h"
 #include "proj.cuh"
@@ -15,7 +17,7 @@ namespace m2 {
 namespace {
 
 enum { kRow = 1, kCol = 2, kBlock = 4 };
-constexpr int kThreads = 256;
+constexpr int kThreads = 512, kLines = kThreads / 16, kPer = kGroup / kLines, kWarps = kThreads / 32;
 
 struct Tile {
     int64_t M, N;
@@ -25,144 +27,372 @@ struct Tile {
     const uint8_t* s_in;     // scales of an e4m3 input [M, nb]
     uint8_t *qr, *sr, *qc, *sc;
     int64_t ps;              // bytes between the rows of sr
+    bool even;               // rows lie at even distances, sequences or not
 };
 
-// Thread (tx, ty) has rows ty + 16 i and columns 8 tx + j (VEC: one access) or tx + 16 j.
-template <typename TI, bool VEC, int MODE>
-__global__ void __launch_bounds__(kThreads) quant8_kernel(const TI* __restrict__ x, const Tile p) {
-    __shared__ float tops[8][kGroup];
-    __shared__ uint8_t bytes[kGroup];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t m0 = (int64_t)(blockIdx.x / p.nb) * kGroup;
-    const uint32_t nb = blockIdx.x % p.nb;
-    const int64_t n0 = (int64_t)nb * kGroup;
-    const int rows = (int)min((int64_t)kGroup, p.M - m0), cols = (int)min((int64_t)kGroup, p.N - n0);
-    const auto col = [&](int j) { return VEC ? 8 * tx + j : tx + 16 * j; };
-    const auto place = [&](int64_t m, const Tok& s) {
-        const uint32_t b = (uint32_t)m / p.T;
-        return (int64_t)b * s.b + (int64_t)((uint32_t)m - b * p.T) * s.t + n0;
-    };
-    float v[8][8];
+// Two e4m3 pairs of products v f, v in fp32.
+template <bool CLEAN> __device__ __forceinline__ uint32_t e4m3_four(const float* v, f2 lo, f2 hi) {
+    float f[4];
+    unpack2(mul2(pack2(v[0], v[1]), lo), f[0], f[1]);
+    unpack2(mul2(pack2(v[2], v[3]), hi), f[2], f[3]);
+    return e4m3_pair<CLEAN>(f[0], f[1]) | e4m3_pair<CLEAN>(f[2], f[3]) << 16;
+}
+
+// Eight neighbours of a row as they lie in memory, read by one access (VEC) or one by one, and
+// Tops, the largest magnitudes in a column of such.
+template <typename TI> struct Eight;
+template <> struct Eight<__nv_bfloat16> {
+    uint32_t w[4];
+    struct Tops {
+        uint32_t w[4];   // of either sign
+        __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0; }
+        __device__ __forceinline__ void join(const uint32_t (&o)[4]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = ty + 16 * i;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-        if (r >= rows) continue;
-        const TI* from = x + place(m0 + r, p.sx);
-        if constexpr (sizeof(TI) == 1) {
-            const float s = scale_value(p.s_in[(m0 + r) * p.nb + nb]);
-            if (VEC) {
-                if (8 * tx < cols) {
-                    const uint2 w = *reinterpret_cast<const uint2*>(from + 8 * tx);
-                    e4m3_quad(w.x, v[i]);
-                    e4m3_quad(w.y, v[i] + 4);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (col(j) < cols) {
-                        float f[4];
-                        e4m3_quad(from[col(j)], f);
-                        v[i][j] = f[0];
-                    }
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] *= s;
-        } else if constexpr (VEC && sizeof(TI) == 2) {
-            if (8 * tx < cols) Conv<TI, 8>::to(load_raw<TI, 8>(from + 8 * tx), v[i]);
-        } else if constexpr (VEC) {
-            if (8 * tx < cols) {
-                Conv<TI, 4>::to(load_raw<TI, 4>(from + 8 * tx), v[i]);
-                Conv<TI, 4>::to(load_raw<TI, 4>(from + 8 * tx + 4), v[i] + 4);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (col(j) < cols) v[i][j] = to_f32(from[col(j)]);
+            for (int j = 0; j < 4; ++j) w[j] = larger(w[j], o[j]);
         }
-    }
-    const auto store = [&](uint8_t* q, int i, auto inv) {
-        const int r = ty + 16 * i;
-        if (r >= rows) return;
-        uint32_t w[4];
+        __device__ __forceinline__ void join_lane(int other) {
+            uint32_t o[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = e4m3_pair(v[i][2 * j] * inv(2 * j), v[i][2 * j + 1] * inv(2 * j + 1));
-        uint8_t* to = q + place(m0 + r, p.sq);
-        if (VEC) {
-            if (8 * tx < cols) *reinterpret_cast<uint2*>(to + 8 * tx) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
-        } else {
+            for (int j = 0; j < 4; ++j) o[j] = __shfl_xor_sync(0xffffffffu, w[j], other);
+            join(o);
+        }
+        __device__ __forceinline__ void get(float (&t)[8]) const {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (col(j) < cols) to[col(j)] = (uint8_t)(w[j / 2] >> (j & 1 ? 8 : 0));
+            for (int j = 0; j < 4; ++j) t[2 * j] = fabsf(bf_lo(w[j])), t[2 * j + 1] = fabsf(bf_hi(w[j]));
         }
     };
-    if constexpr (MODE & kRow) {
+    // max(|a|, |b|) of both halves, NaN left out, of either sign
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0; }
+    template <bool VEC> __device__ __forceinline__ void load(const __nv_bfloat16* p, int count) {
+        if constexpr (VEC) {
+            if (count <= 0) return;
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else {
+            const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float top = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) top = top_of(top, v[i][j]);
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const uint32_t byte = scale_byte(top);
-            const float f = scale_inverse(byte);
-            if (tx == 0 && ty + 16 * i < rows) p.sr[(m0 + ty + 16 * i) * p.ps + nb] = (uint8_t)byte;
-            store(p.qr, i, [&](int) { return f; });
+            for (int j = 0; j < 4; ++j)
+                w[j] = (2 * j < count ? __ldg(u + 2 * j) : 0) | (uint32_t)(2 * j + 1 < count ? __ldg(u + 2 * j + 1) : 0) << 16;
         }
     }
-    if constexpr (MODE & kCol) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float top = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top = top_of(top, v[i][j]);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            if (lane < 16) tops[warp][col(j)] = top;
-        }
-        __syncthreads();
-        if (threadIdx.x < kGroup) {
-            float top = 0.f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) top = fmaxf(top, tops[k][threadIdx.x]);
-            bytes[threadIdx.x] = (uint8_t)scale_byte(top);
-            if (threadIdx.x < cols) p.sc[m0 / kGroup * p.N + n0 + threadIdx.x] = bytes[threadIdx.x];
-        }
-        __syncthreads();
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = scale_inverse(bytes[col(j)]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) store(p.qc, i, [&](int j) { return f[j]; });
+    __device__ __forceinline__ float top() const {
+        const uint32_t m = larger(larger(w[0], w[1]), larger(w[2], w[3]));
+        return fmaxf(fabsf(bf_lo(m)), fabsf(bf_hi(m)));
     }
-    if constexpr (MODE & kBlock) {
+    __device__ __forceinline__ void into(Tops& t) const { t.join(w); }
+    // Unpacked anew at each use (the statement hides what it was unpacked to before), so that the
+    // packed words alone are kept from one pass over the tile to the next.
+    __device__ __forceinline__ void get(float (&v)[8]) {
+        asm volatile("" : "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3]));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[2 * j] = bf_lo(w[j]), v[2 * j + 1] = bf_hi(w[j]);
+    }
+};
+template <> struct Eight<float> {
+    float f[8];
+    struct Tops {
+        float t[8];
+        __device__ __forceinline__ void zero() {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) t[j] = 0.f;
+        }
+        __device__ __forceinline__ void join_lane(int other) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) t[j] = fmaxf(t[j], __shfl_xor_sync(0xffffffffu, t[j], other));
+        }
+        __device__ __forceinline__ void get(float (&o)[8]) const {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = t[j];
+        }
+    };
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = 0.f;
+    }
+    template <bool VEC> __device__ __forceinline__ void load(const float* p, int count) {
+        if constexpr (VEC) {
+            if (count <= 0) return;
+            const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p + 4));
+            f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = j < count ? __ldg(p + j) : 0.f;
+        }
+    }
+    __device__ __forceinline__ float top() const {
+        float t = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t = fmaxf(t, fabsf(f[j]));
+        return t;
+    }
+    __device__ __forceinline__ void into(Tops& t) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t.t[j] = fmaxf(t.t[j], fabsf(f[j]));
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = f[j];
+    }
+};
+
+// Eight bytes of a row, `count` of them inside it.
+template <bool VEC> __device__ __forceinline__ void store_eight(uint8_t* to, int count, uint32_t lo, uint32_t hi) {
+    if (VEC ? count > 0 : count >= 8) {
+        *reinterpret_cast<uint2*>(to) = make_uint2(lo, hi);
+    } else if (!VEC) {   // the row's end: nothing behind it is written
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < count) to[j] = (uint8_t)((j < 4 ? lo : hi) >> (8 * (j & 3)));
+    }
+}
+
+// The largest magnitudes t of 8 columns a lane (lanes 0-15 of each warp) to the tile's column
+// scales: written to p.sc, and the bytes left in shared memory.
+__device__ __forceinline__ void column_scales(const Tile& p, float (*tops)[kGroup], uint8_t* bytes, uint32_t mb, int64_t n0, int cols) {
+    if (threadIdx.x < kGroup) {
         float top = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int k = 0; k < kWarps; ++k) top = fmaxf(top, tops[k][threadIdx.x]);
+        bytes[threadIdx.x] = (uint8_t)scale_byte(top);
+        if (threadIdx.x < cols) p.sc[mb * p.N + n0 + threadIdx.x] = bytes[threadIdx.x];
+    }
+    __syncthreads();
+}
+__device__ __forceinline__ void column_inverses(const uint8_t* bytes, int tx, float (&t)[8]) {
+    const uint2 w = *reinterpret_cast<const uint2*>(bytes + 8 * tx);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top = top_of(top, v[i][j]);
+    for (int j = 0; j < 8; ++j) t[j] = scale_inverse((j < 4 ? w.x : w.y) >> (8 * (j & 3)) & 0xffu);
+}
+__device__ __forceinline__ void put_tops(float (*tops)[kGroup], int warp, int tx, const float (&t)[8]) {
+    float4* to = reinterpret_cast<float4*>(&tops[warp][8 * tx]);
+    to[0] = make_float4(t[0], t[1], t[2], t[3]);
+    to[1] = make_float4(t[4], t[5], t[6], t[7]);
+}
+
+// Thread (tx, ty) has rows ty + 32 i and columns 8 tx + j.
+template <typename TI, bool VEC, int MODE>
+__global__ void __launch_bounds__(kThreads, sizeof(TI) == 2 && MODE == kRow ? 3 : 2) quant8_kernel(const TI* __restrict__ x, const Tile p) {
+    __shared__ __align__(16) float tops[kWarps][kGroup];
+    __shared__ __align__(8) uint8_t bytes[kGroup];
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t mb = blockIdx.x / p.nb, nb = blockIdx.x - mb * p.nb;
+    const int64_t m0 = (int64_t)mb * kGroup, n0 = (int64_t)nb * kGroup;
+    const int rows = (int)min((int64_t)kGroup, p.M - m0), cols = (int)min((int64_t)kGroup, p.N - n0), count = cols - 8 * tx;
+    // where the rows' values lie, in x and in q
+    int64_t from[kPer], to[kPer];
+    if (p.even) {
+        from[0] = (m0 + ty) * p.sx.t + n0 + 8 * tx, to[0] = (m0 + ty) * p.sq.t + n0 + 8 * tx;
+#pragma unroll
+        for (int i = 1; i < kPer; ++i) from[i] = from[i - 1] + kLines * p.sx.t, to[i] = to[i - 1] + kLines * p.sq.t;
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const uint32_t m = (uint32_t)(m0 + ty + kLines * i), b = m / p.T, t = m - b * p.T;
+            from[i] = b * p.sx.b + t * p.sx.t + n0 + 8 * tx, to[i] = b * p.sq.b + t * p.sq.t + n0 + 8 * tx;
+        }
+    }
+    Eight<TI> raw[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        raw[i].zero();
+        if (ty + kLines * i < rows) raw[i].template load<VEC>(x + from[i], count);
+    }
+    // largest magnitude of row i's eight values; with CLEAN, of those that are finite
+    const auto top_in = [&](auto clean, int i) {
+        if (!decltype(clean)::value) return raw[i].top();
+        float v[8], top = 0.f;
+        raw[i].get(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = top_of<true>(top, v[j]);
+        return top;
+    };
+    const auto put = [&](auto clean, uint8_t* q, int i, auto inv) {
+        constexpr bool CLEAN = decltype(clean)::value;
+        if (ty + kLines * i >= rows) return;
+        float v[8];
+        raw[i].get(v);
+        store_eight<VEC>(q + to[i], count, e4m3_four<CLEAN>(v, inv(0), inv(1)), e4m3_four<CLEAN>(v + 4, inv(2), inv(3)));
+    };
+    // each returns false where there are infinities to be looked for (and is called again with `clean`)
+    const auto rows_go = [&](auto clean) {
+        constexpr bool CLEAN = decltype(clean)::value;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            float top = top_in(clean, i);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (!CLEAN && __any_sync(0xffffffffu, infinite(top))) return false;
+            const uint32_t byte = scale_byte(top);
+            const f2 f = dup2(scale_inverse(byte));
+            if (tx == 0 && ty + kLines * i < rows) p.sr[(m0 + ty + kLines * i) * p.ps + nb] = (uint8_t)byte;
+            put(clean, p.qr, i, [&](int) { return f; });
+        }
+        return true;
+    };
+    const auto cols_go = [&](auto clean) {
+        constexpr bool CLEAN = decltype(clean)::value;
+        float t[8];
+        if constexpr (CLEAN) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) t[j] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                float v[8];
+                raw[i].get(v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) t[j] = top_of<true>(t[j], v[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) t[j] = fmaxf(t[j], __shfl_xor_sync(0xffffffffu, t[j], 16));
+        } else {
+            typename Eight<TI>::Tops all;
+            all.zero();
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) raw[i].into(all);
+            all.join_lane(16);
+            all.get(t);
+        }
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) bad |= infinite(t[j]);
+        if (lane < 16) put_tops(tops, warp, tx, t);
+        if (__syncthreads_or(bad) && !CLEAN) return false;
+        column_scales(p, tops, bytes, mb, n0, cols);
+        column_inverses(bytes, tx, t);
+        f2 f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = pack2(t[2 * j], t[2 * j + 1]);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) put(clean, p.qc, i, [&](int j) { return f[j]; });
+        return true;
+    };
+    const auto block_go = [&](auto clean) {
+        constexpr bool CLEAN = decltype(clean)::value;
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) top = fmaxf(top, top_in(clean, i));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (lane == 0) tops[0][warp] = top;
+        if (lane == 0) tops[CLEAN][warp] = top;
         __syncthreads();
-        top = tops[0][0];
+        top = tops[CLEAN][0];
 #pragma unroll
-        for (int k = 1; k < 8; ++k) top = fmaxf(top, tops[0][k]);
+        for (int k = 1; k < kWarps; ++k) top = fmaxf(top, tops[CLEAN][k]);
+        if (!CLEAN && infinite(top)) return false;
         const uint32_t byte = scale_byte(top);
-        const float f = scale_inverse(byte);
+        const f2 f = dup2(scale_inverse(byte));
         if (threadIdx.x == 0) p.sr[blockIdx.x] = (uint8_t)byte;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) store(p.qr, i, [&](int) { return f; });
+        for (int i = 0; i < kPer; ++i) put(clean, p.qr, i, [&](int) { return f; });
+        return true;
+    };
+    const std::false_type plain{};
+    const std::true_type clean{};
+    if constexpr (MODE & kRow)
+        if (!rows_go(plain)) rows_go(clean);
+    if constexpr (MODE & kCol)
+        if (!cols_go(plain)) cols_go(clean);
+    if constexpr (MODE & kBlock)
+        if (!block_go(plain)) block_go(clean);
+}
+
+// e4m3 in groups along rows to e4m3 in groups along columns.  The bits of an e4m3 number in the
+// places of fp32's low exponent and high mantissa bits are its magnitude times 2^-120, subnormal
+// ones too: shifts and one product, where conversions by way of fp16 run at a quarter of the rate;
+// the sign is put back as it was.
+template <bool VEC> __global__ void __launch_bounds__(kThreads, 2) quant8_turn_kernel(const uint8_t* __restrict__ x, const Tile p) {
+    __shared__ __align__(16) float tops[kWarps][kGroup];
+    __shared__ __align__(8) uint8_t bytes[kGroup];
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t mb = blockIdx.x / p.nb, nb = blockIdx.x - mb * p.nb;
+    const int64_t m0 = (int64_t)mb * kGroup, n0 = (int64_t)nb * kGroup;
+    const int rows = (int)min((int64_t)kGroup, p.M - m0), cols = (int)min((int64_t)kGroup, p.N - n0), count = cols - 8 * tx;
+    const int64_t from = (m0 + ty) * p.sx.t + n0 + 8 * tx, to = (m0 + ty) * p.sq.t + n0 + 8 * tx;
+    uint32_t w[kPer][2];
+    float lift[kPer], rest[kPer];   // 2^120 times the row's scale, as two factors in range
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        w[i][0] = w[i][1] = 0;
+        lift[i] = 0.f, rest[i] = 1.f;
+        if (ty + kLines * i >= rows) continue;
+        const uint8_t* f = x + from + i * (kLines * p.sx.t);
+        if constexpr (VEC) {
+            if (count > 0) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2*>(f));
+                w[i][0] = v.x, w[i][1] = v.y;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < count) w[i][j / 4] |= (uint32_t)__ldg(f + j) << (8 * (j & 3));
+        }
+        const int e = 120 + (int)__ldg(p.s_in + (m0 + ty + kLines * i) * p.nb + nb);   // 2^(e - 127)
+        lift[i] = scale_value((uint32_t)min(e, 254));
+        rest[i] = scale_value((uint32_t)max(e - 127, 127));   // 1 up to e = 254, then 2^(e - 254)
     }
+    // NaN, and scales of 2^8 and up: what takes a second look
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        bad |= rest[i] != 1.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) bad |= __vcmpeq4(w[i][h] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+    }
+    // the magnitude of value j of row i
+    const auto value = [&](auto careful, int i, int j) {
+        const uint32_t k = 8 * (j & 3), v = w[i][j / 4];
+        const uint32_t b = (k < 20 ? v << (20 - k) : v >> (k - 20)) & 0x07f00000u;
+        const float f = __uint_as_float(b) * lift[i];
+        return decltype(careful)::value ? (b == 0x07f00000u ? __uint_as_float(0x7fffffffu) : f * rest[i]) : f;
+    };
+    const auto run = [&](auto careful) {
+        float t[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            t[j] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) t[j] = fmaxf(t[j], value(careful, i, j));
+            t[j] = fmaxf(t[j], __shfl_xor_sync(0xffffffffu, t[j], 16));
+        }
+        if (lane < 16) put_tops(tops, warp, tx, t);
+        __syncthreads();
+        column_scales(p, tops, bytes, mb, n0, cols);
+        column_inverses(bytes, tx, t);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (ty + kLines * i >= rows) continue;
+            uint32_t o[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float v[4];
+                asm volatile("" : "+r"(w[i][h]));   // unpacked anew, as above
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = value(careful, i, 4 * h + j);
+                o[h] = e4m3_four<false>(v, pack2(t[4 * h], t[4 * h + 1]), pack2(t[4 * h + 2], t[4 * h + 3])) | (w[i][h] & 0x80808080u);
+            }
+            store_eight<VEC>(p.qc + to + i * (kLines * p.sq.t), count, o[0], o[1]);
+        }
+    };
+    if (__syncthreads_or(bad)) run(std::true_type{});
+    else run(std::false_type{});
+}
+
+int64_t blocks_of(Tile& p) {
+    p.nb = (uint32_t)((p.N + kGroup - 1) / kGroup);
+    p.even = p.M == p.T || (p.sx.b == p.T * p.sx.t && p.sq.b == p.T * p.sq.t);
+    return (p.M + kGroup - 1) / kGroup * p.nb;
 }
 
 template <typename TI, int MODE> cudaError_t go(const TI* x, Tile p, cudaStream_t st) {
     if (p.M == 0 || p.N == 0) return cudaSuccess;
-    p.nb = (uint32_t)((p.N + kGroup - 1) / kGroup);
-    const int64_t blocks = (p.M + kGroup - 1) / kGroup * p.nb;
+    const int64_t blocks = blocks_of(p), es = sizeof(TI);
     if (blocks >= (int64_t(1) << 31) || p.M >= (int64_t(1) << 31)) return kGridLimit;
-    const int64_t es = sizeof(TI);
-    const bool v = p.N % 8 == 0 && vec_ok(x, p.sx, es == 1 ? 8 : 16, es) && (!p.qr || vec_ok(p.qr, p.sq, 8, 1)) &&
+    const bool v = p.N % 8 == 0 && vec_ok(x, p.sx, 16, es) && (!p.qr || vec_ok(p.qr, p.sq, 8, 1)) &&
                    (!p.qc || vec_ok(p.qc, p.sq, 8, 1));
     if (v) quant8_kernel<TI, true, MODE><<<(unsigned)blocks, kThreads, 0, st>>>(x, p);
     else quant8_kernel<TI, false, MODE><<<(unsigned)blocks, kThreads, 0, st>>>(x, p);
@@ -177,20 +407,26 @@ template <int MODE> cudaError_t go(bool bf16, const void* x, const Tile& p, cuda
 }  // namespace
 
 cudaError_t launch_quant8(const Quant8Args& a, const void* x, uint8_t* q, uint8_t* s, cudaStream_t st) {
-    const Tile p{a.b * a.T, a.D, (uint32_t)a.T, 0, a.sx, a.sq, nullptr, q, s, nullptr, nullptr, (a.D + kGroup - 1) / kGroup};
+    const Tile p{a.b * a.T, a.D, (uint32_t)a.T, 0, a.sx, a.sq, nullptr, q, s, nullptr, nullptr, (a.D + kGroup - 1) / kGroup, false};
     return a.block ? go<kBlock>(a.bf16, x, p, st) : go<kRow>(a.bf16, x, p, st);
 }
 
 cudaError_t launch_quant8_both(bool bf16, int64_t M, int64_t N, const void* x, int64_t px, uint8_t* qr, uint8_t* sr,
                                int64_t ps, uint8_t* qc, uint8_t* sc, int64_t pq, cudaStream_t st) {
-    const Tile p{M, N, (uint32_t)M, 0, Tok{0, px}, Tok{0, pq}, nullptr, qr, sr, qc, sc, ps};
+    const Tile p{M, N, (uint32_t)M, 0, Tok{0, px}, Tok{0, pq}, nullptr, qr, sr, qc, sc, ps, false};
     return !qc ? go<kRow>(bf16, x, p, st) : !qr ? go<kCol>(bf16, x, p, st) : go<kRow | kCol>(bf16, x, p, st);
 }
 
 cudaError_t launch_quant8_turn(int64_t M, int64_t N, const uint8_t* q, int64_t px, const uint8_t* s, uint8_t* qc,
                                uint8_t* sc, int64_t pq, cudaStream_t st) {
-    const Tile p{M, N, (uint32_t)M, 0, Tok{0, px}, Tok{0, pq}, s, nullptr, nullptr, qc, sc, 0};
-    return go<uint8_t, kCol>(q, p, st);
+    Tile p{M, N, (uint32_t)M, 0, Tok{0, px}, Tok{0, pq}, s, nullptr, nullptr, qc, sc, 0, false};
+    if (M == 0 || N == 0) return cudaSuccess;
+    const int64_t blocks = blocks_of(p);
+    if (blocks >= (int64_t(1) << 31) || M >= (int64_t(1) << 31)) return kGridLimit;
+    const bool v = N % 8 == 0 && vec_ok(q, p.sx, 8, 1) && vec_ok(qc, p.sq, 8, 1);
+    if (v) quant8_turn_kernel<true><<<(unsigned)blocks, kThreads, 0, st>>>(q, p);
+    else quant8_turn_kernel<false><<<(unsigned)blocks, kThreads, 0, st>>>(q, p);
+    return cudaGetLastError();
 }
 
 }  // namespace m2
