@@ -19,6 +19,7 @@
 #include <algorithm>
 #include <atomic>
 
+#include "common.cuh"
 #include "internal.h"
 #include "proj.cuh"
 #include "tc5.cuh"
@@ -91,6 +92,11 @@ __device__ __forceinline__ uint32_t block_rank() {
 // Every thread of the cluster's blocks meets; what they wrote before is visible behind it.
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+__device__ __forceinline__ void send(uint32_t at, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
 // This block's shared address, in the block of the cluster that has the given rank.
 __device__ __forceinline__ uint32_t of_block(const void* p, uint32_t rank) {
@@ -186,9 +192,9 @@ struct Bars {
 // The scales of four rows (32 apart) for the contracted blocks k0 .. k0 + 3, as the 16 bytes that
 // a lane of the tensor memory's copy holds.  Rows and blocks behind the ends read the last one's:
 // what they scale is zero or not stored.  No branches, so that all loads are in flight at once.
-__device__ __forceinline__ uint4 gather_scales(const Scales& s, const uint8_t* const* at, int k0, int kb) {
+__device__ __forceinline__ uint4 gather_scales(const Scales& s, bool words, const uint8_t* const* at, int k0, int kb) {
     uint32_t w[4];
-    if (s.words) {
+    if (words) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = __ldg(reinterpret_cast<const uint32_t*>(at[j] + k0));
     } else {
@@ -388,7 +394,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             if (tile >= q.tiles) return;
 #pragma unroll
             for (int h = 0; h < C::SFB; ++h)
-                if (h < parts) to[h] = gather_scales(s, at + 4 * h, kb, q.kb);
+                if (h < parts) to[h] = gather_scales(s, s.words, at + 4 * h, kb, q.kb);
             if ((kb += 4) >= q.kb) {
                 kb = 0;
                 if ((tile += step) < q.tiles) begin();
@@ -521,6 +527,228 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     }
 }
 
+// ---- few rows --------------------------------------------------------------------------
+// Where the result's rows are few (single tokens), the operand that is read once is the large one:
+// its rows are the accumulator's lanes, 128 a tile, and BN columns hold the few.  A cluster of
+// blocks splits a tile's contracted blocks; each column of the tile belongs to one of them, to
+// which the others send their parts through the cluster's shared memory, and which adds them in the
+// order of the blocks.
+// Warp roles: 0 TMA, 1 MMA (and tensor memory), 2-5 scales, then the epilogue.
+constexpr int kFewThreads = 192;
+constexpr int kFewRows = 128;
+constexpr int kFewBlocks = 32;   // contracted blocks a block: its scales stay in tensor memory
+
+template <int BN> struct Few {
+    static constexpr int A_BYTES = BM * BK, STAGE = A_BYTES + BN * BK;
+    static constexpr int SETS = kFewBlocks / 4;
+    static constexpr int SF_BYTES = 1024;                // of a set: 128 rows of A and of B
+    static constexpr uint32_t COLS = 128;
+    static_assert(BN + SETS * 8 <= 128, "tensor memory");
+    // parts of the block's own columns, from every block of the cluster
+    static int join_bytes(int split) { return split > 1 ? (BN + split - 1) / split * split * BM * 4 : 0; }
+    // stages of a block that shares its SM with `others`
+    static int stages(int split, int others) {
+        return (227 * 1024 / (1 + others) - 2048 - 1024 - SETS * SF_BYTES - join_bytes(split)) / STAGE;
+    }
+    static int smem(int split, int ns) { return 1024 + ns * STAGE + SETS * SF_BYTES + join_bytes(split); }
+};
+constexpr int kFewStages = 8;
+
+struct FewShape {
+    int R, C, kb;     // lanes' rows, few rows, contracted blocks
+    int ns;           // stages
+    int64_t ldo;
+};
+
+template <int BN, bool A_MN, typename TO>
+__global__ void __launch_bounds__(kFewThreads, 2)
+proj8_few_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const Scales sa,
+                 const Scales sb, TO* __restrict__ out, const FewShape q, int32_t* err) {
+    using C = Few<BN>;
+    constexpr int STAGE = C::STAGE;
+    const int ns = q.ns;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t* ssf = smem + ns * STAGE;
+    float* join = reinterpret_cast<float*>(ssf + C::SETS * C::SF_BYTES);   // [block][own column][128]
+    struct FewBars {
+        uint64_t full[kFewStages], empty[kFewStages], sf_full, acc_full;
+        uint32_t tmem;
+        int abort;
+    };
+    __shared__ FewBars bars;
+    volatile int* abort = &bars.abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t split;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(split));
+    const uint32_t rank = block_rank();
+    const int r0 = (int)(blockIdx.x / split) * BM, c0 = blockIdx.y * BN;
+    const int k0 = (int)((int64_t)q.kb * rank / split), n = (int)((int64_t)q.kb * (rank + 1) / split) - k0;
+
+    // Warps 2 to 5 ask for their first set's scales before anything is set up: what the products wait
+    // for longest (2 us after the others were ready).
+    const uint8_t *at[4], *bt[4];
+    uint4 sets[2];
+    const bool whole = k0 % 4 == 0;   // words start where the block's share does
+    const auto gather = [&](int set) {
+        sets[0] = gather_scales(sa, sa.words && whole, at, k0 + 4 * set, k0 + n);
+        sets[1] = gather_scales(sb, sb.words && whole, bt, k0 + 4 * set, k0 + n);
+    };
+    grid_dep_launch();   // the next kernel may set itself up beside this one
+    if (warp >= 2) {
+        grid_dep_wait();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            at[j] = sa.p + (int64_t)(min(r0 + lane + 32 * j, sa.rows - 1) >> sa.shift) * sa.rs;
+            bt[j] = sb.p + (int64_t)(min(c0 + lane + 32 * j, sb.rows - 1) >> sb.shift) * sb.rs;
+        }
+        if (4 * (warp - 2) < n) gather(warp - 2);
+    } else if (warp == 0) {
+        if (elected()) {
+            prefetch_tmap(&tm_a);
+            prefetch_tmap(&tm_b);
+        }
+        if (lane < ns) {
+            mbar_init(&bars.full[lane], 1);
+            mbar_init(&bars.empty[lane], 1);
+        }
+        if (lane == 0) {
+            mbar_init(&bars.sf_full, 128);
+            mbar_init(&bars.acc_full, 1);
+            bars.abort = 0;
+        }
+        fence_barrier_init();
+    } else {
+        alloc_tmem<false>(&bars.tmem, C::COLS);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem;
+    if (split > 1) cluster_arrive();   // this block has begun
+    bool ok = true;
+
+    if (warp == 0) {
+        grid_dep_wait();   // what is read was written by the kernel before
+        int st = 0, it = 0;
+        for (uint32_t phase = 1; it < n; ++it) {
+            ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.empty[st], phase, abort, kWaitNs));
+            if (!ok) break;
+            if (elected()) {
+                const int k = (k0 + it) * BK;
+                uint8_t* a = smem + st * STAGE;
+                mbar_arrive_expect_tx(&bars.full[st], STAGE);
+                tma_load_2d(a, &tm_a, &bars.full[st], A_MN ? r0 : k, A_MN ? k : r0);
+                tma_load_2d(a + C::A_BYTES, &tm_b, &bars.full[st], k, c0);
+            }
+            __syncwarp();
+            if (++st == ns) st = 0, phase ^= 1;
+        }
+        if (!ok && lane == 0)   // copies in flight land before the block ends
+            for (int i = it - 1; i >= 0 && i >= it - ns; --i) mbar_wait(&bars.full[i % ns], i / ns & 1, kWaitNs);
+    } else if (warp == 1) {
+        constexpr uint32_t idesc = idesc_mx(BM, BN, A_MN, 0);
+        constexpr uint32_t a_step = (A_MN ? 32 * 128 : 32) >> 4, b_step = 32 >> 4;
+        const uint64_t a0 = smem_desc_sw128(smem_u32(smem), A_MN ? 128 * BK : 16, 1024);
+        const uint64_t b0 = smem_desc_sw128(smem_u32(smem) + C::A_BYTES, 16, 1024);
+        const uint64_t s0 = scale_desc(smem_u32(ssf));
+        ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.sf_full, 0, abort, kWaitNs));
+        tc_fence_after();
+        int st = 0;
+        uint32_t phase = 0;
+        for (int i = 0; i < n && ok; ++i) {
+            ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.full[st], phase, abort, kWaitNs));
+            if (!ok) break;
+            tc_fence_after();
+            if (elected()) {
+                const uint32_t set = i / 4, id4 = i & 3, ta = tmem + BN + set * 8;
+                if (id4 == 0) {
+                    copy_scales<false>(ta, s0 + set * (C::SF_BYTES >> 4));
+                    copy_scales<false>(ta + 4, s0 + set * (C::SF_BYTES >> 4) + (512 >> 4));
+                }
+                const uint32_t at = st * (STAGE >> 4), id = idesc | id4 << 4 | id4 << 29;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_scaled<false>(tmem, a0 + at + k * a_step, b0 + at + k * b_step, id, ta, ta + 4, i > 0 || k > 0);
+                commit<false>(&bars.empty[st]);
+                if (i + 1 == n) commit<false>(&bars.acc_full);
+            }
+            __syncwarp();
+            if (++st == ns) st = 0, phase ^= 1;
+        }
+        if (!ok && elected()) {   // products in flight are done before the block ends
+            commit<false>(&bars.acc_full);
+            mbar_wait(&bars.acc_full, 0, kWaitNs);
+        }
+    }
+    const int quad = warp & 3, row = quad * 32 + lane;   // of the tile, where the warp is an epilogue's
+    const int cols = min(BN, q.C - c0);
+    const uint32_t own = (BN + split - 1) / split;   // columns a block
+    if (warp >= 2) {
+        for (int set = warp - 2; 4 * set < n; set += 4) {
+            if (set > warp - 2) gather(set);
+            uint4* to = reinterpret_cast<uint4*>(ssf + set * C::SF_BYTES) + lane;
+            to[0] = sets[0];
+            to[32] = sets[1];
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&bars.sf_full);
+        ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.acc_full, 0, abort, kWaitNs));
+        tc_fence_after();
+        if (split > 1) cluster_wait();   // the others have begun
+        const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16);
+        TO* o = out + (int64_t)c0 * q.ldo + r0 + row;
+        uint32_t owner = 0, slot = 0;   // of column c + j
+        uint32_t part = split > 1 ? of_block(join + rank * own * BM + row, 0) : 0;
+#pragma unroll 1
+        for (int c = 0; c < cols && ok; c += 16) {
+            uint32_t v[16];
+            tmem_ld16_sync(from + c, v);
+            if (split > 1) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    if (c + j < cols) send(part, __uint_as_float(v[j]));
+                    part += BM * 4;
+                    if (++slot == own && ++owner < split) slot = 0, part = of_block(join + rank * own * BM + row, owner);
+                }
+            } else if (r0 + row < q.R) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j, o += q.ldo)
+                    if (c + j < cols) *o = from_f32<TO>(__uint_as_float(v[j]));
+            }
+        }
+    } else if (split > 1) {
+        __syncwarp();
+        cluster_wait();
+    }
+    __syncwarp();
+    tc_fence_before();
+    if (split > 1) {
+        cluster_sync();   // the parts are there
+        if (warp >= 2 && r0 + row < q.R && !*abort) {
+            const int from_c = rank * own, to_c = min(cols, from_c + (int)own);
+            TO* o = out + (int64_t)(c0 + from_c) * q.ldo + r0 + row;
+            const float* from = join + row;
+#pragma unroll 2
+            for (int c = from_c; c < to_c; ++c, from += BM, o += q.ldo) {
+                float sum = from[0];
+#pragma unroll
+                for (int s = 1; s < 8; ++s)
+                    if (s < (int)split) sum += from[s * own * BM];
+                *o = from_f32<TO>(sum);
+            }
+        }
+    } else {
+        __syncthreads();
+    }
+    if (threadIdx.x == 0 && *abort) record_error(err, kErrTimeoutProj8);
+    if (warp == 1) {
+        tc_fence_after();
+        free_tmem<false>(tmem, C::COLS);
+    }
+}
+
 // `across` contracted values (MN-major) or rows (K-major) a copy; 128 of the inner index.
 bool map_of(CUtensorMap* m, const Operand& o, int64_t rows, int64_t depth, int across) {
     const uint64_t dims[2] = {(uint64_t)(o.mn ? rows : depth), (uint64_t)(o.mn ? depth : rows)};
@@ -529,6 +757,27 @@ bool map_of(CUtensorMap* m, const Operand& o, int64_t rows, int64_t depth, int a
     return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, o.q, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// A launch in clusters of `blocks` along x (a lone block is one of its own).
+struct Launch {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    Launch(int threads, int smem, int blocks, cudaStream_t st) {
+        cfg.blockDim = dim3((unsigned)threads);
+        cfg.dynamicSmemBytes = (size_t)smem;
+        cfg.stream = st;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)blocks;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    // May begin while the kernel before it ends (and waits for it before it reads anything).
+    void early() {
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.numAttrs = 2;
+    }
+};
 // Clusters of `blocks` that the device holds at once (`known`: what was found before, by device).
 template <typename K> int resident_clusters(K k, cudaLaunchConfig_t cfg, int blocks, std::atomic<int>* known) {
     int dev = 0, n = 0;
@@ -541,6 +790,11 @@ template <typename K> int resident_clusters(K k, cudaLaunchConfig_t cfg, int blo
     }
     known[dev].store(n, std::memory_order_relaxed);
     return n;
+}
+
+Scales scales_of(const Operand& o, int64_t rows, int kb) {
+    const bool words = o.ks == 1 && o.rs % 4 == 0 && kb <= o.rs && reinterpret_cast<uintptr_t>(o.s) % 4 == 0;
+    return Scales{o.s, o.rs, o.ks, o.shift, (int)rows, words};
 }
 
 // Contracted blocks whose sum may stay in tensor memory for an fp32 result.  The tensor cores'
@@ -569,34 +823,62 @@ cudaError_t go(const Operand& A, const Operand& B, int64_t R, int64_t Cn, int64_
     if (tiles >= (int64_t(1) << 30)) return kGridLimit;
     const int kb = (int)((depth + BK - 1) / BK);
     const Shape q{(int)R, (int)Cn, kb, (int)tr, (int)tiles, kPanel, sizeof(TO) == 4 ? kChunk : kb, copied, ldo};
-    const auto scales = [&](const Operand& o, int64_t rows) {
-        const bool words = o.ks == 1 && o.rs % 4 == 0 && kb <= o.rs && reinterpret_cast<uintptr_t>(o.s) % 4 == 0;
-        return Scales{o.s, o.rs, o.ks, o.shift, (int)rows, words};
-    };
-    const Scales sa = scales(A, R), sb = scales(B, Cn);
+    const Scales sa = scales_of(A, R, kb), sb = scales_of(B, Cn, kb);
     auto k = proj8_kernel<BN, PAIRS, A_MN, B_MN, TO>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kBlocks;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    Launch l(kThreads, C::SMEM, kBlocks, st);
     static std::atomic<int> known[kDevices];
-    const int64_t most = resident_clusters(k, cfg, kBlocks, known);
-    cfg.gridDim = dim3((unsigned)(kBlocks * (tiles < most ? tiles : most)));
-    return cudaLaunchKernelEx(&cfg, k, ma, mb, mo, sa, sb, out, q, device_error_word());
+    const int64_t most = resident_clusters(k, l.cfg, kBlocks, known);
+    l.cfg.gridDim = dim3((unsigned)(kBlocks * (tiles < most ? tiles : most)));
+    return cudaLaunchKernelEx(&l.cfg, k, ma, mb, mo, sa, sb, out, q, device_error_word());
 }
+
+// A's rows to the lanes, B's few to the columns: out[j * ldo + i].
+template <int BN, bool A_MN, typename TO>
+cudaError_t go_few(const Operand& A, const Operand& B, int64_t R, int64_t Cn, int64_t depth, TO* out, int64_t ldo,
+                   cudaStream_t st) {
+    using C = Few<BN>;
+    CUtensorMap ma, mb;
+    if (!map_of(&ma, A, R, depth, 128) || !map_of(&mb, B, Cn, depth, BN)) return cudaErrorInvalidValue;
+    const int64_t tr = (R + BM - 1) / BM, tc = (Cn + BN - 1) / BN;
+    if (tr * 8 >= (int64_t(1) << 31) || tc > 65535) return kGridLimit;
+    FewShape q{(int)R, (int)Cn, (int)((depth + BK - 1) / BK), 0, ldo};
+    auto k = proj8_few_kernel<BN, A_MN, TO>;
+    constexpr int most = 226 * 1024;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e != cudaSuccess) return e;
+    // The most blocks a tile with which all run at once, an SM to each (w of 10576 x 2560, 83 tiles, one
+    // token: 8.5 us with one block a tile, 8.9 with three, two to an SM; 2560 x 5120, 20 tiles: 9.0 with
+    // two, 6.5 with five, 10.7 with seven, of which some clusters wait); fewer where the largest share
+    // stays the same.  A block's share is at most kFewBlocks.
+    static std::atomic<int> known[9][kDevices];
+    int split = (q.kb + kFewBlocks - 1) / kFewBlocks;
+    for (int n = std::min(8, q.kb); n > split; --n) {
+        const Launch l(kFewThreads, most, n, st);
+        if (tr * tc > resident_clusters(k, l.cfg, n, known[n])) continue;
+        const int share = (q.kb + n - 1) / n;
+        split = (q.kb + share - 1) / share;
+    }
+    const int others = tr * tc * split > sm_count();
+    q.ns = std::min({C::stages(split, others), kFewStages, (q.kb + split - 1) / split});
+    Launch l(kFewThreads, C::smem(split, q.ns), split, st);
+    l.early();
+    l.cfg.gridDim = dim3((unsigned)(tr * split), (unsigned)tc);
+    return cudaLaunchKernelEx(&l.cfg, k, ma, mb, scales_of(A, R, q.kb), scales_of(B, Cn, q.kb), out, q, device_error_word());
+}
+
+// Whether the few rows' kernel takes a product.
+bool few(int64_t R, int64_t depth) { return R <= kFewRows && (depth + BK - 1) / BK <= 8 * kFewBlocks; }
 
 template <bool A_MN, bool B_MN, typename TO>
 cudaError_t pick(const Operand& A, const Operand& B, int64_t R, int64_t C, int64_t depth, TO* out, int64_t ldo,
                  cudaStream_t st) {
-    if (R > 256) return go<224, 2, A_MN, B_MN, TO>(A, B, R, C, depth, out, ldo, st);
+    if constexpr (!A_MN)
+        if (few(R, depth))
+            return R <= 16   ? go_few<16, B_MN, TO>(B, A, C, R, depth, out, ldo, st)
+                   : R <= 32 ? go_few<32, B_MN, TO>(B, A, C, R, depth, out, ldo, st)
+                             : go_few<64, B_MN, TO>(B, A, C, R, depth, out, ldo, st);
     return go<224, 1, A_MN, B_MN, TO>(A, B, R, C, depth, out, ldo, st);
 }
 

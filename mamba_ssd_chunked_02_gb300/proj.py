@@ -20,6 +20,8 @@ from __future__ import annotations
 
 import ctypes
 
+import torch
+
 from . import layer as _layer
 
 ADD_NORM_QUANT = 1
@@ -97,12 +99,11 @@ def proj8_fwd(x, x_scales, w, w_scales, *, dtype=None, y=None, stream=None):
 
     x [b,T,K] e4m3 with x_scales in row groups, w [N,K] e4m3 with w_scales in block groups, as
     quant8 and add_norm_fwd return them.  Prompts and single tokens alike."""
-    from torch import bfloat16, float32
     if dtype is None:
-        dtype = bfloat16 if y is None else y.dtype
-    if dtype not in (bfloat16, float32):
+        dtype = torch.bfloat16 if y is None else y.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise TypeError(f"unsupported element type {dtype}: dtype must be torch.bfloat16 or torch.float32")
-    return _ext().proj8_fwd(x, x_scales, w, w_scales, dtype == float32, y, stream)
+    return _ext().proj8_fwd(x, x_scales, w, w_scales, dtype is torch.float32, y, stream)
 
 
 def proj8_bwd(dy, x, x_scales, w, w_scales, *, need_dx=True, need_dw=True, grads=None, workspace=None, stream=None):
