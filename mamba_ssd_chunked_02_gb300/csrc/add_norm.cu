@@ -12,6 +12,7 @@
 #include <initializer_list>
 #include <utility>
 
+#include "common.cuh"
 #include "internal.h"
 #include "proj.cuh"
 
@@ -55,6 +56,8 @@ fwd_kernel(const TI* __restrict__ x, const TR* res, const float* __restrict__ w,
     __shared__ float2 red[32];
     const int64_t row = WARP ? (int64_t)blockIdx.x * kTeams + (threadIdx.x >> 5) : blockIdx.x;
     const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;
+    grid_dep_wait();
+    grid_dep_launch();
     if (row >= q.rows) return;
     const int64_t b = (uint32_t)row / q.T, t = (uint32_t)row - (uint32_t)b * q.T;
     const TI* xr = x + b * q.sx.b + t * q.sx.t;
@@ -131,6 +134,8 @@ bwd_kernel(const TR* __restrict__ total, const float* __restrict__ w, const TI* 
     __shared__ float2 red[2][32];
     const int slot = WARP ? (int)blockIdx.x * kTeams + (threadIdx.x >> 5) : blockIdx.x;
     const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;
+    grid_dep_wait();
+    grid_dep_launch();
     if (slot >= slots) return;
     const int units = U::count(q.D);
     float* pr = part ? part + (int64_t)slot * q.D : nullptr;
@@ -231,12 +236,16 @@ cudaError_t fwd_go(const AddNormArgs& a, const void* x_, const void* res_, const
     TR* t = static_cast<TR*>(t_);
     const int64_t n = Units<TI, VEC>::count((int)a.D);
     const unsigned wb = (unsigned)((q.rows + kTeams - 1) / kTeams), bb = (unsigned)q.rows;
-    if (n <= 32) fwd_kernel<TI, TR, VEC, 1, true, QUANT><<<wb, kTeams * 32, 0, st>>>(x, res, w, y, s, t, q);
-    else if (n <= 64) fwd_kernel<TI, TR, VEC, 2, true, QUANT><<<wb, kTeams * 32, 0, st>>>(x, res, w, y, s, t, q);
-    else if (n <= 512) fwd_kernel<TI, TR, VEC, 1, false, QUANT><<<bb, threads_of(n, 1), 0, st>>>(x, res, w, y, s, t, q);
-    else if (n <= 2048) fwd_kernel<TI, TR, VEC, 2, false, QUANT><<<bb, threads_of(n, 2), 0, st>>>(x, res, w, y, s, t, q);
-    else fwd_kernel<TI, TR, VEC, 0, false, QUANT><<<bb, 1024, 0, st>>>(x, res, w, y, s, t, q);
-    return cudaGetLastError();
+    const auto go = [&](auto k, unsigned blocks, int threads) {
+        return launch_kernel(k, dim3(blocks), dim3((unsigned)threads), 0, st, early(blocks), x, res, w, y, s, t, q);
+    };
+    cudaError_t e;
+    if (n <= 32) e = go(fwd_kernel<TI, TR, VEC, 1, true, QUANT>, wb, kTeams * 32);
+    else if (n <= 64) e = go(fwd_kernel<TI, TR, VEC, 2, true, QUANT>, wb, kTeams * 32);
+    else if (n <= 512) e = go(fwd_kernel<TI, TR, VEC, 1, false, QUANT>, bb, threads_of(n, 1));
+    else if (n <= 2048) e = go(fwd_kernel<TI, TR, VEC, 2, false, QUANT>, bb, threads_of(n, 2));
+    else e = go(fwd_kernel<TI, TR, VEC, 0, false, QUANT>, bb, 1024);
+    return e;
 }
 
 template <typename TI, typename TR, bool VEC>
@@ -251,12 +260,16 @@ cudaError_t bwd_go(const AddNormArgs& a, const void* t_, const float* w, const v
     const int64_t n = Units<TI, VEC>::count((int)a.D);
     const int slots = (int)add_norm_bwd_slots(a);
     const unsigned wb = (unsigned)((slots + kTeams - 1) / kTeams), bb = (unsigned)slots;
-    if (n <= 32) bwd_kernel<TI, TR, VEC, 1, true><<<wb, kTeams * 32, 0, st>>>(t, w, dy, dt, dx, dr, part, slots, q);
-    else if (n <= 64) bwd_kernel<TI, TR, VEC, 2, true><<<wb, kTeams * 32, 0, st>>>(t, w, dy, dt, dx, dr, part, slots, q);
-    else if (n <= 512) bwd_kernel<TI, TR, VEC, 1, false><<<bb, threads_of(n, 1), 0, st>>>(t, w, dy, dt, dx, dr, part, slots, q);
-    else if (n <= 2048) bwd_kernel<TI, TR, VEC, 2, false><<<bb, threads_of(n, 2), 0, st>>>(t, w, dy, dt, dx, dr, part, slots, q);
-    else bwd_kernel<TI, TR, VEC, 0, false><<<bb, 1024, 0, st>>>(t, w, dy, dt, dx, dr, part, slots, q);
-    return cudaGetLastError();
+    const auto go = [&](auto k, unsigned blocks, int threads) {
+        return launch_kernel(k, dim3(blocks), dim3((unsigned)threads), 0, st, early(blocks), t, w, dy, dt, dx, dr, part, slots, q);
+    };
+    cudaError_t e;
+    if (n <= 32) e = go(bwd_kernel<TI, TR, VEC, 1, true>, wb, kTeams * 32);
+    else if (n <= 64) e = go(bwd_kernel<TI, TR, VEC, 2, true>, wb, kTeams * 32);
+    else if (n <= 512) e = go(bwd_kernel<TI, TR, VEC, 1, false>, bb, threads_of(n, 1));
+    else if (n <= 2048) e = go(bwd_kernel<TI, TR, VEC, 2, false>, bb, threads_of(n, 2));
+    else e = go(bwd_kernel<TI, TR, VEC, 0, false>, bb, 1024);
+    return e;
 }
 
 // Every access of a unit is aligned.

@@ -10,8 +10,8 @@
 // no transposed copy is made: the forward product takes x and w with the contracted index
 // inside, dx = dy w takes w with it outside, dw = dy^T x both.
 //
-// proj8_kernel: a cluster of PAIRS pairs of blocks; a pair's two tensor cores work on one tile
-// of 256 x BN (cta_group::2), and the pairs, one below the other, share B's tile by multicast.
+// proj8_kernel: pairs of blocks whose two tensor cores work on one tile of 256 x BN (cta_group::2),
+// each block with 128 rows of A and half of B's columns in its shared memory.
 // Warp roles: 0 TMA, 1 MMA (and tensor memory), 2 scales of A, 3 scales of B, 4-11 epilogue,
 // 12 hands the scales to the tensor cores.
 #include <cuda_bf16.h>
@@ -33,7 +33,7 @@ using namespace tc;
 constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s: far beyond any legitimate wait
 constexpr int kThreads = 416;
 constexpr int kDevices = 64;
-constexpr int kPanel = 12;
+constexpr int kPanel = 12;   // columns of tiles a panel   // columns of tiles a panel
 constexpr int BM = 128, BK = 128;
 
 // D[tmem] (+)= A B with block scales (kind::mxf8f6f4: one scale per 32 contracted values).
@@ -62,8 +62,8 @@ template <bool PAIR> __device__ __forceinline__ void copy_scales(uint32_t tmem, 
     if constexpr (PAIR) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
     else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
-// Arrives at `bar` of this block, or of the cluster's blocks in `mask`, when what was issued is done.
-template <bool PAIR> __device__ __forceinline__ void commit(uint64_t* bar, uint32_t mask = 0) {
+// Arrives at `bar` of this block, or of the pair's blocks in `mask`, when what was issued is done.
+template <bool PAIR> __device__ __forceinline__ void commit(uint64_t* bar, uint32_t mask = 3) {
     if constexpr (PAIR)
         asm volatile(
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
@@ -107,20 +107,12 @@ __device__ __forceinline__ uint32_t of_block(const void* p, uint32_t rank) {
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// A tile into this block's shared memory, its bytes counted at a barrier of the pair's even block;
-// or into that of every block in `mask`, each counted at its own pair's.
+// A tile into this block's shared memory, its bytes counted at a barrier of the pair's even block.
 __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* m, uint32_t bar, int x, int y) {
     asm volatile(
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
         "l"(m), "r"(bar), "r"(x), "r"(y)
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_pairs(void* dst, const CUtensorMap* m, uint32_t bar, int x, int y, uint32_t mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
-        " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
-        "l"(m), "r"(bar), "r"(x), "r"(y), "h"((uint16_t)mask)
         : "memory");
 }
 __device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* m, const void* src, int x, int y) {
@@ -159,14 +151,17 @@ struct Shape {
     int64_t ldo;
 };
 
-// PAIRS pairs of blocks: each pair a tile of 256 x BN, a block 128 rows of A and BN / 2 columns of B.
-template <int BN, int PAIRS, bool B_MN, int ES> struct Cfg {
+// A pair's tile of 256 x BN: a block has 128 rows of A and BN / 2 columns of B.
+template <int BN, bool B_MN, int ES> struct Cfg {
     static constexpr int HALF = BN / 2;
     static constexpr int A_BYTES = BM * BK;
     // columns of B in a stage: MN-major copies are whole boxes of 128
-    static constexpr int B_BYTES = (B_MN ? 128 : HALF) * BK, B_PART = B_BYTES / PAIRS;
+    static constexpr int B_BYTES = (B_MN ? 128 : HALF) * BK;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int NSF = 4;
+    // Two accumulators and the scales of NSF sets in 512 columns.  At 256 columns the accumulators
+    // share 32: a tile's products begin when those of the tile before have been read.
+    static constexpr bool SHARED = BN == 256;
+    static constexpr int NSF = SHARED ? 2 : 4;
     static constexpr int SFB = (BN + 127) / 128;                 // scale tiles of B
     static constexpr int SF_BYTES = 512 * (1 + SFB);
     // parts of 32 x 32 on their way out, of each of the epilogue's 8 warps
@@ -174,16 +169,17 @@ template <int BN, int PAIRS, bool B_MN, int ES> struct Cfg {
     static constexpr int FIXED = 1024 + NSF * SF_BYTES + OUT_BYTES;
     static constexpr int NS = (227 * 1024 - FIXED - 512) / STAGE < 6 ? (227 * 1024 - FIXED - 512) / STAGE : 6;
     static constexpr int SMEM = FIXED + NS * STAGE;
-    static constexpr uint32_t SF_COL = 2 * BN, SF_COLS = 4 * (1 + SFB);
+    static constexpr uint32_t ACC = SHARED ? BN - 32 : BN;       // from one accumulator to the other
+    static constexpr uint32_t SF_COL = ACC + BN, SF_COLS = 4 * (1 + SFB);
     static constexpr uint32_t COLS = 512;
-    static_assert(2 * BN + NSF * SF_COLS <= COLS, "tensor memory");
-    static_assert(STAGE % 1024 == 0 && B_PART % 1024 == 0 && HALF <= 128, "tiles");
+    static_assert(SF_COL + NSF * SF_COLS <= COLS, "tensor memory");
+    static_assert(STAGE % 1024 == 0 && HALF <= 128, "tiles");
 };
 
 struct Bars {
     uint64_t full[6], empty[6];
     uint64_t sf_there[4], sf_full[4], sf_empty[4];
-    uint64_t acc_full[2], acc_empty[2];
+    uint64_t acc_full[2], acc_empty[2], acc_shared;
     uint64_t drain;
     uint32_t tmem;
     int abort;
@@ -211,12 +207,12 @@ __device__ __forceinline__ uint4 gather_scales(const Scales& s, bool words, cons
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int BN, int PAIRS, bool A_MN, bool B_MN, typename TO>
+template <int BN, bool A_MN, bool B_MN, typename TO>
 __global__ void __launch_bounds__(kThreads, 1)
 proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
              const __grid_constant__ CUtensorMap tm_o, const Scales sa, const Scales sb, TO* __restrict__ out, const Shape q,
              int32_t* err) {
-    using C = Cfg<BN, PAIRS, B_MN, sizeof(TO)>;
+    using C = Cfg<BN, B_MN, sizeof(TO)>;
     constexpr bool PAIR = true;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -225,12 +221,10 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     __shared__ Bars bars;
     volatile int* abort = &bars.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // rank in the pair, the pair of the cluster, the pair's even block, which counts its copies
-    const int rank = (int)block_rank() & 1, pair = (int)block_rank() >> 1;
-    const uint32_t even = block_rank() & ~1u;
-    const int first = blockIdx.x / (2 * PAIRS), step = gridDim.x / (2 * PAIRS);
-    constexpr int kRows = 2 * BM, kAll = (1 << 2 * PAIRS) - 1;
-    const uint32_t both = 3u << (2 * pair);
+    // the even block (rank 0) counts the copies and issues the products of both
+    const int rank = (int)block_rank();
+    const int first = blockIdx.x / 2, step = gridDim.x / 2;
+    constexpr int kRows = 2 * BM;
     // Tiles go down panels of q.panel columns of tiles, a row of the panel at a time: the clusters that
     // run side by side then share few rows of A and of B.
     const auto place = [&](int tile, int* r, int* c) {
@@ -239,12 +233,12 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         *r = in / w;
         *c = p * q.panel + in - *r * w;
     };
-    const auto row_of = [&](int r) { return (r * PAIRS + pair) * kRows + rank * BM; };
+    const auto row_of = [&](int r) { return r * kRows + rank * BM; };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NS; ++i) {
             mbar_init(&bars.full[i], 1);
-            mbar_init(&bars.empty[i], PAIRS);   // every pair that the copy reaches
+            mbar_init(&bars.empty[i], 1);
         }
         for (int i = 0; i < C::NSF; ++i) {
             mbar_init(&bars.sf_there[i], 2);   // warps 2 and 3
@@ -255,6 +249,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             mbar_init(&bars.acc_full[i], 1);
             mbar_init(&bars.acc_empty[i], 16);   // eight warps of two blocks
         }
+        mbar_init(&bars.acc_shared, 8);         // the four warps of two blocks that read the shared columns
         mbar_init(&bars.drain, 1);
         bars.abort = 0;
         fence_barrier_init();
@@ -265,7 +260,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = bars.tmem;
-
+    grid_dep_wait();   // what is read was written by the kernel before
     // The producing and the issuing warp run whole, with one lane elected for each instruction: what
     // the loop counts then stays in uniform registers, where the copies and products take it from
     // (issued from a loop of one lane, four products took 650 cycles instead of 450).
@@ -277,7 +272,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         int it = 0, st = 0;
         uint32_t phase = 1;
         bool ok = true;
-        const uint32_t full0 = of_block(&bars.full[0], even);
+        const uint32_t full0 = of_block(&bars.full[0], 0);
         for (int tile = first; tile < q.tiles && ok; tile += step) {
             int r, c;
             place(tile, &r, &c);
@@ -291,17 +286,13 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                     if (rank == 0) mbar_arrive_expect_tx(&bars.full[st], 2 * C::STAGE);
                     const uint32_t bar = full0 + 8 * st;
                     tma_load_pair(a, &tm_a, bar, A_MN ? r0 : kb * BK, A_MN ? kb * BK : r0);
-                    if constexpr (PAIRS == 1) {
-                        tma_load_pair(b, &tm_b, bar, B_MN ? c0 : kb * BK, B_MN ? kb * BK : c0);
-                    } else {   // this pair's part of the tile, for the blocks of the same rank
-                        const int at = kb * BK + (B_MN ? pair * (BK / PAIRS) : 0), col = c0 + (B_MN ? 0 : pair * (C::HALF / PAIRS));
-                        tma_load_pairs(b + pair * C::B_PART, &tm_b, bar, B_MN ? col : at, B_MN ? at : col, (0x55u & kAll) << rank);
-                    }
+                    tma_load_pair(b, &tm_b, bar, B_MN ? c0 : kb * BK, B_MN ? kb * BK : c0);
                 }
                 __syncwarp();
                 if (++st == C::NS) st = 0, phase ^= 1;
             }
         }
+        grid_dep_launch();   // all copies are asked for: the next kernel may set itself up as blocks end
         if (!ok && lane == 0) {   // copies in flight land before the block ends
             if (rank == 0)
                 for (int i = it - 1; i >= 0 && i >= it - C::NS; --i)
@@ -325,9 +316,11 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 for (int k0 = 0; k0 < q.kb && ok; k0 += q.chunk, ++t) {
                     const int acc = t & 1, k1 = min(q.kb, k0 + q.chunk);
                     ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.acc_empty[acc], (t / 2 & 1) ^ 1, abort, kWaitNs));
+                    if (C::SHARED && ok && t > 0)
+                        ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.acc_shared, (t - 1) & 1, abort, kWaitNs));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t d = tmem + acc * BN;
+                    const uint32_t d = tmem + acc * C::ACC;
                     bool there = false;   // the next stage's operands, asked for ahead
                     for (int kb = k0; kb < k1 && ok; kb += 4) {
                         const uint32_t ta = tmem + C::SF_COL + sf * C::SF_COLS;
@@ -358,9 +351,9 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                                 for (int k = 0; k < 4; ++k)
                                     mma_scaled<PAIR>(d, a0 + at + k * a_step, b0 + at + k * b_step, idesc | i << 4 | i << 29, ta,
                                                      ta + 4, kb > k0 || i > 0 || k > 0);
-                                commit<PAIR>(&bars.empty[now], kAll);
-                                if (i == 3 || last) commit<PAIR>(&bars.sf_empty[sf], both);
-                                if (last) commit<PAIR>(&bars.acc_full[acc], both);
+                                commit<PAIR>(&bars.empty[now]);
+                                if (i == 3 || last) commit<PAIR>(&bars.sf_empty[sf]);
+                                if (last) commit<PAIR>(&bars.acc_full[acc]);
                             }
                             there = __all_sync(0xffffffffu, there);
                         }
@@ -368,7 +361,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                     }
                 }
             if (!ok && elected()) {
-                commit<PAIR>(&bars.drain, 1u << even);
+                commit<PAIR>(&bars.drain, 1);
                 mbar_wait(&bars.drain, 0, kWaitNs);
             }
         }
@@ -432,7 +425,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         // Scales in shared memory to the tensor cores' proxy.  A warp of its own, as the fence waits for
         // all that its warp has in flight: behind the loads of later sets it took 2000 cycles.
         if (lane == 0) {
-            const uint32_t full0 = of_block(&bars.sf_full[0], even);
+            const uint32_t full0 = of_block(&bars.sf_full[0], 0);
             int left = first < q.tiles ? ((q.tiles - 1 - first) / step + 1) * ((q.kb + 3) / 4) : 0;
             int sf = 0;
             for (uint32_t phase = 0; left > 0; --left) {
@@ -459,15 +452,23 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 if (!ok) break;
                 tc_fence_after();
                 const int r0 = row_of(rt) + quad * 32, c0 = ct * BN;
-                const uint32_t from = tmem + acc * BN + ((uint32_t)(quad * 32) << 16);
+                const uint32_t from = tmem + acc * C::ACC + ((uint32_t)(quad * 32) << 16);
                 if (k0 > 0) {   // what is added to has been written
                     if (elected()) bulk_wait<0>();
                     __syncwarp();
                 }
 #pragma unroll 1
-                for (int c = 32 * half; c < BN; c += 64) {
+                for (int i = half; i < BN / 32; i += 2) {
+                    // the columns that the next tile's accumulator shares come first: the last 32 of the
+                    // even accumulator, the first of the odd one
+                    const int c = 32 * (C::SHARED && acc == 0 && half == 1 ? (i + 6) % 8 : i);
                     uint32_t v[32];
                     tmem_ld32_sync(from + c, v);
+                    if (C::SHARED && i == half && half != acc) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_at(of_block(&bars.acc_shared, 0));
+                    }
                     if (r0 >= q.R || c0 + c >= q.C) continue;
                     uint8_t* part = stage + n * C::OUT;
                     if (C::OUTS == 2) n ^= 1;
@@ -511,7 +512,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_at(of_block(&bars.acc_empty[acc], even));
+                if (lane == 0) arrive_at(of_block(&bars.acc_empty[acc], 0));
             }
         }
         __syncwarp();
@@ -594,7 +595,6 @@ proj8_few_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
         sets[0] = gather_scales(sa, sa.words && whole, at, k0 + 4 * set, k0 + n);
         sets[1] = gather_scales(sb, sb.words && whole, bt, k0 + 4 * set, k0 + n);
     };
-    grid_dep_launch();   // the next kernel may set itself up beside this one
     if (warp >= 2) {
         grid_dep_wait();
 #pragma unroll
@@ -630,7 +630,8 @@ proj8_few_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     bool ok = true;
 
     if (warp == 0) {
-        grid_dep_wait();   // what is read was written by the kernel before
+        grid_dep_wait();     // what is read was written by the kernel before
+        grid_dep_launch();   // the next one may set itself up beside this one
         int st = 0, it = 0;
         for (uint32_t phase = 1; it < n; ++it) {
             ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.empty[st], phase, abort, kWaitNs));
@@ -802,12 +803,12 @@ Scales scales_of(const Operand& o, int64_t rows, int kb) {
 // result's norm, 1024 by 3.5e-6 where sums in fp32 registers are off by 5e-7.
 constexpr int kChunk = 32;
 
-template <int BN, int PAIRS, bool A_MN, bool B_MN, typename TO>
+template <int BN, bool A_MN, bool B_MN, typename TO>
 cudaError_t go(const Operand& A, const Operand& B, int64_t R, int64_t Cn, int64_t depth, TO* out, int64_t ldo,
                cudaStream_t st) {
-    using C = Cfg<BN, PAIRS, B_MN, sizeof(TO)>;
+    using C = Cfg<BN, B_MN, sizeof(TO)>;
     CUtensorMap ma, mb, mo;
-    if (!map_of(&ma, A, R, depth, 128) || !map_of(&mb, B, Cn, depth, (B_MN ? BK : C::HALF) / PAIRS))
+    if (!map_of(&ma, A, R, depth, 128) || !map_of(&mb, B, Cn, depth, B_MN ? BK : C::HALF))
         return cudaErrorInvalidValue;
     // the result by copies of 32 x 32, where its rows start on 16 bytes
     const uint64_t dims[2] = {(uint64_t)Cn, (uint64_t)R};
@@ -818,16 +819,17 @@ cudaError_t go(const Operand& A, const Operand& B, int64_t R, int64_t Cn, int64_
                                   2, dims, strides, box,
                                   sizeof(TO) == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
     if (!copied) mo = ma;   // not used
-    constexpr int kRows = 2 * BM * PAIRS, kBlocks = 2 * PAIRS;
+    constexpr int kRows = 2 * BM, kBlocks = 2;
     const int64_t tr = (R + kRows - 1) / kRows, tiles = tr * ((Cn + BN - 1) / BN);
     if (tiles >= (int64_t(1) << 30)) return kGridLimit;
     const int kb = (int)((depth + BK - 1) / BK);
     const Shape q{(int)R, (int)Cn, kb, (int)tr, (int)tiles, kPanel, sizeof(TO) == 4 ? kChunk : kb, copied, ldo};
     const Scales sa = scales_of(A, R, kb), sb = scales_of(B, Cn, kb);
-    auto k = proj8_kernel<BN, PAIRS, A_MN, B_MN, TO>;
+    auto k = proj8_kernel<BN, A_MN, B_MN, TO>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     Launch l(kThreads, C::SMEM, kBlocks, st);
+    l.early();
     static std::atomic<int> known[kDevices];
     const int64_t most = resident_clusters(k, l.cfg, kBlocks, known);
     l.cfg.gridDim = dim3((unsigned)(kBlocks * (tiles < most ? tiles : most)));
@@ -879,7 +881,18 @@ cudaError_t pick(const Operand& A, const Operand& B, int64_t R, int64_t C, int64
             return R <= 16   ? go_few<16, B_MN, TO>(B, A, C, R, depth, out, ldo, st)
                    : R <= 32 ? go_few<32, B_MN, TO>(B, A, C, R, depth, out, ldo, st)
                              : go_few<64, B_MN, TO>(B, A, C, R, depth, out, ldo, st);
-    return go<224, 1, A_MN, B_MN, TO>(A, B, R, C, depth, out, ldo, st);
+    // Tiles of 224 columns, whose two accumulators lie apart; of 256 where B is MN-major, so that a
+    // block's half of the columns is whole lines of memory (dx of 32768 x 10576 x 2560: 676 us at 224, of
+    // which half the rows of a copy lie across two lines); of 128 where the pairs' rounds come out
+    // shorter.  A round takes what its contracted blocks take, and what its ends take.
+    constexpr int kWide = B_MN ? 256 : 224;
+    const int64_t pairs = sm_count() / 2, tr = (R + 255) / 256, kb = (depth + BK - 1) / BK;
+    const auto cycles = [&](int64_t bn, int64_t block, int64_t ends) {
+        return (tr * ((C + bn - 1) / bn) + pairs - 1) / pairs * (kb * block + ends);
+    };
+    if (cycles(128, 330, 3000) < cycles(kWide, 2 * kWide + 40, 4000))
+        return go<128, A_MN, B_MN, TO>(A, B, R, C, depth, out, ldo, st);
+    return go<kWide, A_MN, B_MN, TO>(A, B, R, C, depth, out, ldo, st);
 }
 
 template <typename TO>

@@ -5,11 +5,13 @@
 //
 // Bytes bound: a block of 512 threads holds a tile of 128 x 128 in registers, 4 x 8 values a
 // thread, so that both kinds of groups come from one reading (the backward product takes dy
-// along its rows for dx and along its columns for dw).
+// along its rows for dx and along its columns for dw).  Kernels here and in add_norm.cu may begin
+// while the one before them ends, and wait for it before they read.
 #include <cuda_bf16.h>
 
 #include <type_traits>
 
+#include "common.cuh"
 #include "internal.h"
 #include "proj.cuh"
 
@@ -183,6 +185,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(TI) == 2 && MODE == kRow ? 3 
     const uint32_t mb = blockIdx.x / p.nb, nb = blockIdx.x - mb * p.nb;
     const int64_t m0 = (int64_t)mb * kGroup, n0 = (int64_t)nb * kGroup;
     const int rows = (int)min((int64_t)kGroup, p.M - m0), cols = (int)min((int64_t)kGroup, p.N - n0), count = cols - 8 * tx;
+    grid_dep_wait();
+    grid_dep_launch();
     // where the rows' values lie, in x and in q
     int64_t from[kPer], to[kPer];
     if (p.even) {
@@ -313,6 +317,8 @@ template <bool VEC> __global__ void __launch_bounds__(kThreads, 2) quant8_turn_k
     const int64_t m0 = (int64_t)mb * kGroup, n0 = (int64_t)nb * kGroup;
     const int rows = (int)min((int64_t)kGroup, p.M - m0), cols = (int)min((int64_t)kGroup, p.N - n0), count = cols - 8 * tx;
     const int64_t from = (m0 + ty) * p.sx.t + n0 + 8 * tx, to = (m0 + ty) * p.sq.t + n0 + 8 * tx;
+    grid_dep_wait();
+    grid_dep_launch();
     uint32_t w[kPer][2];
     float lift[kPer], rest[kPer];   // 2^120 times the row's scale, as two factors in range
 #pragma unroll
@@ -394,9 +400,8 @@ template <typename TI, int MODE> cudaError_t go(const TI* x, Tile p, cudaStream_
     if (blocks >= (int64_t(1) << 31) || p.M >= (int64_t(1) << 31)) return kGridLimit;
     const bool v = p.N % 8 == 0 && vec_ok(x, p.sx, 16, es) && (!p.qr || vec_ok(p.qr, p.sq, 8, 1)) &&
                    (!p.qc || vec_ok(p.qc, p.sq, 8, 1));
-    if (v) quant8_kernel<TI, true, MODE><<<(unsigned)blocks, kThreads, 0, st>>>(x, p);
-    else quant8_kernel<TI, false, MODE><<<(unsigned)blocks, kThreads, 0, st>>>(x, p);
-    return cudaGetLastError();
+    return launch_kernel(v ? quant8_kernel<TI, true, MODE> : quant8_kernel<TI, false, MODE>, dim3((unsigned)blocks),
+                         dim3(kThreads), 0, st, early(blocks), x, p);
 }
 
 template <int MODE> cudaError_t go(bool bf16, const void* x, const Tile& p, cudaStream_t st) {
@@ -424,9 +429,8 @@ cudaError_t launch_quant8_turn(int64_t M, int64_t N, const uint8_t* q, int64_t p
     const int64_t blocks = blocks_of(p);
     if (blocks >= (int64_t(1) << 31) || M >= (int64_t(1) << 31)) return kGridLimit;
     const bool v = N % 8 == 0 && vec_ok(q, p.sx, 8, 1) && vec_ok(qc, p.sq, 8, 1);
-    if (v) quant8_turn_kernel<true><<<(unsigned)blocks, kThreads, 0, st>>>(q, p);
-    else quant8_turn_kernel<false><<<(unsigned)blocks, kThreads, 0, st>>>(q, p);
-    return cudaGetLastError();
+    return launch_kernel(v ? quant8_turn_kernel<true> : quant8_turn_kernel<false>, dim3((unsigned)blocks), dim3(kThreads), 0,
+                         st, early(blocks), q, p);
 }
 
 }  // namespace m2
