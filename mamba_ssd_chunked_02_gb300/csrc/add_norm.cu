@@ -6,8 +6,13 @@
 // Backward, with g = dy w and n = t r:
 //   dt = r (g - n mean(g n)) + dtotal;  dx = dresidual = dt;  dw = sum over tokens of dy n
 //
-// Bytes bound: every tensor moves once.  A team (a warp for narrow rows, else a block) holds its
-// row in registers between the sum and the result; what wide rows do not fit is read again.
+// Bytes bound: every tensor moves once.  b8 T4096 D2560 bf16 with an fp32 residual: forward 145 us,
+// in 8 bits 137 us (6.7 TB/s, the measured copy rate), backward 209 us (6.4 TB/s, 0.96); one token
+// 2.1 us, the launch.
+//
+// A team (a warp for narrow rows, else a block) holds a forward row in registers between the sum
+// and the result; what wide rows do not fit is read again.  A backward team walks over tokens, so
+// that its part of dw stays in registers; the parts are summed by a second kernel, in a fixed order.
 #include <algorithm>
 #include <initializer_list>
 #include <utility>
@@ -25,6 +30,7 @@ struct Rows {
     int64_t rows;
     float eps;
     Tok sx, sres, sy, st;
+    bool flat;   // rows lie at even distances in all of the backward's inputs
 };
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -32,7 +38,15 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-// Sum over the team; `red` is not in use by an earlier call when a block's threads come here.
+// Sums over the team; `red` is not in use by an earlier call when a block's threads come here.
+template <bool WARP> __device__ __forceinline__ float team_sum(float a, float* red) {
+    a = warp_sum(a);
+    if (WARP) return a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    if (lane == 0) red[warp] = a;
+    __syncthreads();
+    return warp_sum(lane < nw ? red[lane] : 0.f);
+}
 template <bool WARP> __device__ __forceinline__ float2 team_sum(float a, float b, float2* red) {
     a = warp_sum(a);
     b = warp_sum(b);
@@ -40,6 +54,18 @@ template <bool WARP> __device__ __forceinline__ float2 team_sum(float a, float b
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
     if (lane == 0) red[warp] = make_float2(a, b);
     __syncthreads();
+    if (nw <= 8) {   // few: every thread adds them all, two a load (rows of 1024: 94 us, by shuffles 107)
+        const float4* all = reinterpret_cast<const float4*>(red);
+        float2 s = nw & 1 ? red[nw - 1] : make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < nw / 2) {
+                const float4 v = all[i];
+                s.x += v.x + v.z;
+                s.y += v.y + v.w;
+            }
+        return s;
+    }
     const float2 v = lane < nw ? red[lane] : make_float2(0.f, 0.f);
     return make_float2(warp_sum(v.x), warp_sum(v.y));
 }
@@ -51,9 +77,9 @@ template <typename TI, typename TR, bool VEC, int VPT, bool WARP, bool QUANT>
 __global__ void __launch_bounds__(WARP ? kTeams * 32 : 1024)
 fwd_kernel(const TI* __restrict__ x, const TR* res, const float* __restrict__ w, TI* __restrict__ y,
            uint8_t* __restrict__ s, TR* total, Rows q) {
-    using U = Units<TI, VEC>;
+    using U = Units<16 / sizeof(TI), VEC>;
     constexpr int V = U::V;
-    __shared__ float2 red[32];
+    __shared__ float red[32];
     const int64_t row = WARP ? (int64_t)blockIdx.x * kTeams + (threadIdx.x >> 5) : blockIdx.x;
     const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;
     grid_dep_wait();
@@ -80,7 +106,7 @@ fwd_kernel(const TI* __restrict__ x, const TR* res, const float* __restrict__ w,
         }
         U::store(tr, u, q.D, v);
     };
-    const auto scale = [&] { return __frsqrt_rn(team_sum<WARP>(ss, 0.f, red).x / (float)q.D + q.eps); };
+    const auto scale = [&] { return __frsqrt_rn(team_sum<WARP>(ss, red) / (float)q.D + q.eps); };
     auto result = [&](int u, float (&v)[V], float r) {
         float f[V];
         if (u < units) {
@@ -123,22 +149,33 @@ fwd_kernel(const TI* __restrict__ x, const TR* res, const float* __restrict__ w,
     }
 }
 
+// A backward unit's V channels are 16 bytes of the residual's type, so that neighbouring lanes'
+// accesses touch (with 8 channels of fp32 a lane, every access reads half of each sector).
+template <typename TR, bool VEC> using BwdUnits = Units<16 / sizeof(TR), VEC>;
+template <typename E, int V> __device__ __forceinline__ void fetch(const uint4* from, float (&o)[V]) {
+    Conv<E, V>::to(*reinterpret_cast<const typename Pack<E, V>::Raw*>(from), o);
+}
+
 // Team `slot` of `slots` has tokens slot, slot + slots, ...; its dw goes to part[slot].
-template <typename TI, typename TR, bool VEC, int VPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? kTeams * 32 : 1024)
+// AHEAD: the next row is copied into each thread's own room in shared memory while this one is
+// summed and applied.
+template <typename TI, typename TR, bool VEC, int VPT, bool WARP, bool AHEAD>
+__global__ void __launch_bounds__(WARP ? kTeams * 32 : VPT == 1 ? 512 : 1024, WARP ? 3 : VPT == 1 ? 2 : 1)
 bwd_kernel(const TR* __restrict__ total, const float* __restrict__ w, const TI* __restrict__ dy,
            const TR* __restrict__ dtotal, TI* __restrict__ dx, TR* __restrict__ dres, float* __restrict__ part, int slots,
            Rows q) {
-    using U = Units<TI, VEC>;
+    using U = BwdUnits<TR, VEC>;
+    static_assert(!AHEAD || (VEC && VPT > 0), "copies are of whole units");
     constexpr int V = U::V, K = VPT > 0 ? VPT : 1;
-    __shared__ float2 red[2][32];
+    __shared__ __align__(16) float2 red[2][32];
+    extern __shared__ __align__(16) uint4 room[];   // [2 rows][K][total, dtotal, dy][threads], then w
+    constexpr int kD = V * (int)sizeof(TI), kUnit = 32 + kD;   // bytes of dy's piece, of a unit
     const int slot = WARP ? (int)blockIdx.x * kTeams + (threadIdx.x >> 5) : blockIdx.x;
     const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;
     grid_dep_wait();
     grid_dep_launch();
-    if (slot >= slots) return;
-    const int units = U::count(q.D);
-    float* pr = part ? part + (int64_t)slot * q.D : nullptr;
+    const int units = U::count(q.D), bt = blockDim.x;
+    float* pr = part && slot < slots ? part + (int64_t)slot * q.D : nullptr;
     const float inv = 1.f / (float)q.D;
     float acc[K][V];
 #pragma unroll
@@ -146,40 +183,69 @@ bwd_kernel(const TR* __restrict__ total, const float* __restrict__ w, const TI* 
 #pragma unroll
         for (int j = 0; j < V; ++j) acc[k][j] = 0.f;
     int parity = 0;
-    for (int64_t row = slot; row < q.rows; row += slots) {
-        const int64_t b = (uint32_t)row / q.T, t = (uint32_t)row - (uint32_t)b * q.T;
-        const TR* tr = total + b * q.st.b + t * q.st.t;
-        const TI* dr = dy + b * q.sy.b + t * q.sy.t;
-        const TR* er = dtotal ? dtotal + b * q.sres.b + t * q.sres.t : nullptr;
-        float ss = 0.f, gv = 0.f;
-        auto sums = [&](int u, float (&v)[V], float (&d)[V]) {
-            U::load(tr, u, q.D, v);
-            U::load(dr, u, q.D, d);
-            float f[V];
+    const auto place = [&](int64_t row, const Tok& s) {
+        if (q.flat) return row * s.t;
+        const uint32_t b = (uint32_t)row / q.T;
+        return (int64_t)b * s.b + (int64_t)((uint32_t)row - b * q.T) * s.t;
+    };
+    const auto piece = [&](int at, int k, int i) {
+        unsigned char* base = reinterpret_cast<unsigned char*>(room) + (at * K + k) * kUnit * bt;
+        return reinterpret_cast<uint4*>(base + (i < 2 ? (i * bt + threadIdx.x) * 16 : 32 * bt + threadIdx.x * kD));
+    };
+    const auto copy = [&](int64_t row, int at) {   // a group of copies, empty behind the last row
+        if (row >= q.rows) return stage_commit();
+        const TR* tr = total + place(row, q.st);
+        const TI* dr = dy + place(row, q.sy);
+        const TR* er = dtotal ? dtotal + place(row, q.sres) : nullptr;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int u = tid + k * nt;
+            if (u >= units) continue;
+            stage_copy<16>(piece(at, k, 0), tr + u * V, true);
+            if (er) stage_copy<16>(piece(at, k, 1), er + u * V, true);
+            stage_copy<kD>(piece(at, k, 2), dr + u * V, true);
+        }
+        stage_commit();
+    };
+    // each unit's weights, kept beside the rows: what comes from L1 is pushed out of it by the copies
+    // (read twice a row from there, they held the row up for longer than its sums)
+    float* ws = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(room) + 2 * K * kUnit * bt);
+    const auto weights = [&](int u, float (&f)[V]) {
+        if constexpr (AHEAD) {
+            U::load(ws, u, q.D, f);
+        } else {
 #pragma unroll
             for (int j = 0; j < V; ++j) f[j] = 1.f;
             if (w) U::load(w, u, q.D, f);
+        }
+    };
+    if constexpr (AHEAD) {
+        for (int i = threadIdx.x; i < q.D; i += bt) ws[i] = w ? w[i] : 1.f;
+        __syncthreads();
+    }
+    if (slot >= slots) return;
+    if constexpr (AHEAD) copy(slot, 0);
+    for (int64_t row = slot; row < q.rows; row += slots) {
+        float ss = 0.f, gv = 0.f, r, m;
+        const auto sums = [&](int u, const float (&v)[V], const float (&d)[V]) {
+            float f[V];
+            weights(u, f);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 ss = fmaf(v[j], v[j], ss);
                 gv = fmaf(d[j] * f[j], v[j], gv);
             }
         };
-        float r, m;
-        auto scales = [&] {
+        const auto scales = [&] {
             // two halves of red in turn: the next token's sums do not overwrite one being read
             const float2 s = team_sum<WARP>(ss, gv, red[parity]);
-            parity ^= 1;
             r = __frsqrt_rn(s.x * inv + q.eps);
             m = r * (s.y * inv);
         };
-        // a: this unit's part of dw, added to
-        auto result = [&](int u, const float (&v)[V], const float (&d)[V], float (&a)[V]) {
-            float f[V], e[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) f[j] = 1.f, e[j] = 0.f;
-            if (w) U::load(w, u, q.D, f);
-            if (er) U::load(er, u, q.D, e);
+        // e: dtotal; a: this unit's part of dw, added to
+        const auto result = [&](int u, const float (&v)[V], const float (&d)[V], float (&e)[V], float (&a)[V]) {
+            float f[V];
+            weights(u, f);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float n = v[j] * r;
@@ -189,30 +255,78 @@ bwd_kernel(const TR* __restrict__ total, const float* __restrict__ w, const TI* 
             U::store(dx + row * q.D, u, q.D, e);
             if (dres) U::store(dres + row * q.D, u, q.D, e);
         };
-        if constexpr (VPT > 0) {
-            float v[K][V], d[K][V];
+        const auto zero = [](float (&e)[V]) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) e[j] = 0.f;
+        };
+        if constexpr (AHEAD) {
+            copy(row + slots, parity ^ 1);
+            stage_wait<1>();
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (tid + k * nt < units) sums(tid + k * nt, v[k], d[k]);
+                if (tid + k * nt < units) {
+                    float v[V], d[V];
+                    fetch<TR>(piece(parity, k, 0), v);
+                    fetch<TI>(piece(parity, k, 2), d);
+                    sums(tid + k * nt, v, d);
+                }
             scales();
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (tid + k * nt < units) result(tid + k * nt, v[k], d[k], acc[k]);
+                if (tid + k * nt < units) {
+                    float v[V], d[V], e[V];
+                    fetch<TR>(piece(parity, k, 0), v);
+                    fetch<TI>(piece(parity, k, 2), d);
+                    if (dtotal) fetch<TR>(piece(parity, k, 1), e);
+                    else zero(e);
+                    result(tid + k * nt, v, d, e, acc[k]);
+                }
         } else {
-            float v[V], d[V];
-            for (int u = tid; u < units; u += nt) sums(u, v, d);
-            scales();
-            for (int u = tid; u < units; u += nt) {
-                U::load(tr, u, q.D, v);
-                U::load(dr, u, q.D, d);
-                float a[V];
+            const TR* tr = total + place(row, q.st);
+            const TI* dr = dy + place(row, q.sy);
+            const TR* er = dtotal ? dtotal + place(row, q.sres) : nullptr;
+            float v[K][V], d[K][V], e[V];
+            const auto third = [&](int u) {
+                if (er) U::load(er, u, q.D, e);
+                else zero(e);
+            };
+            if constexpr (VPT > 0) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) a[j] = 0.f;
-                if (pr && row != slot) U::load(pr, u, q.D, a);
-                result(u, v, d, a);
-                if (pr) U::store(pr, u, q.D, a);
+                for (int k = 0; k < K; ++k)
+                    if (tid + k * nt < units) {
+                        U::load(tr, tid + k * nt, q.D, v[k]);
+                        U::load(dr, tid + k * nt, q.D, d[k]);
+                    }
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (tid + k * nt < units) sums(tid + k * nt, v[k], d[k]);
+                scales();
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (tid + k * nt < units) {
+                        third(tid + k * nt);
+                        result(tid + k * nt, v[k], d[k], e, acc[k]);
+                    }
+            } else {
+                for (int u = tid; u < units; u += nt) {
+                    U::load(tr, u, q.D, v[0]);
+                    U::load(dr, u, q.D, d[0]);
+                    sums(u, v[0], d[0]);
+                }
+                scales();
+                for (int u = tid; u < units; u += nt) {
+                    U::load(tr, u, q.D, v[0]);
+                    U::load(dr, u, q.D, d[0]);
+                    third(u);
+                    float a[V];
+                    zero(a);
+                    if (pr && row != slot) U::load(pr, u, q.D, a);
+                    result(u, v[0], d[0], e, a);
+                    if (pr) U::store(pr, u, q.D, a);
+                }
             }
         }
+        parity ^= 1;
     }
     if (VPT > 0 && pr)
 #pragma unroll
@@ -221,7 +335,8 @@ bwd_kernel(const TR* __restrict__ total, const float* __restrict__ w, const TI* 
 }
 
 Rows rows_of(const AddNormArgs& a) {
-    return Rows{(uint32_t)a.T, (int)a.D, a.b * a.T, a.eps, a.sx, a.sres, a.sy, a.st};
+    const auto even = [&](const Tok& s) { return a.b <= 1 || s.b == a.T * s.t; };
+    return Rows{(uint32_t)a.T, (int)a.D, a.b * a.T, a.eps, a.sx, a.sres, a.sy, a.st, even(a.sres) && even(a.sy) && even(a.st)};
 }
 int threads_of(int64_t units, int vpt) { return (int)std::min<int64_t>(1024, (units + vpt * 32 - 1) / (vpt * 32) * 32); }
 
@@ -234,7 +349,7 @@ cudaError_t fwd_go(const AddNormArgs& a, const void* x_, const void* res_, const
     const TR* res = static_cast<const TR*>(res_);
     TI* y = static_cast<TI*>(y_);
     TR* t = static_cast<TR*>(t_);
-    const int64_t n = Units<TI, VEC>::count((int)a.D);
+    const int64_t n = Units<16 / sizeof(TI), VEC>::count((int)a.D);
     const unsigned wb = (unsigned)((q.rows + kTeams - 1) / kTeams), bb = (unsigned)q.rows;
     const auto go = [&](auto k, unsigned blocks, int threads) {
         return launch_kernel(k, dim3(blocks), dim3((unsigned)threads), 0, st, early(blocks), x, res, w, y, s, t, q);
@@ -257,28 +372,31 @@ cudaError_t bwd_go(const AddNormArgs& a, const void* t_, const float* w, const v
     const TI* dy = static_cast<const TI*>(dy_);
     TI* dx = static_cast<TI*>(dx_);
     TR* dr = static_cast<TR*>(dr_);
-    const int64_t n = Units<TI, VEC>::count((int)a.D);
+    const int64_t n = BwdUnits<TR, VEC>::count((int)a.D);
     const int slots = (int)add_norm_bwd_slots(a);
     const unsigned wb = (unsigned)((slots + kTeams - 1) / kTeams), bb = (unsigned)slots;
-    const auto go = [&](auto k, unsigned blocks, int threads) {
-        return launch_kernel(k, dim3(blocks), dim3((unsigned)threads), 0, st, early(blocks), t, w, dy, dt, dx, dr, part, slots, q);
+    const auto go = [&](auto k, unsigned blocks, int threads, int ahead) {   // ahead: units a thread, 0: none is copied
+        const size_t room = ahead ? (size_t)2 * ahead * (32 + BwdUnits<TR, VEC>::V * sizeof(TI)) * threads + 4 * (size_t)a.D : 0;
+        if (room > 40 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)room);
+            if (e != cudaSuccess) return e;
+        }
+        return launch_kernel(k, dim3(blocks), dim3((unsigned)threads), room, st, early(blocks), t, w, dy, dt, dx, dr, part, slots, q);
     };
-    cudaError_t e;
-    if (n <= 32) e = go(bwd_kernel<TI, TR, VEC, 1, true>, wb, kTeams * 32);
-    else if (n <= 64) e = go(bwd_kernel<TI, TR, VEC, 2, true>, wb, kTeams * 32);
-    else if (n <= 512) e = go(bwd_kernel<TI, TR, VEC, 1, false>, bb, threads_of(n, 1));
-    else if (n <= 2048) e = go(bwd_kernel<TI, TR, VEC, 2, false>, bb, threads_of(n, 2));
-    else e = go(bwd_kernel<TI, TR, VEC, 0, false>, bb, 1024);
-    return e;
+    if (n <= 32) return go(bwd_kernel<TI, TR, VEC, 1, true, VEC>, wb, kTeams * 32, VEC);
+    if (n <= 64) return go(bwd_kernel<TI, TR, VEC, 2, true, VEC>, wb, kTeams * 32, 2 * VEC);
+    if (n <= 512) return go(bwd_kernel<TI, TR, VEC, 1, false, VEC>, bb, threads_of(n, 1), VEC);
+    if (n <= 2048) return go(bwd_kernel<TI, TR, VEC, 2, false, VEC>, bb, threads_of(n, 2), 2 * VEC);
+    return go(bwd_kernel<TI, TR, VEC, 0, false, false>, bb, 1024, 0);
 }
 
-// Every access of a unit is aligned.
-bool vec(const AddNormArgs& a, const float* w, std::initializer_list<std::pair<const void*, Tok>> io,
+// Every access of a unit of V channels is aligned.
+bool vec(const AddNormArgs& a, int64_t V, const float* w, std::initializer_list<std::pair<const void*, Tok>> io,
          std::initializer_list<std::pair<const void*, Tok>> res, const void* q8) {
-    const int64_t es = a.bf16 ? 2 : 4, rs = a.res_bf16 ? 2 : 4, V = a.bf16 ? 8 : 4;
+    const int64_t es = a.bf16 ? 2 : 4, rs = a.res_bf16 ? 2 : 4;
     if (a.D % V || reinterpret_cast<uintptr_t>(w) % 16) return false;
     for (const auto& t : io)
-        if (!vec_ok(t.first, t.second, 16, es)) return false;
+        if (!vec_ok(t.first, t.second, V * es, es)) return false;
     for (const auto& t : res)
         if (t.first && !vec_ok(t.first, t.second, 16, rs)) return false;
     return !q8 || vec_ok(q8, a.sy, V, 1);
@@ -289,8 +407,8 @@ bool vec(const AddNormArgs& a, const float* w, std::initializer_list<std::pair<c
 cudaError_t launch_add_norm_fwd(const AddNormArgs& a, const void* x, const void* residual, const float* w, void* y,
                                 uint8_t* s, void* total, cudaStream_t st) {
     if (a.b * a.T == 0 || a.D == 0) return cudaSuccess;
-    const bool v = a.quant ? vec(a, w, {{x, a.sx}}, {{residual, a.sres}, {total, a.st}}, y)
-                           : vec(a, w, {{x, a.sx}, {y, a.sy}}, {{residual, a.sres}, {total, a.st}}, nullptr);
+    const bool v = a.quant ? vec(a, a.bf16 ? 8 : 4, w, {{x, a.sx}}, {{residual, a.sres}, {total, a.st}}, y)
+                           : vec(a, a.bf16 ? 8 : 4, w, {{x, a.sx}, {y, a.sy}}, {{residual, a.sres}, {total, a.st}}, nullptr);
     const auto go = [&](auto f) { return f(a, x, residual, w, y, s, total, st); };
     typedef __nv_bfloat16 bf;
     if (!a.bf16)
@@ -304,9 +422,11 @@ cudaError_t launch_add_norm_fwd(const AddNormArgs& a, const void* x, const void*
 }
 
 int64_t add_norm_bwd_slots(const AddNormArgs& a) {
-    // the threads an SM holds, in teams of a row's width
-    const int64_t units = a.bf16 ? (a.D + 7) / 8 : (a.D + 3) / 4;
-    const int64_t per_sm = units <= 64 ? 64 : std::max<int64_t>(1, 2048 / threads_of(units, units <= 512 ? 1 : 2));
+    // the teams an SM holds, by registers and by the room of the rows copied ahead
+    const int64_t units = a.res_bf16 ? (a.D + 7) / 8 : (a.D + 3) / 4;
+    const int64_t per_sm = units <= 32 ? 3 * kTeams : units <= 64 ? 2 * kTeams
+                           : units <= 512 ? std::max<int64_t>(2, 1280 / threads_of(units, 1))
+                                          : std::max<int64_t>(1, 1000 / threads_of(units, 2));
     return std::max<int64_t>(1, std::min<int64_t>(a.b * a.T, (int64_t)sm_count() * per_sm));
 }
 
@@ -317,7 +437,7 @@ cudaError_t launch_add_norm_bwd(const AddNormArgs& a, const void* total, const f
     if (!dw) part = nullptr;
     if (!none) {
         const Tok row{0, a.D};
-        const bool v = vec(a, w, {{dy, a.sy}, {dx, row}}, {{total, a.st}, {dtotal, a.sres}, {dres, row}}, nullptr) &&
+        const bool v = vec(a, a.res_bf16 ? 8 : 4, w, {{dy, a.sy}, {dx, row}}, {{total, a.st}, {dtotal, a.sres}, {dres, row}}, nullptr) &&
                        reinterpret_cast<uintptr_t>(part) % 16 == 0;
         const auto go = [&](auto f) { return f(a, total, w, dy, dtotal, dx, dres, part, st); };
         typedef __nv_bfloat16 bf;

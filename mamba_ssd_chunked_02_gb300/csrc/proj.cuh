@@ -56,8 +56,8 @@ template <bool CLEAN> __device__ __forceinline__ uint32_t e4m3_pair(float lo, fl
 // How a thread's values lie in a row of D: its unit u is V neighbours (VEC: D is a multiple of V
 // and every access aligned), or lane + 32 j of a group of 128, each in its own access.  Either
 // way kLanes neighbouring lanes hold a group.
-template <typename T, bool VEC> struct Units {
-    static constexpr int V = VEC && sizeof(T) == 2 ? 8 : 4, kLanes = kGroup / V;
+template <int WIDE, bool VEC> struct Units {
+    static constexpr int V = VEC ? WIDE : 4, kLanes = kGroup / V;
     static __host__ __device__ int count(int D) { return VEC ? D / V : (D + kGroup - 1) / kGroup * 32; }
     static __device__ __forceinline__ int at(int u, int j) { return VEC ? u * V + j : (u >> 5) * kGroup + (u & 31) + 32 * j; }
 
