@@ -54,16 +54,15 @@ template <bool WARP> __device__ __forceinline__ float2 team_sum(float a, float b
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
     if (lane == 0) red[warp] = make_float2(a, b);
     __syncthreads();
-    if (nw <= 8) {   // few: every thread adds them all, two a load (rows of 1024: 94 us, by shuffles 107)
+    if (nw <= 10) {   // few: every thread adds them all, two a load (rows of 1024: 94 us, by shuffles 107)
         const float4* all = reinterpret_cast<const float4*>(red);
         float2 s = nw & 1 ? red[nw - 1] : make_float2(0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < nw / 2) {
-                const float4 v = all[i];
-                s.x += v.x + v.z;
-                s.y += v.y + v.w;
-            }
+#pragma unroll 4
+        for (int i = 0; i < nw / 2; ++i) {
+            const float4 v = all[i];
+            s.x += v.x + v.z;
+            s.y += v.y + v.w;
+        }
         return s;
     }
     const float2 v = lane < nw ? red[lane] : make_float2(0.f, 0.f);
