@@ -177,8 +177,9 @@ __device__ __forceinline__ void put_tops(float (*tops)[kGroup], int warp, int tx
 }
 
 // Thread (tx, ty) has rows ty + 32 i and columns 8 tx + j.
-template <typename TI, bool VEC, int MODE>
+template <typename TI, bool VEC, int MODE, int kThreads = 512>
 __global__ void __launch_bounds__(kThreads, sizeof(TI) == 2 && MODE == kRow ? 3 : 2) quant8_kernel(const TI* __restrict__ x, const Tile p) {
+    constexpr int kLines = kThreads / 16, kPer = kGroup / kLines, kWarps = kThreads / 32;
     __shared__ __align__(16) float tops[kWarps][kGroup];
     __shared__ __align__(8) uint8_t bytes[kGroup];
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -400,8 +401,10 @@ template <typename TI, int MODE> cudaError_t go(const TI* x, Tile p, cudaStream_
     if (blocks >= (int64_t(1) << 31) || p.M >= (int64_t(1) << 31)) return kGridLimit;
     const bool v = p.N % 8 == 0 && vec_ok(x, p.sx, 16, es) && (!p.qr || vec_ok(p.qr, p.sq, 8, 1)) &&
                    (!p.qc || vec_ok(p.qc, p.sq, 8, 1));
-    return launch_kernel(v ? quant8_kernel<TI, true, MODE> : quant8_kernel<TI, false, MODE>, dim3((unsigned)blocks),
-                         dim3(kThreads), 0, st, early(blocks), x, p);
+    // blocks of 128 x 128 by 1024 threads, of which an SM holds as many tiles' loads at once as fit it
+    constexpr int T = MODE == kBlock ? 1024 : kThreads;
+    return launch_kernel(v ? quant8_kernel<TI, true, MODE, T> : quant8_kernel<TI, false, MODE, T>, dim3((unsigned)blocks),
+                         dim3(T), 0, st, early(blocks), x, p);
 }
 
 template <int MODE> cudaError_t go(bool bf16, const void* x, const Tile& p, cudaStream_t st) {
