@@ -8,6 +8,9 @@ decay per channel and state, gated) -> projection.  Both take padded prompts of
 different lengths and then go on token by token from the states that the prompt left;
 main() checks that this gives what the whole sequence gives, and takes a training step
 whose gradients are chained by hand through the operators' backward calls.
+
+SSDBlock is SSDLayer in a residual stream, as a model stacks it: the norm of the sum
+before it, and both projections in 8 bits, forward and backward.
 """
 import math
 import os
@@ -39,6 +42,16 @@ class SSDLayer:
         """z, the convolution's input and the raw step sizes: column slices of one product."""
         return (u @ self.w_in.t()).split([self.inner, self.conv_dim, self.h], -1)
 
+    def _project_back(self, dproj, k):
+        """Gradients of _project's input and weight."""
+        return dproj @ self.w_in, torch.einsum("btp,btw->pw", dproj.float(), k["u"].float())
+
+    def _output(self, v, keep=None):
+        return v @ self.w_out.t()
+
+    def _output_back(self, dout, k):
+        return (dout @ self.w_out).contiguous(), torch.einsum("btw,bti->wi", dout.float(), k["v"].float())
+
     def _steps(self, raw, lengths=None):
         dt = torch.nn.functional.softplus(raw.float() + self.dt_bias)
         if lengths is not None:      # a step of 0 leaves the state as it is, whatever the padding holds
@@ -59,7 +72,7 @@ class SSDLayer:
         v = m2.norm_fwd(y.flatten(2), self.w_norm, z)
         if keep is not None:
             keep.update(u=u, z=z, xbc=xbc, raw=raw, a=a, dt=dt, y=y, v=v)
-        return v @ self.w_out.t(), (window, state)
+        return self._output(v, keep), (window, state)
 
     def step(self, u, cache):
         """u [b,width], one token; the cache moves on in place."""
@@ -67,22 +80,74 @@ class SSDLayer:
         z, xbc, raw = self._project(u)
         x, B, C = self._heads(m2.conv_step(window, xbc, self.w_conv, self.b_conv))
         y = m2.ssd_decode(state, x.contiguous(), self._steps(raw), self.A, B.contiguous(), C.contiguous(), self.D)
-        return m2.norm_fwd(y.flatten(1)[:, None], self.w_norm, z[:, None])[:, 0] @ self.w_out.t()
+        return self._output(m2.norm_fwd(y.flatten(1)[:, None], self.w_norm, z[:, None])[:, 0])
 
     def backward(self, dout, k):
         """Gradients for dL/d(output) = dout, from what forward kept (no lengths)."""
-        io = dout.dtype
-        g = {"w_out": torch.einsum("btw,bti->wi", dout.float(), k["v"].float())}
-        n = m2.norm_bwd(k["y"].flatten(2), self.w_norm, k["z"], (dout @ self.w_out).contiguous())
+        io, g = dout.dtype, {}
+        dv, g["w_out"] = self._output_back(dout, k)
+        n = m2.norm_bwd(k["y"].flatten(2), self.w_norm, k["z"], dv)
         x, B, C = (t.contiguous() for t in self._heads(k["a"]))
         s = m2.ssd_bwd(x, k["dt"], self.A, B, C, self.D, None, n["dx"].view_as(x))
         da = torch.cat([s[name].flatten(2) for name in ("dx", "dB", "dC")], -1).to(io)
         c = m2.conv_bwd(k["xbc"], self.w_conv, self.b_conv, None, da)
         draw = s["ddt"] * torch.sigmoid(k["raw"].float() + self.dt_bias)
         dproj = torch.cat([n["dz"], c["dx"], draw.to(io)], -1)
-        g.update(w_norm=n["dw"], A=s["dA"], D=s["dD"], w_conv=c["dw"], b_conv=c["dbias"], dt_bias=draw.sum((0, 1)),
-                 w_in=torch.einsum("btp,btw->pw", dproj.float(), k["u"].float()))
-        return dproj @ self.w_in, g
+        du, g["w_in"] = self._project_back(dproj, k)
+        g.update(w_norm=n["dw"], A=s["dA"], D=s["dD"], w_conv=c["dw"], b_conv=c["dbias"], dt_bias=draw.sum((0, 1)))
+        return du, g
+
+
+class SSDBlock(SSDLayer):
+    """(x, residual) -> (layer(norm(x + residual)), x + residual), the residual in fp32.  The norm's
+    output, the gated norm's and the weights go to the products in 8 bits; quantise() follows every
+    change of the weights."""
+
+    def __init__(self, width, heads, **kw):
+        super().__init__(width, heads, **kw)
+        self.w_pre = torch.ones(width, device="cuda")
+        self.quantise()
+
+    def quantise(self):
+        self.q_in, self.q_out = m2.quant8(self.w_in, group="block"), m2.quant8(self.w_out, group="block")
+
+    def _project(self, u):
+        return m2.proj8_fwd(*u, *self.q_in).split([self.inner, self.conv_dim, self.h], -1)
+
+    def _project_back(self, dproj, k):
+        g = m2.proj8_bwd(dproj, *k["u"], *self.q_in)
+        return g["dx"], g["dw"]
+
+    def _output(self, v, keep=None):
+        v8 = m2.quant8(v)
+        if keep is not None:
+            keep["v8"] = v8
+        return m2.proj8_fwd(*v8, *self.q_out)
+
+    def _output_back(self, dout, k):
+        g = m2.proj8_bwd(dout, *k["v8"], *self.q_out)
+        return g["dx"], g["dw"]
+
+    def forward(self, x, residual=None, lengths=None, keep=None):
+        """x [b,T,width], residual [b,T,width] fp32 or None -> (output, residual, cache)."""
+        q, scales, total = m2.add_norm_fwd(x, residual, self.w_pre, quant=True, residual_f32=True)
+        out, cache = super().forward((q, scales), lengths, keep)
+        if keep is not None:
+            keep["total"] = total
+        return out, total, cache
+
+    def step(self, x, residual, cache):
+        """One token: x [b,width], residual [b,width] fp32 or None -> (output, residual)."""
+        q, scales, total = m2.add_norm_fwd(x, residual, self.w_pre, quant=True, residual_f32=True)
+        return super().step((q, scales), cache), total
+
+    def backward(self, dout, dtotal, k):
+        """Gradients of (x, residual), and of the weights, for dL/d(output) = dout and
+        dL/d(residual out) = dtotal."""
+        du, g = super().backward(dout, k)
+        n = m2.add_norm_bwd(k["total"], self.w_pre, du, dtotal)
+        g["w_pre"] = n["dw"]
+        return n["dx"], n["dresidual"], g
 
 
 class ScanLayer:
@@ -145,9 +210,55 @@ def generate(layer, u, prompt, lengths):
     return out, cache
 
 
+def stack(blocks, x, keep=None):
+    """Blocks one behind the other: (the sum at the end, their caches)."""
+    residual, caches = None, []
+    for i, block in enumerate(blocks):
+        x, residual, cache = block.forward(x, residual, keep=None if keep is None else keep[i])
+        caches.append(cache)
+    return x + residual, caches
+
+
+def stack_step(blocks, x, caches):
+    """One token of stack()."""
+    residual = None
+    for block, cache in zip(blocks, caches):
+        x, residual = block.step(x, residual, cache)
+    return x + residual
+
+
+def stack_back(blocks, dsum, keep):
+    """Gradients of stack()'s input and of every block's weights for dL/d(sum) = dsum (fp32)."""
+    dx, dresidual, grads = dsum.to(torch.bfloat16), dsum, []
+    for block, k in zip(reversed(blocks), reversed(keep)):
+        dx, dresidual, g = block.backward(dx, dresidual, k)
+        grads.insert(0, g)
+    return dx, grads
+
+
+def blocks_main():
+    blocks = [SSDBlock(256, heads=8) for _ in range(2)]
+    x = _randn(2, 160, 256, dtype=torch.bfloat16)
+    whole, _ = stack(blocks, x)
+    _, caches = stack(blocks, x[:, :150])
+    tokens = torch.stack([stack_step(blocks, x[:, t], caches) for t in range(150, 160)], 1)
+    far = ((tokens - whole[:, 150:]).norm() / whole[:, 150:].norm()).item()
+    keep = [{}, {}]
+    out, _ = stack(blocks, x, keep)
+    _, grads = stack_back(blocks, out, keep)             # of |out|^2 / 2
+    for block, g in zip(blocks, grads):
+        for name in ("w_in", "w_out"):
+            w = getattr(block, name)
+            w -= (1e-4 * g[name]).to(w.dtype)
+        block.quantise()
+    print(f"blocks in 8 bits: tokens differ from the whole sequence by {far:.1e}; gradients of the first: "
+          + ", ".join(f"{k} {v.norm().item():.3g}" for k, v in sorted(grads[0].items())))
+
+
 def main():
     torch.manual_seed(0)
     with torch.no_grad():
+        blocks_main()
         for name, layer in (("chunked scan", SSDLayer(256, heads=8)), ("selective scan", ScanLayer(256, 512))):
             u = _randn(3, 200, 256, dtype=torch.bfloat16)
             lengths = torch.tensor([190, 3, 77], dtype=torch.int32, device="cuda")
