@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "internal.h"
 #include "layer.cuh"
 
@@ -18,6 +20,18 @@ constexpr int kGroup = 128;   // values that share a scale
 // Large ones lose by it (the gradients of 32768 x 10576 x 2560 with every kernel early 1635 us, with
 // the products alone 1527).
 inline bool early(int64_t blocks) { return blocks <= 2 * (int64_t)sm_count(); }
+
+// Lets a kernel have `bytes` of dynamic shared memory; asked for once a device (`done`: devices
+// where it has been, a word of one kernel's own).
+template <typename K> cudaError_t allow_smem(K k, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    const bool known = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64;
+    const uint64_t bit = known ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // ---- quantisation -----------------------------------------------------------------
 // A group's scale is 2^e with the smallest e >= -127 for which its largest magnitude is at

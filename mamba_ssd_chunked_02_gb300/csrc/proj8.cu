@@ -147,7 +147,7 @@ struct Shape {
     int tr, tiles;         // tiles along the rows, in all
     int panel;             // tiles of a panel along the columns
     int chunk;             // contracted blocks summed in tensor memory before they are added to the result
-    bool copied;           // the result's rows start on 16 bytes
+    bool copied;           // the result's rows are whole 16 bytes, and start there
     int64_t ldo;
 };
 
@@ -438,7 +438,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     } else {
         // A warp has 32 lanes of tensor memory, the tile's rows, and moves them 32 columns at a time:
         // rounded, into shared memory, and by TMA to the result (coalesced stores where the result's
-        // rows do not start on 16 bytes).
+        // rows are not whole pieces of 16 bytes).
         const int quad = warp & 3, half = (warp - 4) >> 2;
         uint8_t* stage = sout + (warp - 4) * C::OUTS * C::OUT;
         int t = 0, n = 0;
@@ -810,11 +810,12 @@ cudaError_t go(const Operand& A, const Operand& B, int64_t R, int64_t Cn, int64_
     CUtensorMap ma, mb, mo;
     if (!map_of(&ma, A, R, depth, 128) || !map_of(&mb, B, Cn, depth, B_MN ? BK : C::HALF))
         return cudaErrorInvalidValue;
-    // the result by copies of 32 x 32, where its rows start on 16 bytes
+    // the result by copies of 32 x 32, where its rows start on 16 bytes and are whole ones (a copy out
+    // is clipped to 16 bytes, not to elements: it would write behind the row's end)
     const uint64_t dims[2] = {(uint64_t)Cn, (uint64_t)R};
-    const uint64_t strides[1] = {(uint64_t)((R == 1 ? (Cn + 15) / 16 * 16 : ldo) * sizeof(TO))};
+    const uint64_t strides[1] = {(uint64_t)((R == 1 ? Cn : ldo) * sizeof(TO))};
     const uint32_t box[2] = {32, 32};
-    const bool copied = reinterpret_cast<uintptr_t>(out) % 16 == 0 && strides[0] % 16 == 0 &&
+    const bool copied = reinterpret_cast<uintptr_t>(out) % 16 == 0 && strides[0] % 16 == 0 && Cn * sizeof(TO) % 16 == 0 &&
                         make_tmap(&mo, sizeof(TO) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, out,
                                   2, dims, strides, box,
                                   sizeof(TO) == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
@@ -826,7 +827,8 @@ cudaError_t go(const Operand& A, const Operand& B, int64_t R, int64_t Cn, int64_
     const Shape q{(int)R, (int)Cn, kb, (int)tr, (int)tiles, kPanel, sizeof(TO) == 4 ? kChunk : kb, copied, ldo};
     const Scales sa = scales_of(A, R, kb), sb = scales_of(B, Cn, kb);
     auto k = proj8_kernel<BN, A_MN, B_MN, TO>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    static std::atomic<uint64_t> done;
+    cudaError_t e = allow_smem(k, C::SMEM, done);
     if (e != cudaSuccess) return e;
     Launch l(kThreads, C::SMEM, kBlocks, st);
     l.early();
@@ -848,7 +850,8 @@ cudaError_t go_few(const Operand& A, const Operand& B, int64_t R, int64_t Cn, in
     FewShape q{(int)R, (int)Cn, (int)((depth + BK - 1) / BK), 0, ldo};
     auto k = proj8_few_kernel<BN, A_MN, TO>;
     constexpr int most = 226 * 1024;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    static std::atomic<uint64_t> done;
+    cudaError_t e = allow_smem(k, most, done);
     if (e != cudaSuccess) return e;
     // The most blocks a tile with which all run at once, an SM to each (w of 10576 x 2560, 83 tiles, one
     // token: 8.5 us with one block a tile, 8.9 with three, two to an SM; 2560 x 5120, 20 tiles: 9.0 with
