@@ -21,14 +21,15 @@ constexpr int kGroup = 128;   // values that share a scale
 // the products alone 1527).
 inline bool early(int64_t blocks) { return blocks <= 2 * (int64_t)sm_count(); }
 
-// Lets a kernel have `bytes` of dynamic shared memory; asked for once a device (`done`: devices
+// Lets a kernel have `bytes` of dynamic shared memory (and clusters of 16 blocks); asked for once a device (`done`: devices
 // where it has been, a word of one kernel's own).
-template <typename K> cudaError_t allow_smem(K k, int bytes, std::atomic<uint64_t>& done) {
+template <typename K> cudaError_t allow_smem(K k, int bytes, std::atomic<uint64_t>& done, bool wide_clusters = false) {
     int dev = 0;
     const bool known = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64;
     const uint64_t bit = known ? uint64_t(1) << dev : 0;
     if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && wide_clusters) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
     return e;
 }

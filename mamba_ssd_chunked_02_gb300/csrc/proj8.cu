@@ -35,6 +35,7 @@ constexpr int kThreads = 416;
 constexpr int kDevices = 64;
 constexpr int kPanel = 16;   // columns of tiles a panel (32768 x 2560 x 10576: 8 529 us, 16 511 us, all 48 513 us; 16384 x 8192 x 8192: 617, 606, 651)
 constexpr int BM = 128, BK = 128;
+constexpr int kMostPairs = 8;   // pairs that share a tile: 1, 2, 4 or 8
 
 // D[tmem] (+)= A B with block scales (kind::mxf8f6f4: one scale per 32 contracted values).
 // PAIR: two blocks' tensor cores on one tile, issued by the even one; every address holds for
@@ -63,7 +64,7 @@ template <bool PAIR> __device__ __forceinline__ void copy_scales(uint32_t tmem, 
     else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
 // Arrives at `bar` of this block, or of the pair's blocks in `mask`, when what was issued is done.
-template <bool PAIR> __device__ __forceinline__ void commit(uint64_t* bar, uint32_t mask = 3) {
+template <bool PAIR> __device__ __forceinline__ void commit(uint64_t* bar, uint32_t mask = 1) {
     if constexpr (PAIR)
         asm volatile(
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
@@ -149,6 +150,7 @@ struct Shape {
     int chunk;             // contracted blocks summed in tensor memory before they are added to the result
     bool copied;           // the result's rows are whole 16 bytes, and start there
     int64_t ldo;
+    int split, share;      // pairs of a tile, contracted blocks of each
 };
 
 // A pair's tile of 256 x BN: a block has 128 rows of A and BN / 2 columns of B.
@@ -207,7 +209,8 @@ __device__ __forceinline__ uint4 gather_scales(const Scales& s, bool words, cons
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int BN, bool A_MN, bool B_MN, typename TO>
+// SPLIT: a cluster of q.split pairs takes one tile, a share of the contracted blocks each.
+template <int BN, bool A_MN, bool B_MN, typename TO, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
              const __grid_constant__ CUtensorMap tm_o, const Scales sa, const Scales sb, TO* __restrict__ out, const Shape q,
@@ -221,9 +224,11 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     __shared__ Bars bars;
     volatile int* abort = &bars.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // the even block (rank 0) counts the copies and issues the products of both
-    const int rank = (int)block_rank();
-    const int first = blockIdx.x / 2, step = gridDim.x / 2;
+    // the even block (rank 0 of the pair) counts the copies and issues the products of both
+    const int in_cluster = (int)block_rank(), rank = SPLIT ? in_cluster & 1 : in_cluster, even = in_cluster - rank;
+    const uint32_t both = 3u << even;
+    const int first = blockIdx.x / (SPLIT ? 2 * q.split : 2), step = SPLIT ? q.tiles : gridDim.x / 2;
+    const int from_k = SPLIT ? (even >> 1) * q.share : 0, to_k = SPLIT ? min(q.kb, from_k + q.share) : q.kb;
     constexpr int kRows = 2 * BM;
     // Tiles go down panels of q.panel columns of tiles, a row of the panel at a time: the clusters that
     // run side by side then share few rows of A and of B.
@@ -261,6 +266,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     tc_fence_after();
     const uint32_t tmem = bars.tmem;
     grid_dep_wait();   // what is read was written by the kernel before
+    [[maybe_unused]] float sum[SPLIT ? 64 : 1] = {};   // of a row, 64 columns: a warp's of the pair's share
     // The producing and the issuing warp run whole, with one lane elected for each instruction: what
     // the loop counts then stays in uniform registers, where the copies and products take it from
     // (issued from a loop of one lane, four products took 650 cycles instead of 450).
@@ -272,12 +278,12 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         int it = 0, st = 0;
         uint32_t phase = 1;
         bool ok = true;
-        const uint32_t full0 = of_block(&bars.full[0], 0);
+        const uint32_t full0 = of_block(&bars.full[0], even);
         for (int tile = first; tile < q.tiles && ok; tile += step) {
             int r, c;
             place(tile, &r, &c);
             const int r0 = row_of(r), c0 = c * BN + rank * C::HALF;
-            for (int kb = 0; kb < q.kb; ++kb, ++it) {
+            for (int kb = from_k; kb < to_k; ++kb, ++it) {
                 ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.empty[st], phase, abort, kWaitNs));
                 if (!ok) break;
                 if (elected()) {
@@ -313,8 +319,8 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             uint32_t phase = 0, sf_phase = 0;
             bool ok = true;
             for (int tile = first; tile < q.tiles && ok; tile += step)
-                for (int k0 = 0; k0 < q.kb && ok; k0 += q.chunk, ++t) {
-                    const int acc = t & 1, k1 = min(q.kb, k0 + q.chunk);
+                for (int k0 = from_k; k0 < to_k && ok; k0 += q.chunk, ++t) {
+                    const int acc = t & 1, k1 = min(to_k, k0 + q.chunk);
                     ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.acc_empty[acc], (t / 2 & 1) ^ 1, abort, kWaitNs));
                     if (C::SHARED && ok && t > 0)
                         ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.acc_shared, (t - 1) & 1, abort, kWaitNs));
@@ -351,9 +357,9 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                                 for (int k = 0; k < 4; ++k)
                                     mma_scaled<PAIR>(d, a0 + at + k * a_step, b0 + at + k * b_step, idesc | i << 4 | i << 29, ta,
                                                      ta + 4, kb > k0 || i > 0 || k > 0);
-                                commit<PAIR>(&bars.empty[now]);
-                                if (i == 3 || last) commit<PAIR>(&bars.sf_empty[sf]);
-                                if (last) commit<PAIR>(&bars.acc_full[acc]);
+                                commit<PAIR>(&bars.empty[now], both);
+                                if (i == 3 || last) commit<PAIR>(&bars.sf_empty[sf], both);
+                                if (last) commit<PAIR>(&bars.acc_full[acc], both);
                             }
                             there = __all_sync(0xffffffffu, there);
                         }
@@ -361,7 +367,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                     }
                 }
             if (!ok && elected()) {
-                commit<PAIR>(&bars.drain, 1);
+                commit<PAIR>(&bars.drain, 1u << even);
                 mbar_wait(&bars.drain, 0, kWaitNs);
             }
         }
@@ -374,7 +380,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         const int parts = warp == 2 ? 1 : C::SFB;
         const uint8_t* at[4 * C::SFB];   // scales of rows lane + 32 j of the tile
         uint4 next[kFly][C::SFB];
-        int tile = first, kb = 0;
+        int tile = first, kb = from_k;
         const auto begin = [&] {
             int r, c;
             place(tile, &r, &c);
@@ -388,13 +394,13 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
 #pragma unroll
             for (int h = 0; h < C::SFB; ++h)
                 if (h < parts) to[h] = gather_scales(s, s.words, at + 4 * h, kb, q.kb);
-            if ((kb += 4) >= q.kb) {
-                kb = 0;
+            if ((kb += 4) >= to_k) {
+                kb = from_k;
                 if ((tile += step) < q.tiles) begin();
             }
         };
         int left = first < q.tiles ? (q.tiles - 1 - first) / step + 1 : 0;
-        left *= (q.kb + 3) / 4;
+        left *= (to_k - from_k + 3) / 4;
         int sf = 0;
         uint32_t phase = 1;
         if (left) begin();
@@ -425,8 +431,8 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         // Scales in shared memory to the tensor cores' proxy.  A warp of its own, as the fence waits for
         // all that its warp has in flight: behind the loads of later sets it took 2000 cycles.
         if (lane == 0) {
-            const uint32_t full0 = of_block(&bars.sf_full[0], 0);
-            int left = first < q.tiles ? ((q.tiles - 1 - first) / step + 1) * ((q.kb + 3) / 4) : 0;
+            const uint32_t full0 = of_block(&bars.sf_full[0], even);
+            int left = first < q.tiles ? ((q.tiles - 1 - first) / step + 1) * ((to_k - from_k + 3) / 4) : 0;
             int sf = 0;
             for (uint32_t phase = 0; left > 0; --left) {
                 if (!mbar_wait_or_abort(&bars.sf_there[sf], phase, abort, kWaitNs)) break;
@@ -434,6 +440,26 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 arrive_at(full0 + 8 * sf);
                 if (++sf == C::NSF) sf = 0, phase ^= 1;
             }
+        }
+    } else if constexpr (SPLIT) {
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        bool ok = true;
+        int t = 0;
+        for (int k0 = from_k; k0 < to_k; k0 += q.chunk, ++t) {
+            const int acc = t & 1;
+            ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.acc_full[acc], t / 2 & 1, abort, kWaitNs));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint32_t v[32];
+                tmem_ld32_sync(tmem + acc * C::ACC + lanes + 64 * ((warp - 4) >> 2) + 32 * u, v);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) sum[32 * u + j] += __uint_as_float(v[j]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_at(of_block(&bars.acc_empty[acc], even));
         }
     } else {
         // A warp has 32 lanes of tensor memory, the tile's rows, and moves them 32 columns at a time:
@@ -467,7 +493,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                     if (C::SHARED && i == half && half != acc) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) arrive_at(of_block(&bars.acc_shared, 0));
+                        if (lane == 0) arrive_at(of_block(&bars.acc_shared, even));
                     }
                     if (r0 >= q.R || c0 + c >= q.C) continue;
                     uint8_t* part = stage + n * C::OUT;
@@ -505,14 +531,15 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                                 constexpr int E = 16 / sizeof(TO);
                                 const int piece = (lane / E) ^ (sizeof(TO) == 2 ? r >> 1 & 3 : r & 7);
                                 const TO w = reinterpret_cast<const TO*>(part)[r * 32 + piece * E + lane % E];
-                                *o = k0 == 0 ? w : from_f32<TO>(to_f32(w) + to_f32(*o));
+                                if (sizeof(TO) == 2 || k0 == 0) *o = w;
+                                else atomicAdd(reinterpret_cast<float*>(o), to_f32(w));   // this thread's alone: no load waited for
                             }
                         __syncwarp();
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_at(of_block(&bars.acc_empty[acc], 0));
+                if (lane == 0) arrive_at(of_block(&bars.acc_empty[acc], even));
             }
         }
         __syncwarp();
@@ -521,6 +548,60 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     __syncwarp();
     tc_fence_before();
     cluster_sync();
+    if constexpr (SPLIT) {
+        // Every pair is done with its operands, whose room takes the shares' sums: a block owns BN / split
+        // of its 128 rows' columns, gets them from the blocks of its half of the rows, and adds them in the
+        // order of the pairs.  In fours of a row's columns, a column of fours 129 rows apart from the next:
+        // lanes are rows when they are sent, fours of a row when they are read.
+        static_assert(BN == 128 && C::NS * C::STAGE >= BN / 4 * 129 * 16, "room for the sums");
+        constexpr int P = BM + 1;
+        const int own = BN / q.split, fours = own / 4, tid = threadIdx.x - 128;   // powers of two
+        float4* join = reinterpret_cast<float4*>(smem);   // [pair][four][row]
+        if (warp >= 4 && warp < 12) {
+            const int row = (warp & 3) * 32 + lane, c0 = 64 * ((warp - 4) >> 2);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {   // sixteen columns have one owner
+                const int c = c0 + 16 * g;
+                uint32_t to = of_block(join + ((even >> 1) * fours + (c & (own - 1)) / 4) * P + row, 2 * (c / own) + rank);
+#pragma unroll
+                for (int j = 0; j < 16; j += 4, to += P * 16)
+                    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(sum[16 * g + j]),
+                                 "f"(sum[16 * g + j + 1]), "f"(sum[16 * g + j + 2]), "f"(sum[16 * g + j + 3])
+                                 : "memory");
+            }
+        }
+        cluster_sync();
+        if (warp >= 4 && warp < 12 && !*abort) {
+            int rt, ct;
+            place(first, &rt, &ct);
+            const int four = tid & (fours - 1), r0 = row_of(rt), c0 = ct * BN + (even >> 1) * own + 4 * four;
+            const int rows = min(BM, q.R - r0), cols = q.C - c0;
+            if (cols > 0)
+#pragma unroll 2
+                for (int row = tid / fours; row < rows; row += 256 / fours) {
+                    const float4* at = join + four * P + row;
+                    float4 v = at[0];
+#pragma unroll
+                    for (int s = 1; s < kMostPairs; ++s)
+                        if (s < q.split) {
+                            const float4 w = at[s * fours * P];
+                            v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+                        }
+                    TO* o = out + (int64_t)(r0 + row) * q.ldo + c0;
+                    if (q.copied) {   // whole pieces of 16 bytes
+                        if constexpr (sizeof(TO) == 2)
+                            *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+                        else
+                            *reinterpret_cast<float4*>(o) = v;
+                    } else {
+                        o[0] = from_f32<TO>(v.x);
+                        if (cols > 1) o[1] = from_f32<TO>(v.y);
+                        if (cols > 2) o[2] = from_f32<TO>(v.z);
+                        if (cols > 3) o[3] = from_f32<TO>(v.w);
+                    }
+                }
+        }
+    }
     if (threadIdx.x == 0 && *abort) record_error(err, kErrTimeoutProj8);
     if (warp == 1) {
         tc_fence_after();
@@ -803,9 +884,23 @@ Scales scales_of(const Operand& o, int64_t rows, int kb) {
 // result's norm, 1024 by 3.5e-6 where sums in fp32 registers are off by 5e-7.
 constexpr int kChunk = 32;
 
-template <int BN, bool A_MN, bool B_MN, typename TO>
+// Contracted blocks of a pair, where a tile's are split: whole words of scales each.
+int share_of(int kb, int split) { return split == 1 ? kb : ((kb + split - 1) / split + 3) / 4 * 4; }
+
+// Clusters of `split` pairs with a tile of 128 columns each that the device holds at once.
+template <bool A_MN, bool B_MN, typename TO> int split_clusters(int split) {
+    using C = Cfg<128, B_MN, sizeof(TO)>;
+    auto k = proj8_kernel<128, A_MN, B_MN, TO, true>;
+    static std::atomic<uint64_t> done;
+    static std::atomic<int> known[kMostPairs + 1][kDevices];
+    if (allow_smem(k, C::SMEM, done, true) != cudaSuccess) return 0;
+    const Launch l(kThreads, C::SMEM, 2 * split, nullptr);
+    return resident_clusters(k, l.cfg, 2 * split, known[split]);
+}
+
+template <int BN, bool A_MN, bool B_MN, typename TO, bool SPLIT = false>
 cudaError_t go(const Operand& A, const Operand& B, int64_t R, int64_t Cn, int64_t depth, TO* out, int64_t ldo,
-               cudaStream_t st) {
+               cudaStream_t st, int split = 1) {
     using C = Cfg<BN, B_MN, sizeof(TO)>;
     CUtensorMap ma, mb, mo;
     if (!map_of(&ma, A, R, depth, 128) || !map_of(&mb, B, Cn, depth, B_MN ? BK : C::HALF))
@@ -820,21 +915,22 @@ cudaError_t go(const Operand& A, const Operand& B, int64_t R, int64_t Cn, int64_
                                   2, dims, strides, box,
                                   sizeof(TO) == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
     if (!copied) mo = ma;   // not used
-    constexpr int kRows = 2 * BM, kBlocks = 2;
+    constexpr int kRows = 2 * BM;
     const int64_t tr = (R + kRows - 1) / kRows, tiles = tr * ((Cn + BN - 1) / BN);
     if (tiles >= (int64_t(1) << 30)) return kGridLimit;
     const int kb = (int)((depth + BK - 1) / BK);
-    const Shape q{(int)R, (int)Cn, kb, (int)tr, (int)tiles, kPanel, sizeof(TO) == 4 ? kChunk : kb, copied, ldo};
+    if ((int64_t)(split - 1) * share_of(kb, split) >= kb) return cudaErrorInvalidValue;   // a pair without blocks
+    const Shape q{(int)R, (int)Cn, kb, (int)tr, (int)tiles, kPanel, sizeof(TO) == 4 ? kChunk : kb, copied, ldo, split, share_of(kb, split)};
     const Scales sa = scales_of(A, R, kb), sb = scales_of(B, Cn, kb);
-    auto k = proj8_kernel<BN, A_MN, B_MN, TO>;
+    auto k = proj8_kernel<BN, A_MN, B_MN, TO, SPLIT>;
     static std::atomic<uint64_t> done;
-    cudaError_t e = allow_smem(k, C::SMEM, done);
+    cudaError_t e = allow_smem(k, C::SMEM, done, SPLIT);
     if (e != cudaSuccess) return e;
-    Launch l(kThreads, C::SMEM, kBlocks, st);
+    Launch l(kThreads, C::SMEM, 2 * split, st);
     l.early();
     static std::atomic<int> known[kDevices];
-    const int64_t most = resident_clusters(k, l.cfg, kBlocks, known);
-    l.cfg.gridDim = dim3((unsigned)(kBlocks * (tiles < most ? tiles : most)));
+    const int64_t most = SPLIT ? tiles : resident_clusters(k, l.cfg, 2, known);
+    l.cfg.gridDim = dim3((unsigned)(2 * split * (tiles < most ? tiles : most)));
     return cudaLaunchKernelEx(&l.cfg, k, ma, mb, mo, sa, sb, out, q, device_error_word());
 }
 
@@ -893,6 +989,19 @@ cudaError_t pick(const Operand& A, const Operand& B, int64_t R, int64_t C, int64
     const auto cycles = [&](int64_t bn, int64_t block, int64_t ends) {
         return (tr * ((C + bn - 1) / bn) + pairs - 1) / pairs * (kb * block + ends);
     };
+    // Few tiles: the pairs to each with which a block's share and the join take least, of those that run side
+    // by side (256 x 8192 x 256: 18.0 us with one pair a tile, 13.2 with two, 9.9 with four, 10.0 with eight;
+    // 256 x 2048 x 256: 7.8, 7.7, 7.5; gradients of 30490 x 192 x 80: 126 us, now 45).  A single pair's
+    // blocks wait for memory longer where both operands are MN-major.
+    const int64_t t128 = tr * ((C + 127) / 128), block = B_MN ? 800 : 380;
+    int split = 1;
+    int64_t least = kb * block;
+    for (int n = 2; n <= kMostPairs; n *= 2) {
+        const int64_t share = share_of((int)kb, n), take = share * block + (n < 8 ? 3000 : 6000);
+        if (t128 * n > pairs || (n - 1) * share >= kb) break;
+        if (take < least && t128 <= split_clusters<A_MN, B_MN, TO>(n)) split = n, least = take;
+    }
+    if (split > 1) return go<128, A_MN, B_MN, TO, true>(A, B, R, C, depth, out, ldo, st, split);
     if (cycles(128, 330, 3000) < cycles(kWide, 2 * kWide + 40, 4000))
         return go<128, A_MN, B_MN, TO>(A, B, R, C, depth, out, ldo, st);
     return go<kWide, A_MN, B_MN, TO>(A, B, R, C, depth, out, ldo, st);

@@ -40,6 +40,29 @@ def test_long_sums(M, K, N):
     product(g["dw"], R.dequant(*R.quant(d, 128, 1), 128, 1).t(), R.dequant(*R.quant(x, 128, 1), 128, 1), "dw")
 
 
+@pytest.mark.parametrize("M,K,N", [(150, 2560, 130), (300, 4200, 260), (129, 11000, 60), (257, 5113, 77)])
+def test_sums_split_between_blocks(M, K, N):
+    """Few tiles with long sums: two, four or eight pairs of blocks a tile, shares of unequal length;
+    operands with the contracted index inside (y), outside (dw) and one of each (dx)."""
+    ops, x, w = _operands(M, K, N, 30)
+    for dt in (F32, BF16):
+        y = m2.proj8_fwd(*ops, dtype=dt)
+        product(y, x, w.t(), "y")
+        assert torch.equal(y, m2.proj8_fwd(*ops, dtype=dt))
+    # the same sizes in turn: K tokens, K outputs
+    ops, x, w = _operands(K, M, N, 31)
+    dy = Gen(32).randn(K, N)
+    got = [m2.proj8_bwd(dy.cuda(), *ops, need_dx=False)["dw"] for _ in range(2)]
+    product(got[0], R.dequant(*R.quant(f64(dy), 128, 1), 128, 1).t(), R.dequant(*R.quant(x, 128, 1), 128, 1), "dw")
+    assert torch.equal(got[0], got[1])
+    ops, x, w = _operands(M, N, K, 33)
+    for dt in (F32, BF16):
+        dy = Gen(34).randn(M, K, dtype=dt)
+        dx = m2.proj8_bwd(dy.cuda(), *ops, need_dw=False)["dx"]
+        product(dx, R.dequant(*R.quant(f64(dy), 1, 128), 1, 128), w, "dx")
+    assert m2.device_error() == 0
+
+
 def test_long_sums_of_gradients():
     """dw over 20000 tokens, dx over 9000 outputs: several accumulators a result."""
     M, K, N = 20000, 140, 130
