@@ -108,6 +108,11 @@ __device__ __forceinline__ uint32_t of_block(const void* p, uint32_t rank) {
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// The same where nothing written is handed over (tensor memory has been read): the release above waits
+// for the thread's stores, copies out among them, some 2000 cycles.
+__device__ __forceinline__ void arrive_read_at(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 // A tile into this block's shared memory, its bytes counted at a barrier of the pair's even block.
 __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* m, uint32_t bar, int x, int y) {
     asm volatile(
@@ -166,8 +171,9 @@ template <int BN, bool B_MN, int ES> struct Cfg {
     static constexpr int NSF = SHARED ? 2 : 4;
     static constexpr int SFB = (BN + 127) / 128;                 // scale tiles of B
     static constexpr int SF_BYTES = 512 * (1 + SFB);
-    // parts of 32 x 32 on their way out, of each of the epilogue's 8 warps
-    static constexpr int OUT = 32 * 32 * ES, OUTS = ES == 2 ? 2 : 1, OUT_BYTES = 8 * OUTS * OUT;
+    // a part on its way out, of each of the epilogue's 8 warps: 32 rows of 128 bytes
+    static constexpr int PART = 128 / ES, OUT = 32 * 128, OUT_BYTES = 8 * OUT;
+    static constexpr int SPAN = (BN / 2 + 63) / 64 * 64;         // columns of the epilogue's first four warps
     static constexpr int FIXED = 1024 + NSF * SF_BYTES + OUT_BYTES;
     static constexpr int NS = (227 * 1024 - FIXED - 512) / STAGE < 6 ? (227 * 1024 - FIXED - 512) / STAGE : 6;
     static constexpr int SMEM = FIXED + NS * STAGE;
@@ -213,7 +219,8 @@ __device__ __forceinline__ uint4 gather_scales(const Scales& s, bool words, cons
 template <int BN, bool A_MN, bool B_MN, typename TO, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-             const __grid_constant__ CUtensorMap tm_o, const Scales sa, const Scales sb, TO* __restrict__ out, const Shape q,
+             const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_half, const Scales sa,
+             const Scales sb, TO* __restrict__ out, const Shape q,
              int32_t* err) {
     using C = Cfg<BN, B_MN, sizeof(TO)>;
     constexpr bool PAIR = true;
@@ -459,15 +466,17 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_at(of_block(&bars.acc_empty[acc], even));
+            if (lane == 0) arrive_read_at(of_block(&bars.acc_empty[acc], even));
         }
     } else {
-        // A warp has 32 lanes of tensor memory, the tile's rows, and moves them 32 columns at a time:
-        // rounded, into shared memory, and by TMA to the result (coalesced stores where the result's
-        // rows are not whole pieces of 16 bytes).
+        // A warp has 32 lanes of tensor memory, the tile's rows, and moves lines of 128 bytes of half the
+        // columns: rounded, into shared memory, and by TMA to the result (coalesced stores where the result's
+        // rows are not whole pieces of 16 bytes).  The copies take 6 to 8 cycles a row, of 64 bytes or of 128
+        // (13764 x 69 x 5967 bf16, the result's bytes alone: 58 us by lines of 64, see DESIGN).
         const int quad = warp & 3, half = (warp - 4) >> 2;
-        uint8_t* stage = sout + (warp - 4) * C::OUTS * C::OUT;
-        int t = 0, n = 0;
+        const int begin = half * C::SPAN, end = half ? BN : C::SPAN;
+        uint8_t* part = sout + (warp - 4) * C::OUT;
+        int t = 0;
         bool ok = true;
         for (int tile = first; tile < q.tiles && ok; tile += step) {
             int rt, ct;
@@ -483,63 +492,74 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                     if (elected()) bulk_wait<0>();
                     __syncwarp();
                 }
+                // the columns that the next tile's accumulator shares come first: the last 32 of the even
+                // accumulator, the first of the odd one
+                const bool back = C::SHARED && acc == 0 && half == 1;
 #pragma unroll 1
-                for (int i = half; i < BN / 32; i += 2) {
-                    // the columns that the next tile's accumulator shares come first: the last 32 of the
-                    // even accumulator, the first of the odd one
-                    const int c = 32 * (C::SHARED && acc == 0 && half == 1 ? (i + 6) % 8 : i);
-                    uint32_t v[32];
-                    tmem_ld32_sync(from + c, v);
-                    if (C::SHARED && i == half && half != acc) {
+                for (int at = begin; at < end; at += C::PART) {
+                    const int c = back ? begin + end - C::PART - at : at;
+                    const bool wide = C::PART == 64 && c + 64 <= end;
+                    uint32_t v[C::PART / 32][32];
+                    tmem_ld32(from + c, v[0]);
+                    if (C::PART == 64 && wide) tmem_ld32(from + c + 32, v[C::PART / 32 - 1]);
+#pragma unroll
+                    for (int h = 0; h < C::PART / 32; ++h) tmem_wait_ld_regs(v[h]);
+                    if (C::SHARED && at == begin && half != acc) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) arrive_at(of_block(&bars.acc_shared, even));
+                        if (lane == 0) arrive_read_at(of_block(&bars.acc_shared, even));
                     }
                     if (r0 >= q.R || c0 + c >= q.C) continue;
-                    uint8_t* part = stage + n * C::OUT;
-                    if (C::OUTS == 2) n ^= 1;
-                    if (elected()) bulk_wait_read<C::OUTS - 1>();   // the last copy from this part has read it
+                    if (elected()) bulk_wait_read<0>();   // the last copy has read the part
                     __syncwarp();
-                    uint4* row = reinterpret_cast<uint4*>(part + lane * 32 * sizeof(TO));
                     // 16-byte pieces in the places where a swizzled copy looks for them
+                    const int line = sizeof(TO) == 2 && !wide ? 64 : 128;
+                    uint4* row = reinterpret_cast<uint4*>(part + lane * line);
+                    const int turn = line == 64 ? lane >> 1 & 3 : lane & 7;
 #pragma unroll
-                    for (int p = 0; p < (int)sizeof(TO) * 2; ++p) {
-                        if constexpr (sizeof(TO) == 2)
-                            row[p ^ (lane >> 1 & 3)] =
-                                make_uint4(pack_bf16x2(__uint_as_float(v[8 * p]), __uint_as_float(v[8 * p + 1])),
-                                           pack_bf16x2(__uint_as_float(v[8 * p + 2]), __uint_as_float(v[8 * p + 3])),
-                                           pack_bf16x2(__uint_as_float(v[8 * p + 4]), __uint_as_float(v[8 * p + 5])),
-                                           pack_bf16x2(__uint_as_float(v[8 * p + 6]), __uint_as_float(v[8 * p + 7])));
-                        else
-                            row[p ^ (lane & 7)] = make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
+                    for (int p = 0; p < 8; ++p) {
+                        if constexpr (sizeof(TO) == 2) {
+                            if (p >= 4 && !wide) break;
+                            const uint32_t* f = v[p / 4] + 8 * (p & 3);
+                            row[p ^ turn] = make_uint4(pack_bf16x2(__uint_as_float(f[0]), __uint_as_float(f[1])),
+                                                       pack_bf16x2(__uint_as_float(f[2]), __uint_as_float(f[3])),
+                                                       pack_bf16x2(__uint_as_float(f[4]), __uint_as_float(f[5])),
+                                                       pack_bf16x2(__uint_as_float(f[6]), __uint_as_float(f[7])));
+                        } else {
+                            row[p ^ turn] = make_uint4(v[0][4 * p], v[0][4 * p + 1], v[0][4 * p + 2], v[0][4 * p + 3]);
+                        }
                     }
                     if (q.copied) {
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (elected()) {
-                            if (k0 == 0) tma_store_2d(&tm_o, part, c0 + c, r0);
-                            else tma_reduce_add_2d(&tm_o, part, c0 + c, r0);
+                            if (k0 > 0) tma_reduce_add_2d(&tm_o, part, c0 + c, r0);
+                            else tma_store_2d(C::PART == 64 && !wide ? &tm_half : &tm_o, part, c0 + c, r0);
                             bulk_commit();
                         }
                     } else {
                         __syncwarp();
                         const int rows = min(32, q.R - r0);
-                        TO* o = out + (int64_t)r0 * q.ldo + c0 + c + lane;
-                        if (c0 + c + lane < q.C)
+                        constexpr int E = 16 / sizeof(TO);
+#pragma unroll
+                        for (int h = 0; h < C::PART / 32; ++h) {
+                            const int col = 32 * h + lane;
+                            if (c0 + c + col >= q.C || col >= end - c) break;
+                            TO* o = out + (int64_t)r0 * q.ldo + c0 + c + col;
 #pragma unroll 8
                             for (int r = 0; r < rows; ++r, o += q.ldo) {
-                                constexpr int E = 16 / sizeof(TO);
-                                const int piece = (lane / E) ^ (sizeof(TO) == 2 ? r >> 1 & 3 : r & 7);
-                                const TO w = reinterpret_cast<const TO*>(part)[r * 32 + piece * E + lane % E];
+                                const int piece = col / E ^ (line == 64 ? r >> 1 & 3 : r & 7);
+                                const TO w = reinterpret_cast<const TO*>(part + r * line)[piece * E + col % E];
                                 if (sizeof(TO) == 2 || k0 == 0) *o = w;
                                 else atomicAdd(reinterpret_cast<float*>(o), to_f32(w));   // this thread's alone: no load waited for
                             }
+                        }
                         __syncwarp();
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_at(of_block(&bars.acc_empty[acc], even));
+                if (lane == 0) arrive_read_at(of_block(&bars.acc_empty[acc], even));
             }
         }
         __syncwarp();
@@ -902,19 +922,20 @@ template <int BN, bool A_MN, bool B_MN, typename TO, bool SPLIT = false>
 cudaError_t go(const Operand& A, const Operand& B, int64_t R, int64_t Cn, int64_t depth, TO* out, int64_t ldo,
                cudaStream_t st, int split = 1) {
     using C = Cfg<BN, B_MN, sizeof(TO)>;
-    CUtensorMap ma, mb, mo;
+    CUtensorMap ma, mb, mo, mh;
     if (!map_of(&ma, A, R, depth, 128) || !map_of(&mb, B, Cn, depth, B_MN ? BK : C::HALF))
         return cudaErrorInvalidValue;
-    // the result by copies of 32 x 32, where its rows start on 16 bytes and are whole ones (a copy out
+    // the result by copies of 32 lines, where its rows start on 16 bytes and are whole ones (a copy out
     // is clipped to 16 bytes, not to elements: it would write behind the row's end)
     const uint64_t dims[2] = {(uint64_t)Cn, (uint64_t)R};
     const uint64_t strides[1] = {(uint64_t)((R == 1 ? Cn : ldo) * sizeof(TO))};
-    const uint32_t box[2] = {32, 32};
+    const uint32_t box[2] = {C::PART, 32}, half[2] = {32, 32};
+    const CUtensorMapDataType type = sizeof(TO) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
     const bool copied = reinterpret_cast<uintptr_t>(out) % 16 == 0 && strides[0] % 16 == 0 && Cn * sizeof(TO) % 16 == 0 &&
-                        make_tmap(&mo, sizeof(TO) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, out,
-                                  2, dims, strides, box,
-                                  sizeof(TO) == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+                        make_tmap(&mo, type, out, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) &&
+                        (C::PART == 32 || make_tmap(&mh, type, out, 2, dims, strides, half, CU_TENSOR_MAP_SWIZZLE_64B));
     if (!copied) mo = ma;   // not used
+    if (!copied || C::PART == 32) mh = ma;
     constexpr int kRows = 2 * BM;
     const int64_t tr = (R + kRows - 1) / kRows, tiles = tr * ((Cn + BN - 1) / BN);
     if (tiles >= (int64_t(1) << 30)) return kGridLimit;
@@ -931,7 +952,7 @@ cudaError_t go(const Operand& A, const Operand& B, int64_t R, int64_t Cn, int64_
     static std::atomic<int> known[kDevices];
     const int64_t most = SPLIT ? tiles : resident_clusters(k, l.cfg, 2, known);
     l.cfg.gridDim = dim3((unsigned)(2 * split * (tiles < most ? tiles : most)));
-    return cudaLaunchKernelEx(&l.cfg, k, ma, mb, mo, sa, sb, out, q, device_error_word());
+    return cudaLaunchKernelEx(&l.cfg, k, ma, mb, mo, mh, sa, sb, out, q, device_error_word());
 }
 
 // A's rows to the lanes, B's few to the columns: out[j * ldo + i].
