@@ -77,6 +77,21 @@ template <> struct Eight<__nv_bfloat16> {
             w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
         } else {
             const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
+            if (count >= 8) {   // the widest accesses that the row's start allows (the same for all its lanes)
+                const uint32_t at = (uint32_t)reinterpret_cast<uintptr_t>(p);
+                if (at % 16 == 0) return load<true>(p, count);
+                if (at % 4 == 0) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] = __ldg(reinterpret_cast<const uint32_t*>(p) + j);
+                } else {   // a half, three words, a half
+                    uint32_t v[5] = {(uint32_t)__ldg(u) << 16, 0, 0, 0, (uint32_t)__ldg(u + 7)};
+#pragma unroll
+                    for (int j = 0; j < 3; ++j) v[j + 1] = __ldg(reinterpret_cast<const uint32_t*>(u + 1) + j);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] = __funnelshift_l(v[j], v[j + 1], 16);
+                }
+                return;
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 w[j] = (2 * j < count ? __ldg(u + 2 * j) : 0) | (uint32_t)(2 * j + 1 < count ? __ldg(u + 2 * j + 1) : 0) << 16;
@@ -122,6 +137,7 @@ template <> struct Eight<float> {
             const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p + 4));
             f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
         } else {
+            if (count >= 8 && reinterpret_cast<uintptr_t>(p) % 16 == 0) return load<true>(p, count);
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] = j < count ? __ldg(p + j) : 0.f;
         }
@@ -328,12 +344,10 @@ template <bool VEC> __global__ void __launch_bounds__(kThreads, 2) quant8_turn_k
         lift[i] = 0.f, rest[i] = 1.f;
         if (ty + kLines * i >= rows) continue;
         const uint8_t* f = x + from + i * (kLines * p.sx.t);
-        if constexpr (VEC) {
-            if (count > 0) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2*>(f));
-                w[i][0] = v.x, w[i][1] = v.y;
-            }
-        } else {
+        if (VEC ? count > 0 : count >= 8) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(f));
+            w[i][0] = v.x, w[i][1] = v.y;
+        } else if (!VEC) {   // the row's end
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (j < count) w[i][j / 4] |= (uint32_t)__ldg(f + j) << (8 * (j & 3));
@@ -425,14 +439,14 @@ cudaError_t launch_quant8_both(bool bf16, int64_t M, int64_t N, const void* x, i
     return !qc ? go<kRow>(bf16, x, p, st) : !qr ? go<kCol>(bf16, x, p, st) : go<kRow | kCol>(bf16, x, p, st);
 }
 
+// Rows of q and qc start on 16 bytes.
 cudaError_t launch_quant8_turn(int64_t M, int64_t N, const uint8_t* q, int64_t px, const uint8_t* s, uint8_t* qc,
                                uint8_t* sc, int64_t pq, cudaStream_t st) {
     Tile p{M, N, (uint32_t)M, 0, Tok{0, px}, Tok{0, pq}, s, nullptr, nullptr, qc, sc, 0, false};
     if (M == 0 || N == 0) return cudaSuccess;
     const int64_t blocks = blocks_of(p);
     if (blocks >= (int64_t(1) << 31) || M >= (int64_t(1) << 31)) return kGridLimit;
-    const bool v = N % 8 == 0 && vec_ok(q, p.sx, 8, 1) && vec_ok(qc, p.sq, 8, 1);
-    return launch_kernel(v ? quant8_turn_kernel<true> : quant8_turn_kernel<false>, dim3((unsigned)blocks), dim3(kThreads), 0,
+    return launch_kernel(N % 8 == 0 ? quant8_turn_kernel<true> : quant8_turn_kernel<false>, dim3((unsigned)blocks), dim3(kThreads), 0,
                          st, early(blocks), q, p);
 }
 
