@@ -164,13 +164,21 @@ struct Quant8Args {
     Tok sx, sq;
 };
 cudaError_t launch_quant8(const Quant8Args& a, const void* x, uint8_t* q, uint8_t* s, cudaStream_t st);
-// x [M, N], pitch px: in groups along its rows (qr, sr [M, N / 128]) and along its columns
-// (qc, sc [M / 128, N]); either pair may be null.  pq: pitch of both, ps: of sr.
-cudaError_t launch_quant8_both(bool bf16, int64_t M, int64_t N, const void* x, int64_t px, uint8_t* qr,
-                               uint8_t* sr, int64_t ps, uint8_t* qc, uint8_t* sc, int64_t pq, cudaStream_t st);
-// e4m3 in groups along rows to e4m3 in groups along columns.
-cudaError_t launch_quant8_turn(int64_t M, int64_t N, const uint8_t* q, int64_t px, const uint8_t* s, uint8_t* qc,
-                               uint8_t* sc, int64_t pq, cudaStream_t st);
+// The backward product's operands: dy [M, N] in groups along its rows (dyr, sr [M, ps]) and along its
+// columns (dyc, sc [M / 128, N]), x [M, K] in groups along its columns (xc, sx [M / 128, K]).  pn, pk:
+// pitches, whole lines of 128 bytes, so that a line of a copy is one of memory.
+struct Quant8Operands {
+    int64_t pn, pk, ps;
+    uint8_t *dyr, *sr, *dyc, *sc, *xc, *sx;
+};
+// dy's for the gradients that are wanted.  Small calls make x's in the same launch (`turned`; 1500 x 1095 x
+// 1002: all of the gradients 31 -> 28 us); others leave it to launch_quant8_turn, beside the product that reads it.
+cudaError_t launch_quant8_operands(bool bf16, int64_t M, int64_t N, int64_t K, const void* dy, int64_t py, const uint8_t* x,
+                                   int64_t px, const uint8_t* s, const Quant8Operands& o, bool dx, bool dw, bool* turned,
+                                   cudaStream_t st);
+// x [M, K] in e4m3, groups along its rows.  Rows start on 16 bytes.
+cudaError_t launch_quant8_turn(int64_t M, int64_t K, const uint8_t* x, int64_t px, const uint8_t* s, const Quant8Operands& o,
+                               cudaStream_t st);
 
 // A matrix operand of the product: `rows` of the result's rows (or columns) by `depth`
 // contracted values.  mn: the contracted index is the outer one in memory (pitch between

@@ -74,26 +74,19 @@ bool proj_args(const mamba2_proj8_shape* s, const mamba2_proj8_pitches* p, Proj*
     return true;
 }
 
-// The backward product's workspace: dy along its rows and its columns, x along its columns.
-struct Work {
-    int64_t pn, pk;   // pitches
-    uint8_t *dyr, *sr, *dyc, *sc, *xc, *sx;
-    size_t bytes;
-};
-Work work_of(const Proj& a, void* base) {
-    Work w;
-    w.pn = up(a.N, 128), w.pk = up(a.K, 128);
+// The backward product's workspace.
+size_t work_of(const Proj& a, void* base, Quant8Operands* w) {
+    w->pn = up(a.N, 128), w->pk = up(a.K, 128), w->ps = up(groups(a.N), 4);
     size_t at = 0;
     const auto take = [&](int64_t n) {
         uint8_t* p = static_cast<uint8_t*>(base) + at;
         at += (size_t)up(n, 256);
         return p;
     };
-    w.dyr = take(a.M * w.pn), w.sr = take(a.M * up(groups(a.N), 4));
-    w.dyc = take(a.M * w.pn), w.sc = take(groups(a.M) * a.N);
-    w.xc = take(a.M * w.pk), w.sx = take(groups(a.M) * a.K);
-    w.bytes = at;
-    return w;
+    w->dyr = take(a.M * w->pn), w->sr = take(a.M * w->ps);
+    w->dyc = take(a.M * w->pn), w->sc = take(groups(a.M) * a.N);
+    w->xc = take(a.M * w->pk), w->sx = take(groups(a.M) * a.K);
+    return at;
 }
 
 }  // namespace
@@ -172,7 +165,8 @@ size_t mamba2_proj8_bwd_workspace_size(const mamba2_proj8_shape* shape) {
     Proj a;
     mamba2_status e;
     if (!proj_args(shape, nullptr, &a, &e) || a.M == 0 || a.N == 0) return 0;
-    return work_of(a, nullptr).bytes;
+    Quant8Operands w;
+    return work_of(a, nullptr, &w);
 }
 
 mamba2_status mamba2_proj8_bwd(const mamba2_proj8_shape* shape, const mamba2_proj8_pitches* pitches, const void* dy,
@@ -194,16 +188,17 @@ mamba2_status mamba2_proj8_bwd(const mamba2_proj8_shape* shape, const mamba2_pro
         return from_cuda(c);
     }
     if (!dx && !dw) return MAMBA2_OK;
-    const Work k = work_of(a, workspace);
-    const int64_t nb = groups(a.N), kb = groups(a.K);
-    cudaError_t c = launch_quant8_both(a.bf16, a.M, a.N, dy, a.py, dx ? k.dyr : nullptr, k.sr, up(nb, 4), dw ? k.dyc : nullptr, k.sc,
-                                       k.pn, st);
+    Quant8Operands k;
+    work_of(a, workspace, &k);
+    const int64_t kb = groups(a.K);
+    bool turned;
+    cudaError_t c = launch_quant8_operands(a.bf16, a.M, a.N, a.K, dy, a.py, x, a.px, x_scales, k, dx, dw, &turned, st);
     if (c == cudaSuccess && dx) {
-        const Operand W{w, a.pw, true, w_scales, 1, kb, 7}, D{k.dyr, k.pn, false, k.sr, up(nb, 4), 1, 0};
+        const Operand W{w, a.pw, true, w_scales, 1, kb, 7}, D{k.dyr, k.pn, false, k.sr, k.ps, 1, 0};
         c = launch_proj8(D, W, a.M, a.K, a.N, dx, a.K, a.bf16, st);
     }
     if (c == cudaSuccess && dw) {
-        c = launch_quant8_turn(a.M, a.K, x, a.px, x_scales, k.xc, k.sx, k.pk, st);
+        if (!turned) c = launch_quant8_turn(a.M, a.K, x, a.px, x_scales, k, st);
         const Operand X{k.xc, k.pk, true, k.sx, 1, a.K, 0}, D{k.dyc, k.pn, true, k.sc, 1, a.N, 0};
         if (c == cudaSuccess) c = launch_proj8(D, X, a.N, a.K, a.M, dw, a.K, false, st);
     }

@@ -194,12 +194,12 @@ __device__ __forceinline__ void put_tops(float (*tops)[kGroup], int warp, int tx
 
 // Thread (tx, ty) has rows ty + 32 i and columns 8 tx + j.
 template <typename TI, bool VEC, int MODE, int kThreads = 512>
-__global__ void __launch_bounds__(kThreads, sizeof(TI) == 2 && MODE == kRow ? 3 : 2) quant8_kernel(const TI* __restrict__ x, const Tile p) {
+__device__ __forceinline__ void quant_tile(const TI* __restrict__ x, const Tile& p, uint32_t tile) {
     constexpr int kLines = kThreads / 16, kPer = kGroup / kLines, kWarps = kThreads / 32;
     __shared__ __align__(16) float tops[kWarps][kGroup];
     __shared__ __align__(8) uint8_t bytes[kGroup];
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t mb = blockIdx.x / p.nb, nb = blockIdx.x - mb * p.nb;
+    const uint32_t mb = tile / p.nb, nb = tile - mb * p.nb;
     const int64_t m0 = (int64_t)mb * kGroup, n0 = (int64_t)nb * kGroup;
     const int rows = (int)min((int64_t)kGroup, p.M - m0), cols = (int)min((int64_t)kGroup, p.N - n0), count = cols - 8 * tx;
     grid_dep_wait();
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(TI) == 2 && MODE == kRow ? 3 
         if (!CLEAN && infinite(top)) return false;
         const uint32_t byte = scale_byte(top);
         const f2 f = dup2(scale_inverse(byte));
-        if (threadIdx.x == 0) p.sr[blockIdx.x] = (uint8_t)byte;
+        if (threadIdx.x == 0) p.sr[tile] = (uint8_t)byte;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) put(clean, p.qr, i, [&](int) { return f; });
         return true;
@@ -322,15 +322,27 @@ __global__ void __launch_bounds__(kThreads, sizeof(TI) == 2 && MODE == kRow ? 3 
         if (!block_go(plain)) block_go(clean);
 }
 
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // e4m3 in groups along rows to e4m3 in groups along columns.  The bits of an e4m3 number in the
-// places of fp32's low exponent and high mantissa bits are its magnitude times 2^-120, subnormal
-// ones too: shifts and one product, where conversions by way of fp16 run at a quarter of the rate;
-// the sign is put back as it was.
-template <bool VEC> __global__ void __launch_bounds__(kThreads, 2) quant8_turn_kernel(const uint8_t* __restrict__ x, const Tile p) {
+// places of a bf16's (or fp32's) low exponent and high mantissa bits are its magnitude times 2^-120,
+// subnormal ones too: a shift and a product by a power of two, where conversions by way of fp16 run at
+// a quarter of the rate; the sign is put back as it was.  In bf16, two at a time, everything is exact but
+// for values below 2^-126: rows of scales below 2^-111, 2^8 and up, and NaN take the way through fp32.
+template <bool VEC> __device__ __forceinline__ void turn_tile(const uint8_t* __restrict__ x, const Tile& p, uint32_t tile) {
     __shared__ __align__(16) float tops[kWarps][kGroup];
     __shared__ __align__(8) uint8_t bytes[kGroup];
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t mb = blockIdx.x / p.nb, nb = blockIdx.x - mb * p.nb;
+    const uint32_t mb = tile / p.nb, nb = tile - mb * p.nb;
     const int64_t m0 = (int64_t)mb * kGroup, n0 = (int64_t)nb * kGroup;
     const int rows = (int)min((int64_t)kGroup, p.M - m0), cols = (int)min((int64_t)kGroup, p.N - n0), count = cols - 8 * tx;
     const int64_t from = (m0 + ty) * p.sx.t + n0 + 8 * tx, to = (m0 + ty) * p.sq.t + n0 + 8 * tx;
@@ -338,6 +350,7 @@ template <bool VEC> __global__ void __launch_bounds__(kThreads, 2) quant8_turn_k
     grid_dep_launch();
     uint32_t w[kPer][2];
     float lift[kPer], rest[kPer];   // 2^120 times the row's scale, as two factors in range
+    bool bad = false;               // what takes the careful way
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         w[i][0] = w[i][1] = 0;
@@ -353,11 +366,10 @@ template <bool VEC> __global__ void __launch_bounds__(kThreads, 2) quant8_turn_k
                 if (j < count) w[i][j / 4] |= (uint32_t)__ldg(f + j) << (8 * (j & 3));
         }
         const int e = 120 + (int)__ldg(p.s_in + (m0 + ty + kLines * i) * p.nb + nb);   // 2^(e - 127)
+        bad |= e < 120 + 16 && ((w[i][0] | w[i][1]) & 0x7f7f7f7fu) != 0;
         lift[i] = scale_value((uint32_t)min(e, 254));
         rest[i] = scale_value((uint32_t)max(e - 127, 127));   // 1 up to e = 254, then 2^(e - 254)
     }
-    // NaN, and scales of 2^8 and up: what takes a second look
-    bool bad = false;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         bad |= rest[i] != 1.f;
@@ -365,19 +377,18 @@ template <bool VEC> __global__ void __launch_bounds__(kThreads, 2) quant8_turn_k
         for (int h = 0; h < 2; ++h) bad |= __vcmpeq4(w[i][h] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
     }
     // the magnitude of value j of row i
-    const auto value = [&](auto careful, int i, int j) {
+    const auto value = [&](int i, int j) {
         const uint32_t k = 8 * (j & 3), v = w[i][j / 4];
         const uint32_t b = (k < 20 ? v << (20 - k) : v >> (k - 20)) & 0x07f00000u;
-        const float f = __uint_as_float(b) * lift[i];
-        return decltype(careful)::value ? (b == 0x07f00000u ? __uint_as_float(0x7fffffffu) : f * rest[i]) : f;
+        return b == 0x07f00000u ? __uint_as_float(0x7fffffffu) : __uint_as_float(b) * lift[i] * rest[i];
     };
-    const auto run = [&](auto careful) {
+    const auto carefully = [&] {
         float t[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             t[j] = 0.f;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) t[j] = fmaxf(t[j], value(careful, i, j));
+            for (int i = 0; i < kPer; ++i) t[j] = fmaxf(t[j], value(i, j));
             t[j] = fmaxf(t[j], __shfl_xor_sync(0xffffffffu, t[j], 16));
         }
         if (lane < 16) put_tops(tops, warp, tx, t);
@@ -393,14 +404,65 @@ template <bool VEC> __global__ void __launch_bounds__(kThreads, 2) quant8_turn_k
                 float v[4];
                 asm volatile("" : "+r"(w[i][h]));   // unpacked anew, as above
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = value(careful, i, 4 * h + j);
+                for (int j = 0; j < 4; ++j) v[j] = value(i, 4 * h + j);
                 o[h] = e4m3_four<false>(v, pack2(t[4 * h], t[4 * h + 1]), pack2(t[4 * h + 2], t[4 * h + 3])) | (w[i][h] & 0x80808080u);
             }
             store_eight<VEC>(p.qc + to + i * (kLines * p.sq.t), count, o[0], o[1]);
         }
     };
-    if (__syncthreads_or(bad)) run(std::true_type{});
-    else run(std::false_type{});
+    if (__syncthreads_or(bad)) return carefully();
+    // columns 0 and 2, 1 and 3, 4 and 6, 5 and 7 of each row
+    uint32_t v[kPer][4], top[4] = {};
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const uint32_t up = __float_as_uint(lift[i]) >> 16, by = up | up << 16;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            v[i][h] = mul_bf16x2((h & 1 ? w[i][h / 2] >> 4 : w[i][h / 2] << 4) & 0x07f007f0u, by);
+            top[h] = max_bf16x2(top[h], v[i][h]);
+        }
+    }
+    float t[8];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        top[h] = max_bf16x2(top[h], __shfl_xor_sync(0xffffffffu, top[h], 16));
+        t[4 * (h / 2) + (h & 1)] = bf_lo(top[h]), t[4 * (h / 2) + (h & 1) + 2] = bf_hi(top[h]);
+    }
+    if (lane < 16) put_tops(tops, warp, tx, t);
+    __syncthreads();
+    column_scales(p, tops, bytes, mb, n0, cols);
+    column_inverses(bytes, tx, t);
+    uint32_t inv[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+        inv[h] = __float_as_uint(t[4 * (h / 2) + (h & 1)]) >> 16 | (__float_as_uint(t[4 * (h / 2) + (h & 1) + 2]) & 0xffff0000u);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (ty + kLines * i >= rows) continue;
+        uint32_t o[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t a = mul_bf16x2(v[i][2 * h], inv[2 * h]), b = mul_bf16x2(v[i][2 * h + 1], inv[2 * h + 1]);
+            o[h] = e4m3_pair<false>(bf_lo(a), bf_lo(b)) | e4m3_pair<false>(bf_hi(a), bf_hi(b)) << 16 | (w[i][h] & 0x80808080u);
+        }
+        store_eight<VEC>(p.qc + to + i * (kLines * p.sq.t), count, o[0], o[1]);
+    }
+}
+
+template <typename TI, bool VEC, int MODE, int kThreads = 512>
+__global__ void __launch_bounds__(kThreads, sizeof(TI) == 2 && MODE == kRow ? 3 : 2) quant8_kernel(const TI* __restrict__ x, const Tile p) {
+    quant_tile<TI, VEC, MODE, kThreads>(x, p, blockIdx.x);
+}
+// Four blocks an SM (32768 x 2560: 58 us; two 75, by the way through fp32 65).
+template <bool VEC> __global__ void __launch_bounds__(kThreads, 4) quant8_turn_kernel(const uint8_t* __restrict__ x, const Tile p) {
+    turn_tile<VEC>(x, p, blockIdx.x);
+}
+// The backward product's operands in one launch: `tiles` of dy, then those of x.
+template <typename TI, bool VEC>
+__global__ void __launch_bounds__(kThreads, 2)
+quant8_operands_kernel(const TI* __restrict__ dy, const Tile p, uint32_t tiles, const uint8_t* __restrict__ x, const Tile q) {
+    if (blockIdx.x < tiles) quant_tile<TI, VEC, kRow | kCol>(dy, p, blockIdx.x);
+    else turn_tile<false>(x, q, blockIdx.x - tiles);
 }
 
 int64_t blocks_of(Tile& p) {
@@ -409,12 +471,16 @@ int64_t blocks_of(Tile& p) {
     return (p.M + kGroup - 1) / kGroup * p.nb;
 }
 
+template <typename TI> bool vectors(const TI* x, const Tile& p) {
+    return p.N % 8 == 0 && vec_ok(x, p.sx, 16, sizeof(TI)) && (!p.qr || vec_ok(p.qr, p.sq, 8, 1)) &&
+           (!p.qc || vec_ok(p.qc, p.sq, 8, 1));
+}
+
 template <typename TI, int MODE> cudaError_t go(const TI* x, Tile p, cudaStream_t st) {
     if (p.M == 0 || p.N == 0) return cudaSuccess;
-    const int64_t blocks = blocks_of(p), es = sizeof(TI);
+    const int64_t blocks = blocks_of(p);
     if (blocks >= (int64_t(1) << 31) || p.M >= (int64_t(1) << 31)) return kGridLimit;
-    const bool v = p.N % 8 == 0 && vec_ok(x, p.sx, 16, es) && (!p.qr || vec_ok(p.qr, p.sq, 8, 1)) &&
-                   (!p.qc || vec_ok(p.qc, p.sq, 8, 1));
+    const bool v = vectors(x, p);
     // blocks of 128 x 128 by 1024 threads, of which an SM holds as many tiles' loads at once as fit it
     constexpr int T = MODE == kBlock ? 1024 : kThreads;
     return launch_kernel(v ? quant8_kernel<TI, true, MODE, T> : quant8_kernel<TI, false, MODE, T>, dim3((unsigned)blocks),
@@ -433,21 +499,29 @@ cudaError_t launch_quant8(const Quant8Args& a, const void* x, uint8_t* q, uint8_
     return a.block ? go<kBlock>(a.bf16, x, p, st) : go<kRow>(a.bf16, x, p, st);
 }
 
-cudaError_t launch_quant8_both(bool bf16, int64_t M, int64_t N, const void* x, int64_t px, uint8_t* qr, uint8_t* sr,
-                               int64_t ps, uint8_t* qc, uint8_t* sc, int64_t pq, cudaStream_t st) {
-    const Tile p{M, N, (uint32_t)M, 0, Tok{0, px}, Tok{0, pq}, nullptr, qr, sr, qc, sc, ps, false};
-    return !qc ? go<kRow>(bf16, x, p, st) : !qr ? go<kCol>(bf16, x, p, st) : go<kRow | kCol>(bf16, x, p, st);
+cudaError_t launch_quant8_operands(bool bf16, int64_t M, int64_t N, int64_t K, const void* dy, int64_t py, const uint8_t* x,
+                                   int64_t px, const uint8_t* s, const Quant8Operands& o, bool dx, bool dw, bool* turned,
+                                   cudaStream_t st) {
+    Tile p{M, N, (uint32_t)M, 0, Tok{0, py}, Tok{0, o.pn}, nullptr, dx ? o.dyr : nullptr, o.sr, dw ? o.dyc : nullptr, o.sc, o.ps, false};
+    Tile q{M, K, (uint32_t)M, 0, Tok{0, px}, Tok{0, o.pk}, s, nullptr, nullptr, o.xc, o.sx, 0, false};
+    const int64_t tiles = blocks_of(p), all = tiles + blocks_of(q);
+    *turned = dx && dw && early(all);
+    if (!*turned) return !dw ? go<kRow>(bf16, dy, p, st) : !dx ? go<kCol>(bf16, dy, p, st) : go<kRow | kCol>(bf16, dy, p, st);
+    const auto together = [&](auto* d) {
+        using TI = std::remove_const_t<std::remove_pointer_t<decltype(d)>>;
+        return launch_kernel(vectors(d, p) ? quant8_operands_kernel<TI, true> : quant8_operands_kernel<TI, false>,
+                             dim3((unsigned)all), dim3(kThreads), 0, st, true, d, p, (uint32_t)tiles, x, q);
+    };
+    return bf16 ? together(static_cast<const __nv_bfloat16*>(dy)) : together(static_cast<const float*>(dy));
 }
 
-// Rows of q and qc start on 16 bytes.
-cudaError_t launch_quant8_turn(int64_t M, int64_t N, const uint8_t* q, int64_t px, const uint8_t* s, uint8_t* qc,
-                               uint8_t* sc, int64_t pq, cudaStream_t st) {
-    Tile p{M, N, (uint32_t)M, 0, Tok{0, px}, Tok{0, pq}, s, nullptr, nullptr, qc, sc, 0, false};
-    if (M == 0 || N == 0) return cudaSuccess;
-    const int64_t blocks = blocks_of(p);
+cudaError_t launch_quant8_turn(int64_t M, int64_t K, const uint8_t* x, int64_t px, const uint8_t* s, const Quant8Operands& o,
+                               cudaStream_t st) {
+    Tile q{M, K, (uint32_t)M, 0, Tok{0, px}, Tok{0, o.pk}, s, nullptr, nullptr, o.xc, o.sx, 0, false};
+    const int64_t blocks = blocks_of(q);
     if (blocks >= (int64_t(1) << 31) || M >= (int64_t(1) << 31)) return kGridLimit;
-    return launch_kernel(N % 8 == 0 ? quant8_turn_kernel<true> : quant8_turn_kernel<false>, dim3((unsigned)blocks), dim3(kThreads), 0,
-                         st, early(blocks), q, p);
+    return launch_kernel(K % 8 == 0 ? quant8_turn_kernel<true> : quant8_turn_kernel<false>, dim3((unsigned)blocks), dim3(kThreads), 0,
+                         st, early(blocks), x, q);
 }
 
 }  // namespace m2

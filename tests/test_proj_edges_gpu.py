@@ -63,6 +63,36 @@ def test_sums_split_between_blocks(M, K, N):
     assert m2.device_error() == 0
 
 
+@pytest.mark.parametrize("K", [64, 131])
+@pytest.mark.parametrize("low,high", [(-100, 7), (-127, -105), (-9, 30), (-127, 40)])
+def test_scales_of_every_size_turned(low, high, K):
+    """x along its columns for dw: every e4m3 number, subnormal ones too, rows of very small and large
+    scales, and of zeros with the smallest.  dw is read off with one row of dy a tile of 128."""
+    r = torch.Generator().manual_seed(40)
+    M = 300
+    bits = torch.randint(0, 256, (M, K), generator=r).to(torch.uint8)
+    bits[(bits & 127) == 127] = 5
+    bits[::17] = 128
+    e = torch.randint(low, high + 1, (M, 1), generator=r)
+    e[::17] = -127
+    room = torch.zeros(M, -(-K // 16) * 16, dtype=torch.uint8, device="cuda")
+    room[:, :K] = bits.cuda()
+    q = room.view(E4M3)[:, :K]
+    s = (e.expand(M, -(-K // 128)) + 127).to(torch.uint8).cuda().view(torch.float8_e8m0fnu)
+    x = bits.view(E4M3).double() * 2.0 ** e.double()
+    want = R.dequant(*R.quant(x, 128, 1), 128, 1)
+    wq, ws = m2.quant8(torch.ones(3, K, device="cuda"), group="block")
+    for row in (0, 1, 130, 299):
+        dy = torch.zeros(M, 3)
+        dy[row, 1] = 1.0
+        dw = m2.proj8_bwd(dy.cuda(), q, s, wq, ws, need_dx=False)["dw"]
+        assert (dw[0] == 0).all() and (dw[2] == 0).all()
+        # one product of a power of two: exact where fp32 holds it
+        exact = want[row].abs() >= 2.0 ** -126
+        assert torch.equal(f64(dw[1])[exact], want[row][exact]), row
+        assert (f64(dw[1])[~exact].abs() <= 2.0 ** -126).all()
+
+
 def test_long_sums_of_gradients():
     """dw over 20000 tokens, dx over 9000 outputs: several accumulators a result."""
     M, K, N = 20000, 140, 130
