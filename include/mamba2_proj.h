@@ -93,8 +93,10 @@ MAMBA2_API mamba2_status mamba2_quant8(const mamba2_quant8_shape* shape,
 /* ---- proj8: matrix product of values in 8 bits ---------------------------------
  *   y[m,n] = sum_k x[m,k] w[n,k]
  * x [tokens, inputs] e4m3 in row groups, w [outputs, inputs] e4m3 in block groups, sums in
- * fp32 on the tensor cores, y io.  Few tokens split the sum over a cluster of blocks
- * (joined in a fixed order).  inputs >= 1; every size at most 2^30. */
+ * fp32 on the tensor cores, y io.  Few tokens, and few tiles with long sums, split the sum
+ * over a cluster of blocks (joined in a fixed order).  inputs >= 1; every size at most 2^30.
+ * Waits in the kernels end after two seconds: one that runs out sets
+ * MAMBA2_DEVERR_TIMEOUT_PROJ8 in the word of mamba2_ssd_device_error, and the result is void. */
 typedef struct mamba2_proj8_shape {
     int64_t tokens, inputs, outputs;
     int32_t dtype;   /* mamba2_dtype of y, dy and dx */
