@@ -7,13 +7,14 @@
 //   dt = r (g - n mean(g n)) + dtotal;  dx = dresidual = dt;  dw = sum over tokens of dy n
 //
 // Bytes bound: every tensor moves once.  b8 T4096 D2560 bf16 with an fp32 residual: forward 145 us,
-// in 8 bits 137 us (6.7 TB/s, the measured copy rate), backward 209 us (6.4 TB/s, 0.96); one token
-// 2.1 us, the launch.
+// in 8 bits 137 us (6.7 TB/s, the measured copy rate), backward 206 us (6.5 TB/s, 0.97), with a bf16
+// residual 123 us (0.82: issue slots, twice the values a byte); one token 2.1 us, the launch.
 //
 // A team (a warp for narrow rows, else a block) holds a forward row in registers between the sum
 // and the result; what wide rows do not fit is read again.  A backward team walks over tokens, so
 // that its part of dw stays in registers; the parts are summed by a second kernel, in a fixed order.
 #include <algorithm>
+#include <atomic>
 #include <initializer_list>
 #include <utility>
 
@@ -167,7 +168,7 @@ bwd_kernel(const TR* __restrict__ total, const float* __restrict__ w, const TI* 
     static_assert(!AHEAD || (VEC && VPT > 0), "copies are of whole units");
     constexpr int V = U::V, K = VPT > 0 ? VPT : 1;
     __shared__ __align__(16) float2 red[2][32];
-    extern __shared__ __align__(16) uint4 room[];   // [2 rows][K][total, dtotal, dy][threads], then w
+    extern __shared__ __align__(16) uint4 room[];   // [2 rows][K][total, dtotal, dy][threads]
     constexpr int kD = V * (int)sizeof(TI), kUnit = 32 + kD;   // bytes of dy's piece, of a unit
     const int slot = WARP ? (int)blockIdx.x * kTeams + (threadIdx.x >> 5) : blockIdx.x;
     const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;
@@ -176,11 +177,12 @@ bwd_kernel(const TR* __restrict__ total, const float* __restrict__ w, const TI* 
     const int units = U::count(q.D), bt = blockDim.x;
     float* pr = part && slot < slots ? part + (int64_t)slot * q.D : nullptr;
     const float inv = 1.f / (float)q.D;
-    float acc[K][V];
+    constexpr int P = V / 2;   // pairs: the arithmetic is packed
+    f2 acc[K][P];
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[k][j] = 0.f;
+        for (int j = 0; j < P; ++j) acc[k][j] = 0;
     int parity = 0;
     const auto place = [&](int64_t row, const Tok& s) {
         if (q.flat) return row * s.t;
@@ -206,50 +208,53 @@ bwd_kernel(const TR* __restrict__ total, const float* __restrict__ w, const TI* 
         }
         stage_commit();
     };
-    // each unit's weights, kept beside the rows: what comes from L1 is pushed out of it by the copies
-    // (read twice a row from there, they held the row up for longer than its sums)
-    float* ws = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(room) + 2 * K * kUnit * bt);
-    const auto weights = [&](int u, float (&f)[V]) {
-        if constexpr (AHEAD) {
-            U::load(ws, u, q.D, f);
-        } else {
+    // a thread's channels are the same in every row: their weights stay in registers (read from L1, which the
+    // copies push them out of, the rows took 222 us instead of 207; from shared memory 138 instead of 123 with a bf16 residual)
+    f2 wr[K][P];
+    const auto load_weights = [&](int u, f2 (&o)[P]) {
+        float f[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) f[j] = 1.f;
-            if (w) U::load(w, u, q.D, f);
-        }
+        for (int j = 0; j < V; ++j) f[j] = 1.f;
+        if (w && u < units) U::load(w, u, q.D, f);
+#pragma unroll
+        for (int j = 0; j < P; ++j) o[j] = pack2(f[2 * j], f[2 * j + 1]);
     };
-    if constexpr (AHEAD) {
-        for (int i = threadIdx.x; i < q.D; i += bt) ws[i] = w ? w[i] : 1.f;
-        __syncthreads();
-    }
+    if constexpr (VPT > 0)
+#pragma unroll
+        for (int k = 0; k < K; ++k) load_weights(tid + k * nt, wr[k]);
+    const auto put = [&](int u, const f2 (&a)[P]) {
+        float f[V];
+#pragma unroll
+        for (int j = 0; j < P; ++j) unpack2(a[j], f[2 * j], f[2 * j + 1]);
+        U::store(pr, u, q.D, f);
+    };
     if (slot >= slots) return;
     if constexpr (AHEAD) copy(slot, 0);
     for (int64_t row = slot; row < q.rows; row += slots) {
-        float ss = 0.f, gv = 0.f, r, m;
-        const auto sums = [&](int u, const float (&v)[V], const float (&d)[V]) {
-            float f[V];
-            weights(u, f);
+        f2 ss = 0, gv = 0, r, less;   // less: -mean(g n)
+        const auto sums = [&](const f2 (&f)[P], const float (&v)[V], const float (&d)[V]) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                ss = fmaf(v[j], v[j], ss);
-                gv = fmaf(d[j] * f[j], v[j], gv);
+            for (int j = 0; j < P; ++j) {
+                const f2 x = pack2(v[2 * j], v[2 * j + 1]);
+                ss = fma2(x, x, ss);
+                gv = fma2(mul2(pack2(d[2 * j], d[2 * j + 1]), f[j]), x, gv);
             }
         };
         const auto scales = [&] {
             // two halves of red in turn: the next token's sums do not overwrite one being read
-            const float2 s = team_sum<WARP>(ss, gv, red[parity]);
-            r = __frsqrt_rn(s.x * inv + q.eps);
-            m = r * (s.y * inv);
+            const float2 s = team_sum<WARP>(sum2(ss), sum2(gv), red[parity]);
+            const float one = __frsqrt_rn(s.x * inv + q.eps);
+            r = dup2(one);
+            less = dup2(-one * (s.y * inv));
         };
         // e: dtotal; a: this unit's part of dw, added to
-        const auto result = [&](int u, const float (&v)[V], const float (&d)[V], float (&e)[V], float (&a)[V]) {
-            float f[V];
-            weights(u, f);
+        const auto result = [&](int u, const f2 (&f)[P], const float (&v)[V], const float (&d)[V], float (&e)[V], f2 (&a)[P]) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float n = v[j] * r;
-                a[j] = fmaf(d[j], n, a[j]);
-                e[j] = fmaf(r, fmaf(-n, m, d[j] * f[j]), e[j]);
+            for (int j = 0; j < P; ++j) {
+                const f2 n = mul2(pack2(v[2 * j], v[2 * j + 1]), r), g = pack2(d[2 * j], d[2 * j + 1]);
+                a[j] = fma2(g, n, a[j]);
+                const f2 t = fma2(n, less, mul2(g, f[j]));
+                unpack2(fma2(r, t, pack2(e[2 * j], e[2 * j + 1])), e[2 * j], e[2 * j + 1]);
             }
             U::store(dx + row * q.D, u, q.D, e);
             if (dres) U::store(dres + row * q.D, u, q.D, e);
@@ -267,7 +272,7 @@ bwd_kernel(const TR* __restrict__ total, const float* __restrict__ w, const TI* 
                     float v[V], d[V];
                     fetch<TR>(piece(parity, k, 0), v);
                     fetch<TI>(piece(parity, k, 2), d);
-                    sums(tid + k * nt, v, d);
+                    sums(wr[k], v, d);
                 }
             scales();
 #pragma unroll
@@ -278,7 +283,7 @@ bwd_kernel(const TR* __restrict__ total, const float* __restrict__ w, const TI* 
                     fetch<TI>(piece(parity, k, 2), d);
                     if (dtotal) fetch<TR>(piece(parity, k, 1), e);
                     else zero(e);
-                    result(tid + k * nt, v, d, e, acc[k]);
+                    result(tid + k * nt, wr[k], v, d, e, acc[k]);
                 }
         } else {
             const TR* tr = total + place(row, q.st);
@@ -298,30 +303,35 @@ bwd_kernel(const TR* __restrict__ total, const float* __restrict__ w, const TI* 
                     }
 #pragma unroll
                 for (int k = 0; k < K; ++k)
-                    if (tid + k * nt < units) sums(tid + k * nt, v[k], d[k]);
+                    if (tid + k * nt < units) sums(wr[k], v[k], d[k]);
                 scales();
 #pragma unroll
                 for (int k = 0; k < K; ++k)
                     if (tid + k * nt < units) {
                         third(tid + k * nt);
-                        result(tid + k * nt, v[k], d[k], e, acc[k]);
+                        result(tid + k * nt, wr[k], v[k], d[k], e, acc[k]);
                     }
             } else {
                 for (int u = tid; u < units; u += nt) {
                     U::load(tr, u, q.D, v[0]);
                     U::load(dr, u, q.D, d[0]);
-                    sums(u, v[0], d[0]);
+                    load_weights(u, wr[0]);
+                    sums(wr[0], v[0], d[0]);
                 }
                 scales();
                 for (int u = tid; u < units; u += nt) {
                     U::load(tr, u, q.D, v[0]);
                     U::load(dr, u, q.D, d[0]);
                     third(u);
-                    float a[V];
-                    zero(a);
-                    if (pr && row != slot) U::load(pr, u, q.D, a);
-                    result(u, v[0], d[0], e, a);
-                    if (pr) U::store(pr, u, q.D, a);
+                    float part_of[V];
+                    zero(part_of);
+                    if (pr && row != slot) U::load(pr, u, q.D, part_of);
+                    f2 a[P];
+#pragma unroll
+                    for (int j = 0; j < P; ++j) a[j] = pack2(part_of[2 * j], part_of[2 * j + 1]);
+                    load_weights(u, wr[0]);
+                    result(u, wr[0], v[0], d[0], e, a);
+                    if (pr) put(u, a);
                 }
             }
         }
@@ -330,7 +340,7 @@ bwd_kernel(const TR* __restrict__ total, const float* __restrict__ w, const TI* 
     if (VPT > 0 && pr)
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (tid + k * nt < units) U::store(pr, tid + k * nt, q.D, acc[k]);
+            if (tid + k * nt < units) put(tid + k * nt, acc[k]);
 }
 
 Rows rows_of(const AddNormArgs& a) {
@@ -362,9 +372,34 @@ cudaError_t fwd_go(const AddNormArgs& a, const void* x_, const void* res_, const
     return e;
 }
 
+constexpr int kDevices = 64;
+constexpr int kSharedMost = 128 * 1024;   // bytes of an SM, for the rows copied ahead
+constexpr int kRoomMost = 2 * 2 * 48 * 1024;   // of a block: two rows, two units of three pieces a thread
+
+// Blocks of kernel k that an SM holds, having let it have its shared memory; asked for once for the
+// sizes that were last asked for on a device (`known`: this kernel's threads, room and blocks, by device).
+template <typename K> cudaError_t resident_blocks(K k, int threads, int room, std::atomic<uint64_t>* known, int* blocks) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t key = (uint64_t)threads << 32 | (uint64_t)room << 8;
+    const uint64_t old = dev < kDevices ? known[dev].load(std::memory_order_relaxed) : 0;
+    if ((old & ~uint64_t(255)) == key) return *blocks = (int)(old & 255), cudaSuccess;
+    // the most that any size asks for, so that calls of two sizes at once do not take it from each other
+    if (room && (e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoomMost)) != cudaSuccess) return e;
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, k, threads, (size_t)room)) != cudaSuccess) return e;
+    // Copies land by way of L1: with 228 KB of an SM taken from it they come at three quarters of the rate,
+    // whatever is in flight (fp32, D 2560: 262 us, with 164 KB 200).
+    *blocks = std::max(1, std::min(*blocks, kSharedMost / (room + 1536)));
+    if (room && (e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, 72)) != cudaSuccess) return e;
+    if (dev < kDevices) known[dev].store(key | (uint64_t)*blocks, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
+// *slots: the teams that it takes (rows of part).
 template <typename TI, typename TR, bool VEC>
 cudaError_t bwd_go(const AddNormArgs& a, const void* t_, const float* w, const void* dy_, const void* dt_, void* dx_,
-                   void* dr_, float* part, cudaStream_t st) {
+                   void* dr_, float* part, int* slots, cudaStream_t st) {
     const Rows q = rows_of(a);
     if (q.rows >= (int64_t(1) << 31)) return kGridLimit;
     const TR *t = static_cast<const TR*>(t_), *dt = static_cast<const TR*>(dt_);
@@ -372,21 +407,25 @@ cudaError_t bwd_go(const AddNormArgs& a, const void* t_, const float* w, const v
     TI* dx = static_cast<TI*>(dx_);
     TR* dr = static_cast<TR*>(dr_);
     const int64_t n = BwdUnits<TR, VEC>::count((int)a.D);
-    const int slots = (int)add_norm_bwd_slots(a);
-    const unsigned wb = (unsigned)((slots + kTeams - 1) / kTeams), bb = (unsigned)slots;
-    const auto go = [&](auto k, unsigned blocks, int threads, int ahead) {   // ahead: units a thread, 0: none is copied
-        const size_t room = ahead ? (size_t)2 * ahead * (32 + BwdUnits<TR, VEC>::V * sizeof(TI)) * threads + 4 * (size_t)a.D : 0;
-        if (room > 40 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)room);
-            if (e != cudaSuccess) return e;
-        }
-        return launch_kernel(k, dim3(blocks), dim3((unsigned)threads), room, st, early(blocks), t, w, dy, dt, dx, dr, part, slots, q);
+    const int64_t most = add_norm_bwd_slots(a);
+    static std::atomic<uint64_t> known[5][kDevices];   // by form
+    // ahead: units a thread, 0: none is copied
+    const auto go = [&](int form, auto k, bool warp, int threads, int ahead) {
+        const int room = ahead ? 2 * ahead * (32 + BwdUnits<TR, VEC>::V * (int)sizeof(TI)) * threads : 0;
+        int per_sm;
+        const cudaError_t e = resident_blocks(k, threads, room, known[form], &per_sm);
+        if (e != cudaSuccess) return e;
+        const int64_t teams = warp ? kTeams : 1;
+        *slots = (int)std::min(most, (int64_t)sm_count() * per_sm * teams);
+        const unsigned blocks = (unsigned)((*slots + teams - 1) / teams);
+        return launch_kernel(k, dim3(blocks), dim3((unsigned)threads), (size_t)room, st, early(blocks), t, w, dy, dt, dx, dr, part,
+                             *slots, q);
     };
-    if (n <= 32) return go(bwd_kernel<TI, TR, VEC, 1, true, VEC>, wb, kTeams * 32, VEC);
-    if (n <= 64) return go(bwd_kernel<TI, TR, VEC, 2, true, VEC>, wb, kTeams * 32, 2 * VEC);
-    if (n <= 512) return go(bwd_kernel<TI, TR, VEC, 1, false, VEC>, bb, threads_of(n, 1), VEC);
-    if (n <= 2048) return go(bwd_kernel<TI, TR, VEC, 2, false, VEC>, bb, threads_of(n, 2), 2 * VEC);
-    return go(bwd_kernel<TI, TR, VEC, 0, false, false>, bb, 1024, 0);
+    if (n <= 32) return go(0, bwd_kernel<TI, TR, VEC, 1, true, VEC>, true, kTeams * 32, VEC);
+    if (n <= 64) return go(1, bwd_kernel<TI, TR, VEC, 2, true, VEC>, true, kTeams * 32, 2 * VEC);
+    if (n <= 512) return go(2, bwd_kernel<TI, TR, VEC, 1, false, VEC>, false, threads_of(n, 1), VEC);
+    if (n <= 2048) return go(3, bwd_kernel<TI, TR, VEC, 2, false, VEC>, false, threads_of(n, 2), 2 * VEC);
+    return go(4, bwd_kernel<TI, TR, VEC, 0, false, false>, false, 1024, 0);
 }
 
 // Every access of a unit of V channels is aligned.
@@ -421,11 +460,9 @@ cudaError_t launch_add_norm_fwd(const AddNormArgs& a, const void* x, const void*
 }
 
 int64_t add_norm_bwd_slots(const AddNormArgs& a) {
-    // the teams an SM holds, by registers and by the room of the rows copied ahead
+    // what the workspace has room for: no fewer teams than any form of the kernel has on an SM at once
     const int64_t units = a.res_bf16 ? (a.D + 7) / 8 : (a.D + 3) / 4;
-    const int64_t per_sm = units <= 32 ? 3 * kTeams : units <= 64 ? 2 * kTeams
-                           : units <= 512 ? std::max<int64_t>(2, 1280 / threads_of(units, 1))
-                                          : std::max<int64_t>(1, 1000 / threads_of(units, 2));
+    const int64_t per_sm = units <= 64 ? 4 * kTeams : std::max<int64_t>(1, 2048 / threads_of(units, units <= 512 ? 1 : 2));
     return std::max<int64_t>(1, std::min<int64_t>(a.b * a.T, (int64_t)sm_count() * per_sm));
 }
 
@@ -433,19 +470,20 @@ cudaError_t launch_add_norm_bwd(const AddNormArgs& a, const void* total, const f
                                 const void* dtotal, void* dx, void* dres, float* dw, float* part, cudaStream_t st) {
     if (a.D == 0) return cudaSuccess;
     const bool none = a.b * a.T == 0;
+    int slots = 0;
     if (!dw) part = nullptr;
     if (!none) {
         const Tok row{0, a.D};
         const bool v = vec(a, a.res_bf16 ? 8 : 4, w, {{dy, a.sy}, {dx, row}}, {{total, a.st}, {dtotal, a.sres}, {dres, row}}, nullptr) &&
                        reinterpret_cast<uintptr_t>(part) % 16 == 0;
-        const auto go = [&](auto f) { return f(a, total, w, dy, dtotal, dx, dres, part, st); };
+        const auto go = [&](auto f) { return f(a, total, w, dy, dtotal, dx, dres, part, &slots, st); };
         typedef __nv_bfloat16 bf;
         const cudaError_t e = !a.bf16     ? (v ? go(bwd_go<float, float, true>) : go(bwd_go<float, float, false>))
                               : !a.res_bf16 ? (v ? go(bwd_go<bf, float, true>) : go(bwd_go<bf, float, false>))
                                             : (v ? go(bwd_go<bf, bf, true>) : go(bwd_go<bf, bf, false>));
         if (e != cudaSuccess) return e;
     }
-    return dw ? launch_column_sum(part, none ? 0 : add_norm_bwd_slots(a), a.D, dw, a.D, nullptr, st) : cudaSuccess;
+    return dw ? launch_column_sum(part, slots, a.D, dw, a.D, nullptr, st) : cudaSuccess;
 }
 
 }  // namespace m2

@@ -172,6 +172,36 @@ def test_far_offsets():
     assert m2.device_error() == 0
 
 
+def test_two_widths_at_once():
+    """Calls of two sizes of one form of the gradient, from two threads on streams of their own."""
+    import threading
+    sizes, want, got, bad = (2560, 4096), {}, {}, []
+    args = {}
+    for D in sizes:
+        r = Gen(20 + D)
+        args[D] = [r.randn(300, D).cuda(), r.randn(D).cuda(), r.randn(300, D).cuda(), r.randn(300, D).cuda()]
+        want[D] = m2.add_norm_bwd(*args[D])
+    torch.cuda.synchronize()
+
+    def work(D):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(200):
+                    got[D] = m2.add_norm_bwd(*args[D])
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=(D,)) for D in sizes]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+    for D in sizes:
+        assert torch.equal(got[D]["dx"], want[D]["dx"]) and torch.equal(got[D]["dw"], want[D]["dw"])
+
+
 def test_graphs_that_share_a_workspace():
     """Two captured backward calls over one workspace, replayed in turn on one stream."""
     a, _, _ = _operands(300, 256, 200, 10)
