@@ -39,7 +39,9 @@ using namespace tc;
 constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s: far beyond any legitimate wait
 constexpr int kThreads = 416;
 constexpr int kDevices = 64;
-constexpr int kPanel = 16;   // columns of tiles a panel (32768 x 2560 x 10576: 8 529 us, 16 511 us, all 48 513 us; 16384 x 8192 x 8192: 617, 606, 651)
+// Columns of tiles a panel (32768 x 2560 x 10576: 8 528 us, 12 516, 16 511, 24 506, all 48 513; 16384 x 8192 x
+// 8192: 12 608 us, 16 606, 24 612, 48 651).
+constexpr int kPanel = 16;
 constexpr int BM = 128, BK = 128;
 constexpr int kMostPairs = 8;   // pairs that share a tile: 1, 2, 4 or 8
 
@@ -1017,7 +1019,7 @@ cudaError_t pick(const Operand& A, const Operand& B, int64_t R, int64_t C, int64
     };
     // Few tiles: the pairs to each with which a block's share and the join take least, of those that run side
     // by side (256 x 8192 x 256: 18.0 us with one pair a tile, 13.2 with two, 9.9 with four, 10.0 with eight;
-    // 256 x 2048 x 256: 7.8, 7.7, 7.5; gradients of 30490 x 192 x 80: 126 us, now 45).  A single pair's
+    // 256 x 2048 x 256: 7.8, 7.7, 7.5; all gradients of 30490 x 192 x 80: 126 us, now 41).  A single pair's
     // blocks wait for memory longer where both operands are MN-major.
     const int64_t t128 = tr * ((C + 127) / 128), block = B_MN ? 800 : 380;
     int split = 1;
