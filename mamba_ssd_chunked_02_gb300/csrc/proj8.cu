@@ -662,6 +662,10 @@ template <int BN> struct Few {
     static int smem(int split, int ns) { return 1024 + ns * STAGE + SETS * SF_BYTES + join_bytes(split); }
 };
 constexpr int kFewStages = 8;
+// Shared memory that leaves room for no more blocks on an SM than its tensor memory has columns for: a block that
+// waits for columns never holds up one of another cluster, which may hold the columns that its own cluster waits for.
+constexpr int kFewLeast = 47 * 1024;
+static_assert(4 * Few<64>::COLS <= 512 && 5 * (kFewLeast + 1024) > 228 * 1024, "four blocks an SM");
 
 struct FewShape {
     int R, C, kb;     // lanes' rows, few rows, contracted blocks
@@ -991,7 +995,7 @@ cudaError_t go_few(const Operand& A, const Operand& B, int64_t R, int64_t Cn, in
     }
     const int others = tr * tc * split > sm_count();
     q.ns = std::min({C::stages(split, others), kFewStages, (q.kb + split - 1) / split});
-    Launch l(kFewThreads, C::smem(split, q.ns), split, st);
+    Launch l(kFewThreads, std::max(C::smem(split, q.ns), kFewLeast), split, st);
     l.early();
     l.cfg.gridDim = dim3((unsigned)(tr * split), (unsigned)tc);
     return cudaLaunchKernelEx(&l.cfg, k, ma, mb, scales_of(A, R, q.kb), scales_of(B, Cn, q.kb), out, q, device_error_word());
