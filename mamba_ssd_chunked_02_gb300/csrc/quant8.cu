@@ -100,8 +100,8 @@ template <> struct Eight<__nv_bfloat16> {
         }
     }
     __device__ __forceinline__ float top() const {
-        const uint32_t m = larger(larger(w[0], w[1]), larger(w[2], w[3]));
-        return fmaxf(fabsf(bf_lo(m)), fabsf(bf_hi(m)));
+        const uint32_t m = larger(larger(w[0], w[1]), larger(w[2], w[3]));   // NaN only where all are
+        return fmaxf(fmaxf(0.f, fabsf(bf_lo(m))), fabsf(bf_hi(m)));
     }
     __device__ __forceinline__ void into(Tops& t) const { t.join(w); }
     // Unpacked anew at each use (the statement hides what it was unpacked to before), so that the
