@@ -10,7 +10,7 @@
  *
  * Values in 8 bits.  A group of values is held as e4m3 numbers q (one byte each: sign,
  * 4 exponent bits, 3 mantissa bits, largest 448, no infinity) and one scale s = 2^e
- * (e8m0: the byte e + 127), of which they stand for q s.  Quantising takes the smallest
+ * (e8m0: the byte e + 127; 255 is NaN), of which they stand for q s.  Quantising takes the smallest
  * e >= -127 for which the group's largest magnitude is at most 448 * 2^e, and rounds x / s
  * to nearest even.  Infinities and NaN become NaN; the scale is that of the other values
  * (2^-127 in a group of zeros).  Groups are

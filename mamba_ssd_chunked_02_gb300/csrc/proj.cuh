@@ -46,8 +46,6 @@ __device__ __forceinline__ uint32_t scale_byte(float top) {
 }
 // 2^-e for the byte e + 127 (at most 247): an exact factor, in [2^-120, 2^127].
 __device__ __forceinline__ float scale_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
-// 2^e; the byte 0 is 2^-127, a subnormal.
-__device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(byte ? byte << 23 : 0x400000u); }
 
 // A group's scale is that of its finite values; what is not finite becomes e4m3's NaN.  fmaxf
 // leaves NaN out and the conversion keeps it, so that infinities alone need a second look: a

@@ -339,7 +339,7 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
 // places of a bf16's (or fp32's) low exponent and high mantissa bits are its magnitude times 2^-120,
 // subnormal ones too: a shift and a product by a power of two, where conversions by way of fp16 run at
 // a quarter of the rate; the sign is put back as it was.  In bf16, two at a time, everything is exact but
-// for values below 2^-126: rows of scales below 2^-111, 2^8 and up, and NaN take the way through fp32.
+// for values below 2^-126: rows of scales below 2^-111, 2^8 and up, and NaN take the way by whole numbers.
 template <bool VEC> __device__ __forceinline__ void turn_tile(const uint8_t* __restrict__ x, const Tile& p, uint32_t tile) {
     __shared__ __align__(16) float tops[kWarps][kGroup];
     __shared__ __align__(8) uint8_t bytes[kGroup];
@@ -350,25 +350,27 @@ template <bool VEC> __device__ __forceinline__ void turn_tile(const uint8_t* __r
     const int64_t from = (m0 + ty) * p.sx.t + n0 + 8 * tx, to = (m0 + ty) * p.sq.t + n0 + 8 * tx;
     grid_dep_wait();
     grid_dep_launch();
-    // all loads first: none waits for another
-    uint32_t w[kPer][2], e[kPer];   // the row's scale: 2^(e - 127)
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        w[i][0] = w[i][1] = e[i] = 0;
-        if (ty + kLines * i < rows) e[i] = __ldg(p.s_in + (m0 + ty + kLines * i) * p.nb + nb);
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    const auto scale_of = [&](int i) {   // row i's: 2^(e - 127)
+        return ty + kLines * i < rows ? __ldg(p.s_in + (m0 + ty + kLines * i) * p.nb + nb) : 0;
+    };
+    const auto load = [&](int i, uint32_t (&o)[2]) {
         const uint8_t* f = x + from + i * (kLines * p.sx.t);
+        o[0] = o[1] = 0;
         if (ty + kLines * i < rows && (VEC ? count > 0 : count >= 8)) {
             const uint2 v = __ldg(reinterpret_cast<const uint2*>(f));
-            w[i][0] = v.x, w[i][1] = v.y;
+            o[0] = v.x, o[1] = v.y;
         } else if (!VEC && ty + kLines * i < rows) {   // the row's end
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (j < count) w[i][j / 4] |= (uint32_t)__ldg(f + j) << (8 * (j & 3));
+                if (j < count) o[j / 4] |= (uint32_t)__ldg(f + j) << (8 * (j & 3));
         }
-    }
+    };
+    // all loads first: none waits for another
+    uint32_t w[kPer][2], e[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) e[i] = scale_of(i);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) load(i, w[i]);
     bool bad = false;   // what takes the careful way
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -376,38 +378,56 @@ template <bool VEC> __device__ __forceinline__ void turn_tile(const uint8_t* __r
 #pragma unroll
         for (int h = 0; h < 2; ++h) bad |= __vcmpeq4(w[i][h] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
     }
-    // the magnitude of value j of row i
-    const auto value = [&](int i, int j) {
-        const uint32_t k = 8 * (j & 3), v = w[i][j / 4];
-        const uint32_t b = (k < 20 ? v << (20 - k) : v >> (k - 20)) & 0x07f00000u;
-        // 2^120 times the row's scale, as two factors in range
-        const float lift = scale_value(min(e[i] + 120, 254u)), rest = scale_value(max(e[i], 134u) - 7);
-        return b == 0x07f00000u ? __uint_as_float(0x7fffffffu) : __uint_as_float(b) * lift * rest;
+    // A value as a number's bits, with 8 bits of exponent more than an fp32's sign leaves room for: the magnitude's
+    // bits, its exponent moved on by the scale byte.  They order as the values do; what the scales stand for goes up
+    // to 448 * 2^127, and an fp32 maximum rounds up to 2^128.  All ones: NaN, a NaN scale's among them.
+    constexpr uint32_t kNaN = 0xffffffffu;
+    const auto bits = [&](const uint32_t (&v)[2], uint32_t byte, int j) {
+        const uint32_t k = 8 * (j & 3), b = (k < 20 ? v[j / 4] << (20 - k) : v[j / 4] >> (k - 20)) & 0x07f00000u;
+        const uint32_t n = __float_as_uint(__uint_as_float(b) * 0x1p120f) + (byte << 23);
+        return b == 0x07f00000u || byte == 255 ? kNaN : b ? n : 0u;
     };
+    // Reads the rows again, one by one: the other way's registers are its own.
     const auto carefully = [&] {
-        float t[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            t[j] = 0.f;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) t[j] = fmaxf(t[j], value(i, j));
-            t[j] = fmaxf(t[j], __shfl_xor_sync(0xffffffffu, t[j], 16));
-        }
-        if (lane < 16) put_tops(tops, warp, tx, t);
-        __syncthreads();
-        column_scales(p, tops, bytes, mb, n0, cols);
-        column_inverses(bytes, tx, t);
-#pragma unroll
+        uint32_t t[8] = {}, v[2];
+#pragma unroll 1
         for (int i = 0; i < kPer; ++i) {
-            if (ty + kLines * i >= rows) continue;
+            load(i, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t n = bits(v, scale_of(i), j);
+                t[j] = max(t[j], n == kNaN ? 0u : n);
+            }
+        }
+        float most[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) most[j] = __uint_as_float(max(t[j], __shfl_xor_sync(0xffffffffu, t[j], 16)));
+        if (lane < 16) put_tops(tops, warp, tx, most);
+        __syncthreads();
+        if (threadIdx.x < kGroup) {   // as scale_byte, with 127 more in the exponent
+            uint32_t m = 0;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) m = max(m, __float_as_uint(tops[k][threadIdx.x]));
+            bytes[threadIdx.x] = (uint8_t)max((int)(m >> 23) - 135 + ((m & 0x7fffffu) > 0x600000u ? 1 : 0), 0);
+            if (threadIdx.x < cols) p.sc[mb * p.N + n0 + threadIdx.x] = bytes[threadIdx.x];
+        }
+        __syncthreads();
+        const uint2 down = *reinterpret_cast<const uint2*>(bytes + 8 * tx);
+#pragma unroll 1
+        for (int i = 0; i < kPer; ++i) {
+            if (ty + kLines * i >= rows) break;
+            load(i, v);
             uint32_t o[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float v[4];
-                asm volatile("" : "+r"(w[i][h]));   // unpacked anew, as above
+                float f[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = value(i, 4 * h + j);
-                o[h] = e4m3_four<false>(v, pack2(t[4 * h], t[4 * h + 1]), pack2(t[4 * h + 2], t[4 * h + 3])) | (w[i][h] & 0x80808080u);
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t n = bits(v, scale_of(i), 4 * h + j), by = (h ? down.y : down.x) >> (8 * j) & 0xffu;
+                    // below 2^-126 there is no e4m3 number
+                    f[j] = n == kNaN ? __uint_as_float(0x7fffffffu) : n < (by + 1) << 23 ? 0.f : __uint_as_float(n - (by << 23));
+                }
+                o[h] = e4m3_pair<false>(f[0], f[1]) | e4m3_pair<false>(f[2], f[3]) << 16 | (v[h] & 0x80808080u);
             }
             store_eight<VEC>(p.qc + to + i * (kLines * p.sq.t), count, o[0], o[1]);
         }
