@@ -103,8 +103,8 @@ typedef struct mamba2_proj8_shape {
     int32_t flags;   /* 0 */
 } mamba2_proj8_shape;
 
-/* Elements between rows (pitches NULL: ceil(inputs / 16) * 16 for x and w, outputs for y);
- * y also serves dy. */
+/* Elements between rows (pitches NULL: ceil(inputs / 16) * 16 for x and w, outputs for y), at
+ * least a row's length; y also serves dy, whose rows may overlap (0: one row for all tokens). */
 typedef struct mamba2_proj8_pitches {
     int64_t x, w, y;
 } mamba2_proj8_pitches;

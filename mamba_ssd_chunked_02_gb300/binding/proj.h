@@ -54,9 +54,10 @@ void* rows16(const Call& c, PyObject* o, const char* name, const Lead& l, int64_
         raise(PyExc_ValueError, std::string(name) + ": rows of 8-bit values must start on 16-byte boundaries (quant8 lays them out so)");
     return p;
 }
-// The distance between a tensor's tokens where it is the same throughout.
-int64_t pitch_of(const char* name, const Lead& l, const int64_t* st) {
+// The distance between a tensor's tokens where it is the same throughout; at least `width`.
+int64_t pitch_of(const char* name, const Lead& l, const int64_t* st, int64_t width) {
     if (l.b > 1 && l.T > 0 && st[0] != l.T * st[1]) raise(PyExc_ValueError, std::string(name) + ": tokens must lie at even distances");
+    if (l.b * l.T > 1 && st[1] < width) raise(PyExc_ValueError, std::string(name) + ": rows must not overlap each other");
     return st[1];
 }
 void* scales_of(const Call& c, PyObject* o, const char* name, at::IntArrayRef shape, bool written = false) {
@@ -238,11 +239,11 @@ struct Operands {
         N = t->size(0);
         int64_t st[2];
         x = rows16(c, ox, "x", l, l.D, st);
-        p.x = pitch_of("x", l, st);
+        p.x = pitch_of("x", l, st, l.D);
         xs = scales_of(c, oxs, "x_scales", Sizes(l, groups(l.D)));
         const Lead lw{1, N, l.D, true};
         w = rows16(c, ow, "w", lw, l.D, st);
-        p.w = st[1];
+        p.w = pitch_of("w", lw, st, l.D);
         const int64_t nb[2] = {groups(N), groups(l.D)};
         ws = scales_of(c, ows, "w_scales", at::IntArrayRef(nb, 2));
     }
@@ -258,7 +259,7 @@ PyObject* proj8_fwd(Args a) {
     int64_t st[2];
     Out y = token_new(c, a[5], "y", type, o.l, o.N, st);
     mamba2_proj8_pitches p = o.p;
-    p.y = pitch_of("y", o.l, st);
+    p.y = pitch_of("y", o.l, st, o.N);
     const mamba2_proj8_shape sh{o.tokens(), o.l.D, o.N, code(type), 0};
     c.distinct();
     check("mamba2_proj8_fwd", mamba2_proj8_fwd(&sh, &p, (uint8_t*)o.x, (uint8_t*)o.xs, (uint8_t*)o.w, (uint8_t*)o.ws, y.at, on.raw));
@@ -274,7 +275,7 @@ PyObject* proj8_bwd(Args a) {
     int64_t st[2];
     void* dy = token_of(c, a[0], "dy", c.io, o.l, o.N, st);
     mamba2_proj8_pitches p = o.p;
-    p.y = pitch_of("dy", o.l, st);
+    p.y = pitch_of("dy", o.l, st, 0);
     const mamba2_proj8_shape sh{o.tokens(), o.l.D, o.N, c.dtype(), 0};
     Dict g(a[7]);
     void *dx = nullptr, *dw = nullptr;

@@ -54,7 +54,8 @@ struct Proj {
     bool bf16;
 };
 
-bool proj_args(const mamba2_proj8_shape* s, const mamba2_proj8_pitches* p, Proj* a, mamba2_status* e) {
+// back: the pitch of y is that of dy, whose rows are read and may lie in one another.
+bool proj_args(const mamba2_proj8_shape* s, const mamba2_proj8_pitches* p, bool back, Proj* a, mamba2_status* e) {
     *e = MAMBA2_ERR_INVALID_ARG;
     if (!s || s->tokens < 0 || s->inputs < 0 || s->outputs < 0 || s->flags ||
         (s->dtype != MAMBA2_F32 && s->dtype != MAMBA2_BF16))
@@ -67,7 +68,7 @@ bool proj_args(const mamba2_proj8_shape* s, const mamba2_proj8_pitches* p, Proj*
     // a single row's pitch is not used, but the copies' maps want one that could be
     if (a->M <= 1) a->px = up(a->K, 16), a->py = a->N;
     if (a->N <= 1) a->pw = up(a->K, 16);
-    if (a->px < a->K || a->pw < a->K || a->py < a->N || a->px % 16 || a->pw % 16 || a->px >= kMaxStride ||
+    if (a->px < a->K || a->pw < a->K || a->py < (back ? 0 : a->N) || a->px % 16 || a->pw % 16 || a->px >= kMaxStride ||
         a->pw >= kMaxStride || a->py >= kMaxStride)
         return false;
     *e = MAMBA2_OK;
@@ -151,7 +152,7 @@ mamba2_status mamba2_proj8_fwd(const mamba2_proj8_shape* shape, const mamba2_pro
                                void* stream) {
     Proj a;
     mamba2_status e;
-    if (!proj_args(shape, pitches, &a, &e)) return e;
+    if (!proj_args(shape, pitches, false, &a, &e)) return e;
     const int64_t all = a.M * a.N;
     if (!req(x, all, 16) || !req(x_scales, all, 1) || !req(w, all, 16) || !req(w_scales, all, 1) ||
         !req(y, all, a.bf16 ? 2 : 4))
@@ -164,7 +165,7 @@ mamba2_status mamba2_proj8_fwd(const mamba2_proj8_shape* shape, const mamba2_pro
 size_t mamba2_proj8_bwd_workspace_size(const mamba2_proj8_shape* shape) {
     Proj a;
     mamba2_status e;
-    if (!proj_args(shape, nullptr, &a, &e) || a.M == 0 || a.N == 0) return 0;
+    if (!proj_args(shape, nullptr, true, &a, &e) || a.M == 0 || a.N == 0) return 0;
     Quant8Operands w;
     return work_of(a, nullptr, &w);
 }
@@ -174,7 +175,7 @@ mamba2_status mamba2_proj8_bwd(const mamba2_proj8_shape* shape, const mamba2_pro
                                void* dx, float* dw, void* workspace, size_t workspace_bytes, void* stream) {
     Proj a;
     mamba2_status e;
-    if (!proj_args(shape, pitches, &a, &e)) return e;
+    if (!proj_args(shape, pitches, true, &a, &e)) return e;
     const int64_t all = a.M * a.N, es = a.bf16 ? 2 : 4;
     if (!req(dy, all, es) || !req(x, all, 16) || !req(x_scales, all, 1) || !req(w, all, 16) || !req(w_scales, all, 1) ||
         !opt(dx, es) || !opt(dw, 4))

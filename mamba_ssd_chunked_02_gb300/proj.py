@@ -8,7 +8,9 @@ contiguous.  Values in 8 bits are a pair: q (torch.float8_e4m3fn) and its scales
 (torch.float8_e8m0fnu, contiguous), one for each 128 values of a row ("row": [.., ceil(D/128)])
 or for each block of 128 x 128 ("block": [ceil(N/128), ceil(K/128)]); they stand for q times
 scale.  Rows of q start on 16-byte boundaries: what these functions return does, as a slice of
-rows padded to 16 where D is not a multiple of 16.
+rows padded to 16 where D is not a multiple of 16.  The tokens of the product's x, y and dy lie at
+one distance throughout (sequences cut out of longer ones do not), those of x and y not within one
+another; the other operators take any distances, and read tokens that share memory in place.
 
 Tensors live on the current CUDA device; everything runs on `stream` (default: the current
 stream), on which the tensors have to be ready.  Outputs and workspaces are allocated with torch
