@@ -2,11 +2,16 @@
 ahead in turn, sums in turn, dw added up over rows; at widths of each form (one and two units a
 thread, teams of a warp and of a block, wide rows that are read again), for each pair of types.
 Bounds as in test_proj_gpu.py."""
+import ctypes
+import sys
+import threading
+
 import pytest
 import torch
 
 import mamba_ssd_chunked_02_gb300 as m2
 import proj_ref as R
+from mamba_ssd_chunked_02_gb300 import proj as L
 from test_proj_gpu import BF16, F32, Gen, close, f64
 
 pytestmark = pytest.mark.gpu
@@ -54,3 +59,55 @@ def test_many_rows_at_uneven_distances(D, T, dt, rt):
     close(g["dx"], dx, "dx", size)
     close(g["dresidual"], dx, "dresidual", size)
     close(g["dw"], dw, "dw")
+
+
+def test_two_widths_from_two_threads_at_once():
+    """Two sizes of one form of the kernel, which ask for different amounts of shared memory, called
+    through the C ABI from two threads without a pause: ctypes lets the other thread run during a
+    call, so that calls of both sizes are under way at once.  Every call has its own output; the
+    status and the results of all of them are looked at."""
+    vp = ctypes.c_void_p
+    f = ctypes.CFUNCTYPE(ctypes.c_int, *[vp] * 10, ctypes.c_size_t, vp)(("mamba2_add_norm_bwd", m2.load()))
+    rows, rounds, calls, sizes = 24, 40, 100, (2560, 8192)
+    bad, state = [], {}
+    for D in sizes:
+        r = Gen(60 + D)
+        ins = [r.randn(rows, D).cuda(), r.randn(D).cuda(), r.randn(rows, D).cuda(), r.randn(rows, D).cuda()]
+        want = m2.add_norm_bwd(*ins)
+        shape = L.AddNormShape(1, rows, D, 1e-5, m2.F32, m2.F32, 0)
+        space = torch.empty(m2.add_norm_bwd_workspace_size(shape), dtype=torch.uint8, device="cuda")
+        dx, dw = torch.empty(calls, rows, D, device="cuda"), torch.empty(calls, D, device="cuda")
+        wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+        stream = torch.cuda.Stream()
+        args = [[vp(ctypes.addressof(shape)), None, *(vp(t.data_ptr()) for t in ins), vp(dx[k].data_ptr()), None,
+                 vp(dw[k].data_ptr()), vp(space.data_ptr()), space.nbytes, vp(stream.cuda_stream)] for k in range(calls)]
+        state[D] = shape, ins, want, space, dx, dw, wrong, stream, args
+    torch.cuda.synchronize()
+
+    def work(D):
+        _, _, want, _, dx, dw, wrong, stream, args = state[D]
+        try:
+            with torch.cuda.stream(stream):
+                for _ in range(rounds):
+                    dx.zero_()
+                    dw.zero_()
+                    status = [f(*a) for a in args]
+                    assert not any(status), status
+                    wrong.add_((dx != want["dx"]).sum() + (dw != want["dw"]).sum())
+                    stream.synchronize()
+        except BaseException as e:
+            bad.append(e)
+
+    old = sys.getswitchinterval()
+    sys.setswitchinterval(1e-5)
+    try:
+        threads = [threading.Thread(target=work, args=(D,)) for D in sizes]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(old)
+    torch.cuda.synchronize()
+    assert not bad, bad
+    assert all(state[D][6].item() == 0 for D in sizes)
