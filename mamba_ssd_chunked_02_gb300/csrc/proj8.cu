@@ -116,8 +116,11 @@ __device__ __forceinline__ uint32_t of_block(const void* p, uint32_t rank) {
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// The same where nothing written is handed over (tensor memory has been read): the release above waits
-// for the thread's stores, copies out among them, some 2000 cycles.
+// The same where tensor memory has been read and is given back: nothing is written that the waiter reads, and what
+// orders the reads before the other block's later products are tcgen05.wait::ld, tcgen05.fence::before_thread_sync in
+// front of the arrival and ::after_thread_sync behind the wait, which hold with a relaxed arrival; its scope, like that
+// of the waits in proj8_kernel, is the cluster's.  The release above waits for the thread's stores, copies out among
+// them, some 2000 cycles.
 __device__ __forceinline__ void arrive_read_at(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -299,7 +302,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             place(tile, &r, &c);
             const int r0 = row_of(r), c0 = c * BN + rank * C::HALF;
             for (int kb = from_k; kb < to_k; ++kb, ++it) {
-                ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.empty[st], phase, abort, kWaitNs));
+                ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.empty[st], phase, abort, kWaitNs));
                 if (!ok) break;
                 if (elected()) {
                     uint8_t* a = smem + st * C::STAGE;
@@ -317,7 +320,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         if (!ok && lane == 0) {   // copies in flight land before the block ends
             if (rank == 0)
                 for (int i = it - 1; i >= 0 && i >= it - C::NS; --i)
-                    mbar_wait(&bars.full[i % C::NS], i / C::NS & 1, kWaitNs);
+                    mbar_wait<true>(&bars.full[i % C::NS], i / C::NS & 1, kWaitNs);
             else   // counted at the other block's barriers: a wait ran out long after the last was issued
                 for (int i = 0; i < 1000; ++i) __nanosleep(1000);
         }
@@ -336,16 +339,16 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             for (int tile = first; tile < q.tiles && ok; tile += step)
                 for (int k0 = from_k; k0 < to_k && ok; k0 += q.chunk, ++t) {
                     const int acc = t & 1, k1 = min(to_k, k0 + q.chunk);
-                    ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.acc_empty[acc], (t / 2 & 1) ^ 1, abort, kWaitNs));
+                    ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.acc_empty[acc], (t / 2 & 1) ^ 1, abort, kWaitNs));
                     if (C::SHARED && ok && t > 0)
-                        ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.acc_shared, (t - 1) & 1, abort, kWaitNs));
+                        ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.acc_shared, (t - 1) & 1, abort, kWaitNs));
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t d = tmem + acc * C::ACC;
                     bool there = false;   // the next stage's operands, asked for ahead
                     for (int kb = k0; kb < k1 && ok; kb += 4) {
                         const uint32_t ta = tmem + C::SF_COL + sf * C::SF_COLS;
-                        ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.sf_full[sf], sf_phase, abort, kWaitNs));
+                        ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.sf_full[sf], sf_phase, abort, kWaitNs));
                         if (!ok) break;
                         tc_fence_after();
                         if (elected()) {
@@ -358,14 +361,14 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                         for (int i = 0; i < 4; ++i) {
                             if (kb + i >= k1) break;
                             if (!there) {
-                                ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.full[st], phase, abort, kWaitNs));
+                                ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.full[st], phase, abort, kWaitNs));
                                 if (!ok) break;
                             }
                             tc_fence_after();
                             const int now = st;
                             if (++st == C::NS) st = 0, phase ^= 1;
                             const bool last = kb + i + 1 == k1;
-                            there = !last && mbar_test_wait(smem_u32(&bars.full[st]), phase);
+                            there = !last && mbar_test_wait<true>(smem_u32(&bars.full[st]), phase);
                             if (elected()) {
                                 const uint32_t at = now * (C::STAGE >> 4);
 #pragma unroll
@@ -429,7 +432,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 uint4 w[C::SFB];
 #pragma unroll
                 for (int h = 0; h < C::SFB; ++h) w[h] = next[u][h];
-                ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.sf_empty[sf], phase, abort, kWaitNs));
+                ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.sf_empty[sf], phase, abort, kWaitNs));
                 if (!ok) break;
                 uint4* to = reinterpret_cast<uint4*>(ssf + sf * C::SF_BYTES) + (warp == 2 ? 0 : 32) + lane;
 #pragma unroll
@@ -462,7 +465,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         int t = 0;
         for (int k0 = from_k; k0 < to_k; k0 += q.chunk, ++t) {
             const int acc = t & 1;
-            ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.acc_full[acc], t / 2 & 1, abort, kWaitNs));
+            ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.acc_full[acc], t / 2 & 1, abort, kWaitNs));
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -490,7 +493,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             place(tile, &rt, &ct);
             for (int k0 = 0; k0 < q.kb; k0 += q.chunk, ++t) {
                 const int acc = t & 1;
-                ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.acc_full[acc], t / 2 & 1, abort, kWaitNs));
+                ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.acc_full[acc], t / 2 & 1, abort, kWaitNs));
                 if (!ok) break;
                 tc_fence_after();
                 const int r0 = row_of(rt) + quad * 32, c0 = ct * BN;

@@ -3,9 +3,10 @@
 // and stores, and the shared-memory / instruction descriptors they take.
 //
 // Conventions used by the kernels of this library:
-//   * One CTA forms its own cluster (no cluster launch), so shared::cluster
-//     addresses are this CTA's shared::cta addresses.
-//   * Operand tiles are bf16, 128-byte swizzled, written by TMA into 1024-byte
+//   * One CTA forms its own cluster, so shared::cluster addresses are this CTA's
+//     shared::cta addresses, unless the kernel says otherwise (proj8.cu launches
+//     clusters, and has its own forms of what reaches another block).
+//   * Operand tiles are bf16 (proj8.cu: e4m3), 128-byte swizzled, written by TMA into 1024-byte
 //     aligned shared memory.  "K-major": the reduction index is contiguous
 //     (a 128-byte row holds 64 consecutive k of one m/n).  "MN-major": m or n
 //     is contiguous (a 128-byte row holds 64 consecutive m/n of one k).
@@ -48,53 +49,82 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
+// CLUSTER: a barrier at which another block of the cluster arrives, so that the wait's scope is
+// the cluster's (the block's else).
+template <bool CLUSTER = false> __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
     return ok != 0;
 }
 // Non-blocking probe: true when the phase with the given parity has completed.
 // (try_wait may suspend the thread for a while before it returns false; a loop
 // that polls several barriers in turn needs this form.)
-__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+template <bool CLUSTER = false> __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
     return ok != 0;
 }
 // try_wait with a suspend-time hint: the thread sleeps in hardware until the
 // phase completes or about `hint_ns` pass, so a waiting warp does not spin
 // and steal issue slots from the warps doing the work.
-__device__ __forceinline__ bool mbar_try_wait_sleep(uint32_t bar, uint32_t parity, uint32_t hint_ns) {
+template <bool CLUSTER = false> __device__ __forceinline__ bool mbar_try_wait_sleep(uint32_t bar, uint32_t parity, uint32_t hint_ns) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(hint_ns)
-        : "memory");
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(hint_ns)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(hint_ns)
+            : "memory");
     return ok != 0;
 }
 constexpr uint32_t kSuspendHintNs = 1000;
 
 // Wait for the phase with the given parity to complete, for at most limit_ns.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+template <bool CLUSTER = false> __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
     const uint32_t a = smem_u32(bar);
-    if (mbar_try_wait(a, parity)) return true;
+    if (mbar_try_wait<CLUSTER>(a, parity)) return true;
     const uint64_t t0 = globaltimer();
-    while (!mbar_try_wait_sleep(a, parity, kSuspendHintNs)) {
+    while (!mbar_try_wait_sleep<CLUSTER>(a, parity, kSuspendHintNs)) {
         if (globaltimer() - t0 > limit_ns) return false;
     }
     return true;
@@ -103,12 +133,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
 // Wait like mbar_wait, but also give up as soon as *abort becomes nonzero (a
 // shared-memory flag another role of the CTA raised after its own timeout); a
 // timeout raises *abort.  Returns true only when the phase completed.
-__device__ __forceinline__ bool mbar_wait_or_abort(uint64_t* bar, uint32_t parity,
-                                                   volatile int* abort, uint64_t limit_ns) {
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool mbar_wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
     const uint32_t a = smem_u32(bar);
-    if (mbar_try_wait(a, parity)) return true;
+    if (mbar_try_wait<CLUSTER>(a, parity)) return true;
     const uint64_t t0 = globaltimer();
-    while (!mbar_try_wait_sleep(a, parity, kSuspendHintNs)) {
+    while (!mbar_try_wait_sleep<CLUSTER>(a, parity, kSuspendHintNs)) {
         if (*abort) return false;
         if (globaltimer() - t0 > limit_ns) {
             *abort = 1;
