@@ -95,8 +95,12 @@ MAMBA2_API mamba2_status mamba2_quant8(const mamba2_quant8_shape* shape,
  * x [tokens, inputs] e4m3 in row groups, w [outputs, inputs] e4m3 in block groups, sums in
  * fp32 on the tensor cores, y io.  Few tokens, and few tiles with long sums, split the sum
  * over a cluster of blocks (joined in a fixed order).  inputs >= 1; every size at most 2^30.
- * Waits in the kernels end after two seconds: one that runs out sets
- * MAMBA2_DEVERR_TIMEOUT_PROJ8 in the word of mamba2_ssd_device_error, and the result is void. */
+ * A wait for a copy, a product or another warp's work ends after two seconds: one that runs out
+ * sets MAMBA2_DEVERR_TIMEOUT_PROJ8 in the word of mamba2_ssd_device_error, and the result is void.  A
+ * cluster of blocks that comes to a stop so ends within six: those that wait for the one that gave up
+ * take two more, what is in flight two at most.  (No limit of their own have the barriers at which a
+ * cluster's blocks meet, which these waits lead to, the wait for the kernel before, and that for
+ * tensor memory, which another stream's kernels may hold.) */
 typedef struct mamba2_proj8_shape {
     int64_t tokens, inputs, outputs;
     int32_t dtype;   /* mamba2_dtype of y, dy and dx */
@@ -114,6 +118,16 @@ MAMBA2_API mamba2_status mamba2_proj8_fwd(const mamba2_proj8_shape* shape,
                                           const uint8_t* x, const uint8_t* x_scales,
                                           const uint8_t* w, const uint8_t* w_scales,
                                           void* y, void* stream);
+
+/* Diagnostic: the failure path of these waits, without a fault.  Runs mamba2_proj8_fwd on tensors of
+ * the default pitches with waits of `limit_us` microseconds (1 .. 100000), while one block of each
+ * cluster keeps its scales back, for which the others then wait in vain.  The kernel returns
+ * normally and the context stays usable; afterwards MAMBA2_DEVERR_TIMEOUT_PROJ8 is set, and y is
+ * as it was. */
+MAMBA2_API mamba2_status mamba2_proj8_selftest_timeout(const mamba2_proj8_shape* shape,
+                                                       const uint8_t* x, const uint8_t* x_scales,
+                                                       const uint8_t* w, const uint8_t* w_scales,
+                                                       void* y, uint32_t limit_us, void* stream);
 
 /* Gradients for dL/dy = dy [tokens, outputs] io: dx [tokens, inputs] io and dw [outputs,
  * inputs] fp32, contiguous; either may be NULL (not wanted).  Both products are taken in 8 bits:

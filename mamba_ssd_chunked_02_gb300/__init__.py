@@ -24,7 +24,7 @@ Around a layer's projections (module proj, C ABI in include/mamba2_proj.h):
   add_norm_fwd, add_norm_bwd (norm of the sum with the residual, in 8 bits if wanted),
   quant8 (values to e4m3 with power-of-two scales), proj8_fwd, proj8_bwd (matrix product
   of such values); add_norm_bwd_workspace_size, proj8_bwd_workspace_size (of an
-  AddNormShape, Proj8Shape).
+  AddNormShape, Proj8Shape), proj8_selftest_timeout.
 
 Pages: "NVIDIA CUDA Tile로 Mamba-2 순방향 전달 커널 가속화" (devin.kr),
 "Mamba-2 아키텍처의 핵심 연산" (y_t = c_t^T h_t + D x_t) and "세 가지 핵심 커널
@@ -543,4 +543,4 @@ from .layer import (ConvShape, NormShape, ScanShape, conv_bwd, conv_bwd_workspac
                     conv_fwd, conv_step, norm_bwd, norm_bwd_workspace_size, norm_fwd, scan_bwd,
                     scan_bwd_workspace_size, scan_fwd, scan_selftest_turn_timeout, scan_step, scan_workspace_size)
 from .proj import (AddNormShape, Proj8Shape, add_norm_bwd, add_norm_bwd_workspace_size, add_norm_fwd,  # noqa: E402,F401
-                   proj8_bwd, proj8_bwd_workspace_size, proj8_fwd, quant8)
+                   proj8_bwd, proj8_bwd_workspace_size, proj8_fwd, proj8_selftest_timeout, quant8)

@@ -190,8 +190,14 @@ struct Operand {
     int64_t rs, ks;
     int shift;
 };
+// How long the product's kernels wait at a barrier; withhold: a self-test, in which one block of each cluster keeps its
+// scales back.
+struct Proj8Watch {
+    uint64_t limit_ns = 2000000000ull;   // 2 s: far beyond any legitimate wait
+    bool withhold = false;
+};
 // out[i * ldo + j] = sum_k A[i, k] B[j, k], i < R, j < C, in bf16 or fp32.
 cudaError_t launch_proj8(const Operand& A, const Operand& B, int64_t R, int64_t C, int64_t depth, void* out,
-                         int64_t ldo, bool bf16, cudaStream_t st);
+                         int64_t ldo, bool bf16, cudaStream_t st, const Proj8Watch& watch = {});
 
 }  // namespace m2

@@ -36,7 +36,6 @@ namespace {
 
 using namespace tc;
 
-constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s: far beyond any legitimate wait
 constexpr int kThreads = 416;
 constexpr int kDevices = 64;
 // Columns of tiles a panel (32768 x 2560 x 10576: 8 528 us, 12 516, 16 511, 24 506, all 48 513; 16384 x 8192 x
@@ -137,6 +136,29 @@ __device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* m, const vo
                  "r"(smem_u32(src)), "r"(x), "r"(y)
                  : "memory");
 }
+// Where a wait has run out in this block, every block of the cluster is told so: before the barrier at which they
+// all meet, so that behind it all know.
+__device__ __forceinline__ void tell_abort(int* abort, int lane, uint32_t blocks) {
+    if (lane == 0 && *reinterpret_cast<volatile int*>(abort))
+        for (uint32_t r = 0; r < blocks; ++r) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(of_block(abort, r)), "r"(1) : "memory");
+}
+// Behind a wait that ran out and the barrier that told all of it, by all threads: waits until the copies that this
+// block's barriers count, the last of each stage, have landed, at most limit_ns for all of them.  A copy whose bytes are
+// not yet expected there, and a product that no one waits for any more, end within microseconds; the block stays for a
+// thousand.
+template <bool CLUSTER>
+__device__ __forceinline__ void give_up(uint64_t* full, int issued, int stages, uint64_t limit_ns, int32_t* err) {
+    if (threadIdx.x == 0) {
+        record_error(err, kErrTimeoutProj8);
+        const uint64_t t0 = globaltimer();
+        for (int i = issued - 1; i >= 0 && i >= issued - stages; --i) {
+            const uint64_t gone = globaltimer() - t0;
+            if (!mbar_wait<CLUSTER>(&full[i % stages], i / stages & 1, gone < limit_ns ? limit_ns - gone : 0)) break;
+        }
+    }
+    __nanosleep(1000000);
+    __syncwarp();
+}
 // One lane of a warp that is whole.
 __device__ __forceinline__ bool elected() {
     uint32_t p;
@@ -167,6 +189,7 @@ struct Shape {
     bool copied;           // the result's rows are whole 16 bytes, and start there
     int64_t ldo;
     int split, share;      // pairs of a tile, contracted blocks of each
+    Proj8Watch watch;
 };
 
 // A pair's tile of 256 x BN: a block has 128 rows of A and BN / 2 columns of B.
@@ -284,6 +307,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     tc_fence_after();
     const uint32_t tmem = bars.tmem;
     grid_dep_wait();   // what is read was written by the kernel before
+    int issued = 0;    // copies' stages that warp 0 asked for
     [[maybe_unused]] float sum[SPLIT ? 64 : 1] = {};   // of a row, 64 columns: a warp's of the pair's share
     // The producing and the issuing warp run whole, with one lane elected for each instruction: what
     // the loop counts then stays in uniform registers, where the copies and products take it from
@@ -302,7 +326,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             place(tile, &r, &c);
             const int r0 = row_of(r), c0 = c * BN + rank * C::HALF;
             for (int kb = from_k; kb < to_k; ++kb, ++it) {
-                ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.empty[st], phase, abort, kWaitNs));
+                ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.empty[st], phase, abort, q.watch.limit_ns));
                 if (!ok) break;
                 if (elected()) {
                     uint8_t* a = smem + st * C::STAGE;
@@ -317,13 +341,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             }
         }
         grid_dep_launch();   // all copies are asked for: the next kernel may set itself up as blocks end
-        if (!ok && lane == 0) {   // copies in flight land before the block ends
-            if (rank == 0)
-                for (int i = it - 1; i >= 0 && i >= it - C::NS; --i)
-                    mbar_wait<true>(&bars.full[i % C::NS], i / C::NS & 1, kWaitNs);
-            else   // counted at the other block's barriers: a wait ran out long after the last was issued
-                for (int i = 0; i < 1000; ++i) __nanosleep(1000);
-        }
+        issued = it;
     } else if (warp == 1) {
         if (rank == 0) {
             constexpr uint32_t idesc = idesc_mx(kRows, BN, A_MN, B_MN);
@@ -339,16 +357,16 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             for (int tile = first; tile < q.tiles && ok; tile += step)
                 for (int k0 = from_k; k0 < to_k && ok; k0 += q.chunk, ++t) {
                     const int acc = t & 1, k1 = min(to_k, k0 + q.chunk);
-                    ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.acc_empty[acc], (t / 2 & 1) ^ 1, abort, kWaitNs));
+                    ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.acc_empty[acc], (t / 2 & 1) ^ 1, abort, q.watch.limit_ns));
                     if (C::SHARED && ok && t > 0)
-                        ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.acc_shared, (t - 1) & 1, abort, kWaitNs));
+                        ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.acc_shared, (t - 1) & 1, abort, q.watch.limit_ns));
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t d = tmem + acc * C::ACC;
                     bool there = false;   // the next stage's operands, asked for ahead
                     for (int kb = k0; kb < k1 && ok; kb += 4) {
                         const uint32_t ta = tmem + C::SF_COL + sf * C::SF_COLS;
-                        ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.sf_full[sf], sf_phase, abort, kWaitNs));
+                        ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.sf_full[sf], sf_phase, abort, q.watch.limit_ns));
                         if (!ok) break;
                         tc_fence_after();
                         if (elected()) {
@@ -361,7 +379,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                         for (int i = 0; i < 4; ++i) {
                             if (kb + i >= k1) break;
                             if (!there) {
-                                ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.full[st], phase, abort, kWaitNs));
+                                ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.full[st], phase, abort, q.watch.limit_ns));
                                 if (!ok) break;
                             }
                             tc_fence_after();
@@ -386,7 +404,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 }
             if (!ok && elected()) {
                 commit<PAIR>(&bars.drain, 1u << even);
-                mbar_wait(&bars.drain, 0, kWaitNs);
+                mbar_wait(&bars.drain, 0, q.watch.limit_ns);
             }
         }
     } else if (warp < 4) {
@@ -432,7 +450,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 uint4 w[C::SFB];
 #pragma unroll
                 for (int h = 0; h < C::SFB; ++h) w[h] = next[u][h];
-                ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.sf_empty[sf], phase, abort, kWaitNs));
+                ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.sf_empty[sf], phase, abort, q.watch.limit_ns));
                 if (!ok) break;
                 uint4* to = reinterpret_cast<uint4*>(ssf + sf * C::SF_BYTES) + (warp == 2 ? 0 : 32) + lane;
 #pragma unroll
@@ -451,9 +469,10 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         if (lane == 0) {
             const uint32_t full0 = of_block(&bars.sf_full[0], even);
             int left = first < q.tiles ? ((q.tiles - 1 - first) / step + 1) * ((to_k - from_k + 3) / 4) : 0;
+            if (q.watch.withhold && in_cluster == 1) left = 0;
             int sf = 0;
             for (uint32_t phase = 0; left > 0; --left) {
-                if (!mbar_wait_or_abort(&bars.sf_there[sf], phase, abort, kWaitNs)) break;
+                if (!mbar_wait_or_abort(&bars.sf_there[sf], phase, abort, q.watch.limit_ns)) break;
                 fence_proxy_async_smem();
                 arrive_at(full0 + 8 * sf);
                 if (++sf == C::NSF) sf = 0, phase ^= 1;
@@ -465,7 +484,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         int t = 0;
         for (int k0 = from_k; k0 < to_k; k0 += q.chunk, ++t) {
             const int acc = t & 1;
-            ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.acc_full[acc], t / 2 & 1, abort, kWaitNs));
+            ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.acc_full[acc], t / 2 & 1, abort, q.watch.limit_ns));
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -493,7 +512,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             place(tile, &rt, &ct);
             for (int k0 = 0; k0 < q.kb; k0 += q.chunk, ++t) {
                 const int acc = t & 1;
-                ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.acc_full[acc], t / 2 & 1, abort, kWaitNs));
+                ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.acc_full[acc], t / 2 & 1, abort, q.watch.limit_ns));
                 if (!ok) break;
                 tc_fence_after();
                 const int r0 = row_of(rt) + quad * 32, c0 = ct * BN;
@@ -576,8 +595,15 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         if (elected()) bulk_wait<0>();   // copies out of this block's shared memory
     }
     __syncwarp();
+    tell_abort(&bars.abort, lane, SPLIT ? 2 * q.split : 2);
+    __syncwarp();
     tc_fence_before();
     cluster_sync();
+    if (*abort) {
+        // the even block's barriers count both blocks' copies
+        give_up<true>(bars.full, rank == 0 ? issued : 0, C::NS, q.watch.limit_ns, err);
+        cluster_sync();
+    }
     if constexpr (SPLIT) {
         // Every pair is done with its operands, whose room takes the shares' sums: a block owns BN / split
         // of its 128 rows' columns, gets them from the blocks of its half of the rows, and adds them in the
@@ -587,7 +613,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         constexpr int P = BM + 1;
         const int own = BN / q.split, fours = own / 4, tid = threadIdx.x - 128;   // powers of two
         float4* join = reinterpret_cast<float4*>(smem);   // [pair][four][row]
-        if (warp >= 4 && warp < 12) {
+        if (warp >= 4 && warp < 12 && !*abort) {
             const int row = (warp & 3) * 32 + lane, c0 = 64 * ((warp - 4) >> 2);
 #pragma unroll
             for (int g = 0; g < 4; ++g) {   // sixteen columns have one owner
@@ -632,7 +658,6 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 }
         }
     }
-    if (threadIdx.x == 0 && *abort) record_error(err, kErrTimeoutProj8);
     if (warp == 1) {
         tc_fence_after();
         free_tmem<PAIR>(tmem, C::COLS);
@@ -674,6 +699,7 @@ struct FewShape {
     int R, C, kb;     // lanes' rows, few rows, contracted blocks
     int ns;           // stages
     int64_t ldo;
+    Proj8Watch watch;
 };
 
 template <int BN, bool A_MN, typename TO>
@@ -688,7 +714,7 @@ proj8_few_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     uint8_t* ssf = smem + ns * STAGE;
     float* join = reinterpret_cast<float*>(ssf + C::SETS * C::SF_BYTES);   // [block][own column][128]
     struct FewBars {
-        uint64_t full[kFewStages], empty[kFewStages], sf_full, acc_full;
+        uint64_t full[kFewStages], empty[kFewStages], sf_full, acc_full, drain;
         uint32_t tmem;
         int abort;
     };
@@ -730,6 +756,7 @@ proj8_few_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
         if (lane == 0) {
             mbar_init(&bars.sf_full, 128);
             mbar_init(&bars.acc_full, 1);
+            mbar_init(&bars.drain, 1);
             bars.abort = 0;
         }
         fence_barrier_init();
@@ -743,13 +770,14 @@ proj8_few_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     const uint32_t tmem = bars.tmem;
     if (split > 1) cluster_arrive();   // this block has begun
     bool ok = true;
+    int issued = 0;   // copies' stages that warp 0 asked for
 
     if (warp == 0) {
         grid_dep_wait();     // what is read was written by the kernel before
         grid_dep_launch();   // the next one may set itself up beside this one
         int st = 0, it = 0;
         for (uint32_t phase = 1; it < n; ++it) {
-            ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.empty[st], phase, abort, kWaitNs));
+            ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.empty[st], phase, abort, q.watch.limit_ns));
             if (!ok) break;
             if (elected()) {
                 const int k = (k0 + it) * BK;
@@ -761,20 +789,19 @@ proj8_few_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
             __syncwarp();
             if (++st == ns) st = 0, phase ^= 1;
         }
-        if (!ok && lane == 0)   // copies in flight land before the block ends
-            for (int i = it - 1; i >= 0 && i >= it - ns; --i) mbar_wait(&bars.full[i % ns], i / ns & 1, kWaitNs);
+        issued = it;
     } else if (warp == 1) {
         constexpr uint32_t idesc = idesc_mx(BM, BN, A_MN, 0);
         constexpr uint32_t a_step = (A_MN ? 32 * 128 : 32) >> 4, b_step = 32 >> 4;
         const uint64_t a0 = smem_desc_sw128(smem_u32(smem), A_MN ? 128 * BK : 16, 1024);
         const uint64_t b0 = smem_desc_sw128(smem_u32(smem) + C::A_BYTES, 16, 1024);
         const uint64_t s0 = scale_desc(smem_u32(ssf));
-        ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.sf_full, 0, abort, kWaitNs));
+        ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.sf_full, 0, abort, q.watch.limit_ns));
         tc_fence_after();
         int st = 0;
         uint32_t phase = 0;
         for (int i = 0; i < n && ok; ++i) {
-            ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.full[st], phase, abort, kWaitNs));
+            ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.full[st], phase, abort, q.watch.limit_ns));
             if (!ok) break;
             tc_fence_after();
             if (elected()) {
@@ -794,8 +821,8 @@ proj8_few_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
             if (++st == ns) st = 0, phase ^= 1;
         }
         if (!ok && elected()) {   // products in flight are done before the block ends
-            commit<false>(&bars.acc_full);
-            mbar_wait(&bars.acc_full, 0, kWaitNs);
+            commit<false>(&bars.drain);
+            mbar_wait(&bars.drain, 0, q.watch.limit_ns);
         }
     }
     const int quad = warp & 3, row = quad * 32 + lane;   // of the tile, where the warp is an epilogue's
@@ -809,8 +836,8 @@ proj8_few_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
             to[32] = sets[1];
         }
         fence_proxy_async_smem();
-        mbar_arrive(&bars.sf_full);
-        ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.acc_full, 0, abort, kWaitNs));
+        if (!(q.watch.withhold && rank == 0 && warp == 2)) mbar_arrive(&bars.sf_full);
+        ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars.acc_full, 0, abort, q.watch.limit_ns));
         tc_fence_after();
         if (split > 1) cluster_wait();   // the others have begun
         const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16);
@@ -839,6 +866,8 @@ proj8_few_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
         cluster_wait();
     }
     __syncwarp();
+    if (split > 1) tell_abort(&bars.abort, lane, split);
+    __syncwarp();
     tc_fence_before();
     if (split > 1) {
         cluster_sync();   // the parts are there
@@ -858,7 +887,7 @@ proj8_few_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     } else {
         __syncthreads();
     }
-    if (threadIdx.x == 0 && *abort) record_error(err, kErrTimeoutProj8);
+    if (*abort) give_up<false>(bars.full, issued, ns, q.watch.limit_ns, err);
     if (warp == 1) {
         tc_fence_after();
         free_tmem<false>(tmem, C::COLS);
@@ -934,7 +963,7 @@ template <bool A_MN, bool B_MN, typename TO> int split_clusters(int split) {
 
 template <int BN, bool A_MN, bool B_MN, typename TO, bool SPLIT = false>
 cudaError_t go(const Operand& A, const Operand& B, int64_t R, int64_t Cn, int64_t depth, TO* out, int64_t ldo,
-               cudaStream_t st, int split = 1) {
+               const Proj8Watch& watch, cudaStream_t st, int split = 1) {
     using C = Cfg<BN, B_MN, sizeof(TO)>;
     CUtensorMap ma, mb, mo, mh;
     if (!map_of(&ma, A, R, depth, 128) || !map_of(&mb, B, Cn, depth, B_MN ? BK : C::HALF))
@@ -955,7 +984,8 @@ cudaError_t go(const Operand& A, const Operand& B, int64_t R, int64_t Cn, int64_
     if (tiles >= (int64_t(1) << 30)) return kGridLimit;
     const int kb = (int)((depth + BK - 1) / BK);
     if ((int64_t)(split - 1) * share_of(kb, split) >= kb) return cudaErrorInvalidValue;   // a pair without blocks
-    const Shape q{(int)R, (int)Cn, kb, (int)tr, (int)tiles, kPanel, sizeof(TO) == 4 ? kChunk : kb, copied, ldo, split, share_of(kb, split)};
+    const Shape q{(int)R, (int)Cn, kb, (int)tr, (int)tiles, kPanel, sizeof(TO) == 4 ? kChunk : kb, copied, ldo, split, share_of(kb, split),
+                  watch};
     const Scales sa = scales_of(A, R, kb), sb = scales_of(B, Cn, kb);
     auto k = proj8_kernel<BN, A_MN, B_MN, TO, SPLIT>;
     static std::atomic<uint64_t> done;
@@ -972,13 +1002,13 @@ cudaError_t go(const Operand& A, const Operand& B, int64_t R, int64_t Cn, int64_
 // A's rows to the lanes, B's few to the columns: out[j * ldo + i].
 template <int BN, bool A_MN, typename TO>
 cudaError_t go_few(const Operand& A, const Operand& B, int64_t R, int64_t Cn, int64_t depth, TO* out, int64_t ldo,
-                   cudaStream_t st) {
+                   const Proj8Watch& watch, cudaStream_t st) {
     using C = Few<BN>;
     CUtensorMap ma, mb;
     if (!map_of(&ma, A, R, depth, 128) || !map_of(&mb, B, Cn, depth, BN)) return cudaErrorInvalidValue;
     const int64_t tr = (R + BM - 1) / BM, tc = (Cn + BN - 1) / BN;
     if (tr * 8 >= (int64_t(1) << 31) || tc > 65535) return kGridLimit;
-    FewShape q{(int)R, (int)Cn, (int)((depth + BK - 1) / BK), 0, ldo};
+    FewShape q{(int)R, (int)Cn, (int)((depth + BK - 1) / BK), 0, ldo, watch};
     auto k = proj8_few_kernel<BN, A_MN, TO>;
     constexpr int most = 226 * 1024;
     static std::atomic<uint64_t> done;
@@ -1009,12 +1039,12 @@ bool few(int64_t R, int64_t depth) { return R <= kFewRows && (depth + BK - 1) / 
 
 template <bool A_MN, bool B_MN, typename TO>
 cudaError_t pick(const Operand& A, const Operand& B, int64_t R, int64_t C, int64_t depth, TO* out, int64_t ldo,
-                 cudaStream_t st) {
+                 const Proj8Watch& watch, cudaStream_t st) {
     if constexpr (!A_MN)
         if (few(R, depth))
-            return R <= 16   ? go_few<16, B_MN, TO>(B, A, C, R, depth, out, ldo, st)
-                   : R <= 32 ? go_few<32, B_MN, TO>(B, A, C, R, depth, out, ldo, st)
-                             : go_few<64, B_MN, TO>(B, A, C, R, depth, out, ldo, st);
+            return R <= 16   ? go_few<16, B_MN, TO>(B, A, C, R, depth, out, ldo, watch, st)
+                   : R <= 32 ? go_few<32, B_MN, TO>(B, A, C, R, depth, out, ldo, watch, st)
+                             : go_few<64, B_MN, TO>(B, A, C, R, depth, out, ldo, watch, st);
     // Tiles of 224 columns, whose two accumulators lie apart; of 256 where B is MN-major, so that a
     // block's half of the columns is whole lines of memory (dx of 32768 x 10576 x 2560: 676 us at 224, of
     // which half the rows of a copy lie across two lines); of 128 where the pairs' rounds come out
@@ -1036,27 +1066,27 @@ cudaError_t pick(const Operand& A, const Operand& B, int64_t R, int64_t C, int64
         if (t128 * n > pairs || (n - 1) * share >= kb) break;
         if (take < least && t128 <= split_clusters<A_MN, B_MN, TO>(n)) split = n, least = take;
     }
-    if (split > 1) return go<128, A_MN, B_MN, TO, true>(A, B, R, C, depth, out, ldo, st, split);
+    if (split > 1) return go<128, A_MN, B_MN, TO, true>(A, B, R, C, depth, out, ldo, watch, st, split);
     if (cycles(128, 330, 3000) < cycles(kWide, 2 * kWide + 40, 4000))
-        return go<128, A_MN, B_MN, TO>(A, B, R, C, depth, out, ldo, st);
-    return go<kWide, A_MN, B_MN, TO>(A, B, R, C, depth, out, ldo, st);
+        return go<128, A_MN, B_MN, TO>(A, B, R, C, depth, out, ldo, watch, st);
+    return go<kWide, A_MN, B_MN, TO>(A, B, R, C, depth, out, ldo, watch, st);
 }
 
 template <typename TO>
 cudaError_t pick(const Operand& A, const Operand& B, int64_t R, int64_t C, int64_t depth, TO* out, int64_t ldo,
-                 cudaStream_t st) {
-    if (A.mn && B.mn) return pick<true, true, TO>(A, B, R, C, depth, out, ldo, st);
-    if (B.mn) return pick<false, true, TO>(A, B, R, C, depth, out, ldo, st);
-    return pick<false, false, TO>(A, B, R, C, depth, out, ldo, st);
+                 const Proj8Watch& watch, cudaStream_t st) {
+    if (A.mn && B.mn) return pick<true, true, TO>(A, B, R, C, depth, out, ldo, watch, st);
+    if (B.mn) return pick<false, true, TO>(A, B, R, C, depth, out, ldo, watch, st);
+    return pick<false, false, TO>(A, B, R, C, depth, out, ldo, watch, st);
 }
 
 }  // namespace
 
 cudaError_t launch_proj8(const Operand& A, const Operand& B, int64_t R, int64_t C, int64_t depth, void* out,
-                         int64_t ldo, bool bf16, cudaStream_t st) {
+                         int64_t ldo, bool bf16, cudaStream_t st, const Proj8Watch& watch) {
     if (R == 0 || C == 0) return cudaSuccess;
-    return bf16 ? pick(A, B, R, C, depth, static_cast<__nv_bfloat16*>(out), ldo, st)
-                : pick(A, B, R, C, depth, static_cast<float*>(out), ldo, st);
+    return bf16 ? pick(A, B, R, C, depth, static_cast<__nv_bfloat16*>(out), ldo, watch, st)
+                : pick(A, B, R, C, depth, static_cast<float*>(out), ldo, watch, st);
 }
 
 }  // namespace m2

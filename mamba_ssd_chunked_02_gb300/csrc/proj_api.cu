@@ -75,6 +75,13 @@ bool proj_args(const mamba2_proj8_shape* s, const mamba2_proj8_pitches* p, bool 
     return true;
 }
 
+cudaError_t forward(const Proj& a, const uint8_t* x, const uint8_t* x_scales, const uint8_t* w, const uint8_t* w_scales,
+                    void* y, cudaStream_t st, const Proj8Watch& watch) {
+    const int64_t kb = groups(a.K);
+    const Operand W{w, a.pw, false, w_scales, kb, 1, 7}, X{x, a.px, false, x_scales, kb, 1, 0};
+    return launch_proj8(X, W, a.M, a.N, a.K, y, a.py, a.bf16, st, watch);
+}
+
 // The backward product's workspace.
 size_t work_of(const Proj& a, void* base, Quant8Operands* w) {
     w->pn = up(a.N, 128), w->pk = up(a.K, 128), w->ps = up(groups(a.N), 4);
@@ -157,9 +164,20 @@ mamba2_status mamba2_proj8_fwd(const mamba2_proj8_shape* shape, const mamba2_pro
     if (!req(x, all, 16) || !req(x_scales, all, 1) || !req(w, all, 16) || !req(w_scales, all, 1) ||
         !req(y, all, a.bf16 ? 2 : 4))
         return MAMBA2_ERR_INVALID_ARG;
-    const int64_t kb = groups(a.K);
-    const Operand W{w, a.pw, false, w_scales, kb, 1, 7}, X{x, a.px, false, x_scales, kb, 1, 0};
-    return from_cuda(launch_proj8(X, W, a.M, a.N, a.K, y, a.py, a.bf16, static_cast<cudaStream_t>(stream)));
+    return from_cuda(forward(a, x, x_scales, w, w_scales, y, static_cast<cudaStream_t>(stream), Proj8Watch{}));
+}
+
+mamba2_status mamba2_proj8_selftest_timeout(const mamba2_proj8_shape* shape, const uint8_t* x, const uint8_t* x_scales,
+                                            const uint8_t* w, const uint8_t* w_scales, void* y, uint32_t limit_us,
+                                            void* stream) {
+    Proj a;
+    mamba2_status e;
+    if (!proj_args(shape, nullptr, false, &a, &e)) return e;
+    if (limit_us < 1 || limit_us > 100000 || a.M == 0 || a.N == 0 || !req(x, 1, 16) || !req(x_scales, 1, 1) ||
+        !req(w, 1, 16) || !req(w_scales, 1, 1) || !req(y, 1, a.bf16 ? 2 : 4))
+        return MAMBA2_ERR_INVALID_ARG;
+    return from_cuda(forward(a, x, x_scales, w, w_scales, y, static_cast<cudaStream_t>(stream),
+                             Proj8Watch{(uint64_t)limit_us * 1000, true}));
 }
 
 size_t mamba2_proj8_bwd_workspace_size(const mamba2_proj8_shape* shape) {

@@ -12,8 +12,10 @@
 //     is contiguous (a 128-byte row holds 64 consecutive m/n of one k).
 //   * Accumulators are fp32 in tensor memory: for M = 128 and one CTA, row i
 //     of D is TMEM lane i and column j is TMEM column base + j.
-//   * Every wait is bounded (wall-clock, %globaltimer); callers turn a false
-//     return into an error flag and an orderly exit.
+//   * Every wait on an mbarrier or a flag is bounded (wall-clock, %globaltimer);
+//     callers turn a false return into an error flag and an orderly exit.  (The
+//     barriers of a cluster, tcgen05.alloc, the wait for groups of copies out and
+//     griddepcontrol.wait have no limit to give.)
 #pragma once
 
 #include <cuda.h>

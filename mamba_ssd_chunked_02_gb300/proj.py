@@ -31,7 +31,7 @@ QUANT8_BLOCK = 1
 
 # Symbols of include/mamba2_proj.h (checked by the CPU test suite).
 SYMBOLS = ("mamba2_add_norm_fwd", "mamba2_add_norm_bwd", "mamba2_add_norm_bwd_workspace_size", "mamba2_quant8",
-           "mamba2_proj8_fwd", "mamba2_proj8_bwd", "mamba2_proj8_bwd_workspace_size")
+           "mamba2_proj8_fwd", "mamba2_proj8_bwd", "mamba2_proj8_bwd_workspace_size", "mamba2_proj8_selftest_timeout")
 
 _i64, _i32 = ctypes.c_int64, ctypes.c_int32
 
@@ -106,6 +106,24 @@ def proj8_fwd(x, x_scales, w, w_scales, *, dtype=None, y=None, stream=None):
     if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise TypeError(f"unsupported element type {dtype}: dtype must be torch.bfloat16 or torch.float32")
     return _ext().proj8_fwd(x, x_scales, w, w_scales, dtype is torch.float32, y, stream)
+
+
+def proj8_selftest_timeout(x, x_scales, w, w_scales, y, *, limit_us=2000, stream=None):
+    """The failure path of the product's waits (mamba2_proj8_selftest_timeout): contiguous x [tokens,K],
+    w [N,K] and y [tokens,N] as proj8_fwd takes them, K a multiple of 16.  Sets DEVERR_TIMEOUT_PROJ8,
+    and leaves y as it is."""
+    from . import _check, _dtype_code, _ptr, _stream, load
+    (M, K), N = x.shape, w.shape[0]
+    if K % 16:
+        raise ValueError(f"K must be a multiple of 16, got {K}")
+    q, s, kb = torch.float8_e4m3fn, torch.float8_e8m0fnu, -(-K // 128)
+    vp = ctypes.c_void_p
+    f = ctypes.CFUNCTYPE(ctypes.c_int, *[vp] * 6, ctypes.c_uint32, vp)(("mamba2_proj8_selftest_timeout", load()))
+    shape = Proj8Shape(M, K, N, _dtype_code(y.dtype), 0)
+    _check("mamba2_proj8_selftest_timeout", f(
+        ctypes.addressof(shape), _ptr(x, "x", q, (M, K)),
+        _ptr(x_scales, "x_scales", s, (M, kb)), _ptr(w, "w", q, (N, K)), _ptr(w_scales, "w_scales", s, (-(-N // 128), kb)),
+        _ptr(y, "y", y.dtype, (M, N)), int(limit_us), _stream(stream)))
 
 
 def proj8_bwd(dy, x, x_scales, w, w_scales, *, need_dx=True, need_dw=True, grads=None, workspace=None, stream=None):

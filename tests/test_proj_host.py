@@ -1,4 +1,6 @@
 """Projection operators on the host (no GPU): refusals beside test_proj.py's."""
+import ctypes
+
 import pytest
 
 import mamba_ssd_chunked_02_gb300 as m2
@@ -19,3 +21,22 @@ def test_gradient_pitches(lib):
         assert _call(lib, "proj8_bwd", _proj(), p, *back, *SIZE) == m2.ERR_INVALID_ARG
     # a pitch of dy of 0 is taken: the workspace is what is missing here
     assert _call(lib, "proj8_bwd", _proj(), _longs(32, 32, 0), *back, None, 0, None) == m2.ERR_WORKSPACE
+
+
+def test_timeout_selftest_refusals(lib):
+    ok = [P] * 5                          # x, scales, w, scales, y
+
+    f = lib.mamba2_proj8_selftest_timeout
+    f.restype = ctypes.c_int
+
+    def status(shape=None, ptrs=ok, limit=1000):
+        return f(ctypes.byref(shape or _proj()), *(ctypes.c_void_p(p) for p in ptrs), ctypes.c_uint32(limit), None)
+
+    assert status(limit=0) == m2.ERR_INVALID_ARG and status(limit=100001) == m2.ERR_INVALID_ARG
+    for bad in (dict(tokens=0), dict(outputs=0), dict(tokens=-1), dict(dtype=5), dict(flags=1)):
+        assert status(_proj(**bad)) == m2.ERR_INVALID_ARG
+    assert status(_proj(inputs=0)) == m2.ERR_UNSUPPORTED
+    for k in range(5):
+        assert status(ptrs=[None if i == k else P for i in range(5)]) == m2.ERR_INVALID_ARG
+    for k in (0, 2):
+        assert status(ptrs=[P + 8 if i == k else P for i in range(5)]) == m2.ERR_INVALID_ARG
