@@ -5,7 +5,7 @@ import pytest
 
 import mamba_ssd_chunked_02_gb300 as m2
 from mamba_ssd_chunked_02_gb300 import build as m2build
-from test_proj import P, SIZE, _call, _longs, _proj
+from test_proj import P, SIZE, _call, _longs, _norm, _proj
 
 
 @pytest.fixture(scope="module")
@@ -40,3 +40,15 @@ def test_timeout_selftest_refusals(lib):
         assert status(ptrs=[None if i == k else P for i in range(5)]) == m2.ERR_INVALID_ARG
     for k in (0, 2):
         assert status(ptrs=[P + 8 if i == k else P for i in range(5)]) == m2.ERR_INVALID_ARG
+
+
+def test_strides_of_x_are_not_looked_at_in_add_norm_s_gradient(lib):
+    """It has no x: what the strides say of one is not checked (the workspace is what is missing here)."""
+    back = [P] * 7                        # total, w, dy, dtotal, dx, dresidual, dw
+    for x in ((-1, 5), (1 << 50, -7)):
+        st = _longs(*x, 128, 32, 128, 32, 128, 32)
+        assert _call(lib, "add_norm_bwd", _norm(), st, *back, None, 0, None) == m2.ERR_WORKSPACE
+    for k in (2, 4, 6):
+        bad = [128, 32] * 4
+        bad[k] = -1
+        assert _call(lib, "add_norm_bwd", _norm(), _longs(*bad), *back, *SIZE) == m2.ERR_INVALID_ARG
