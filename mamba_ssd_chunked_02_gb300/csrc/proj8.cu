@@ -119,7 +119,7 @@ __device__ __forceinline__ void arrive_at(uint32_t bar) {
 // orders the reads before the other block's later products are tcgen05.wait::ld, tcgen05.fence::before_thread_sync in
 // front of the arrival and ::after_thread_sync behind the wait, which hold with a relaxed arrival; its scope, like that
 // of the waits in proj8_kernel, is the cluster's.  The release above waits for the thread's stores, copies out among
-// them, some 2000 cycles.
+// them, some 2000 cycles.  (Waits that all acquire at that scope: 4096 x 768 x 768 7.8 us instead of 7.5.)
 __device__ __forceinline__ void arrive_read_at(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -136,28 +136,27 @@ __device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* m, const vo
                  "r"(smem_u32(src)), "r"(x), "r"(y)
                  : "memory");
 }
+// A warp whose wait ran out stays a millisecond before it goes where the block, or the cluster, meets: what other
+// warps asked for and no one waits for any more (copies, products) ends within microseconds.
+__device__ __noinline__ void stay() {   // once: apart from what runs when all is well
+    for (const uint64_t t0 = globaltimer(); globaltimer() - t0 < 1000000;) __nanosleep(1000);
+}
+__device__ __forceinline__ void linger(bool ok) {
+    if (!ok) stay();
+}
+// Waits until the copies that were asked for, the last of each stage, have landed: at most limit_ns for all of them.
+template <Scope S> __device__ __forceinline__ void land(uint64_t* full, int issued, int stages, uint64_t limit_ns) {
+    const uint64_t t0 = globaltimer();
+    for (int i = issued - 1; i >= 0 && i >= issued - stages; --i) {
+        const uint64_t gone = globaltimer() - t0;
+        if (!mbar_wait<S>(&full[i % stages], i / stages & 1, gone < limit_ns ? limit_ns - gone : 0)) return;
+    }
+}
 // Where a wait has run out in this block, every block of the cluster is told so: before the barrier at which they
-// all meet, so that behind it all know.
+// all meet, so that behind it all know, and none joins sums that are not there.
 __device__ __forceinline__ void tell_abort(int* abort, int lane, uint32_t blocks) {
     if (lane == 0 && *reinterpret_cast<volatile int*>(abort))
         for (uint32_t r = 0; r < blocks; ++r) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(of_block(abort, r)), "r"(1) : "memory");
-}
-// Behind a wait that ran out and the barrier that told all of it, by all threads: waits until the copies that this
-// block's barriers count, the last of each stage, have landed, at most limit_ns for all of them.  A copy whose bytes are
-// not yet expected there, and a product that no one waits for any more, end within microseconds; the block stays for a
-// thousand.
-template <bool CLUSTER>
-__device__ __forceinline__ void give_up(uint64_t* full, int issued, int stages, uint64_t limit_ns, int32_t* err) {
-    if (threadIdx.x == 0) {
-        record_error(err, kErrTimeoutProj8);
-        const uint64_t t0 = globaltimer();
-        for (int i = issued - 1; i >= 0 && i >= issued - stages; --i) {
-            const uint64_t gone = globaltimer() - t0;
-            if (!mbar_wait<CLUSTER>(&full[i % stages], i / stages & 1, gone < limit_ns ? limit_ns - gone : 0)) break;
-        }
-    }
-    __nanosleep(1000000);
-    __syncwarp();
 }
 // One lane of a warp that is whole.
 __device__ __forceinline__ bool elected() {
@@ -184,7 +183,6 @@ struct Scales {
 struct Shape {
     int R, C, kb;          // rows, columns, contracted blocks
     int tr, tiles;         // tiles along the rows, in all
-    int panel;             // tiles of a panel along the columns
     int chunk;             // contracted blocks summed in tensor memory before they are added to the result
     bool copied;           // the result's rows are whole 16 bytes, and start there
     int64_t ldo;
@@ -257,7 +255,6 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
              const Scales sb, TO* __restrict__ out, const Shape q,
              int32_t* err) {
     using C = Cfg<BN, B_MN, sizeof(TO)>;
-    constexpr bool PAIR = true;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t* sout = smem + C::NS * C::STAGE;
@@ -271,13 +268,13 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     const int first = blockIdx.x / (SPLIT ? 2 * q.split : 2), step = SPLIT ? q.tiles : gridDim.x / 2;
     const int from_k = SPLIT ? (even >> 1) * q.share : 0, to_k = SPLIT ? min(q.kb, from_k + q.share) : q.kb;
     constexpr int kRows = 2 * BM;
-    // Tiles go down panels of q.panel columns of tiles, a row of the panel at a time: the clusters that
+    // Tiles go down panels of kPanel columns of tiles, a row of the panel at a time: the clusters that
     // run side by side then share few rows of A and of B.
     const auto place = [&](int tile, int* r, int* c) {
-        const int tc = q.tiles / q.tr, each = q.panel * q.tr, p = tile / each, in = tile - p * each,
-                  w = min(q.panel, tc - p * q.panel);
+        const int tc = q.tiles / q.tr, each = kPanel * q.tr, p = tile / each, in = tile - p * each,
+                  w = min(kPanel, tc - p * kPanel);
         *r = in / w;
-        *c = p * q.panel + in - *r * w;
+        *c = p * kPanel + in - *r * w;
     };
     const auto row_of = [&](int r) { return r * kRows + rank * BM; };
 
@@ -300,14 +297,13 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         bars.abort = 0;
         fence_barrier_init();
     }
-    if (warp == 1) alloc_tmem<PAIR>(&bars.tmem, C::COLS);
+    if (warp == 1) alloc_tmem<true>(&bars.tmem, C::COLS);
     __syncwarp();
     tc_fence_before();
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = bars.tmem;
     grid_dep_wait();   // what is read was written by the kernel before
-    int issued = 0;    // copies' stages that warp 0 asked for
     [[maybe_unused]] float sum[SPLIT ? 64 : 1] = {};   // of a row, 64 columns: a warp's of the pair's share
     // The producing and the issuing warp run whole, with one lane elected for each instruction: what
     // the loop counts then stays in uniform registers, where the copies and products take it from
@@ -326,7 +322,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             place(tile, &r, &c);
             const int r0 = row_of(r), c0 = c * BN + rank * C::HALF;
             for (int kb = from_k; kb < to_k; ++kb, ++it) {
-                ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.empty[st], phase, abort, q.watch.limit_ns));
+                ok = __all_sync(0xffffffffu, mbar_wait_or_abort<kClusterBare>(&bars.empty[st], phase, abort, q.watch.limit_ns));
                 if (!ok) break;
                 if (elected()) {
                     uint8_t* a = smem + st * C::STAGE;
@@ -341,7 +337,9 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             }
         }
         grid_dep_launch();   // all copies are asked for: the next kernel may set itself up as blocks end
-        issued = it;
+        // the even block's barriers count both blocks' copies
+        if (!ok && rank == 0 && lane == 0) land<kClusterBare>(bars.full, it, C::NS, q.watch.limit_ns);
+        linger(ok);
     } else if (warp == 1) {
         if (rank == 0) {
             constexpr uint32_t idesc = idesc_mx(kRows, BN, A_MN, B_MN);
@@ -357,45 +355,45 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             for (int tile = first; tile < q.tiles && ok; tile += step)
                 for (int k0 = from_k; k0 < to_k && ok; k0 += q.chunk, ++t) {
                     const int acc = t & 1, k1 = min(to_k, k0 + q.chunk);
-                    ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.acc_empty[acc], (t / 2 & 1) ^ 1, abort, q.watch.limit_ns));
+                    ok = __all_sync(0xffffffffu, mbar_wait_or_abort<kClusterBare>(&bars.acc_empty[acc], (t / 2 & 1) ^ 1, abort, q.watch.limit_ns));
                     if (C::SHARED && ok && t > 0)
-                        ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.acc_shared, (t - 1) & 1, abort, q.watch.limit_ns));
+                        ok = __all_sync(0xffffffffu, mbar_wait_or_abort<kClusterBare>(&bars.acc_shared, (t - 1) & 1, abort, q.watch.limit_ns));
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t d = tmem + acc * C::ACC;
                     bool there = false;   // the next stage's operands, asked for ahead
                     for (int kb = k0; kb < k1 && ok; kb += 4) {
                         const uint32_t ta = tmem + C::SF_COL + sf * C::SF_COLS;
-                        ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.sf_full[sf], sf_phase, abort, q.watch.limit_ns));
+                        ok = __all_sync(0xffffffffu, mbar_wait_or_abort<kCluster>(&bars.sf_full[sf], sf_phase, abort, q.watch.limit_ns));
                         if (!ok) break;
                         tc_fence_after();
                         if (elected()) {
                             const uint64_t from = s0 + (uint32_t)(sf * (C::SF_BYTES >> 4));
 #pragma unroll
-                            for (int h = 0; h <= C::SFB; ++h) copy_scales<PAIR>(ta + 4 * h, from + h * (512 >> 4));
+                            for (int h = 0; h <= C::SFB; ++h) copy_scales<true>(ta + 4 * h, from + h * (512 >> 4));
                         }
                         __syncwarp();
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             if (kb + i >= k1) break;
                             if (!there) {
-                                ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.full[st], phase, abort, q.watch.limit_ns));
+                                ok = __all_sync(0xffffffffu, mbar_wait_or_abort<kClusterBare>(&bars.full[st], phase, abort, q.watch.limit_ns));
                                 if (!ok) break;
                             }
                             tc_fence_after();
                             const int now = st;
                             if (++st == C::NS) st = 0, phase ^= 1;
                             const bool last = kb + i + 1 == k1;
-                            there = !last && mbar_test_wait<true>(smem_u32(&bars.full[st]), phase);
+                            there = !last && mbar_test_wait<kClusterBare>(smem_u32(&bars.full[st]), phase);
                             if (elected()) {
                                 const uint32_t at = now * (C::STAGE >> 4);
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
-                                    mma_scaled<PAIR>(d, a0 + at + k * a_step, b0 + at + k * b_step, idesc | i << 4 | i << 29, ta,
+                                    mma_scaled<true>(d, a0 + at + k * a_step, b0 + at + k * b_step, idesc | i << 4 | i << 29, ta,
                                                      ta + 4, kb > k0 || i > 0 || k > 0);
-                                commit<PAIR>(&bars.empty[now], both);
-                                if (i == 3 || last) commit<PAIR>(&bars.sf_empty[sf], both);
-                                if (last) commit<PAIR>(&bars.acc_full[acc], both);
+                                commit<true>(&bars.empty[now], both);
+                                if (i == 3 || last) commit<true>(&bars.sf_empty[sf], both);
+                                if (last) commit<true>(&bars.acc_full[acc], both);
                             }
                             there = __all_sync(0xffffffffu, there);
                         }
@@ -403,9 +401,10 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                     }
                 }
             if (!ok && elected()) {
-                commit<PAIR>(&bars.drain, 1u << even);
+                commit<true>(&bars.drain, 1u << even);
                 mbar_wait(&bars.drain, 0, q.watch.limit_ns);
             }
+            linger(ok);
         }
     } else if (warp < 4) {
         // The scales of the next kFly sets are on their way while this set's room is waited for (a load
@@ -450,7 +449,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 uint4 w[C::SFB];
 #pragma unroll
                 for (int h = 0; h < C::SFB; ++h) w[h] = next[u][h];
-                ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.sf_empty[sf], phase, abort, q.watch.limit_ns));
+                ok = __all_sync(0xffffffffu, mbar_wait_or_abort<kCluster>(&bars.sf_empty[sf], phase, abort, q.watch.limit_ns));
                 if (!ok) break;
                 uint4* to = reinterpret_cast<uint4*>(ssf + sf * C::SF_BYTES) + (warp == 2 ? 0 : 32) + lane;
 #pragma unroll
@@ -463,6 +462,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 --left;
             }
         }
+        linger(ok);
     } else if (warp == 12) {
         // Scales in shared memory to the tensor cores' proxy.  A warp of its own, as the fence waits for
         // all that its warp has in flight: behind the loads of later sets it took 2000 cycles.
@@ -477,6 +477,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 arrive_at(full0 + 8 * sf);
                 if (++sf == C::NSF) sf = 0, phase ^= 1;
             }
+            linger(left <= 0);
         }
     } else if constexpr (SPLIT) {
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -484,7 +485,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         int t = 0;
         for (int k0 = from_k; k0 < to_k; k0 += q.chunk, ++t) {
             const int acc = t & 1;
-            ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.acc_full[acc], t / 2 & 1, abort, q.watch.limit_ns));
+            ok = __all_sync(0xffffffffu, mbar_wait_or_abort<kClusterBare>(&bars.acc_full[acc], t / 2 & 1, abort, q.watch.limit_ns));
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -498,6 +499,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             __syncwarp();
             if (lane == 0) arrive_read_at(of_block(&bars.acc_empty[acc], even));
         }
+        linger(ok);
     } else {
         // A warp has 32 lanes of tensor memory, the tile's rows, and moves lines of 128 bytes of half the
         // columns: rounded, into shared memory, and by TMA to the result (coalesced stores where the result's
@@ -512,7 +514,7 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             place(tile, &rt, &ct);
             for (int k0 = 0; k0 < q.kb; k0 += q.chunk, ++t) {
                 const int acc = t & 1;
-                ok = __all_sync(0xffffffffu, mbar_wait_or_abort<true>(&bars.acc_full[acc], t / 2 & 1, abort, q.watch.limit_ns));
+                ok = __all_sync(0xffffffffu, mbar_wait_or_abort<kClusterBare>(&bars.acc_full[acc], t / 2 & 1, abort, q.watch.limit_ns));
                 if (!ok) break;
                 tc_fence_after();
                 const int r0 = row_of(rt) + quad * 32, c0 = ct * BN;
@@ -593,17 +595,15 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         }
         __syncwarp();
         if (elected()) bulk_wait<0>();   // copies out of this block's shared memory
+        linger(ok);
     }
     __syncwarp();
-    tell_abort(&bars.abort, lane, SPLIT ? 2 * q.split : 2);
-    __syncwarp();
+    if constexpr (SPLIT) {
+        tell_abort(&bars.abort, lane, 2 * q.split);
+        __syncwarp();
+    }
     tc_fence_before();
     cluster_sync();
-    if (*abort) {
-        // the even block's barriers count both blocks' copies
-        give_up<true>(bars.full, rank == 0 ? issued : 0, C::NS, q.watch.limit_ns, err);
-        cluster_sync();
-    }
     if constexpr (SPLIT) {
         // Every pair is done with its operands, whose room takes the shares' sums: a block owns BN / split
         // of its 128 rows' columns, gets them from the blocks of its half of the rows, and adds them in the
@@ -658,9 +658,10 @@ proj8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 }
         }
     }
+    if (threadIdx.x == 0 && *abort) record_error(err, kErrTimeoutProj8);
     if (warp == 1) {
         tc_fence_after();
-        free_tmem<PAIR>(tmem, C::COLS);
+        free_tmem<true>(tmem, C::COLS);
     }
 }
 
@@ -770,7 +771,6 @@ proj8_few_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     const uint32_t tmem = bars.tmem;
     if (split > 1) cluster_arrive();   // this block has begun
     bool ok = true;
-    int issued = 0;   // copies' stages that warp 0 asked for
 
     if (warp == 0) {
         grid_dep_wait();     // what is read was written by the kernel before
@@ -789,7 +789,7 @@ proj8_few_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
             __syncwarp();
             if (++st == ns) st = 0, phase ^= 1;
         }
-        issued = it;
+        if (!ok && lane == 0) land<kBlock>(bars.full, it, ns, q.watch.limit_ns);
     } else if (warp == 1) {
         constexpr uint32_t idesc = idesc_mx(BM, BN, A_MN, 0);
         constexpr uint32_t a_step = (A_MN ? 32 * 128 : 32) >> 4, b_step = 32 >> 4;
@@ -865,6 +865,7 @@ proj8_few_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
         __syncwarp();
         cluster_wait();
     }
+    linger(ok);
     __syncwarp();
     if (split > 1) tell_abort(&bars.abort, lane, split);
     __syncwarp();
@@ -887,7 +888,7 @@ proj8_few_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     } else {
         __syncthreads();
     }
-    if (*abort) give_up<false>(bars.full, issued, ns, q.watch.limit_ns, err);
+    if (threadIdx.x == 0 && *abort) record_error(err, kErrTimeoutProj8);
     if (warp == 1) {
         tc_fence_after();
         free_tmem<false>(tmem, C::COLS);
@@ -984,7 +985,7 @@ cudaError_t go(const Operand& A, const Operand& B, int64_t R, int64_t Cn, int64_
     if (tiles >= (int64_t(1) << 30)) return kGridLimit;
     const int kb = (int)((depth + BK - 1) / BK);
     if ((int64_t)(split - 1) * share_of(kb, split) >= kb) return cudaErrorInvalidValue;   // a pair without blocks
-    const Shape q{(int)R, (int)Cn, kb, (int)tr, (int)tiles, kPanel, sizeof(TO) == 4 ? kChunk : kb, copied, ldo, split, share_of(kb, split),
+    const Shape q{(int)R, (int)Cn, kb, (int)tr, (int)tiles, sizeof(TO) == 4 ? kChunk : kb, copied, ldo, split, share_of(kb, split),
                   watch};
     const Scales sa = scales_of(A, R, kb), sb = scales_of(B, Cn, kb);
     auto k = proj8_kernel<BN, A_MN, B_MN, TO, SPLIT>;

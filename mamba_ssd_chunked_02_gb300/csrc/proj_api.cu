@@ -39,6 +39,7 @@ bool norm_args(const mamba2_add_norm_shape* s, const mamba2_add_norm_strides* st
     a->quant = !back && (s->flags & MAMBA2_ADD_NORM_QUANT);
     const int64_t q_row = up(a->D, 16), q_strides[2] = {a->T * q_row, q_row};
     const int64_t* sy = st ? st->y : a->quant ? q_strides : nullptr;
+    a->sx = Tok{0, 0};
     if ((!back && !in_strides(st ? st->x : nullptr, a->T, a->D, &a->sx)) ||
         !in_strides(st ? st->residual : nullptr, a->T, a->D, &a->sres))
         return false;

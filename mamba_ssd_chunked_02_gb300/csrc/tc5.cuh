@@ -51,82 +51,55 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// CLUSTER: a barrier at which another block of the cluster arrives, so that the wait's scope is
-// the cluster's (the block's else).
-template <bool CLUSTER = false> __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    if constexpr (CLUSTER)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
+// What a wait orders.  kBlock: arrivals of this block's threads and of its own asynchronous
+// operations.  Where another block of the cluster arrives the scope is the cluster's: kCluster
+// acquires what was written before; kClusterBare does not, for a thread behind whose wait come only
+// asynchronous operations, of the tensor cores (ordered by tcgen05.fence::after_thread_sync) or copies.
+enum Scope { kBlock, kCluster, kClusterBare };
+#define M2_MBAR_WAIT(WAIT, SEM, HINT)                                    \
+    asm volatile("{\n\t.reg .pred p;\n\t"                               \
+                 "mbarrier." WAIT ".parity" SEM ".shared::cta.b64 p, [%1], %2" HINT ";\n\t" \
+                 "selp.u32 %0, 1, 0, p;\n\t}"                            \
+                 : "=r"(ok)                                              \
+                 : "r"(bar), "r"(parity), "r"(hint_ns)                   \
+                 : "memory")
+template <Scope S = kBlock> __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok, hint_ns = 0;
+    if constexpr (S == kBlock) M2_MBAR_WAIT("try_wait", "", "");
+    else if constexpr (S == kCluster) M2_MBAR_WAIT("try_wait", ".acquire.cluster", "");
+    else M2_MBAR_WAIT("try_wait", ".relaxed.cluster", "");
     return ok != 0;
 }
 // Non-blocking probe: true when the phase with the given parity has completed.
 // (try_wait may suspend the thread for a while before it returns false; a loop
 // that polls several barriers in turn needs this form.)
-template <bool CLUSTER = false> __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    if constexpr (CLUSTER)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
+template <Scope S = kBlock> __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok, hint_ns = 0;
+    if constexpr (S == kBlock) M2_MBAR_WAIT("test_wait", "", "");
+    else if constexpr (S == kCluster) M2_MBAR_WAIT("test_wait", ".acquire.cluster", "");
+    else M2_MBAR_WAIT("test_wait", ".relaxed.cluster", "");
     return ok != 0;
 }
 // try_wait with a suspend-time hint: the thread sleeps in hardware until the
 // phase completes or about `hint_ns` pass, so a waiting warp does not spin
 // and steal issue slots from the warps doing the work.
-template <bool CLUSTER = false> __device__ __forceinline__ bool mbar_try_wait_sleep(uint32_t bar, uint32_t parity, uint32_t hint_ns) {
+template <Scope S = kBlock>
+__device__ __forceinline__ bool mbar_try_wait_sleep(uint32_t bar, uint32_t parity, uint32_t hint_ns) {
     uint32_t ok;
-    if constexpr (CLUSTER)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(hint_ns)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(hint_ns)
-            : "memory");
+    if constexpr (S == kBlock) M2_MBAR_WAIT("try_wait", "", ", %3");
+    else if constexpr (S == kCluster) M2_MBAR_WAIT("try_wait", ".acquire.cluster", ", %3");
+    else M2_MBAR_WAIT("try_wait", ".relaxed.cluster", ", %3");
     return ok != 0;
 }
+#undef M2_MBAR_WAIT
 constexpr uint32_t kSuspendHintNs = 1000;
 
 // Wait for the phase with the given parity to complete, for at most limit_ns.
-template <bool CLUSTER = false> __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+template <Scope S = kBlock> __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
     const uint32_t a = smem_u32(bar);
-    if (mbar_try_wait<CLUSTER>(a, parity)) return true;
+    if (mbar_try_wait<S>(a, parity)) return true;
     const uint64_t t0 = globaltimer();
-    while (!mbar_try_wait_sleep<CLUSTER>(a, parity, kSuspendHintNs)) {
+    while (!mbar_try_wait_sleep<S>(a, parity, kSuspendHintNs)) {
         if (globaltimer() - t0 > limit_ns) return false;
     }
     return true;
@@ -135,12 +108,12 @@ template <bool CLUSTER = false> __device__ __forceinline__ bool mbar_wait(uint64
 // Wait like mbar_wait, but also give up as soon as *abort becomes nonzero (a
 // shared-memory flag another role of the CTA raised after its own timeout); a
 // timeout raises *abort.  Returns true only when the phase completed.
-template <bool CLUSTER = false>
+template <Scope S = kBlock>
 __device__ __forceinline__ bool mbar_wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
     const uint32_t a = smem_u32(bar);
-    if (mbar_try_wait<CLUSTER>(a, parity)) return true;
+    if (mbar_try_wait<S>(a, parity)) return true;
     const uint64_t t0 = globaltimer();
-    while (!mbar_try_wait_sleep<CLUSTER>(a, parity, kSuspendHintNs)) {
+    while (!mbar_try_wait_sleep<S>(a, parity, kSuspendHintNs)) {
         if (*abort) return false;
         if (globaltimer() - t0 > limit_ns) {
             *abort = 1;
