@@ -12,7 +12,9 @@
 //
 // A team (a warp for narrow rows, else a block) holds a forward row in registers between the sum
 // and the result; what wide rows do not fit is read again.  A backward team walks over tokens, so
-// that its part of dw stays in registers; the parts are summed by a second kernel, in a fixed order.
+// that its part of dw stays in registers; the parts are summed by a second kernel, in a fixed order.  Rows of more than
+// 2048 units (8192 channels, 16384 with a bf16 residual) are read twice, and their part of dw stays in memory: as many
+// values in rows of 16384 with an fp32 residual 259 us.
 #include <algorithm>
 #include <atomic>
 #include <initializer_list>

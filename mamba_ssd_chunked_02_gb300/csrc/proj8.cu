@@ -16,8 +16,8 @@
 // Warp roles: 0 TMA, 1 MMA (and tensor memory), 2 scales of A, 3 scales of B, 4-11 epilogue,
 // 12 hands the scales to the tensor cores.
 //
-// Bound by the tensor cores where sums are long: 32768 x 2560 x 10576 511 us in a burst (3.47 PFLOP/s; twice
-// the measured bf16 rate is 3.91), 605 us when it runs on (the power limit; 464 us on zeros); by the result's
+// Bound by the tensor cores where sums are long: 32768 x 2560 x 10576 517 us in a burst (3.43 PFLOP/s; twice
+// the measured bf16 rate is 3.91), 600 us when it runs on (the power limit; 464 us on zeros); by the result's
 // bytes where they are short (13764 x 69 x 5968 bf16: 38 us, 4.3 TB/s); by the launch and memory's latency
 // where all is small.  Single blocks with 128 x 128 tiles took 983 us.
 #include <cuda_bf16.h>
@@ -1015,7 +1015,7 @@ cudaError_t go_few(const Operand& A, const Operand& B, int64_t R, int64_t Cn, in
     static std::atomic<uint64_t> done;
     cudaError_t e = allow_smem(k, most, done);
     if (e != cudaSuccess) return e;
-    // The most blocks a tile with which all run at once, an SM to each (w of 10576 x 2560, 83 tiles, one
+    // The most blocks a tile with which all run at once, an SM to each (with w in L2: 10576 x 2560, 83 tiles, one
     // token: 8.5 us with one block a tile, 8.9 with three, two to an SM; 2560 x 5120, 20 tiles: 9.0 with
     // two, 6.5 with five, 10.7 with seven, of which some clusters wait); fewer where the largest share
     // stays the same.  A block's share is at most kFewBlocks.

@@ -5,9 +5,9 @@
 //
 // Bytes bound: a block of 512 threads holds a tile of 128 x 128 in registers, 4 x 8 values a
 // thread, so that both kinds of groups come from one reading (the backward product takes dy
-// along its rows for dx and along its columns for dw).  bf16 rows 32768 x 5120: 79 us, 6.4 TB/s
-// (0.96 of the measured copy rate); fp32 blocks 10576 x 2560: 25 us (5.4); dy of 32768 x 10576 both
-// ways: 283 us (4.9), issue slots at 0.56 (the next tile copied ahead: 300); x turned: 46 us (3.6).  Kernels here and in add_norm.cu
+// along its rows for dx and along its columns for dw).  In a graph: bf16 rows 32768 x 5120 79 us, 6.4 TB/s
+// (0.96 of the measured copy rate; a call 81); fp32 blocks 10576 x 2560 25 us (5.4; a call 26.7); dy of 32768 x 10576 both
+// ways 283 us (4.9), issue slots at 0.56 (the next tile copied ahead: 300); x turned 46 us (3.6).  Kernels here and in add_norm.cu
 // may begin while the one before them ends, and wait for it before they read.
 #include <cuda_bf16.h>
 
@@ -471,13 +471,15 @@ template <bool VEC> __device__ __forceinline__ void turn_tile(const uint8_t* __r
     }
 }
 
-// bf16 rows: four blocks an SM, though some registers spill (32768 x 5120: 78.8 us, three 81.8).
+// bf16 rows: four blocks an SM, though of 32 registers 48 to 64 bytes spill (32768 x 5120: 78.8 us, three 81.8).  Both
+// ways: two, at 64 registers, of which bf16 spills 12 to 32 bytes.
 template <typename TI, bool VEC, int MODE, int kThreads = 512>
 __global__ void __launch_bounds__(kThreads, sizeof(TI) == 2 && MODE == kRow ? 4 : 2) quant8_kernel(const TI* __restrict__ x, const Tile p) {
     quant_tile<TI, VEC, MODE, kThreads>(x, p, blockIdx.x);
 }
-// Three blocks an SM (32768 x 2560: 46 us, four 47; where each row's loads waited for the last's 58, with two
-// blocks then 75).
+// Three blocks an SM at 40 registers, none of them spilled where rows are whole units (20 bytes else; 264 and more
+// where the careful way kept the rows in registers: 0.6 us).  32768 x 2560: 46 us, four blocks 47; where each row's
+// loads waited for the last's 58, with two blocks then 75.
 template <bool VEC> __global__ void __launch_bounds__(kThreads, 3) quant8_turn_kernel(const uint8_t* __restrict__ x, const Tile p) {
     turn_tile<VEC>(x, p, blockIdx.x);
 }
